@@ -373,6 +373,85 @@ flp_status flp_embedding_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_d
                                   size_t workspace_bytes, void* stream);
 
 /*
+ * The lookup with a scaling factor, as models that multiply their embedding by
+ * sqrt(D) use it: out[i] = scale * weight[ids[i]] (each product rounded once to
+ * x_dtype), and d_weight = scale * (the sum above), the fp32 sum times scale rounded
+ * once.  scale: any finite value.  Everything else as for the two calls above, whose
+ * results scale = 1 gives bit for bit; the backward's workspace is
+ * flp_embedding_backward_workspace_bytes(N, D, V).
+ */
+flp_status flp_embedding_scaled_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                        const void* weight, const void* ids, flp_dtype id_dtype,
+                                        float scale, void* out, void* stream);
+flp_status flp_embedding_scaled_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                         const void* grad, const void* ids, flp_dtype id_dtype,
+                                         float scale, void* d_weight, flp_dtype dw_dtype,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Dropout between the embedding and the head, with a mask that is never stored:
+ *
+ *   out[e] = x[e] / (1 - q) where u[e] >= 65536 q, else 0;   q = round(65536 p) / 65536
+ *
+ * u[e] is the 16-bit piece e % 8 (low halves first) of the 128 bits that the ten-round
+ * 4 x 32 counter-based generator of Salmon et al. (2011) gives for the key rng[0] and
+ * the counter (e / 8, rng[1]).  The mask depends on e, p and rng only: the backward is
+ * the same call on the gradient, with the same p and rng.  A dropped element is 0
+ * whatever x[e] is (infinite or NaN included).
+ *
+ *   n         elements; x and out are [n] x_dtype (FLP_BF16, FLP_F16 or FLP_F32),
+ *             aligned to their element size.
+ *   p         probability of dropping, 0 <= p <= 1 (rounded to a multiple of 2^-16;
+ *             1 drops everything).
+ *   rng       two int64 on the device: seed and offset, any values (read as unsigned).
+ *             Calls with different offsets draw independent masks; since they are
+ *             read on the device, a captured call draws a new mask when the caller
+ *             changes them between replays.
+ */
+flp_status flp_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p, const int64_t* rng,
+                       void* out, void* stream);
+
+/*
+ * Layer norm of the rows x[i, :], as it stands in front of the head:
+ *
+ *   mean_i = sum_d x_id / D,   rstd_i = 1 / sqrt(sum_d (x_id - mean_i)^2 / D + eps)
+ *   out    = (x - mean) rstd weight + bias
+ *
+ *   x, out    [N, D] x_dtype (FLP_BF16, FLP_F16 or FLP_F32).  Any D >= 1 (below 2^28):
+ *             rows need no alignment beyond their element size.
+ *   weight, bias  [D] of w_dtype (x_dtype or FLP_F32), each may be NULL (1 and 0).
+ *   eps       >= 0, finite.  A constant row with eps = 0 has no norm (NaN).
+ *   out_mean, out_rstd  [N] float32, or NULL; the backward reads both.
+ *
+ * fp32 arithmetic, one rounding per output element; a row's results do not depend on
+ * the other rows.
+ */
+flp_status flp_layer_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                  flp_dtype w_dtype, const void* weight, const void* bias,
+                                  double eps, void* out, float* out_mean, float* out_rstd,
+                                  void* stream);
+/*
+ *   d_x       = rstd (g - mean_d(g) - xhat mean_d(g xhat)),  g = grad_out * weight
+ *   d_weight  = sum_i grad_out_i xhat_i,   d_bias = sum_i grad_out_i
+ *
+ *   grad_out, d_x       [N, D] x_dtype.  d_weight, d_bias [D] w_dtype.  d_x, d_weight
+ *             and d_bias may each be NULL to skip it.
+ *   mean, rstd  [N] as written by the forward for the same x and eps.
+ *   workspace >= flp_layer_norm_backward_workspace_bytes(N, D) bytes, 16-byte aligned:
+ *             partial sums of d_weight and d_bias (not needed, and not touched, when
+ *             both are NULL).
+ *
+ * The sums over rows are fp32 in a fixed order and rounded once; N = 0 writes zeros to
+ * d_weight and d_bias.
+ */
+size_t flp_layer_norm_backward_workspace_bytes(int64_t N, int64_t D);
+flp_status flp_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, const void* grad_out,
+                                   const void* x, flp_dtype w_dtype, const void* weight,
+                                   const float* mean, const float* rstd, void* d_x,
+                                   void* d_weight, void* d_bias, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
  * Measurement probes (not part of the operator): the achievable dense bf16
  * MFMA rate and the shader clock it runs at, and the achievable streaming-read
  * bandwidth, so that figures can be quoted against measured peaks as well as
@@ -419,7 +498,9 @@ typedef enum flp_kernel_kind {
   FLP_K_LOGITS_BACKWARD = 8,  /* flp_logits_backward */
   FLP_K_ROWS = 9,       /* indexed variants: row selection, gather, scatter */
   FLP_K_EMBEDDING = 10, /* flp_embedding_forward / flp_embedding_backward */
-  FLP_K_COUNT = 11
+  FLP_K_DROPOUT = 11,   /* flp_dropout */
+  FLP_K_LAYER_NORM = 12, /* flp_layer_norm_forward / flp_layer_norm_backward */
+  FLP_K_COUNT = 13
 } flp_kernel_kind;
 
 void flp_profile_enable(int on);

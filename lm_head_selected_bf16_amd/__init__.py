@@ -18,7 +18,10 @@ from ._abi import (FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpErro
                    flp_backward, flp_backward_chunk_rows, flp_backward_indexed,
                    flp_backward_indexed_workspace_bytes,
                    flp_backward_workspace_bytes, flp_build_info, flp_embedding_backward,
-                   flp_embedding_backward_workspace_bytes, flp_embedding_forward, flp_forward,
+                   flp_embedding_backward_workspace_bytes, flp_embedding_forward,
+                   flp_embedding_scaled_backward, flp_embedding_scaled_forward, flp_forward,
+                   flp_dropout, flp_layer_norm_backward, flp_layer_norm_backward_workspace_bytes,
+                   flp_layer_norm_forward,
                    flp_forward_indexed, flp_forward_noalloc, FLP_FORWARD_NOALLOC_MAX_BYTES,
                    flp_forward_indexed_workspace_bytes, flp_forward_partial,
                    flp_forward_partial_bytes, flp_forward_workspace_bytes, flp_logits_backward,
@@ -32,7 +35,9 @@ from .torch_ops import (LinearLogp, backward, backward_workspace_bytes,  # noqa:
                         logits_logp, merge, LinearLogpIndexed, LogitsLogpIndexed,
                         backward_indexed, forward_indexed, linear_logp_indexed,
                         logits_backward_indexed, logits_forward_indexed, logits_logp_indexed,
-                        Embedding, embedding, embedding_backward, embedding_forward)
+                        Embedding, embedding, embedding_backward, embedding_forward,
+                        Dropout, dropout, dropout_forward, LayerNorm, layer_norm,
+                        layer_norm_backward, layer_norm_forward)
 
 __all__ = [
     "FLP_BF16", "FLP_F16", "FLP_F32", "FLP_I32", "FLP_I64", "FLP_OK", "FlpError",
@@ -55,4 +60,9 @@ __all__ = [
     "LogitsLogpIndexed", "logits_forward_indexed", "logits_backward_indexed",
     "logits_logp_indexed",
     "Embedding", "embedding", "embedding_forward", "embedding_backward",
+    "flp_embedding_scaled_forward", "flp_embedding_scaled_backward",
+    "Dropout", "dropout", "dropout_forward", "flp_dropout",
+    "LayerNorm", "layer_norm", "layer_norm_forward", "layer_norm_backward",
+    "flp_layer_norm_forward", "flp_layer_norm_backward",
+    "flp_layer_norm_backward_workspace_bytes",
 ]

@@ -29,6 +29,7 @@ FLP_OK = 0
 
 # Every symbol include/flp.h declares, with (restype, argtypes).
 _i64, _sz, _vp, _fp, _int = ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int
+_float, _double = ctypes.c_float, ctypes.c_double
 SIGNATURES = {
     "flp_forward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "flp_forward": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _fp, _vp, _int, _fp, _fp, _fp, _vp,
@@ -60,6 +61,16 @@ SIGNATURES = {
     "flp_embedding_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "flp_embedding_backward": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _int, _vp, _int, _vp, _sz,
                                       _vp]),
+    "flp_embedding_scaled_forward": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _int, _float, _vp,
+                                            _vp]),
+    "flp_embedding_scaled_backward": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _int, _float, _vp,
+                                             _int, _vp, _sz, _vp]),
+    "flp_dropout": (_int, [_i64, _int, _vp, _double, _vp, _vp, _vp]),
+    "flp_layer_norm_forward": (_int, [_i64, _i64, _int, _vp, _int, _vp, _vp, _double, _vp, _fp, _fp,
+                                      _vp]),
+    "flp_layer_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "flp_layer_norm_backward": (_int, [_i64, _i64, _int, _vp, _vp, _int, _vp, _fp, _fp, _vp, _vp,
+                                       _vp, _vp, _sz, _vp]),
     "flp_probe_scratch_bytes": (_sz, []),
     "flp_probe_mfma": (_int, [_int, _i64, _vp, _sz, ctypes.POINTER(ctypes.c_double),
                               ctypes.POINTER(ctypes.c_double), _vp]),
@@ -248,6 +259,45 @@ def flp_embedding_backward(N, D, V, x_dtype, grad, ids, id_dtype, d_weight, dw_d
                                              dw_dtype, workspace, workspace_bytes, stream))
 
 
+def flp_embedding_scaled_forward(N, D, V, x_dtype, weight, ids, id_dtype, scale, out,
+                                 stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_embedding_scaled_forward(N, D, V, x_dtype, weight, ids, id_dtype, scale,
+                                                   out, stream))
+
+
+def flp_embedding_scaled_backward(N, D, V, x_dtype, grad, ids, id_dtype, scale, d_weight, dw_dtype,
+                                  workspace, workspace_bytes, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_embedding_scaled_backward(N, D, V, x_dtype, grad, ids, id_dtype, scale,
+                                                    d_weight, dw_dtype, workspace, workspace_bytes,
+                                                    stream))
+
+
+def flp_dropout(n, x_dtype, x, p, rng, out, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_dropout(n, x_dtype, x, p, rng, out, stream))
+
+
+def flp_layer_norm_forward(N, D, x_dtype, x, w_dtype, weight, bias, eps, out, out_mean, out_rstd,
+                           stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_layer_norm_forward(N, D, x_dtype, x, w_dtype, weight, bias, eps, out,
+                                             out_mean, out_rstd, stream))
+
+
+def flp_layer_norm_backward_workspace_bytes(N: int, D: int) -> int:
+    return int(load().flp_layer_norm_backward_workspace_bytes(N, D))
+
+
+def flp_layer_norm_backward(N, D, x_dtype, grad_out, x, w_dtype, weight, mean, rstd, d_x, d_weight,
+                            d_bias, workspace, workspace_bytes, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_layer_norm_backward(N, D, x_dtype, grad_out, x, w_dtype, weight, mean,
+                                              rstd, d_x, d_weight, d_bias, workspace,
+                                              workspace_bytes, stream))
+
+
 def flp_probe_scratch_bytes() -> int:
     return int(load().flp_probe_scratch_bytes())
 
@@ -268,7 +318,7 @@ def flp_probe_read(buffer: int, nbytes: int, scratch: int, scratch_bytes: int, s
 
 
 KERNEL_KINDS = ("forward", "merge", "dlogits", "transpose", "d_hidden", "d_weight", "d_bias",
-                "logits_forward", "logits_backward", "rows", "embedding")
+                "logits_forward", "logits_backward", "rows", "embedding", "dropout", "layer_norm")
 
 
 def flp_profile_enable(on: bool) -> None:

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -561,10 +562,17 @@ flp_status flp_logits_backward_indexed(int64_t N, int64_t V, flp_dtype x_dtype,
 flp_status flp_embedding_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
                                  const void* weight, const void* ids, flp_dtype id_dtype,
                                  void* out, void* stream) {
+  return flp_embedding_scaled_forward(N, D, V, x_dtype, weight, ids, id_dtype, 1.0f, out, stream);
+}
+
+flp_status flp_embedding_scaled_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                        const void* weight, const void* ids, flp_dtype id_dtype,
+                                        float scale, void* out, void* stream) {
   flp_status st = validate_embedding_forward(N, D, V, x_dtype, weight, ids, id_dtype, out);
+  if (st == FLP_OK && !std::isfinite(scale)) st = FLP_INVALID_ARGUMENT;
   if (st != FLP_OK || N == 0) return st;
   if ((st = check_device()) != FLP_OK) return st;
-  if (launch_embedding_forward(x_dtype, weight, ids, id_dtype == FLP_I64, N, D, V, out,
+  if (launch_embedding_forward(x_dtype, weight, ids, id_dtype == FLP_I64, N, D, V, scale, out,
                                static_cast<hipStream_t>(stream)) != hipSuccess)
     return FLP_HIP_ERROR;
   return FLP_OK;
@@ -579,8 +587,17 @@ flp_status flp_embedding_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_d
                                   const void* grad, const void* ids, flp_dtype id_dtype,
                                   void* d_weight, flp_dtype dw_dtype, void* workspace,
                                   size_t workspace_bytes, void* stream) {
+  return flp_embedding_scaled_backward(N, D, V, x_dtype, grad, ids, id_dtype, 1.0f, d_weight,
+                                       dw_dtype, workspace, workspace_bytes, stream);
+}
+
+flp_status flp_embedding_scaled_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                         const void* grad, const void* ids, flp_dtype id_dtype,
+                                         float scale, void* d_weight, flp_dtype dw_dtype,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
   flp_status st = validate_embedding_backward(N, D, V, x_dtype, grad, ids, id_dtype, d_weight,
                                               dw_dtype, workspace, workspace_bytes);
+  if (st == FLP_OK && !std::isfinite(scale)) st = FLP_INVALID_ARGUMENT;
   if (st != FLP_OK) return st;
   if (N == 0)
     return zero_sums(d_weight, size_t(V) * D * dtype_size(dw_dtype), nullptr, V,
@@ -606,7 +623,86 @@ flp_status flp_embedding_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_d
   a.head = reinterpret_cast<float*>(at(workspace, L.head_off));
   a.tail = reinterpret_cast<float*>(at(workspace, L.tail_off));
   a.d_weight = d_weight;
+  a.scale = scale;
   if (launch_embedding_backward(a, static_cast<hipStream_t>(stream)) != hipSuccess)
+    return FLP_HIP_ERROR;
+  return FLP_OK;
+}
+
+// ---- layer norm ----
+
+flp_status flp_layer_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                  flp_dtype w_dtype, const void* weight, const void* bias,
+                                  double eps, void* out, float* out_mean, float* out_rstd,
+                                  void* stream) {
+  flp_status st = validate_layer_norm_forward(N, D, x_dtype, x, w_dtype, weight, bias, eps, out,
+                                              out_mean, out_rstd);
+  if (st != FLP_OK || N == 0) return st;
+  if ((st = check_device()) != FLP_OK) return st;
+  NormFwdArgs a{};
+  a.N = N;
+  a.D = D;
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.eps = float(eps);
+  a.out = out;
+  a.mean = out_mean;
+  a.rstd = out_rstd;
+  if (launch_layer_norm_forward(x_dtype, w_dtype, a, static_cast<hipStream_t>(stream)) !=
+      hipSuccess)
+    return FLP_HIP_ERROR;
+  return FLP_OK;
+}
+
+size_t flp_layer_norm_backward_workspace_bytes(int64_t N, int64_t D) {
+  if (N < 1 || D < 1) return 0;
+  return norm_layout(N, D).total;
+}
+
+flp_status flp_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, const void* grad_out,
+                                   const void* x, flp_dtype w_dtype, const void* weight,
+                                   const float* mean, const float* rstd, void* d_x,
+                                   void* d_weight, void* d_bias, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  flp_status st = validate_layer_norm_backward(N, D, x_dtype, grad_out, x, w_dtype, weight, mean,
+                                               rstd, d_x, d_weight, d_bias, workspace,
+                                               workspace_bytes);
+  if (st != FLP_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool params = d_weight != nullptr || d_bias != nullptr;
+  if (!params && (d_x == nullptr || N == 0)) return FLP_OK;
+  if ((st = check_device()) != FLP_OK) return st;
+  const NormLayout L = norm_layout(N, D);
+  NormBwdArgs a{};
+  a.N = N;
+  a.D = D;
+  a.grad = grad_out;
+  a.x = x;
+  a.weight = weight;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.d_x = N > 0 ? d_x : nullptr;
+  a.d_weight = d_weight;
+  a.d_bias = d_bias;
+  a.slabs = N > 0 ? L.slabs : 0;  // no rows: the fold writes zeros
+  a.slab_rows = L.slab_rows;
+  a.part = static_cast<float*>(workspace);
+  if (launch_layer_norm_backward(x_dtype, w_dtype, a, s) != hipSuccess) return FLP_HIP_ERROR;
+  return FLP_OK;
+}
+
+// ---- dropout ----
+
+flp_status flp_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p, const int64_t* rng,
+                       void* out, void* stream) {
+  flp_status st = validate_dropout(n, x_dtype, x, p, rng, out);
+  if (st != FLP_OK || n == 0) return st;
+  if ((st = check_device()) != FLP_OK) return st;
+  const uint32_t drop = dropout_threshold(p);
+  const float scale = drop < 65536u ? 65536.0f / float(65536u - drop) : 0.0f;
+  if (launch_dropout(x_dtype, n, x, reinterpret_cast<const uint64_t*>(rng), drop, scale, out,
+                     static_cast<hipStream_t>(stream)) != hipSuccess)
     return FLP_HIP_ERROR;
   return FLP_OK;
 }

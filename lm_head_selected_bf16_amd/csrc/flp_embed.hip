@@ -5,8 +5,10 @@
 // misses FP64 parity, so here every segment accumulates in fp32 and rounds
 // once).
 //
-//   out[i]      = E[ids[i]]                 (a zero row for ids outside [0, V))
-//   d_E[v]      = sum over tokens i with ids[i] == v of grad[i], in ascending i
+//   out[i]      = s E[ids[i]]               (a zero row for ids outside [0, V))
+//   d_E[v]      = s (sum over tokens i with ids[i] == v of grad[i], in ascending i)
+//
+// with s = 1 for the plain lookup.
 //
 // The backward sorts the (id, token) pairs by id with a stable LSD radix sort
 // (8-bit digits, blocks of 256 keys; ranks inside a block come from an
@@ -24,6 +26,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "flp_launch.h"
 
 namespace flp {
@@ -38,11 +42,23 @@ __device__ __forceinline__ int64_t load_id(const void* ids, bool i64, int64_t i)
              : int64_t(reinterpret_cast<const int32_t*>(ids)[i]);
 }
 
-// One wave per token row, four rows per workgroup: 16-byte copies.
+// One 16-byte chunk times `scale`, rounded once per element.
+template <class T>
+__device__ __forceinline__ u32x4 scale_chunk(u32x4 v, float scale) {
+  typedef T vec __attribute__((ext_vector_type(16 / sizeof(T))));
+  vec x = __builtin_bit_cast(vec, v);
+#pragma unroll
+  for (int k = 0; k < int(16 / sizeof(T)); ++k) x[k] = T(float(x[k]) * scale);
+  return __builtin_bit_cast(u32x4, x);
+}
+
+// One wave per token row, four rows per workgroup: 16-byte chunks, copied as they are
+// (T = void) or multiplied by `scale`.
+template <class T>
 __global__ __launch_bounds__(256) void k_embed_fwd(const u32x4* __restrict__ weight,
                                                    const void* __restrict__ ids, int i64,
                                                    int64_t N, int64_t V, int64_t row_vec,
-                                                   u32x4* __restrict__ out) {
+                                                   float scale, u32x4* __restrict__ out) {
   const int lane = threadIdx.x & 63;
   const int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (i >= N) return;
@@ -50,7 +66,12 @@ __global__ __launch_bounds__(256) void k_embed_fwd(const u32x4* __restrict__ wei
   u32x4* dst = out + i * row_vec;
   if (v >= 0 && v < V) {
     const u32x4* src = weight + v * row_vec;
-    for (int64_t c = lane; c < row_vec; c += 64) dst[c] = src[c];
+    for (int64_t c = lane; c < row_vec; c += 64) {
+      if constexpr (std::is_void<T>::value)
+        dst[c] = src[c];
+      else
+        dst[c] = scale_chunk<T>(src[c], scale);
+    }
   } else {
     const u32x4 z = {0u, 0u, 0u, 0u};
     for (int64_t c = lane; c < row_vec; c += 64) dst[c] = z;
@@ -238,9 +259,12 @@ __device__ __forceinline__ uint32_t round_16(float f, bool f16) {
 }
 
 template <int XS, bool OUT_F32>
-__device__ __forceinline__ void store_chunk(const float* acc, void* dW, int64_t v, int64_t row_vec,
-                                            int64_t c, bool f16) {
+__device__ __forceinline__ void store_chunk(const float* sum, float scale, void* dW, int64_t v,
+                                            int64_t row_vec, int64_t c, bool f16) {
   constexpr int EPC = 16 / XS;
+  float acc[EPC];  // the finished fp32 sum times `scale` (1: the same bits), rounded below
+#pragma unroll
+  for (int k = 0; k < EPC; ++k) acc[k] = sum[k] * scale;
   if constexpr (OUT_F32) {
     float* out = static_cast<float*>(dW) + (v * row_vec + c) * EPC;
 #pragma unroll
@@ -269,12 +293,12 @@ __device__ __forceinline__ void store_chunk(const float* acc, void* dW, int64_t 
 constexpr int kSegGroup = int(kEmbSegGroup);
 
 template <int XS, bool OUT_F32>
-__device__ __forceinline__ void finish_run(const float* acc, int64_t j, int a, bool whole,
+__device__ __forceinline__ void finish_run(const float* acc, float scale, int64_t j, int a, bool whole,
                                            uint32_t k, float* head, float* tail, void* dW,
                                            int64_t row_vec, int64_t c, bool f16) {
   constexpr int EPC = 16 / XS;
   if (whole) {
-    store_chunk<XS, OUT_F32>(acc, dW, int64_t(k), row_vec, c, f16);
+    store_chunk<XS, OUT_F32>(acc, scale, dW, int64_t(k), row_vec, c, f16);
   } else {
     float* slot = (a == 0 ? head : tail) + (j * row_vec + c) * EPC;
 #pragma unroll
@@ -296,7 +320,7 @@ __global__ __launch_bounds__(256) void k_embed_runs(const u32x4* __restrict__ gr
                                                     int64_t V, int64_t row_vec,
                                                     float* __restrict__ head,
                                                     float* __restrict__ tail, void* __restrict__ dW,
-                                                    int64_t n_groups, ZeroRider z) {
+                                                    int64_t n_groups, float scale, ZeroRider z) {
   if (int64_t(blockIdx.x) >= n_groups) {
     ride(z, int64_t(blockIdx.x) - n_groups);
     return;
@@ -340,7 +364,7 @@ __global__ __launch_bounds__(256) void k_embed_runs(const u32x4* __restrict__ gr
     for (int p = 0; p < kSegGroup; ++p) {
       if (p < m) {
         if (p > a && skey[p] != skey[p - 1]) {
-          finish_run<XS, OUT_F32>(acc, j, a, whole[a] != 0, skey[p - 1], head, tail, dW,
+          finish_run<XS, OUT_F32>(acc, scale, j, a, whole[a] != 0, skey[p - 1], head, tail, dW,
                                   row_vec, c, f16 != 0);
 #pragma unroll
           for (int q = 0; q < EPC; ++q) acc[q] = 0.0f;
@@ -353,7 +377,7 @@ __global__ __launch_bounds__(256) void k_embed_runs(const u32x4* __restrict__ gr
       }
     }
     if (m > a)  // the group's last run
-      finish_run<XS, OUT_F32>(acc, j, a, whole[a] != 0, skey[a], head, tail, dW, row_vec, c,
+      finish_run<XS, OUT_F32>(acc, scale, j, a, whole[a] != 0, skey[a], head, tail, dW, row_vec, c,
                               f16 != 0);
   }
 }
@@ -371,7 +395,7 @@ __global__ __launch_bounds__(256) void k_embed_rows(const int32_t* __restrict__ 
                                                     int64_t V, int64_t row_vec,
                                                     const float* __restrict__ head,
                                                     const float* __restrict__ tail, int f16,
-                                                    void* __restrict__ dW) {
+                                                    float scale, void* __restrict__ dW) {
   constexpr int EPC = 16 / XS;
   __shared__ int32_t list[256];
   __shared__ int32_t count;
@@ -414,7 +438,7 @@ __global__ __launch_bounds__(256) void k_embed_rows(const int32_t* __restrict__ 
 #pragma unroll
         for (int q = 0; q < EPC; ++q) acc[q] += h[q];
       }
-      store_chunk<XS, OUT_F32>(acc, dW, v, row_vec, c, f16 != 0);
+      store_chunk<XS, OUT_F32>(acc, scale, dW, v, row_vec, c, f16 != 0);
     }
   }
 }
@@ -428,12 +452,23 @@ int embed_sort_passes(int64_t V) {
 }
 
 hipError_t launch_embedding_forward(flp_dtype x, const void* weight, const void* ids, bool i64,
-                                    int64_t N, int64_t D, int64_t V, void* out, hipStream_t s) {
+                                    int64_t N, int64_t D, int64_t V, float scale, void* out,
+                                    hipStream_t s) {
   ProfScope ps(FLP_K_EMBEDDING, s);
   const int64_t row_vec = D * int64_t(dtype_size(x)) / 16;
-  hipLaunchKernelGGL(k_embed_fwd, dim3(unsigned((N + 3) / 4)), dim3(256), 0, s,
-                     static_cast<const u32x4*>(weight), ids, int(i64), N, V, row_vec,
-                     static_cast<u32x4*>(out));
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned((N + 3) / 4)), dim3(256), 0, s,
+                       static_cast<const u32x4*>(weight), ids, int(i64), N, V, row_vec, scale,
+                       static_cast<u32x4*>(out));
+  };
+  if (scale == 1.0f)
+    launch(k_embed_fwd<void>);
+  else if (x == FLP_BF16)
+    launch(k_embed_fwd<__bf16>);
+  else if (x == FLP_F16)
+    launch(k_embed_fwd<_Float16>);
+  else
+    launch(k_embed_fwd<float>);
   return hipGetLastError();
 }
 
@@ -486,21 +521,21 @@ hipError_t launch_embedding_backward(const EmbedBwdArgs& a, hipStream_t s) {
   const int32_t* tok = a.vals[fin];
   if (a.x == FLP_F32) {
     hipLaunchKernelGGL((k_embed_runs<4, true>), ga, dim3(256), 0, s, g, 0, keys, tok, a.seg_begin,
-                       a.seg_end, N, V, row_vec, a.head, a.tail, a.d_weight, n_groups, zr);
+                       a.seg_end, N, V, row_vec, a.head, a.tail, a.d_weight, n_groups, a.scale, zr);
     hipLaunchKernelGGL((k_embed_rows<4, true>), gb, dim3(256), 0, s, a.seg_begin, a.seg_end, V,
-                       row_vec, a.head, a.tail, 0, a.d_weight);
+                       row_vec, a.head, a.tail, 0, a.scale, a.d_weight);
   } else if (a.dw == FLP_F32) {
     hipLaunchKernelGGL((k_embed_runs<2, true>), ga, dim3(256), 0, s, g, f16, keys, tok,
                        a.seg_begin, a.seg_end, N, V, row_vec, a.head, a.tail, a.d_weight,
-                       n_groups, zr);
+                       n_groups, a.scale, zr);
     hipLaunchKernelGGL((k_embed_rows<2, true>), gb, dim3(256), 0, s, a.seg_begin, a.seg_end, V,
-                       row_vec, a.head, a.tail, f16, a.d_weight);
+                       row_vec, a.head, a.tail, f16, a.scale, a.d_weight);
   } else {
     hipLaunchKernelGGL((k_embed_runs<2, false>), ga, dim3(256), 0, s, g, f16, keys, tok,
                        a.seg_begin, a.seg_end, N, V, row_vec, a.head, a.tail, a.d_weight,
-                       n_groups, zr);
+                       n_groups, a.scale, zr);
     hipLaunchKernelGGL((k_embed_rows<2, false>), gb, dim3(256), 0, s, a.seg_begin, a.seg_end, V,
-                       row_vec, a.head, a.tail, f16, a.d_weight);
+                       row_vec, a.head, a.tail, f16, a.scale, a.d_weight);
   }
   return hipGetLastError();
 }

@@ -137,11 +137,46 @@ struct EmbedBwdArgs {
   float* head;               // [ceil(N / kEmbSegGroup)][D] fp32 pieces of segments that span groups
   float* tail;               // same shape
   void* d_weight;            // [V][D] dw
+  float scale;               // factor of the summed gradient rows
 };
 int embed_sort_passes(int64_t V);
 hipError_t launch_embedding_forward(flp_dtype x, const void* weight, const void* ids, bool i64,
-                                    int64_t N, int64_t D, int64_t V, void* out, hipStream_t s);
+                                    int64_t N, int64_t D, int64_t V, float scale, void* out,
+                                    hipStream_t s);
 hipError_t launch_embedding_backward(const EmbedBwdArgs& a, hipStream_t s);
+
+// Layer norm (flp_norm.hip).
+struct NormFwdArgs {
+  int64_t N, D;
+  const void* x;             // [N][D]
+  const void* weight;        // [D] or null
+  const void* bias;          // [D] or null
+  float eps;
+  void* out;                 // [N][D]
+  float* mean;               // [N] or null
+  float* rstd;               // [N] or null
+};
+struct NormBwdArgs {
+  int64_t N, D;
+  const void* grad;          // [N][D]
+  const void* x;             // [N][D]
+  const void* weight;        // [D] or null
+  const float* mean;         // [N]
+  const float* rstd;         // [N]
+  void* d_x;                 // [N][D] or null
+  void* d_weight;            // [D] or null
+  void* d_bias;              // [D] or null
+  int64_t slabs, slab_rows;  // rows are summed in slabs of slab_rows
+  float* part;               // [slabs][2][D] partial d_weight and d_bias
+};
+hipError_t launch_layer_norm_forward(flp_dtype x, flp_dtype w, const NormFwdArgs& a,
+                                     hipStream_t s);
+hipError_t launch_layer_norm_backward(flp_dtype x, flp_dtype w, const NormBwdArgs& a,
+                                      hipStream_t s);
+
+// Dropout (flp_dropout.hip): elements whose 16 random bits are below `drop` become 0.
+hipError_t launch_dropout(flp_dtype x_dtype, int64_t n, const void* x, const uint64_t* rng,
+                          uint32_t drop, float scale, void* out, hipStream_t s);
 
 // Measurement probes (flp_probe.hip); they synchronise the stream.
 size_t probe_scratch_bytes();

@@ -561,4 +561,86 @@ flp_status validate_embedding_backward(int64_t N, int64_t D, int64_t V, flp_dtyp
   return FLP_OK;
 }
 
+NormLayout norm_layout(int64_t N, int64_t D) {
+  NormLayout L;
+  L.slab_rows = std::max(kNormMinRows, ceil_div(N, kNormSlabs));
+  L.slabs = ceil_div(N, L.slab_rows);
+  L.total = align_up(size_t(L.slabs) * 2 * size_t(D) * 4);
+  return L;
+}
+
+namespace {
+
+flp_status check_norm_dims(int64_t N, int64_t D, flp_dtype x, flp_dtype w) {
+  if (N < 0 || D < 1) return FLP_INVALID_ARGUMENT;
+  if (x != FLP_BF16 && x != FLP_F16 && x != FLP_F32) return FLP_UNSUPPORTED_DTYPE;
+  if (w != x && w != FLP_F32) return FLP_UNSUPPORTED_DTYPE;
+  // the column kernels take 32 columns per 256-thread workgroup of a launch
+  if (D >= (int64_t(1) << 28) || !mul_ok(std::max<int64_t>(N, 1), D)) return FLP_UNSUPPORTED_SHAPE;
+  return FLP_OK;
+}
+
+}  // namespace
+
+flp_status validate_layer_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                       flp_dtype w_dtype, const void* weight, const void* bias,
+                                       double eps, const void* out, const float* mean,
+                                       const float* rstd) {
+  flp_status st = check_norm_dims(N, D, x_dtype, w_dtype);
+  if (st != FLP_OK) return st;
+  if (!(eps >= 0.0) || eps > double(std::numeric_limits<float>::max())) return FLP_INVALID_ARGUMENT;
+  if (N == 0) return FLP_OK;
+  if (!x || !out) return FLP_INVALID_ARGUMENT;
+  const size_t xs = dtype_size(x_dtype), ws = dtype_size(w_dtype);
+  if (!aligned(x, xs) || !aligned(out, xs) || !aligned(weight, ws) || !aligned(bias, ws) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
+    return FLP_MISALIGNED;
+  const Span ins[] = {span(x, size_t(N) * D * xs), span(weight, size_t(D) * ws),
+                      span(bias, size_t(D) * ws)};
+  const Span outs[] = {span(out, size_t(N) * D * xs), span(mean, size_t(N) * 4),
+                       span(rstd, size_t(N) * 4)};
+  return any_alias(outs, 3, ins, 3) ? FLP_INVALID_ARGUMENT : FLP_OK;
+}
+
+flp_status validate_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, const void* grad,
+                                        const void* x, flp_dtype w_dtype, const void* weight,
+                                        const float* mean, const float* rstd, const void* d_x,
+                                        const void* d_weight, const void* d_bias,
+                                        const void* workspace, size_t workspace_bytes) {
+  flp_status st = check_norm_dims(N, D, x_dtype, w_dtype);
+  if (st != FLP_OK) return st;
+  const size_t xs = dtype_size(x_dtype), ws = dtype_size(w_dtype);
+  const bool params = d_weight != nullptr || d_bias != nullptr;
+  if (!d_x && !params) return FLP_OK;
+  if (N > 0 && (!grad || !x || !mean || !rstd || (params && !workspace)))
+    return FLP_INVALID_ARGUMENT;
+  if (!aligned(grad, xs) || !aligned(x, xs) || !aligned(d_x, xs) || !aligned(weight, ws) ||
+      !aligned(d_weight, ws) || !aligned(d_bias, ws) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+      !aligned(workspace, 16))
+    return FLP_MISALIGNED;
+  const Span ins[] = {span(grad, size_t(N) * D * xs), span(x, size_t(N) * D * xs),
+                      span(weight, size_t(D) * ws), span(mean, size_t(N) * 4),
+                      span(rstd, size_t(N) * 4)};
+  const Span outs[] = {span(d_x, size_t(N) * D * xs), span(d_weight, size_t(D) * ws),
+                       span(d_bias, size_t(D) * ws),
+                       span(params && N > 0 ? workspace : nullptr, workspace_bytes)};
+  if (any_alias(outs, 4, ins, 5)) return FLP_INVALID_ARGUMENT;
+  if (params && N > 0 && workspace_bytes < norm_layout(N, D).total) return FLP_WORKSPACE_TOO_SMALL;
+  return FLP_OK;
+}
+
+flp_status validate_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p,
+                            const int64_t* rng, const void* out) {
+  if (n < 0 || !(p >= 0.0 && p <= 1.0)) return FLP_INVALID_ARGUMENT;
+  if (x_dtype != FLP_BF16 && x_dtype != FLP_F16 && x_dtype != FLP_F32) return FLP_UNSUPPORTED_DTYPE;
+  if (!mul_ok(n, 4)) return FLP_UNSUPPORTED_SHAPE;
+  if (n == 0) return FLP_OK;
+  if (!x || !rng || !out) return FLP_INVALID_ARGUMENT;
+  const size_t xs = dtype_size(x_dtype);
+  if (!aligned(x, xs) || !aligned(out, xs) || !aligned(rng, 8)) return FLP_MISALIGNED;
+  const Span ins[] = {span(x, size_t(n) * xs), span(rng, 16)};
+  const Span outs[] = {span(out, size_t(n) * xs)};
+  return any_alias(outs, 1, ins, 2) ? FLP_INVALID_ARGUMENT : FLP_OK;
+}
+
 }  // namespace flp

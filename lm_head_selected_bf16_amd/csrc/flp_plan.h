@@ -100,6 +100,18 @@ struct EmbLayout {
 };
 EmbLayout emb_layout(int64_t N, int64_t D, int64_t V);
 
+// ---- layer norm backward: slabs of rows whose d_weight and d_bias partials are added ----
+constexpr int64_t kNormSlabs = 256;    // at most this many slabs (one workgroup per compute unit)
+constexpr int64_t kNormMinRows = 8;    // rows of a slab, at least
+struct NormLayout {
+  int64_t slab_rows = 0, slabs = 0;
+  size_t total = 0;       // fp32 [slabs][2][D]
+};
+NormLayout norm_layout(int64_t N, int64_t D);
+
+// ---- dropout: elements whose 16 random bits are below this are dropped (65536: all) ----
+inline uint32_t dropout_threshold(double p) { return uint32_t(p * 65536.0 + 0.5); }
+
 // ---- validation (pure host logic; never dereferences a pointer) ----
 flp_status validate_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
                             const void* hidden, const void* weight, const float* bias,
@@ -172,5 +184,18 @@ flp_status validate_embedding_backward(int64_t N, int64_t D, int64_t V, flp_dtyp
                                        const void* grad, const void* ids, flp_dtype id_dtype,
                                        const void* d_weight, flp_dtype dw_dtype,
                                        const void* workspace, size_t workspace_bytes);
+
+// Layer norm; the parameters have the rows' type or fp32.
+flp_status validate_layer_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                       flp_dtype w_dtype, const void* weight, const void* bias,
+                                       double eps, const void* out, const float* mean,
+                                       const float* rstd);
+flp_status validate_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, const void* grad,
+                                        const void* x, flp_dtype w_dtype, const void* weight,
+                                        const float* mean, const float* rstd, const void* d_x,
+                                        const void* d_weight, const void* d_bias,
+                                        const void* workspace, size_t workspace_bytes);
+flp_status validate_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p,
+                            const int64_t* rng, const void* out);
 
 }  // namespace flp

@@ -15,6 +15,8 @@ targets and temperature are not differentiable.
 """
 from __future__ import annotations
 
+import contextlib
+import math
 from typing import Optional, Tuple
 
 import torch
@@ -36,6 +38,14 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
 
 def _stream(device: torch.device) -> int:
     return int(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(device: torch.device):
+    """The device as the current one while a call is made (the library works on the current
+    HIP device)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _check(fn: str, status: int) -> None:
@@ -474,19 +484,32 @@ def _prepare_embedding(weight, ids):
     return V, D, ids.reshape(-1), int(ids.numel())
 
 
-def embedding_forward(weight: torch.Tensor, ids: torch.Tensor) -> torch.Tensor:
-    """weight[ids] with the ids' shape + [D], through flp_embedding_forward."""
+def _embedding_scale(scale) -> float:
+    scale = float(scale)
+    if not math.isfinite(scale):
+        raise ValueError("scale must be finite")
+    return scale
+
+
+def embedding_forward(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """scale * weight[ids] with the ids' shape + [D], through flp_embedding_scaled_forward."""
     V, D, i1, N = _prepare_embedding(weight, ids)
-    out = torch.empty(tuple(ids.shape) + (D,), dtype=weight.dtype, device=weight.device)
-    st = _abi.flp_embedding_forward(N, D, V, _X_DTYPES[weight.dtype], _ptr(weight), _ptr(i1),
-                                    _T_DTYPES[ids.dtype], _ptr(out), _stream(weight.device))
-    _check("flp_embedding_forward", st)
+    scale = _embedding_scale(scale)
+    dev = weight.device
+    if ids.device != dev:
+        raise ValueError("weight and ids must be on one device")
+    with _on(dev):
+        out = torch.empty(tuple(ids.shape) + (D,), dtype=weight.dtype, device=dev)
+        st = _abi.flp_embedding_scaled_forward(N, D, V, _X_DTYPES[weight.dtype], _ptr(weight),
+                                               _ptr(i1), _T_DTYPES[ids.dtype], scale, _ptr(out),
+                                               _stream(dev))
+    _check("flp_embedding_scaled_forward", st)
     return out
 
 
 def embedding_backward(grad: torch.Tensor, ids: torch.Tensor, num_embeddings: int,
-                       dw_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
-    """d_weight [V, D] of sum(grad * weight[ids]) through flp_embedding_backward."""
+                       dw_dtype: Optional[torch.dtype] = None, scale: float = 1.0) -> torch.Tensor:
+    """d_weight [V, D] of sum(grad * scale * weight[ids]) through flp_embedding_scaled_backward."""
     if grad.dtype not in _X_DTYPES or not grad.is_contiguous() or not grad.is_cuda:
         raise ValueError("grad must be a contiguous bfloat16 / float16 / float32 GPU tensor")
     if ids.dtype not in _T_DTYPES or not ids.is_contiguous():
@@ -494,36 +517,203 @@ def embedding_backward(grad: torch.Tensor, ids: torch.Tensor, num_embeddings: in
     D = int(grad.shape[-1])
     if tuple(grad.shape[:-1]) != tuple(ids.shape):
         raise ValueError("grad must have the ids' shape + [D]")
+    scale = _embedding_scale(scale)
     N, V = int(ids.numel()), int(num_embeddings)
     dwt = grad.dtype if dw_dtype is None else dw_dtype
     dev = grad.device
-    d_weight = torch.empty((V, D), dtype=dwt, device=dev)
-    ws = torch.empty(max(_abi.flp_embedding_backward_workspace_bytes(N, D, V), 16),
-                     dtype=torch.uint8, device=dev)
-    st = _abi.flp_embedding_backward(N, D, V, _X_DTYPES[grad.dtype], _ptr(grad), _ptr(ids),
-                                     _T_DTYPES[ids.dtype], _ptr(d_weight), _X_DTYPES[dwt],
-                                     _ptr(ws), ws.numel(), _stream(dev))
-    _check("flp_embedding_backward", st)
+    if ids.device != dev:
+        raise ValueError("grad and ids must be on one device")
+    with _on(dev):
+        d_weight = torch.empty((V, D), dtype=dwt, device=dev)
+        ws = torch.empty(max(_abi.flp_embedding_backward_workspace_bytes(N, D, V), 16),
+                         dtype=torch.uint8, device=dev)
+        st = _abi.flp_embedding_scaled_backward(N, D, V, _X_DTYPES[grad.dtype], _ptr(grad),
+                                                _ptr(ids), _T_DTYPES[ids.dtype], scale,
+                                                _ptr(d_weight), _X_DTYPES[dwt], _ptr(ws),
+                                                ws.numel(), _stream(dev))
+    _check("flp_embedding_scaled_backward", st)
     return d_weight
 
 
 class Embedding(torch.autograd.Function):
-    """Autograd node of the untied embedding lookup; the ids are not differentiable."""
+    """Autograd node of the untied embedding lookup; the ids and the scale are not
+    differentiable."""
 
     @staticmethod
-    def forward(ctx, weight, ids):
+    def forward(ctx, weight, ids, scale=1.0):
         ctx.save_for_backward(ids)
         ctx.num_embeddings = int(weight.shape[0])
-        return embedding_forward(weight, ids)
+        ctx.scale = scale
+        return embedding_forward(weight, ids, scale)
 
     @staticmethod
     def backward(ctx, grad):
         (ids,) = ctx.saved_tensors
         if not ctx.needs_input_grad[0]:
-            return None, None
-        return embedding_backward(grad.contiguous(), ids, ctx.num_embeddings), None
+            return None, None, None
+        return (embedding_backward(grad.contiguous(), ids, ctx.num_embeddings, scale=ctx.scale),
+                None, None)
 
 
-def embedding(weight, ids):
-    """weight[ids] (zero rows for ids outside [0, V)), differentiable in weight."""
-    return Embedding.apply(weight, ids)
+def embedding(weight, ids, scale=1.0):
+    """scale * weight[ids] (zero rows for ids outside [0, V)), differentiable in weight."""
+    return Embedding.apply(weight, ids, scale)
+
+
+# ---- dropout ------------------------------------------------------------------------------------
+#
+# The mask is a function of the element's position, p and rng (int64 [2] on the device: seed and
+# offset), so it is drawn again in the backward instead of being stored.
+
+def dropout_forward(x: torch.Tensor, p: float, rng: torch.Tensor) -> torch.Tensor:
+    """x with each element dropped with probability p and the others scaled, through flp_dropout."""
+    if x.dtype not in _X_DTYPES:
+        raise TypeError("x must be bfloat16, float16 or float32")
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous GPU tensor")
+    if rng.dtype != torch.int64 or tuple(rng.shape) != (2,):
+        raise ValueError("rng must be int64 [2]: seed and offset")
+    if rng.device != x.device or not rng.is_contiguous():
+        raise ValueError("rng must be contiguous and on the device of x")
+    p = float(p)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError("p must be between 0 and 1")
+    with _on(x.device):
+        out = torch.empty_like(x)
+        st = _abi.flp_dropout(x.numel(), _X_DTYPES[x.dtype], _ptr(x), p, _ptr(rng), _ptr(out),
+                              _stream(x.device))
+    _check("flp_dropout", st)
+    return out
+
+
+class Dropout(torch.autograd.Function):
+    """Autograd node of dropout: the backward is the same call on the gradient."""
+
+    @staticmethod
+    def forward(ctx, x, p, rng):
+        ctx.save_for_backward(rng)
+        ctx.p = p
+        return dropout_forward(x, p, rng)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (rng,) = ctx.saved_tensors
+        if not ctx.needs_input_grad[0]:
+            return None, None, None
+        return dropout_forward(grad.contiguous(), ctx.p, rng), None, None
+
+
+def dropout(x, p, rng):
+    """x with each element dropped with probability p and the others times 1 / (1 - p),
+    differentiable in x.  rng: int64 [2] on the device of x, (seed, offset); give every call of a
+    step its own offset.  The backward reads rng again, so write a new pair into a new tensor
+    rather than changing this one before the backward has run."""
+    return Dropout.apply(x, p, rng)
+
+
+# ---- layer norm ---------------------------------------------------------------------------------
+
+def _prepare_norm(x, weight, bias):
+    if x.dtype not in _X_DTYPES:
+        raise TypeError("x must be bfloat16, float16 or float32")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have a last dimension of at least one element")
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous GPU tensor")
+    D = int(x.shape[-1])
+    wd = x.dtype
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        if t.dtype not in (x.dtype, torch.float32):
+            raise TypeError(f"{name} must have the dtype of x or float32")
+        if tuple(t.shape) != (D,) or not t.is_contiguous() or t.device != x.device:
+            raise ValueError(f"{name} must be contiguous [D] on the device of x")
+        wd = t.dtype
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same dtype")
+    return x.numel() // D, D, wd
+
+
+def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                       return_stats: bool = True):
+    """(out, mean, rstd) of the layer norm over the last dimension through
+    flp_layer_norm_forward; mean and rstd are float32 of the leading shape, or None."""
+    N, D, wd = _prepare_norm(x, weight, bias)
+    dev = x.device
+    with _on(dev):
+        out = torch.empty_like(x)
+        mean = rstd = None
+        if return_stats:
+            mean, rstd = torch.empty((2,) + tuple(x.shape[:-1]), dtype=torch.float32,
+                                     device=dev).unbind(0)
+        st = _abi.flp_layer_norm_forward(N, D, _X_DTYPES[x.dtype], _ptr(x), _X_DTYPES[wd],
+                                         _ptr(weight), _ptr(bias), float(eps), _ptr(out),
+                                         _ptr(mean), _ptr(rstd), _stream(dev))
+    _check("flp_layer_norm_forward", st)
+    return out, mean, rstd
+
+
+def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
+                        rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                        need_input: bool = True, need_weight: bool = True, need_bias: bool = True,
+                        w_dtype: Optional[torch.dtype] = None):
+    """(d_x, d_weight, d_bias) through flp_layer_norm_backward; unrequested ones are None.
+    d_weight and d_bias have w_dtype (the weight's, by default)."""
+    N, D, wd = _prepare_norm(x, weight, None)
+    if w_dtype is not None:
+        if w_dtype not in (x.dtype, torch.float32) or (weight is not None and w_dtype != wd):
+            raise TypeError("w_dtype must be the weight's dtype, or that of x or float32")
+        wd = w_dtype
+    if grad_out.dtype != x.dtype or grad_out.shape != x.shape or not grad_out.is_contiguous():
+        raise ValueError("grad_out must be contiguous with the dtype and shape of x")
+    lead = tuple(x.shape[:-1])
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or tuple(t.shape) != lead or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous float32 with the leading shape of x")
+    dev = x.device
+    if any(t.device != dev for t in (grad_out, mean, rstd)):
+        raise ValueError("grad_out, mean and rstd must be on the device of x")
+    with _on(dev):
+        d_x = torch.empty_like(x) if need_input else None
+        d_weight = torch.empty(D, dtype=wd, device=dev) if need_weight else None
+        d_bias = torch.empty(D, dtype=wd, device=dev) if need_bias else None
+        ws = None
+        if need_weight or need_bias:
+            ws = torch.empty(max(_abi.flp_layer_norm_backward_workspace_bytes(N, D), 16),
+                             dtype=torch.uint8, device=dev)
+        st = _abi.flp_layer_norm_backward(N, D, _X_DTYPES[x.dtype], _ptr(grad_out), _ptr(x),
+                                          _X_DTYPES[wd], _ptr(weight), _ptr(mean), _ptr(rstd),
+                                          _ptr(d_x), _ptr(d_weight), _ptr(d_bias), _ptr(ws),
+                                          0 if ws is None else ws.numel(), _stream(dev))
+    _check("flp_layer_norm_backward", st)
+    return d_x, d_weight, d_bias
+
+
+class LayerNorm(torch.autograd.Function):
+    """Autograd node of the layer norm; the forward saves the mean and rstd of every row."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        out, mean, rstd = layer_norm_forward(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.w_dtype = next((t.dtype for t in (weight, bias) if t is not None), None)
+        return out
+
+    @staticmethod
+    def backward(ctx, grad):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need_x, need_w, need_b, _ = ctx.needs_input_grad
+        dx, dw, db = layer_norm_backward(grad.contiguous(), x, mean, rstd, weight, need_x, need_w,
+                                         need_b, ctx.w_dtype)
+        return dx, dw, db, None
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """(x - mean) / sqrt(var + eps) * weight + bias over the last dimension, differentiable in
+    x, weight and bias; weight and bias [D] in the dtype of x or float32."""
+    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad
+                                              for t in (x, weight, bias)):
+        return layer_norm_forward(x, weight, bias, eps, return_stats=False)[0]
+    return LayerNorm.apply(x, weight, bias, eps)

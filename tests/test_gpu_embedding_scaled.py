@@ -1,0 +1,98 @@
+"""The scaled embedding against its definition in 64 bits, and against the plain lookup at
+scale 1 (the same bits)."""
+import math
+
+import pytest
+import torch
+
+import flp_inputs
+import oracle
+from gpu_common import flp, say
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+CASES = [  # dtype, N, D, V, ids, ids outside the table, id type, d_weight type
+    (BF16, 3000, 64, 5000, "zipf", (-1, 5000), torch.int64, None),
+    (BF16, 700, 2688, 900, "uniform", (), torch.int32, F32),
+    (F16, 700, 96, 300, "zipf", (300,), torch.int64, None),
+    (F32, 900, 36, 2000, "zipf", (-2,), torch.int32, None),
+    (BF16, 1500, 64, 4000, "same", (), torch.int64, None),
+    (F32, 1, 4, 1, "uniform", (), torch.int64, None),
+]
+
+
+@pytest.mark.parametrize("scale", [math.sqrt(2688), -0.3, 2.0 ** -40, 0.0])
+@pytest.mark.parametrize("k", range(len(CASES)))
+def test_parity(k, scale):
+    dtype, N, D, V, draw, bad, idt, dwt = CASES[k]
+    inp = flp_inputs.make_embedding_inputs(N, D, V, dtype, 60 + k, ids=draw, invalid=bad)
+    m = flp()
+    ids = inp["ids"].to(idt).cuda()
+    w, g = inp["weight"].cuda(), inp["grad"].cuda()
+    out = m.embedding_forward(w, ids, scale)
+    dw = m.embedding_backward(g, ids, V, dw_dtype=dwt, scale=scale)
+    s32 = float(torch.tensor(scale, dtype=F32))  # the factor enters in fp32
+    ref = torch.from_numpy(oracle.embedding_forward(inp["weight"], inp["ids"])) * s32
+    tiny = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    err = (out.double().cpu() - ref).abs()
+    # the product is exact to 24 bits in fp32, then rounded to the type
+    assert bool((err <= ref.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -24) + tiny).all())
+    exact = torch.from_numpy(oracle.embedding_backward(inp["grad"], inp["ids"], V)) * s32
+    size = torch.from_numpy(oracle.embedding_backward(inp["grad"].abs(), inp["ids"], V)) * abs(s32)
+    wt = dw.dtype
+    # at most N fp32 additions, the product and the final rounding
+    tol = size * N * 2.0 ** -24 + exact.abs() * (torch.finfo(wt).eps / 2 + 2.0 ** -24)
+    tiny = torch.finfo(wt).smallest_normal * torch.finfo(wt).eps
+    err = (dw.double().cpu() - exact).abs()
+    say(f"  case {k} scale {scale}: d_weight max error {float(err.max()):.3e}")
+    assert bool((err <= tol + tiny).all())
+
+
+def test_scale_one_is_the_plain_lookup():
+    inp = flp_inputs.make_embedding_inputs(2000, 128, 700, BF16, 70, ids="zipf", invalid=(-1,))
+    m = flp()
+    w, ids, g = inp["weight"].cuda(), inp["ids"].cuda(), inp["grad"].cuda()
+    w[3, 5] = float("nan")
+    w[4, 6] = float("inf")
+    plain, scaled = torch.empty(2000, 128, dtype=BF16, device="cuda"), None
+    st = m.flp_embedding_forward(2000, 128, 700, m.FLP_BF16, w.data_ptr(), ids.data_ptr(),
+                                 m.FLP_I64, plain.data_ptr(),
+                                 torch.cuda.current_stream().cuda_stream)
+    assert st == m.FLP_OK
+    scaled = m.embedding(w, ids, scale=1.0)
+    assert torch.equal(plain.view(torch.int16), scaled.view(torch.int16))
+    # a power of two scales every gradient exactly
+    a, b = m.embedding_backward(g, ids, 700), m.embedding_backward(g, ids, 700, scale=0.5)
+    assert torch.equal(a.float() * 0.5, b.float())
+
+
+def test_autograd_and_ids_outside_the_table():
+    m = flp()
+    w = torch.randn(50, 64, device="cuda", requires_grad=True)
+    ids = torch.tensor([[3, -1, 50], [3, 49, 1 << 40]], device="cuda")
+    out = m.embedding(w, ids, scale=8.0)
+    assert out.shape == (2, 3, 64)
+    assert not out[0, 1:].any() and not out[1, 2].any()
+    g = torch.randn_like(out)
+    (dw,) = torch.autograd.grad(out, [w], g)
+    ref = torch.zeros(50, 64, device="cuda", dtype=torch.float64)
+    ref[3] = 8 * (g[0, 0].double() + g[1, 0].double())
+    ref[49] = 8 * g[1, 1].double()
+    assert bool(((dw.double() - ref).abs() <= ref.abs() * 2 ** -23 + 16 * 2.0 ** -24).all())
+    empty = m.embedding(w, ids[:0], scale=8.0)
+    (dw,) = torch.autograd.grad(empty, [w], torch.empty_like(empty))
+    assert empty.shape == (0, 3, 64) and not dw.any()
+
+
+def test_refusals():
+    m = flp()
+    w = torch.randn(50, 64, device="cuda")
+    ids = torch.zeros(3, dtype=torch.int64, device="cuda")
+    for bad in (float("nan"), float("inf")):
+        with pytest.raises(ValueError):
+            m.embedding(w, ids, scale=bad)
+    with pytest.raises(ValueError):
+        m.embedding(w, ids.cpu(), scale=2.0)
+    with pytest.raises(m.FlpError):
+        m.embedding(torch.randn(5, 6, device="cuda"), ids, scale=2.0)
