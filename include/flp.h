@@ -412,6 +412,72 @@ flp_status flp_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p, co
                        void* out, void* stream);
 
 /*
+ * Softmax cross entropy of the projected rows, without keeping the logits
+ * z_iv = hidden_i . W_v + b_v: the training loss whose per-token part is -logp of
+ * flp_forward, with label smoothing s and a squared log-partition term c:
+ *
+ *   loss_i = (1 - s) (lse_i - z_i[t_i]) + s (lse_i - mean_v z_iv) + c lse_i^2
+ *
+ * for rows whose target lies in [0, V); the others (padding) have loss 0 exactly, take
+ * part in no sum or count and get zero gradients, whatever their hidden row holds.
+ *
+ *   label_smoothing  0 <= s <= 1.   z_loss  c >= 0, finite.
+ *   reduction    FLP_REDUCE_NONE: out_loss [N]; FLP_REDUCE_SUM: out_loss [1], the sum;
+ *                FLP_REDUCE_MEAN: out_loss [1], the sum over the number of counted rows
+ *                (0 when there are none).
+ *   out_loss     float32.
+ *   out_stats    [2, N] float32, or NULL: lse, and the part of it that its rounding left
+ *                out (0 unless lse is large); the backward reads both.
+ *   workspace    >= flp_cross_entropy_forward_workspace_bytes(N, D, V), 16-byte aligned.
+ *   N = 0 writes 0 to a reduced loss.
+ *   Everything else as for flp_forward.
+ *
+ * A vocabulary entry masked through the bias (-infinity, or the lowest float32) has
+ * probability 0; with label smoothing an entry of -infinity makes the loss infinite, as
+ * its definition does.  The rows' losses and lse do not depend on the other rows; the
+ * reductions add the rows in an order fixed by N.
+ */
+typedef enum flp_reduction {
+  FLP_REDUCE_NONE = 0,
+  FLP_REDUCE_SUM = 1,
+  FLP_REDUCE_MEAN = 2
+} flp_reduction;
+
+size_t flp_cross_entropy_forward_workspace_bytes(int64_t N, int64_t D, int64_t V);
+flp_status flp_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                     const void* hidden, const void* weight, const float* bias,
+                                     const void* targets, flp_dtype t_dtype,
+                                     double label_smoothing, double z_loss,
+                                     flp_reduction reduction, float* out_loss, float* out_stats,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+/*
+ *   dz_iv    = g_i ((1 + 2 c lse_i) exp(z_iv - lse_i) - (1 - s) onehot(t_i)_v - s / V)
+ *   d_hidden = dz W,  d_weight = dz^T hidden,  d_bias = sum_i dz_i
+ *
+ * g_i is grad_out[i] (FLP_REDUCE_NONE), grad_out[0] (FLP_REDUCE_SUM) or grad_out[0] over
+ * the number of counted rows (FLP_REDUCE_MEAN), 0 for rows that are not counted.
+ *
+ *   stats      [2, N] as written by the forward for the same inputs.
+ *   d_hidden [N, D], d_weight [V, D] x_dtype, d_bias [V] float32: each may be NULL.
+ *   workspace  >= flp_cross_entropy_backward_workspace_bytes(N, D, V, x_dtype, 0);
+ *              chunk_rows as for flp_backward_workspace_bytes.
+ *
+ * For FLP_F16, dz is held times a power of two that brings its largest row factor to
+ * 2^10, taken back when the fp32 sums are rounded: small gradients (a mean over many
+ * rows) do not underflow on the way.
+ */
+size_t flp_cross_entropy_backward_workspace_bytes(int64_t N, int64_t D, int64_t V,
+                                                  flp_dtype x_dtype, int64_t chunk_rows);
+flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                      const float* grad_out, const float* stats,
+                                      const void* hidden, const void* weight, const float* bias,
+                                      const void* targets, flp_dtype t_dtype,
+                                      double label_smoothing, double z_loss,
+                                      flp_reduction reduction, void* d_hidden, void* d_weight,
+                                      float* d_bias, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
  * Layer norm of the rows x[i, :], as it stands in front of the head:
  *
  *   mean_i = sum_d x_id / D,   rstd_i = 1 / sqrt(sum_d (x_id - mean_i)^2 / D + eps)
@@ -500,7 +566,8 @@ typedef enum flp_kernel_kind {
   FLP_K_EMBEDDING = 10, /* flp_embedding_forward / flp_embedding_backward */
   FLP_K_DROPOUT = 11,   /* flp_dropout */
   FLP_K_LAYER_NORM = 12, /* flp_layer_norm_forward / flp_layer_norm_backward */
-  FLP_K_COUNT = 13
+  FLP_K_LOSS = 13,      /* flp_cross_entropy_*: row losses, their sum, gradient factors */
+  FLP_K_COUNT = 14
 } flp_kernel_kind;
 
 void flp_profile_enable(int on);

@@ -20,6 +20,9 @@ from ._abi import (FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpErro
                    flp_backward_workspace_bytes, flp_build_info, flp_embedding_backward,
                    flp_embedding_backward_workspace_bytes, flp_embedding_forward,
                    flp_embedding_scaled_backward, flp_embedding_scaled_forward, flp_forward,
+                   FLP_REDUCE_MEAN, FLP_REDUCE_NONE, FLP_REDUCE_SUM, flp_cross_entropy_backward,
+                   flp_cross_entropy_backward_workspace_bytes, flp_cross_entropy_forward,
+                   flp_cross_entropy_forward_workspace_bytes,
                    flp_dropout, flp_layer_norm_backward, flp_layer_norm_backward_workspace_bytes,
                    flp_layer_norm_forward,
                    flp_forward_indexed, flp_forward_noalloc, FLP_FORWARD_NOALLOC_MAX_BYTES,
@@ -36,6 +39,8 @@ from .torch_ops import (LinearLogp, backward, backward_workspace_bytes,  # noqa:
                         backward_indexed, forward_indexed, linear_logp_indexed,
                         logits_backward_indexed, logits_forward_indexed, logits_logp_indexed,
                         Embedding, embedding, embedding_backward, embedding_forward,
+                        LinearCrossEntropy, cross_entropy_backward, cross_entropy_forward,
+                        linear_cross_entropy,
                         Dropout, dropout, dropout_forward, LayerNorm, layer_norm,
                         layer_norm_backward, layer_norm_forward)
 
@@ -61,6 +66,10 @@ __all__ = [
     "logits_logp_indexed",
     "Embedding", "embedding", "embedding_forward", "embedding_backward",
     "flp_embedding_scaled_forward", "flp_embedding_scaled_backward",
+    "LinearCrossEntropy", "linear_cross_entropy", "cross_entropy_forward",
+    "cross_entropy_backward", "flp_cross_entropy_forward", "flp_cross_entropy_backward",
+    "flp_cross_entropy_forward_workspace_bytes", "flp_cross_entropy_backward_workspace_bytes",
+    "FLP_REDUCE_NONE", "FLP_REDUCE_SUM", "FLP_REDUCE_MEAN",
     "Dropout", "dropout", "dropout_forward", "flp_dropout",
     "LayerNorm", "layer_norm", "layer_norm_forward", "layer_norm_backward",
     "flp_layer_norm_forward", "flp_layer_norm_backward",

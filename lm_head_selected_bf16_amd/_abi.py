@@ -14,6 +14,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libflp.so")
 
 # flp_dtype
 FLP_BF16, FLP_F32, FLP_I64, FLP_I32, FLP_F16 = 0, 1, 2, 3, 4
+# flp_reduction
+FLP_REDUCE_NONE, FLP_REDUCE_SUM, FLP_REDUCE_MEAN = 0, 1, 2
 # flp_status
 STATUS_NAMES = {
     0: "FLP_OK",
@@ -65,6 +67,13 @@ SIGNATURES = {
                                             _vp]),
     "flp_embedding_scaled_backward": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _int, _float, _vp,
                                              _int, _vp, _sz, _vp]),
+    "flp_cross_entropy_forward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "flp_cross_entropy_forward": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _fp, _vp, _int, _double,
+                                         _double, _int, _fp, _fp, _vp, _sz, _vp]),
+    "flp_cross_entropy_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _i64]),
+    "flp_cross_entropy_backward": (_int, [_i64, _i64, _i64, _int, _fp, _fp, _vp, _vp, _fp, _vp,
+                                          _int, _double, _double, _int, _vp, _vp, _fp, _vp, _sz,
+                                          _vp]),
     "flp_dropout": (_int, [_i64, _int, _vp, _double, _vp, _vp, _vp]),
     "flp_layer_norm_forward": (_int, [_i64, _i64, _int, _vp, _int, _vp, _vp, _double, _vp, _fp, _fp,
                                       _vp]),
@@ -274,6 +283,35 @@ def flp_embedding_scaled_backward(N, D, V, x_dtype, grad, ids, id_dtype, scale, 
                                                     stream))
 
 
+def flp_cross_entropy_forward_workspace_bytes(N: int, D: int, V: int) -> int:
+    return int(load().flp_cross_entropy_forward_workspace_bytes(N, D, V))
+
+
+def flp_cross_entropy_forward(N, D, V, x_dtype, hidden, weight, bias, targets, t_dtype,
+                              label_smoothing, z_loss, reduction, out_loss, out_stats, workspace,
+                              workspace_bytes, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_cross_entropy_forward(N, D, V, x_dtype, hidden, weight, bias, targets,
+                                                t_dtype, label_smoothing, z_loss, reduction,
+                                                out_loss, out_stats, workspace, workspace_bytes,
+                                                stream))
+
+
+def flp_cross_entropy_backward_workspace_bytes(N: int, D: int, V: int, x_dtype: int,
+                                               chunk_rows: int = 0) -> int:
+    return int(load().flp_cross_entropy_backward_workspace_bytes(N, D, V, x_dtype, chunk_rows))
+
+
+def flp_cross_entropy_backward(N, D, V, x_dtype, grad_out, stats, hidden, weight, bias, targets,
+                               t_dtype, label_smoothing, z_loss, reduction, d_hidden, d_weight,
+                               d_bias, workspace, workspace_bytes, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_cross_entropy_backward(N, D, V, x_dtype, grad_out, stats, hidden, weight,
+                                                 bias, targets, t_dtype, label_smoothing, z_loss,
+                                                 reduction, d_hidden, d_weight, d_bias, workspace,
+                                                 workspace_bytes, stream))
+
+
 def flp_dropout(n, x_dtype, x, p, rng, out, stream) -> int:
     """Raw call: every pointer argument is an int address (0 for NULL)."""
     return int(load().flp_dropout(n, x_dtype, x, p, rng, out, stream))
@@ -318,7 +356,8 @@ def flp_probe_read(buffer: int, nbytes: int, scratch: int, scratch_bytes: int, s
 
 
 KERNEL_KINDS = ("forward", "merge", "dlogits", "transpose", "d_hidden", "d_weight", "d_bias",
-                "logits_forward", "logits_backward", "rows", "embedding", "dropout", "layer_norm")
+                "logits_forward", "logits_backward", "rows", "embedding", "dropout", "layer_norm",
+                "loss")
 
 
 def flp_profile_enable(on: bool) -> None:

@@ -17,7 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libflp.so")
-SOURCES = ["flp_kernels.hip", "flp_rows.hip", "flp_embed.hip", "flp_dropout.hip", "flp_norm.hip",
+SOURCES = ["flp_kernels.hip", "flp_rows.hip", "flp_loss.hip", "flp_embed.hip", "flp_dropout.hip", "flp_norm.hip",
            "flp_probe.hip", "flp_noalloc.hip",
            "flp_api.cpp", "flp_plan.cpp"]
 

@@ -50,6 +50,119 @@ flp_status zero_sums(void* d_weight, size_t dw_bytes, float* d_bias, int64_t V, 
   return FLP_OK;
 }
 
+// The chunk loop of a validated, non-empty backward.  With `loss`, dz takes the cross
+// entropy's form: grad_out holds the softmax's factors and *loss the other terms, both
+// written by launch_loss_grad.
+flp_status enqueue_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                            const float* grad_out, const float* lse, const void* hidden,
+                            const void* weight, const float* bias, const void* targets,
+                            flp_dtype t_dtype, const float* temperature, const LossGradArgs* loss,
+                            void* d_hidden, void* d_weight, flp_dtype dw_dtype, float* d_bias,
+                            void* workspace, size_t workspace_bytes, hipStream_t s) {
+  const BwdLayout L = bwd_layout_for_bytes(N, D, V, x_dtype, dw_dtype, workspace_bytes,
+                                           d_hidden != nullptr, d_weight != nullptr,
+                                           d_bias != nullptr);
+  const size_t xs = dtype_size(x_dtype);
+  const size_t ts = dtype_size(t_dtype);
+  void* dz = d_hidden ? at(workspace, L.dz_off) : nullptr;
+  void* wT = d_hidden ? at(workspace, L.wt_off) : nullptr;
+  void* dzT = d_weight ? at(workspace, L.dzt_off) : nullptr;
+  void* hT = d_weight ? at(workspace, L.ht_off) : nullptr;
+  float* dbp = d_bias ? reinterpret_cast<float*>(at(workspace, L.dbp_off)) : nullptr;
+  const float* scale = loss != nullptr && loss->rescale ? loss->unscale : nullptr;
+  float* acc = nullptr;
+  if (d_weight) {
+    if (dw_dtype == FLP_F32)
+      acc = static_cast<float*>(d_weight);
+    else if (L.use_acc)
+      acc = reinterpret_cast<float*>(at(workspace, L.acc_off));
+  }
+  for (int64_t c = 0; c < L.n_chunks; ++c) {
+    const int64_t r0 = c * L.chunk;
+    const int64_t rows = (N - r0 < L.chunk) ? N - r0 : L.chunk;
+    const bool last = c + 1 == L.n_chunks;
+    const void* h_chunk = static_cast<const char*>(hidden) + size_t(r0) * D * xs;
+    DzArgs z;
+    z.hidden = h_chunk;
+    z.weight = weight;
+    z.bias = bias;
+    z.targets = static_cast<const char*>(targets) + size_t(r0) * ts;
+    z.t64 = t_dtype == FLP_I64;
+    z.temperature = temperature ? temperature + r0 : nullptr;
+    z.grad_out = grad_out + r0;
+    z.lse = lse + r0;
+    z.rows = rows;
+    z.D = D;
+    z.V = V;
+    z.ldz = L.ldz;
+    z.ldt = L.ldt;
+    z.dz = dz;
+    z.dzT = dzT;
+    z.dbias_part = dbp;
+    if (loss != nullptr) {
+      z.onehot = loss->onehot + r0;
+      z.uniform = loss->uniform + r0;
+      z.lse_rest = loss->lse_rest + r0;
+    }
+    if (launch_dz(x_dtype, z, s) != hipSuccess) return FLP_HIP_ERROR;
+    if (d_hidden) {
+      // W^T is made once, after the first dlogits: that kernel re-reads hidden, which
+      // the forward left in the Infinity Cache and streaming 1.4 GB of W and W^T
+      // through it first would evict.
+      if (c == 0 && launch_transpose(x_dtype, weight, V, L.ldz, D, D, wT, s) != hipSuccess)
+        return FLP_HIP_ERROR;
+      GemmArgs g;
+      g.a = dz;
+      g.b = wT;
+      g.lda_b = 128;
+      g.ldb_b = 128;
+      g.a_ks = L.ldt * 128;
+      g.b_ks = D * 128;
+      g.M = rows;
+      g.N = D;
+      g.K = L.ldz;  // dz and W^T are zero past V
+      g.out = static_cast<char*>(d_hidden) + size_t(r0) * D * xs;
+      g.ldo = D;
+      g.acc = nullptr;
+      g.load_acc = 0;
+      g.store_acc = 0;
+      g.scale = scale;
+      if (launch_dx(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
+    }
+    if (d_weight) {
+      const int64_t kpad = round_up(rows, kTokPad);  // dz^T and hidden^T are zero past rows
+      const hipError_t e =
+          loss != nullptr ? launch_transpose_live(x_dtype, h_chunk, rows, kpad, D, z.targets,
+                                                  t_dtype == FLP_I64, V, hT, s)
+                          : launch_transpose(x_dtype, h_chunk, rows, kpad, D, D, hT, s);
+      if (e != hipSuccess) return FLP_HIP_ERROR;
+      GemmArgs g;
+      g.a = dzT;
+      g.b = hT;
+      g.lda_b = 128;
+      g.ldb_b = 128;
+      g.a_ks = L.ldz * 128;
+      g.b_ks = D * 128;
+      g.M = V;
+      g.N = D;
+      g.K = kpad;
+      g.out = d_weight;
+      g.ldo = D;
+      g.acc = acc;
+      g.load_acc = (acc != nullptr && c > 0) ? 1 : 0;
+      g.store_acc = (acc != nullptr && (dw_dtype == FLP_F32 || !last)) ? 1 : 0;
+      g.scale = scale;
+      if (launch_dw(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
+    }
+    if (d_bias) {
+      if (launch_dbias_fold(dbp, (rows + kDzRowTile - 1) / kDzRowTile, L.ldz, V, d_bias, c == 0, scale,
+                            s) != hipSuccess)
+        return FLP_HIP_ERROR;
+    }
+  }
+  return FLP_OK;
+}
+
 // ---- optional per-kernel event timing ----
 struct ProfRec {
   int kind;
@@ -285,97 +398,9 @@ flp_status flp_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
   if (N == 0) return zero_sums(d_weight, size_t(V) * D * dtype_size(dw_dtype), d_bias, V, s);
   if (!d_hidden && !d_weight && !d_bias) return FLP_OK;
   if ((st = check_device()) != FLP_OK) return st;
-  const BwdLayout L = bwd_layout_for_bytes(N, D, V, x_dtype, dw_dtype, workspace_bytes,
-                                           d_hidden != nullptr, d_weight != nullptr,
-                                           d_bias != nullptr);
-  const size_t xs = dtype_size(x_dtype);
-  const size_t ts = dtype_size(t_dtype);
-  void* dz = d_hidden ? at(workspace, L.dz_off) : nullptr;
-  void* wT = d_hidden ? at(workspace, L.wt_off) : nullptr;
-  void* dzT = d_weight ? at(workspace, L.dzt_off) : nullptr;
-  void* hT = d_weight ? at(workspace, L.ht_off) : nullptr;
-  float* dbp = d_bias ? reinterpret_cast<float*>(at(workspace, L.dbp_off)) : nullptr;
-  float* acc = nullptr;
-  if (d_weight) {
-    if (dw_dtype == FLP_F32)
-      acc = static_cast<float*>(d_weight);
-    else if (L.use_acc)
-      acc = reinterpret_cast<float*>(at(workspace, L.acc_off));
-  }
-  for (int64_t c = 0; c < L.n_chunks; ++c) {
-    const int64_t r0 = c * L.chunk;
-    const int64_t rows = (N - r0 < L.chunk) ? N - r0 : L.chunk;
-    const bool last = c + 1 == L.n_chunks;
-    const void* h_chunk = static_cast<const char*>(hidden) + size_t(r0) * D * xs;
-    DzArgs z;
-    z.hidden = h_chunk;
-    z.weight = weight;
-    z.bias = bias;
-    z.targets = static_cast<const char*>(targets) + size_t(r0) * ts;
-    z.t64 = t_dtype == FLP_I64;
-    z.temperature = temperature ? temperature + r0 : nullptr;
-    z.grad_out = grad_out + r0;
-    z.lse = lse + r0;
-    z.rows = rows;
-    z.D = D;
-    z.V = V;
-    z.ldz = L.ldz;
-    z.ldt = L.ldt;
-    z.dz = dz;
-    z.dzT = dzT;
-    z.dbias_part = dbp;
-    if (launch_dz(x_dtype, z, s) != hipSuccess) return FLP_HIP_ERROR;
-    if (d_hidden) {
-      // W^T is made once, after the first dlogits: that kernel re-reads hidden, which
-      // the forward left in the Infinity Cache and streaming 1.4 GB of W and W^T
-      // through it first would evict.
-      if (c == 0 && launch_transpose(x_dtype, weight, V, L.ldz, D, D, wT, s) != hipSuccess)
-        return FLP_HIP_ERROR;
-      GemmArgs g;
-      g.a = dz;
-      g.b = wT;
-      g.lda_b = 128;
-      g.ldb_b = 128;
-      g.a_ks = L.ldt * 128;
-      g.b_ks = D * 128;
-      g.M = rows;
-      g.N = D;
-      g.K = L.ldz;  // dz and W^T are zero past V
-      g.out = static_cast<char*>(d_hidden) + size_t(r0) * D * xs;
-      g.ldo = D;
-      g.acc = nullptr;
-      g.load_acc = 0;
-      g.store_acc = 0;
-      if (launch_dx(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
-    }
-    if (d_weight) {
-      const int64_t kpad = round_up(rows, kTokPad);  // dz^T and hidden^T are zero past rows
-      if (launch_transpose(x_dtype, h_chunk, rows, kpad, D, D, hT, s) != hipSuccess)
-        return FLP_HIP_ERROR;
-      GemmArgs g;
-      g.a = dzT;
-      g.b = hT;
-      g.lda_b = 128;
-      g.ldb_b = 128;
-      g.a_ks = L.ldz * 128;
-      g.b_ks = D * 128;
-      g.M = V;
-      g.N = D;
-      g.K = kpad;
-      g.out = d_weight;
-      g.ldo = D;
-      g.acc = acc;
-      g.load_acc = (acc != nullptr && c > 0) ? 1 : 0;
-      g.store_acc = (acc != nullptr && (dw_dtype == FLP_F32 || !last)) ? 1 : 0;
-      if (launch_dw(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
-    }
-    if (d_bias) {
-      if (launch_dbias_fold(dbp, (rows + kDzRowTile - 1) / kDzRowTile, L.ldz, V, d_bias, c == 0,
-                            s) != hipSuccess)
-        return FLP_HIP_ERROR;
-    }
-  }
-  return FLP_OK;
+  return enqueue_backward(N, D, V, x_dtype, grad_out, lse, hidden, weight, bias, targets, t_dtype,
+                          temperature, nullptr, d_hidden, d_weight, dw_dtype, d_bias, workspace,
+                          workspace_bytes, s);
 }
 
 // ---- indexed (row-subset) variants ----
@@ -627,6 +652,122 @@ flp_status flp_embedding_scaled_backward(int64_t N, int64_t D, int64_t V, flp_dt
   if (launch_embedding_backward(a, static_cast<hipStream_t>(stream)) != hipSuccess)
     return FLP_HIP_ERROR;
   return FLP_OK;
+}
+
+// ---- linear cross entropy ----
+
+size_t flp_cross_entropy_forward_workspace_bytes(int64_t N, int64_t D, int64_t V) {
+  if (N < 0 || D < 1 || V < 1) return 0;
+  return loss_fwd_layout(N, D, V).total;
+}
+
+flp_status flp_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                     const void* hidden, const void* weight, const float* bias,
+                                     const void* targets, flp_dtype t_dtype,
+                                     double label_smoothing, double z_loss,
+                                     flp_reduction reduction, float* out_loss, float* out_stats,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  flp_status st = validate_cross_entropy_forward(N, D, V, x_dtype, hidden, weight, bias, targets,
+                                                 t_dtype, label_smoothing, z_loss, reduction,
+                                                 out_loss, out_stats, workspace, workspace_bytes);
+  if (st != FLP_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (N == 0) {  // the sum over no rows
+    if (reduction == FLP_REDUCE_NONE) return FLP_OK;
+    if ((st = check_device()) != FLP_OK) return st;
+    return launch_fill(out_loss, 1, 0.0f, s) == hipSuccess ? FLP_OK : FLP_HIP_ERROR;
+  }
+  if ((st = check_device()) != FLP_OK) return st;
+  const LossFwdLayout L = loss_fwd_layout(N, D, V);
+  float* logp = reinterpret_cast<float*>(at(workspace, L.logp_off));
+  float* lse = out_stats ? out_stats : reinterpret_cast<float*>(at(workspace, L.lse_off));
+  FwdArgs f;
+  f.hidden = hidden;
+  f.weight = weight;
+  f.bias = bias;
+  f.targets = targets;
+  f.t64 = t_dtype == FLP_I64;
+  f.temperature = nullptr;
+  f.N = N;
+  f.D = D;
+  f.V = V;
+  f.t_off = 0;
+  f.part = reinterpret_cast<float2*>(at(workspace, L.fwd.part_off));
+  f.zt = reinterpret_cast<float*>(at(workspace, L.fwd.zt_off));
+  f.zsum = label_smoothing != 0.0 ? reinterpret_cast<float*>(at(workspace, L.zsum_off)) : nullptr;
+  f.zunit = loss_zunit(V);
+  if (launch_loss_forward(x_dtype, f, s) != hipSuccess) return FLP_HIP_ERROR;
+  MergeArgs m;
+  m.part = f.part;
+  m.zt = f.zt;
+  m.targets = targets;
+  m.t64 = f.t64;
+  m.N = N;
+  m.V = V;
+  m.n_vt = L.fwd.n_vt;
+  m.logp = logp;
+  m.lse = lse;
+  m.lse_rest = out_stats ? out_stats + N : nullptr;
+  if (launch_merge(m, s) != hipSuccess) return FLP_HIP_ERROR;
+  LossRowsArgs r{};
+  r.N = N;
+  r.V = V;
+  r.n_vt = L.fwd.n_vt;
+  r.targets = targets;
+  r.t64 = f.t64;
+  r.logp = logp;
+  r.lse = lse;
+  r.zsum = f.zsum;
+  r.zunit = f.zunit;
+  r.terms = LossTerms{label_smoothing, z_loss, int(reduction)};
+  const bool rows = reduction == FLP_REDUCE_NONE;
+  r.rows = rows ? out_loss : reinterpret_cast<float*>(at(workspace, L.rows_off));
+  r.loss = rows ? nullptr : out_loss;
+  if (launch_loss_rows(r, s) != hipSuccess) return FLP_HIP_ERROR;
+  return FLP_OK;
+}
+
+size_t flp_cross_entropy_backward_workspace_bytes(int64_t N, int64_t D, int64_t V,
+                                                  flp_dtype x_dtype, int64_t chunk_rows) {
+  const size_t b = flp_backward_workspace_bytes(N, D, V, x_dtype, x_dtype, chunk_rows);
+  return b == 0 ? 0 : loss_grad_layout(N).total + b;
+}
+
+flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                      const float* grad_out, const float* stats,
+                                      const void* hidden, const void* weight, const float* bias,
+                                      const void* targets, flp_dtype t_dtype,
+                                      double label_smoothing, double z_loss,
+                                      flp_reduction reduction, void* d_hidden, void* d_weight,
+                                      float* d_bias, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  flp_status st = validate_cross_entropy_backward(
+      N, D, V, x_dtype, grad_out, stats, hidden, weight, bias, targets, t_dtype, label_smoothing,
+      z_loss, reduction, d_hidden, d_weight, d_bias, workspace, workspace_bytes);
+  if (st != FLP_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (N == 0) return zero_sums(d_weight, size_t(V) * D * dtype_size(x_dtype), d_bias, V, s);
+  if (!d_hidden && !d_weight && !d_bias) return FLP_OK;
+  if ((st = check_device()) != FLP_OK) return st;
+  const LossGradLayout L = loss_grad_layout(N);
+  LossGradArgs g{};
+  g.N = N;
+  g.V = V;
+  g.targets = targets;
+  g.t64 = t_dtype == FLP_I64;
+  g.grad_out = grad_out;
+  g.lse = stats;
+  g.lse_rest = stats + N;
+  g.terms = LossTerms{label_smoothing, z_loss, int(reduction)};
+  g.rescale = x_dtype == FLP_F16;
+  g.softmax = reinterpret_cast<float*>(at(workspace, L.softmax_off));
+  g.onehot = reinterpret_cast<float*>(at(workspace, L.onehot_off));
+  g.uniform = reinterpret_cast<float*>(at(workspace, L.uniform_off));
+  g.unscale = reinterpret_cast<float*>(at(workspace, L.unscale_off));
+  if (launch_loss_grad(g, s) != hipSuccess) return FLP_HIP_ERROR;
+  return enqueue_backward(N, D, V, x_dtype, g.softmax, stats, hidden, weight, bias, targets, t_dtype,
+                          nullptr, &g, d_hidden, d_weight, x_dtype, d_bias,
+                          at(workspace, L.total), workspace_bytes - L.total, s);
 }
 
 // ---- layer norm ----

@@ -60,6 +60,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kGroupM = 8;        // row tiles per scheduling group
 constexpr int kTileCols = 256;    // vocabulary tile of the logits kernels
 constexpr int kHalfCols = 128;    // columns per wave column in the logits kernels
+// The exponent z log2 e - M log2 e as one FMA is off by the rounding of M log2 e.  Beyond
+// this size the cross entropy takes the difference z - M first, which is exact for the
+// entries that matter (entries masked with -1e30 or the lowest fp32 value would otherwise
+// overflow the exponential), and with lse also what its own rounding left out.
+constexpr float kHugeLogit = 1e4f;
 
 struct BF16 {
   static constexpr int kSize = 2;
@@ -592,7 +597,11 @@ __device__ __forceinline__ float lane_sum(const float (&e)[WNB][4]) {
   return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
 }
 
-template <class E, int BM, int WM, bool ODD, int NS = 2>
+// LOSS (the cross entropy's forward) adds, when p.zsum is given, the tile's sum of logits
+// per row (times p.zunit, a power of two at most 1 / V, so that columns masked with the
+// lowest fp32 value cannot overflow it), and is safe for tiles and rows masked with such
+// values (kHugeLogit).
+template <class E, int BM, int WM, bool ODD, int NS = 2, bool LOSS = false>
 __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
   using Eng = LogitEngine<E, BM, WM, NS>;
   constexpr int RW = Eng::RW, WMB = Eng::WMB, WNB = Eng::WNB, NT = Eng::NT;
@@ -620,7 +629,8 @@ __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
   __syncthreads();
 
   // [2][BM] row max of y = h W^T + b per wave column, [2][BM] row sums, [BM] row max of z
-  static_assert(5 * BM * sizeof(float) <= Eng::kLds, "the row reductions fit the operand ring");
+  // (LOSS: and [2][BM] row sums of logits)
+  static_assert(7 * BM * sizeof(float) <= Eng::kLds, "the row reductions fit the operand ring");
   float* red = reinterpret_cast<float*>(smem);
   const int64_t cw = col0 + wn * kHalfCols;
   // Columns of this wave at or past lim are vocabulary padding (lim < 128 only in
@@ -661,6 +671,21 @@ __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
     for (int nb = 0; nb < WNB; ++nb)
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[mb][nb][r] += bcol[nb][r];
+    if constexpr (LOSS) {
+      if (p.zsum != nullptr) {
+        float zs = 0.f;
+#pragma unroll
+        for (int nb = 0; nb < WNB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (lim == kHalfCols || nb * 16 + 4 * g + r < lim)
+              zs = fmaf(acc[mb][nb][r], p.zunit, zs);
+        f32x2_t q = pair16(zs);
+        zs = q.x + q.y;
+        q = pair32(zs);
+        if (g == 0) red[5 * BM + wn * BM + rl] = q.x + q.y;
+      }
+    }
     if (lim < kHalfCols) {  // the last vocabulary tile: padding columns drop out
 #pragma unroll
       for (int nb = 0; nb < WNB; ++nb)
@@ -694,6 +719,14 @@ __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
     for (int nb = 0; nb < WNB; ++nb)
 #pragma unroll
       for (int r = 0; r < 4; ++r) e[nb][r] = fast_exp2(fmaf(acc[mb][nb][r], k, -Ml));
+    if constexpr (LOSS) {
+      if (fabsf(M) > kHugeLogit) {
+#pragma unroll
+        for (int nb = 0; nb < WNB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) e[nb][r] = fast_exp2((acc[mb][nb][r] - M) * kLog2e);
+      }
+    }
     float s = lane_sum<WNB>(e);
     f32x2_t q = pair16(s);
     s = q.x + q.y;
@@ -721,6 +754,10 @@ __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
       const float M = red[4 * BM + rl];
       const float S = red[2 * BM + rl] + red[3 * BM + rl];
       p.part[int64_t(tn) * p.N + row] = make_float2(M, S);
+      if constexpr (LOSS) {
+        if (p.zsum != nullptr)
+          p.zsum[int64_t(tn) * p.N + row] = red[5 * BM + rl] + red[6 * BM + rl];
+      }
     }
   }
 }
@@ -807,6 +844,8 @@ __global__ __launch_bounds__(256) void k_merge(MergeArgs p) {
     const bool valid = t >= 0 && t < p.V;
     p.logp[row] = valid ? (zt - M) - ls : 0.0f;
     if (p.lse != nullptr) p.lse[row] = M + ls;
+    // what that sum's rounding left out (exact: |M| >= |ls| wherever it matters)
+    if (p.lse_rest != nullptr) p.lse_rest[row] = ls - ((M + ls) - M);
   }
 }
 
@@ -990,7 +1029,9 @@ __global__ __launch_bounds__(256) void k_logits_bwd(LogitsArgs p) {
 // of K.  The transposes of W and of hidden (k_transpose16) apply the same order, so
 // every product pairs the same dz, W and hidden entries as in the natural order.
 
-template <class E, int BM, int WM, bool ODD>
+// LOSS (the cross entropy's backward): dz = c p + onehot o + u with the per-row factors
+// p.grad_out (c), p.onehot (o) and p.uniform (u); no temperature.
+template <class E, int BM, int WM, bool ODD, bool LOSS = false>
 __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
   using Eng = LogitEngine<E, BM, WM>;
   constexpr int RW = Eng::RW, WMB = Eng::WMB, WNB = Eng::WNB, NT = Eng::NT;
@@ -1052,7 +1093,15 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
     rlse[mb] = p.lse[rowc(mb)];
     rtemp[mb] = 1.0f;
   }
-  if (p.temperature != nullptr) {
+  float ronehot[WMB], runif[WMB], rrest[WMB];  // LOSS only
+  if constexpr (LOSS) {
+#pragma unroll
+    for (int mb = 0; mb < WMB; ++mb) {
+      ronehot[mb] = p.onehot[rowc(mb)];
+      runif[mb] = p.uniform[rowc(mb)];
+      rrest[mb] = p.lse_rest[rowc(mb)];
+    }
+  } else if (p.temperature != nullptr) {
 #pragma unroll
     for (int mb = 0; mb < WMB; ++mb) rtemp[mb] = p.temperature[rowc(mb)];
   }
@@ -1095,7 +1144,7 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
     const int64_t t = !rv ? -1 : p.t64 ? rt64[mb] : int64_t(rt32[mb]);
     const bool valid = t >= 0 && t < p.V;
     rg[mb] = valid ? rgrad[mb] * invT : 0.f;
-    rl[mb] = (rv ? rlse[mb] : 0.f) * kLog2e;
+    rl[mb] = (rv ? rlse[mb] : 0.f) * (LOSS ? 1.0f : kLog2e);
     rk[mb] = invT * kLog2e;
     const int64_t trel = t - cw;
     rtc[mb] = !valid ? -2 : (trel >= 0 && trel < kHalfCols) ? int(trel) : -1;
@@ -1120,7 +1169,32 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
       // Few rows of a wave have their target among its 128 columns, so that part
       // runs under a branch most waves skip.
       float vt = 0.f;
-      if (tcol >= 0) {
+      if (LOSS) {
+        // The softmax in place of the logits, then one FMA per entry.
+        const float L = rl[mb];
+        if (fabsf(L) > kHugeLogit) {
+#pragma unroll
+          for (int nb = 0; nb < WNB; ++nb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[mb][nb][r] = fast_exp2(((acc[mb][nb][r] - L) - rrest[mb]) * kLog2e);
+        } else {
+          const float Lk = L * kLog2e;
+#pragma unroll
+          for (int nb = 0; nb < WNB; ++nb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[mb][nb][r] = fast_exp2(fmaf(acc[mb][nb][r], kLog2e, -Lk));
+        }
+        const float o = ronehot[mb] + runif[mb];
+        if (tcol >= 0) {
+#pragma unroll
+          for (int nb = 0; nb < WNB; ++nb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (nb * 16 + 4 * g + r == tcol) vt = fmaf(G, acc[mb][nb][r], o);
+        }
+      } else if (tcol >= 0) {
         float yt = 0.f;
 #pragma unroll
         for (int nb = 0; nb < WNB; ++nb)
@@ -1133,7 +1207,9 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
 #pragma unroll
       for (int nb = 0; nb < WNB; ++nb)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[mb][nb][r] = nG * fast_exp2(fmaf(acc[mb][nb][r], k, -Ll));
+        for (int r = 0; r < 4; ++r)
+          acc[mb][nb][r] = LOSS ? fmaf(G, acc[mb][nb][r], runif[mb])
+                                : nG * fast_exp2(fmaf(acc[mb][nb][r], k, -Ll));
       if (tcol >= 0) {
 #pragma unroll
         for (int nb = 0; nb < WNB; ++nb)
@@ -1313,7 +1389,9 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
 //   d_weight: M = V, N = D, K = tokens (padded); A = dz^T, B = hidden^T.
 // LOAD: start from the fp32 accumulator p.acc; STORE: 0 = element type to p.out,
 // 1 = fp32 to p.acc.
-template <class E, int BM, int BN, int WM, int WN, bool LOAD, int STORE, int NS = 2, int NSA = NS>
+// SCALED: the result is multiplied by *p.scale before it is rounded to p.out.
+template <class E, int BM, int BN, int WM, int WN, bool LOAD, int STORE, int NS = 2, int NSA = NS,
+          bool SCALED = false>
 __global__ __launch_bounds__(64 * WM * WN) void k_gemm(GemmArgs p) {
   using Eng = Engine<E, BM, BN, WM, WN, NS, NSA>;
   constexpr int RW = Eng::RW, CW = Eng::CW, WMB = Eng::WMB, WNB = Eng::WNB;
@@ -1341,6 +1419,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(GemmArgs p) {
   Eng::template run<false>(acc, reinterpret_cast<const char*>(p.a) + m0 * p.lda_b, p.lda_b,
                            p.a_ks, p.M - m0, reinterpret_cast<const char*>(p.b) + n0 * p.ldb_b,
                            p.ldb_b, p.b_ks, p.N - n0, p.K * E::kSize, smem);
+  if constexpr (SCALED) {
+    static_assert(STORE == 0, "only the rounded result is scaled");
+    const float scale = *p.scale;
+#pragma unroll
+    for (int mb = 0; mb < WMB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < WNB; ++nb) acc[mb][nb] *= scale;
+  }
 
   if constexpr (STORE == 0 && E::kSize == 2) {
     // 16-bit output: the tile is staged in the operand ring (rows of BN values plus 16
@@ -1389,19 +1475,34 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(GemmArgs p) {
   }
 }
 
+// Whether a row's target lies in [0, V).
+struct LiveRows {
+  const void* targets;
+  int t64;
+  int64_t V;
+  __device__ __forceinline__ bool operator()(int64_t r) const {
+    const int64_t t = load_target(targets, t64, r);
+    return t >= 0 && t < V;
+  }
+};
+
 // ---- tiled transpose ---------------------------------------------------------------------------
 // dst = src^T in the K-blocked layout (dst has `cols` rows and K = rows_pad);
 // entries r in [rows, rows_pad) are written as zeros.
-template <class T>
+// LIVE: source rows whose target is outside [0, V) count as zeros, whatever they hold (a
+// padded row's infinities and NaN must not reach a product with its zero gradients).
+template <class T, bool LIVE = false>
 __global__ __launch_bounds__(256) void k_transpose(const T* __restrict__ src, int64_t rows,
                                                    int64_t rows_pad, int64_t cols, int64_t ld_src,
-                                                   T* __restrict__ dst) {
+                                                   T* __restrict__ dst, LiveRows live) {
   __shared__ T tile[64][65];
   const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   for (int k = ty; k < 64; k += 4) {
     const int64_t r = r0 + k, c = c0 + tx;
-    tile[k][tx] = (r < rows && c < cols) ? src[r * ld_src + c] : T(0);
+    bool in = r < rows && c < cols;
+    if constexpr (LIVE) in = in && live(r);
+    tile[k][tx] = in ? src[r * ld_src + c] : T(0);
   }
   __syncthreads();
   for (int k = ty; k < 64; k += 4) {
@@ -1416,9 +1517,10 @@ __global__ __launch_bounds__(256) void k_transpose(const T* __restrict__ src, in
 // 16-byte aligned source rows and rows_pad a multiple of 64.  The destination's K
 // positions take the fragment-major order of the 16-bit backward GEMMs: K
 // position 32 b + 8 g + 4 h + r holds source row 32 b + 16 h + 4 g + r.
+template <bool LIVE = false>
 __global__ __launch_bounds__(256) void k_transpose16(const uint16_t* __restrict__ src, int64_t rows,
                                                      int64_t rows_pad, int64_t cols, int64_t ld_src,
-                                                     uint16_t* __restrict__ dst) {
+                                                     uint16_t* __restrict__ dst, LiveRows live) {
   __shared__ uint32_t tile[64][33];  // [row][column pair], 132-byte rows
   const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
   const int t = threadIdx.x, j = t & 7, q = t >> 3;
@@ -1427,7 +1529,9 @@ __global__ __launch_bounds__(256) void k_transpose16(const uint16_t* __restrict_
     const int rl = q + 32 * p;
     const int64_t r = r0 + rl, c = c0 + 8 * j;
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (r < rows && c < cols) v = *reinterpret_cast<const u32x4*>(src + r * ld_src + c);
+    bool in = r < rows && c < cols;
+    if constexpr (LIVE) in = in && live(r);
+    if (in) v = *reinterpret_cast<const u32x4*>(src + r * ld_src + c);
 #pragma unroll
     for (int e = 0; e < 4; ++e) tile[rl][4 * j + e] = v[e];
   }
@@ -1451,12 +1555,15 @@ __global__ __launch_bounds__(256) void k_transpose16(const uint16_t* __restrict_
 
 // ---- d_bias: ascending fold of the per-row-tile partials --------------------------------------
 __global__ __launch_bounds__(256) void k_dbias_fold(const float* part, int64_t n_parts, int64_t ldz,
-                                                    int64_t V, float* d_bias, int init) {
+                                                    int64_t V, float* d_bias, int init,
+                                                    const float* scale) {
   const int64_t v = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (v >= V) return;
-  float s = init ? 0.0f : d_bias[v];
+  // scale: a power of two that the finished sums are multiplied by (exact both ways)
+  const float f = scale != nullptr ? *scale : 1.0f;
+  float s = init ? 0.0f : d_bias[v] / f;
   for (int64_t r = 0; r < n_parts; ++r) s += part[r * ldz + v];
-  d_bias[v] = s;
+  d_bias[v] = s * f;
 }
 
 // ---- launch helpers ----------------------------------------------------------------------------
@@ -1478,15 +1585,15 @@ hipError_t prepare(K kernel, size_t lds, std::atomic<int> (&ready)[kMaxDevices])
   return e;
 }
 
-template <class E, int BM, int WM, bool ODD, int NS = 2>
+template <class E, int BM, int WM, bool ODD, bool LOSS, int NS = 2>
 hipError_t fwd_cfg(const FwdArgs& a, hipStream_t s) {
   using Eng = LogitEngine<E, BM, WM, NS>;
   static std::atomic<int> ready[kMaxDevices];
-  const hipError_t e = prepare(k_fwd<E, BM, WM, ODD, NS>, Eng::kLds, ready);
+  const hipError_t e = prepare(k_fwd<E, BM, WM, ODD, NS, LOSS>, Eng::kLds, ready);
   if (e != hipSuccess) return e;
   const int64_t blocks = ((a.N + BM - 1) / BM) * ((a.V + kTileCols - 1) / kTileCols);
-  hipLaunchKernelGGL((k_fwd<E, BM, WM, ODD, NS>), dim3(unsigned(blocks)), dim3(Eng::NT), Eng::kLds,
-                     s, a);
+  hipLaunchKernelGGL((k_fwd<E, BM, WM, ODD, NS, LOSS>), dim3(unsigned(blocks)), dim3(Eng::NT),
+                     Eng::kLds, s, a);
   return hipGetLastError();
 }
 
@@ -1496,7 +1603,7 @@ bool odd_stages(int64_t D) {
   return ((D * E::kSize) / kStageBytes) % 2 == 1;
 }
 
-template <class E, bool ODD>
+template <class E, bool ODD, bool LOSS>
 hipError_t fwd_rows(const FwdArgs& a, hipStream_t s) {
   if (a.N <= 32) {
     // Over at most 256 vocabulary tiles (a vocabulary shard) the few workgroups each
@@ -1504,40 +1611,47 @@ hipError_t fwd_rows(const FwdArgs& a, hipStream_t s) {
     // (four LDS stages, 147 KB).  Over the full vocabulary the 2-stage tiles, two
     // workgroups per compute unit, stream W faster.
     const int64_t vt = (a.V + kTileCols - 1) / kTileCols;
-    if (vt <= 256) return fwd_cfg<E, 32, 2, ODD, 4>(a, s);
-    return fwd_cfg<E, 32, 2, ODD>(a, s);
+    if (vt <= 256) return fwd_cfg<E, 32, 2, ODD, LOSS, 4>(a, s);
+    return fwd_cfg<E, 32, 2, ODD, LOSS>(a, s);
   }
-  if (a.N <= 64) return fwd_cfg<E, 64, 2, ODD>(a, s);
-  if (a.N <= 128) return fwd_cfg<E, 128, 2, ODD>(a, s);
-  return fwd_cfg<E, 256, 4, ODD>(a, s);
+  if (a.N <= 64) return fwd_cfg<E, 64, 2, ODD, LOSS>(a, s);
+  if (a.N <= 128) return fwd_cfg<E, 128, 2, ODD, LOSS>(a, s);
+  return fwd_cfg<E, 256, 4, ODD, LOSS>(a, s);
 }
 
-template <class E>
+template <class E, bool LOSS = false>
 hipError_t fwd_dispatch(const FwdArgs& a, hipStream_t s) {
-  return odd_stages<E>(a.D) ? fwd_rows<E, true>(a, s) : fwd_rows<E, false>(a, s);
+  return odd_stages<E>(a.D) ? fwd_rows<E, true, LOSS>(a, s) : fwd_rows<E, false, LOSS>(a, s);
 }
 
-template <class E, int BM, int WM, bool ODD>
+template <class E, int BM, int WM, bool ODD, bool LOSS>
 hipError_t dz_cfg(const DzArgs& a, hipStream_t s) {
   using Eng = LogitEngine<E, BM, WM>;
   constexpr size_t lds = Eng::kLds;
   static std::atomic<int> ready[kMaxDevices];
-  const hipError_t e = prepare(k_dz<E, BM, WM, ODD>, lds, ready);
+  const hipError_t e = prepare(k_dz<E, BM, WM, ODD, LOSS>, lds, ready);
   if (e != hipSuccess) return e;
   const int64_t blocks = ((a.rows + BM - 1) / BM) * ((a.V + kTileCols - 1) / kTileCols);
-  hipLaunchKernelGGL((k_dz<E, BM, WM, ODD>), dim3(unsigned(blocks)), dim3(Eng::NT), lds, s, a);
+  hipLaunchKernelGGL((k_dz<E, BM, WM, ODD, LOSS>), dim3(unsigned(blocks)), dim3(Eng::NT), lds, s, a);
   return hipGetLastError();
 }
 
-template <class E, int BM, int BN, int WM, int WN, bool LOAD, int STORE, int NS = 2, int NSA = NS>
+template <class E, bool LOSS>
+hipError_t dz_dispatch(const DzArgs& a, hipStream_t s) {
+  return odd_stages<E>(a.D) ? dz_cfg<E, int(kDzRowTile), 4, true, LOSS>(a, s)
+                            : dz_cfg<E, int(kDzRowTile), 4, false, LOSS>(a, s);
+}
+
+template <class E, int BM, int BN, int WM, int WN, bool LOAD, int STORE, int NS = 2, int NSA = NS,
+          bool SCALED = false>
 hipError_t gemm_cfg(const GemmArgs& a, hipStream_t s) {
   using Eng = Engine<E, BM, BN, WM, WN, NS, NSA>;
   static std::atomic<int> ready[kMaxDevices];
-  const hipError_t e = prepare(k_gemm<E, BM, BN, WM, WN, LOAD, STORE, NS, NSA>, Eng::kLds, ready);
+  const hipError_t e = prepare(k_gemm<E, BM, BN, WM, WN, LOAD, STORE, NS, NSA, SCALED>, Eng::kLds, ready);
   if (e != hipSuccess) return e;
   const int64_t blocks = ((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
-  hipLaunchKernelGGL((k_gemm<E, BM, BN, WM, WN, LOAD, STORE, NS, NSA>), dim3(unsigned(blocks)),
-                     dim3(Eng::NT), Eng::kLds, s, a);
+  hipLaunchKernelGGL((k_gemm<E, BM, BN, WM, WN, LOAD, STORE, NS, NSA, SCALED>),
+                     dim3(unsigned(blocks)), dim3(Eng::NT), Eng::kLds, s, a);
   return hipGetLastError();
 }
 
@@ -1555,13 +1669,13 @@ constexpr int kGemmNSA = 3;
 // measured on the 16-bit training shape (D = 2688, V = 131072): 64 x 16 tiles are
 // fastest up to 64 rows, 64 x 32 up to 128, 128 x 64 up to 512, 128 x 128 up to
 // 1024, and the 256 x 224 tile from 2048 rows on.
-template <class E>
+template <class E, bool SCALED = false>
 hipError_t dx_tiles16(const GemmArgs& a, hipStream_t s) {
-  if (a.M <= 64) return gemm_cfg<E, 64, 16, 4, 1, false, 0, 8>(a, s);
-  if (a.M <= 128) return gemm_cfg<E, 64, 32, 4, 1, false, 0, 8>(a, s);
-  if (a.M <= 512) return gemm_cfg<E, 128, 64, 2, 2, false, 0, 4>(a, s);
-  if (a.M <= 1024) return gemm_cfg<E, 128, 128, 2, 2, false, 0, 3>(a, s);
-  return gemm_cfg<E, 256, 224, 4, 2, false, 0, 2, kGemmNSA>(a, s);
+  if (a.M <= 64) return gemm_cfg<E, 64, 16, 4, 1, false, 0, 8, 8, SCALED>(a, s);
+  if (a.M <= 128) return gemm_cfg<E, 64, 32, 4, 1, false, 0, 8, 8, SCALED>(a, s);
+  if (a.M <= 512) return gemm_cfg<E, 128, 64, 2, 2, false, 0, 4, 4, SCALED>(a, s);
+  if (a.M <= 1024) return gemm_cfg<E, 128, 128, 2, 2, false, 0, 3, 3, SCALED>(a, s);
+  return gemm_cfg<E, 256, 224, 4, 2, false, 0, 2, kGemmNSA, SCALED>(a, s);
 }
 template <class E>
 hipError_t dx_dispatch(const GemmArgs& a, hipStream_t s);
@@ -1571,6 +1685,7 @@ hipError_t dx_dispatch<BF16>(const GemmArgs& a, hipStream_t s) {
 }
 template <>
 hipError_t dx_dispatch<F16>(const GemmArgs& a, hipStream_t s) {
+  if (a.scale != nullptr) return dx_tiles16<F16, true>(a, s);
   return dx_tiles16<F16>(a, s);
 }
 template <>
@@ -1591,6 +1706,10 @@ hipError_t dw_dispatch<BF16>(const GemmArgs& a, hipStream_t s) {
 }
 template <>
 hipError_t dw_dispatch<F16>(const GemmArgs& a, hipStream_t s) {
+  if (a.scale != nullptr && !a.store_acc) {  // the rounded result only
+    if (a.load_acc) return gemm_cfg<F16, 256, 224, 4, 2, true, 0, 2, kGemmNSA, true>(a, s);
+    return gemm_cfg<F16, 256, 224, 4, 2, false, 0, 2, kGemmNSA, true>(a, s);
+  }
   if (a.load_acc) {
     if (a.store_acc) return gemm_cfg<F16, 256, 224, 4, 2, true, 1, 2, kGemmNSA>(a, s);
     return gemm_cfg<F16, 256, 224, 4, 2, true, 0, 2, kGemmNSA>(a, s);
@@ -1609,6 +1728,13 @@ hipError_t dw_dispatch<F32>(const GemmArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_loss_forward(flp_dtype x, const FwdArgs& a, hipStream_t s) {
+  ProfScope ps(FLP_K_FORWARD, s);
+  if (x == FLP_BF16) return fwd_dispatch<BF16, true>(a, s);
+  if (x == FLP_F16) return fwd_dispatch<F16, true>(a, s);
+  return fwd_dispatch<F32, true>(a, s);
+}
 
 hipError_t launch_forward(flp_dtype x, const FwdArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_FORWARD, s);
@@ -1671,14 +1797,10 @@ hipError_t launch_logits_backward(flp_dtype x, const LogitsArgs& a, hipStream_t 
 
 hipError_t launch_dz(flp_dtype x, const DzArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_DLOGITS, s);
-  if (x == FLP_BF16)
-    return odd_stages<BF16>(a.D) ? dz_cfg<BF16, int(kDzRowTile), 4, true>(a, s)
-                                 : dz_cfg<BF16, int(kDzRowTile), 4, false>(a, s);
-  if (x == FLP_F16)
-    return odd_stages<F16>(a.D) ? dz_cfg<F16, int(kDzRowTile), 4, true>(a, s)
-                                : dz_cfg<F16, int(kDzRowTile), 4, false>(a, s);
-  return odd_stages<F32>(a.D) ? dz_cfg<F32, int(kDzRowTile), 4, true>(a, s)
-                              : dz_cfg<F32, int(kDzRowTile), 4, false>(a, s);
+  const bool loss = a.onehot != nullptr;
+  if (x == FLP_BF16) return loss ? dz_dispatch<BF16, true>(a, s) : dz_dispatch<BF16, false>(a, s);
+  if (x == FLP_F16) return loss ? dz_dispatch<F16, true>(a, s) : dz_dispatch<F16, false>(a, s);
+  return loss ? dz_dispatch<F32, true>(a, s) : dz_dispatch<F32, false>(a, s);
 }
 
 hipError_t launch_dx(flp_dtype x, const GemmArgs& a, hipStream_t s) {
@@ -1700,19 +1822,36 @@ hipError_t launch_transpose(flp_dtype x, const void* src, int64_t rows, int64_t 
   ProfScope ps(FLP_K_TRANSPOSE, s);
   const dim3 grid(unsigned((cols + 63) / 64), unsigned((rows_pad + 63) / 64));
   if (x != FLP_F32)
-    hipLaunchKernelGGL(k_transpose16, grid, dim3(256), 0, s, static_cast<const uint16_t*>(src),
-                       rows, rows_pad, cols, ld_src, static_cast<uint16_t*>(dst));
+    hipLaunchKernelGGL(k_transpose16<>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(src),
+                       rows, rows_pad, cols, ld_src, static_cast<uint16_t*>(dst), LiveRows{});
   else
     hipLaunchKernelGGL(k_transpose<float>, grid, dim3(256), 0, s, static_cast<const float*>(src),
-                       rows, rows_pad, cols, ld_src, static_cast<float*>(dst));
+                       rows, rows_pad, cols, ld_src, static_cast<float*>(dst), LiveRows{});
+  return hipGetLastError();
+}
+
+hipError_t launch_transpose_live(flp_dtype x, const void* src, int64_t rows, int64_t rows_pad,
+                                 int64_t cols, const void* targets, bool t64, int64_t V, void* dst,
+                                 hipStream_t s) {
+  ProfScope ps(FLP_K_TRANSPOSE, s);
+  const dim3 grid(unsigned((cols + 63) / 64), unsigned((rows_pad + 63) / 64));
+  const LiveRows live{targets, t64 ? 1 : 0, V};
+  if (x != FLP_F32)
+    hipLaunchKernelGGL(k_transpose16<true>, grid, dim3(256), 0, s,
+                       static_cast<const uint16_t*>(src), rows, rows_pad, cols, cols,
+                       static_cast<uint16_t*>(dst), live);
+  else
+    hipLaunchKernelGGL((k_transpose<float, true>), grid, dim3(256), 0, s,
+                       static_cast<const float*>(src), rows, rows_pad, cols, cols,
+                       static_cast<float*>(dst), live);
   return hipGetLastError();
 }
 
 hipError_t launch_dbias_fold(const float* part, int64_t n_parts, int64_t ldz, int64_t V,
-                             float* d_bias, int init, hipStream_t s) {
+                             float* d_bias, int init, const float* scale, hipStream_t s) {
   ProfScope ps(FLP_K_DBIAS, s);
   hipLaunchKernelGGL(k_dbias_fold, dim3(unsigned((V + 255) / 256)), dim3(256), 0, s, part, n_parts,
-                     ldz, V, d_bias, init);
+                     ldz, V, d_bias, init, scale);
   return hipGetLastError();
 }
 

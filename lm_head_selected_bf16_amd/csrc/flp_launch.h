@@ -29,6 +29,8 @@ struct FwdArgs {
   int64_t t_off;    // vocabulary id of weight row 0 (0 unless a shard)
   float2* part;     // [n_vt][N]
   float* zt;        // [N]
+  float* zsum = nullptr;  // cross entropy: [n_vt][N] sums of logits times zunit, or null
+  float zunit = 0.f;
 };
 struct MergeArgs {
   const float2* part;
@@ -38,6 +40,7 @@ struct MergeArgs {
   int64_t N, V, n_vt;
   float* logp;
   float* lse;       // may be null
+  float* lse_rest = nullptr;  // [N] the part of lse that its rounding lost, may be null
 };
 struct DzArgs {
   const void* hidden;   // chunk start
@@ -52,6 +55,10 @@ struct DzArgs {
   void* dz;                  // [ldt rows][ldz] K-blocked, or null when d_hidden is not needed
   void* dzT;                 // [ldz rows][ldt] K-blocked, or null when d_weight is not needed
   float* dbias_part;         // [rows_alloc / kDzRowTile][ldz] or null
+  // cross entropy (null otherwise; grad_out then holds the softmax's factor): chunk start
+  const float* onehot = nullptr;   // the target entry's added term
+  const float* uniform = nullptr;  // every entry's added term
+  const float* lse_rest = nullptr;
 };
 struct LogitsArgs {
   const void* logits;        // [N][V]
@@ -91,9 +98,11 @@ struct GemmArgs {
   float* acc;            // fp32 accumulator [M][N] (dW) or null
   int load_acc;          // continue from acc
   int store_acc;         // store fp32 to acc (else store to out in x dtype)
+  const float* scale = nullptr;  // fp16: factor of the rounded result, or null for 1
 };
 
 hipError_t launch_forward(flp_dtype x, const FwdArgs& a, hipStream_t s);
+hipError_t launch_loss_forward(flp_dtype x, const FwdArgs& a, hipStream_t s);
 hipError_t launch_merge(const MergeArgs& a, hipStream_t s);
 hipError_t launch_fill(float* dst, int64_t n, float value, hipStream_t s);
 hipError_t launch_logits_forward(flp_dtype x, const LogitsArgs& a, hipStream_t s);
@@ -105,8 +114,13 @@ hipError_t launch_dw(flp_dtype x, const GemmArgs& a, hipStream_t s);
 // with cols rows and K = rows_pad; K entries in [rows, rows_pad) are zero-filled.
 hipError_t launch_transpose(flp_dtype x, const void* src, int64_t rows, int64_t rows_pad, int64_t cols,
                             int64_t ld_src, void* dst, hipStream_t s);
+// The same for hidden rows (row stride cols): rows whose target is outside [0, V) read as
+// zeros.
+hipError_t launch_transpose_live(flp_dtype x, const void* src, int64_t rows, int64_t rows_pad,
+                                 int64_t cols, const void* targets, bool t64, int64_t V, void* dst,
+                                 hipStream_t s);
 hipError_t launch_dbias_fold(const float* part, int64_t n_parts, int64_t ldz, int64_t V,
-                             float* d_bias, int init, hipStream_t s);
+                             float* d_bias, int init, const float* scale, hipStream_t s);
 const char* kernel_ids();
 
 // Row selection for the indexed variants (flp_rows.hip).  launch_zero clears
@@ -177,6 +191,40 @@ hipError_t launch_layer_norm_backward(flp_dtype x, flp_dtype w, const NormBwdArg
 // Dropout (flp_dropout.hip): elements whose 16 random bits are below `drop` become 0.
 hipError_t launch_dropout(flp_dtype x_dtype, int64_t n, const void* x, const uint64_t* rng,
                           uint32_t drop, float scale, void* out, hipStream_t s);
+
+// Row kernels of the cross entropy (flp_loss.hip).
+struct LossTerms {
+  double smoothing, z_loss;
+  int reduction;             // flp_reduction
+};
+struct LossRowsArgs {        // forward: per-row losses, then their sum or mean
+  int64_t N, V, n_vt;
+  const void* targets;
+  int t64;
+  const float* logp;         // [N]
+  const float* lse;          // [N]
+  const float* zsum;         // [n_vt][N] or null
+  float zunit;
+  LossTerms terms;
+  float* rows;               // [N] per-row losses
+  float* loss;               // [1], or null for no reduction
+};
+struct LossGradArgs {        // backward: the per-row factors of the logit gradient
+  int64_t N, V;
+  const void* targets;
+  int t64;
+  const float* grad_out;     // [N], or [1] for a reduced loss
+  const float* lse;          // [N]
+  LossTerms terms;
+  int rescale;               // bring the largest factor to [2^10, 2^11) (fp16)
+  float* softmax;            // [N] factor of the softmax
+  float* onehot;             // [N] term of the target entry
+  float* uniform;            // [N] term of every entry
+  float* unscale;            // [1] factor that takes the scaling back
+  const float* lse_rest;     // [N]
+};
+hipError_t launch_loss_rows(const LossRowsArgs& a, hipStream_t s);
+hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s);
 
 // Measurement probes (flp_probe.hip); they synchronise the stream.
 size_t probe_scratch_bytes();

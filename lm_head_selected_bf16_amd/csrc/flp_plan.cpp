@@ -561,6 +561,113 @@ flp_status validate_embedding_backward(int64_t N, int64_t D, int64_t V, flp_dtyp
   return FLP_OK;
 }
 
+LossFwdLayout loss_fwd_layout(int64_t N, int64_t D, int64_t V) {
+  LossFwdLayout L;
+  L.fwd = fwd_layout(N, D, V);
+  const size_t row = align_up(size_t(N) * 4);
+  L.logp_off = L.fwd.total;
+  L.lse_off = L.logp_off + row;
+  L.rows_off = L.lse_off + row;
+  L.zsum_off = L.rows_off + row;
+  L.total = L.zsum_off + align_up(size_t(L.fwd.n_vt) * size_t(N) * 4);
+  return L;
+}
+
+float loss_zunit(int64_t V) {
+  float u = 1.0f;
+  for (int64_t v = 1; v < V; v *= 2) u *= 0.5f;
+  return u;
+}
+
+LossGradLayout loss_grad_layout(int64_t N) {
+  LossGradLayout L;
+  const size_t row = align_up(size_t(N) * 4);
+  L.onehot_off = row;
+  L.uniform_off = 2 * row;
+  L.unscale_off = 3 * row;
+  L.total = 3 * row + kAlign;
+  return L;
+}
+
+namespace {
+
+flp_status check_loss_terms(double label_smoothing, double z_loss, flp_reduction reduction) {
+  if (!(label_smoothing >= 0.0 && label_smoothing <= 1.0)) return FLP_INVALID_ARGUMENT;
+  if (!(z_loss >= 0.0 && z_loss <= double(std::numeric_limits<float>::max())))
+    return FLP_INVALID_ARGUMENT;
+  if (reduction != FLP_REDUCE_NONE && reduction != FLP_REDUCE_SUM && reduction != FLP_REDUCE_MEAN)
+    return FLP_INVALID_ARGUMENT;
+  return FLP_OK;
+}
+
+}  // namespace
+
+flp_status validate_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype x,
+                                          const void* hidden, const void* weight,
+                                          const float* bias, const void* targets, flp_dtype t,
+                                          double label_smoothing, double z_loss,
+                                          flp_reduction reduction, const float* out_loss,
+                                          const float* out_stats, const void* workspace,
+                                          size_t workspace_bytes) {
+  flp_status st = check_dims(N, D, V, x, t);
+  if (st != FLP_OK) return st;
+  if ((st = check_loss_terms(label_smoothing, z_loss, reduction)) != FLP_OK) return st;
+  const bool rows = reduction == FLP_REDUCE_NONE;
+  if (N == 0) {
+    if (!rows && !out_loss) return FLP_INVALID_ARGUMENT;
+    return aligned(out_loss, 4) ? FLP_OK : FLP_MISALIGNED;
+  }
+  if (!hidden || !weight || !targets || !out_loss || !workspace) return FLP_INVALID_ARGUMENT;
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(workspace, 16) ||
+      !aligned(bias, 4) || !aligned(out_loss, 4) || !aligned(out_stats, 4) ||
+      !aligned(targets, dtype_size(t)))
+    return FLP_MISALIGNED;
+  const size_t xs = dtype_size(x);
+  const Span ins[] = {span(hidden, size_t(N) * D * xs), span(weight, size_t(V) * D * xs),
+                      span(bias, size_t(V) * 4), span(targets, size_t(N) * dtype_size(t))};
+  const Span outs[] = {span(out_loss, rows ? size_t(N) * 4 : 4), span(out_stats, size_t(N) * 8),
+                       span(workspace, workspace_bytes)};
+  if (any_alias(outs, 3, ins, 4)) return FLP_INVALID_ARGUMENT;
+  if (workspace_bytes < loss_fwd_layout(N, D, V).total) return FLP_WORKSPACE_TOO_SMALL;
+  return FLP_OK;
+}
+
+flp_status validate_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype x,
+                                           const float* grad_out, const float* stats,
+                                           const void* hidden, const void* weight,
+                                           const float* bias, const void* targets, flp_dtype t,
+                                           double label_smoothing, double z_loss,
+                                           flp_reduction reduction, const void* d_hidden,
+                                           const void* d_weight, const float* d_bias,
+                                           const void* workspace, size_t workspace_bytes) {
+  flp_status st = check_dims(N, D, V, x, t);
+  if (st != FLP_OK) return st;
+  if ((st = check_loss_terms(label_smoothing, z_loss, reduction)) != FLP_OK) return st;
+  if (N == 0) return validate_empty_sums(D, V, dtype_size(x), weight, bias, d_weight, x, d_bias);
+  if (!grad_out || !stats || !hidden || !weight || !targets) return FLP_INVALID_ARGUMENT;
+  if (!d_hidden && !d_weight && !d_bias) return FLP_OK;
+  if (!workspace) return FLP_INVALID_ARGUMENT;
+  const size_t xs = dtype_size(x);
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(workspace, 16) ||
+      !aligned(grad_out, 4) || !aligned(stats, 4) || !aligned(bias, 4) ||
+      !aligned(targets, dtype_size(t)) || !aligned(d_hidden, 16) || !aligned(d_weight, 16) ||
+      !aligned(d_bias, 4))
+    return FLP_MISALIGNED;
+  const size_t g = reduction == FLP_REDUCE_NONE ? size_t(N) * 4 : 4;
+  const Span ins[] = {span(grad_out, g), span(stats, size_t(N) * 8),
+                      span(hidden, size_t(N) * D * xs), span(weight, size_t(V) * D * xs),
+                      span(bias, size_t(V) * 4), span(targets, size_t(N) * dtype_size(t))};
+  const Span outs[] = {span(d_hidden, size_t(N) * D * xs), span(d_weight, size_t(V) * D * xs),
+                       span(d_bias, size_t(V) * 4), span(workspace, workspace_bytes)};
+  if (any_alias(outs, 4, ins, 6)) return FLP_INVALID_ARGUMENT;
+  const size_t front = loss_grad_layout(N).total;
+  if (workspace_bytes < front) return FLP_WORKSPACE_TOO_SMALL;
+  const BwdLayout L = bwd_layout_for_bytes(N, D, V, x, x, workspace_bytes - front,
+                                           d_hidden != nullptr, d_weight != nullptr,
+                                           d_bias != nullptr);
+  return L.chunk == 0 ? FLP_WORKSPACE_TOO_SMALL : FLP_OK;
+}
+
 NormLayout norm_layout(int64_t N, int64_t D) {
   NormLayout L;
   L.slab_rows = std::max(kNormMinRows, ceil_div(N, kNormSlabs));

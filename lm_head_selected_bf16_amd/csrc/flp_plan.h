@@ -100,6 +100,22 @@ struct EmbLayout {
 };
 EmbLayout emb_layout(int64_t N, int64_t D, int64_t V);
 
+// ---- linear cross entropy ----
+// Forward: the logp forward's partials, then logp, lse and the row losses [N] and the
+// vocabulary tiles' sums of logits [n_vt][N].
+struct LossFwdLayout {
+  FwdLayout fwd;
+  size_t logp_off = 0, lse_off = 0, rows_off = 0, zsum_off = 0, total = 0;
+};
+LossFwdLayout loss_fwd_layout(int64_t N, int64_t D, int64_t V);
+// Factor of the summed logits: the largest power of two that is at most 1 / V.
+float loss_zunit(int64_t V);
+// Backward: the per-row factors of dz, in front of the logp backward's workspace.
+struct LossGradLayout {
+  size_t softmax_off = 0, onehot_off = 0, uniform_off = 0, unscale_off = 0, total = 0;
+};
+LossGradLayout loss_grad_layout(int64_t N);
+
 // ---- layer norm backward: slabs of rows whose d_weight and d_bias partials are added ----
 constexpr int64_t kNormSlabs = 256;    // at most this many slabs (one workgroup per compute unit)
 constexpr int64_t kNormMinRows = 8;    // rows of a slab, at least
@@ -184,6 +200,24 @@ flp_status validate_embedding_backward(int64_t N, int64_t D, int64_t V, flp_dtyp
                                        const void* grad, const void* ids, flp_dtype id_dtype,
                                        const void* d_weight, flp_dtype dw_dtype,
                                        const void* workspace, size_t workspace_bytes);
+
+// Linear cross entropy.
+flp_status validate_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                          const void* hidden, const void* weight,
+                                          const float* bias, const void* targets,
+                                          flp_dtype t_dtype, double label_smoothing, double z_loss,
+                                          flp_reduction reduction, const float* out_loss,
+                                          const float* out_stats, const void* workspace,
+                                          size_t workspace_bytes);
+flp_status validate_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                           const float* grad_out, const float* stats,
+                                           const void* hidden, const void* weight,
+                                           const float* bias, const void* targets,
+                                           flp_dtype t_dtype, double label_smoothing,
+                                           double z_loss, flp_reduction reduction,
+                                           const void* d_hidden, const void* d_weight,
+                                           const float* d_bias, const void* workspace,
+                                           size_t workspace_bytes);
 
 // Layer norm; the parameters have the rows' type or fp32.
 flp_status validate_layer_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,

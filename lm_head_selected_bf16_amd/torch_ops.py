@@ -560,6 +560,127 @@ def embedding(weight, ids, scale=1.0):
     return Embedding.apply(weight, ids, scale)
 
 
+# ---- linear cross entropy -----------------------------------------------------------------------
+#
+# The training loss of the head: -logp with label smoothing, a squared log-partition term and a
+# reduction, without the logits.  Targets outside [0, V) are padding: loss 0, not counted, zero
+# gradients.
+
+_REDUCTIONS = {"none": _abi.FLP_REDUCE_NONE, "sum": _abi.FLP_REDUCE_SUM,
+               "mean": _abi.FLP_REDUCE_MEAN}
+
+
+def _prepare_loss(hidden, weight, targets, bias, reduction):
+    if reduction not in _REDUCTIONS:
+        raise ValueError("reduction must be 'none', 'sum' or 'mean'")
+    prep = _prepare(hidden, weight, targets, bias, None)
+    if any(t is not None and t.device != hidden.device for t in (weight, targets, bias)):
+        raise ValueError("hidden, weight, targets and bias must be on one device")
+    return prep, _REDUCTIONS[reduction]
+
+
+def cross_entropy_forward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                          bias: Optional[torch.Tensor] = None, label_smoothing: float = 0.0,
+                          z_loss: float = 0.0, reduction: str = "mean", return_stats: bool = True
+                          ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(loss, stats) through flp_cross_entropy_forward: loss float32 with the targets' shape
+    (reduction "none") or a scalar; stats float32 [2, *targets' shape], stats[0] = lse."""
+    (h2, t1, _, lead, N, D, V), red = _prepare_loss(hidden, weight, targets, bias, reduction)
+    dev = hidden.device
+    with _on(dev):
+        loss = torch.empty(lead if reduction == "none" else (), dtype=torch.float32, device=dev)
+        stats = None
+        if return_stats:
+            stats = torch.empty((2,) + lead, dtype=torch.float32, device=dev)
+        ws = torch.empty(max(_abi.flp_cross_entropy_forward_workspace_bytes(N, D, V), 16),
+                         dtype=torch.uint8, device=dev)
+        st = _abi.flp_cross_entropy_forward(N, D, V, _X_DTYPES[hidden.dtype], _ptr(h2),
+                                            _ptr(weight), _ptr(bias), _ptr(t1),
+                                            _T_DTYPES[targets.dtype], float(label_smoothing),
+                                            float(z_loss), red, _ptr(loss), _ptr(stats), _ptr(ws),
+                                            ws.numel(), _stream(dev))
+    _check("flp_cross_entropy_forward", st)
+    return loss, stats
+
+
+def cross_entropy_backward(grad_out: torch.Tensor, stats: torch.Tensor, hidden: torch.Tensor,
+                           weight: torch.Tensor, targets: torch.Tensor,
+                           bias: Optional[torch.Tensor] = None, label_smoothing: float = 0.0,
+                           z_loss: float = 0.0, reduction: str = "mean", need_hidden: bool = True,
+                           need_weight: bool = True, need_bias: Optional[bool] = None,
+                           workspace_bytes: Optional[int] = None):
+    """(d_hidden, d_weight, d_bias) through flp_cross_entropy_backward; unrequested ones are
+    None.  grad_out: float32, of the loss's shape.  The workspace is as large as the backward of
+    linear_logp takes by default; a smaller one runs more row chunks with the same bits."""
+    (h2, t1, _, lead, N, D, V), red = _prepare_loss(hidden, weight, targets, bias, reduction)
+    dev = hidden.device
+    want = lead if reduction == "none" else ()
+    for name, x, shape in (("grad_out", grad_out, want), ("stats", stats, (2,) + lead)):
+        if (x.dtype != torch.float32 or tuple(x.shape) != shape or not x.is_contiguous()
+                or x.device != dev):
+            raise ValueError(f"{name} must be contiguous float32 of shape {tuple(shape)} on the "
+                             "device of hidden")
+    if need_bias is None:
+        need_bias = bias is not None
+    xd = _X_DTYPES[hidden.dtype]
+    if workspace_bytes is None:
+        full, least = (_abi.flp_cross_entropy_backward_workspace_bytes(N, D, V, xd, c)
+                       for c in (max(N, 1), 0))
+        workspace_bytes = full if full <= DEFAULT_BWD_WORKSPACE else max(least,
+                                                                         DEFAULT_BWD_WORKSPACE)
+    with _on(dev):
+        d_hidden = torch.empty_like(hidden) if need_hidden else None
+        d_weight = torch.empty_like(weight) if need_weight else None
+        d_bias = torch.empty(V, dtype=torch.float32, device=dev) if need_bias else None
+        ws = torch.empty(max(int(workspace_bytes), 16), dtype=torch.uint8, device=dev)
+        st = _abi.flp_cross_entropy_backward(N, D, V, xd, _ptr(grad_out), _ptr(stats), _ptr(h2),
+                                             _ptr(weight), _ptr(bias), _ptr(t1),
+                                             _T_DTYPES[targets.dtype], float(label_smoothing),
+                                             float(z_loss), red, _ptr(d_hidden), _ptr(d_weight),
+                                             _ptr(d_bias), _ptr(ws), ws.numel(), _stream(dev))
+    _check("flp_cross_entropy_backward", st)
+    return d_hidden, d_weight, d_bias
+
+
+class LinearCrossEntropy(torch.autograd.Function):
+    """Autograd node of the linear cross entropy: the forward saves the rows' lse, the backward recomputes
+    the logits."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, targets, bias, label_smoothing, z_loss, reduction):
+        loss, stats = cross_entropy_forward(hidden, weight, targets, bias, label_smoothing, z_loss,
+                                          reduction)
+        ctx.save_for_backward(hidden, weight, targets, bias, stats)
+        ctx.terms = (label_smoothing, z_loss, reduction)
+        return loss
+
+    @staticmethod
+    def backward(ctx, g):
+        hidden, weight, targets, bias, stats = ctx.saved_tensors
+        need_h, need_w, _, need_b = ctx.needs_input_grad[:4]
+        dh, dw, db = cross_entropy_backward(g.contiguous(), stats, hidden, weight, targets, bias,
+                                            *ctx.terms, need_hidden=need_h, need_weight=need_w,
+                                            need_bias=need_b)
+        return dh, dw, None, db, None, None, None
+
+
+def linear_cross_entropy(hidden, weight, targets, bias=None, label_smoothing=0.0, z_loss=0.0,
+                         reduction="mean"):
+    """Cross entropy of hidden @ weight^T + bias against targets, differentiable in hidden, weight
+    and bias:
+
+        (1 - s) (lse - z[target]) + s (lse - mean(z)) + z_loss lse^2,   s = label_smoothing
+
+    per row ("none"), summed ("sum") or averaged over the rows whose target lies in [0, V)
+    ("mean", 0 when there are none); the other rows are padding with loss 0 and no gradient."""
+    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad
+                                              for t in (hidden, weight, bias)):
+        return cross_entropy_forward(hidden, weight, targets, bias, label_smoothing, z_loss,
+                                     reduction, return_stats=False)[0]
+    return LinearCrossEntropy.apply(hidden, weight, targets, bias, label_smoothing, z_loss,
+                                    reduction)
+
+
 # ---- dropout ------------------------------------------------------------------------------------
 #
 # The mask is a function of the element's position, p and rng (int64 [2] on the device: seed and

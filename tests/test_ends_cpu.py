@@ -1,4 +1,4 @@
-"""Gates of the scaled embedding, dropout and layer norm on a machine without a GPU: fake
+"""Gates of the scaled embedding, dropout, layer norm and linear cross entropy on a machine without a GPU: fake
 addresses, every call returns before the device is touched; and the argument checks of their
 Python entry points that need no device."""
 import pytest
@@ -138,6 +138,88 @@ def test_scaled_embedding_keeps_the_gates_of_the_lookup():
                                                   A[3], 64, 0)) == "FLP_WORKSPACE_TOO_SMALL"
 
 
+def ce_fwd(**kw):
+    a = dict(N=N, D=D, V=V, x=BF16, h=A[0], w=A[1], b=A[2], t=A[3], td=I64, s=0.1, c=1e-4,
+             red=abi.FLP_REDUCE_MEAN, loss=A[4], lse=A[5], ws=A[6],
+             wsb=abi.flp_cross_entropy_forward_workspace_bytes(N, D, V))
+    a.update(kw)
+    return name(abi.flp_cross_entropy_forward(a["N"], a["D"], a["V"], a["x"], a["h"], a["w"],
+                                              a["b"], a["t"], a["td"], a["s"], a["c"], a["red"],
+                                              a["loss"], a["lse"], a["ws"], a["wsb"], 0))
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(N=-1), "FLP_INVALID_ARGUMENT"),
+    (dict(D=48), "FLP_UNSUPPORTED_SHAPE"),
+    (dict(x=I64), "FLP_UNSUPPORTED_DTYPE"),
+    (dict(td=F32), "FLP_UNSUPPORTED_DTYPE"),
+    (dict(s=-0.1), "FLP_INVALID_ARGUMENT"),
+    (dict(s=1.1), "FLP_INVALID_ARGUMENT"),
+    (dict(s=NAN), "FLP_INVALID_ARGUMENT"),
+    (dict(c=-1.0), "FLP_INVALID_ARGUMENT"),
+    (dict(c=INF), "FLP_INVALID_ARGUMENT"),
+    (dict(red=3), "FLP_INVALID_ARGUMENT"),
+    (dict(h=0), "FLP_INVALID_ARGUMENT"),
+    (dict(t=0), "FLP_INVALID_ARGUMENT"),
+    (dict(loss=0), "FLP_INVALID_ARGUMENT"),
+    (dict(ws=0), "FLP_INVALID_ARGUMENT"),
+    (dict(h=A[0] + 8), "FLP_MISALIGNED"),
+    (dict(loss=A[4] + 2), "FLP_MISALIGNED"),
+    (dict(t=A[3] + 4), "FLP_MISALIGNED"),
+    (dict(loss=A[5] + 8 * N - 4), "FLP_INVALID_ARGUMENT"),  # the loss inside the statistics
+    (dict(ws=A[1] + 256), "FLP_INVALID_ARGUMENT"),          # workspace inside the weight
+    (dict(wsb=256), "FLP_WORKSPACE_TOO_SMALL"),
+    (dict(N=0, loss=0), "FLP_INVALID_ARGUMENT"),            # a reduced loss is written
+    (dict(N=0, loss=A[4] + 1), "FLP_MISALIGNED"),
+    (dict(N=0, red=abi.FLP_REDUCE_NONE, h=0, t=0, loss=0, lse=0, ws=0), "FLP_OK"),
+])
+def test_cross_entropy_forward_gates(kw, expect):
+    assert ce_fwd(**kw) == expect
+
+
+def ce_bwd(**kw):
+    a = dict(N=N, D=D, V=V, x=BF16, g=A[0], lse=A[1], h=A[2], w=A[3], b=A[4], t=A[5], td=I32,
+             s=0.0, c=0.0, red=abi.FLP_REDUCE_MEAN, dh=A[6], dw=A[7], db=A[8], ws=A[9],
+             wsb=abi.flp_cross_entropy_backward_workspace_bytes(N, D, V, BF16, 0))
+    a.update(kw)
+    return name(abi.flp_cross_entropy_backward(a["N"], a["D"], a["V"], a["x"], a["g"], a["lse"],
+                                               a["h"], a["w"], a["b"], a["t"], a["td"], a["s"],
+                                               a["c"], a["red"], a["dh"], a["dw"], a["db"],
+                                               a["ws"], a["wsb"], 0))
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(D=100), "FLP_UNSUPPORTED_SHAPE"),
+    (dict(s=2.0), "FLP_INVALID_ARGUMENT"),
+    (dict(c=NAN), "FLP_INVALID_ARGUMENT"),
+    (dict(red=-1), "FLP_INVALID_ARGUMENT"),
+    (dict(g=0), "FLP_INVALID_ARGUMENT"),
+    (dict(lse=0), "FLP_INVALID_ARGUMENT"),
+    (dict(ws=0), "FLP_INVALID_ARGUMENT"),
+    (dict(dh=A[6] + 2), "FLP_MISALIGNED"),
+    (dict(dh=A[2]), "FLP_INVALID_ARGUMENT"),
+    (dict(db=A[7] + 64), "FLP_INVALID_ARGUMENT"),
+    (dict(ws=A[0] - 256), "FLP_INVALID_ARGUMENT"),          # workspace runs into grad_out
+    (dict(wsb=64), "FLP_WORKSPACE_TOO_SMALL"),
+    (dict(wsb=abi.flp_cross_entropy_backward_workspace_bytes(N, D, V, BF16, 0) - 1),
+     "FLP_WORKSPACE_TOO_SMALL"),
+    (dict(dh=0, dw=0, db=0, ws=0), "FLP_OK"),
+    (dict(N=0, g=0, lse=0, h=0, t=0, dw=0, db=0, ws=0), "FLP_OK"),
+    (dict(N=0, g=0, lse=0, h=0, t=0, dw=A[7] + 8, ws=0), "FLP_MISALIGNED"),
+])
+def test_cross_entropy_backward_gates(kw, expect):
+    assert ce_bwd(**kw) == expect
+
+
+def test_cross_entropy_workspace_bytes():
+    n_vt = -(-V // 256)
+    assert (abi.flp_cross_entropy_forward_workspace_bytes(N, D, V)
+            >= abi.flp_forward_workspace_bytes(N, D, V) + n_vt * N * 4 + 3 * N * 4)
+    assert (abi.flp_cross_entropy_backward_workspace_bytes(N, D, V, BF16, 0)
+            >= abi.flp_backward_workspace_bytes(N, D, V, BF16, BF16, 0) + 3 * N * 4 + 4)
+    assert abi.flp_cross_entropy_backward_workspace_bytes(0, D, V, BF16, 0) == 0
+
+
 def test_python_checks():
     x = torch.zeros(4, 8)
     rng = torch.zeros(2, dtype=torch.int64)
@@ -151,3 +233,8 @@ def test_python_checks():
         flp.dropout(x.long(), 0.1, rng)
     with pytest.raises(ValueError, match="GPU"):
         flp.embedding(x, torch.zeros(3, dtype=torch.int64), scale=2.0)
+    t = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError, match="reduction"):
+        flp.linear_cross_entropy(x, x, t, reduction="average")
+    with pytest.raises(ValueError, match="GPU"):
+        flp.linear_cross_entropy(x, x, t)

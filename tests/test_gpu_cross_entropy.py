@@ -1,0 +1,391 @@
+"""Linear cross entropy against its definition in 64 bits: every type, ragged rows and
+vocabularies, label smoothing, z-loss and the three reductions, padded rows that hold infinities
+and NaN, vocabulary entries masked by the bias, row chunks, fp16 gradients far below the type's
+range, differences, determinism, streams and graphs."""
+import math
+
+import pytest
+import torch
+
+from gpu_common import flp, say
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+U = 2.0 ** -24
+
+
+def make(N, D, V, dtype, seed, bias=True, ignored=0.1, w_std=0.05):
+    g = torch.Generator().manual_seed(seed)
+    h = torch.randn(N, D, generator=g).to(dtype).cuda()
+    w = (torch.randn(V, D, generator=g) * w_std).to(dtype).cuda()
+    b = (torch.randn(V, generator=g) * 0.3).cuda() if bias else None
+    t = torch.randint(0, V, (N,), generator=g)
+    t[torch.rand(N, generator=g) < ignored] = -100
+    if N > 3 and ignored:
+        t[1], t[2] = V, -1
+    up = torch.randn(N, generator=g).cuda()
+    return h, w, b, t.cuda(), up
+
+
+def reference(h, w, b, t, s, c, reduction, up):
+    """Losses, lse and gradients in 64 bits, with the logits and dz for the error bounds."""
+    V = w.shape[0]
+    ok = (t >= 0) & (t < V)
+    h = torch.where(ok[:, None], h.double(), 0.0)
+    w = w.double()
+    z = h @ w.t()
+    if b is not None:
+        z = z + b.double()
+    lse = torch.logsumexp(z, 1)
+    tc = torch.where(ok, t, 0)[:, None]
+    loss = (1 - s) * (lse - z.gather(1, tc)[:, 0]) + c * lse ** 2
+    if s:
+        loss = loss + s * (lse - z.mean(1))
+    loss = torch.where(ok, loss, 0.0)
+    n = max(int(ok.sum()), 1)
+    g = {"none": up.double(), "sum": torch.ones_like(lse) * float(up[0]),
+         "mean": torch.ones_like(lse) * float(up[0]) / n}[reduction]
+    g = torch.where(ok, g, 0.0)[:, None]
+    p = torch.exp(z - lse[:, None])
+    onehot = torch.zeros_like(z).scatter_(1, tc, 1.0)
+    dz = g * ((1 + 2 * c * lse)[:, None] * p - (1 - s) * onehot - s / V)
+    dz = torch.where(ok[:, None], dz, 0.0)
+    total = {"none": loss, "sum": loss.sum(), "mean": loss.sum() / n}[reduction]
+    return dict(loss=total, rows=loss, lse=lse, ok=ok, n=n, z=z, p=p, g=g, dz=dz, h=h, w=w,
+                dh=dz @ w, dw=dz.t() @ h, db=dz.sum(0))
+
+
+def rounding(t, ref):
+    f = torch.finfo(t)
+    return (f.eps / 2) * ref.abs().clamp(min=f.smallest_normal)
+
+
+def check(name, got, ref, tol):
+    err = (got.double() - ref).abs()
+    worst = float((err / tol).max()) if err.numel() else 0.0
+    say(f"  {name}: worst error {worst:.3f} of its bound")
+    assert bool((err <= tol).all()), (name, worst)
+
+
+def bounds(r, s, c, reduction, dtype):
+    """Error bounds.  A logit is a chain of D fp32 products (D U times the sum of their sizes),
+    plus the bias; exp and its argument are off by (|z| + 4) 4 U; sums of V exponentials by
+    (V / 256 + 32) U at most.  dz then holds one rounding to the inputs' type, and each gradient
+    a chain of fp32 products and one rounding."""
+    D, V, N = r["h"].shape[1], r["w"].shape[0], r["h"].shape[0]
+    ez = (r["h"].abs() @ r["w"].abs().t()) * D * U + 2 * U * r["z"].abs()
+    top = ez.max(1).values
+    zmax = r["z"].abs().max(1).values
+    elog = (zmax + 4) * 4 * U + (V / 256 + 32) * U
+    elss = 2 * top + 2 * elog
+    erow = (2 + 2 * c * r["lse"].abs()) * elss + 8 * U * (r["rows"].abs() + zmax * (1 + V * U)
+                                                          + c * r["lse"] ** 2)
+    if s:
+        erow = erow + s * (V / 256 + 64) * U * zmax
+    erow = torch.where(r["ok"], erow, 0.0)
+    rel = (2 * top + 2 * elog)[:, None]  # of p
+    a = (1 + 2 * c * r["lse"].abs())[:, None]
+    ga = r["g"].abs()
+    edz = ga * a * r["p"] * (rel + 8 * U) + 2 * c * ga * r["p"] * elss[:, None] + 4 * U * ga * (
+        r["p"] * a + (r["dz"].abs() / ga.clamp(min=1e-300)).clamp(max=2 + float(a.max())))
+    # the exponential and the matrix products flush what is below the smallest normal number,
+    # 2^-126 (logits spread over several hundred reach it): p, and dz itself
+    edz = edz + torch.where(r["ok"][:, None], 2.0 ** -126 * (1 + ga * a), 0.0)
+    half = torch.finfo(dtype).eps / 2 if dtype != F32 else 0.0
+    return erow, edz + (r["dz"].abs() + edz) * half
+
+
+def run(h, w, b, t, up, s=0.0, c=0.0, reduction="mean", **kw):
+    m = flp()
+    loss, stats = m.cross_entropy_forward(h, w, t, b, s, c, reduction)
+    g = up if reduction == "none" else up[0].clone()
+    dh, dw, db = m.cross_entropy_backward(g, stats, h, w, t, b, s, c, reduction,
+                                          need_bias=True, **kw)
+    return loss, stats[0], dh, dw, db
+
+
+def compare(h, w, b, t, up, s=0.0, c=0.0, reduction="mean", **kw):
+    loss, lse, dh, dw, db = run(h, w, b, t, up, s, c, reduction, **kw)
+    r = reference(h, w, b, t, s, c, reduction, up)
+    erow, edz = bounds(r, s, c, reduction, h.dtype)
+    N, D = h.shape
+    V = w.shape[0]
+    if reduction == "none":
+        check("loss", loss, r["loss"], erow + 2 * U * r["rows"].abs() + 1e-300)
+    else:
+        div = r["n"] if reduction == "mean" else 1
+        tol = (erow.sum() + (N / 1024 + 16) * U * r["rows"].abs().sum()) / div
+        check("loss", loss, r["loss"], tol + 2 * U * r["loss"].abs() + 1e-300)
+    # fp16: entries of dz below 2^-24 / 2^10 of the largest row factor are lost (subnormal step)
+    sub = 0.0
+    if h.dtype == F16:
+        sub = float((r["g"].abs() * (1 + 2 * c * r["lse"].abs())[:, None]).max()) * 2.0 ** -34
+    edz = edz + torch.where(r["ok"][:, None], sub, 0.0)
+    check("d_hidden", dh, r["dh"], edz @ r["w"].abs() + V * U * (r["dz"].abs() @ r["w"].abs())
+          + rounding(h.dtype, r["dh"]) * 1.01 + 1e-300)
+    check("d_weight", dw, r["dw"], edz.t() @ r["h"].abs()
+          + N * U * (r["dz"].abs().t() @ r["h"].abs()) + rounding(h.dtype, r["dw"]) * 1.01 + 1e-300)
+    # d_bias adds the unrounded fp32 entries
+    check("d_bias", db, r["db"], edz.sum(0) + N * U * r["dz"].abs().sum(0) + 1e-300)
+    assert not dh[~r["ok"]].any()
+    return loss, lse, dh, dw, db
+
+
+SHAPES = [(1, 32, 1), (1, 64, 255), (3, 32, 256), (33, 96, 257), (64, 256, 4096), (65, 160, 1000),
+          (130, 96, 2049), (300, 64, 777), (600, 224, 5003)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("k", range(len(SHAPES)))
+def test_shapes(k, dtype):
+    N, D, V = SHAPES[k]
+    args = make(N, D, V, dtype, 10 * k, ignored=0.1 if N > 1 else 0.0)
+    for s, c, red in ((0.0, 0.0, "mean"), (0.1, 1e-3, "none")):
+        say(f"N={N} D={D} V={V} {dtype} s={s} c={c} {red}")
+        compare(*args, s=s, c=c, reduction=red)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
+@pytest.mark.parametrize("s,c,bias", [(0.0, 1e-2, False), (0.3, 0.0, True), (1.0, 1e-4, True)])
+def test_terms(dtype, reduction, s, c, bias):
+    compare(*make(130, 64, 1300, dtype, 5, bias=bias), s=s, c=c, reduction=reduction)
+
+
+def test_int32_targets_and_leading_shape():
+    m = flp()
+    h, w, b, t, up = make(24, 64, 500, BF16, 6)
+    want = m.linear_cross_entropy(h, w, t, b, 0.1, 1e-3, "none")
+    got = m.linear_cross_entropy(h.view(2, 3, 4, 64), w, t.int().view(2, 3, 4), b, 0.1, 1e-3,
+                                 "none")
+    assert got.shape == (2, 3, 4) and torch.equal(got.view(-1), want)
+
+
+def test_plain_loss_is_minus_logp():
+    m = flp()
+    h, w, b, t, up = make(300, 96, 3001, BF16, 7)
+    loss = m.linear_cross_entropy(h, w, t, b, reduction="none")
+    assert torch.equal(loss, -m.linear_logp(h, w, t, b) + 0.0)
+
+
+def test_padded_rows_hold_anything():
+    """Rows whose target is outside the vocabulary: infinities and NaN in their hidden rows reach
+    neither a loss nor a gradient."""
+    for dtype in (BF16, F16, F32):
+        h, w, b, t, up = make(70, 64, 600, dtype, 8)
+        clean = run(h, w, b, t, up, 0.1, 1e-3, "mean")
+        pad = (t < 0) | (t >= 600)
+        assert int(pad.sum()) > 3
+        bad = h.clone()
+        bad[pad] = float("nan")
+        bad[pad.nonzero()[0]] = float("inf")
+        got = run(bad, w, b, t, up, 0.1, 1e-3, "mean")
+        for k, (x, y) in enumerate(zip(got, clean)):
+            if k == 1:  # lse of a padded row is whatever its logits are
+                x, y = x[~pad], y[~pad]
+            assert torch.equal(x, y), k
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_nothing_but_padding(dtype):
+    h, w, b, t, up = make(40, 64, 300, dtype, 9)
+    t.fill_(-100)
+    for reduction in ("none", "sum", "mean"):
+        loss, lse, dh, dw, db = run(h, w, b, t, up, 0.1, 1e-3, reduction)
+        for x in (loss, dh, dw, db):
+            assert not x.any()
+
+
+@pytest.mark.parametrize("low", [-math.inf, torch.finfo(F32).min, -1e30])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_masked_vocabulary(dtype, low):
+    """Entries masked through the bias, whole 256-column tiles among them: probability 0 and no
+    gradient, the loss that of the remaining vocabulary."""
+    m = flp()
+    h, w, b, t, up = make(50, 64, 1500, dtype, 10, ignored=0.0)
+    keep = torch.zeros(1500, dtype=torch.bool, device="cuda")
+    keep[256:300] = True
+    keep[1024:1400] = True
+    masked = torch.where(keep, b, torch.full_like(b, low))
+    t = keep.nonzero()[:, 0][t % int(keep.sum())]
+    loss, lse, dh, dw, db = run(h, w, masked, t, up, 0.0, 1e-3, "none")
+    index = torch.cumsum(keep, 0) - 1
+    r = reference(h, w[keep].contiguous(), b[keep].contiguous(), index[t], 0.0, 1e-3, "none", up)
+    erow, edz = bounds(r, 0.0, 1e-3, "none", dtype)
+    check("loss", loss, r["loss"], erow + 2 * U * r["rows"].abs())
+    assert not dw[~keep].any() and not db[~keep].any()
+    check("d_bias", db[keep], r["db"], edz.sum(0) + 50 * U * r["dz"].abs().sum(0))
+    check("d_hidden", dh, r["dh"], edz @ r["w"].abs()
+          + 1500 * U * (r["dz"].abs() @ r["w"].abs()) + rounding(dtype, r["dh"]) * 1.01)
+
+
+def test_lowest_everywhere_is_uniform():
+    """Every entry masked with the lowest fp32 value: the row is uniform over the vocabulary."""
+    h, w, b, t, up = make(20, 64, 700, F32, 11, ignored=0.0)
+    b = torch.full_like(b, torch.finfo(F32).min)
+    loss, lse, dh, dw, db = run(h, w, b, t, up, 0.0, 0.0, "none")
+    assert bool((loss.double() - math.log(700)).abs().max() <= 64 * U * math.log(700))
+    p = torch.full((20, 700), 1.0 / 700, device="cuda", dtype=torch.float64)
+    dz = up.double()[:, None] * (p - torch.nn.functional.one_hot(t, 700))
+    check("d_bias", db, dz.sum(0), 64 * U * dz.abs().sum(0))
+
+
+def test_smoothing_over_the_lowest_value_stays_finite():
+    """Half the vocabulary at the lowest fp32 value, label smoothing on: the mean of the logits
+    is representable although their sum is not."""
+    m = flp()
+    h, w, b, t, up = make(20, 64, 4096, F32, 12, ignored=0.0)
+    b[2048:] = torch.finfo(F32).min
+    loss = m.linear_cross_entropy(h, w, t % 2048, b, label_smoothing=0.25, reduction="none")
+    want = 0.25 * 0.5 * -float(torch.finfo(F32).min)
+    assert bool((loss.double() / want - 1).abs().max() < 1e-5)
+
+
+def test_large_and_confident_logits():
+    """Logits of several hundred, and rows whose target has probability 1 up to rounding."""
+    for dtype in (BF16, F32):
+        h, w, b, t, up = make(40, 64, 900, dtype, 13, w_std=6.0, ignored=0.0)
+        with torch.no_grad():
+            t[:20] = (h[:20].float() @ w.float().t() + b).argmax(1)
+        compare(h, w, b, t, up, c=1e-4, reduction="none")
+
+
+def test_small_fp16_gradients_do_not_underflow():
+    """A mean over 2000 rows, and an upstream gradient of 2^-12: dz is below what fp16 holds."""
+    h, w, b, t, up = make(2000, 64, 3000, F16, 14)
+    up[0] = 2.0 ** -12
+    compare(h, w, b, t, up, s=0.1, reduction="mean")
+    up = up * 2.0 ** 40  # and gradients beyond its largest value, over a sum in range
+    r = reference(h, w, b, t, 0.0, 0.0, "mean", up)
+    loss, lse, dh, dw, db = run(h, w, b, t, up, 0.0, 0.0, "mean")
+    check("d_bias", db, r["db"], r["dz"].abs().sum(0) * 1e-3)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_row_chunks_keep_the_bits(dtype):
+    """The smallest workspace (256-row chunks) and the largest give the same gradients."""
+    m = flp()
+    h, w, b, t, up = make(700, 64, 2000, dtype, 15)
+    code = {BF16: m.FLP_BF16, F16: m.FLP_F16, F32: m.FLP_F32}[dtype]
+    least = m.flp_cross_entropy_backward_workspace_bytes(700, 64, 2000, code, 256)
+    one = m.flp_cross_entropy_backward_workspace_bytes(700, 64, 2000, code, 700)
+    a = run(h, w, b, t, up, 0.1, 1e-3, "mean", workspace_bytes=least)
+    z = run(h, w, b, t, up, 0.1, 1e-3, "mean", workspace_bytes=one)
+    assert all(torch.equal(x, y) for x, y in zip(a, z))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_do_not_depend_on_the_batch(dtype):
+    m = flp()
+    h, w, b, t, up = make(333, 96, 2500, dtype, 16)
+    loss, lse, dh, dw, db = run(h, w, b, t, up, 0.1, 1e-3, "none")
+    again = run(h, w, b, t, up, 0.1, 1e-3, "none")
+    assert all(torch.equal(x, y) for x, y in zip((loss, lse, dh, dw, db), again))
+    for lo, hi in ((0, 1), (100, 133), (200, 333)):
+        s = slice(lo, hi)
+        part = run(h[s].contiguous(), w, b, t[s].contiguous(), up[s].contiguous(), 0.1, 1e-3,
+                   "none")
+        for x, y in zip(part[:3], (loss, lse, dh)):
+            assert torch.equal(x, y[s])
+
+
+def test_gradient_against_differences():
+    m = flp()
+    h, w, b, t, up = make(6, 32, 40, F32, 17, ignored=0.0, w_std=0.3)
+    t[5] = -1
+    leaves = [x.clone().requires_grad_(True) for x in (h, w, b)]
+    for reduction in ("mean", "sum"):
+        loss = m.linear_cross_entropy(leaves[0], leaves[1], t, leaves[2], 0.1, 1e-2, reduction)
+        grads = torch.autograd.grad(loss, leaves)
+        step = 2.0 ** -6
+        for k, x in enumerate((h, w, b)):
+            flat = x.view(-1)
+            for e in range(0, flat.numel(), 37):
+                old = float(flat[e])
+                vals = []
+                for d in (step, -step):
+                    flat[e] = old + d
+                    vals.append(float(m.linear_cross_entropy(h, w, t, b, 0.1, 1e-2, reduction)))
+                flat[e] = old
+                diff = (vals[0] - vals[1]) / (2 * step)
+                # a third derivative below 40 over six rows, and 64 U of a loss below 64
+                assert abs(diff - float(grads[k].view(-1)[e])) < 40 * 6 * step ** 2 / 6 * 0.05 \
+                    + 64 * 64 * U / (2 * step)
+
+
+def test_autograd_asks_only_for_what_needs_a_gradient():
+    m = flp()
+    h, w, b, t, up = make(60, 64, 500, BF16, 18)
+    _, _, dh, dw, db = run(h, w, b, t, torch.ones_like(up), 0.1, 0.0, "mean")
+    for need in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 1)):
+        leaves = [x.clone().requires_grad_(bool(n)) for x, n in zip((h, w, b), need)]
+        m.linear_cross_entropy(leaves[0], leaves[1], t, leaves[2], 0.1).backward()
+        for x, n, want in zip(leaves, need, (dh, dw, db)):
+            assert (x.grad is not None) == bool(n)
+            assert x.grad is None or torch.equal(x.grad, want)
+    # twice through the same graph
+    x = h.clone().requires_grad_(True)
+    loss = m.linear_cross_entropy(x, w, t, b, 0.1)
+    one = torch.autograd.grad(loss, [x], retain_graph=True)[0]
+    two = torch.autograd.grad(loss * 2, [x])[0]
+    assert torch.equal(one, dh) and torch.equal(one.float() * 2, two.float())
+
+
+def test_empty_batch():
+    m = flp()
+    w = torch.randn(300, 64, device="cuda", dtype=BF16, requires_grad=True)
+    h = torch.empty(0, 64, device="cuda", dtype=BF16, requires_grad=True)
+    t = torch.empty(0, dtype=torch.int64, device="cuda")
+    for reduction in ("none", "sum", "mean"):
+        loss = m.linear_cross_entropy(h, w, t, reduction=reduction)
+        assert loss.numel() == (0 if reduction == "none" else 1) and not loss.any()
+        dw, dh = torch.autograd.grad(loss.sum(), [w, h])
+        assert not dw.any() and dh.shape == (0, 64)
+
+
+def test_graph_replays_with_new_inputs():
+    m = flp()
+    h, w, b, t, up = make(260, 64, 1500, BF16, 19)
+    g = torch.ones((), device="cuda")
+
+    def step():
+        loss, stats = m.cross_entropy_forward(h, w, t, b, 0.1, 1e-3)
+        return (loss,) + m.cross_entropy_backward(g, stats, h, w, t, b, 0.1, 1e-3)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for rep in range(4):
+        nh, _, _, nt, _ = make(260, 64, 1500, BF16, 100 + rep)
+        h.copy_(nh)
+        t.copy_(nt)
+        g.fill_(0.5 + rep)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, step())), rep
+
+
+def test_refusals():
+    m = flp()
+    h, w, b, t, up = make(8, 64, 100, BF16, 20)
+    for kw in (dict(label_smoothing=-0.1), dict(label_smoothing=1.5), dict(z_loss=-1.0),
+               dict(z_loss=float("nan"))):
+        with pytest.raises(m.FlpError):
+            m.linear_cross_entropy(h, w, t, **kw)
+    with pytest.raises(ValueError):
+        m.linear_cross_entropy(h, w, t, reduction="max")
+    with pytest.raises(ValueError):
+        m.linear_cross_entropy(h, w, t.cpu())
+    with pytest.raises(ValueError):
+        m.linear_cross_entropy(h, w, t, b.double())
+    with pytest.raises(TypeError):
+        m.linear_cross_entropy(h, w.float(), t)
+    with pytest.raises(m.FlpError):
+        m.linear_cross_entropy(h[:, :40].contiguous(), w[:, :40].contiguous(), t)
+    loss, stats = m.cross_entropy_forward(h, w, t, b)
+    with pytest.raises(ValueError):
+        m.cross_entropy_backward(up, stats, h, w, t, b)  # a scalar is wanted
+    with pytest.raises(ValueError):
+        m.cross_entropy_backward(torch.ones((), device="cuda"), stats[:1], h, w, t, b)
