@@ -1568,23 +1568,6 @@ __global__ __launch_bounds__(256) void k_dbias_fold(const float* part, int64_t n
 
 // ---- launch helpers ----------------------------------------------------------------------------
 
-// Dynamic LDS above 64 KiB must be opted into per kernel and device.  Each launch
-// site keeps a per-device record of having done so; two threads that race on the
-// first launch both set the same attribute.
-constexpr int kMaxDevices = 64;
-template <class K>
-hipError_t prepare(K kernel, size_t lds, std::atomic<int> (&ready)[kMaxDevices]) {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  const bool tracked = dev >= 0 && dev < kMaxDevices;
-  if (tracked && ready[dev].load(std::memory_order_acquire) != 0) return hipSuccess;
-  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
-  if (e == hipSuccess && tracked) ready[dev].store(1, std::memory_order_release);
-  return e;
-}
-
 template <class E, int BM, int WM, bool ODD, bool LOSS, int NS = 2>
 hipError_t fwd_cfg(const FwdArgs& a, hipStream_t s) {
   using Eng = LogitEngine<E, BM, WM, NS>;

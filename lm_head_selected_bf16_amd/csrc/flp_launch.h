@@ -3,6 +3,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+
 #include "flp_plan.h"
 
 namespace flp {
@@ -17,6 +19,23 @@ flp_status enqueue_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype, c
                            const void* weight, const float* bias, const void* targets,
                            flp_dtype t_dtype, const float* temperature, float* out_logp,
                            float* out_lse, void* workspace, hipStream_t s);
+
+// Dynamic LDS above 64 KiB must be opted into per kernel and device.  Each launch
+// site keeps a per-device record of having done so; two threads that race on the
+// first launch both set the same attribute.
+constexpr int kMaxDevices = 64;
+template <class K>
+hipError_t prepare(K kernel, size_t lds, std::atomic<int> (&ready)[kMaxDevices]) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const bool tracked = dev >= 0 && dev < kMaxDevices;
+  if (tracked && ready[dev].load(std::memory_order_acquire) != 0) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+  if (e == hipSuccess && tracked) ready[dev].store(1, std::memory_order_release);
+  return e;
+}
 
 struct FwdArgs {
   const void* hidden;
@@ -165,6 +184,7 @@ struct NormFwdArgs {
   const void* x;             // [N][D]
   const void* weight;        // [D] or null
   const void* bias;          // [D] or null
+  bool wide;                 // the parameters are fp32 (set by the launcher)
   float eps;
   void* out;                 // [N][D]
   float* mean;               // [N] or null
@@ -175,13 +195,14 @@ struct NormBwdArgs {
   const void* grad;          // [N][D]
   const void* x;             // [N][D]
   const void* weight;        // [D] or null
+  bool wide;                 // the parameters are fp32 (set by the launcher)
   const float* mean;         // [N]
   const float* rstd;         // [N]
   void* d_x;                 // [N][D] or null
   void* d_weight;            // [D] or null
   void* d_bias;              // [D] or null
   int64_t slabs, slab_rows;  // rows are summed in slabs of slab_rows
-  float* part;               // [slabs][2][D] partial d_weight and d_bias
+  float* part;               // [slabs][2][D] partial d_weight and d_bias, or null for neither
 };
 hipError_t launch_layer_norm_forward(flp_dtype x, flp_dtype w, const NormFwdArgs& a,
                                      hipStream_t s);

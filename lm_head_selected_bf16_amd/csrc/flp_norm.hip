@@ -8,6 +8,9 @@
 // All arithmetic is fp32 (the variance from the centred values, so a large common
 // offset of a row does not cancel); out, d_x, d_w and d_b are rounded once.
 //
+// Bound by memory: the forward reads x and writes out, the backward reads grad and x and
+// writes d_x.
+//
 // A row's sums run in an order fixed by D alone, so out, mean, rstd and d_x of a
 // row are bitwise the same whatever the other rows are.  d_w and d_b add rows in
 // fixed slabs (cut by N alone), each slab in ascending order, then the slabs in
@@ -16,6 +19,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "flp_launch.h"
@@ -23,10 +27,288 @@
 namespace flp {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 template <class T>
 __device__ __forceinline__ float to_f32(T v) {
   return float(v);
 }
+
+// ---- rows held in registers (D up to kTeamMax) ------------------------------------------------
+//
+// A team of TEAM threads (one wave, or four) owns a row; thread t holds the chunks of
+// eight elements t, t + TEAM, ... (at most NCH).  A row is read from memory once, with
+// 16-byte loads that all stay in flight, and both its sums run over the registers.  Rows
+// need no alignment: the loads and stores are of the element's alignment, which the
+// memory path takes at full width; only a row's last, partial chunk goes element by
+// element.
+constexpr int kChunk = 8;
+
+typedef u32x4 loose __attribute__((aligned(2)));
+
+template <class T>
+struct Chunk {
+  static constexpr int kWords = kChunk * int(sizeof(T)) / 16;
+  typedef T vec __attribute__((ext_vector_type(kChunk)));
+  union {
+    u32x4 w[kWords];
+    vec v;
+  };
+
+  // n valid elements of the chunk at p (zeros past them); n <= 0 loads nothing.
+  __device__ __forceinline__ void load(const T* p, int64_t n) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = u32x4{0u, 0u, 0u, 0u};
+    if (n >= kChunk) {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) w[k] = reinterpret_cast<const loose*>(p)[k];
+    } else if (n > 0) {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k)
+        if (k < n) v[k] = p[k];
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int64_t n) const {
+    if (n >= kChunk) {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) reinterpret_cast<loose*>(p)[k] = w[k];
+    } else if (n > 0) {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k)
+        if (k < n) p[k] = v[k];
+    }
+  }
+};
+
+// Eight parameters as fp32 (`wide`: they are stored as fp32, else in T).
+template <class T>
+__device__ __forceinline__ void load_params(const void* base, bool wide, int64_t d, int64_t n,
+                                            float (&x)[kChunk]) {
+  if (sizeof(T) == 4 || wide) {
+    Chunk<float> c;
+    c.load(static_cast<const float*>(base) + d, n);
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) x[k] = c.v[k];
+  } else {
+    Chunk<T> c;
+    c.load(static_cast<const T*>(base) + d, n);
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) x[k] = to_f32(T(c.v[k]));
+  }
+}
+
+// Sum over the wave, the same bits in every lane: quad permutations, the mirrors of 8
+// and 16 lanes (each then meets the other half's value), and the 16- and 32-lane swaps,
+// all of them VALU moves.
+__device__ __forceinline__ float wave_sum(float x) {
+  auto dpp = [](float v, auto ctrl) {
+    return __int_as_float(
+        __builtin_amdgcn_mov_dpp(__float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  x += dpp(x, std::integral_constant<int, 0xB1>{});
+  x += dpp(x, std::integral_constant<int, 0x4E>{});
+  x += dpp(x, std::integral_constant<int, 0x141>{});
+  x += dpp(x, std::integral_constant<int, 0x140>{});
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Sum over the team, the same bits in every thread.  A team of four waves meets in LDS
+// (`red`: a float per wave of the workgroup, another slot on every call in turn).
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float x, float* red) {
+  x = wave_sum(x);
+  if constexpr (TEAM == 64) return x;
+  const int wave = threadIdx.x >> 6, first = wave & ~3;
+  if ((threadIdx.x & 63) == 0) red[wave] = x;
+  __syncthreads();
+  return (red[first] + red[first + 1]) + (red[first + 2] + red[first + 3]);
+}
+
+constexpr int kTeamThreads = 512;
+
+template <class T, int TEAM, int NCH>
+__global__ __launch_bounds__(256) void k_norm_fwd_row(NormFwdArgs p) {
+  constexpr int kTeams = 256 / TEAM;
+  __shared__ float red[2][4];
+  const int t = threadIdx.x % TEAM;
+  const int64_t D = p.D;
+  const float inv = 1.0f / float(D);
+  // Every team of the workgroup takes part in every step (they share barriers).
+  for (int64_t r0 = int64_t(blockIdx.x) * kTeams; r0 < p.N; r0 += int64_t(gridDim.x) * kTeams) {
+    const int64_t row = r0 + threadIdx.x / TEAM;
+    const bool live = row < p.N;
+    const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * D;
+    Chunk<T> c[NCH];
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t d = int64_t(k * TEAM + t) * kChunk;
+      c[k].load(x + d, live ? D - d : 0);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      float q = 0.f;
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) q += to_f32(T(c[k].v[e]));
+      s += q;
+    }
+    const float mean = team_sum<TEAM>(s, red[0]) * inv;
+    float var = 0.f;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t n = D - int64_t(k * TEAM + t) * kChunk;
+      float q = 0.f;
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) {
+        const float v = e < n ? to_f32(T(c[k].v[e])) - mean : 0.f;
+        q = fmaf(v, v, q);
+      }
+      var += q;
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(team_sum<TEAM>(var, red[1]), inv, p.eps));
+    T* out = static_cast<T*>(p.out) + (live ? row : 0) * D;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t d = int64_t(k * TEAM + t) * kChunk;
+      const int64_t n = live ? D - d : 0;
+      float w[kChunk], b[kChunk];
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) {
+        w[e] = 1.0f;
+        b[e] = 0.0f;
+      }
+      if (p.weight != nullptr) load_params<T>(p.weight, p.wide, d, n, w);
+      if (p.bias != nullptr) load_params<T>(p.bias, p.wide, d, n, b);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e)
+        c[k].v[e] = T(fmaf((to_f32(T(c[k].v[e])) - mean) * rstd, w[e], b[e]));
+      c[k].store(out + d, n);
+    }
+    if (t == 0 && live) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+  }
+}
+
+// d_x, and the slab's partial d_w and d_b.  Every thread owns the same columns in every
+// row of its slab, so the parameter sums stay in its registers and the rows are read
+// once.  The weight waits in LDS as fp32, in two planes (the chunks' first and second
+// four elements) so that a wave's 16-byte reads are contiguous.
+template <class T, int TEAM, int NCH>
+__global__ __launch_bounds__(kTeamThreads) void k_norm_bwd_row(NormBwdArgs p) {
+  constexpr int kTeams = kTeamThreads / TEAM;
+  extern __shared__ f32x4 lds[];
+  __shared__ float red[2][2][8];
+  const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+  const int64_t D = p.D;
+  const int plane = int((D + kChunk - 1) / kChunk);
+  const float inv = 1.0f / float(D);
+  const int64_t r1 = min(p.N, (int64_t(blockIdx.x) + 1) * p.slab_rows);
+  for (int c = threadIdx.x; c < plane; c += kTeamThreads) {
+    float w[kChunk];
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) w[e] = 1.0f;
+    if (p.weight != nullptr) load_params<T>(p.weight, p.wide, c * kChunk, D - c * kChunk, w);
+    lds[c] = f32x4{w[0], w[1], w[2], w[3]};
+    lds[plane + c] = f32x4{w[4], w[5], w[6], w[7]};
+  }
+  __syncthreads();
+  float aw[NCH][kChunk], ab[NCH][kChunk];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k)
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) aw[k][e] = ab[k][e] = 0.f;
+  int turn = 0;
+  for (int64_t r0 = int64_t(blockIdx.x) * p.slab_rows; r0 < r1; r0 += kTeams, turn ^= 1) {
+    const int64_t row = r0 + team;
+    const bool live = row < r1;
+    const int64_t at = (live ? row : r0) * D;
+    const T* x = static_cast<const T*>(p.x) + at;
+    const T* g = static_cast<const T*>(p.grad) + at;
+    Chunk<T> cx[NCH], cg[NCH];
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t d = int64_t(k * TEAM + t) * kChunk;
+      cx[k].load(x + d, live ? D - d : 0);
+      cg[k].load(g + d, live ? D - d : 0);
+    }
+    const float mean = p.mean[live ? row : r0], rstd = p.rstd[live ? row : r0];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int c = k * TEAM + t;
+      if (c >= plane) continue;  // past the row: zeros, and no weight
+      const f32x4 w0 = lds[c], w1 = lds[plane + c];
+      float q1 = 0.f, q2 = 0.f;
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) {
+        const float gr = to_f32(T(cg[k].v[e]));
+        const float xhat = (to_f32(T(cx[k].v[e])) - mean) * rstd;
+        const float gw = gr * (e < 4 ? w0[e & 3] : w1[e & 3]);
+        q1 += gw;
+        q2 = fmaf(gw, xhat, q2);
+        aw[k][e] = fmaf(gr, xhat, aw[k][e]);
+        ab[k][e] += gr;
+      }
+      s1 += q1;
+      s2 += q2;
+    }
+    if (p.d_x == nullptr) continue;  // uniform over the launch
+    const float m1 = team_sum<TEAM>(s1, red[turn][0]) * inv;
+    const float m2 = team_sum<TEAM>(s2, red[turn][1]) * inv;
+    T* dx = static_cast<T*>(p.d_x) + at;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int c = k * TEAM + t;
+      if (c >= plane) continue;
+      const f32x4 w0 = lds[c], w1 = lds[plane + c];
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) {
+        const float xhat = (to_f32(T(cx[k].v[e])) - mean) * rstd;
+        const float gw = to_f32(T(cg[k].v[e])) * (e < 4 ? w0[e & 3] : w1[e & 3]);
+        cx[k].v[e] = T(rstd * (gw - m1 - xhat * m2));
+      }
+      cx[k].store(dx + int64_t(c) * kChunk, live ? D - int64_t(c) * kChunk : 0);
+    }
+  }
+  if (p.part == nullptr) return;
+  // The teams add their sums in order, first those of d_w, then those of d_b.
+  float* out = p.part + int64_t(blockIdx.x) * 2 * D;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    for (int j = 0; j < kTeams; ++j) {
+      __syncthreads();
+      if (team != j) continue;
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) {
+        const int c = k * TEAM + t;
+        if (c >= plane) continue;
+        const float(&a)[kChunk] = which == 0 ? aw[k] : ab[k];
+        f32x4 v0 = {a[0], a[1], a[2], a[3]}, v1 = {a[4], a[5], a[6], a[7]};
+        if (j > 0) {
+          v0 += lds[c];
+          v1 += lds[plane + c];
+        }
+        if (j + 1 < kTeams) {
+          lds[c] = v0;
+          lds[plane + c] = v1;
+        } else {
+          Chunk<float> o;
+#pragma unroll
+          for (int e = 0; e < kChunk; ++e) o.v[e] = e < 4 ? v0[e & 3] : v1[e & 3];
+          o.store(out + which * D + int64_t(c) * kChunk, D - int64_t(c) * kChunk);
+        }
+      }
+    }
+  }
+}
+
+// ---- wider rows ----------------------------------------------------------------------------------
 
 constexpr int kRowThreads = 256;
 
@@ -41,8 +323,8 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// One workgroup per row, any D: the row is read three times (mean, variance,
-// output); only the first read reaches HBM.
+// One workgroup per row: the row is read three times (mean, variance, output); only the
+// first read reaches HBM.
 template <class T, class W>
 __global__ __launch_bounds__(kRowThreads) void k_norm_fwd(NormFwdArgs p) {
   __shared__ float red[4];
@@ -150,22 +432,69 @@ __global__ __launch_bounds__(256) void k_norm_fold(NormBwdArgs p) {
 // threads).
 unsigned row_grid(int64_t N) { return unsigned(std::min<int64_t>(N, 1 << 20)); }
 
+// Rows of up to 4096 elements belong to one wave, which needs no barrier; up to 16384 to
+// four waves (a wave's registers hold no more); wider ones take the looping kernels.
+constexpr int64_t kWaveMax = 64 * kChunk * 8, kTeamMax = 256 * kChunk * 8;
+
+// f(TEAM, NCH) for the smallest instance that holds a row.
+template <class F>
+void by_width(int64_t D, F f) {
+  const int64_t chunks = (D + kChunk - 1) / kChunk;
+  using std::integral_constant;
+  if (D <= kWaveMax) {
+    const int64_t k = (chunks + 63) / 64;
+    constexpr integral_constant<int, 64> w{};
+    if (k <= 1) return f(w, integral_constant<int, 1>{});
+    if (k <= 2) return f(w, integral_constant<int, 2>{});
+    if (k <= 4) return f(w, integral_constant<int, 4>{});
+    if (k <= 6) return f(w, integral_constant<int, 6>{});
+    return f(w, integral_constant<int, 8>{});
+  }
+  const int64_t k = (chunks + 255) / 256;
+  constexpr integral_constant<int, 256> w{};
+  if (k <= 4) return f(w, integral_constant<int, 4>{});
+  if (k <= 6) return f(w, integral_constant<int, 6>{});
+  return f(w, integral_constant<int, 8>{});
+}
+
 template <class T, class W>
 hipError_t norm_fwd(const NormFwdArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm_fwd<T, W>), dim3(row_grid(a.N)), dim3(kRowThreads), 0, s, a);
+  if (a.D > kTeamMax) {
+    hipLaunchKernelGGL((k_norm_fwd<T, W>), dim3(row_grid(a.N)), dim3(kRowThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  by_width(a.D, [&](auto team, auto nch) {
+    constexpr int kTeam = decltype(team)::value, kNch = decltype(nch)::value;
+    hipLaunchKernelGGL((k_norm_fwd_row<T, kTeam, kNch>),
+                       dim3(row_grid((a.N + 256 / kTeam - 1) / (256 / kTeam))), dim3(256), 0, s, a);
+  });
   return hipGetLastError();
 }
 
 template <class T, class W>
 hipError_t norm_bwd(const NormBwdArgs& a, hipStream_t s) {
-  if (a.d_x != nullptr)
-    hipLaunchKernelGGL((k_norm_dx<T, W>), dim3(row_grid(a.N)), dim3(kRowThreads), 0, s, a);
-  if (a.d_weight != nullptr || a.d_bias != nullptr) {
-    if (a.slabs > 0)
+  const bool params = a.d_weight != nullptr || a.d_bias != nullptr;
+  if (a.D > kTeamMax) {
+    if (a.d_x != nullptr)
+      hipLaunchKernelGGL((k_norm_dx<T, W>), dim3(row_grid(a.N)), dim3(kRowThreads), 0, s, a);
+    if (params && a.slabs > 0)
       hipLaunchKernelGGL(k_norm_params<T>, dim3(unsigned((a.D + 63) / 64), unsigned(a.slabs)),
                          dim3(256), 0, s, a);
-    hipLaunchKernelGGL(k_norm_fold<W>, dim3(unsigned((a.D + 31) / 32), 2), dim3(256), 0, s, a);
+  } else if (a.slabs > 0) {
+    hipError_t e = hipSuccess;
+    by_width(a.D, [&](auto team, auto nch) {
+      constexpr int kTeam = decltype(team)::value, kNch = decltype(nch)::value;
+      static std::atomic<int> ready[kMaxDevices];
+      e = prepare(k_norm_bwd_row<T, kTeam, kNch>, kTeam * kNch * kChunk * 4, ready);
+      if (e != hipSuccess) return;
+      const size_t lds = size_t((a.D + kChunk - 1) / kChunk) * kChunk * 4;
+      hipLaunchKernelGGL((k_norm_bwd_row<T, kTeam, kNch>), dim3(unsigned(a.slabs)),
+                         dim3(kTeamThreads), lds, s, a);
+    });
+    if (e != hipSuccess) return e;
   }
+  if (params)
+    hipLaunchKernelGGL(k_norm_fold<W>, dim3(unsigned((a.D + 31) / 32), 2), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -182,13 +511,18 @@ hipError_t by_types(flp_dtype x, flp_dtype w, F f) {
 hipError_t launch_layer_norm_forward(flp_dtype x, flp_dtype w, const NormFwdArgs& a,
                                      hipStream_t s) {
   ProfScope ps(FLP_K_LAYER_NORM, s);
-  return by_types(x, w, [&](auto t, auto u) { return norm_fwd<decltype(t), decltype(u)>(a, s); });
+  NormFwdArgs b = a;
+  b.wide = w == FLP_F32;
+  return by_types(x, w, [&](auto t, auto u) { return norm_fwd<decltype(t), decltype(u)>(b, s); });
 }
 
 hipError_t launch_layer_norm_backward(flp_dtype x, flp_dtype w, const NormBwdArgs& a,
                                       hipStream_t s) {
   ProfScope ps(FLP_K_LAYER_NORM, s);
-  return by_types(x, w, [&](auto t, auto u) { return norm_bwd<decltype(t), decltype(u)>(a, s); });
+  NormBwdArgs b = a;
+  b.wide = w == FLP_F32;
+  if (a.d_weight == nullptr && a.d_bias == nullptr) b.part = nullptr;
+  return by_types(x, w, [&](auto t, auto u) { return norm_bwd<decltype(t), decltype(u)>(b, s); });
 }
 
 }  // namespace flp
