@@ -35,7 +35,7 @@ __device__ __forceinline__ float to_f32(T v) {
   return float(v);
 }
 
-// ---- rows held in registers (D up to kTeamMax) ------------------------------------------------
+// ---- rows held in registers (up to kTeamMax elements) ------------------------------------------------
 //
 // A team of TEAM threads (one wave, or four) owns a row; thread t holds the chunks of
 // eight elements t, t + TEAM, ... (at most NCH).  A row is read from memory once, with
@@ -129,76 +129,125 @@ __device__ __forceinline__ float team_sum(float x, float* red) {
 }
 
 constexpr int kTeamThreads = 512;
+// Workgroups of a forward launch: two per compute unit (256 and 1024 measured the same).
+constexpr int64_t kFwdGroups = 512;
 
+// A row's chunks of one thread.
 template <class T, int TEAM, int NCH>
-__global__ __launch_bounds__(256) void k_norm_fwd_row(NormFwdArgs p) {
-  constexpr int kTeams = 256 / TEAM;
-  __shared__ float red[2][4];
-  const int t = threadIdx.x % TEAM;
-  const int64_t D = p.D;
-  const float inv = 1.0f / float(D);
-  // Every team of the workgroup takes part in every step (they share barriers).
-  for (int64_t r0 = int64_t(blockIdx.x) * kTeams; r0 < p.N; r0 += int64_t(gridDim.x) * kTeams) {
-    const int64_t row = r0 + threadIdx.x / TEAM;
-    const bool live = row < p.N;
-    const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * D;
-    Chunk<T> c[NCH];
+struct Row {
+  Chunk<T> c[NCH];
+  __device__ __forceinline__ void load(const T* row, int64_t D, int t, bool live) {
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t d = int64_t(k * TEAM + t) * kChunk;
-      c[k].load(x + d, live ? D - d : 0);
+      c[k].load(row + d, live ? D - d : 0);
     }
+  }
+};
+
+// A [D] parameter in LDS as fp32, in two planes (the chunks' first and second four
+// elements) so that a wave's 16-byte reads are contiguous; `value` where it is absent.
+template <class T>
+__device__ __forceinline__ void stage_param(f32x4* lds, const void* base, bool wide, int64_t D,
+                                            float value) {
+  const int plane = int((D + kChunk - 1) / kChunk);
+  for (int c = threadIdx.x; c < plane; c += kTeamThreads) {
+    float w[kChunk];
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) w[e] = value;
+    if (base != nullptr) load_params<T>(base, wide, int64_t(c) * kChunk, D - int64_t(c) * kChunk, w);
+    lds[c] = f32x4{w[0], w[1], w[2], w[3]};
+    lds[plane + c] = f32x4{w[4], w[5], w[6], w[7]};
+  }
+}
+
+// The workgroups stay and take rows in turn: the parameters are staged in LDS once, and
+// the next row is in flight while the current one is worked on.  16384 x 2688 bf16 on
+// MI355X: 38 us for 176 MB (4.6 TB/s; one row per wave and launch took 46, with the
+// parameters read from the caches).
+template <class T, int TEAM, int NCH>
+__global__ __launch_bounds__(kTeamThreads) void k_norm_fwd_row(NormFwdArgs p) {
+  constexpr int kTeams = kTeamThreads / TEAM;
+  extern __shared__ f32x4 lds[];
+  __shared__ float red[2][2][8];
+  const int t = threadIdx.x % TEAM;
+  const int64_t D = p.D, step = int64_t(gridDim.x) * kTeams;
+  const int plane = int((D + kChunk - 1) / kChunk);
+  const float inv = 1.0f / float(D);
+  const T* x = static_cast<const T*>(p.x);
+  int64_t row = int64_t(blockIdx.x) * kTeams + threadIdx.x / TEAM;
+  int turn = 0;
+  auto work = [&](Row<T, TEAM, NCH>& cur, Row<T, TEAM, NCH>& nxt) {
+    const bool live = row < p.N;
+    nxt.load(x + (row + step) * D, D, t, row + step < p.N);
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       float q = 0.f;
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) q += to_f32(T(c[k].v[e]));
+      for (int e = 0; e < kChunk; ++e) q += to_f32(T(cur.c[k].v[e]));
       s += q;
     }
-    const float mean = team_sum<TEAM>(s, red[0]) * inv;
+    const float mean = team_sum<TEAM>(s, red[turn][0]) * inv;
     float var = 0.f;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int64_t n = D - int64_t(k * TEAM + t) * kChunk;
       float q = 0.f;
+      if (n >= kChunk) {
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) {
-        const float v = e < n ? to_f32(T(c[k].v[e])) - mean : 0.f;
-        q = fmaf(v, v, q);
+        for (int e = 0; e < kChunk; ++e) {
+          const float v = to_f32(T(cur.c[k].v[e])) - mean;
+          q = fmaf(v, v, q);
+        }
+      } else if (n > 0) {
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) {
+          const float v = e < n ? to_f32(T(cur.c[k].v[e])) - mean : 0.f;
+          q = fmaf(v, v, q);
+        }
       }
       var += q;
     }
-    const float rstd = 1.0f / sqrtf(fmaf(team_sum<TEAM>(var, red[1]), inv, p.eps));
-    T* out = static_cast<T*>(p.out) + (live ? row : 0) * D;
+    const float rstd = 1.0f / sqrtf(fmaf(team_sum<TEAM>(var, red[turn][1]), inv, p.eps));
+    T* out = static_cast<T*>(p.out) + row * D;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      const int64_t d = int64_t(k * TEAM + t) * kChunk;
-      const int64_t n = live ? D - d : 0;
-      float w[kChunk], b[kChunk];
-#pragma unroll
-      for (int e = 0; e < kChunk; ++e) {
-        w[e] = 1.0f;
-        b[e] = 0.0f;
-      }
-      if (p.weight != nullptr) load_params<T>(p.weight, p.wide, d, n, w);
-      if (p.bias != nullptr) load_params<T>(p.bias, p.wide, d, n, b);
+      const int c = k * TEAM + t;
+      __builtin_amdgcn_sched_barrier(0);  // one chunk's parameters at a time in registers
+      if (c >= plane) continue;
+      const f32x4 w0 = lds[c], w1 = lds[plane + c];
+      const f32x4 b0 = lds[2 * plane + c], b1 = lds[3 * plane + c];
 #pragma unroll
       for (int e = 0; e < kChunk; ++e)
-        c[k].v[e] = T(fmaf((to_f32(T(c[k].v[e])) - mean) * rstd, w[e], b[e]));
-      c[k].store(out + d, n);
+        cur.c[k].v[e] = T(fmaf((to_f32(T(cur.c[k].v[e])) - mean) * rstd,
+                               e < 4 ? w0[e & 3] : w1[e & 3], e < 4 ? b0[e & 3] : b1[e & 3]));
+      cur.c[k].store(out + int64_t(c) * kChunk, live ? D - int64_t(c) * kChunk : 0);
     }
     if (t == 0 && live) {
       if (p.mean != nullptr) p.mean[row] = mean;
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
+    row += step;
+    turn ^= 1;
+  };
+  Row<T, TEAM, NCH> a, b;
+  a.load(x + row * D, D, t, row < p.N);
+  stage_param<T>(lds, p.weight, p.wide, D, 1.0f);
+  stage_param<T>(lds + 2 * plane, p.bias, p.wide, D, 0.0f);
+  __syncthreads();
+  // Every team of the workgroup makes every step (they share barriers): r0 is its first.
+  for (int64_t r0 = int64_t(blockIdx.x) * kTeams; r0 < p.N; r0 += 2 * step) {
+    work(a, b);
+    if (r0 + step < p.N) work(b, a);
   }
 }
 
 // d_x, and the slab's partial d_w and d_b.  Every thread owns the same columns in every
 // row of its slab, so the parameter sums stay in its registers and the rows are read
-// once.  The weight waits in LDS as fp32, in two planes (the chunks' first and second
-// four elements) so that a wave's 16-byte reads are contiguous.
+// once.  16384 x 2688 bf16 on MI355X: 61 us for 264 MB (4.3 TB/s; a large copy reaches
+// 4.9).  Loading the next row ahead as the forward does spills and takes 72 us; teams in
+// workgroups of 256 threads take 70.
 template <class T, int TEAM, int NCH>
 __global__ __launch_bounds__(kTeamThreads) void k_norm_bwd_row(NormBwdArgs p) {
   constexpr int kTeams = kTeamThreads / TEAM;
@@ -209,72 +258,75 @@ __global__ __launch_bounds__(kTeamThreads) void k_norm_bwd_row(NormBwdArgs p) {
   const int plane = int((D + kChunk - 1) / kChunk);
   const float inv = 1.0f / float(D);
   const int64_t r1 = min(p.N, (int64_t(blockIdx.x) + 1) * p.slab_rows);
-  for (int c = threadIdx.x; c < plane; c += kTeamThreads) {
-    float w[kChunk];
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) w[e] = 1.0f;
-    if (p.weight != nullptr) load_params<T>(p.weight, p.wide, c * kChunk, D - c * kChunk, w);
-    lds[c] = f32x4{w[0], w[1], w[2], w[3]};
-    lds[plane + c] = f32x4{w[4], w[5], w[6], w[7]};
-  }
-  __syncthreads();
+  const T* x = static_cast<const T*>(p.x);
+  const T* g = static_cast<const T*>(p.grad);
+  int64_t row = int64_t(blockIdx.x) * p.slab_rows + team;
   float aw[NCH][kChunk], ab[NCH][kChunk];
 #pragma unroll
   for (int k = 0; k < NCH; ++k)
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) aw[k][e] = ab[k][e] = 0.f;
   int turn = 0;
-  for (int64_t r0 = int64_t(blockIdx.x) * p.slab_rows; r0 < r1; r0 += kTeams, turn ^= 1) {
-    const int64_t row = r0 + team;
+  Row<T, TEAM, NCH> cx, cg;
+  float mean, rstd;
+  auto load = [&] {
     const bool live = row < r1;
-    const int64_t at = (live ? row : r0) * D;
-    const T* x = static_cast<const T*>(p.x) + at;
-    const T* g = static_cast<const T*>(p.grad) + at;
-    Chunk<T> cx[NCH], cg[NCH];
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int64_t d = int64_t(k * TEAM + t) * kChunk;
-      cx[k].load(x + d, live ? D - d : 0);
-      cg[k].load(g + d, live ? D - d : 0);
-    }
-    const float mean = p.mean[live ? row : r0], rstd = p.rstd[live ? row : r0];
+    cx.load(x + row * D, D, t, live);
+    cg.load(g + row * D, D, t, live);
+    mean = live ? p.mean[row] : 0.f;
+    rstd = live ? p.rstd[row] : 0.f;
+  };
+  load();
+  stage_param<T>(lds, p.weight, p.wide, D, 1.0f);
+  __syncthreads();
+  for (int64_t r0 = int64_t(blockIdx.x) * p.slab_rows; r0 < r1; r0 += kTeams) {
+    const bool live = row < r1;
+    // sums over gw and gw (x - mean): the second takes its rstd afterwards
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int c = k * TEAM + t;
+      __builtin_amdgcn_sched_barrier(0);
       if (c >= plane) continue;  // past the row: zeros, and no weight
       const f32x4 w0 = lds[c], w1 = lds[plane + c];
       float q1 = 0.f, q2 = 0.f;
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
-        const float gr = to_f32(T(cg[k].v[e]));
-        const float xhat = (to_f32(T(cx[k].v[e])) - mean) * rstd;
+        const float gr = to_f32(T(cg.c[k].v[e]));
+        const float xc = to_f32(T(cx.c[k].v[e])) - mean;
         const float gw = gr * (e < 4 ? w0[e & 3] : w1[e & 3]);
         q1 += gw;
-        q2 = fmaf(gw, xhat, q2);
-        aw[k][e] = fmaf(gr, xhat, aw[k][e]);
+        q2 = fmaf(gw, xc, q2);
+        aw[k][e] = fmaf(gr * rstd, xc, aw[k][e]);
         ab[k][e] += gr;
       }
       s1 += q1;
       s2 += q2;
     }
-    if (p.d_x == nullptr) continue;  // uniform over the launch
-    const float m1 = team_sum<TEAM>(s1, red[turn][0]) * inv;
-    const float m2 = team_sum<TEAM>(s2, red[turn][1]) * inv;
-    T* dx = static_cast<T*>(p.d_x) + at;
+    if (p.d_x != nullptr) {  // uniform over the launch
+      const float m1 = team_sum<TEAM>(s1, red[turn][0]) * inv;
+      const float m2 = team_sum<TEAM>(s2, red[turn][1]) * inv * rstd;
+      // d_x = rstd gw - rstd m1 - (x - mean) rstd^2 m2
+      const float a0 = -(rstd * m1), a1 = -(rstd * rstd * m2);
+      T* dx = static_cast<T*>(p.d_x) + row * D;
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int c = k * TEAM + t;
-      if (c >= plane) continue;
-      const f32x4 w0 = lds[c], w1 = lds[plane + c];
+      for (int k = 0; k < NCH; ++k) {
+        const int c = k * TEAM + t;
+        __builtin_amdgcn_sched_barrier(0);
+        if (c >= plane) continue;
+        const f32x4 w0 = lds[c], w1 = lds[plane + c];
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) {
-        const float xhat = (to_f32(T(cx[k].v[e])) - mean) * rstd;
-        const float gw = to_f32(T(cg[k].v[e])) * (e < 4 ? w0[e & 3] : w1[e & 3]);
-        cx[k].v[e] = T(rstd * (gw - m1 - xhat * m2));
+        for (int e = 0; e < kChunk; ++e) {
+          const float xc = to_f32(T(cx.c[k].v[e])) - mean;
+          const float gw = to_f32(T(cg.c[k].v[e])) * (e < 4 ? w0[e & 3] : w1[e & 3]);
+          cx.c[k].v[e] = T(fmaf(gw, rstd, fmaf(xc, a1, a0)));
+        }
+        cx.c[k].store(dx + int64_t(c) * kChunk, live ? D - int64_t(c) * kChunk : 0);
       }
-      cx[k].store(dx + int64_t(c) * kChunk, live ? D - int64_t(c) * kChunk : 0);
     }
+    row += kTeams;
+    turn ^= 1;
+    load();
   }
   if (p.part == nullptr) return;
   // The teams add their sums in order, first those of d_w, then those of d_b.
@@ -408,73 +460,95 @@ __global__ __launch_bounds__(256) void k_norm_params(NormBwdArgs p) {
   }
 }
 
-// d_w (blockIdx.y = 0) and d_b (1) from the slab partials: 32 columns per
-// workgroup, eight threads per column each adding every eighth slab in ascending
-// order, then the eight in order.
+// d_w (blockIdx.y = 0) and d_b (1) from the slab partials: 16 columns per workgroup,
+// sixteen threads per column each adding every sixteenth slab in ascending order (eight
+// loads in flight), then the sixteen by a fixed tree.
 template <class W>
 __global__ __launch_bounds__(256) void k_norm_fold(NormBwdArgs p) {
-  __shared__ float s[8][32];
+  __shared__ float s[16][17];
   W* out = static_cast<W*>(blockIdx.y == 0 ? p.d_weight : p.d_bias);
   if (out == nullptr) return;
-  const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
-  const int64_t d = int64_t(blockIdx.x) * 32 + c;
+  const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int64_t d = int64_t(blockIdx.x) * 16 + c;
   float a = 0.f;
-  if (d < p.D)
-    for (int64_t k = q; k < p.slabs; k += 8) a += p.part[(k * 2 + blockIdx.y) * p.D + d];
+  if (d < p.D) {
+    const float* src = p.part + int64_t(blockIdx.y) * p.D + d;
+    for (int64_t k = q; k < p.slabs; k += 128) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = k + 16 * u < p.slabs ? src[(k + 16 * u) * 2 * p.D] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) a += v[u];
+    }
+  }
   s[q][c] = a;
-  __syncthreads();
-  if (q == 0 && d < p.D)
-    out[d] = W(((s[0][c] + s[1][c]) + (s[2][c] + s[3][c])) +
-               ((s[4][c] + s[5][c]) + (s[6][c] + s[7][c])));
+#pragma unroll
+  for (int h = 8; h >= 1; h >>= 1) {
+    __syncthreads();
+    if (q < h) s[q][c] += s[q + h][c];
+  }
+  if (q == 0 && d < p.D) out[d] = W(s[0][c]);
 }
 
 // Rows beyond this many workgroups are taken in turn (a launch holds fewer than 2^32
 // threads).
 unsigned row_grid(int64_t N) { return unsigned(std::min<int64_t>(N, 1 << 20)); }
 
-// Rows of up to 4096 elements belong to one wave, which needs no barrier; up to 16384 to
-// four waves (a wave's registers hold no more); wider ones take the looping kernels.
-constexpr int64_t kWaveMax = 64 * kChunk * 8, kTeamMax = 256 * kChunk * 8;
+// A thread holds up to 8 chunks of a 16-bit row or 6 of an fp32 one (a seventh spills in
+// the backward).  Rows that fit one wave that way belong to one wave, which needs no
+// barrier; wider ones to four; beyond that the looping kernels take them.
+template <class T>
+constexpr int kMaxChunks = sizeof(T) == 2 ? 8 : 6;
+template <class T>
+constexpr int64_t kTeamMax = int64_t(256) * kMaxChunks<T> * kChunk;
 
 // f(TEAM, NCH) for the smallest instance that holds a row.
-template <class F>
+template <class T, class F>
 void by_width(int64_t D, F f) {
-  const int64_t chunks = (D + kChunk - 1) / kChunk;
   using std::integral_constant;
-  if (D <= kWaveMax) {
+  const int64_t chunks = (D + kChunk - 1) / kChunk;
+  if (chunks <= 64 * kMaxChunks<T>) {
     const int64_t k = (chunks + 63) / 64;
     constexpr integral_constant<int, 64> w{};
     if (k <= 1) return f(w, integral_constant<int, 1>{});
     if (k <= 2) return f(w, integral_constant<int, 2>{});
     if (k <= 4) return f(w, integral_constant<int, 4>{});
     if (k <= 6) return f(w, integral_constant<int, 6>{});
-    return f(w, integral_constant<int, 8>{});
+    if constexpr (kMaxChunks<T> > 6) return f(w, integral_constant<int, 8>{});
   }
   const int64_t k = (chunks + 255) / 256;
   constexpr integral_constant<int, 256> w{};
+  if (sizeof(T) == 4 && k <= 2) return f(w, integral_constant<int, sizeof(T) == 4 ? 2 : 4>{});
   if (k <= 4) return f(w, integral_constant<int, 4>{});
   if (k <= 6) return f(w, integral_constant<int, 6>{});
-  return f(w, integral_constant<int, 8>{});
+  if constexpr (kMaxChunks<T> > 6) return f(w, integral_constant<int, 8>{});
 }
 
 template <class T, class W>
 hipError_t norm_fwd(const NormFwdArgs& a, hipStream_t s) {
-  if (a.D > kTeamMax) {
+  if (a.D > kTeamMax<T>) {
     hipLaunchKernelGGL((k_norm_fwd<T, W>), dim3(row_grid(a.N)), dim3(kRowThreads), 0, s, a);
     return hipGetLastError();
   }
-  by_width(a.D, [&](auto team, auto nch) {
+  hipError_t e = hipSuccess;
+  by_width<T>(a.D, [&](auto team, auto nch) {
     constexpr int kTeam = decltype(team)::value, kNch = decltype(nch)::value;
-    hipLaunchKernelGGL((k_norm_fwd_row<T, kTeam, kNch>),
-                       dim3(row_grid((a.N + 256 / kTeam - 1) / (256 / kTeam))), dim3(256), 0, s, a);
+    constexpr int64_t kTeams = kTeamThreads / kTeam;
+    static std::atomic<int> ready[kMaxDevices];
+    e = prepare(k_norm_fwd_row<T, kTeam, kNch>, 2 * kTeam * kNch * kChunk * 4, ready);
+    if (e != hipSuccess) return;
+    const int64_t grid = std::min<int64_t>((a.N + kTeams - 1) / kTeams, kFwdGroups);
+    const size_t lds = size_t((a.D + kChunk - 1) / kChunk) * kChunk * 2 * 4;
+    hipLaunchKernelGGL((k_norm_fwd_row<T, kTeam, kNch>), dim3(unsigned(grid)), dim3(kTeamThreads),
+                       lds, s, a);
   });
-  return hipGetLastError();
+  return e != hipSuccess ? e : hipGetLastError();
 }
 
 template <class T, class W>
 hipError_t norm_bwd(const NormBwdArgs& a, hipStream_t s) {
   const bool params = a.d_weight != nullptr || a.d_bias != nullptr;
-  if (a.D > kTeamMax) {
+  if (a.D > kTeamMax<T>) {
     if (a.d_x != nullptr)
       hipLaunchKernelGGL((k_norm_dx<T, W>), dim3(row_grid(a.N)), dim3(kRowThreads), 0, s, a);
     if (params && a.slabs > 0)
@@ -482,7 +556,7 @@ hipError_t norm_bwd(const NormBwdArgs& a, hipStream_t s) {
                          dim3(256), 0, s, a);
   } else if (a.slabs > 0) {
     hipError_t e = hipSuccess;
-    by_width(a.D, [&](auto team, auto nch) {
+    by_width<T>(a.D, [&](auto team, auto nch) {
       constexpr int kTeam = decltype(team)::value, kNch = decltype(nch)::value;
       static std::atomic<int> ready[kMaxDevices];
       e = prepare(k_norm_bwd_row<T, kTeam, kNch>, kTeam * kNch * kChunk * 4, ready);
@@ -494,7 +568,7 @@ hipError_t norm_bwd(const NormBwdArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (params)
-    hipLaunchKernelGGL(k_norm_fold<W>, dim3(unsigned((a.D + 31) / 32), 2), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_norm_fold<W>, dim3(unsigned((a.D + 15) / 16), 2), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

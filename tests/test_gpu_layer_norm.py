@@ -94,7 +94,7 @@ def compare(x, w, b, go, eps=1e-5):
     return y, mean, rstd, dx, dw, db
 
 
-WIDTHS = [1, 2, 7, 8, 64, 129, 520, 1000, 1345, 2688, 4096, 4097, 8200, 16384, 16385, 40001]
+WIDTHS = [1, 2, 7, 8, 64, 129, 520, 1000, 1345, 2688, 4096, 4097, 8200, 12288, 12289, 16384, 16385, 40001]
 
 
 @pytest.mark.parametrize("D", WIDTHS)
