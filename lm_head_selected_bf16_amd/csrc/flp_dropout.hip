@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "flp_chunk.h"
 #include "flp_launch.h"
 
 namespace flp {
@@ -43,22 +44,26 @@ __device__ __forceinline__ Words random_words(uint64_t block, uint64_t seed, uin
   return Words{{c0, c1, c2, c3}};
 }
 
-// Eight elements per thread and step; a launch holds fewer than 2^32 threads, so very
-// long inputs take several steps.
+// A chunk of eight elements per thread (two, four and eight at once measured slower).  A
+// launch holds fewer than 2^32 threads, so very long inputs take several steps.  Bound by
+// memory: 16384 x 2688 bf16 on MI355X take 32 us for 176 MB (5.5 TB/s; element by element
+// it took 82).
 template <class T>
 __global__ __launch_bounds__(256) void k_dropout(int64_t n, const T* __restrict__ x,
                                                  const uint64_t* __restrict__ rng, uint32_t drop,
                                                  float scale, T* __restrict__ out) {
   const uint64_t seed = rng[0], offset = rng[1];
   const int64_t step = int64_t(gridDim.x) * 256;
-  for (int64_t b = int64_t(blockIdx.x) * 256 + threadIdx.x; b * 8 < n; b += step) {
+  for (int64_t b = int64_t(blockIdx.x) * 256 + threadIdx.x; b * kChunk < n; b += step) {
+    Chunk<T> c;
+    c.load(x + b * kChunk, n - b * kChunk);
     const Words r = random_words(uint64_t(b), seed, offset);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int64_t e = b * 8 + k;
-      const uint32_t u = (k & 1) ? r.w[k >> 1] >> 16 : r.w[k >> 1] & 0xFFFFu;
-      if (e < n) out[e] = u >= drop ? T(float(x[e]) * scale) : T(0.0f);
+    for (int k = 0; k < kChunk; ++k) {
+      const uint32_t bits = (k & 1) ? r.w[k >> 1] >> 16 : r.w[k >> 1] & 0xFFFFu;
+      c.v[k] = bits >= drop ? T(float(T(c.v[k])) * scale) : T(0.0f);
     }
+    c.store(out + b * kChunk, n - b * kChunk);
   }
 }
 

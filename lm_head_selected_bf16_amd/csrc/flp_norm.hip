@@ -22,12 +22,12 @@
 #include <atomic>
 #include <type_traits>
 
+#include "flp_chunk.h"
 #include "flp_launch.h"
 
 namespace flp {
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 template <class T>
@@ -39,48 +39,7 @@ __device__ __forceinline__ float to_f32(T v) {
 //
 // A team of TEAM threads (one wave, or four) owns a row; thread t holds the chunks of
 // eight elements t, t + TEAM, ... (at most NCH).  A row is read from memory once, with
-// 16-byte loads that all stay in flight, and both its sums run over the registers.  Rows
-// need no alignment: the loads and stores are of the element's alignment, which the
-// memory path takes at full width; only a row's last, partial chunk goes element by
-// element.
-constexpr int kChunk = 8;
-
-typedef u32x4 loose __attribute__((aligned(2)));
-
-template <class T>
-struct Chunk {
-  static constexpr int kWords = kChunk * int(sizeof(T)) / 16;
-  typedef T vec __attribute__((ext_vector_type(kChunk)));
-  union {
-    u32x4 w[kWords];
-    vec v;
-  };
-
-  // n valid elements of the chunk at p (zeros past them); n <= 0 loads nothing.
-  __device__ __forceinline__ void load(const T* p, int64_t n) {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) w[k] = u32x4{0u, 0u, 0u, 0u};
-    if (n >= kChunk) {
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) w[k] = reinterpret_cast<const loose*>(p)[k];
-    } else if (n > 0) {
-#pragma unroll
-      for (int k = 0; k < kChunk; ++k)
-        if (k < n) v[k] = p[k];
-    }
-  }
-  __device__ __forceinline__ void store(T* p, int64_t n) const {
-    if (n >= kChunk) {
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) reinterpret_cast<loose*>(p)[k] = w[k];
-    } else if (n > 0) {
-#pragma unroll
-      for (int k = 0; k < kChunk; ++k)
-        if (k < n) p[k] = v[k];
-    }
-  }
-};
-
+// 16-byte loads that all stay in flight, and both its sums run over the registers.
 // Eight parameters as fp32 (`wide`: they are stored as fp32, else in T).
 template <class T>
 __device__ __forceinline__ void load_params(const void* base, bool wide, int64_t d, int64_t n,
