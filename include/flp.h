@@ -465,6 +465,10 @@ flp_status flp_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype 
  * For FLP_F16, dz is held times a power of two that brings its largest row factor to
  * 2^10, taken back when the fp32 sums are rounded: small gradients (a mean over many
  * rows) do not underflow on the way.
+ *
+ * Batches of up to 1024 rows sum d_hidden over slabs of the vocabulary, larger ones in
+ * one walk: a row's d_hidden is bitwise the same among batches of one kind, and differs
+ * between the two by the order of that fp32 sum.
  */
 size_t flp_cross_entropy_backward_workspace_bytes(int64_t N, int64_t D, int64_t V,
                                                   flp_dtype x_dtype, int64_t chunk_rows);

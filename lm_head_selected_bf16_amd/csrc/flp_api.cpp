@@ -127,6 +127,10 @@ flp_status enqueue_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
       g.load_acc = 0;
       g.store_acc = 0;
       g.scale = scale;
+      if (loss != nullptr && loss->k_slab > 0) {
+        g.k_slab = loss->k_slab;
+        g.acc = loss->slab_sums;
+      }
       if (launch_dx(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
     }
     if (d_weight) {
@@ -730,7 +734,7 @@ flp_status flp_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype 
 size_t flp_cross_entropy_backward_workspace_bytes(int64_t N, int64_t D, int64_t V,
                                                   flp_dtype x_dtype, int64_t chunk_rows) {
   const size_t b = flp_backward_workspace_bytes(N, D, V, x_dtype, x_dtype, chunk_rows);
-  return b == 0 ? 0 : loss_grad_layout(N).total + b;
+  return b == 0 ? 0 : loss_grad_layout(N, D, V).total + b;
 }
 
 flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
@@ -749,7 +753,7 @@ flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype
   if (N == 0) return zero_sums(d_weight, size_t(V) * D * dtype_size(x_dtype), d_bias, V, s);
   if (!d_hidden && !d_weight && !d_bias) return FLP_OK;
   if ((st = check_device()) != FLP_OK) return st;
-  const LossGradLayout L = loss_grad_layout(N);
+  const LossGradLayout L = loss_grad_layout(N, D, V);
   LossGradArgs g{};
   g.N = N;
   g.V = V;
@@ -758,6 +762,8 @@ flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype
   g.grad_out = grad_out;
   g.lse = stats;
   g.lse_rest = stats + N;
+  g.k_slab = L.k_slab;
+  g.slab_sums = reinterpret_cast<float*>(at(workspace, L.slab_off));
   g.terms = LossTerms{label_smoothing, z_loss, int(reduction)};
   g.rescale = x_dtype == FLP_F16;
   g.softmax = reinterpret_cast<float*>(at(workspace, L.softmax_off));

@@ -37,6 +37,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -1388,7 +1389,7 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
 //   d_hidden: M = tokens, N = D, K = V (padded); A = dz, B = W^T.
 //   d_weight: M = V, N = D, K = tokens (padded); A = dz^T, B = hidden^T.
 // LOAD: start from the fp32 accumulator p.acc; STORE: 0 = element type to p.out,
-// 1 = fp32 to p.acc.
+// 1 = fp32 to p.acc, 2 = the fp32 sums of K slab blockIdx.y to p.acc[blockIdx.y].
 // SCALED: the result is multiplied by *p.scale before it is rounded to p.out.
 template <class E, int BM, int BN, int WM, int WN, bool LOAD, int STORE, int NS = 2, int NSA = NS,
           bool SCALED = false>
@@ -1403,6 +1404,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(GemmArgs p) {
   tile_of<1>(blockIdx.x, nbm, nbn, tm, tn);
   const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
   const int64_t nl = n0 + wn * CW + 4 * g;
+  int64_t k0 = 0, kn = p.K;
+  if constexpr (STORE == 2) {
+    k0 = int64_t(blockIdx.y) * p.k_slab;
+    kn = min(p.k_slab, p.K - k0);
+  }
+  const int64_t st0 = k0 * E::kSize / 128;  // first 128-byte K stage
 
   f32x4_t acc[WMB][WNB];
 #pragma unroll
@@ -1416,9 +1423,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(GemmArgs p) {
       acc[mb][nb] = x;
     }
   }
-  Eng::template run<false>(acc, reinterpret_cast<const char*>(p.a) + m0 * p.lda_b, p.lda_b,
-                           p.a_ks, p.M - m0, reinterpret_cast<const char*>(p.b) + n0 * p.ldb_b,
-                           p.ldb_b, p.b_ks, p.N - n0, p.K * E::kSize, smem);
+  Eng::template run<false>(acc,
+                           reinterpret_cast<const char*>(p.a) + m0 * p.lda_b + st0 * p.a_ks,
+                           p.lda_b, p.a_ks, p.M - m0,
+                           reinterpret_cast<const char*>(p.b) + n0 * p.ldb_b + st0 * p.b_ks,
+                           p.ldb_b, p.b_ks, p.N - n0, kn * E::kSize, smem);
   if constexpr (SCALED) {
     static_assert(STORE == 0, "only the rounded result is scaled");
     const float scale = *p.scale;
@@ -1467,8 +1476,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(GemmArgs p) {
 #pragma unroll
     for (int nb = 0; nb < WNB; ++nb) {
       if (nl + nb * 16 >= p.N) continue;
-      if (STORE == 1)
-        *reinterpret_cast<f32x4_t*>(p.acc + m * p.N + nl + nb * 16) = acc[mb][nb];
+      if (STORE >= 1)
+        *reinterpret_cast<f32x4_t*>(p.acc + ((STORE == 2 ? int64_t(blockIdx.y) * p.M : 0) + m) * p.N +
+                                    nl + nb * 16) = acc[mb][nb];
       else
         store4<E>(p.out, m * p.ldo + nl + nb * 16, acc[mb][nb]);
     }
@@ -1645,8 +1655,9 @@ hipError_t gemm_cfg(const GemmArgs& a, hipStream_t s) {
   const hipError_t e = prepare(k_gemm<E, BM, BN, WM, WN, LOAD, STORE, NS, NSA, SCALED>, Eng::kLds, ready);
   if (e != hipSuccess) return e;
   const int64_t blocks = ((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
+  const unsigned slabs = STORE == 2 ? unsigned((a.K + a.k_slab - 1) / a.k_slab) : 1u;
   hipLaunchKernelGGL((k_gemm<E, BM, BN, WM, WN, LOAD, STORE, NS, NSA, SCALED>),
-                     dim3(unsigned(blocks)), dim3(Eng::NT), Eng::kLds, s, a);
+                     dim3(unsigned(blocks), slabs), dim3(Eng::NT), Eng::kLds, s, a);
   return hipGetLastError();
 }
 
@@ -1658,6 +1669,50 @@ constexpr int kGemmNSA = 3;
 // The per-element MFMA chain does not depend on the tile shape, so the GEMM
 // variants may use different tiles and still give the same bits.
 //
+// d_hidden in vocabulary slabs (the cross entropy's backward of few rows): the slabs'
+// fp32 sums side by side, then added in ascending order and rounded once.
+template <class E>
+__global__ __launch_bounds__(256) void k_slab_fold(GemmArgs p, int slabs) {
+  const int64_t n = p.M * p.N;  // a multiple of 32
+  const float scale = p.scale != nullptr ? *p.scale : 1.0f;
+  for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
+       i += int64_t(gridDim.x) * 1024) {
+    f32x4_t s = *reinterpret_cast<const f32x4_t*>(p.acc + i);
+    for (int k = 1; k < slabs; ++k) s += *reinterpret_cast<const f32x4_t*>(p.acc + k * n + i);
+    store4<E>(p.out, i, s * scale);
+  }
+}
+
+// The largest tile whose slabs give every compute unit a workgroup: larger tiles read
+// less of dz and W^T per product (1000 x 2688 x 131072 bf16 on MI355X: 256 x 224 tiles
+// 609 us, 128 x 128 tiles 1020 us).  The tile does not change the bits.
+template <class E>
+hipError_t dx_slabs(const GemmArgs& a, hipStream_t s) {
+  constexpr bool k16 = E::kSize == 2;
+  const int64_t slabs = (a.K + a.k_slab - 1) / a.k_slab;
+  auto fills = [&](int64_t bm, int64_t bn) {
+    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn) * slabs >= 256;
+  };
+  hipError_t e;
+  if (k16 && a.M > 128 && fills(256, 224))
+    e = gemm_cfg<E, 256, k16 ? 224 : 128, 4, 2, false, 2, 2, k16 ? kGemmNSA : 2>(a, s);
+  else if (a.M > 64 && fills(128, 128))
+    e = gemm_cfg<E, 128, 128, 2, 2, false, 2, k16 ? 3 : 2>(a, s);
+  else if (a.M > 128)
+    e = gemm_cfg<E, 128, 64, 2, 2, false, 2, 4>(a, s);
+  else if (a.M <= 64 && fills(64, 128))
+    e = gemm_cfg<E, 64, 128, 2, 2, false, 2, 3>(a, s);
+  else if (fills(64, 32))
+    e = gemm_cfg<E, 64, 32, 4, 1, false, 2, 8>(a, s);
+  else
+    e = gemm_cfg<E, 64, 16, 4, 1, false, 2, 8>(a, s);
+  if (e != hipSuccess) return e;
+  const int64_t n = a.M * a.N;
+  hipLaunchKernelGGL(k_slab_fold<E>, dim3(unsigned(std::min<int64_t>((n + 1023) / 1024, 4096))),
+                     dim3(256), 0, s, a, int((a.K + a.k_slab - 1) / a.k_slab));
+  return hipGetLastError();
+}
+
 // d_hidden walks the whole vocabulary for every tile and cannot split K without
 // changing the bits, so a batch of few rows has few tiles: there the tiles shrink
 // (more workgroups stream W^T side by side) and the LDS ring deepens.  Thresholds
@@ -1666,6 +1721,7 @@ constexpr int kGemmNSA = 3;
 // 1024, and the 256 x 224 tile from 2048 rows on.
 template <class E, bool SCALED = false>
 hipError_t dx_tiles16(const GemmArgs& a, hipStream_t s) {
+  if (a.k_slab > 0) return dx_slabs<E>(a, s);
   if (a.M <= 64) return gemm_cfg<E, 64, 16, 4, 1, false, 0, 8, 8, SCALED>(a, s);
   if (a.M <= 128) return gemm_cfg<E, 64, 32, 4, 1, false, 0, 8, 8, SCALED>(a, s);
   if (a.M <= 512) return gemm_cfg<E, 128, 64, 2, 2, false, 0, 4, 4, SCALED>(a, s);
@@ -1685,6 +1741,7 @@ hipError_t dx_dispatch<F16>(const GemmArgs& a, hipStream_t s) {
 }
 template <>
 hipError_t dx_dispatch<F32>(const GemmArgs& a, hipStream_t s) {
+  if (a.k_slab > 0) return dx_slabs<F32>(a, s);
   // as for 16 bits: smaller tiles and a deeper ring where there are few rows (64 rows over
   // D = 256, V = 4096 on MI355X: 241 -> 28 us)
   if (a.M <= 64) return gemm_cfg<F32, 64, 16, 4, 1, false, 0, 8>(a, s);

@@ -118,6 +118,7 @@ struct GemmArgs {
   int load_acc;          // continue from acc
   int store_acc;         // store fp32 to acc (else store to out in x dtype)
   const float* scale = nullptr;  // fp16: factor of the rounded result, or null for 1
+  int64_t k_slab = 0;    // d_hidden: > 0 sums K in slabs of this length, held in acc [slabs][M][N]
 };
 
 hipError_t launch_forward(flp_dtype x, const FwdArgs& a, hipStream_t s);
@@ -243,6 +244,8 @@ struct LossGradArgs {        // backward: the per-row factors of the logit gradi
   float* uniform;            // [N] term of every entry
   float* unscale;            // [1] factor that takes the scaling back
   const float* lse_rest;     // [N]
+  int64_t k_slab;            // vocabulary slab of d_hidden, 0 for none
+  float* slab_sums;          // [slabs][N][D]
 };
 hipError_t launch_loss_rows(const LossRowsArgs& a, hipStream_t s);
 hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s);

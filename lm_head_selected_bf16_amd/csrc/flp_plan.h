@@ -110,11 +110,19 @@ struct LossFwdLayout {
 LossFwdLayout loss_fwd_layout(int64_t N, int64_t D, int64_t V);
 // Factor of the summed logits: the largest power of two that is at most 1 / V.
 float loss_zunit(int64_t V);
-// Backward: the per-row factors of dz, in front of the logp backward's workspace.
+// Backward: the per-row factors of dz and the slab sums of d_hidden, in front of the logp
+// backward's workspace.
+//
+// A batch of up to kSlabRows rows sums d_hidden over slabs of the vocabulary: its few
+// output tiles would otherwise walk the whole vocabulary one after another and leave most
+// compute units idle.  The slab length depends on V alone, so among such batches a row's
+// d_hidden does not depend on the others.
+constexpr int64_t kSlabRows = 1024;
 struct LossGradLayout {
-  size_t softmax_off = 0, onehot_off = 0, uniform_off = 0, unscale_off = 0, total = 0;
+  size_t softmax_off = 0, onehot_off = 0, uniform_off = 0, unscale_off = 0, slab_off = 0, total = 0;
+  int64_t k_slab = 0;     // columns of a slab (a multiple of 256), 0: one walk
 };
-LossGradLayout loss_grad_layout(int64_t N);
+LossGradLayout loss_grad_layout(int64_t N, int64_t D, int64_t V);
 
 // ---- layer norm backward: slabs of rows whose d_weight and d_bias partials are added ----
 constexpr int64_t kNormSlabs = 256;    // at most this many slabs (one workgroup per compute unit)

@@ -289,6 +289,25 @@ def test_rows_do_not_depend_on_the_batch(dtype):
             assert torch.equal(x, y[s])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("N", [5, 64, 65, 128, 129, 512, 513, 1023, 1024, 1025])
+def test_slabs_of_the_vocabulary(dtype, N):
+    """Row counts around every tile of d_hidden, over a vocabulary of several slabs and a ragged
+    last one, and past the last row count that takes slabs."""
+    compare(*make(N, 96, 9001, dtype, 30 + N), s=0.1, c=1e-3, reduction="mean")
+
+
+def test_slabs_keep_rows_apart():
+    m = flp()
+    h, w, b, t, up = make(1024, 64, 9000, BF16, 31)
+    dh = run(h, w, b, t, up, reduction="none")[2]
+    for lo, hi in ((0, 1), (3, 60), (200, 330), (300, 1000)):
+        s = slice(lo, hi)
+        part = run(h[s].contiguous(), w, b, t[s].contiguous(), up[s].contiguous(),
+                   reduction="none")[2]
+        assert torch.equal(part, dh[s])
+
+
 def test_gradient_against_differences():
     m = flp()
     h, w, b, t, up = make(6, 32, 40, F32, 17, ignored=0.0, w_std=0.3)
