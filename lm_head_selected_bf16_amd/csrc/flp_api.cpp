@@ -647,8 +647,6 @@ flp_status flp_embedding_scaled_backward(int64_t N, int64_t D, int64_t V, flp_dt
     a.vals[k] = reinterpret_cast<int32_t*>(at(workspace, L.vals_off[k]));
   }
   a.hist = reinterpret_cast<int32_t*>(at(workspace, L.hist_off));
-  a.seg_begin = reinterpret_cast<int32_t*>(at(workspace, L.seg_begin_off));
-  a.seg_end = reinterpret_cast<int32_t*>(at(workspace, L.seg_end_off));
   a.head = reinterpret_cast<float*>(at(workspace, L.head_off));
   a.tail = reinterpret_cast<float*>(at(workspace, L.tail_off));
   a.d_weight = d_weight;

@@ -11,18 +11,20 @@
 // with s = 1 for the plain lookup.
 //
 // The backward sorts the (id, token) pairs by id with a stable LSD radix sort
-// (8-bit digits, blocks of 256 keys; ranks inside a block come from an
-// in-order count, so the sort is deterministic) and finds each id's segment in
-// the sorted list.  The sorted list is then cut into fixed groups of 32
-// positions, one workgroup each, so a frequent id does not serialise on one
-// wave: inside a group every run of equal ids is summed in fp32 in token order;
-// a segment that spans several groups adds its per-group pieces in group order.
-// Every order is fixed by the sorted list: the output is bitwise reproducible.
+// (9-bit digits, blocks of 256 keys; ranks inside a block come from an in-order
+// count, so the sort is deterministic).  The sorted list is then cut into fixed
+// groups of 32 positions, one workgroup each, so a frequent id does not serialise
+// on one wave: inside a group every run of equal ids is summed in fp32 in token
+// order; a segment that spans several groups adds its per-group pieces in group
+// order.  Every order is fixed by the sorted list: the output is bitwise
+// reproducible.
 //
-// The rows of ids that do not occur are most of d_E's bytes.  The sort's
-// scatter passes occupy few compute units, so their launches (and the group
-// pass) carry extra "rider" workgroups that write those zero rows alongside;
-// the first sort pass marks the ids that occur before any rider runs.
+// Writing d_E is most of the work, and most of its rows are zeros (ids that do not
+// occur).  The sort's scatter passes occupy few compute units and wait on latency, so
+// each of them carries extra "rider" workgroups that clear a share of d_E; the rows of
+// ids that occur are written after the last of them.  N = 16384, D = 2688, V = 131072
+// bf16 on MI355X: 174 us for 793 MB in six launches (riders that spared the occurring
+// rows, behind a pass that marked them: 190 us in eleven).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -78,108 +80,108 @@ __global__ __launch_bounds__(256) void k_embed_fwd(const u32x4* __restrict__ wei
   }
 }
 
-// Zero rows of ids that do not occur, written by workgroups appended to another
-// kernel's grid: workgroup r of the riders clears rows v0 + 4 r .. v0 + 4 r + 3 of
-// [v0, v1) (one wave per row) whose id is unmarked.  seg_end[v] != 0 marks an id
-// that occurs (set by the first sort pass, later overwritten by its segment end,
-// which is never 0).
+// A share of d_E to be cleared by workgroups appended to another kernel's grid: the
+// 16-byte chunks [c0, c1), `per` per workgroup.  One store per thread is fastest (352 MB
+// on MI355X: 50 us beside a sort pass; 4 stores per thread 55, 16 stores 64); only a share
+// beyond 16 GB takes more, since a launch holds fewer than 2^32 threads.
 struct ZeroRider {
-  u32x4* dW;               // d_E [V][row_vec]
-  const int32_t* seg_end;  // [V]
-  int64_t v0, v1;          // rows of this launch
-  int64_t row_vec;         // 16-byte chunks per d_E row
-  int64_t blocks() const { return (v1 - v0 + 3) / 4; }
+  u32x4* dW;
+  int64_t c0, c1, per;
+  ZeroRider(void* d_weight, int64_t first, int64_t last)
+      : dW(static_cast<u32x4*>(d_weight)), c0(first), c1(last),
+        per(256 * (1 + (last - first) / (int64_t(1) << 30))) {}
+  int64_t blocks() const { return (c1 - c0 + per - 1) / per; }
 };
 
 __device__ __forceinline__ void ride(const ZeroRider& z, int64_t r) {
-  const int64_t v = z.v0 + r * 4 + (threadIdx.x >> 6);
-  if (v >= z.v1 || z.seg_end[v] != 0) return;
+  const int64_t c1 = min(z.c1, z.c0 + (r + 1) * z.per);
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  u32x4* row = z.dW + v * z.row_vec;
-  for (int64_t c = threadIdx.x & 63; c < z.row_vec; c += 64) __builtin_nontemporal_store(zero, row + c);
+  for (int64_t c = z.c0 + r * z.per + threadIdx.x; c < c1; c += 256)
+    __builtin_nontemporal_store(zero, z.dW + c);
 }
 
 // Sort keys: the id, or V for an id outside [0, V) (those sort last and are
-// dropped); values: the token index.  The same grid clears the [V] segment
-// bounds (an id that does not occur keeps an empty segment).
-__global__ __launch_bounds__(256) void k_sort_init(const void* __restrict__ ids, int i64, int64_t N,
-                                                   int64_t V, uint32_t* __restrict__ keys,
-                                                   int32_t* __restrict__ vals,
-                                                   int32_t* __restrict__ seg_begin,
-                                                   int32_t* __restrict__ seg_end) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i < V) {
-    seg_begin[i] = 0;
-    seg_end[i] = 0;
+// dropped); values: the token index.  The first pass reads them from the ids.
+constexpr int kDigitBits = int(kEmbDigitBits), kDigits = 1 << kDigitBits;
+struct SortArgs {
+  const void* ids;
+  int i64;
+  int64_t V;
+  const uint32_t* keys;  // [n], or null in the first pass
+  const int32_t* vals;
+  int64_t n;
+  int shift;
+  int64_t n_blocks, ld;  // ld: n_blocks rounded up to 4
+  int32_t* hist;         // [kDigits][ld]
+  __device__ __forceinline__ uint32_t key(int64_t i) const {
+    if (keys != nullptr) return keys[i];
+    const int64_t v = load_id(ids, i64 != 0, i);
+    return (v >= 0 && v < V) ? uint32_t(v) : uint32_t(V);
   }
-  if (i >= N) return;
-  const int64_t v = load_id(ids, i64 != 0, i);
-  keys[i] = (v >= 0 && v < V) ? uint32_t(v) : uint32_t(V);
-  vals[i] = int32_t(i);
-}
+};
 
-// Per-block digit counts, stored digit-major: hist[d * n_blocks + b].  With
-// `mark` set (the first pass), also marks every id that occurs: mark[id] = 1.
-__global__ __launch_bounds__(256) void k_sort_hist(const uint32_t* __restrict__ keys, int64_t n,
-                                                   int shift, int64_t n_blocks,
-                                                   int32_t* __restrict__ hist,
-                                                   int32_t* __restrict__ mark, int64_t V) {
-  __shared__ int32_t cnt[256];
-  const int t = threadIdx.x;
+// Per-block digit counts, stored digit-major: hist[d * ld + b].
+__global__ __launch_bounds__(256) void k_sort_hist(SortArgs p) {
   const int64_t b = blockIdx.x;
-  cnt[t] = 0;
+  __shared__ int32_t cnt[kDigits];
+  const int t = threadIdx.x;
+  for (int d = t; d < kDigits; d += 256) cnt[d] = 0;
   __syncthreads();
-  for (int k = t; k < kSortBlock; k += 256) {
-    const int64_t i = b * kSortBlock + k;
-    if (i < n) {
-      const uint32_t key = keys[i];
-      atomicAdd(&cnt[(key >> shift) & 255u], 1);
-      if (mark != nullptr && int64_t(key) < V) mark[key] = 1;
-    }
-  }
+  const int64_t i = b * kSortBlock + t;
+  if (i < p.n) atomicAdd(&cnt[(p.key(i) >> p.shift) & (kDigits - 1)], 1);
   __syncthreads();
-  hist[int64_t(t) * n_blocks + b] = cnt[t];
+  for (int d = t; d < kDigits; d += 256) p.hist[d * p.ld + b] = cnt[d];
 }
 
 // Stable scatter of one radix pass.  A block holds 256 consecutive keys.  Its
 // offset for digit d is the count of all keys with a smaller digit plus the
-// count of keys with digit d in earlier blocks (thread d sums its digit's
-// counts, then an exclusive scan over the 256 digit totals in LDS); a key's
+// count of keys with digit d in earlier blocks (each thread sums its digits'
+// counts, then an exclusive scan over the digit totals in LDS); a key's
 // place adds the number of keys before it in the block with the same digit.
-__global__ __launch_bounds__(256) void k_sort_scatter(const uint32_t* __restrict__ kin,
-                                                      const int32_t* __restrict__ vin, int64_t n,
-                                                      int shift, int64_t n_blocks,
-                                                      const int32_t* __restrict__ hist,
-                                                      uint32_t* __restrict__ kout,
+__global__ __launch_bounds__(256) void k_sort_scatter(SortArgs p, uint32_t* __restrict__ kout,
                                                       int32_t* __restrict__ vout, ZeroRider z) {
-  if (int64_t(blockIdx.x) >= n_blocks) {
-    ride(z, int64_t(blockIdx.x) - n_blocks);
+  const int64_t b = blockIdx.x;
+  if (b >= p.n_blocks) {
+    ride(z, b - p.n_blocks);
     return;
   }
-  __shared__ int32_t tot[256];
-  __shared__ int32_t run[256];
+  typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+  __shared__ int32_t tot[kDigits];
+  __shared__ int32_t run[kDigits];
   __shared__ int32_t dig[256];
   const int t = threadIdx.x;
-  const int64_t b = blockIdx.x;
-  int32_t before = 0, all = 0;
-  const int32_t* h = hist + int64_t(t) * n_blocks;
-  for (int64_t q0 = 0; q0 < n_blocks; q0 += 8) {  // eight counts in flight
-    int32_t c[8];
+  constexpr int kPer = kDigits / 256;
+  int32_t before[kPer];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) c[u] = (q0 + u < n_blocks) ? h[q0 + u] : 0;
+  for (int e = 0; e < kPer; ++e) {
+    before[e] = 0;
+    int32_t all = 0;
+    const int32_t* h = p.hist + int64_t(t + 256 * e) * p.ld;
+    for (int64_t q0 = 0; q0 < p.n_blocks; q0 += 32) {  // eight 16-byte loads in flight
+      i32x4 c[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      before += (q0 + u < b) ? c[u] : 0;
-      all += c[u];
+      for (int u = 0; u < 8; ++u)
+        c[u] = q0 + 4 * u < p.n_blocks ? *reinterpret_cast<const i32x4*>(h + q0 + 4 * u)
+                                       : i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t q = q0 + 4 * u + k;
+          const int32_t x = q < p.n_blocks ? c[u][k] : 0;  // the padding is not written
+          before[e] += q < b ? x : 0;
+          all += x;
+        }
     }
+    tot[t + 256 * e] = all;
   }
-  tot[t] = all;
   __syncthreads();
-  if (t < 64) {  // exclusive scan of the 256 digit totals by one wave, 4 per lane
-    int32_t x[4], sum = 0;
+  if (t < 64) {  // exclusive scan of the digit totals by one wave
+    constexpr int kLane = kDigits / 64;
+    int32_t x[kLane], sum = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[k] = tot[4 * t + k];
+    for (int k = 0; k < kLane; ++k) {
+      x[k] = tot[kLane * t + k];
       sum += x[k];
     }
     int32_t inc = sum;
@@ -188,19 +190,20 @@ __global__ __launch_bounds__(256) void k_sort_scatter(const uint32_t* __restrict
       const int32_t y = __shfl_up(inc, off);
       if (t >= off) inc += y;
     }
-    int32_t p = inc - sum;
+    int32_t at = inc - sum;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      run[4 * t + k] = p;
-      p += x[k];
+    for (int k = 0; k < kLane; ++k) {
+      run[kLane * t + k] = at;
+      at += x[k];
     }
   }
   __syncthreads();
-  run[t] += before;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) run[t + 256 * e] += before[e];
   const int64_t i = b * kSortBlock + t;
-  const bool valid = i < n;
-  const uint32_t key = valid ? kin[i] : 0u;
-  const int d = valid ? int((key >> shift) & 255u) : -1;
+  const bool valid = i < p.n;
+  const uint32_t key = valid ? p.key(i) : 0u;
+  const int d = valid ? int((key >> p.shift) & (kDigits - 1)) : -1;
   dig[t] = d;
   __syncthreads();
   int r = 0;
@@ -208,21 +211,8 @@ __global__ __launch_bounds__(256) void k_sort_scatter(const uint32_t* __restrict
   if (valid) {
     const int32_t pos = run[d] + r;
     kout[pos] = key;
-    vout[pos] = vin[i];
+    vout[pos] = p.keys != nullptr ? p.vals[i] : int32_t(i);
   }
-}
-
-// Segment of each id in the sorted keys: [seg_begin[v], seg_end[v]) (both
-// zero-filled before, so an id that does not occur has an empty segment).
-__global__ __launch_bounds__(256) void k_seg_bounds(const uint32_t* __restrict__ keys, int64_t n,
-                                                    int64_t V, int32_t* __restrict__ seg_begin,
-                                                    int32_t* __restrict__ seg_end) {
-  const int64_t p = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (p >= n) return;
-  const uint32_t k = keys[p];
-  if (int64_t(k) >= V) return;
-  if (p == 0 || keys[p - 1] != k) seg_begin[k] = int32_t(p);
-  if (p == n - 1 || keys[p + 1] != k) seg_end[k] = int32_t(p + 1);
 }
 
 template <int SIZE>
@@ -288,8 +278,8 @@ __device__ __forceinline__ void store_chunk(const float* sum, float scale, void*
 // (= ascending token) order.  A run that is its id's whole segment is written to
 // d_W at once; a run that starts at the group's first position goes to the
 // group's head slot, any other run that reaches past the group to its tail slot
-// (a group holds at most one of each).  Thread t owns the 16-byte chunks
-// t, t + 256, ... of a row.
+// (a group holds at most one of each).  Thread t owns one 16-byte chunk of a row:
+// chunk kColThreads blockIdx.y + t.
 constexpr int kSegGroup = int(kEmbSegGroup);
 
 template <int XS, bool OUT_F32>
@@ -311,20 +301,18 @@ __device__ __forceinline__ void finish_run(const float* acc, float scale, int64_
   }
 }
 
+// Threads per workgroup of the two passes below, one 16-byte chunk of the row each (128
+// of them fill a 336-chunk row's workgroups better than 256: 61 -> 46 us).
+constexpr int kColThreads = 128;
+
 template <int XS, bool OUT_F32>
-__global__ __launch_bounds__(256) void k_embed_runs(const u32x4* __restrict__ grad, int f16,
+__global__ __launch_bounds__(kColThreads) void k_embed_runs(const u32x4* __restrict__ grad, int f16,
                                                     const uint32_t* __restrict__ keys,
-                                                    const int32_t* __restrict__ tok,
-                                                    const int32_t* __restrict__ seg_begin,
-                                                    const int32_t* __restrict__ seg_end, int64_t N,
+                                                    const int32_t* __restrict__ tok, int64_t N,
                                                     int64_t V, int64_t row_vec,
                                                     float* __restrict__ head,
                                                     float* __restrict__ tail, void* __restrict__ dW,
-                                                    int64_t n_groups, float scale, ZeroRider z) {
-  if (int64_t(blockIdx.x) >= n_groups) {
-    ride(z, int64_t(blockIdx.x) - n_groups);
-    return;
-  }
+                                                    float scale) {
   constexpr int EPC = 16 / XS;
   __shared__ uint32_t skey[kSegGroup];
   __shared__ int32_t stok[kSegGroup];
@@ -339,16 +327,18 @@ __global__ __launch_bounds__(256) void k_embed_runs(const u32x4* __restrict__ gr
     const bool live = in && int64_t(k) < V;
     skey[threadIdx.x] = k;
     stok[threadIdx.x] = live ? tok[s0 + threadIdx.x] : -1;
-    // a run inside the group is the whole segment iff the segment starts at or after
-    // the group start and ends at or before the group end
-    whole[threadIdx.x] =
-        live ? uint8_t(seg_begin[k] >= s0 && seg_end[k] <= s0 + kSegGroup) : uint8_t(0);
+    // a run inside the group is the whole segment iff neither neighbour of the group has
+    // its id (a dropped id's key V is never a live one)
+    const uint32_t prev = s0 > 0 ? keys[s0 - 1] : uint32_t(V);
+    const uint32_t next = s0 + kSegGroup < N ? keys[s0 + kSegGroup] : uint32_t(V);
+    whole[threadIdx.x] = uint8_t(live && k != prev && k != next);
   }
   __syncthreads();
   // summed positions: the prefix of the group with ids in [0, V) (dropped ids sort last)
   int m = 0;
   while (m < n && int64_t(skey[m]) < V) ++m;
-  for (int64_t c = threadIdx.x; c < row_vec; c += 256) {
+  const int64_t c = int64_t(blockIdx.y) * kColThreads + threadIdx.x;
+  if (c < row_vec) {
     // every row of the group in flight at once, then the runs in order
     u32x4 x4[kSegGroup];
 #pragma unroll
@@ -384,62 +374,64 @@ __global__ __launch_bounds__(256) void k_embed_runs(const u32x4* __restrict__ gr
 
 // Pass B: an id whose segment spans several groups adds its pieces in group
 // order (the first group's head or tail slot, then the head slots of the
-// following groups); an id inside one group was written by pass A, and an id
-// that does not occur by a zero-row rider.  Workgroup b of B tests the ids b,
-// b + B, ..., one per thread (the stride spreads frequent ids, which are often
-// neighbours, over many workgroups), lists the spanning ones in LDS, then
-// combines them one after another with all 256 threads, eight pieces in flight.
+// following groups); an id inside one group was written by pass A.  One workgroup
+// per group: the group in which a spanning segment begins combines it, eight pieces
+// in flight.
 template <int XS, bool OUT_F32>
-__global__ __launch_bounds__(256) void k_embed_rows(const int32_t* __restrict__ seg_begin,
-                                                    const int32_t* __restrict__ seg_end,
+__global__ __launch_bounds__(kColThreads) void k_embed_rows(const uint32_t* __restrict__ keys, int64_t N,
                                                     int64_t V, int64_t row_vec,
                                                     const float* __restrict__ head,
                                                     const float* __restrict__ tail, int f16,
                                                     float scale, void* __restrict__ dW) {
   constexpr int EPC = 16 / XS;
-  __shared__ int32_t list[256];
   __shared__ int32_t count;
   const int t = threadIdx.x;
-  const int64_t v_t = int64_t(blockIdx.x) + int64_t(t) * gridDim.x;
-  if (t == 0) count = 0;
-  __syncthreads();
-  if (v_t < V) {
-    const int32_t b = seg_begin[v_t], e = seg_end[v_t];
-    if (e > b && b / kSegGroup != (e - 1) / kSegGroup) list[atomicAdd(&count, 1)] = t;
+  const int64_t g0 = blockIdx.x, s0 = g0 * kSegGroup;
+  if (s0 + kSegGroup >= N) return;  // nothing follows the last group
+  const uint32_t k = keys[s0 + kSegGroup - 1];
+  if (int64_t(k) >= V || keys[s0 + kSegGroup] != k) return;
+  const bool from_start = keys[s0] == k;
+  if (from_start && s0 > 0 && keys[s0 - 1] == k) return;  // began in an earlier group
+  // Groups after g0 whose first position has the id: all up to the first that has not.
+  int64_t g1 = g0;
+  for (;;) {
+    if (t == 0) count = kColThreads;
+    __syncthreads();
+    const int64_t s = (g1 + 1 + t) * kSegGroup;
+    if (s >= N || keys[s] != k) atomicMin(&count, t);
+    __syncthreads();
+    const int n = count;
+    g1 += n;
+    if (n < kColThreads) break;
+    __syncthreads();
   }
-  __syncthreads();
-  const int n = count;
-  for (int k = 0; k < n; ++k) {
-    const int64_t v = int64_t(blockIdx.x) + int64_t(list[k]) * gridDim.x;
-    const int64_t b = seg_begin[v], e = seg_end[v];
-    const int64_t g0 = b / kSegGroup, g1 = (e - 1) / kSegGroup;
-    const float* first = (b == g0 * kSegGroup) ? head : tail;
-    for (int64_t c = t; c < row_vec; c += 256) {
-      float acc[EPC];
-      const float* f = first + (g0 * row_vec + c) * EPC;
+  const float* first = from_start ? head : tail;
+  const int64_t c = int64_t(blockIdx.y) * kColThreads + t;
+  if (c < row_vec) {
+    float acc[EPC];
+    const float* f = first + (g0 * row_vec + c) * EPC;
 #pragma unroll
-      for (int q = 0; q < EPC; ++q) acc[q] = f[q];
-      int64_t g = g0 + 1;
-      for (; g + 8 <= g1 + 1; g += 8) {  // eight pieces in flight, added in group order
-        float x[8][EPC];
+    for (int q = 0; q < EPC; ++q) acc[q] = f[q];
+    int64_t g = g0 + 1;
+    for (; g + 8 <= g1 + 1; g += 8) {  // eight pieces in flight, added in group order
+      float x[8][EPC];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float* h = head + ((g + u) * row_vec + c) * EPC;
+      for (int u = 0; u < 8; ++u) {
+        const float* h = head + ((g + u) * row_vec + c) * EPC;
 #pragma unroll
-          for (int q = 0; q < EPC; ++q) x[u][q] = h[q];
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-#pragma unroll
-          for (int q = 0; q < EPC; ++q) acc[q] += x[u][q];
+        for (int q = 0; q < EPC; ++q) x[u][q] = h[q];
       }
-      for (; g <= g1; ++g) {
-        const float* h = head + (g * row_vec + c) * EPC;
 #pragma unroll
-        for (int q = 0; q < EPC; ++q) acc[q] += h[q];
-      }
-      store_chunk<XS, OUT_F32>(acc, scale, dW, v, row_vec, c, f16 != 0);
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int q = 0; q < EPC; ++q) acc[q] += x[u][q];
     }
+    for (; g <= g1; ++g) {
+      const float* h = head + (g * row_vec + c) * EPC;
+#pragma unroll
+      for (int q = 0; q < EPC; ++q) acc[q] += h[q];
+    }
+    store_chunk<XS, OUT_F32>(acc, scale, dW, int64_t(k), row_vec, c, f16 != 0);
   }
 }
 
@@ -448,7 +440,7 @@ __global__ __launch_bounds__(256) void k_embed_rows(const int32_t* __restrict__ 
 int embed_sort_passes(int64_t V) {
   int bits = 0;
   while ((uint64_t(V) >> bits) != 0) ++bits;  // keys run up to V (the dropped-id key)
-  return (bits + 7) / 8;
+  return (bits + kDigitBits - 1) / kDigitBits;
 }
 
 hipError_t launch_embedding_forward(flp_dtype x, const void* weight, const void* ids, bool i64,
@@ -475,68 +467,45 @@ hipError_t launch_embedding_forward(flp_dtype x, const void* weight, const void*
 hipError_t launch_embedding_backward(const EmbedBwdArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_EMBEDDING, s);
   const int64_t N = a.N, V = a.V;
-  const int64_t n_blocks = (N + kSortBlock - 1) / kSortBlock;
-  const int64_t init_n = N > V ? N : V;
-  hipLaunchKernelGGL(k_sort_init, dim3(unsigned((init_n + 255) / 256)), dim3(256), 0, s, a.ids,
-                     int(a.i64), N, V, a.keys[0], a.vals[0], a.seg_begin, a.seg_end);
+  SortArgs p{};
+  p.ids = a.ids;
+  p.i64 = int(a.i64);
+  p.V = V;
+  p.n = N;
+  p.n_blocks = (N + kSortBlock - 1) / kSortBlock;
+  p.ld = (p.n_blocks + 3) / 4 * 4;
+  p.hist = a.hist;
   const int passes = embed_sort_passes(V);
-  // Zero rows ride on the scatter launches (latency-bound, with most compute
-  // units idle) and on the group pass: the group pass takes the upper half of
-  // the rows, the scatters share the lower half evenly.
-  ZeroRider z{};
-  z.dW = static_cast<u32x4*>(a.d_weight);
-  z.seg_end = a.seg_end;
-  z.row_vec = a.D * int64_t(dtype_size(a.dw)) / 16;
-  const int64_t lower = V - V / 2;
-  const int n_sort_slices = passes;
-  int slice = 0;
-  auto next_slice = [&]() {
-    ZeroRider r = z;
-    r.v0 = lower * slice / n_sort_slices;
-    r.v1 = lower * (slice + 1) / n_sort_slices;
-    ++slice;
-    return r;
-  };
-  for (int p = 0; p < passes; ++p) {
-    const int src = p & 1, dst = src ^ 1;
-    hipLaunchKernelGGL(k_sort_hist, dim3(unsigned(n_blocks)), dim3(256), 0, s, a.keys[src], N,
-                       8 * p, n_blocks, a.hist, p == 0 ? a.seg_end : nullptr, V);
-    const ZeroRider zs = next_slice();
-    hipLaunchKernelGGL(k_sort_scatter, dim3(unsigned(n_blocks + zs.blocks())), dim3(256), 0, s,
-                       a.keys[src], a.vals[src], N, 8 * p, n_blocks, a.hist, a.keys[dst],
-                       a.vals[dst], zs);
+  const int64_t chunks = V * (a.D * int64_t(dtype_size(a.dw)) / 16);
+  for (int k = 0; k < passes; ++k) {
+    const int src = k & 1, dst = src ^ 1;
+    p.keys = k == 0 ? nullptr : a.keys[src];
+    p.vals = a.vals[src];
+    p.shift = kDigitBits * k;
+    hipLaunchKernelGGL(k_sort_hist, dim3(unsigned(p.n_blocks)), dim3(256), 0, s, p);
+    const ZeroRider z(a.d_weight, chunks / passes * k,
+                      k + 1 == passes ? chunks : chunks / passes * (k + 1));
+    hipLaunchKernelGGL(k_sort_scatter, dim3(unsigned(p.n_blocks + z.blocks())), dim3(256), 0, s, p,
+                       a.keys[dst], a.vals[dst], z);
   }
   const int fin = passes & 1;
-  hipLaunchKernelGGL(k_seg_bounds, dim3(unsigned((N + 255) / 256)), dim3(256), 0, s, a.keys[fin],
-                     N, V, a.seg_begin, a.seg_end);
   const int64_t row_vec = a.D * int64_t(dtype_size(a.x)) / 16;
-  const int64_t n_groups = (N + kSegGroup - 1) / kSegGroup;
-  ZeroRider zr = z;
-  zr.v0 = lower;
-  zr.v1 = V;
-  const dim3 ga(unsigned(n_groups + zr.blocks())), gb(unsigned((V + 255) / 256));
+  const dim3 groups(unsigned((N + kSegGroup - 1) / kSegGroup),
+                    unsigned((row_vec + kColThreads - 1) / kColThreads));
   const int f16 = a.x == FLP_F16 ? 1 : 0;
   const u32x4* g = static_cast<const u32x4*>(a.grad);
-  const uint32_t* keys = a.keys[fin];
-  const int32_t* tok = a.vals[fin];
-  if (a.x == FLP_F32) {
-    hipLaunchKernelGGL((k_embed_runs<4, true>), ga, dim3(256), 0, s, g, 0, keys, tok, a.seg_begin,
-                       a.seg_end, N, V, row_vec, a.head, a.tail, a.d_weight, n_groups, a.scale, zr);
-    hipLaunchKernelGGL((k_embed_rows<4, true>), gb, dim3(256), 0, s, a.seg_begin, a.seg_end, V,
-                       row_vec, a.head, a.tail, 0, a.scale, a.d_weight);
-  } else if (a.dw == FLP_F32) {
-    hipLaunchKernelGGL((k_embed_runs<2, true>), ga, dim3(256), 0, s, g, f16, keys, tok,
-                       a.seg_begin, a.seg_end, N, V, row_vec, a.head, a.tail, a.d_weight,
-                       n_groups, a.scale, zr);
-    hipLaunchKernelGGL((k_embed_rows<2, true>), gb, dim3(256), 0, s, a.seg_begin, a.seg_end, V,
-                       row_vec, a.head, a.tail, f16, a.scale, a.d_weight);
-  } else {
-    hipLaunchKernelGGL((k_embed_runs<2, false>), ga, dim3(256), 0, s, g, f16, keys, tok,
-                       a.seg_begin, a.seg_end, N, V, row_vec, a.head, a.tail, a.d_weight,
-                       n_groups, a.scale, zr);
-    hipLaunchKernelGGL((k_embed_rows<2, false>), gb, dim3(256), 0, s, a.seg_begin, a.seg_end, V,
-                       row_vec, a.head, a.tail, f16, a.scale, a.d_weight);
-  }
+  auto sums = [&](auto runs, auto rows) {
+    hipLaunchKernelGGL(runs, groups, dim3(kColThreads), 0, s, g, f16, a.keys[fin], a.vals[fin], N, V,
+                       row_vec, a.head, a.tail, a.d_weight, a.scale);
+    hipLaunchKernelGGL(rows, groups, dim3(kColThreads), 0, s, a.keys[fin], N, V, row_vec, a.head, a.tail,
+                       f16, a.scale, a.d_weight);
+  };
+  if (a.x == FLP_F32)
+    sums(k_embed_runs<4, true>, k_embed_rows<4, true>);
+  else if (a.dw == FLP_F32)
+    sums(k_embed_runs<2, true>, k_embed_rows<2, true>);
+  else
+    sums(k_embed_runs<2, false>, k_embed_rows<2, false>);
   return hipGetLastError();
 }
 

@@ -165,9 +165,7 @@ struct EmbedBwdArgs {
   int64_t N, D, V;
   uint32_t* keys[2];         // [N] radix-sort ping-pong buffers
   int32_t* vals[2];          // [N]
-  int32_t* hist;             // [256][ceil(N / kEmbSortBlock)]
-  int32_t* seg_begin;        // [V]
-  int32_t* seg_end;          // [V]
+  int32_t* hist;             // [2^kEmbDigitBits][ceil(N / kEmbSortBlock) rounded up to 4]
   float* head;               // [ceil(N / kEmbSegGroup)][D] fp32 pieces of segments that span groups
   float* tail;               // same shape
   void* d_weight;            // [V][D] dw

@@ -221,11 +221,11 @@ EmbLayout emb_layout(int64_t N, int64_t D, int64_t V) {
     off += align_up(n * 4);
   }
   L.hist_off = off;
-  off += align_up(size_t(256) * size_t(L.n_blocks) * 4);
-  L.seg_begin_off = off;
-  off += align_up(size_t(V) * 4);
-  L.seg_end_off = off;
-  off += align_up(size_t(V) * 4);
+  // The documented size counts two words per id beside the digit counts of 256 digits; the
+  // 512 digits' counts may take more than those.
+  const size_t hist = (size_t(1) << kEmbDigitBits) * size_t(round_up(L.n_blocks, 4)) * 4;
+  off += std::max(align_up(hist), align_up(size_t(256) * size_t(L.n_blocks) * 4) +
+                                      2 * align_up(size_t(V) * 4));
   const size_t groups = size_t(ceil_div(std::max<int64_t>(N, 1), kEmbSegGroup));
   L.head_off = off;
   off += align_up(groups * size_t(D) * 4);

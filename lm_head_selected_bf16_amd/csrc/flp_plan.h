@@ -89,13 +89,14 @@ struct IdxLayout {
 IdxLayout idx_layout(int64_t N, int64_t D, int64_t n_rows, flp_dtype x, bool backward,
                      bool need_dh);
 
-// ---- embedding backward: radix-sort buffers and the per-id segments ----
+// ---- embedding backward: radix-sort buffers and the pieces of spanning segments ----
 constexpr int64_t kEmbSortBlock = 256;  // keys per block of a radix pass
+constexpr int64_t kEmbDigitBits = 9;    // bits of a radix digit (two passes up to V = 262143)
 constexpr int64_t kEmbSegGroup = 32;    // sorted positions per group of the segment sums
 struct EmbLayout {
   int64_t n_blocks = 0;   // radix-sort blocks of kEmbSortBlock keys
   size_t keys_off[2] = {0, 0}, vals_off[2] = {0, 0};
-  size_t hist_off = 0, seg_begin_off = 0, seg_end_off = 0;
+  size_t hist_off = 0;
   size_t head_off = 0, tail_off = 0, total = 0;  // fp32 [ceil(N / kEmbSegGroup)][D] each
 };
 EmbLayout emb_layout(int64_t N, int64_t D, int64_t V);
