@@ -529,12 +529,12 @@ def embedding_backward(grad: torch.Tensor, ids: torch.Tensor, num_embeddings: in
         raise ValueError("grad and ids must be on one device")
     with _on(dev):
         d_weight = torch.empty((V, D), dtype=dwt, device=dev)
-        ws = torch.empty(max(_abi.flp_embedding_backward_workspace_bytes(N, D, V), 16),
-                         dtype=torch.uint8, device=dev)
-        st = _abi.flp_embedding_scaled_backward(N, D, V, _X_DTYPES[grad.dtype], _ptr(grad),
-                                                _ptr(ids), _T_DTYPES[ids.dtype], scale,
-                                                _ptr(d_weight), _X_DTYPES[dwt], _ptr(ws),
-                                                ws.numel(), _stream(dev))
+        size = max(_abi.flp_embedding_backward_workspace_bytes(N, D, V), 16)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        st = _abi.flp_embedding_scaled_backward(N, D, V, _X_DTYPES[grad.dtype], grad.data_ptr(),
+                                                ids.data_ptr(), _T_DTYPES[ids.dtype], scale,
+                                                d_weight.data_ptr(), _X_DTYPES[dwt],
+                                                ws.data_ptr(), size, _stream(dev))
     _check("flp_embedding_scaled_backward", st)
     return d_weight
 
@@ -703,10 +703,18 @@ def dropout_forward(x: torch.Tensor, p: float, rng: torch.Tensor) -> torch.Tenso
     p = float(p)
     if not 0.0 <= p <= 1.0:
         raise ValueError("p must be between 0 and 1")
-    with _on(x.device):
-        out = torch.empty_like(x)
-        st = _abi.flp_dropout(x.numel(), _X_DTYPES[x.dtype], _ptr(x), p, _ptr(rng), _ptr(out),
-                              _stream(x.device))
+    return _launch_dropout(x, p, rng)
+
+
+def _launch_dropout(x, p, rng):
+    """The call on arguments that have been checked (the backward's were in the forward)."""
+    dev = x.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch_dropout(x, p, rng)
+    out = torch.empty_like(x)
+    st = _abi.flp_dropout(x.numel(), _X_DTYPES[x.dtype], x.data_ptr(), p, rng.data_ptr(),
+                          out.data_ptr(), _stream(dev))
     _check("flp_dropout", st)
     return out
 
@@ -717,7 +725,7 @@ class Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, p, rng):
         ctx.save_for_backward(rng)
-        ctx.p = p
+        ctx.p = float(p)
         return dropout_forward(x, p, rng)
 
     @staticmethod
@@ -725,7 +733,7 @@ class Dropout(torch.autograd.Function):
         (rng,) = ctx.saved_tensors
         if not ctx.needs_input_grad[0]:
             return None, None, None
-        return dropout_forward(grad.contiguous(), ctx.p, rng), None, None
+        return _launch_dropout(grad.contiguous(), ctx.p, rng), None, None
 
 
 def dropout(x, p, rng):
@@ -765,19 +773,28 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                        return_stats: bool = True):
     """(out, mean, rstd) of the layer norm over the last dimension through
     flp_layer_norm_forward; mean and rstd are float32 of the leading shape, or None."""
+    out, stats = _launch_norm(x, weight, bias, eps, return_stats)
+    return (out, stats[0], stats[1]) if return_stats else (out, None, None)
+
+
+def _launch_norm(x, weight, bias, eps, return_stats):
+    """(out, stats) with stats float32 [2, *leading shape] (mean, then rstd) or None."""
     N, D, wd = _prepare_norm(x, weight, bias)
     dev = x.device
-    with _on(dev):
-        out = torch.empty_like(x)
-        mean = rstd = None
-        if return_stats:
-            mean, rstd = torch.empty((2,) + tuple(x.shape[:-1]), dtype=torch.float32,
-                                     device=dev).unbind(0)
-        st = _abi.flp_layer_norm_forward(N, D, _X_DTYPES[x.dtype], _ptr(x), _X_DTYPES[wd],
-                                         _ptr(weight), _ptr(bias), float(eps), _ptr(out),
-                                         _ptr(mean), _ptr(rstd), _stream(dev))
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch_norm(x, weight, bias, eps, return_stats)
+    out = torch.empty_like(x)
+    stats, mean, rstd = None, 0, 0
+    if return_stats:
+        stats = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev)
+        mean = stats.data_ptr()
+        rstd = mean + 4 * N
+    st = _abi.flp_layer_norm_forward(N, D, _X_DTYPES[x.dtype], x.data_ptr(), _X_DTYPES[wd],
+                                     _ptr(weight), _ptr(bias), float(eps), out.data_ptr(), mean,
+                                     rstd, _stream(dev))
     _check("flp_layer_norm_forward", st)
-    return out, mean, rstd
+    return out, stats
 
 
 def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
@@ -786,7 +803,7 @@ def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Ten
                         w_dtype: Optional[torch.dtype] = None):
     """(d_x, d_weight, d_bias) through flp_layer_norm_backward; unrequested ones are None.
     d_weight and d_bias have w_dtype (the weight's, by default)."""
-    N, D, wd = _prepare_norm(x, weight, None)
+    _, D, wd = _prepare_norm(x, weight, None)
     if w_dtype is not None:
         if w_dtype not in (x.dtype, torch.float32) or (weight is not None and w_dtype != wd):
             raise TypeError("w_dtype must be the weight's dtype, or that of x or float32")
@@ -797,21 +814,31 @@ def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Ten
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t.dtype != torch.float32 or tuple(t.shape) != lead or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous float32 with the leading shape of x")
-    dev = x.device
-    if any(t.device != dev for t in (grad_out, mean, rstd)):
+    if any(t.device != x.device for t in (grad_out, mean, rstd)):
         raise ValueError("grad_out, mean and rstd must be on the device of x")
-    with _on(dev):
-        d_x = torch.empty_like(x) if need_input else None
-        d_weight = torch.empty(D, dtype=wd, device=dev) if need_weight else None
-        d_bias = torch.empty(D, dtype=wd, device=dev) if need_bias else None
-        ws = None
-        if need_weight or need_bias:
-            ws = torch.empty(max(_abi.flp_layer_norm_backward_workspace_bytes(N, D), 16),
-                             dtype=torch.uint8, device=dev)
-        st = _abi.flp_layer_norm_backward(N, D, _X_DTYPES[x.dtype], _ptr(grad_out), _ptr(x),
-                                          _X_DTYPES[wd], _ptr(weight), _ptr(mean), _ptr(rstd),
-                                          _ptr(d_x), _ptr(d_weight), _ptr(d_bias), _ptr(ws),
-                                          0 if ws is None else ws.numel(), _stream(dev))
+    return _launch_norm_backward(grad_out, x, mean.data_ptr(), rstd.data_ptr(), weight, need_input,
+                                 need_weight, need_bias, wd)
+
+
+def _launch_norm_backward(grad, x, mean, rstd, weight, need_input, need_weight, need_bias, wd):
+    """The call on arguments that have been checked; mean and rstd are addresses."""
+    dev = x.device
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch_norm_backward(grad, x, mean, rstd, weight, need_input, need_weight,
+                                         need_bias, wd)
+    D = x.shape[-1]
+    N = x.numel() // D
+    d_x = torch.empty_like(x) if need_input else None
+    d_weight = torch.empty(D, dtype=wd, device=dev) if need_weight else None
+    d_bias = torch.empty(D, dtype=wd, device=dev) if need_bias else None
+    ws, size = None, 0
+    if need_weight or need_bias:
+        size = max(_abi.flp_layer_norm_backward_workspace_bytes(N, D), 16)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    st = _abi.flp_layer_norm_backward(N, D, _X_DTYPES[x.dtype], grad.data_ptr(), x.data_ptr(),
+                                      _X_DTYPES[wd], _ptr(weight), mean, rstd, _ptr(d_x),
+                                      _ptr(d_weight), _ptr(d_bias), _ptr(ws), size, _stream(dev))
     _check("flp_layer_norm_backward", st)
     return d_x, d_weight, d_bias
 
@@ -821,17 +848,18 @@ class LayerNorm(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
-        out, mean, rstd = layer_norm_forward(x, weight, bias, eps)
-        ctx.save_for_backward(x, weight, mean, rstd)
-        ctx.w_dtype = next((t.dtype for t in (weight, bias) if t is not None), None)
+        out, stats = _launch_norm(x, weight, bias, eps, True)
+        ctx.save_for_backward(x, weight, stats)
+        ctx.w_dtype = next((t.dtype for t in (weight, bias) if t is not None), x.dtype)
         return out
 
     @staticmethod
     def backward(ctx, grad):
-        x, weight, mean, rstd = ctx.saved_tensors
+        x, weight, stats = ctx.saved_tensors
         need_x, need_w, need_b, _ = ctx.needs_input_grad
-        dx, dw, db = layer_norm_backward(grad.contiguous(), x, mean, rstd, weight, need_x, need_w,
-                                         need_b, ctx.w_dtype)
+        mean = stats.data_ptr()
+        dx, dw, db = _launch_norm_backward(grad.contiguous(), x, mean, mean + 2 * stats.numel(),
+                                           weight, need_x, need_w, need_b, ctx.w_dtype)
         return dx, dw, db, None
 
 
