@@ -681,8 +681,7 @@ flp_status flp_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype 
   }
   if ((st = check_device()) != FLP_OK) return st;
   const LossFwdLayout L = loss_fwd_layout(N, D, V);
-  float* logp = reinterpret_cast<float*>(at(workspace, L.logp_off));
-  float* lse = out_stats ? out_stats : reinterpret_cast<float*>(at(workspace, L.lse_off));
+  const bool rows = reduction == FLP_REDUCE_NONE;
   FwdArgs f;
   f.hidden = hidden;
   f.weight = weight;
@@ -707,25 +706,25 @@ flp_status flp_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype 
   m.N = N;
   m.V = V;
   m.n_vt = L.fwd.n_vt;
-  m.logp = logp;
-  m.lse = lse;
+  m.logp = nullptr;
+  m.lse = out_stats;
   m.lse_rest = out_stats ? out_stats + N : nullptr;
-  if (launch_merge(m, s) != hipSuccess) return FLP_HIP_ERROR;
-  LossRowsArgs r{};
+  m.zsum = f.zsum;
+  m.zmean = float(1.0 / (double(f.zunit) * double(V)));
+  m.smoothing = float(label_smoothing);
+  m.z_loss = float(z_loss);
+  m.loss = rows ? out_loss : reinterpret_cast<float*>(at(workspace, L.rows_off));
+  if (launch_loss_merge(m, s) != hipSuccess) return FLP_HIP_ERROR;
+  if (rows) return FLP_OK;
+  LossSumArgs r{};
   r.N = N;
   r.V = V;
-  r.n_vt = L.fwd.n_vt;
   r.targets = targets;
   r.t64 = f.t64;
-  r.logp = logp;
-  r.lse = lse;
-  r.zsum = f.zsum;
-  r.zunit = f.zunit;
-  r.terms = LossTerms{label_smoothing, z_loss, int(reduction)};
-  const bool rows = reduction == FLP_REDUCE_NONE;
-  r.rows = rows ? out_loss : reinterpret_cast<float*>(at(workspace, L.rows_off));
-  r.loss = rows ? nullptr : out_loss;
-  if (launch_loss_rows(r, s) != hipSuccess) return FLP_HIP_ERROR;
+  r.rows = m.loss;
+  r.mean = reduction == FLP_REDUCE_MEAN;
+  r.loss = out_loss;
+  if (launch_loss_sum(r, s) != hipSuccess) return FLP_HIP_ERROR;
   return FLP_OK;
 }
 
@@ -762,7 +761,9 @@ flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype
   g.lse_rest = stats + N;
   g.k_slab = L.k_slab;
   g.slab_sums = reinterpret_cast<float*>(at(workspace, L.slab_off));
-  g.terms = LossTerms{label_smoothing, z_loss, int(reduction)};
+  g.smoothing = float(label_smoothing);
+  g.z_loss = float(z_loss);
+  g.reduction = int(reduction);
   g.rescale = x_dtype == FLP_F16;
   g.softmax = reinterpret_cast<float*>(at(workspace, L.softmax_off));
   g.onehot = reinterpret_cast<float*>(at(workspace, L.onehot_off));

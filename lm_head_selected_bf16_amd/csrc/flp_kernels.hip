@@ -783,10 +783,14 @@ __device__ __forceinline__ float merge_term(float2 q, float M) {
   return q.x == -INFINITY ? 0.f : q.y * fast_exp2((q.x - M) * kLog2e);
 }
 
-template <int R, int LL>
+//
+// LOSS (the cross entropy): the tiles' sums of logits (p.zsum, if any) are added over
+// the same leaves and tree, and the row's loss is written instead of logp:
+//   loss = (1 - s) (lse - z_t) + s (lse - mean z) + c lse^2,  0 for an ignored target.
+template <int R, int LL, bool LOSS = false>
 __global__ __launch_bounds__(256) void k_merge(MergeArgs p) {
   constexpr int P = kMergeLeaves / (256 / R);  // leaves per thread
-  __shared__ float sm[4][R], ss[4][R];
+  __shared__ float sm[4][R], ss[4][R], sz[4][R];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int rl = tid % R, c = tid / R;  // row in the workgroup, thread of the row
   const int64_t row = int64_t(blockIdx.x) * R + rl;
@@ -838,12 +842,45 @@ __global__ __launch_bounds__(256) void k_merge(MergeArgs p) {
 #pragma unroll
   for (int k = R; k < 64; k <<= 1) sum += lane_xor(sum, k);
   if (lane < R) ss[wave][rl] = sum;
+  if constexpr (LOSS) {
+    if (p.zsum != nullptr) {  // uniform over the launch
+      float z[P];
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        z[k] = 0.f;
+        for (int64_t v = v0 + k * L; v < v0 + (k + 1) * L; ++v)
+          z[k] += (live && v < v1) ? p.zsum[v * p.N + row] : 0.f;
+      }
+      float zs;
+      if constexpr (P == 8)
+        zs = ((z[0] + z[1]) + (z[2] + z[3])) + ((z[4] + z[5]) + (z[6] + z[7]));
+      else
+        zs = z[0];
+#pragma unroll
+      for (int k = R; k < 64; k <<= 1) zs += lane_xor(zs, k);
+      if (lane < R) sz[wave][rl] = zs;
+    }
+  }
   __syncthreads();
   if (fin) {
     const float S = (ss[0][rl] + ss[1][rl]) + (ss[2][rl] + ss[3][rl]);
     const float ls = logf(S);
     const bool valid = t >= 0 && t < p.V;
-    p.logp[row] = valid ? (zt - M) - ls : 0.0f;
+    if constexpr (LOSS) {
+      float loss = 0.f;
+      if (valid) {
+        const float lse = M + ls;
+        loss = ls - (zt - M);
+        if (p.zsum != nullptr) {
+          const float zs = (sz[0][rl] + sz[1][rl]) + (sz[2][rl] + sz[3][rl]);
+          loss = fmaf(1.0f - p.smoothing, loss, p.smoothing * (lse - zs * p.zmean));
+        }
+        if (p.z_loss != 0.f) loss = fmaf(p.z_loss * lse, lse, loss);
+      }
+      p.loss[row] = loss;
+    } else {
+      p.logp[row] = valid ? (zt - M) - ls : 0.0f;
+    }
     if (p.lse != nullptr) p.lse[row] = M + ls;
     // what that sum's rounding left out (exact: |M| >= |ls| wherever it matters)
     if (p.lse_rest != nullptr) p.lse_rest[row] = ls - ((M + ls) - M);
@@ -1800,27 +1837,31 @@ hipError_t launch_forward(flp_dtype x, const FwdArgs& a, hipStream_t s) {
   return fwd_dispatch<F32>(a, s);
 }
 
-template <int R>
+template <int R, bool LOSS>
 void merge_rows(const MergeArgs& a, hipStream_t s) {
   const dim3 grid(unsigned((a.N + R - 1) / R));
   const int64_t L = (a.n_vt + kMergeLeaves - 1) / kMergeLeaves;
   if (L == 1)
-    hipLaunchKernelGGL((k_merge<R, 1>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_merge<R, 1, LOSS>), grid, dim3(256), 0, s, a);
   else if (L == 2)
-    hipLaunchKernelGGL((k_merge<R, 2>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_merge<R, 2, LOSS>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((k_merge<R, 0>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_merge<R, 0, LOSS>), grid, dim3(256), 0, s, a);
 }
 
-hipError_t launch_merge(const MergeArgs& a, hipStream_t s) {
+template <bool LOSS>
+hipError_t merge_all(const MergeArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_MERGE, s);
   // One row per workgroup while that still gives a few workgroups per compute unit.
   if (a.N <= kMergeRowMax)
-    merge_rows<1>(a, s);
+    merge_rows<1, LOSS>(a, s);
   else
-    merge_rows<8>(a, s);
+    merge_rows<8, LOSS>(a, s);
   return hipGetLastError();
 }
+
+hipError_t launch_merge(const MergeArgs& a, hipStream_t s) { return merge_all<false>(a, s); }
+hipError_t launch_loss_merge(const MergeArgs& a, hipStream_t s) { return merge_all<true>(a, s); }
 
 hipError_t launch_fill(float* dst, int64_t n, float value, hipStream_t s) {
   if (n <= 0) return hipSuccess;

@@ -60,6 +60,11 @@ struct MergeArgs {
   float* logp;
   float* lse;       // may be null
   float* lse_rest = nullptr;  // [N] the part of lse that its rounding lost, may be null
+  // cross entropy (launch_loss_merge, which writes loss and not logp)
+  const float* zsum = nullptr;  // [n_vt][N] sums of logits, or null without smoothing
+  float zmean = 0.f;            // factor of their sum that gives the row's mean
+  float smoothing = 0.f, z_loss = 0.f;
+  float* loss = nullptr;        // [N]
 };
 struct DzArgs {
   const void* hidden;   // chunk start
@@ -124,6 +129,7 @@ struct GemmArgs {
 hipError_t launch_forward(flp_dtype x, const FwdArgs& a, hipStream_t s);
 hipError_t launch_loss_forward(flp_dtype x, const FwdArgs& a, hipStream_t s);
 hipError_t launch_merge(const MergeArgs& a, hipStream_t s);
+hipError_t launch_loss_merge(const MergeArgs& a, hipStream_t s);
 hipError_t launch_fill(float* dst, int64_t n, float value, hipStream_t s);
 hipError_t launch_logits_forward(flp_dtype x, const LogitsArgs& a, hipStream_t s);
 hipError_t launch_logits_backward(flp_dtype x, const LogitsArgs& a, hipStream_t s);
@@ -213,21 +219,13 @@ hipError_t launch_dropout(flp_dtype x_dtype, int64_t n, const void* x, const uin
                           uint32_t drop, float scale, void* out, hipStream_t s);
 
 // Row kernels of the cross entropy (flp_loss.hip).
-struct LossTerms {
-  double smoothing, z_loss;
-  int reduction;             // flp_reduction
-};
-struct LossRowsArgs {        // forward: per-row losses, then their sum or mean
-  int64_t N, V, n_vt;
+struct LossSumArgs {         // forward: the sum or mean of the rows' losses
+  int64_t N, V;
   const void* targets;
   int t64;
-  const float* logp;         // [N]
-  const float* lse;          // [N]
-  const float* zsum;         // [n_vt][N] or null
-  float zunit;
-  LossTerms terms;
-  float* rows;               // [N] per-row losses
-  float* loss;               // [1], or null for no reduction
+  const float* rows;         // [N] per-row losses
+  int mean;
+  float* loss;               // [1]
 };
 struct LossGradArgs {        // backward: the per-row factors of the logit gradient
   int64_t N, V;
@@ -235,7 +233,8 @@ struct LossGradArgs {        // backward: the per-row factors of the logit gradi
   int t64;
   const float* grad_out;     // [N], or [1] for a reduced loss
   const float* lse;          // [N]
-  LossTerms terms;
+  float smoothing, z_loss;
+  int reduction;             // flp_reduction
   int rescale;               // bring the largest factor to [2^10, 2^11) (fp16)
   float* softmax;            // [N] factor of the softmax
   float* onehot;             // [N] term of the target entry
@@ -245,7 +244,7 @@ struct LossGradArgs {        // backward: the per-row factors of the logit gradi
   int64_t k_slab;            // vocabulary slab of d_hidden, 0 for none
   float* slab_sums;          // [slabs][N][D]
 };
-hipError_t launch_loss_rows(const LossRowsArgs& a, hipStream_t s);
+hipError_t launch_loss_sum(const LossSumArgs& a, hipStream_t s);
 hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s);
 
 // Measurement probes (flp_probe.hip); they synchronise the stream.

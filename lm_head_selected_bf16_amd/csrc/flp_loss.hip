@@ -1,7 +1,6 @@
-// Row kernels of the linear cross entropy: what stands between the logit tiles
-// (flp_kernels.hip) and the caller.
+// Row kernels of the linear cross entropy: what stands between the logit tiles and their
+// merge (flp_kernels.hip) and the caller.  The reduced loss is a sum over the rows, and
 //
-//   loss_i = (1 - s) (lse_i - z_it) + s (lse_i - mean_v z_iv) + c lse_i^2      (0 if ignored)
 //   dz_iv  = g_i ((1 + 2 c lse_i) p_iv - (1 - s) [v = t_i] - s / V)
 //
 // with the label smoothing s and the z-loss factor c; g_i is the upstream gradient of
@@ -18,40 +17,6 @@ __device__ __forceinline__ bool counted(const void* t, int t64, int64_t i, int64
   const int64_t v = t64 ? static_cast<const int64_t*>(t)[i]
                         : int64_t(static_cast<const int32_t*>(t)[i]);
   return v >= 0 && v < V;
-}
-
-// 16 rows per workgroup, 16 threads per row: the vocabulary tiles' sums of logits are
-// added tile c, c + 16, ... per thread, then the 16 threads by a fixed tree, so a row's
-// sum does not depend on the batch.
-__global__ __launch_bounds__(256) void k_loss_rows(LossRowsArgs p) {
-  __shared__ float sm[16][17];
-  const int rl = threadIdx.x & 15, c = threadIdx.x >> 4;
-  const int64_t row = int64_t(blockIdx.x) * 16 + rl;
-  float zs = 0.f;
-  if (p.zsum != nullptr) {
-    if (row < p.N)
-      for (int64_t t = c; t < p.n_vt; t += 16) zs += p.zsum[t * p.N + row];
-    sm[c][rl] = zs;
-    __syncthreads();
-#pragma unroll
-    for (int h = 8; h >= 1; h >>= 1) {
-      if (c < h) sm[c][rl] += sm[c + h][rl];
-      __syncthreads();
-    }
-    zs = sm[0][rl];
-  }
-  if (c != 0 || row >= p.N) return;
-  float loss = 0.f;
-  if (counted(p.targets, p.t64, row, p.V)) {
-    const float lse = p.lse[row], s = float(p.terms.smoothing), zl = float(p.terms.z_loss);
-    loss = -p.logp[row];
-    if (p.zsum != nullptr) {
-      const float mean = zs * float(1.0 / (double(p.zunit) * double(p.V)));
-      loss = fmaf(1.0f - s, loss, s * (lse - mean));
-    }
-    if (zl != 0.f) loss = fmaf(zl * lse, lse, loss);
-  }
-  p.rows[row] = loss;
 }
 
 constexpr int kSumThreads = 1024;
@@ -71,7 +36,7 @@ __device__ __forceinline__ T sum_all(T v, T* red) {
 }
 
 // The reduced loss, by one workgroup: a batch has few rows next to what its logits cost.
-__global__ __launch_bounds__(kSumThreads) void k_loss_sum(LossRowsArgs p) {
+__global__ __launch_bounds__(kSumThreads) void k_loss_sum(LossSumArgs p) {
   __shared__ float fred[16];
   __shared__ int64_t ired[16];
   float s = 0.f;
@@ -83,7 +48,7 @@ __global__ __launch_bounds__(kSumThreads) void k_loss_sum(LossRowsArgs p) {
   s = sum_all(s, fred);
   n = sum_all(n, ired);
   if (threadIdx.x == 0)
-    *p.loss = p.terms.reduction == FLP_REDUCE_MEAN ? s / float(n > 0 ? n : 1) : s;
+    *p.loss = p.mean ? s / float(n > 0 ? n : 1) : s;
 }
 
 // Per-row factors of dz, by one workgroup (it counts the rows of a mean, and finds the
@@ -93,21 +58,21 @@ __global__ __launch_bounds__(kSumThreads) void k_loss_sum(LossRowsArgs p) {
 __global__ __launch_bounds__(kSumThreads) void k_loss_grad(LossGradArgs p) {
   __shared__ int64_t ired[16];
   __shared__ float fred[16];
-  const float s = float(p.terms.smoothing), zl = float(p.terms.z_loss);
+  const float s = p.smoothing, zl = p.z_loss;
   float inv = 1.0f;
-  if (p.terms.reduction == FLP_REDUCE_MEAN) {
+  if (p.reduction == FLP_REDUCE_MEAN) {
     int64_t n = 0;
     for (int64_t i = threadIdx.x; i < p.N; i += kSumThreads)
       n += counted(p.targets, p.t64, i, p.V) ? 1 : 0;
     n = sum_all(n, ired);
     inv = 1.0f / float(n > 0 ? n : 1);
   }
-  const float up = p.terms.reduction != FLP_REDUCE_NONE ? p.grad_out[0] * inv : 0.f;
+  const float up = p.reduction != FLP_REDUCE_NONE ? p.grad_out[0] * inv : 0.f;
   const float sv = s / float(p.V);
   float big = 0.f;
   for (int64_t i = threadIdx.x; i < p.N; i += kSumThreads) {
     const bool in = counted(p.targets, p.t64, i, p.V);
-    const float g = !in ? 0.f : p.terms.reduction == FLP_REDUCE_NONE ? p.grad_out[i] : up;
+    const float g = !in ? 0.f : p.reduction == FLP_REDUCE_NONE ? p.grad_out[i] : up;
     const float c = in ? g * fmaf(2.0f * zl, p.lse[i], 1.0f) : 0.f;
     p.softmax[i] = c;
     p.onehot[i] = -g * (1.0f - s);
@@ -141,11 +106,9 @@ __global__ __launch_bounds__(kSumThreads) void k_loss_grad(LossGradArgs p) {
 
 }  // namespace
 
-hipError_t launch_loss_rows(const LossRowsArgs& a, hipStream_t s) {
+hipError_t launch_loss_sum(const LossSumArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_LOSS, s);
-  hipLaunchKernelGGL(k_loss_rows, dim3(unsigned((a.N + 15) / 16)), dim3(256), 0, s, a);
-  if (a.loss != nullptr)
-    hipLaunchKernelGGL(k_loss_sum, dim3(1), dim3(kSumThreads), 0, s, a);
+  hipLaunchKernelGGL(k_loss_sum, dim3(1), dim3(kSumThreads), 0, s, a);
   return hipGetLastError();
 }
 

@@ -570,11 +570,8 @@ flp_status validate_embedding_backward(int64_t N, int64_t D, int64_t V, flp_dtyp
 LossFwdLayout loss_fwd_layout(int64_t N, int64_t D, int64_t V) {
   LossFwdLayout L;
   L.fwd = fwd_layout(N, D, V);
-  const size_t row = align_up(size_t(N) * 4);
-  L.logp_off = L.fwd.total;
-  L.lse_off = L.logp_off + row;
-  L.rows_off = L.lse_off + row;
-  L.zsum_off = L.rows_off + row;
+  L.rows_off = L.fwd.total;
+  L.zsum_off = L.rows_off + align_up(size_t(N) * 4);
   L.total = L.zsum_off + align_up(size_t(L.fwd.n_vt) * size_t(N) * 4);
   return L;
 }

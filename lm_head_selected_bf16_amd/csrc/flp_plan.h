@@ -102,11 +102,11 @@ struct EmbLayout {
 EmbLayout emb_layout(int64_t N, int64_t D, int64_t V);
 
 // ---- linear cross entropy ----
-// Forward: the logp forward's partials, then logp, lse and the row losses [N] and the
-// vocabulary tiles' sums of logits [n_vt][N].
+// Forward: the logp forward's partials, then the row losses [N] and the vocabulary tiles'
+// sums of logits [n_vt][N].
 struct LossFwdLayout {
   FwdLayout fwd;
-  size_t logp_off = 0, lse_off = 0, rows_off = 0, zsum_off = 0, total = 0;
+  size_t rows_off = 0, zsum_off = 0, total = 0;
 };
 LossFwdLayout loss_fwd_layout(int64_t N, int64_t D, int64_t V);
 // Factor of the summed logits: the largest power of two that is at most 1 / V.
