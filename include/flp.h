@@ -487,7 +487,7 @@ flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype
  *   mean_i = sum_d x_id / D,   rstd_i = 1 / sqrt(sum_d (x_id - mean_i)^2 / D + eps)
  *   out    = (x - mean) rstd weight + bias
  *
- *   x, out    [N, D] x_dtype (FLP_BF16, FLP_F16 or FLP_F32).  Any D >= 1 (below 2^28):
+ *   x, out    [N, D] x_dtype (FLP_BF16, FLP_F16 or FLP_F32).  Any D >= 1 (below 2^27):
  *             rows need no alignment beyond their element size.
  *   weight, bias  [D] of w_dtype (x_dtype or FLP_F32), each may be NULL (1 and 0).
  *   eps       >= 0, finite.  A constant row with eps = 0 has no norm (NaN).

@@ -28,6 +28,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "flp_launch.h"
@@ -278,8 +279,7 @@ __device__ __forceinline__ void store_chunk(const float* sum, float scale, void*
 // (= ascending token) order.  A run that is its id's whole segment is written to
 // d_W at once; a run that starts at the group's first position goes to the
 // group's head slot, any other run that reaches past the group to its tail slot
-// (a group holds at most one of each).  Thread t owns one 16-byte chunk of a row:
-// chunk kColThreads blockIdx.y + t.
+// (a group holds at most one of each).  Each thread owns one 16-byte chunk of a row.
 constexpr int kSegGroup = int(kEmbSegGroup);
 
 template <int XS, bool OUT_F32>
@@ -337,8 +337,8 @@ __global__ __launch_bounds__(kColThreads) void k_embed_runs(const u32x4* __restr
   // summed positions: the prefix of the group with ids in [0, V) (dropped ids sort last)
   int m = 0;
   while (m < n && int64_t(skey[m]) < V) ++m;
-  const int64_t c = int64_t(blockIdx.y) * kColThreads + threadIdx.x;
-  if (c < row_vec) {
+  for (int64_t c = int64_t(blockIdx.y) * kColThreads + threadIdx.x; c < row_vec;
+       c += int64_t(gridDim.y) * kColThreads) {
     // every row of the group in flight at once, then the runs in order
     u32x4 x4[kSegGroup];
 #pragma unroll
@@ -406,8 +406,8 @@ __global__ __launch_bounds__(kColThreads) void k_embed_rows(const uint32_t* __re
     __syncthreads();
   }
   const float* first = from_start ? head : tail;
-  const int64_t c = int64_t(blockIdx.y) * kColThreads + t;
-  if (c < row_vec) {
+  for (int64_t c = int64_t(blockIdx.y) * kColThreads + t; c < row_vec;
+       c += int64_t(gridDim.y) * kColThreads) {
     float acc[EPC];
     const float* f = first + (g0 * row_vec + c) * EPC;
 #pragma unroll
@@ -491,7 +491,7 @@ hipError_t launch_embedding_backward(const EmbedBwdArgs& a, hipStream_t s) {
   const int fin = passes & 1;
   const int64_t row_vec = a.D * int64_t(dtype_size(a.x)) / 16;
   const dim3 groups(unsigned((N + kSegGroup - 1) / kSegGroup),
-                    unsigned((row_vec + kColThreads - 1) / kColThreads));
+                    unsigned(std::min<int64_t>((row_vec + kColThreads - 1) / kColThreads, 65535)));
   const int f16 = a.x == FLP_F16 ? 1 : 0;
   const u32x4* g = static_cast<const u32x4*>(a.grad);
   auto sums = [&](auto runs, auto rows) {

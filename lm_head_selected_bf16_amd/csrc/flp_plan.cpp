@@ -692,8 +692,9 @@ flp_status check_norm_dims(int64_t N, int64_t D, flp_dtype x, flp_dtype w) {
   if (N < 0 || D < 1) return FLP_INVALID_ARGUMENT;
   if (x != FLP_BF16 && x != FLP_F16 && x != FLP_F32) return FLP_UNSUPPORTED_DTYPE;
   if (w != x && w != FLP_F32) return FLP_UNSUPPORTED_DTYPE;
-  // the column kernels take 16 columns per 256-thread workgroup of a launch
-  if (D >= (int64_t(1) << 28) || !mul_ok(std::max<int64_t>(N, 1), D)) return FLP_UNSUPPORTED_SHAPE;
+  // the column kernels take 16 columns per 256-thread workgroup, and a launch holds fewer
+  // than 2^32 threads
+  if (D >= (int64_t(1) << 27) || !mul_ok(std::max<int64_t>(N, 1), D)) return FLP_UNSUPPORTED_SHAPE;
   return FLP_OK;
 }
 

@@ -20,6 +20,7 @@ import math
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _abi
 from ._abi import FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpError
@@ -659,6 +660,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         hidden, weight, targets, bias, stats = ctx.saved_tensors
         need_h, need_w, _, need_b = ctx.needs_input_grad[:4]
@@ -729,6 +731,7 @@ class Dropout(torch.autograd.Function):
         return dropout_forward(x, p, rng)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         (rng,) = ctx.saved_tensors
         if not ctx.needs_input_grad[0]:
@@ -854,6 +857,7 @@ class LayerNorm(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         x, weight, stats = ctx.saved_tensors
         need_x, need_w, need_b, _ = ctx.needs_input_grad

@@ -132,7 +132,8 @@ def compare(h, w, b, t, up, s=0.0, c=0.0, reduction="mean", **kw):
 
 
 SHAPES = [(1, 32, 1), (1, 64, 255), (3, 32, 256), (33, 96, 257), (64, 256, 4096), (65, 160, 1000),
-          (130, 96, 2049), (300, 64, 777), (600, 224, 5003)]
+          (130, 96, 2049), (300, 64, 777), (600, 224, 5003),
+          (5, 32, 70001), (9, 32, 140001), (2100, 32, 70001)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
@@ -384,6 +385,37 @@ def test_graph_replays_with_new_inputs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, step())), rep
+
+
+def test_second_derivatives_are_refused():
+    m = flp()
+    h, w, b, t, up = make(8, 64, 100, F32, 21)
+    h.requires_grad_(True)
+    # with a constant upstream gradient the first derivative is a constant to autograd
+    (g,) = torch.autograd.grad(m.linear_cross_entropy(h, w, t, b), [h], create_graph=True)
+    with pytest.raises(RuntimeError, match="does not require grad"):
+        g.sum().backward()
+    one = torch.ones((), device="cuda", requires_grad=True)
+    (g,) = torch.autograd.grad(m.linear_cross_entropy(h, w, t, b), [h], one, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
+def test_two_streams_at_once():
+    """Two batches on two streams, each with its own workspaces, give what they give alone."""
+    m = flp()
+    batches = [make(300, 64, 3000, BF16, 40 + k) for k in range(2)]
+    want = [run(*b, 0.1, 1e-3, "mean") for b in batches]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    for _ in range(3):
+        got = []
+        for b, s in zip(batches, streams):
+            with torch.cuda.stream(s):
+                got.append(run(*b, 0.1, 1e-3, "mean"))
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(x, y))
 
 
 def test_refusals():

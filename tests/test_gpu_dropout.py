@@ -143,6 +143,15 @@ def test_graph_draws_a_new_mask_per_replay():
         assert torch.equal(y, m.dropout_forward(x, 0.3, rng_tensor(5, step)))
 
 
+def test_second_derivatives_are_refused():
+    m = flp()
+    x = torch.randn(64, device="cuda", requires_grad=True)
+    y = m.dropout(x, 0.5, rng_tensor(1, 1))
+    (g,) = torch.autograd.grad(y, [x], torch.ones_like(y, requires_grad=True), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
 def test_empty_and_refusals():
     m = flp()
     rng = rng_tensor(0, 0)
