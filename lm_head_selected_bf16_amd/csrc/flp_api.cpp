@@ -929,7 +929,7 @@ const char* flp_status_string(flp_status status) {
 
 const char* flp_build_info(void) {
   static const std::string info = [] {
-    char buf[1024];
+    char buf[2048];
     std::snprintf(buf, sizeof(buf),
                   "flp 0.2 gfx950 fallback=none vocab_tile=%lld row_quantum=%lld git=%s | %s",
                   (long long)kVocabTile, (long long)kRowQuantum,

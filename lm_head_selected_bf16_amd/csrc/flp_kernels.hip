@@ -1957,13 +1957,17 @@ const char* kernel_ids() {
   return "engine: direct global->LDS (buffer_load_dwordx4 lds, whole lines), 2 LDS stages x 128 B of K "
          "(3-8 for the small dX tiles), "
          "mfma_f32_16x16x32_bf16 | 16x16x32_f16 | 16x16x4f32; k_fwd<BM 32/64/128 x BN 256 2x2 waves (BM 32: 4 stages over <= 256 vocabulary tiles), "
-         "BM 256 4x2 waves>; k_merge<1 or 8 rows; 256 leaves, fixed tree>; k_dz<BM 256 x BN 256, 4x2 waves>; "
+         "BM 256 4x2 waves>; k_merge<1 or 8 rows; 256 leaves, fixed tree>; k_dz<BM 256 x BN 256, 4x2 waves; fp32 <= 128 rows: BM 64, 128>; "
          "k_gemm dX, dW<256x224, 4x2 waves, K-blocked operands; dX for <= 1024 rows: 64x16, "
          "64x32, 128x64, 128x128>; k_transpose (K-blocked); "
          "k_dbias_fold; k_fill; k_logits_fwd, k_logits_bwd<one wave per row>; "
          "rows: k_mark, k_compact, k_gather, k_scatter_rows, k_scatter_hidden; "
-         "embedding: k_embed_fwd, radix sort (k_sort_init, k_sort_hist, k_sort_scatter; zero-row "
-         "riders), k_seg_bounds, k_embed_runs<32-position groups>, k_embed_rows";
+         "cross entropy: k_fwd, k_merge, k_dz with loss terms, k_loss_sum, k_loss_grad, k_gemm dX "
+         "over vocabulary slabs and k_slab_fold (<= 1024 rows); "
+         "embedding: k_embed_fwd (scaled), radix sort (k_sort_hist, k_sort_scatter; 9-bit digits, "
+         "zero riders), k_embed_runs<32-position groups>, k_embed_rows; k_dropout; layer norm: "
+         "k_norm_fwd_row, k_norm_bwd_row<one or four waves per row>, k_norm_fold; wide rows: "
+         "k_norm_fwd, k_norm_dx, k_norm_params";
 }
 
 }  // namespace flp

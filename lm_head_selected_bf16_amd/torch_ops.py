@@ -629,10 +629,10 @@ def cross_entropy_backward(grad_out: torch.Tensor, stats: torch.Tensor, hidden: 
         need_bias = bias is not None
     xd = _X_DTYPES[hidden.dtype]
     if workspace_bytes is None:
-        full, least = (_abi.flp_cross_entropy_backward_workspace_bytes(N, D, V, xd, c)
-                       for c in (max(N, 1), 0))
-        workspace_bytes = full if full <= DEFAULT_BWD_WORKSPACE else max(least,
-                                                                         DEFAULT_BWD_WORKSPACE)
+        workspace_bytes = _abi.flp_cross_entropy_backward_workspace_bytes(N, D, V, xd, max(N, 1))
+        if workspace_bytes > DEFAULT_BWD_WORKSPACE:
+            least = _abi.flp_cross_entropy_backward_workspace_bytes(N, D, V, xd, 0)
+            workspace_bytes = max(least, DEFAULT_BWD_WORKSPACE)
     with _on(dev):
         d_hidden = torch.empty_like(hidden) if need_hidden else None
         d_weight = torch.empty_like(weight) if need_weight else None
