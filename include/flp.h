@@ -466,7 +466,7 @@ flp_status flp_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype 
  * 2^10, taken back when the fp32 sums are rounded: small gradients (a mean over many
  * rows) do not underflow on the way.
  *
- * Batches of up to 1024 rows sum d_hidden over slabs of the vocabulary, larger ones in
+ * Batches of up to 8192 rows sum d_hidden over slabs of the vocabulary, larger ones in
  * one walk: a row's d_hidden is bitwise the same among batches of one kind, and differs
  * between the two by the order of that fp32 sum.
  */
@@ -480,6 +480,38 @@ flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype
                                       flp_reduction reduction, void* d_hidden, void* d_weight,
                                       float* d_bias, void* workspace, size_t workspace_bytes,
                                       void* stream);
+
+/*
+ * Loss and gradients of a training step in one call, for an upstream gradient of 1
+ * (reduction FLP_REDUCE_SUM or FLP_REDUCE_MEAN; FLP_BF16 or FLP_F32).  Row chunk by row
+ * chunk, the forward leaves its fp32 logits in the workspace and dz is made from them
+ * instead of from a second product, so a step takes three products of the size of the
+ * logits where forward and backward calls take four.  out_loss, out_stats and the
+ * gradients have the bits of those two calls with grad_out = 1.
+ *
+ *   out_loss   [1].  out_stats [2, N] or NULL.  d_hidden, d_weight, d_bias as for
+ *              flp_cross_entropy_backward, each may be NULL.
+ *   workspace  >= flp_cross_entropy_gradients_workspace_bytes(N, D, V, x_dtype, 0);
+ *              chunk_rows as for flp_backward_workspace_bytes.  A chunk of all rows takes
+ *              about 8 (FLP_BF16) or 12 (FLP_F32) bytes per logit.
+ *   N = 0 writes zeros to out_loss, d_weight and d_bias.
+ */
+size_t flp_cross_entropy_gradients_workspace_bytes(int64_t N, int64_t D, int64_t V,
+                                                   flp_dtype x_dtype, int64_t chunk_rows);
+flp_status flp_cross_entropy_gradients(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                       const void* hidden, const void* weight, const float* bias,
+                                       const void* targets, flp_dtype t_dtype,
+                                       double label_smoothing, double z_loss,
+                                       flp_reduction reduction, float* out_loss, float* out_stats,
+                                       void* d_hidden, void* d_weight, float* d_bias,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+/*
+ * x[e] *= *factor in place (one rounding), for gradients made with an upstream gradient
+ * of 1.  x: [n] x_dtype, aligned to its element size; factor: one float32 on the device.
+ * A factor of exactly 1 leaves x alone and costs a launch.
+ */
+flp_status flp_scale_inplace(int64_t n, flp_dtype x_dtype, void* x, const float* factor,
+                             void* stream);
 
 /*
  * Layer norm of the rows x[i, :], as it stands in front of the head:

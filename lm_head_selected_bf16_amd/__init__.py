@@ -22,7 +22,8 @@ from ._abi import (FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpErro
                    flp_embedding_scaled_backward, flp_embedding_scaled_forward, flp_forward,
                    FLP_REDUCE_MEAN, FLP_REDUCE_NONE, FLP_REDUCE_SUM, flp_cross_entropy_backward,
                    flp_cross_entropy_backward_workspace_bytes, flp_cross_entropy_forward,
-                   flp_cross_entropy_forward_workspace_bytes,
+                   flp_cross_entropy_forward_workspace_bytes, flp_cross_entropy_gradients,
+                   flp_cross_entropy_gradients_workspace_bytes, flp_scale_inplace,
                    flp_dropout, flp_layer_norm_backward, flp_layer_norm_backward_workspace_bytes,
                    flp_layer_norm_forward,
                    flp_forward_indexed, flp_forward_noalloc, FLP_FORWARD_NOALLOC_MAX_BYTES,
@@ -40,6 +41,7 @@ from .torch_ops import (LinearLogp, backward, backward_workspace_bytes,  # noqa:
                         logits_backward_indexed, logits_forward_indexed, logits_logp_indexed,
                         Embedding, embedding, embedding_backward, embedding_forward,
                         LinearCrossEntropy, cross_entropy_backward, cross_entropy_forward,
+                        cross_entropy_gradients,
                         linear_cross_entropy,
                         Dropout, dropout, dropout_forward, LayerNorm, layer_norm,
                         layer_norm_backward, layer_norm_forward)
@@ -69,6 +71,8 @@ __all__ = [
     "LinearCrossEntropy", "linear_cross_entropy", "cross_entropy_forward",
     "cross_entropy_backward", "flp_cross_entropy_forward", "flp_cross_entropy_backward",
     "flp_cross_entropy_forward_workspace_bytes", "flp_cross_entropy_backward_workspace_bytes",
+    "cross_entropy_gradients", "flp_cross_entropy_gradients",
+    "flp_cross_entropy_gradients_workspace_bytes", "flp_scale_inplace",
     "FLP_REDUCE_NONE", "FLP_REDUCE_SUM", "FLP_REDUCE_MEAN",
     "Dropout", "dropout", "dropout_forward", "flp_dropout",
     "LayerNorm", "layer_norm", "layer_norm_forward", "layer_norm_backward",

@@ -74,6 +74,11 @@ SIGNATURES = {
     "flp_cross_entropy_backward": (_int, [_i64, _i64, _i64, _int, _fp, _fp, _vp, _vp, _fp, _vp,
                                           _int, _double, _double, _int, _vp, _vp, _fp, _vp, _sz,
                                           _vp]),
+    "flp_cross_entropy_gradients_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _i64]),
+    "flp_cross_entropy_gradients": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _fp, _vp, _int,
+                                           _double, _double, _int, _fp, _fp, _vp, _vp, _fp, _vp,
+                                           _sz, _vp]),
+    "flp_scale_inplace": (_int, [_i64, _int, _vp, _fp, _vp]),
     "flp_dropout": (_int, [_i64, _int, _vp, _double, _vp, _vp, _vp]),
     "flp_layer_norm_forward": (_int, [_i64, _i64, _int, _vp, _int, _vp, _vp, _double, _vp, _fp, _fp,
                                       _vp]),
@@ -310,6 +315,26 @@ def flp_cross_entropy_backward(N, D, V, x_dtype, grad_out, stats, hidden, weight
                                                  bias, targets, t_dtype, label_smoothing, z_loss,
                                                  reduction, d_hidden, d_weight, d_bias, workspace,
                                                  workspace_bytes, stream))
+
+
+def flp_cross_entropy_gradients_workspace_bytes(N: int, D: int, V: int, x_dtype: int,
+                                                chunk_rows: int = 0) -> int:
+    return int(load().flp_cross_entropy_gradients_workspace_bytes(N, D, V, x_dtype, chunk_rows))
+
+
+def flp_cross_entropy_gradients(N, D, V, x_dtype, hidden, weight, bias, targets, t_dtype,
+                                label_smoothing, z_loss, reduction, out_loss, out_stats, d_hidden,
+                                d_weight, d_bias, workspace, workspace_bytes, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_cross_entropy_gradients(N, D, V, x_dtype, hidden, weight, bias, targets,
+                                                  t_dtype, label_smoothing, z_loss, reduction,
+                                                  out_loss, out_stats, d_hidden, d_weight, d_bias,
+                                                  workspace, workspace_bytes, stream))
+
+
+def flp_scale_inplace(n, x_dtype, x, factor, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_scale_inplace(n, x_dtype, x, factor, stream))
 
 
 def flp_dropout(n, x_dtype, x, p, rng, out, stream) -> int:

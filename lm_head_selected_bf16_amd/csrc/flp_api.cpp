@@ -2,6 +2,7 @@
 // kernels on the caller's stream.  Fail closed: no fallback path exists.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -50,18 +51,18 @@ flp_status zero_sums(void* d_weight, size_t dw_bytes, float* d_bias, int64_t V, 
   return FLP_OK;
 }
 
-// The chunk loop of a validated, non-empty backward.  With `loss`, dz takes the cross
-// entropy's form: grad_out holds the softmax's factors and *loss the other terms, both
-// written by launch_loss_grad.
-flp_status enqueue_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+// The chunk loop of a validated, non-empty backward, with its buffers at `workspace` as
+// L lays them out.  With `loss`, dz takes the cross entropy's form: grad_out holds the
+// softmax's factors and *loss the other terms, both written by launch_loss_grad.
+// before(first row, rows) is called in front of each chunk's kernels; logits: the
+// chunk's products that it leaves, or null.
+template <class Before>
+flp_status enqueue_backward(const BwdLayout& L, int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
                             const float* grad_out, const float* lse, const void* hidden,
                             const void* weight, const float* bias, const void* targets,
                             flp_dtype t_dtype, const float* temperature, const LossGradArgs* loss,
                             void* d_hidden, void* d_weight, flp_dtype dw_dtype, float* d_bias,
-                            void* workspace, size_t workspace_bytes, hipStream_t s) {
-  const BwdLayout L = bwd_layout_for_bytes(N, D, V, x_dtype, dw_dtype, workspace_bytes,
-                                           d_hidden != nullptr, d_weight != nullptr,
-                                           d_bias != nullptr);
+                            void* workspace, hipStream_t s, float* logits, Before before) {
   const size_t xs = dtype_size(x_dtype);
   const size_t ts = dtype_size(t_dtype);
   void* dz = d_hidden ? at(workspace, L.dz_off) : nullptr;
@@ -82,7 +83,10 @@ flp_status enqueue_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
     const int64_t rows = (N - r0 < L.chunk) ? N - r0 : L.chunk;
     const bool last = c + 1 == L.n_chunks;
     const void* h_chunk = static_cast<const char*>(hidden) + size_t(r0) * D * xs;
+    const flp_status st = before(r0, rows);
+    if (st != FLP_OK) return st;
     DzArgs z;
+    z.logits = logits;
     z.hidden = h_chunk;
     z.weight = weight;
     z.bias = bias;
@@ -166,6 +170,8 @@ flp_status enqueue_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
   }
   return FLP_OK;
 }
+
+flp_status nothing_before(int64_t, int64_t) { return FLP_OK; }
 
 // ---- optional per-kernel event timing ----
 struct ProfRec {
@@ -402,9 +408,12 @@ flp_status flp_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
   if (N == 0) return zero_sums(d_weight, size_t(V) * D * dtype_size(dw_dtype), d_bias, V, s);
   if (!d_hidden && !d_weight && !d_bias) return FLP_OK;
   if ((st = check_device()) != FLP_OK) return st;
-  return enqueue_backward(N, D, V, x_dtype, grad_out, lse, hidden, weight, bias, targets, t_dtype,
-                          temperature, nullptr, d_hidden, d_weight, dw_dtype, d_bias, workspace,
-                          workspace_bytes, s);
+  const BwdLayout L = bwd_layout_for_bytes(N, D, V, x_dtype, dw_dtype, workspace_bytes,
+                                           d_hidden != nullptr, d_weight != nullptr,
+                                           d_bias != nullptr);
+  return enqueue_backward(L, N, D, V, x_dtype, grad_out, lse, hidden, weight, bias, targets,
+                          t_dtype, temperature, nullptr, d_hidden, d_weight, dw_dtype, d_bias,
+                          workspace, s, nullptr, nothing_before);
 }
 
 // ---- indexed (row-subset) variants ----
@@ -770,9 +779,139 @@ flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype
   g.uniform = reinterpret_cast<float*>(at(workspace, L.uniform_off));
   g.unscale = reinterpret_cast<float*>(at(workspace, L.unscale_off));
   if (launch_loss_grad(g, s) != hipSuccess) return FLP_HIP_ERROR;
-  return enqueue_backward(N, D, V, x_dtype, g.softmax, stats, hidden, weight, bias, targets, t_dtype,
-                          nullptr, &g, d_hidden, d_weight, x_dtype, d_bias,
-                          at(workspace, L.total), workspace_bytes - L.total, s);
+  const BwdLayout B = bwd_layout_for_bytes(N, D, V, x_dtype, x_dtype, workspace_bytes - L.total,
+                                           d_hidden != nullptr, d_weight != nullptr,
+                                           d_bias != nullptr);
+  return enqueue_backward(B, N, D, V, x_dtype, g.softmax, stats, hidden, weight, bias, targets,
+                          t_dtype, nullptr, &g, d_hidden, d_weight, x_dtype, d_bias,
+                          at(workspace, L.total), s, nullptr, nothing_before);
+}
+
+size_t flp_cross_entropy_gradients_workspace_bytes(int64_t N, int64_t D, int64_t V,
+                                                   flp_dtype x_dtype, int64_t chunk_rows) {
+  if (N < 1 || D < 1 || V < 1 || chunk_rows < 0) return 0;
+  if (x_dtype != FLP_BF16 && x_dtype != FLP_F32) return 0;
+  if (chunk_rows > 0) return loss_all_layout(N, D, V, x_dtype, chunk_rows, true, true, true).total;
+  return std::min(loss_all_layout(N, D, V, x_dtype, kRowQuantum, true, true, true).total,
+                  loss_all_layout(N, D, V, x_dtype, N, true, true, true).total);
+}
+
+flp_status flp_cross_entropy_gradients(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                       const void* hidden, const void* weight, const float* bias,
+                                       const void* targets, flp_dtype t_dtype,
+                                       double label_smoothing, double z_loss,
+                                       flp_reduction reduction, float* out_loss, float* out_stats,
+                                       void* d_hidden, void* d_weight, float* d_bias,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  flp_status st = validate_cross_entropy_gradients(
+      N, D, V, x_dtype, hidden, weight, bias, targets, t_dtype, label_smoothing, z_loss, reduction,
+      out_loss, out_stats, d_hidden, d_weight, d_bias, workspace, workspace_bytes);
+  if (st != FLP_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((st = check_device()) != FLP_OK) return st;
+  if (N == 0) {
+    if (launch_fill(out_loss, 1, 0.0f, s) != hipSuccess) return FLP_HIP_ERROR;
+    return zero_sums(d_weight, size_t(V) * D * dtype_size(x_dtype), d_bias, V, s);
+  }
+  const LossAllLayout L = loss_all_layout_for_bytes(N, D, V, x_dtype, workspace_bytes,
+                                                    d_hidden != nullptr, d_weight != nullptr,
+                                                    d_bias != nullptr);
+  const bool t64 = t_dtype == FLP_I64;
+  const size_t xs = dtype_size(x_dtype), ts = dtype_size(t_dtype);
+  auto buf = [&](size_t off) { return reinterpret_cast<float*>(at(workspace, off)); };
+  float* rows_loss = buf(L.rows_off);
+  float* inv = nullptr;
+  if (reduction == FLP_REDUCE_MEAN) {
+    inv = buf(L.inv_off);
+    if (launch_loss_count(N, V, targets, t64, inv, s) != hipSuccess) return FLP_HIP_ERROR;
+  }
+  LossGradArgs g{};
+  g.V = V;
+  g.t64 = t64;
+  g.inv = inv;
+  g.smoothing = float(label_smoothing);
+  g.z_loss = float(z_loss);
+  g.reduction = int(reduction);
+  g.unscale = buf(L.grad.unscale_off);
+  g.k_slab = L.grad.k_slab;
+  g.slab_sums = buf(L.grad.slab_off);
+  // enqueue_backward takes these from the batch's first row on
+  g.softmax = buf(L.grad.softmax_off);
+  g.onehot = buf(L.grad.onehot_off);
+  g.uniform = buf(L.grad.uniform_off);
+  g.lse = out_stats ? out_stats : buf(L.lse_off);
+  g.lse_rest = g.lse + N;
+  const LossGradArgs all = g;
+  // A chunk's forward: its products stay for the dlogits kernel, which therefore is no
+  // second matrix product.
+  auto forward = [&](int64_t r0, int64_t rows) {
+    FwdArgs f;
+    f.hidden = static_cast<const char*>(hidden) + size_t(r0) * D * xs;
+    f.weight = weight;
+    f.bias = bias;
+    f.targets = static_cast<const char*>(targets) + size_t(r0) * ts;
+    f.t64 = t64;
+    f.temperature = nullptr;
+    f.N = rows;
+    f.D = D;
+    f.V = V;
+    f.t_off = 0;
+    f.part = reinterpret_cast<float2*>(at(workspace, L.part_off));
+    f.zt = buf(L.zt_off);
+    f.zsum = label_smoothing != 0.0 ? buf(L.zsum_off) : nullptr;
+    f.zunit = loss_zunit(V);
+    f.logits = buf(L.logits_off);
+    if (launch_loss_forward(x_dtype, f, s) != hipSuccess) return FLP_HIP_ERROR;
+    MergeArgs m;
+    m.part = f.part;
+    m.zt = f.zt;
+    m.targets = f.targets;
+    m.t64 = t64;
+    m.N = rows;
+    m.V = V;
+    m.n_vt = ceil_div(V, kVocabTile);
+    m.logp = nullptr;
+    m.lse = const_cast<float*>(all.lse) + r0;
+    m.lse_rest = const_cast<float*>(all.lse_rest) + r0;
+    m.zsum = f.zsum;
+    m.zmean = float(1.0 / (double(f.zunit) * double(V)));
+    m.smoothing = float(label_smoothing);
+    m.z_loss = float(z_loss);
+    m.loss = rows_loss + r0;
+    if (launch_loss_merge(m, s) != hipSuccess) return FLP_HIP_ERROR;
+    LossGradArgs c = all;
+    c.N = rows;
+    c.targets = f.targets;
+    c.lse = m.lse;
+    c.softmax += r0;
+    c.onehot += r0;
+    c.uniform += r0;
+    return launch_loss_grad(c, s) == hipSuccess ? FLP_OK : FLP_HIP_ERROR;
+  };
+  st = enqueue_backward(L.bwd, N, D, V, x_dtype, all.softmax, all.lse, hidden, weight, bias,
+                        targets, t_dtype, nullptr, &all, d_hidden, d_weight, x_dtype, d_bias,
+                        at(workspace, L.bwd_off), s, buf(L.logits_off), forward);
+  if (st != FLP_OK) return st;
+  LossSumArgs r{};
+  r.N = N;
+  r.V = V;
+  r.targets = targets;
+  r.t64 = t64;
+  r.rows = rows_loss;
+  r.mean = reduction == FLP_REDUCE_MEAN;
+  r.loss = out_loss;
+  if (launch_loss_sum(r, s) != hipSuccess) return FLP_HIP_ERROR;
+  return FLP_OK;
+}
+
+flp_status flp_scale_inplace(int64_t n, flp_dtype x_dtype, void* x, const float* factor,
+                             void* stream) {
+  flp_status st = validate_scale_inplace(n, x_dtype, x, factor);
+  if (st != FLP_OK || n == 0) return st;
+  if ((st = check_device()) != FLP_OK) return st;
+  if (launch_scale(x_dtype, n, x, factor, static_cast<hipStream_t>(stream)) != hipSuccess)
+    return FLP_HIP_ERROR;
+  return FLP_OK;
 }
 
 // ---- layer norm ----

@@ -588,6 +588,14 @@ struct Engine {
 template <class E, int BM, int WM, int NS = 2>
 using LogitEngine = Engine<E, BM, kTileCols, WM, 2, NS>;
 
+// Where a wave's accumulators of a logit tile are kept: every store and load is one
+// contiguous KB, and the tile comes back to the lanes it left.
+template <int WMB, int WNB>
+__device__ __forceinline__ f32x4_t* kept_tile(float* logits, int64_t tile, int waves, int wave,
+                                              int lane) {
+  return reinterpret_cast<f32x4_t*>(logits) + ((tile * waves + wave) * (WMB * WNB)) * 64 + lane;
+}
+
 // The fixed per-row tree over the 32 values one lane holds of a wave's 128 columns.
 template <int WNB>
 __device__ __forceinline__ float lane_sum(const float (&e)[WNB][4]) {
@@ -602,7 +610,13 @@ __device__ __forceinline__ float lane_sum(const float (&e)[WNB][4]) {
 // per row (times p.zunit, a power of two at most 1 / V, so that columns masked with the
 // lowest fp32 value cannot overflow it), and is safe for tiles and rows masked with such
 // values (kHugeLogit).
-template <class E, int BM, int WM, bool ODD, int NS = 2, bool LOSS = false>
+// SAVE keeps the products h W^T of the tile in p.logits, in the order of the lanes'
+// accumulators (kept_tile), for the dlogits kernel of the same row chunk.  16384 x 2688 x
+// 131072 bf16 on MI355X: this kernel 8.7 -> 9.8 ms, k_dz 9.4 -> 3.1 ms (17.2 GB read and
+// written, 5.5 TB/s).  It pays where the product costs more than 8 bytes per logit: from
+// D of about 1024 on in bf16 (4096 x 1024 x 50257: 2112 and 2104 us a step), in fp32 from
+// about 100 on.
+template <class E, int BM, int WM, bool ODD, int NS = 2, bool LOSS = false, bool SAVE = false>
 __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
   using Eng = LogitEngine<E, BM, WM, NS>;
   constexpr int RW = Eng::RW, WMB = Eng::WMB, WNB = Eng::WNB, NT = Eng::NT;
@@ -625,6 +639,14 @@ __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
   Eng::template run<ODD>(acc, reinterpret_cast<const char*>(p.hidden) + row0 * kbytes, kbytes, p.N - row0,
            reinterpret_cast<const char*>(p.weight) + col0 * kbytes, kbytes, p.V - col0, kbytes,
            smem);
+  if constexpr (SAVE) {
+    f32x4_t* keep = kept_tile<WMB, WNB>(p.logits, int64_t(tm) * nbn + tn, 2 * WM, wave, lane);
+#pragma unroll
+    for (int mb = 0; mb < WMB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < WNB; ++nb)
+        __builtin_nontemporal_store(acc[mb][nb], keep + (mb * WNB + nb) * 64);
+  }
   // Waves still reading their last fragments after the last stage barrier may read
   // either buffer (buffer 0 when the stage count is odd): LDS is reused below.
   __syncthreads();
@@ -1069,7 +1091,9 @@ __global__ __launch_bounds__(256) void k_logits_bwd(LogitsArgs p) {
 
 // LOSS (the cross entropy's backward): dz = c p + onehot o + u with the per-row factors
 // p.grad_out (c), p.onehot (o) and p.uniform (u); no temperature.
-template <class E, int BM, int WM, bool ODD, bool LOSS = false>
+// KEPT: the tile's products come from p.logits, where the chunk's forward left them, and
+// are not recomputed; everything after them is the same code, so dz has the same bits.
+template <class E, int BM, int WM, bool ODD, bool LOSS = false, bool KEPT = false>
 __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
   using Eng = LogitEngine<E, BM, WM>;
   constexpr int RW = Eng::RW, WMB = Eng::WMB, WNB = Eng::WNB, NT = Eng::NT;
@@ -1092,9 +1116,18 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
   for (int mb = 0; mb < WMB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < WNB; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  Eng::template run<ODD>(acc, reinterpret_cast<const char*>(p.hidden) + row0 * kbytes, kbytes, p.rows - row0,
-           reinterpret_cast<const char*>(p.weight) + col0 * kbytes, kbytes, p.V - col0, kbytes,
-           smem);
+  if constexpr (KEPT) {
+    const f32x4_t* keep = kept_tile<WMB, WNB>(p.logits, int64_t(tm) * nbn + tn, 2 * WM, wave, lane);
+#pragma unroll
+    for (int mb = 0; mb < WMB; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < WNB; ++nb)
+        acc[mb][nb] = __builtin_nontemporal_load(keep + (mb * WNB + nb) * 64);
+  } else {
+    Eng::template run<ODD>(acc, reinterpret_cast<const char*>(p.hidden) + row0 * kbytes, kbytes,
+                           p.rows - row0, reinterpret_cast<const char*>(p.weight) + col0 * kbytes,
+                           kbytes, p.V - col0, kbytes, smem);
+  }
 
   const int64_t cw = col0 + wn * kHalfCols;
   // Columns of this wave at or past lim are vocabulary padding (lim < 128 only in
@@ -1627,6 +1660,28 @@ hipError_t fwd_cfg(const FwdArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The loss's forward over 256-row tiles that keeps the products.
+template <class E, bool ODD>
+hipError_t fwd_keep(const FwdArgs& a, hipStream_t s) {
+  using Eng = LogitEngine<E, int(kDzRowTile), 4, 2>;
+  static std::atomic<int> ready[kMaxDevices];
+  const hipError_t e = prepare(k_fwd<E, int(kDzRowTile), 4, ODD, 2, true, true>, Eng::kLds, ready);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = ((a.N + kDzRowTile - 1) / kDzRowTile) * ((a.V + kTileCols - 1) / kTileCols);
+  hipLaunchKernelGGL((k_fwd<E, int(kDzRowTile), 4, ODD, 2, true, true>), dim3(unsigned(blocks)),
+                     dim3(Eng::NT), Eng::kLds, s, a);
+  return hipGetLastError();
+}
+
+template <class E>
+hipError_t dz_kept(const DzArgs& a, hipStream_t s) {
+  // LDS for the sums over rows only
+  const int64_t blocks = ((a.rows + kDzRowTile - 1) / kDzRowTile) * ((a.V + kTileCols - 1) / kTileCols);
+  hipLaunchKernelGGL((k_dz<E, int(kDzRowTile), 4, false, true, true>), dim3(unsigned(blocks)),
+                     dim3(512), 4 * kTileCols * sizeof(float), s, a);
+  return hipGetLastError();
+}
+
 // Number of 64-byte K stages of a logits tile is odd (D * element size / 64).
 template <class E>
 bool odd_stages(int64_t D) {
@@ -1706,8 +1761,8 @@ constexpr int kGemmNSA = 3;
 // The per-element MFMA chain does not depend on the tile shape, so the GEMM
 // variants may use different tiles and still give the same bits.
 //
-// d_hidden in vocabulary slabs (the cross entropy's backward of few rows): the slabs'
-// fp32 sums side by side, then added in ascending order and rounded once.
+// d_hidden in vocabulary slabs (the cross entropy's backward of up to kSlabRows rows): the
+// slabs' fp32 sums side by side, then added in ascending order and rounded once.
 template <class E>
 __global__ __launch_bounds__(256) void k_slab_fold(GemmArgs p, int slabs) {
   const int64_t n = p.M * p.N;  // a multiple of 32
@@ -1825,6 +1880,11 @@ hipError_t dw_dispatch<F32>(const GemmArgs& a, hipStream_t s) {
 
 hipError_t launch_loss_forward(flp_dtype x, const FwdArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_FORWARD, s);
+  if (a.logits != nullptr) {  // bf16 and fp32
+    if (x == FLP_BF16)
+      return odd_stages<BF16>(a.D) ? fwd_keep<BF16, true>(a, s) : fwd_keep<BF16, false>(a, s);
+    return odd_stages<F32>(a.D) ? fwd_keep<F32, true>(a, s) : fwd_keep<F32, false>(a, s);
+  }
   if (x == FLP_BF16) return fwd_dispatch<BF16, true>(a, s);
   if (x == FLP_F16) return fwd_dispatch<F16, true>(a, s);
   return fwd_dispatch<F32, true>(a, s);
@@ -1896,6 +1956,7 @@ hipError_t launch_logits_backward(flp_dtype x, const LogitsArgs& a, hipStream_t 
 hipError_t launch_dz(flp_dtype x, const DzArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_DLOGITS, s);
   const bool loss = a.onehot != nullptr;
+  if (a.logits != nullptr) return x == FLP_BF16 ? dz_kept<BF16>(a, s) : dz_kept<F32>(a, s);
   if (x == FLP_BF16) return loss ? dz_dispatch<BF16, true>(a, s) : dz_dispatch<BF16, false>(a, s);
   if (x == FLP_F16) return loss ? dz_dispatch<F16, true>(a, s) : dz_dispatch<F16, false>(a, s);
   return loss ? dz_dispatch<F32, true>(a, s) : dz_dispatch<F32, false>(a, s);
@@ -1963,7 +2024,7 @@ const char* kernel_ids() {
          "k_dbias_fold; k_fill; k_logits_fwd, k_logits_bwd<one wave per row>; "
          "rows: k_mark, k_compact, k_gather, k_scatter_rows, k_scatter_hidden; "
          "cross entropy: k_fwd, k_merge, k_dz with loss terms, k_loss_sum, k_loss_grad, k_gemm dX "
-         "over vocabulary slabs and k_slab_fold (<= 1024 rows); "
+         "over vocabulary slabs and k_slab_fold (<= 8192 rows); "
          "embedding: k_embed_fwd (scaled), radix sort (k_sort_hist, k_sort_scatter; 9-bit digits, "
          "zero riders), k_embed_runs<32-position groups>, k_embed_rows; k_dropout; layer norm: "
          "k_norm_fwd_row, k_norm_bwd_row<one or four waves per row>, k_norm_fold; wide rows: "

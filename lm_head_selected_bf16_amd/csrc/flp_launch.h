@@ -50,6 +50,7 @@ struct FwdArgs {
   float* zt;        // [N]
   float* zsum = nullptr;  // cross entropy: [n_vt][N] sums of logits times zunit, or null
   float zunit = 0.f;
+  float* logits = nullptr;  // cross entropy: keep the products (256-row tiles), or null
 };
 struct MergeArgs {
   const float2* part;
@@ -83,6 +84,7 @@ struct DzArgs {
   const float* onehot = nullptr;   // the target entry's added term
   const float* uniform = nullptr;  // every entry's added term
   const float* lse_rest = nullptr;
+  float* logits = nullptr;         // products kept by the forward, or null to recompute
 };
 struct LogitsArgs {
   const void* logits;        // [N][V]
@@ -231,7 +233,8 @@ struct LossGradArgs {        // backward: the per-row factors of the logit gradi
   int64_t N, V;
   const void* targets;
   int t64;
-  const float* grad_out;     // [N], or [1] for a reduced loss
+  const float* grad_out;     // [N], or [1] for a reduced loss, or null for 1
+  const float* inv;          // [1] 1 / rows of the mean, or null to count them here
   const float* lse;          // [N]
   float smoothing, z_loss;
   int reduction;             // flp_reduction
@@ -246,6 +249,11 @@ struct LossGradArgs {        // backward: the per-row factors of the logit gradi
 };
 hipError_t launch_loss_sum(const LossSumArgs& a, hipStream_t s);
 hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s);
+// *inv = 1 / the number of targets in [0, V) (1 if there are none).
+hipError_t launch_loss_count(int64_t N, int64_t V, const void* targets, bool t64, float* inv,
+                             hipStream_t s);
+// x *= *factor in place (n elements); nothing is touched when the factor is 1.
+hipError_t launch_scale(flp_dtype x_dtype, int64_t n, void* x, const float* factor, hipStream_t s);
 
 // Measurement probes (flp_probe.hip); they synchronise the stream.
 size_t probe_scratch_bytes();

@@ -8,6 +8,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
+#include "flp_chunk.h"
 #include "flp_launch.h"
 
 namespace flp {
@@ -35,6 +38,23 @@ __device__ __forceinline__ T sum_all(T v, T* red) {
   return v;
 }
 
+// 1 / the number of counted rows (1 if there are none), in every thread.
+__device__ __forceinline__ float inverse_count(int64_t N, int64_t V, const void* targets, int t64,
+                                               int64_t* red) {
+  int64_t n = 0;
+  for (int64_t i = threadIdx.x; i < N; i += kSumThreads) n += counted(targets, t64, i, V) ? 1 : 0;
+  n = sum_all(n, red);
+  return 1.0f / float(n > 0 ? n : 1);
+}
+
+__global__ __launch_bounds__(kSumThreads) void k_loss_count(int64_t N, int64_t V,
+                                                            const void* targets, int t64,
+                                                            float* inv) {
+  __shared__ int64_t red[16];
+  const float v = inverse_count(N, V, targets, t64, red);
+  if (threadIdx.x == 0) *inv = v;
+}
+
 // The reduced loss, by one workgroup: a batch has few rows next to what its logits cost.
 __global__ __launch_bounds__(kSumThreads) void k_loss_sum(LossSumArgs p) {
   __shared__ float fred[16];
@@ -60,14 +80,10 @@ __global__ __launch_bounds__(kSumThreads) void k_loss_grad(LossGradArgs p) {
   __shared__ float fred[16];
   const float s = p.smoothing, zl = p.z_loss;
   float inv = 1.0f;
-  if (p.reduction == FLP_REDUCE_MEAN) {
-    int64_t n = 0;
-    for (int64_t i = threadIdx.x; i < p.N; i += kSumThreads)
-      n += counted(p.targets, p.t64, i, p.V) ? 1 : 0;
-    n = sum_all(n, ired);
-    inv = 1.0f / float(n > 0 ? n : 1);
-  }
-  const float up = p.reduction != FLP_REDUCE_NONE ? p.grad_out[0] * inv : 0.f;
+  if (p.reduction == FLP_REDUCE_MEAN)
+    inv = p.inv != nullptr ? *p.inv : inverse_count(p.N, p.V, p.targets, p.t64, ired);
+  float up = 0.f;
+  if (p.reduction != FLP_REDUCE_NONE) up = (p.grad_out != nullptr ? p.grad_out[0] : 1.0f) * inv;
   const float sv = s / float(p.V);
   float big = 0.f;
   for (int64_t i = threadIdx.x; i < p.N; i += kSumThreads) {
@@ -104,7 +120,45 @@ __global__ __launch_bounds__(kSumThreads) void k_loss_grad(LossGradArgs p) {
   if (threadIdx.x == 0) *p.unscale = down;
 }
 
+// A chunk of eight elements per thread and step.  An upstream gradient of 1 (the usual
+// case: loss.backward()) ends the launch after one load per thread.
+template <class T>
+__global__ __launch_bounds__(256) void k_scale(int64_t n, T* x, const float* factor) {
+  const float f = *factor;
+  if (f == 1.0f) return;
+  const int64_t step = int64_t(gridDim.x) * 256;
+  for (int64_t b = int64_t(blockIdx.x) * 256 + threadIdx.x; b * kChunk < n; b += step) {
+    Chunk<T> c;
+    c.load(x + b * kChunk, n - b * kChunk);
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) c.v[k] = T(float(T(c.v[k])) * f);
+    c.store(x + b * kChunk, n - b * kChunk);
+  }
+}
+
 }  // namespace
+
+hipError_t launch_loss_count(int64_t N, int64_t V, const void* targets, bool t64, float* inv,
+                             hipStream_t s) {
+  ProfScope ps(FLP_K_LOSS, s);
+  hipLaunchKernelGGL(k_loss_count, dim3(1), dim3(kSumThreads), 0, s, N, V, targets, t64 ? 1 : 0,
+                     inv);
+  return hipGetLastError();
+}
+
+hipError_t launch_scale(flp_dtype x_dtype, int64_t n, void* x, const float* factor,
+                        hipStream_t s) {
+  ProfScope ps(FLP_K_LOSS, s);
+  const dim3 grid(unsigned(std::min<int64_t>((n + 2047) / 2048, 4096)));
+  if (x_dtype == FLP_BF16)
+    hipLaunchKernelGGL(k_scale<__bf16>, grid, dim3(256), 0, s, n, static_cast<__bf16*>(x), factor);
+  else if (x_dtype == FLP_F16)
+    hipLaunchKernelGGL(k_scale<_Float16>, grid, dim3(256), 0, s, n, static_cast<_Float16*>(x),
+                       factor);
+  else
+    hipLaunchKernelGGL(k_scale<float>, grid, dim3(256), 0, s, n, static_cast<float*>(x), factor);
+  return hipGetLastError();
+}
 
 hipError_t launch_loss_sum(const LossSumArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_LOSS, s);

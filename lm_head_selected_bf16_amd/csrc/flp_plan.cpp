@@ -122,6 +122,28 @@ BwdLayout bwd_layout_for_chunk(int64_t N, int64_t D, int64_t V, flp_dtype x, flp
   return L;
 }
 
+namespace {
+
+// Row quanta of a chunk, rounded down to a whole number of d_hidden waves when that is
+// possible.
+int64_t whole_waves(int64_t nq, int64_t D, flp_dtype x) {
+  const bool f32 = x == FLP_F32;
+  const int64_t tm = f32 ? kGemmTile32 : kGemmTileM16, tn = f32 ? kGemmTile32 : kGemmTileN16;
+  const int64_t ct = ceil_div(D, tn);
+  int64_t a = ct, b = kNumCUs;  // gcd
+  while (b != 0) {
+    const int64_t r = a % b;
+    a = b;
+    b = r;
+  }
+  const int64_t wave_rows = (kNumCUs / a) * tm;
+  if (wave_rows % kRowQuantum != 0) return nq;
+  const int64_t wq = wave_rows / kRowQuantum;
+  return nq >= wq ? nq / wq * wq : nq;
+}
+
+}  // namespace
+
 BwdLayout bwd_layout_for_bytes(int64_t N, int64_t D, int64_t V, flp_dtype x, flp_dtype dw,
                                size_t bytes, bool need_dh, bool need_dw, bool need_db) {
   const int64_t full = round_up(std::max<int64_t>(N, 1), kRowQuantum);
@@ -140,23 +162,7 @@ BwdLayout bwd_layout_for_bytes(int64_t N, int64_t D, int64_t V, flp_dtype x, flp
   int64_t nq = 0;
   if (per_quantum > 0 && bytes > fixed) nq = int64_t((bytes - fixed) / per_quantum);
   nq = std::min<int64_t>(nq, full / kRowQuantum);
-  if (need_dh && nq > 0) {
-    // Round the chunk down to a whole number of d_hidden waves when that is possible.
-    const bool f32 = x == FLP_F32;
-    const int64_t tm = f32 ? kGemmTile32 : kGemmTileM16, tn = f32 ? kGemmTile32 : kGemmTileN16;
-    const int64_t ct = ceil_div(D, tn);
-    int64_t a = ct, b = kNumCUs;  // gcd
-    while (b != 0) {
-      const int64_t r = a % b;
-      a = b;
-      b = r;
-    }
-    const int64_t wave_rows = (kNumCUs / a) * tm;
-    if (wave_rows % kRowQuantum == 0) {
-      const int64_t wq = wave_rows / kRowQuantum;
-      if (nq >= wq) nq = nq / wq * wq;
-    }
-  }
+  if (need_dh) nq = whole_waves(nq, D, x);
   for (; nq >= 1; --nq) {
     L = bwd_layout_for_chunk(N, D, V, x, dw, nq * kRowQuantum, need_dh, need_dw, need_db);
     if (L.total <= bytes) return L;
@@ -676,6 +682,100 @@ flp_status validate_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_
                                            d_hidden != nullptr, d_weight != nullptr,
                                            d_bias != nullptr);
   return L.chunk == 0 ? FLP_WORKSPACE_TOO_SMALL : FLP_OK;
+}
+
+LossAllLayout loss_all_layout(int64_t N, int64_t D, int64_t V, flp_dtype x, int64_t chunk,
+                              bool need_dh, bool need_dw, bool need_db) {
+  LossAllLayout L;
+  L.grad = loss_grad_layout(N, D, V);
+  L.bwd = bwd_layout_for_chunk(N, D, V, x, x, chunk, need_dh, need_dw, need_db);
+  const size_t rows = size_t(L.bwd.chunk), n_vt = size_t(L.bwd.ldz / kVocabTile);
+  size_t off = L.grad.total;
+  L.inv_off = off;
+  off += kAlign;
+  L.rows_off = off;
+  off += align_up(size_t(N) * 4);
+  L.lse_off = off;
+  off += align_up(size_t(N) * 8);
+  L.part_off = off;
+  off += align_up(n_vt * rows * 8);
+  L.zt_off = off;
+  off += align_up(rows * 4);
+  L.zsum_off = off;
+  off += align_up(n_vt * rows * 4);
+  L.logits_off = off;
+  off += rows * size_t(L.bwd.ldz) * 4;
+  L.bwd_off = off;
+  L.total = off + L.bwd.total;
+  return L;
+}
+
+LossAllLayout loss_all_layout_for_bytes(int64_t N, int64_t D, int64_t V, flp_dtype x, size_t bytes,
+                                        bool need_dh, bool need_dw, bool need_db) {
+  const int64_t full = ceil_div(std::max<int64_t>(N, 1), kRowQuantum);
+  auto at = [&](int64_t nq) {
+    return loss_all_layout(N, D, V, x, nq * kRowQuantum, need_dh, need_dw, need_db);
+  };
+  LossAllLayout L = at(full);
+  if (L.total <= bytes) return L;
+  int64_t lo = 0, hi = full - 1;  // the most quanta that fit: the size grows with them
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) / 2;
+    if (at(mid).total <= bytes)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  if (need_dh && lo > 0) lo = whole_waves(lo, D, x);
+  if (lo < 1) return LossAllLayout();
+  return at(lo);
+}
+
+flp_status validate_cross_entropy_gradients(int64_t N, int64_t D, int64_t V, flp_dtype x,
+                                            const void* hidden, const void* weight,
+                                            const float* bias, const void* targets, flp_dtype t,
+                                            double label_smoothing, double z_loss,
+                                            flp_reduction reduction, const float* out_loss,
+                                            const float* out_stats, const void* d_hidden,
+                                            const void* d_weight, const float* d_bias,
+                                            const void* workspace, size_t workspace_bytes) {
+  flp_status st = check_dims(N, D, V, x, t);
+  if (st != FLP_OK) return st;
+  if (x == FLP_F16) return FLP_UNSUPPORTED_DTYPE;
+  if ((st = check_loss_terms(label_smoothing, z_loss, reduction)) != FLP_OK) return st;
+  if (reduction == FLP_REDUCE_NONE || !out_loss) return FLP_INVALID_ARGUMENT;
+  const size_t xs = dtype_size(x);
+  if (N > 0 && (!hidden || !weight || !targets || !workspace)) return FLP_INVALID_ARGUMENT;
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(workspace, 16) ||
+      !aligned(bias, 4) || !aligned(targets, dtype_size(t)) || !aligned(out_loss, 4) ||
+      !aligned(out_stats, 4) || !aligned(d_hidden, 16) || !aligned(d_weight, 16) ||
+      !aligned(d_bias, 4))
+    return FLP_MISALIGNED;
+  const Span ins[] = {span(hidden, size_t(N) * D * xs), span(weight, size_t(V) * D * xs),
+                      span(bias, size_t(V) * 4), span(targets, size_t(N) * dtype_size(t))};
+  const Span outs[] = {span(out_loss, 4), span(out_stats, size_t(N) * 8),
+                       span(d_hidden, size_t(N) * D * xs), span(d_weight, size_t(V) * D * xs),
+                       span(d_bias, size_t(V) * 4),
+                       span(N > 0 ? workspace : nullptr, workspace_bytes)};
+  if (any_alias(outs, 6, ins, 4)) return FLP_INVALID_ARGUMENT;
+  if (N == 0) return FLP_OK;
+  const LossAllLayout L = loss_all_layout_for_bytes(N, D, V, x, workspace_bytes,
+                                                    d_hidden != nullptr, d_weight != nullptr,
+                                                    d_bias != nullptr);
+  return L.bwd.chunk == 0 ? FLP_WORKSPACE_TOO_SMALL : FLP_OK;
+}
+
+flp_status validate_scale_inplace(int64_t n, flp_dtype x_dtype, const void* x,
+                                  const float* factor) {
+  if (n < 0) return FLP_INVALID_ARGUMENT;
+  if (x_dtype != FLP_BF16 && x_dtype != FLP_F16 && x_dtype != FLP_F32) return FLP_UNSUPPORTED_DTYPE;
+  if (!mul_ok(n, 4)) return FLP_UNSUPPORTED_SHAPE;
+  if (n == 0) return FLP_OK;
+  if (!x || !factor) return FLP_INVALID_ARGUMENT;
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(factor, 4)) return FLP_MISALIGNED;
+  const Span ins[] = {span(factor, 4)};
+  const Span outs[] = {span(x, size_t(n) * dtype_size(x_dtype))};
+  return any_alias(outs, 1, ins, 1) ? FLP_INVALID_ARGUMENT : FLP_OK;
 }
 
 NormLayout norm_layout(int64_t N, int64_t D) {

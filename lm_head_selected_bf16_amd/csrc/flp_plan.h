@@ -114,16 +114,32 @@ float loss_zunit(int64_t V);
 // Backward: the per-row factors of dz and the slab sums of d_hidden, in front of the logp
 // backward's workspace.
 //
-// A batch of up to kSlabRows rows sums d_hidden over slabs of the vocabulary: its few
-// output tiles would otherwise walk the whole vocabulary one after another and leave most
-// compute units idle.  The slab length depends on V alone, so among such batches a row's
-// d_hidden does not depend on the others.
-constexpr int64_t kSlabRows = 1024;
+// A batch of up to kSlabRows rows sums d_hidden over slabs of the vocabulary: its output
+// tiles are too few, or fill their last wave of workgroups too little, for each to walk the
+// whole vocabulary (bf16 on MI355X, d_hidden in one walk and in slabs: 2048 x 2688 x 131072
+// 2374 and 1200 us, 4096 x 512 x 50257 828 and 257, 8192 x 512 x 50257 862 and 487,
+// 8192 x 2688 x 131072 5030 and 4728).  The slab length depends on V alone, so among such
+// batches a row's d_hidden does not depend on the others.
+constexpr int64_t kSlabRows = 8192;
 struct LossGradLayout {
   size_t softmax_off = 0, onehot_off = 0, uniform_off = 0, unscale_off = 0, slab_off = 0, total = 0;
   int64_t k_slab = 0;     // columns of a slab (a multiple of 256), 0: one walk
 };
 LossGradLayout loss_grad_layout(int64_t N, int64_t D, int64_t V);
+// Loss and gradients in one call: the gradient factors, the rows' losses and lse [2][N],
+// a chunk's forward (partials, target logits, sums of logits, fp32 products), and the
+// chunk's backward.
+struct LossAllLayout {
+  LossGradLayout grad;
+  BwdLayout bwd;
+  size_t inv_off = 0, rows_off = 0, lse_off = 0, part_off = 0, zt_off = 0, zsum_off = 0;
+  size_t logits_off = 0, bwd_off = 0, total = 0;
+};
+LossAllLayout loss_all_layout(int64_t N, int64_t D, int64_t V, flp_dtype x, int64_t chunk,
+                              bool need_dh, bool need_dw, bool need_db);
+// Largest chunk that fits `bytes` (bwd.chunk = 0 when nothing fits).
+LossAllLayout loss_all_layout_for_bytes(int64_t N, int64_t D, int64_t V, flp_dtype x, size_t bytes,
+                                        bool need_dh, bool need_dw, bool need_db);
 
 // ---- layer norm backward: slabs of rows whose d_weight and d_bias partials are added ----
 constexpr int64_t kNormSlabs = 256;    // at most this many slabs (one workgroup per compute unit)
@@ -227,6 +243,17 @@ flp_status validate_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_
                                            const void* d_hidden, const void* d_weight,
                                            const float* d_bias, const void* workspace,
                                            size_t workspace_bytes);
+flp_status validate_cross_entropy_gradients(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
+                                            const void* hidden, const void* weight,
+                                            const float* bias, const void* targets,
+                                            flp_dtype t_dtype, double label_smoothing,
+                                            double z_loss, flp_reduction reduction,
+                                            const float* out_loss, const float* out_stats,
+                                            const void* d_hidden, const void* d_weight,
+                                            const float* d_bias, const void* workspace,
+                                            size_t workspace_bytes);
+flp_status validate_scale_inplace(int64_t n, flp_dtype x_dtype, const void* x,
+                                  const float* factor);
 
 // Layer norm; the parameters have the rows' type or fp32.
 flp_status validate_layer_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,

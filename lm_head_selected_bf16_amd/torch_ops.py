@@ -28,6 +28,9 @@ from ._abi import FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpError
 # Default cap on the backward workspace: a larger workspace only means larger row
 # chunks (same bits); 16 GiB keeps a whole 16384-row chunk of dz and dz^T.
 DEFAULT_BWD_WORKSPACE = 16 << 30
+# The same for the cross entropy's loss-and-gradients call, which keeps a chunk's fp32 logits as
+# well: a whole chunk of 16384 rows over 131072 columns in bfloat16.
+DEFAULT_GRADIENTS_WORKSPACE = 24 << 30
 
 _X_DTYPES = {torch.bfloat16: FLP_BF16, torch.float16: FLP_F16, torch.float32: FLP_F32}
 _T_DTYPES = {torch.int64: FLP_I64, torch.int32: FLP_I32}
@@ -647,27 +650,102 @@ def cross_entropy_backward(grad_out: torch.Tensor, stats: torch.Tensor, hidden: 
     return d_hidden, d_weight, d_bias
 
 
+def cross_entropy_gradients(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                            bias: Optional[torch.Tensor] = None, label_smoothing: float = 0.0,
+                            z_loss: float = 0.0, reduction: str = "mean",
+                            need_hidden: bool = True, need_weight: bool = True,
+                            need_bias: Optional[bool] = None,
+                            workspace_bytes: Optional[int] = None):
+    """(loss, stats, d_hidden, d_weight, d_bias) for an upstream gradient of 1 through
+    flp_cross_entropy_gradients (bfloat16 or float32, reduction "sum" or "mean"): the bits of
+    cross_entropy_forward and cross_entropy_backward with one matrix product less."""
+    (h2, t1, _, lead, N, D, V), red = _prepare_loss(hidden, weight, targets, bias, reduction)
+    dev = hidden.device
+    if need_bias is None:
+        need_bias = bias is not None
+    xd = _X_DTYPES[hidden.dtype]
+    if workspace_bytes is None:
+        size = _abi.flp_cross_entropy_gradients_workspace_bytes
+        workspace_bytes = size(N, D, V, xd, max(N, 1))
+        if workspace_bytes > DEFAULT_GRADIENTS_WORKSPACE:
+            workspace_bytes = max(size(N, D, V, xd, 0), DEFAULT_GRADIENTS_WORKSPACE)
+    with _on(dev):
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        stats = torch.empty((2,) + lead, dtype=torch.float32, device=dev)
+        d_hidden = torch.empty_like(hidden) if need_hidden else None
+        d_weight = torch.empty_like(weight) if need_weight else None
+        d_bias = torch.empty(V, dtype=torch.float32, device=dev) if need_bias else None
+        ws = torch.empty(max(int(workspace_bytes), 16), dtype=torch.uint8, device=dev)
+        st = _abi.flp_cross_entropy_gradients(N, D, V, xd, _ptr(h2), _ptr(weight), _ptr(bias),
+                                              _ptr(t1), _T_DTYPES[targets.dtype],
+                                              float(label_smoothing), float(z_loss), red,
+                                              _ptr(loss), _ptr(stats), _ptr(d_hidden),
+                                              _ptr(d_weight), _ptr(d_bias), _ptr(ws), ws.numel(),
+                                              _stream(dev))
+    _check("flp_cross_entropy_gradients", st)
+    return loss, stats, d_hidden, d_weight, d_bias
+
+
+def _gradients_at_once(hidden, weight, reduction) -> bool:
+    """Whether a training step's loss and gradients come from one call (the same bits).  It saves
+    a product of N D V multiply-adds and moves 8 bytes per logit more, and a few launches more:
+    measured on MI355X, it wins from D = 1024 on in bfloat16 (4096 x 512 x 50257: 1090 us in two
+    calls, 1207 in one; 4096 x 2048 x 50257: 3092 and 2816), in float32 past the 128 rows that the
+    two calls take in smaller tiles, and where that product takes 20 us."""
+    D = hidden.shape[-1]
+    N, V = hidden.numel() // max(D, 1), weight.shape[0]
+    if reduction == "none":
+        return False
+    if hidden.dtype == torch.bfloat16:
+        return D >= 1024 and N * D * V >= 2 * 10 ** 10
+    return hidden.dtype == torch.float32 and D >= 128 and N > 128 and N * D * V >= 2 * 10 ** 9
+
+
 class LinearCrossEntropy(torch.autograd.Function):
-    """Autograd node of the linear cross entropy: the forward saves the rows' lse, the backward recomputes
-    the logits."""
+    """Autograd node of the linear cross entropy.  The forward saves the rows' lse and the
+    backward recomputes the logits; or, where that is faster, the forward makes the gradients for
+    an upstream gradient of 1 along with the loss, and the first backward multiplies them by the
+    upstream gradient in place (a second rounding unless that is a power of two) and hands them
+    over.  Any further backward through the same node recomputes."""
 
     @staticmethod
     def forward(ctx, hidden, weight, targets, bias, label_smoothing, z_loss, reduction):
-        loss, stats = cross_entropy_forward(hidden, weight, targets, bias, label_smoothing, z_loss,
-                                          reduction)
+        terms = (label_smoothing, z_loss, reduction)
+        ctx.grads = None
+        if _gradients_at_once(hidden, weight, reduction):
+            need_h, need_w, _, need_b = ctx.needs_input_grad[:4]
+            loss, stats, *ctx.grads = cross_entropy_gradients(
+                hidden, weight, targets, bias, *terms, need_hidden=need_h, need_weight=need_w,
+                need_bias=need_b)
+        else:
+            loss, stats = cross_entropy_forward(hidden, weight, targets, bias, *terms)
         ctx.save_for_backward(hidden, weight, targets, bias, stats)
-        ctx.terms = (label_smoothing, z_loss, reduction)
+        ctx.terms = terms
         return loss
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g):
-        hidden, weight, targets, bias, stats = ctx.saved_tensors
-        need_h, need_w, _, need_b = ctx.needs_input_grad[:4]
-        dh, dw, db = cross_entropy_backward(g.contiguous(), stats, hidden, weight, targets, bias,
-                                            *ctx.terms, need_hidden=need_h, need_weight=need_w,
-                                            need_bias=need_b)
+        grads, ctx.grads = ctx.grads, None
+        if grads is not None:
+            dh, dw, db = (_scaled(x, g) for x in grads)
+        else:
+            hidden, weight, targets, bias, stats = ctx.saved_tensors
+            need_h, need_w, _, need_b = ctx.needs_input_grad[:4]
+            dh, dw, db = cross_entropy_backward(g.contiguous(), stats, hidden, weight, targets,
+                                                bias, *ctx.terms, need_hidden=need_h,
+                                                need_weight=need_w, need_bias=need_b)
         return dh, dw, None, db, None, None, None
+
+
+def _scaled(x, factor):
+    """x *= factor in place (a scalar float32 tensor), through flp_scale_inplace."""
+    if x is not None:
+        with _on(x.device):
+            st = _abi.flp_scale_inplace(x.numel(), _X_DTYPES[x.dtype], x.data_ptr(),
+                                        factor.data_ptr(), _stream(x.device))
+        _check("flp_scale_inplace", st)
+    return x
 
 
 def linear_cross_entropy(hidden, weight, targets, bias=None, label_smoothing=0.0, z_loss=0.0,

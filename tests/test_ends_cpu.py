@@ -211,6 +211,67 @@ def test_cross_entropy_backward_gates(kw, expect):
     assert ce_bwd(**kw) == expect
 
 
+def ce_all(**kw):
+    a = dict(N=N, D=D, V=V, x=BF16, h=A[0], w=A[1], b=A[2], t=A[3], td=I64, s=0.1, c=1e-4,
+             red=abi.FLP_REDUCE_SUM, loss=A[4], st=A[5], dh=A[6], dw=A[7], db=A[8], ws=A[9],
+             wsb=abi.flp_cross_entropy_gradients_workspace_bytes(N, D, V, BF16, 0))
+    a.update(kw)
+    return name(abi.flp_cross_entropy_gradients(a["N"], a["D"], a["V"], a["x"], a["h"], a["w"],
+                                                a["b"], a["t"], a["td"], a["s"], a["c"], a["red"],
+                                                a["loss"], a["st"], a["dh"], a["dw"], a["db"],
+                                                a["ws"], a["wsb"], 0))
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(N=-1), "FLP_INVALID_ARGUMENT"),
+    (dict(D=40), "FLP_UNSUPPORTED_SHAPE"),
+    (dict(x=F16), "FLP_UNSUPPORTED_DTYPE"),
+    (dict(s=-1.0), "FLP_INVALID_ARGUMENT"),
+    (dict(red=abi.FLP_REDUCE_NONE), "FLP_INVALID_ARGUMENT"),
+    (dict(loss=0), "FLP_INVALID_ARGUMENT"),
+    (dict(h=0), "FLP_INVALID_ARGUMENT"),
+    (dict(ws=0), "FLP_INVALID_ARGUMENT"),
+    (dict(dw=A[7] + 8), "FLP_MISALIGNED"),
+    (dict(dh=A[1] + 64), "FLP_INVALID_ARGUMENT"),
+    (dict(st=A[4] - 8 * N + 4), "FLP_INVALID_ARGUMENT"),    # the statistics run into the loss
+    (dict(ws=A[6] + 16), "FLP_INVALID_ARGUMENT"),
+    (dict(wsb=4096), "FLP_WORKSPACE_TOO_SMALL"),
+    (dict(wsb=abi.flp_cross_entropy_gradients_workspace_bytes(N, D, V, BF16, 0) - 1),
+     "FLP_WORKSPACE_TOO_SMALL"),
+    (dict(N=0, loss=0), "FLP_INVALID_ARGUMENT"),
+])
+def test_cross_entropy_gradients_gates(kw, expect):
+    assert ce_all(**kw) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(n=-1), "FLP_INVALID_ARGUMENT"),
+    (dict(x=I64), "FLP_UNSUPPORTED_DTYPE"),
+    (dict(p=0), "FLP_INVALID_ARGUMENT"),
+    (dict(f=0), "FLP_INVALID_ARGUMENT"),
+    (dict(p=A[0] + 1), "FLP_MISALIGNED"),
+    (dict(f=A[0] + 16), "FLP_INVALID_ARGUMENT"),            # the factor inside x
+    (dict(n=0, p=0, f=0), "FLP_OK"),
+])
+def test_scale_inplace_gates(kw, expect):
+    a = dict(n=100, x=BF16, p=A[0], f=A[1])
+    a.update(kw)
+    assert name(abi.flp_scale_inplace(a["n"], a["x"], a["p"], a["f"], 0)) == expect
+
+
+def test_gradients_workspace_holds_the_chunk():
+    """A whole chunk keeps 4 bytes per logit beside dz and dz^T; the least workspace is a chunk
+    of 256 rows or one of all of them, whichever is smaller."""
+    size = abi.flp_cross_entropy_gradients_workspace_bytes
+    one = size(16384, 2688, 131072, BF16, 16384)
+    assert one >= 16384 * 131072 * 8
+    assert one <= 24 << 30  # what the Python entry point takes without chunks
+    for shape in ((16384, 2688, 131072), (600, 64, 1000), (257, 96, 300)):
+        n = shape[0]
+        assert size(*shape, BF16, 0) == min(size(*shape, BF16, 256), size(*shape, BF16, n))
+    assert size(0, 64, 100, BF16, 0) == 0 and size(10, 64, 100, F16, 0) == 0
+
+
 def test_cross_entropy_workspace_bytes():
     n_vt = -(-V // 256)
     assert (abi.flp_cross_entropy_forward_workspace_bytes(N, D, V)

@@ -275,6 +275,116 @@ def test_row_chunks_keep_the_bits(dtype):
     assert all(torch.equal(x, y) for x, y in zip(a, z))
 
 
+def at_once(h, w, b, t, s, c, reduction, **kw):
+    m = flp()
+    loss, stats, dh, dw, db = m.cross_entropy_gradients(h, w, t, b, s, c, reduction,
+                                                        need_bias=True, **kw)
+    return loss, stats[0], dh, dw, db
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("k", range(len(SHAPES)))
+def test_gradients_at_once_have_the_bits_of_two_calls(k, dtype):
+    N, D, V = SHAPES[k]
+    h, w, b, t, up = make(N, D, V, dtype, 10 * k, ignored=0.1 if N > 1 else 0.0)
+    for s, c, red, bias in ((0.0, 0.0, "mean", None), (0.1, 1e-3, "sum", b)):
+        want = run(h, w, bias, t, torch.ones_like(up), s, c, red)
+        got = at_once(h, w, bias, t, s, c, red)
+        for name, x, y in zip(("loss", "lse", "d_hidden", "d_weight", "d_bias"), got, want):
+            assert torch.equal(x, y), (N, D, V, red, name)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_at_once_in_chunks_and_parts(dtype):
+    m = flp()
+    h, w, b, t, up = make(1100, 96, 2500, dtype, 50)
+    want = run(h, w, b, t, torch.ones_like(up), 0.1, 1e-3, "mean")
+    code = {BF16: m.FLP_BF16, F32: m.FLP_F32}[dtype]
+    size = m.flp_cross_entropy_gradients_workspace_bytes
+    sizes = [size(1100, 96, 2500, code, r) for r in (256, 512, 1100)]
+    assert sizes == sorted(sizes) and size(1100, 96, 2500, code, 0) <= sizes[-1]
+    for wsb in sizes + [size(1100, 96, 2500, code, 0)]:
+        got = at_once(h, w, b, t, 0.1, 1e-3, "mean", workspace_bytes=wsb)
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), wsb
+    for need in ((True, False), (False, True), (False, False)):
+        loss, stats, dh, dw, db = m.cross_entropy_gradients(h, w, t, b, 0.1, 1e-3,
+                                                            need_hidden=need[0],
+                                                            need_weight=need[1], need_bias=False)
+        assert torch.equal(loss, want[0]) and db is None
+        assert (dh is None) != need[0] and (dw is None) != need[1]
+        assert dh is None or torch.equal(dh, want[2])
+        assert dw is None or torch.equal(dw, want[3])
+
+
+def test_gradients_at_once_with_padding_and_masks():
+    """Padded rows of NaN, a vocabulary masked with the lowest value, nothing but padding, and an
+    empty batch."""
+    m = flp()
+    h, w, b, t, up = make(300, 64, 1500, BF16, 51)
+    b[256:600] = torch.finfo(F32).min
+    t = torch.where((t >= 256) & (t < 600), t - 256, t)
+    want = run(h, w, b, t, torch.ones_like(up), 0.0, 1e-3, "mean")
+    bad = h.clone()
+    pad = (t < 0) | (t >= 1500)
+    bad[pad] = float("nan")
+    got = at_once(bad, w, b, t, 0.0, 1e-3, "mean")
+    for k in (0, 2, 3, 4):
+        assert torch.equal(got[k], want[k]), k
+    for x in at_once(h, w, b, torch.full_like(t, -1), 0.0, 1e-3, "mean")[::2]:
+        assert not x.any()
+    loss, stats, dh, dw, db = m.cross_entropy_gradients(h[:0], w, t[:0], b)
+    assert not loss.any() and dh.shape == (0, 64) and not dw.any() and not db.any()
+
+
+# the sizes from which a step's loss and gradients come from one call
+@pytest.mark.parametrize("dtype,N,D,V", [(BF16, 300, 1024, 70000), (F32, 200, 128, 100000)])
+def test_autograd_of_large_steps(dtype, N, D, V):
+    m = flp()
+    h, w, b, t, up = make(N, D, V, dtype, 52, w_std=0.02)
+    unit = run(h, w, b, t, torch.ones_like(up), 0.1, 1e-3, "mean")
+    names = ("hidden", "weight", "bias")
+    leaves = [x.clone().requires_grad_(True) for x in (h, w, b)]
+    loss = m.linear_cross_entropy(leaves[0], leaves[1], t, leaves[2], 0.1, 1e-3)
+    assert torch.equal(loss, unit[0])
+    # first backward (made with the loss), a second one (recomputed), and one with a factor
+    first = torch.autograd.grad(loss, leaves, retain_graph=True)
+    again = torch.autograd.grad(loss, leaves, retain_graph=True)
+    for n, x, y, z in zip(names, first, again, unit[2:]):
+        assert torch.equal(x, z) and torch.equal(y, z), n
+    loss = m.linear_cross_entropy(leaves[0], leaves[1], t, leaves[2], 0.1, 1e-3)
+    half = torch.autograd.grad(loss * 0.5, leaves)
+    for n, x, z in zip(names, half, unit[2:]):
+        assert torch.equal(x.double(), 0.5 * z.double()), n
+    loss = m.linear_cross_entropy(leaves[0], leaves[1], t, leaves[2], 0.1, 1e-3)
+    third = torch.autograd.grad(loss * 3, leaves)
+    for n, x, z in zip(names, third, unit[2:]):
+        # rounded at 1, times 3 in fp32, rounded once more
+        assert bool(((x.double() - 3 * z.double()).abs()
+                     <= torch.finfo(x.dtype).eps / 2 * 3 * z.double().abs() + 1e-300).all()), n
+    # only one leaf asks
+    x = h.clone().requires_grad_(True)
+    (dh,) = torch.autograd.grad(m.linear_cross_entropy(x, w, t, b, 0.1, 1e-3), [x])
+    assert torch.equal(dh, unit[2])
+
+
+def test_scale_inplace():
+    m = flp()
+    code = {BF16: m.FLP_BF16, F16: m.FLP_F16, F32: m.FLP_F32}
+    stream = torch.cuda.current_stream().cuda_stream
+    for dtype in (BF16, F16, F32):
+        for n in (1, 7, 8, 4099):
+            base = torch.randn(n + 9, device="cuda").to(dtype)
+            for f in (1.0, 0.5, 3.0):
+                x = base.clone()
+                factor = torch.tensor(f, device="cuda")
+                # starts one element in: off the 16-byte grid
+                assert m.flp_scale_inplace(n, code[dtype], x[1:].data_ptr(), factor.data_ptr(),
+                                           stream) == m.FLP_OK
+                want = base.clone()
+                want[1:n + 1] = (base[1:n + 1].float() * f).to(dtype)
+                assert torch.equal(x, want)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_rows_do_not_depend_on_the_batch(dtype):
     m = flp()
@@ -291,11 +401,16 @@ def test_rows_do_not_depend_on_the_batch(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
-@pytest.mark.parametrize("N", [5, 64, 65, 128, 129, 512, 513, 1023, 1024, 1025])
+@pytest.mark.parametrize("N", [5, 64, 65, 128, 129, 512, 513, 1025, 2050])
 def test_slabs_of_the_vocabulary(dtype, N):
     """Row counts around every tile of d_hidden, over a vocabulary of several slabs and a ragged
     last one, and past the last row count that takes slabs."""
     compare(*make(N, 96, 9001, dtype, 30 + N), s=0.1, c=1e-3, reduction="mean")
+
+
+@pytest.mark.parametrize("N", [8192, 8193])
+def test_last_row_count_of_slabs(N):
+    compare(*make(N, 32, 4500, BF16, 29), s=0.1, reduction="sum")
 
 
 def test_slabs_keep_rows_apart():
@@ -363,12 +478,15 @@ def test_empty_batch():
         assert not dw.any() and dh.shape == (0, 64)
 
 
-def test_graph_replays_with_new_inputs():
+@pytest.mark.parametrize("at_once", [False, True])
+def test_graph_replays_with_new_inputs(at_once):
     m = flp()
     h, w, b, t, up = make(260, 64, 1500, BF16, 19)
     g = torch.ones((), device="cuda")
 
     def step():
+        if at_once:
+            return m.cross_entropy_gradients(h, w, t, b, 0.1, 1e-3)
         loss, stats = m.cross_entropy_forward(h, w, t, b, 0.1, 1e-3)
         return (loss,) + m.cross_entropy_backward(g, stats, h, w, t, b, 0.1, 1e-3)
 
@@ -435,6 +553,10 @@ def test_refusals():
         m.linear_cross_entropy(h, w.float(), t)
     with pytest.raises(m.FlpError):
         m.linear_cross_entropy(h[:, :40].contiguous(), w[:, :40].contiguous(), t)
+    with pytest.raises(m.FlpError):
+        m.cross_entropy_gradients(h, w, t, reduction="none")
+    with pytest.raises(m.FlpError):
+        m.cross_entropy_gradients(h.half(), w.half(), t)
     loss, stats = m.cross_entropy_forward(h, w, t, b)
     with pytest.raises(ValueError):
         m.cross_entropy_backward(up, stats, h, w, t, b)  # a scalar is wanted
