@@ -109,11 +109,21 @@ flp_status enqueue_backward(const BwdLayout& L, int64_t N, int64_t D, int64_t V,
       z.lse_rest = loss->lse_rest + r0;
     }
     if (launch_dz(x_dtype, z, s) != hipSuccess) return FLP_HIP_ERROR;
+    const int64_t kpad = round_up(rows, kTokPad);  // dz^T and hidden^T are zero past rows
+    // The cross entropy's operands in one launch: hidden^T, and W^T for the first chunk.
+    const bool both = loss != nullptr && d_weight != nullptr;
+    if (both) {
+      const bool w_too = d_hidden != nullptr && c == 0;
+      if (launch_transpose_live(x_dtype, h_chunk, rows, kpad, D, z.targets, t_dtype == FLP_I64, V,
+                                hT, w_too ? weight : nullptr, L.ldz, wT, s) != hipSuccess)
+        return FLP_HIP_ERROR;
+    }
     if (d_hidden) {
       // W^T is made once, after the first dlogits: that kernel re-reads hidden, which
       // the forward left in the Infinity Cache and streaming 1.4 GB of W and W^T
       // through it first would evict.
-      if (c == 0 && launch_transpose(x_dtype, weight, V, L.ldz, D, D, wT, s) != hipSuccess)
+      if (c == 0 && !both &&
+          launch_transpose(x_dtype, weight, V, L.ldz, D, D, wT, s) != hipSuccess)
         return FLP_HIP_ERROR;
       GemmArgs g;
       g.a = dz;
@@ -138,12 +148,8 @@ flp_status enqueue_backward(const BwdLayout& L, int64_t N, int64_t D, int64_t V,
       if (launch_dx(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
     }
     if (d_weight) {
-      const int64_t kpad = round_up(rows, kTokPad);  // dz^T and hidden^T are zero past rows
-      const hipError_t e =
-          loss != nullptr ? launch_transpose_live(x_dtype, h_chunk, rows, kpad, D, z.targets,
-                                                  t_dtype == FLP_I64, V, hT, s)
-                          : launch_transpose(x_dtype, h_chunk, rows, kpad, D, D, hT, s);
-      if (e != hipSuccess) return FLP_HIP_ERROR;
+      if (!both && launch_transpose(x_dtype, h_chunk, rows, kpad, D, D, hT, s) != hipSuccess)
+        return FLP_HIP_ERROR;
       GemmArgs g;
       g.a = dzT;
       g.b = hT;

@@ -1566,6 +1566,26 @@ struct LiveRows {
   }
 };
 
+// A second matrix of the same width in the same launch (W beside a chunk's hidden rows): the
+// workgroups past the first one's rows_pad take its rows, none of which are checked.
+struct PlainRows {
+  const void* src;
+  int64_t rows, rows_pad;
+  void* dst;
+  template <class T>
+  __device__ __forceinline__ bool take(int64_t& r0, const T* __restrict__& s, int64_t& n,
+                                       int64_t& pad, T* __restrict__& d) const {
+    const int64_t first = (pad + 63) / 64 * 64;
+    if (r0 < first) return true;
+    r0 -= first;
+    s = static_cast<const T*>(src);
+    n = rows;
+    pad = rows_pad;
+    d = static_cast<T*>(dst);
+    return false;
+  }
+};
+
 // ---- tiled transpose ---------------------------------------------------------------------------
 // dst = src^T in the K-blocked layout (dst has `cols` rows and K = rows_pad);
 // entries r in [rows, rows_pad) are written as zeros.
@@ -1574,14 +1594,18 @@ struct LiveRows {
 template <class T, bool LIVE = false>
 __global__ __launch_bounds__(256) void k_transpose(const T* __restrict__ src, int64_t rows,
                                                    int64_t rows_pad, int64_t cols, int64_t ld_src,
-                                                   T* __restrict__ dst, LiveRows live) {
+                                                   T* __restrict__ dst, LiveRows live,
+                                                   PlainRows also) {
   __shared__ T tile[64][65];
-  const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
+  int64_t r0 = int64_t(blockIdx.y) * 64;
+  const int64_t c0 = int64_t(blockIdx.x) * 64;
+  bool check = true;
+  if constexpr (LIVE) check = also.take(r0, src, rows, rows_pad, dst);
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   for (int k = ty; k < 64; k += 4) {
     const int64_t r = r0 + k, c = c0 + tx;
     bool in = r < rows && c < cols;
-    if constexpr (LIVE) in = in && live(r);
+    if constexpr (LIVE) in = in && (!check || live(r));
     tile[k][tx] = in ? src[r * ld_src + c] : T(0);
   }
   __syncthreads();
@@ -1600,9 +1624,13 @@ __global__ __launch_bounds__(256) void k_transpose(const T* __restrict__ src, in
 template <bool LIVE = false>
 __global__ __launch_bounds__(256) void k_transpose16(const uint16_t* __restrict__ src, int64_t rows,
                                                      int64_t rows_pad, int64_t cols, int64_t ld_src,
-                                                     uint16_t* __restrict__ dst, LiveRows live) {
+                                                     uint16_t* __restrict__ dst, LiveRows live,
+                                                     PlainRows also) {
   __shared__ uint32_t tile[64][33];  // [row][column pair], 132-byte rows
-  const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
+  int64_t r0 = int64_t(blockIdx.y) * 64;
+  const int64_t c0 = int64_t(blockIdx.x) * 64;
+  bool check = true;
+  if constexpr (LIVE) check = also.take(r0, src, rows, rows_pad, dst);
   const int t = threadIdx.x, j = t & 7, q = t >> 3;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
@@ -1610,7 +1638,7 @@ __global__ __launch_bounds__(256) void k_transpose16(const uint16_t* __restrict_
     const int64_t r = r0 + rl, c = c0 + 8 * j;
     u32x4 v = {0u, 0u, 0u, 0u};
     bool in = r < rows && c < cols;
-    if constexpr (LIVE) in = in && live(r);
+    if constexpr (LIVE) in = in && (!check || live(r));
     if (in) v = *reinterpret_cast<const u32x4*>(src + r * ld_src + c);
 #pragma unroll
     for (int e = 0; e < 4; ++e) tile[rl][4 * j + e] = v[e];
@@ -1982,27 +2010,32 @@ hipError_t launch_transpose(flp_dtype x, const void* src, int64_t rows, int64_t 
   const dim3 grid(unsigned((cols + 63) / 64), unsigned((rows_pad + 63) / 64));
   if (x != FLP_F32)
     hipLaunchKernelGGL(k_transpose16<>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(src),
-                       rows, rows_pad, cols, ld_src, static_cast<uint16_t*>(dst), LiveRows{});
+                       rows, rows_pad, cols, ld_src, static_cast<uint16_t*>(dst), LiveRows{},
+                       PlainRows{});
   else
     hipLaunchKernelGGL(k_transpose<float>, grid, dim3(256), 0, s, static_cast<const float*>(src),
-                       rows, rows_pad, cols, ld_src, static_cast<float*>(dst), LiveRows{});
+                       rows, rows_pad, cols, ld_src, static_cast<float*>(dst), LiveRows{},
+                       PlainRows{});
   return hipGetLastError();
 }
 
 hipError_t launch_transpose_live(flp_dtype x, const void* src, int64_t rows, int64_t rows_pad,
                                  int64_t cols, const void* targets, bool t64, int64_t V, void* dst,
+                                 const void* weight, int64_t weight_pad, void* weight_dst,
                                  hipStream_t s) {
   ProfScope ps(FLP_K_TRANSPOSE, s);
-  const dim3 grid(unsigned((cols + 63) / 64), unsigned((rows_pad + 63) / 64));
+  const PlainRows also{weight, V, weight_pad, weight_dst};
+  const int64_t blocks = (rows_pad + 63) / 64 + (weight != nullptr ? (weight_pad + 63) / 64 : 0);
+  const dim3 grid(unsigned((cols + 63) / 64), unsigned(blocks));
   const LiveRows live{targets, t64 ? 1 : 0, V};
   if (x != FLP_F32)
     hipLaunchKernelGGL(k_transpose16<true>, grid, dim3(256), 0, s,
                        static_cast<const uint16_t*>(src), rows, rows_pad, cols, cols,
-                       static_cast<uint16_t*>(dst), live);
+                       static_cast<uint16_t*>(dst), live, also);
   else
     hipLaunchKernelGGL((k_transpose<float, true>), grid, dim3(256), 0, s,
                        static_cast<const float*>(src), rows, rows_pad, cols, cols,
-                       static_cast<float*>(dst), live);
+                       static_cast<float*>(dst), live, also);
   return hipGetLastError();
 }
 

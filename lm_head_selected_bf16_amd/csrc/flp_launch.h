@@ -143,9 +143,10 @@ hipError_t launch_dw(flp_dtype x, const GemmArgs& a, hipStream_t s);
 hipError_t launch_transpose(flp_dtype x, const void* src, int64_t rows, int64_t rows_pad, int64_t cols,
                             int64_t ld_src, void* dst, hipStream_t s);
 // The same for hidden rows (row stride cols): rows whose target is outside [0, V) read as
-// zeros.
+// zeros.  In the same launch, unless null: weight [V][cols], padded to weight_pad.
 hipError_t launch_transpose_live(flp_dtype x, const void* src, int64_t rows, int64_t rows_pad,
                                  int64_t cols, const void* targets, bool t64, int64_t V, void* dst,
+                                 const void* weight, int64_t weight_pad, void* weight_dst,
                                  hipStream_t s);
 hipError_t launch_dbias_fold(const float* part, int64_t n_parts, int64_t ldz, int64_t V,
                              float* d_bias, int init, const float* scale, hipStream_t s);

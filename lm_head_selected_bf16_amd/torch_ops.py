@@ -56,6 +56,25 @@ def _on(device: torch.device):
     return torch.cuda.device(device)
 
 
+def _first_order(backward):
+    """A backward whose gradients cannot be differentiated again: under create_graph their use
+    in a second backward raises.  (once_differentiable on every call would cost 3 us.)"""
+    guarded = once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return guarded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+    return run
+
+
+def _wants_grad(*tensors) -> bool:
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
 def _check(fn: str, status: int) -> None:
     if status != FLP_OK:
         raise FlpError(fn, status)
@@ -724,7 +743,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         return loss
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, g):
         grads, ctx.grads = ctx.grads, None
         if grads is not None:
@@ -757,8 +776,7 @@ def linear_cross_entropy(hidden, weight, targets, bias=None, label_smoothing=0.0
 
     per row ("none"), summed ("sum") or averaged over the rows whose target lies in [0, V)
     ("mean", 0 when there are none); the other rows are padding with loss 0 and no gradient."""
-    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad
-                                              for t in (hidden, weight, bias)):
+    if not _wants_grad(hidden, weight, bias):
         return cross_entropy_forward(hidden, weight, targets, bias, label_smoothing, z_loss,
                                      reduction, return_stats=False)[0]
     return LinearCrossEntropy.apply(hidden, weight, targets, bias, label_smoothing, z_loss,
@@ -809,7 +827,7 @@ class Dropout(torch.autograd.Function):
         return dropout_forward(x, p, rng)
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, grad):
         (rng,) = ctx.saved_tensors
         if not ctx.needs_input_grad[0]:
@@ -935,10 +953,15 @@ class LayerNorm(torch.autograd.Function):
         return out
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, grad):
         x, weight, stats = ctx.saved_tensors
         need_x, need_w, need_b, _ = ctx.needs_input_grad
+        # A leaf's data may have been exchanged since the forward.
+        N, _, wd = _prepare_norm(x, weight, None)
+        if (grad.shape != x.shape or grad.dtype != x.dtype or grad.device != x.device
+                or stats.numel() != 2 * N or (weight is not None and wd != ctx.w_dtype)):
+            raise ValueError("x or weight has changed since the forward")
         mean = stats.data_ptr()
         dx, dw, db = _launch_norm_backward(grad.contiguous(), x, mean, mean + 2 * stats.numel(),
                                            weight, need_x, need_w, need_b, ctx.w_dtype)
@@ -948,7 +971,6 @@ class LayerNorm(torch.autograd.Function):
 def layer_norm(x, weight=None, bias=None, eps=1e-5):
     """(x - mean) / sqrt(var + eps) * weight + bias over the last dimension, differentiable in
     x, weight and bias; weight and bias [D] in the dtype of x or float32."""
-    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad
-                                              for t in (x, weight, bias)):
-        return layer_norm_forward(x, weight, bias, eps, return_stats=False)[0]
+    if not _wants_grad(x, weight, bias):
+        return _launch_norm(x, weight, bias, eps, False)[0]
     return LayerNorm.apply(x, weight, bias, eps)

@@ -284,3 +284,20 @@ def test_refusals():
         m.layer_norm_backward(go, x, mean[:4], rstd, w)
     with pytest.raises(TypeError):
         m.layer_norm_backward(go, x, mean, rstd, w, w_dtype=F32)
+
+
+@pytest.mark.parametrize("which", ["weight", "x", "device", "dtype"])
+def test_data_exchanged_before_the_backward_is_refused(which):
+    x, w, b, go = make(5, 96, F32, F32, seed=31)
+    x, w, b = (t.requires_grad_() for t in (x, w, b))
+    out = flp().layer_norm(x, w, b)
+    if which == "weight":
+        w.data = w.data[:48].clone()
+    elif which == "x":
+        x.data = x.data[:2].clone()
+    elif which == "device":
+        w.data = w.data.cpu()
+    else:
+        w.data = w.data.to(BF16)
+    with pytest.raises((ValueError, TypeError)):
+        torch.autograd.grad(out, [x], go)
