@@ -746,7 +746,7 @@ flp_status flp_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype 
 size_t flp_cross_entropy_backward_workspace_bytes(int64_t N, int64_t D, int64_t V,
                                                   flp_dtype x_dtype, int64_t chunk_rows) {
   const size_t b = flp_backward_workspace_bytes(N, D, V, x_dtype, x_dtype, chunk_rows);
-  return b == 0 ? 0 : loss_grad_layout(N, D, V).total + b;
+  return b == 0 ? 0 : loss_grad_layout(N, D, V, x_dtype).total + b;
 }
 
 flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
@@ -765,7 +765,7 @@ flp_status flp_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_dtype
   if (N == 0) return zero_sums(d_weight, size_t(V) * D * dtype_size(x_dtype), d_bias, V, s);
   if (!d_hidden && !d_weight && !d_bias) return FLP_OK;
   if ((st = check_device()) != FLP_OK) return st;
-  const LossGradLayout L = loss_grad_layout(N, D, V);
+  const LossGradLayout L = loss_grad_layout(N, D, V, x_dtype);
   LossGradArgs g{};
   g.N = N;
   g.V = V;

@@ -1093,22 +1093,24 @@ __global__ __launch_bounds__(256) void k_logits_bwd(LogitsArgs p) {
 // p.grad_out (c), p.onehot (o) and p.uniform (u); no temperature.
 // KEPT: the tile's products come from p.logits, where the chunk's forward left them, and
 // are not recomputed; everything after them is the same code, so dz has the same bits.
-template <class E, int BM, int WM, bool ODD, bool LOSS = false, bool KEPT = false>
+template <class E, int BM, int WM, bool ODD, bool LOSS = false, bool KEPT = false,
+          int BN = kTileCols>
 __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
-  using Eng = LogitEngine<E, BM, WM>;
+  using Eng = Engine<E, BM, BN, WM, 2>;
+  constexpr int kHalf = BN / 2;  // columns of a wave
   constexpr int RW = Eng::RW, WMB = Eng::WMB, WNB = Eng::WNB, NT = Eng::NT;
   constexpr bool kDirect = E::kSize == 2;  // 16-bit: stores straight from the registers
-  static_assert(!kDirect || (BM == kTileCols && WM == 4), "the 16-bit store path is laid out for "
-                                                          "the 256 x 256 tile with 4 x 2 waves");
+  static_assert(!kDirect || (BM == kTileCols && BN == kTileCols && WM == 4),
+                "the 16-bit store path is laid out for the 256 x 256 tile with 4 x 2 waves");
   extern __shared__ u32x4 smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: tile tests become scalar
   const int wm = wave % WM, wn = wave / WM, i = lane & 15, g = lane >> 4;
   const int nbm = int((p.rows + BM - 1) / BM);
-  const int nbn = int((p.V + kTileCols - 1) / kTileCols);
+  const int nbn = int(p.ldz / BN);  // the vocabulary padded to whole 256-column tiles
   int tm, tn;
   tile_of(blockIdx.x, nbm, nbn, tm, tn);
-  const int64_t row0 = int64_t(tm) * BM, col0 = int64_t(tn) * kTileCols;
+  const int64_t row0 = int64_t(tm) * BM, col0 = int64_t(tn) * BN;
   const int64_t kbytes = p.D * E::kSize;
 
   f32x4_t acc[WMB][WNB];
@@ -1123,16 +1125,16 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
 #pragma unroll
       for (int nb = 0; nb < WNB; ++nb)
         acc[mb][nb] = __builtin_nontemporal_load(keep + (mb * WNB + nb) * 64);
-  } else {
+  } else if (BN == kTileCols || col0 < p.V) {
     Eng::template run<ODD>(acc, reinterpret_cast<const char*>(p.hidden) + row0 * kbytes, kbytes,
                            p.rows - row0, reinterpret_cast<const char*>(p.weight) + col0 * kbytes,
                            kbytes, p.V - col0, kbytes, smem);
   }
 
-  const int64_t cw = col0 + wn * kHalfCols;
+  const int64_t cw = col0 + wn * kHalf;
   // Columns of this wave at or past lim are vocabulary padding (lim < 128 only in
   // the last vocabulary tile).
-  const int lim = int(p.V - cw < kHalfCols ? p.V - cw : kHalfCols);
+  const int lim = int(p.V - cw < kHalf ? p.V - cw : kHalf);
   f32x4_t csum[WNB];
   // The per-row inputs of the wave's rows and the bias are all loaded before the
   // first of them is used (rows past the batch read the last row, whose values are
@@ -1185,7 +1187,7 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
   }
   if (p.bias != nullptr) {
     const float* bw = p.bias + cw + 4 * g;
-    if (lim == kHalfCols) {  // wave-uniform: every column of the wave exists
+    if (lim == kHalf) {  // wave-uniform: every column of the wave exists
 #pragma unroll
       for (int nb = 0; nb < WNB; ++nb)
 #pragma unroll
@@ -1218,7 +1220,7 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
     rl[mb] = (rv ? rlse[mb] : 0.f) * (LOSS ? 1.0f : kLog2e);
     rk[mb] = invT * kLog2e;
     const int64_t trel = t - cw;
-    rtc[mb] = !valid ? -2 : (trel >= 0 && trel < kHalfCols) ? int(trel) : -1;
+    rtc[mb] = !valid ? -2 : (trel >= 0 && trel < kHalf) ? int(trel) : -1;
   }
   {
     // dz = G (onehot - exp(z - lse)) / T, kept in the accumulator registers, with
@@ -1293,7 +1295,7 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
 #pragma unroll
         for (int nb = 0; nb < WNB; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
-      if (lim < kHalfCols) {  // wave-uniform: the last vocabulary tile only
+      if (lim < kHalf) {  // wave-uniform: the last vocabulary tile only
 #pragma unroll
         for (int nb = 0; nb < WNB; ++nb)
 #pragma unroll
@@ -1418,18 +1420,24 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
   // is a reduce-scatter: a lane holds 32 column values (j = 4 nb + r); at the step
   // over lane bit m it keeps the half of its values that bit selects and adds the
   // partner's copy of that half, so after the four steps lane i holds the finished
-  // sums of columns j = 2i and 2i + 1 (30 exchanges instead of 128).
-  static_assert(WNB == 8, "the column reduction is laid out for 32 values per lane");
+  // sums of columns j = 2i and 2i + 1 (30 exchanges instead of 128).  With fewer values
+  // than lanes (a narrow tile) the last steps add the one value left in both partners.
+  constexpr int kVals = 4 * WNB, kLeft = kVals > 16 ? kVals / 16 : 1;
+  static_assert((WNB & (WNB - 1)) == 0, "the column reduction halves the values per lane");
   __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);  // [WM][256]
+  float* red = reinterpret_cast<float*>(smem);  // [WM][BN]
   {
-    float v[4 * WNB];
+    float v[kVals];
 #pragma unroll
     for (int nb = 0; nb < WNB; ++nb)
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[4 * nb + r] = csum[nb][r];
 #pragma unroll
-    for (int h = 2 * WNB, m = 8; h >= 2; h >>= 1, m >>= 1) {
+    for (int h = kVals / 2, m = 8; m >= 1; h >>= 1, m >>= 1) {
+      if (h == 0) {
+        v[0] += lane_xor(v[0], m);
+        continue;
+      }
       const bool up = (i & m) != 0;
 #pragma unroll
       for (int k = 0; k < h; ++k) {
@@ -1439,16 +1447,16 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
       }
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int j = 2 * i + e;
-      red[wm * kTileCols + wn * kHalfCols + (j >> 2) * 16 + 4 * g + (j & 3)] = v[e];
+    for (int e = 0; e < kLeft; ++e) {
+      const int j = kVals >= 16 ? kLeft * i + e : i * kVals / 16;
+      red[wm * BN + wn * kHalf + (j >> 2) * 16 + 4 * g + (j & 3)] = v[e];
     }
   }
   __syncthreads();
-  for (int c = tid; c < kTileCols; c += NT) {
+  for (int c = tid; c < BN; c += NT) {
     float s = red[c];
 #pragma unroll
-    for (int w = 1; w < WM; ++w) s += red[w * kTileCols + c];
+    for (int w = 1; w < WM; ++w) s += red[w * BN + c];
     p.dbias_part[int64_t(tm) * p.ldz + col0 + c] = s;
   }
 }
@@ -1718,18 +1726,25 @@ bool odd_stages(int64_t D) {
 
 template <class E, bool ODD, bool LOSS>
 hipError_t fwd_rows(const FwdArgs& a, hipStream_t s) {
+  const int64_t vt = (a.V + kTileCols - 1) / kTileCols;
   if (a.N <= 32) {
     // Over at most 256 vocabulary tiles (a vocabulary shard) the few workgroups each
     // wait out a load latency per stage with two stages, so they keep three in flight
     // (four LDS stages, 147 KB).  Over the full vocabulary the 2-stage tiles, two
     // workgroups per compute unit, stream W faster.
-    const int64_t vt = (a.V + kTileCols - 1) / kTileCols;
     if (vt <= 256) return fwd_cfg<E, 32, 2, ODD, LOSS, 4>(a, s);
     return fwd_cfg<E, 32, 2, ODD, LOSS>(a, s);
   }
-  if (a.N <= 64) return fwd_cfg<E, 64, 2, ODD, LOSS>(a, s);
-  if (a.N <= 128) return fwd_cfg<E, 128, 2, ODD, LOSS>(a, s);
-  return fwd_cfg<E, 256, 4, ODD, LOSS>(a, s);
+  // The largest tile that gives most compute units a workgroup: larger tiles read less of
+  // hidden and W per product, and every tile gives a row the same bits.  On MI355X:
+  // 64 x 256 x 4096 fp32 24 -> 16 us, 128 x 1024 x 16384 fp32 132 -> 48 and bf16 27 -> 16,
+  // 1000 x 1024 x 8192 fp32 244 -> 143; 64 x 1024 x 50257 fp32 in 32-row tiles 93, in
+  // 64-row tiles 81.
+  auto fills = [&](int64_t bm) { return (a.N + bm - 1) / bm * vt >= 160; };
+  if (a.N > 128 && fills(256)) return fwd_cfg<E, 256, 4, ODD, LOSS>(a, s);
+  if (a.N > 64 && fills(128)) return fwd_cfg<E, 128, 2, ODD, LOSS>(a, s);
+  if (fills(64)) return fwd_cfg<E, 64, 2, ODD, LOSS>(a, s);
+  return fwd_cfg<E, 32, 2, ODD, LOSS, 4>(a, s);
 }
 
 template <class E, bool LOSS = false>
@@ -1737,27 +1752,34 @@ hipError_t fwd_dispatch(const FwdArgs& a, hipStream_t s) {
   return odd_stages<E>(a.D) ? fwd_rows<E, true, LOSS>(a, s) : fwd_rows<E, false, LOSS>(a, s);
 }
 
-template <class E, int BM, int WM, bool ODD, bool LOSS>
+template <class E, int BM, int WM, bool ODD, bool LOSS, int BN = kTileCols>
 hipError_t dz_cfg(const DzArgs& a, hipStream_t s) {
-  using Eng = LogitEngine<E, BM, WM>;
+  using Eng = Engine<E, BM, BN, WM, 2>;
   constexpr size_t lds = Eng::kLds;
   static std::atomic<int> ready[kMaxDevices];
-  const hipError_t e = prepare(k_dz<E, BM, WM, ODD, LOSS>, lds, ready);
+  const hipError_t e = prepare(k_dz<E, BM, WM, ODD, LOSS, false, BN>, lds, ready);
   if (e != hipSuccess) return e;
-  const int64_t blocks = ((a.rows + BM - 1) / BM) * ((a.V + kTileCols - 1) / kTileCols);
-  hipLaunchKernelGGL((k_dz<E, BM, WM, ODD, LOSS>), dim3(unsigned(blocks)), dim3(Eng::NT), lds, s, a);
+  const int64_t blocks = ((a.rows + BM - 1) / BM) * (a.ldz / BN);
+  hipLaunchKernelGGL((k_dz<E, BM, WM, ODD, LOSS, false, BN>), dim3(unsigned(blocks)), dim3(Eng::NT),
+                     lds, s, a);
   return hipGetLastError();
 }
 
-// Few fp32 rows take a tile of 64 or 128 rows (64 rows per row wave as in the 256-row
-// tile, so the sums over rows have the same order and every output the same bits): the
-// fp32 products are slow enough that the empty rows of a 256-row tile cost more than its
-// W traffic.  64 x 256 x 4096 fp32 on MI355X: 72 -> 49 us.
+// fp32 products are slow enough that idle compute units cost more than narrow tiles' extra
+// reads, so few fp32 rows take tiles of 64 or 128 rows by 32 columns, and more of them
+// 256 rows by 32, 64 or 256 columns, the widest that give every compute unit a workgroup.
+// A row wave keeps the 64 rows it has in the 256 x 256 tile, so the sums over rows have the
+// same order and every output the same bits.  On MI355X, 256 columns and here: 64 x 256 x
+// 4096 49 -> 12 us, 128 x 1024 x 50257 161 -> 135, 256 x 256 x 4096 76 -> 19, 1000 x 1024 x
+// 8192 252 -> 145; 1000 x 512 x 16384 156 in 256 columns, 158 in 64, 170 in 32.
 template <class E, bool ODD, bool LOSS>
 hipError_t dz_rows(const DzArgs& a, hipStream_t s) {
   if constexpr (E::kSize == 4) {
-    if (a.rows <= 64) return dz_cfg<E, 64, 1, ODD, LOSS>(a, s);
-    if (a.rows <= 128) return dz_cfg<E, 128, 2, ODD, LOSS>(a, s);
+    if (a.rows <= 64) return dz_cfg<E, 64, 1, ODD, LOSS, 32>(a, s);
+    if (a.rows <= 128) return dz_cfg<E, 128, 2, ODD, LOSS, 32>(a, s);
+    const int64_t per_col = (a.rows + kDzRowTile - 1) / kDzRowTile * a.ldz;
+    if (per_col < 256 * 64) return dz_cfg<E, int(kDzRowTile), 4, ODD, LOSS, 32>(a, s);
+    if (per_col < 256 * kTileCols) return dz_cfg<E, int(kDzRowTile), 4, ODD, LOSS, 64>(a, s);
   }
   return dz_cfg<E, int(kDzRowTile), 4, ODD, LOSS>(a, s);
 }
@@ -2050,8 +2072,8 @@ hipError_t launch_dbias_fold(const float* part, int64_t n_parts, int64_t ldz, in
 const char* kernel_ids() {
   return "engine: direct global->LDS (buffer_load_dwordx4 lds, whole lines), 2 LDS stages x 128 B of K "
          "(3-8 for the small dX tiles), "
-         "mfma_f32_16x16x32_bf16 | 16x16x32_f16 | 16x16x4f32; k_fwd<BM 32/64/128 x BN 256 2x2 waves (BM 32: 4 stages over <= 256 vocabulary tiles), "
-         "BM 256 4x2 waves>; k_merge<1 or 8 rows; 256 leaves, fixed tree>; k_dz<BM 256 x BN 256, 4x2 waves; fp32 <= 128 rows: BM 64, 128>; "
+         "mfma_f32_16x16x32_bf16 | 16x16x32_f16 | 16x16x4f32; k_fwd<BM 32/64/128 x BN 256 2x2 waves (BM 32: 4 stages where few workgroups fit), "
+         "BM 256 4x2 waves>; k_merge<1 or 8 rows; 256 leaves, fixed tree>; k_dz<BM 256 x BN 256, 4x2 waves; fp32: BM 64, 128 x BN 32, BM 256 x BN 32, 64>; "
          "k_gemm dX, dW<256x224, 4x2 waves, K-blocked operands; dX for <= 1024 rows: 64x16, "
          "64x32, 128x64, 128x128>; k_transpose (K-blocked); "
          "k_dbias_fold; k_fill; k_logits_fwd, k_logits_bwd<one wave per row>; "

@@ -12,8 +12,10 @@ namespace {
 
 // Vocabulary slabs of d_hidden for few rows: up to 16 of at least 2048 columns.  bf16 on
 // MI355X, 1000 rows over 1344 x 50257: one walk 443 us, 4 slabs 250, 8 slabs 208, 16 slabs
-// 183 (24 of them 210: more sums to add); 64 rows over 992 x 20000: 55, 23, 23, 24.
-constexpr int64_t kMaxSlabs = 16, kMinSlab = 2048;
+// 183 (24 of them 210: more sums to add); 64 rows over 992 x 20000: 55, 23, 23, 24.  fp32,
+// whose products take longer than the sums: at least 1024 columns (64 x 256 x 4096: slabs of
+// 2048 20 us, 1024 15, 512 12; 4096 x 512 x 8192: 269, 277, 300).
+constexpr int64_t kMaxSlabs = 16, kMinSlab = 2048, kMinSlabF32 = 1024;
 
 
 constexpr int64_t kMaxIndex = std::numeric_limits<int64_t>::max() / 16;
@@ -588,7 +590,7 @@ float loss_zunit(int64_t V) {
   return u;
 }
 
-LossGradLayout loss_grad_layout(int64_t N, int64_t D, int64_t V) {
+LossGradLayout loss_grad_layout(int64_t N, int64_t D, int64_t V, flp_dtype x) {
   LossGradLayout L;
   const size_t row = align_up(size_t(N) * 4);
   L.onehot_off = row;
@@ -597,7 +599,7 @@ LossGradLayout loss_grad_layout(int64_t N, int64_t D, int64_t V) {
   L.slab_off = L.unscale_off + kAlign;
   L.total = L.slab_off;
   const int64_t ldz = round_up(V, kVocabTile);
-  const int64_t slabs = std::min<int64_t>(kMaxSlabs, ldz / kMinSlab);
+  const int64_t slabs = std::min<int64_t>(kMaxSlabs, ldz / (x == FLP_F32 ? kMinSlabF32 : kMinSlab));
   if (N <= kSlabRows && slabs > 1) {
     L.k_slab = round_up(ceil_div(ldz, slabs), kVocabTile);
     L.total += align_up(size_t(ceil_div(ldz, L.k_slab)) * size_t(N) * size_t(D) * 4);
@@ -676,7 +678,7 @@ flp_status validate_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_
   const Span outs[] = {span(d_hidden, size_t(N) * D * xs), span(d_weight, size_t(V) * D * xs),
                        span(d_bias, size_t(V) * 4), span(workspace, workspace_bytes)};
   if (any_alias(outs, 4, ins, 6)) return FLP_INVALID_ARGUMENT;
-  const size_t front = loss_grad_layout(N, D, V).total;
+  const size_t front = loss_grad_layout(N, D, V, x).total;
   if (workspace_bytes < front) return FLP_WORKSPACE_TOO_SMALL;
   const BwdLayout L = bwd_layout_for_bytes(N, D, V, x, x, workspace_bytes - front,
                                            d_hidden != nullptr, d_weight != nullptr,
@@ -687,7 +689,7 @@ flp_status validate_cross_entropy_backward(int64_t N, int64_t D, int64_t V, flp_
 LossAllLayout loss_all_layout(int64_t N, int64_t D, int64_t V, flp_dtype x, int64_t chunk,
                               bool need_dh, bool need_dw, bool need_db) {
   LossAllLayout L;
-  L.grad = loss_grad_layout(N, D, V);
+  L.grad = loss_grad_layout(N, D, V, x);
   L.bwd = bwd_layout_for_chunk(N, D, V, x, x, chunk, need_dh, need_dw, need_db);
   const size_t rows = size_t(L.bwd.chunk), n_vt = size_t(L.bwd.ldz / kVocabTile);
   size_t off = L.grad.total;

@@ -118,14 +118,14 @@ float loss_zunit(int64_t V);
 // tiles are too few, or fill their last wave of workgroups too little, for each to walk the
 // whole vocabulary (bf16 on MI355X, d_hidden in one walk and in slabs: 2048 x 2688 x 131072
 // 2374 and 1200 us, 4096 x 512 x 50257 828 and 257, 8192 x 512 x 50257 862 and 487,
-// 8192 x 2688 x 131072 5030 and 4728).  The slab length depends on V alone, so among such
-// batches a row's d_hidden does not depend on the others.
+// 8192 x 2688 x 131072 5030 and 4728).  The slab length depends on V and the type
+// alone, so among such batches a row's d_hidden does not depend on the others.
 constexpr int64_t kSlabRows = 8192;
 struct LossGradLayout {
   size_t softmax_off = 0, onehot_off = 0, uniform_off = 0, unscale_off = 0, slab_off = 0, total = 0;
   int64_t k_slab = 0;     // columns of a slab (a multiple of 256), 0: one walk
 };
-LossGradLayout loss_grad_layout(int64_t N, int64_t D, int64_t V);
+LossGradLayout loss_grad_layout(int64_t N, int64_t D, int64_t V, flp_dtype x);
 // Loss and gradients in one call: the gradient factors, the rows' losses and lse [2][N],
 // a chunk's forward (partials, target logits, sums of logits, fp32 products), and the
 // chunk's backward.

@@ -709,15 +709,19 @@ def _gradients_at_once(hidden, weight, reduction) -> bool:
     """Whether a training step's loss and gradients come from one call (the same bits).  It saves
     a product of N D V multiply-adds and moves 8 bytes per logit more, and a few launches more:
     measured on MI355X, it wins from D = 1024 on in bfloat16 (4096 x 512 x 50257: 1090 us in two
-    calls, 1207 in one; 4096 x 2048 x 50257: 3092 and 2816), in float32 past the 128 rows that the
-    two calls take in smaller tiles, and where that product takes 20 us."""
+    calls, 1207 in one; 4096 x 2048 x 50257: 3092 and 2816), in float32 where its tiles of 256
+    rows by 256 columns give most compute units a workgroup (the two calls take smaller ones:
+    1000 x 1024 x 8192 548 us in two calls, 556 in one, 1000 x 512 x 16384 560 and 464), and where
+    that product takes 20 us."""
     D = hidden.shape[-1]
     N, V = hidden.numel() // max(D, 1), weight.shape[0]
     if reduction == "none":
         return False
     if hidden.dtype == torch.bfloat16:
         return D >= 1024 and N * D * V >= 2 * 10 ** 10
-    return hidden.dtype == torch.float32 and D >= 128 and N > 128 and N * D * V >= 2 * 10 ** 9
+    tiles = -(-N // 256) * -(-V // 256)
+    return (hidden.dtype == torch.float32 and D >= 128 and N > 128 and tiles >= 192
+            and N * D * V >= 2 * 10 ** 9)
 
 
 class LinearCrossEntropy(torch.autograd.Function):

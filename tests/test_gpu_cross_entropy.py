@@ -408,6 +408,22 @@ def test_slabs_of_the_vocabulary(dtype, N):
     compare(*make(N, 96, 9001, dtype, 30 + N), s=0.1, c=1e-3, reduction="mean")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [4100, 9001])
+def test_padding_rows_change_no_bit(V, dtype):
+    """More rows, all of them padding, move the batch through the tiles of every row count: each
+    sum keeps its order, so nothing changes."""
+    h, w, b, t, up = make(60, 96, V, dtype, 33)
+    want = run(h, w, b, t, up, 0.1, 1e-3, "sum")
+    for N in (64, 100, 128, 250, 300, 700, 2100, 4200):
+        x = torch.cat([h, torch.randn(N - 60, 96, device="cuda").to(dtype)])
+        y = torch.cat([t, torch.full((N - 60,), -1, device="cuda", dtype=t.dtype)])
+        got = run(x, w, b, y, up, 0.1, 1e-3, "sum")
+        assert torch.equal(got[1][:60], want[1]) and torch.equal(got[2][:60], want[2]), N
+        assert not got[2][60:].any(), N
+        assert torch.equal(got[3], want[3]) and torch.equal(got[4], want[4]), N
+
+
 @pytest.mark.parametrize("N", [8192, 8193])
 def test_last_row_count_of_slabs(N):
     compare(*make(N, 32, 4500, BF16, 29), s=0.1, reduction="sum")
