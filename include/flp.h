@@ -360,7 +360,7 @@ flp_status flp_logits_backward_indexed(int64_t N, int64_t V, flp_dtype x_dtype,
  * The backward sorts (id, token) pairs with a stable radix sort and sums each
  * id's segment in fp32 in a fixed order (token order inside each group of 32
  * sorted positions, groups in ascending order): d_weight is bitwise
- * reproducible.  N < 2^31,
+ * reproducible.  N < 2^31 (2^30 in the backward),
  * V < 2^31 - 1.
  */
 flp_status flp_embedding_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,

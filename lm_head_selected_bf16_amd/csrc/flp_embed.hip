@@ -56,28 +56,30 @@ __device__ __forceinline__ u32x4 scale_chunk(u32x4 v, float scale) {
 }
 
 // One wave per token row, four rows per workgroup: 16-byte chunks, copied as they are
-// (T = void) or multiplied by `scale`.
+// (T = void) or multiplied by `scale`.  A launch holds fewer than 2^32 threads, so past
+// 2^25 rows a wave takes several.
 template <class T>
 __global__ __launch_bounds__(256) void k_embed_fwd(const u32x4* __restrict__ weight,
                                                    const void* __restrict__ ids, int i64,
                                                    int64_t N, int64_t V, int64_t row_vec,
                                                    float scale, u32x4* __restrict__ out) {
   const int lane = threadIdx.x & 63;
-  const int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (i >= N) return;
-  const int64_t v = load_id(ids, i64 != 0, i);
-  u32x4* dst = out + i * row_vec;
-  if (v >= 0 && v < V) {
-    const u32x4* src = weight + v * row_vec;
-    for (int64_t c = lane; c < row_vec; c += 64) {
-      if constexpr (std::is_void<T>::value)
-        dst[c] = src[c];
-      else
-        dst[c] = scale_chunk<T>(src[c], scale);
+  for (int64_t i = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); i < N;
+       i += int64_t(gridDim.x) * 4) {
+    const int64_t v = load_id(ids, i64 != 0, i);
+    u32x4* dst = out + i * row_vec;
+    if (v >= 0 && v < V) {
+      const u32x4* src = weight + v * row_vec;
+      for (int64_t c = lane; c < row_vec; c += 64) {
+        if constexpr (std::is_void<T>::value)
+          dst[c] = src[c];
+        else
+          dst[c] = scale_chunk<T>(src[c], scale);
+      }
+    } else {
+      const u32x4 z = {0u, 0u, 0u, 0u};
+      for (int64_t c = lane; c < row_vec; c += 64) dst[c] = z;
     }
-  } else {
-    const u32x4 z = {0u, 0u, 0u, 0u};
-    for (int64_t c = lane; c < row_vec; c += 64) dst[c] = z;
   }
 }
 
@@ -449,7 +451,8 @@ hipError_t launch_embedding_forward(flp_dtype x, const void* weight, const void*
   ProfScope ps(FLP_K_EMBEDDING, s);
   const int64_t row_vec = D * int64_t(dtype_size(x)) / 16;
   auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(unsigned((N + 3) / 4)), dim3(256), 0, s,
+    const int64_t grid = std::min<int64_t>((N + 3) / 4, 1 << 23);
+    hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(256), 0, s,
                        static_cast<const u32x4*>(weight), ids, int(i64), N, V, row_vec, scale,
                        static_cast<u32x4*>(out));
   };

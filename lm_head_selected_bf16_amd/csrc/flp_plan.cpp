@@ -560,6 +560,8 @@ flp_status validate_embedding_backward(int64_t N, int64_t D, int64_t V, flp_dtyp
   flp_status st = check_embedding_dims(N, D, V, x, id);
   if (st != FLP_OK) return st;
   if (dw != x && dw != FLP_F32) return FLP_UNSUPPORTED_DTYPE;
+  // 128 threads per group of 32 positions, and a launch holds fewer than 2^32
+  if (N >= (int64_t(1) << 30)) return FLP_UNSUPPORTED_SHAPE;
   if (!d_weight) return FLP_INVALID_ARGUMENT;
   if (N == 0) return validate_empty_sums(D, V, dtype_size(x), nullptr, nullptr, d_weight, dw, nullptr);
   if (!grad || !ids || !workspace) return FLP_INVALID_ARGUMENT;

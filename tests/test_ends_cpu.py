@@ -136,6 +136,9 @@ def test_scaled_embedding_keeps_the_gates_of_the_lookup():
                                                  0)) == "FLP_INVALID_ARGUMENT"
     assert name(abi.flp_embedding_scaled_backward(N, D, V, BF16, A[0], A[1], I64, 2.0, A[2], BF16,
                                                   A[3], 64, 0)) == "FLP_WORKSPACE_TOO_SMALL"
+    # more positions than one launch takes
+    assert name(abi.flp_embedding_scaled_backward(2 ** 30, 8, V, BF16, A[0], A[1], I64, 2.0, A[2],
+                                                  BF16, A[3], 2 ** 60, 0)) == "FLP_UNSUPPORTED_SHAPE"
 
 
 def ce_fwd(**kw):

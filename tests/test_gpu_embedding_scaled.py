@@ -85,6 +85,16 @@ def test_autograd_and_ids_outside_the_table():
     assert empty.shape == (0, 3, 64) and not dw.any()
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.5])
+def test_more_rows_than_one_launch_has_waves(scale):
+    N = 2 ** 26 + 37
+    w = torch.randn(50, 8, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(0, 50, (N,), device="cuda", dtype=torch.int32)
+    out = flp().embedding_forward(w, ids, scale)
+    for lo in (0, 2 ** 25 - 20, 2 ** 26 - 20, N - 40):  # a half is exact
+        assert torch.equal(out[lo:lo + 40], w[ids[lo:lo + 40].long()] * scale)
+
+
 def test_refusals():
     m = flp()
     w = torch.randn(50, 64, device="cuda")
