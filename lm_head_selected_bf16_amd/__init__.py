@@ -40,10 +40,8 @@ from .torch_ops import (LinearLogp, backward, backward_workspace_bytes,  # noqa:
                         backward_indexed, forward_indexed, linear_logp_indexed,
                         logits_backward_indexed, logits_forward_indexed, logits_logp_indexed,
                         Embedding, embedding, embedding_backward, embedding_forward,
-                        LinearCrossEntropy, cross_entropy_backward, cross_entropy_forward,
-                        cross_entropy_gradients,
-                        linear_cross_entropy,
-                        Dropout, dropout, dropout_forward, LayerNorm, layer_norm,
+                        cross_entropy_backward, cross_entropy_forward, cross_entropy_gradients,
+                        linear_cross_entropy, dropout, dropout_forward, layer_norm,
                         layer_norm_backward, layer_norm_forward)
 
 __all__ = [
@@ -68,14 +66,14 @@ __all__ = [
     "logits_logp_indexed",
     "Embedding", "embedding", "embedding_forward", "embedding_backward",
     "flp_embedding_scaled_forward", "flp_embedding_scaled_backward",
-    "LinearCrossEntropy", "linear_cross_entropy", "cross_entropy_forward",
+    "linear_cross_entropy", "cross_entropy_forward",
     "cross_entropy_backward", "flp_cross_entropy_forward", "flp_cross_entropy_backward",
     "flp_cross_entropy_forward_workspace_bytes", "flp_cross_entropy_backward_workspace_bytes",
     "cross_entropy_gradients", "flp_cross_entropy_gradients",
     "flp_cross_entropy_gradients_workspace_bytes", "flp_scale_inplace",
     "FLP_REDUCE_NONE", "FLP_REDUCE_SUM", "FLP_REDUCE_MEAN",
-    "Dropout", "dropout", "dropout_forward", "flp_dropout",
-    "LayerNorm", "layer_norm", "layer_norm_forward", "layer_norm_backward",
+    "dropout", "dropout_forward", "flp_dropout",
+    "layer_norm", "layer_norm_forward", "layer_norm_backward",
     "flp_layer_norm_forward", "flp_layer_norm_backward",
     "flp_layer_norm_backward_workspace_bytes",
 ]

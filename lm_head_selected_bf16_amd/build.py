@@ -1,4 +1,5 @@
-"""Build the HIP library libflp.so in-tree with hipcc for gfx950.
+"""Build the HIP library libflp.so in-tree with hipcc for gfx950, and the autograd nodes over
+it, _flp_torch.so, with g++.
 
     python -m lm_head_selected_bf16_amd.build
 
@@ -17,6 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libflp.so")
+NODES = os.path.join(PKG, "_flp_torch.so")
 SOURCES = ["flp_kernels.hip", "flp_rows.hip", "flp_loss.hip", "flp_embed.hip", "flp_dropout.hip", "flp_norm.hip",
            "flp_probe.hip", "flp_noalloc.hip",
            "flp_api.cpp", "flp_plan.cpp"]
@@ -58,7 +60,37 @@ def build(verbose: bool = False) -> str:
     if verbose and errs.strip():
         print(errs, file=sys.stderr)
     os.replace(tmp, LIB)
+    build_nodes(verbose)
     return LIB
+
+
+def build_nodes(verbose: bool = False) -> str:
+    """Compile the autograd nodes (host code over the C ABI, with torch's headers) into
+    _flp_torch.so.  Returns the path."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    tmp = NODES + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-DTORCH_EXTENSION_NAME=_flp_torch", "-DTORCH_API_INCLUDE_EXTENSION_H",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include")]
+    for d in [*include_paths(), sysconfig.get_path("include")]:
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "flp_torch.cpp"), "-o", tmp]
+    cmd += [f"-L{d}" for d in library_paths()]
+    cmd += ["-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stderr}")
+    if verbose and res.stderr.strip():
+        print(res.stderr, file=sys.stderr)
+    os.replace(tmp, NODES)
+    return NODES
 
 
 if __name__ == "__main__":

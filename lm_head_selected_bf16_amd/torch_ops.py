@@ -16,6 +16,7 @@ targets and temperature are not differentiable.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import math
 from typing import Optional, Tuple
 
@@ -56,15 +57,23 @@ def _on(device: torch.device):
     return torch.cuda.device(device)
 
 
-def _first_order(backward):
-    """A backward whose gradients cannot be differentiated again: under create_graph their use
-    in a second backward raises.  (once_differentiable on every call would cost 3 us.)"""
-    guarded = once_differentiable(backward)
+_NODES = None
 
-    def run(ctx, *grads):
-        return guarded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
 
-    return run
+def _nodes():
+    """The autograd nodes of csrc/flp_torch.cpp, bound to the loaded library."""
+    global _NODES
+    if _NODES is None:
+        lib = _abi.load()
+        try:
+            from . import _flp_torch
+        except ModuleNotFoundError as e:
+            raise ImportError("_flp_torch.so is missing: build it with `python -m "
+                              "lm_head_selected_bf16_amd.build`") from e
+        _flp_torch.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                         for name in _abi.SIGNATURES})
+        _NODES = _flp_torch
+    return _NODES
 
 
 def _wants_grad(*tensors) -> bool:
@@ -562,29 +571,24 @@ def embedding_backward(grad: torch.Tensor, ids: torch.Tensor, num_embeddings: in
     return d_weight
 
 
-class Embedding(torch.autograd.Function):
-    """Autograd node of the untied embedding lookup; the ids and the scale are not
-    differentiable."""
+class Embedding:
+    """The differentiable lookup, under the name of its autograd node."""
 
     @staticmethod
-    def forward(ctx, weight, ids, scale=1.0):
-        ctx.save_for_backward(ids)
-        ctx.num_embeddings = int(weight.shape[0])
-        ctx.scale = scale
-        return embedding_forward(weight, ids, scale)
-
-    @staticmethod
-    def backward(ctx, grad):
-        (ids,) = ctx.saved_tensors
-        if not ctx.needs_input_grad[0]:
-            return None, None, None
-        return (embedding_backward(grad.contiguous(), ids, ctx.num_embeddings, scale=ctx.scale),
-                None, None)
+    def apply(weight, ids, scale=1.0):
+        return embedding(weight, ids, scale)
 
 
 def embedding(weight, ids, scale=1.0):
     """scale * weight[ids] (zero rows for ids outside [0, V)), differentiable in weight."""
-    return Embedding.apply(weight, ids, scale)
+    if not _wants_grad(weight):
+        return embedding_forward(weight, ids, scale)
+    _prepare_embedding(weight, ids)
+    dev = weight.device
+    if ids.device != dev:
+        raise ValueError("weight and ids must be on one device")
+    with _on(dev):
+        return _nodes().embedding(weight, ids, _embedding_scale(scale), _stream(dev))
 
 
 # ---- linear cross entropy -----------------------------------------------------------------------
@@ -724,30 +728,24 @@ def _gradients_at_once(hidden, weight, reduction) -> bool:
             and N * D * V >= 2 * 10 ** 9)
 
 
-class LinearCrossEntropy(torch.autograd.Function):
-    """Autograd node of the linear cross entropy.  The forward saves the rows' lse and the
-    backward recomputes the logits; or, where that is faster, the forward makes the gradients for
-    an upstream gradient of 1 along with the loss, and the first backward multiplies them by the
+class LossAndGradients(torch.autograd.Function):
+    """Autograd node of the linear cross entropy where its forward makes the gradients for an
+    upstream gradient of 1 along with the loss: the first backward multiplies them by the
     upstream gradient in place (a second rounding unless that is a power of two) and hands them
     over.  Any further backward through the same node recomputes."""
 
     @staticmethod
     def forward(ctx, hidden, weight, targets, bias, label_smoothing, z_loss, reduction):
-        terms = (label_smoothing, z_loss, reduction)
-        ctx.grads = None
-        if _gradients_at_once(hidden, weight, reduction):
-            need_h, need_w, _, need_b = ctx.needs_input_grad[:4]
-            loss, stats, *ctx.grads = cross_entropy_gradients(
-                hidden, weight, targets, bias, *terms, need_hidden=need_h, need_weight=need_w,
-                need_bias=need_b)
-        else:
-            loss, stats = cross_entropy_forward(hidden, weight, targets, bias, *terms)
+        ctx.terms = (label_smoothing, z_loss, reduction)
+        need_h, need_w, _, need_b = ctx.needs_input_grad[:4]
+        loss, stats, *ctx.grads = cross_entropy_gradients(
+            hidden, weight, targets, bias, *ctx.terms, need_hidden=need_h, need_weight=need_w,
+            need_bias=need_b)
         ctx.save_for_backward(hidden, weight, targets, bias, stats)
-        ctx.terms = terms
         return loss
 
     @staticmethod
-    @_first_order
+    @once_differentiable
     def backward(ctx, g):
         grads, ctx.grads = ctx.grads, None
         if grads is not None:
@@ -783,8 +781,14 @@ def linear_cross_entropy(hidden, weight, targets, bias=None, label_smoothing=0.0
     if not _wants_grad(hidden, weight, bias):
         return cross_entropy_forward(hidden, weight, targets, bias, label_smoothing, z_loss,
                                      reduction, return_stats=False)[0]
-    return LinearCrossEntropy.apply(hidden, weight, targets, bias, label_smoothing, z_loss,
-                                    reduction)
+    if _gradients_at_once(hidden, weight, reduction):
+        return LossAndGradients.apply(hidden, weight, targets, bias, label_smoothing, z_loss,
+                                      reduction)
+    _, red = _prepare_loss(hidden, weight, targets, bias, reduction)
+    dev = hidden.device
+    with _on(dev):
+        return _nodes().cross_entropy(hidden, weight, targets, bias, label_smoothing, z_loss, red,
+                                      DEFAULT_BWD_WORKSPACE, _stream(dev))
 
 
 # ---- dropout ------------------------------------------------------------------------------------
@@ -792,8 +796,7 @@ def linear_cross_entropy(hidden, weight, targets, bias=None, label_smoothing=0.0
 # The mask is a function of the element's position, p and rng (int64 [2] on the device: seed and
 # offset), so it is drawn again in the backward instead of being stored.
 
-def dropout_forward(x: torch.Tensor, p: float, rng: torch.Tensor) -> torch.Tensor:
-    """x with each element dropped with probability p and the others scaled, through flp_dropout."""
+def _prepare_dropout(x, p, rng) -> float:
     if x.dtype not in _X_DTYPES:
         raise TypeError("x must be bfloat16, float16 or float32")
     if not x.is_cuda or not x.is_contiguous():
@@ -805,38 +808,19 @@ def dropout_forward(x: torch.Tensor, p: float, rng: torch.Tensor) -> torch.Tenso
     p = float(p)
     if not 0.0 <= p <= 1.0:
         raise ValueError("p must be between 0 and 1")
-    return _launch_dropout(x, p, rng)
+    return p
 
 
-def _launch_dropout(x, p, rng):
-    """The call on arguments that have been checked (the backward's were in the forward)."""
+def dropout_forward(x: torch.Tensor, p: float, rng: torch.Tensor) -> torch.Tensor:
+    """x with each element dropped with probability p and the others scaled, through flp_dropout."""
+    p = _prepare_dropout(x, p, rng)
     dev = x.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _launch_dropout(x, p, rng)
-    out = torch.empty_like(x)
-    st = _abi.flp_dropout(x.numel(), _X_DTYPES[x.dtype], x.data_ptr(), p, rng.data_ptr(),
-                          out.data_ptr(), _stream(dev))
+    with _on(dev):
+        out = torch.empty_like(x)
+        st = _abi.flp_dropout(x.numel(), _X_DTYPES[x.dtype], x.data_ptr(), p, rng.data_ptr(),
+                              out.data_ptr(), _stream(dev))
     _check("flp_dropout", st)
     return out
-
-
-class Dropout(torch.autograd.Function):
-    """Autograd node of dropout: the backward is the same call on the gradient."""
-
-    @staticmethod
-    def forward(ctx, x, p, rng):
-        ctx.save_for_backward(rng)
-        ctx.p = float(p)
-        return dropout_forward(x, p, rng)
-
-    @staticmethod
-    @_first_order
-    def backward(ctx, grad):
-        (rng,) = ctx.saved_tensors
-        if not ctx.needs_input_grad[0]:
-            return None, None, None
-        return _launch_dropout(grad.contiguous(), ctx.p, rng), None, None
 
 
 def dropout(x, p, rng):
@@ -844,7 +828,12 @@ def dropout(x, p, rng):
     differentiable in x.  rng: int64 [2] on the device of x, (seed, offset); give every call of a
     step its own offset.  The backward reads rng again, so write a new pair into a new tensor
     rather than changing this one before the backward has run."""
-    return Dropout.apply(x, p, rng)
+    if not _wants_grad(x):
+        return dropout_forward(x, p, rng)
+    p = _prepare_dropout(x, p, rng)
+    dev = x.device
+    with _on(dev):
+        return _nodes().dropout(x, p, rng, _stream(dev))
 
 
 # ---- layer norm ---------------------------------------------------------------------------------
@@ -876,28 +865,18 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                        return_stats: bool = True):
     """(out, mean, rstd) of the layer norm over the last dimension through
     flp_layer_norm_forward; mean and rstd are float32 of the leading shape, or None."""
-    out, stats = _launch_norm(x, weight, bias, eps, return_stats)
-    return (out, stats[0], stats[1]) if return_stats else (out, None, None)
-
-
-def _launch_norm(x, weight, bias, eps, return_stats):
-    """(out, stats) with stats float32 [2, *leading shape] (mean, then rstd) or None."""
     N, D, wd = _prepare_norm(x, weight, bias)
     dev = x.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _launch_norm(x, weight, bias, eps, return_stats)
-    out = torch.empty_like(x)
-    stats, mean, rstd = None, 0, 0
-    if return_stats:
-        stats = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev)
-        mean = stats.data_ptr()
-        rstd = mean + 4 * N
-    st = _abi.flp_layer_norm_forward(N, D, _X_DTYPES[x.dtype], x.data_ptr(), _X_DTYPES[wd],
-                                     _ptr(weight), _ptr(bias), float(eps), out.data_ptr(), mean,
-                                     rstd, _stream(dev))
+    with _on(dev):
+        out = torch.empty_like(x)
+        mean = rstd = None
+        if return_stats:
+            mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev)
+        st = _abi.flp_layer_norm_forward(N, D, _X_DTYPES[x.dtype], x.data_ptr(), _X_DTYPES[wd],
+                                         _ptr(weight), _ptr(bias), float(eps), out.data_ptr(),
+                                         _ptr(mean), _ptr(rstd), _stream(dev))
     _check("flp_layer_norm_forward", st)
-    return out, stats
+    return out, mean, rstd
 
 
 def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
@@ -919,62 +898,31 @@ def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Ten
             raise ValueError(f"{name} must be contiguous float32 with the leading shape of x")
     if any(t.device != x.device for t in (grad_out, mean, rstd)):
         raise ValueError("grad_out, mean and rstd must be on the device of x")
-    return _launch_norm_backward(grad_out, x, mean.data_ptr(), rstd.data_ptr(), weight, need_input,
-                                 need_weight, need_bias, wd)
-
-
-def _launch_norm_backward(grad, x, mean, rstd, weight, need_input, need_weight, need_bias, wd):
-    """The call on arguments that have been checked; mean and rstd are addresses."""
     dev = x.device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _launch_norm_backward(grad, x, mean, rstd, weight, need_input, need_weight,
-                                         need_bias, wd)
-    D = x.shape[-1]
     N = x.numel() // D
-    d_x = torch.empty_like(x) if need_input else None
-    d_weight = torch.empty(D, dtype=wd, device=dev) if need_weight else None
-    d_bias = torch.empty(D, dtype=wd, device=dev) if need_bias else None
-    ws, size = None, 0
-    if need_weight or need_bias:
-        size = max(_abi.flp_layer_norm_backward_workspace_bytes(N, D), 16)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    st = _abi.flp_layer_norm_backward(N, D, _X_DTYPES[x.dtype], grad.data_ptr(), x.data_ptr(),
-                                      _X_DTYPES[wd], _ptr(weight), mean, rstd, _ptr(d_x),
-                                      _ptr(d_weight), _ptr(d_bias), _ptr(ws), size, _stream(dev))
+    with _on(dev):
+        d_x = torch.empty_like(x) if need_input else None
+        d_weight = torch.empty(D, dtype=wd, device=dev) if need_weight else None
+        d_bias = torch.empty(D, dtype=wd, device=dev) if need_bias else None
+        ws, size = None, 0
+        if need_weight or need_bias:
+            size = max(_abi.flp_layer_norm_backward_workspace_bytes(N, D), 16)
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        st = _abi.flp_layer_norm_backward(N, D, _X_DTYPES[x.dtype], grad_out.data_ptr(),
+                                          x.data_ptr(), _X_DTYPES[wd], _ptr(weight),
+                                          mean.data_ptr(), rstd.data_ptr(), _ptr(d_x),
+                                          _ptr(d_weight), _ptr(d_bias), _ptr(ws), size,
+                                          _stream(dev))
     _check("flp_layer_norm_backward", st)
     return d_x, d_weight, d_bias
-
-
-class LayerNorm(torch.autograd.Function):
-    """Autograd node of the layer norm; the forward saves the mean and rstd of every row."""
-
-    @staticmethod
-    def forward(ctx, x, weight, bias, eps):
-        out, stats = _launch_norm(x, weight, bias, eps, True)
-        ctx.save_for_backward(x, weight, stats)
-        ctx.w_dtype = next((t.dtype for t in (weight, bias) if t is not None), x.dtype)
-        return out
-
-    @staticmethod
-    @_first_order
-    def backward(ctx, grad):
-        x, weight, stats = ctx.saved_tensors
-        need_x, need_w, need_b, _ = ctx.needs_input_grad
-        # A leaf's data may have been exchanged since the forward.
-        N, _, wd = _prepare_norm(x, weight, None)
-        if (grad.shape != x.shape or grad.dtype != x.dtype or grad.device != x.device
-                or stats.numel() != 2 * N or (weight is not None and wd != ctx.w_dtype)):
-            raise ValueError("x or weight has changed since the forward")
-        mean = stats.data_ptr()
-        dx, dw, db = _launch_norm_backward(grad.contiguous(), x, mean, mean + 2 * stats.numel(),
-                                           weight, need_x, need_w, need_b, ctx.w_dtype)
-        return dx, dw, db, None
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5):
     """(x - mean) / sqrt(var + eps) * weight + bias over the last dimension, differentiable in
     x, weight and bias; weight and bias [D] in the dtype of x or float32."""
     if not _wants_grad(x, weight, bias):
-        return _launch_norm(x, weight, bias, eps, False)[0]
-    return LayerNorm.apply(x, weight, bias, eps)
+        return layer_norm_forward(x, weight, bias, eps, return_stats=False)[0]
+    _prepare_norm(x, weight, bias)
+    dev = x.device
+    with _on(dev):
+        return _nodes().layer_norm(x, weight, bias, eps, _stream(dev))

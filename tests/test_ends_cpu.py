@@ -302,3 +302,30 @@ def test_python_checks():
         flp.linear_cross_entropy(x, x, t, reduction="average")
     with pytest.raises(ValueError, match="GPU"):
         flp.linear_cross_entropy(x, x, t)
+
+
+def test_a_status_inside_an_autograd_node_is_the_librarys_error():
+    """A tensor that never reached a GPU: the library refuses the call (there is no GPU here, or
+    the scale is not finite), and the node's exception is the one of every other entry point."""
+    import torch
+
+    from lm_head_selected_bf16_amd import torch_ops
+    w = torch.zeros(4, 8, requires_grad=True)
+    ids = torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(abi.FlpError, match="flp_embedding_scaled_forward failed: "
+                                           "FLP_INVALID_ARGUMENT") as e:
+        torch_ops._nodes().embedding(w, ids, INF, 0)
+    assert e.value.status != 0
+
+
+def test_missing_nodes_are_an_error(monkeypatch):
+    import sys
+
+    import lm_head_selected_bf16_amd as m
+    from lm_head_selected_bf16_amd import torch_ops
+    torch_ops._nodes()
+    monkeypatch.setattr(torch_ops, "_NODES", None)
+    monkeypatch.delattr(m, "_flp_torch")
+    monkeypatch.setitem(sys.modules, "lm_head_selected_bf16_amd._flp_torch", None)
+    with pytest.raises(ImportError, match="_flp_torch.so is missing"):
+        torch_ops._nodes()

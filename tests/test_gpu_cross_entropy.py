@@ -482,6 +482,44 @@ def test_autograd_asks_only_for_what_needs_a_gradient():
     assert torch.equal(one, dh) and torch.equal(one.float() * 2, two.float())
 
 
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("need", range(1, 8))
+def test_autograd_gives_each_leaf_its_gradient(need, bias):
+    m = flp()
+    h, w, b, t, up = make(33, 64, 700, F16, 61, bias=bias)
+    ask = [need & 1, need & 2, need & 4 and bias]
+    if not any(ask):
+        return
+    _, stats = m.cross_entropy_forward(h, w, t, b, 0.1, 1e-3, "none")
+    g = up[:1].expand(33)
+    want = m.cross_entropy_backward(g.contiguous(), stats, h, w, t, b, 0.1, 1e-3, "none")
+    leaves = [None if x is None else x.clone().requires_grad_(bool(a))
+              for x, a in zip((h, w, b), ask)]
+    loss = m.linear_cross_entropy(leaves[0], leaves[1], t, leaves[2], 0.1, 1e-3, "none")
+    got = torch.autograd.grad(loss, [x for x, a in zip(leaves, ask) if a], g)
+    for x, v in zip(got, [v for v, a in zip(want, ask) if a]):
+        assert torch.equal(x, v)
+
+
+@pytest.mark.parametrize("which", ["hidden", "weight", "bias", "device", "dtype"])
+def test_data_exchanged_before_the_backward_is_refused(which):
+    h, w, b, t, up = make(9, 64, 300, F32, 62)
+    h, w, b = (x.requires_grad_() for x in (h, w, b))
+    loss = flp().linear_cross_entropy(h, w, t, b)
+    if which == "hidden":
+        h.data = h.data[:4].clone()
+    elif which == "weight":
+        w.data = w.data[:100].clone()
+    elif which == "bias":
+        b.data = b.data[:100].clone()
+    elif which == "device":
+        w.data = w.data.cpu()
+    else:
+        w.data = w.data.to(BF16)
+    with pytest.raises((ValueError, TypeError)):
+        torch.autograd.grad(loss, [h])
+
+
 def test_empty_batch():
     m = flp()
     w = torch.randn(300, 64, device="cuda", dtype=BF16, requires_grad=True)

@@ -301,3 +301,29 @@ def test_data_exchanged_before_the_backward_is_refused(which):
         w.data = w.data.to(BF16)
     with pytest.raises((ValueError, TypeError)):
         torch.autograd.grad(out, [x], go)
+
+
+@pytest.mark.parametrize("need", range(1, 8))
+@pytest.mark.parametrize("weight,bias", [(True, True), (True, False), (False, True), (False, False)])
+def test_autograd_gives_each_leaf_its_gradient(weight, bias, need):
+    """Every combination of parameters that are there and of leaves that ask, with an upstream
+    gradient that is a broadcast view, against the functional calls."""
+    m = flp()
+    x, w, b, go = make(37, 193, BF16, F32, 41, weight=weight, bias=bias)
+    ask = [need & 1, need & 2 and w is not None, need & 4 and b is not None]
+    if not any(ask):
+        return
+    _, mean, rstd = m.layer_norm_forward(x, w, b)
+    up = go[:1].expand(37, 193)
+    want = m.layer_norm_backward(up.contiguous(), x, mean, rstd, w, w_dtype=None if w is not None
+                                 else F32 if b is not None else BF16)
+    leaves = [None if t is None else t.clone().requires_grad_(bool(a))
+              for t, a in zip((x, w, b), ask)]
+    out = m.layer_norm(*leaves)
+    asked = [t for t, a in zip(leaves, ask) if a]
+    first = torch.autograd.grad(out, asked, up, retain_graph=True)
+    again = torch.autograd.grad(out, asked, up)
+    for f, a, v in zip(first, again, [v for v, a in zip(want, ask) if a]):
+        assert torch.equal(f, v) and torch.equal(a, v)
+    with pytest.raises(RuntimeError):  # the graph is gone
+        torch.autograd.grad(out, asked, up)
