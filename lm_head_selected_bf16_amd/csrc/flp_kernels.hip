@@ -2080,7 +2080,7 @@ const char* kernel_ids() {
          "rows: k_mark, k_compact, k_gather, k_scatter_rows, k_scatter_hidden; "
          "cross entropy: k_fwd, k_merge, k_dz with loss terms, k_loss_sum, k_loss_grad, k_gemm dX "
          "over vocabulary slabs and k_slab_fold (<= 8192 rows); "
-         "embedding: k_embed_fwd (scaled), radix sort (k_sort_hist, k_sort_scatter; 9-bit digits, "
+         "embedding: k_embed_fwd (scaled), radix sort (k_sort_hist, k_sort_scatter; 9-bit digits; <= 4096 tokens: k_sort_rank; "
          "zero riders), k_embed_runs<32-position groups>, k_embed_rows; k_dropout; layer norm: "
          "k_norm_fwd_row, k_norm_bwd_row<one or four waves per row>, k_norm_fold; wide rows: "
          "k_norm_fwd, k_norm_dx, k_norm_params";

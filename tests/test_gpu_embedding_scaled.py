@@ -85,6 +85,35 @@ def test_autograd_and_ids_outside_the_table():
     assert empty.shape == (0, 3, 64) and not dw.any()
 
 
+@pytest.mark.parametrize("ids", ["uniform", "few", "same", "dropped"])
+@pytest.mark.parametrize("idt", [torch.int32, torch.int64])
+def test_sorting_by_counting_keeps_the_order_of_the_radix_passes(ids, idt):
+    """Up to 4096 tokens are sorted in another way.  Dropped ids behind them change nothing else,
+    so the longer list has to give the same bits (of sums whose order shows in the last bit), and
+    shorter ones are checked with whole numbers."""
+    V, D = 3001, 40
+    g = torch.Generator().manual_seed(9)
+    top = {"uniform": V, "few": 7, "same": 1, "dropped": V}[ids]
+    t = torch.randint(0, top, (4096,), generator=g)
+    if ids == "dropped":
+        t[torch.rand(4096, generator=g) < 0.4] = V
+        t[::11] = -5
+    grad = torch.randn(4096, D, generator=g)
+    t, grad = t.to(idt).cuda(), grad.cuda()
+    m = flp()
+    short = m.embedding_backward(grad, t, V)
+    longer = m.embedding_backward(torch.cat([grad, torch.ones(1000, D, device="cuda")]),
+                                  torch.cat([t, torch.full((1000,), -1, dtype=idt, device="cuda")]), V)
+    assert torch.equal(short, longer)
+    whole = (grad * 8).round()
+    for N in (1, 2, 63, 64, 65, 255, 257, 1000, 2047, 2049, 4095):
+        want = torch.zeros(V, D, dtype=torch.float64, device="cuda")
+        ok = (t[:N] >= 0) & (t[:N] < V)
+        want.index_add_(0, t[:N][ok].long(), whole[:N][ok].double())
+        assert torch.equal(m.embedding_backward(whole[:N].contiguous(), t[:N].contiguous(), V).double(),
+                           want), N
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.5])
 def test_more_rows_than_one_launch_has_waves(scale):
     N = 2 ** 26 + 37
