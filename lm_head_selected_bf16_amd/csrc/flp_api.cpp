@@ -107,6 +107,10 @@ flp_status enqueue_backward(const BwdLayout& L, int64_t N, int64_t D, int64_t V,
       z.onehot = loss->onehot + r0;
       z.uniform = loss->uniform + r0;
       z.lse_rest = loss->lse_rest + r0;
+      if (d_bias != nullptr && L.n_chunks == 1 && rows <= kDzRowTile) {
+        z.d_bias = d_bias;
+        z.bias_scale = scale;
+      }
     }
     if (launch_dz(x_dtype, z, s) != hipSuccess) return FLP_HIP_ERROR;
     const int64_t kpad = round_up(rows, kTokPad);  // dz^T and hidden^T are zero past rows
@@ -168,7 +172,7 @@ flp_status enqueue_backward(const BwdLayout& L, int64_t N, int64_t D, int64_t V,
       g.scale = scale;
       if (launch_dw(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
     }
-    if (d_bias) {
+    if (d_bias && z.d_bias == nullptr) {
       if (launch_dbias_fold(dbp, (rows + kDzRowTile - 1) / kDzRowTile, L.ldz, V, d_bias, c == 0, scale,
                             s) != hipSuccess)
         return FLP_HIP_ERROR;

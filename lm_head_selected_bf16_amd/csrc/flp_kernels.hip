@@ -1457,7 +1457,11 @@ __global__ __launch_bounds__(128 * WM) void k_dz(DzArgs p) {
     float s = red[c];
 #pragma unroll
     for (int w = 1; w < WM; ++w) s += red[w * BN + c];
-    p.dbias_part[int64_t(tm) * p.ldz + col0 + c] = s;
+    if (LOSS && p.d_bias != nullptr) {  // the only row tile: finished, as k_dbias_fold would
+      if (col0 + c < p.V) p.d_bias[col0 + c] = (0.0f + s) * (p.bias_scale ? *p.bias_scale : 1.0f);
+    } else {
+      p.dbias_part[int64_t(tm) * p.ldz + col0 + c] = s;
+    }
   }
 }
 
@@ -1610,14 +1614,18 @@ __global__ __launch_bounds__(256) void k_transpose(const T* __restrict__ src, in
   bool check = true;
   if constexpr (LIVE) check = also.take(r0, src, rows, rows_pad, dst);
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  for (int k = ty; k < 64; k += 4) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {  // sixteen loads in flight
+    const int k = ty + 4 * u;
     const int64_t r = r0 + k, c = c0 + tx;
     bool in = r < rows && c < cols;
     if constexpr (LIVE) in = in && (!check || live(r));
     tile[k][tx] = in ? src[r * ld_src + c] : T(0);
   }
   __syncthreads();
-  for (int k = ty; k < 64; k += 4) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const int k = ty + 4 * u;
     const int64_t c = c0 + k, r = r0 + tx;
     if (r < rows_pad && c < cols) dst[kblk<128 / sizeof(T)>(c, r, cols)] = tile[tx][k];
   }

@@ -84,6 +84,8 @@ struct DzArgs {
   const float* onehot = nullptr;   // the target entry's added term
   const float* uniform = nullptr;  // every entry's added term
   const float* lse_rest = nullptr;
+  float* d_bias = nullptr;         // set: the batch is one row tile, whose sums are d_bias itself
+  const float* bias_scale = nullptr;  // what they are multiplied by, or null
   float* logits = nullptr;         // products kept by the forward, or null to recompute
 };
 struct LogitsArgs {
