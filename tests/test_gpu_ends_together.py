@@ -135,3 +135,54 @@ def test_step_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(out, calls()):
             assert torch.equal(a, b), rep
+
+
+def autograd_step(p, ids, targets, rng):
+    """Loss and gradients of one step, on leaves of its own."""
+    m = flp()
+    leaf = {k: v.detach().requires_grad_() for k, v in p.items() if k != "mix"}
+    x = m.dropout(m.embedding(leaf["table"], ids, 4.0), 0.1, rng)
+    loss = m.linear_cross_entropy(m.layer_norm(x, leaf["w"], leaf["b"]), leaf["head"], targets,
+                                  None, 0.1, 1e-3)
+    names = sorted(leaf)
+    return (loss.detach(),) + torch.autograd.grad(loss, [leaf[k] for k in names])
+
+
+def test_autograd_step_in_a_graph():
+    """The same through autograd, whose backward runs on a thread of its own: captured once,
+    replayed with new inputs between eager steps, the same bits."""
+    ids, targets, p, rng = step_inputs(torch.bfloat16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        autograd_step(p, ids, targets, rng)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = autograd_step(p, ids, targets, rng)
+    for rep in range(4):
+        nids, ntargets, _, _ = step_inputs(torch.bfloat16, seed=30 + rep)
+        ids.copy_(nids)
+        targets.copy_(ntargets)
+        rng[1] = rep
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, autograd_step(p, ids, targets, rng)):
+            assert torch.equal(a, b), rep
+
+
+def test_autograd_steps_on_two_streams():
+    """Two steps, each on a stream of its own: forward and backward stay on it."""
+    steps = [step_inputs(torch.bfloat16, seed=50 + k) for k in range(2)]
+    want = [autograd_step(p, ids, t, rng) for ids, t, p, rng in steps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(3):
+        got = []
+        for (ids, t, p, rng), s in zip(steps, streams):
+            with torch.cuda.stream(s):
+                got.append(autograd_step(p, ids, t, rng))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
