@@ -434,7 +434,8 @@ flp_status flp_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p, co
  *
  * A vocabulary entry masked through the bias (-infinity, or the lowest float32) has
  * probability 0; with label smoothing an entry of -infinity makes the loss infinite, as
- * its definition does.  The rows' losses and lse do not depend on the other rows; the
+ * its definition does.  A NaN logit makes the loss and lse of its row NaN (unless the row
+ * is padding).  The rows' losses and lse do not depend on the other rows; the
  * reductions add the rows in an order fixed by N.
  */
 typedef enum flp_reduction {

@@ -733,7 +733,10 @@ __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
     const int rl = wm * RW + mb * 16 + i;
     const int64_t row = row0 + rl;
     const float M = fmaxf(red[rl], red[BM + rl]) * invT[mb];  // row max of z
-    const float Ml = M * kLog2e;
+    // Without a finite logit or +inf in the tile's row, M is -inf and the exponents are taken
+    // as they are: entries of -inf then add 0 and NaN entries make the tile's sum NaN.
+    const float base = M == -INFINITY ? 0.f : M;
+    const float Ml = base * kLog2e;
     const float k = invT[mb] * kLog2e;
     if (wn == 0 && g == 0) red[4 * BM + rl] = M;
     // exp(z - M) = 2^(y (log2 e / T) - M log2 e): one FMA per logit
@@ -747,7 +750,7 @@ __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
 #pragma unroll
         for (int nb = 0; nb < WNB; ++nb)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) e[nb][r] = fast_exp2((acc[mb][nb][r] - M) * kLog2e);
+          for (int r = 0; r < 4; ++r) e[nb][r] = fast_exp2((acc[mb][nb][r] - base) * kLog2e);
       }
     }
     float s = lane_sum<WNB>(e);
@@ -801,8 +804,10 @@ __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
 constexpr int kMergeLeaves = 256;
 constexpr int64_t kMergeRowMax = 2048;  // batches up to this size: one row per workgroup
 
+// A tile of nothing but -inf has the sum 0; one of -inf and NaN has the sum NaN, which has to
+// reach the row's.
 __device__ __forceinline__ float merge_term(float2 q, float M) {
-  return q.x == -INFINITY ? 0.f : q.y * fast_exp2((q.x - M) * kLog2e);
+  return q.x == -INFINITY ? q.y : q.y * fast_exp2((q.x - M) * kLog2e);
 }
 
 //

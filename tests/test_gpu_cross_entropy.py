@@ -220,6 +220,38 @@ def test_masked_vocabulary(dtype, low):
           + 1500 * U * (r["dz"].abs() @ r["w"].abs()) + rounding(dtype, r["dh"]) * 1.01)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("V", [700, 1500, 70001, 140001])
+def test_nan_logits_reach_the_loss(V, dtype):
+    """NaN rows of W that fill whole vocabulary tiles (and one that does not): the loss of every
+    counted row is NaN, its log-probability too, and a padded row's loss stays 0.  Tiles of
+    nothing but -infinity beside them add nothing."""
+    m = flp()
+    h, w, b, t, up = make(20, 64, V, dtype, 22)
+    t = torch.where(t >= 0, t % 200, t)
+    ok = (t >= 0) & (t < V)
+    for lo, hi in ((256, 512), (300, 301), (256, V)):
+        bad = w.clone()
+        bad[lo:hi] = float("nan")
+        for bias in (None, torch.where(torch.arange(V, device="cuda") < 210, b, -math.inf)):
+            for s, c in ((0.0, 0.0), (0.1, 1e-3)):
+                loss, stats = m.cross_entropy_forward(h, bad, t, bias, s, c, "none")
+                assert bool(loss[ok].isnan().all()) and not loss[~ok].any()
+                assert bool(stats[0][ok].isnan().all())
+                assert bool(m.linear_cross_entropy(h, bad, t, bias, s, c).isnan())
+            assert bool(m.linear_logp(h, bad, t, bias)[ok].isnan().all())
+            if dtype != F16:
+                assert bool(m.cross_entropy_gradients(h, bad, t, bias)[0].isnan())
+    # the masked vocabulary alone
+    bias = torch.where(torch.arange(V, device="cuda") < 210, b, -math.inf)
+    part, _ = m.forward_partial(h, w, t, 0, V, bias)
+    assert bool((part[1:, :, 0] == -math.inf).all()) and not part[1:, :, 1].any()
+    loss = m.linear_cross_entropy(h, w, t, bias, reduction="none")
+    few = m.linear_cross_entropy(h, w[:210].contiguous(), torch.where(ok, t, -1),
+                                 b[:210].contiguous(), reduction="none")
+    assert torch.equal(loss, few) and bool(loss.isfinite().all())
+
+
 def test_lowest_everywhere_is_uniform():
     """Every entry masked with the lowest fp32 value: the row is uniform over the vocabulary."""
     h, w, b, t, up = make(20, 64, 700, F32, 11, ignored=0.0)
