@@ -5,8 +5,10 @@
 //   d_x    = rstd (g - mean_d(g) - xhat mean_d(g xhat)),  g = grad w
 //   d_w    = sum_i grad xhat,  d_b = sum_i grad
 //
-// All arithmetic is fp32 (the variance from the centred values, so a large common
-// offset of a row does not cancel); out, d_x, d_w and d_b are rounded once.
+// All arithmetic is fp32; out, d_x, d_w and d_b are rounded once.  The variance comes from
+// centred values, so a large common offset of a row does not cancel, and the mean is
+// corrected by theirs (Centre): a sum of D values over D is off by some of its last
+// places, which a row far from zero with little spread would show.
 //
 // Bound by memory: the forward reads x and writes out, the backward reads grad and x and
 // writes d_x.
@@ -34,6 +36,18 @@ template <class T>
 __device__ __forceinline__ float to_f32(T v) {
   return float(v);
 }
+
+// Mean and rstd of a row from a first mean m and the means u of x - m and q of (x - m)^2:
+// x - m is exact where the offset is large, so m + u is the mean up to half a step, and a
+// constant row has exactly its value as mean and no variance.
+struct Centre {
+  float mean, rstd;
+  __device__ __forceinline__ Centre(float m, float u, float q, float eps) : mean(m + u) {
+    const float d = fmaf(-u, u, q);
+    const float var = d >= 0.f ? d : d < 0.f ? 0.f : q;  // neither: u^2 and q passed fp32
+    rstd = 1.0f / sqrtf(var + eps);
+  }
+};
 
 // ---- rows held in registers (up to kTeamMax elements) ------------------------------------------------
 //
@@ -87,6 +101,20 @@ __device__ __forceinline__ float team_sum(float x, float* red) {
   return (red[first] + red[first + 1]) + (red[first + 2] + red[first + 3]);
 }
 
+// Two sums over a team of four waves, behind one barrier.
+__device__ __forceinline__ void team_sum2(float& x, float& y, float (&red)[3][8]) {
+  x = wave_sum(x);
+  y = wave_sum(y);
+  const int wave = threadIdx.x >> 6, first = wave & ~3;
+  if ((threadIdx.x & 63) == 0) {
+    red[1][wave] = x;
+    red[2][wave] = y;
+  }
+  __syncthreads();
+  x = (red[1][first] + red[1][first + 1]) + (red[1][first + 2] + red[1][first + 3]);
+  y = (red[2][first] + red[2][first + 1]) + (red[2][first + 2] + red[2][first + 3]);
+}
+
 constexpr int kTeamThreads = 512;
 // Workgroups of a forward launch: two per compute unit (256 and 1024 measured the same).
 constexpr int64_t kFwdGroups = 512;
@@ -128,7 +156,7 @@ template <class T, int TEAM, int NCH>
 __global__ __launch_bounds__(kTeamThreads) void k_norm_fwd_row(NormFwdArgs p) {
   constexpr int kTeams = kTeamThreads / TEAM;
   extern __shared__ f32x4 lds[];
-  __shared__ float red[2][2][8];
+  __shared__ float red[2][3][8];
   const int t = threadIdx.x % TEAM;
   const int64_t D = p.D, step = int64_t(gridDim.x) * kTeams;
   const int plane = int((D + kChunk - 1) / kChunk);
@@ -147,28 +175,49 @@ __global__ __launch_bounds__(kTeamThreads) void k_norm_fwd_row(NormFwdArgs p) {
       for (int e = 0; e < kChunk; ++e) q += to_f32(T(cur.c[k].v[e]));
       s += q;
     }
-    const float mean = team_sum<TEAM>(s, red[turn][0]) * inv;
-    float var = 0.f;
+    const float m = team_sum<TEAM>(s, red[turn][0]) * inv;
+    // the thread's part of the sums q of the centred values' squares and u of the values
+    float q = 0.f, u = 0.f;
+    auto centred = [&](auto squares, auto values) {
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int64_t n = D - int64_t(k * TEAM + t) * kChunk;
-      float q = 0.f;
-      if (n >= kChunk) {
+      for (int k = 0; k < NCH; ++k) {
+        const int64_t n = D - int64_t(k * TEAM + t) * kChunk;
+        float cq = 0.f, cu = 0.f;
+        auto add = [&](float v) {
+          if constexpr (decltype(squares)::value) cq = fmaf(v, v, cq);
+          if constexpr (decltype(values)::value) cu += v;
+        };
+        if (n >= kChunk) {
 #pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-          const float v = to_f32(T(cur.c[k].v[e])) - mean;
-          q = fmaf(v, v, q);
+          for (int e = 0; e < kChunk; ++e) add(to_f32(T(cur.c[k].v[e])) - m);
+        } else if (n > 0) {
+#pragma unroll
+          for (int e = 0; e < kChunk; ++e) add(e < n ? to_f32(T(cur.c[k].v[e])) - m : 0.f);
         }
-      } else if (n > 0) {
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-          const float v = e < n ? to_f32(T(cur.c[k].v[e])) - mean : 0.f;
-          q = fmaf(v, v, q);
-        }
+        q += cq;
+        u += cu;
       }
-      var += q;
+    };
+    // One wave corrects its mean only where that is four times the spread or more: below, a
+    // sum's relative rounding moves xhat by at most five times itself (the size above takes
+    // 36.7 us, 37.7 with all rows corrected, 35.5 with none).  A team of four waves always
+    // does, behind the barrier of the squares (4096 x 8192 bf16 27.2 us, 26.5 without the
+    // correction; behind a barrier of its own 34).
+    if constexpr (TEAM == 64) {
+      centred(std::true_type{}, std::false_type{});
+      q = wave_sum(q) * inv;
+      if (!(m * m < 16.0f * q)) {
+        centred(std::false_type{}, std::true_type{});
+        u = wave_sum(u) * inv;
+      }
+    } else {
+      centred(std::true_type{}, std::true_type{});
+      team_sum2(u, q, red[turn]);
+      u *= inv;
+      q *= inv;
     }
-    const float rstd = 1.0f / sqrtf(fmaf(team_sum<TEAM>(var, red[turn][1]), inv, p.eps));
+    const Centre at(m, u, q, p.eps);
+    const float mean = at.mean, rstd = at.rstd;
     T* out = static_cast<T*>(p.out) + row * D;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
@@ -346,13 +395,16 @@ __global__ __launch_bounds__(kRowThreads) void k_norm_fwd(NormFwdArgs p) {
     T* out = static_cast<T*>(p.out) + row * p.D;
     float s = 0.f;
     for (int64_t d = threadIdx.x; d < p.D; d += kRowThreads) s += to_f32(x[d]);
-    const float mean = block_sum(s, red) / float(p.D);
-    float q = 0.f;
+    const float m = block_sum(s, red) / float(p.D);
+    float u = 0.f, q = 0.f;
     for (int64_t d = threadIdx.x; d < p.D; d += kRowThreads) {
-      const float c = to_f32(x[d]) - mean;
+      const float c = to_f32(x[d]) - m;
+      u += c;
       q = fmaf(c, c, q);
     }
-    const float rstd = 1.0f / sqrtf(block_sum(q, red) / float(p.D) + p.eps);
+    u = block_sum(u, red) / float(p.D);
+    const Centre at(m, u, block_sum(q, red) / float(p.D), p.eps);
+    const float mean = at.mean, rstd = at.rstd;
     for (int64_t d = threadIdx.x; d < p.D; d += kRowThreads) {
       float y = (to_f32(x[d]) - mean) * rstd;
       if (w != nullptr) y *= to_f32(w[d]);

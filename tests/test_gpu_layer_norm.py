@@ -1,6 +1,8 @@
 """Layer norm against its definition in 64 bits: widths from one element to rows wider than a
 workgroup holds, rows off the 16-byte grid, every type and parameter combination, the gradients
 against the formula and against differences, determinism, streams and graphs."""
+import math
+
 import pytest
 import torch
 
@@ -173,6 +175,42 @@ def test_degenerate_rows():
     compare(x[rows].contiguous(), w, b, go[rows].contiguous(), eps=0.0)
     one = torch.full((5, 1), 3.0, device="cuda")
     assert torch.equal(m.layer_norm(one, w[:1], b[:1]), b[:1].expand(5, 1))
+
+
+@pytest.mark.parametrize("D", [1, 7, 520, 1000, 1345, 2000, 2688, 5000, 12000, 16385, 20000])
+@pytest.mark.parametrize("dtype,values", [(BF16, (3.0, 4080.0, -0.0996)), (F16, (3.0, 2047.0, -6e4)),
+                                          (F32, (3.0, 4080.3, -0.1, 1e30))])
+def test_constant_rows_are_their_bias(D, dtype, values):
+    """Whatever the value: the mean is the value itself and nothing is left of the row.  rstd is
+    that of the variance 0, which the first mean's error e <= k |x| enters only through the
+    rounding of e^2 - e^2 (at most 4 U e^2)."""
+    m = flp()
+    x = torch.tensor(values, device="cuda").to(dtype)[:, None].expand(-1, D).contiguous()
+    _, w, b, _ = make(1, D, dtype, dtype, 14)
+    y, mean, rstd = m.layer_norm_forward(x, w, b)
+    assert torch.equal(y, b.expand_as(y))
+    assert torch.equal(mean, x[:, 0].float())
+    e = (D / 256 + 32) * U * x[:, 0].double().abs()
+    rel = (rstd.double() * math.sqrt(1e-5) - 1).abs()
+    ok = e < 1e15  # beyond, e^2 passes fp32
+    assert bool((rel <= 4 * U + 2 * U * e ** 2 / 1e-5)[ok].all())
+
+
+@pytest.mark.parametrize("D", [520, 1000, 2688, 6000, 20000])
+def test_mean_of_rows_far_from_zero(D):
+    """Rows whose spread is a small part of their offset.  The first mean is off by k |x|, with
+    k the error of a sum as above; the values centred by it are rounded once, their mean is off by
+    k + 4 U of their mean size, and the corrected mean is rounded to half a step."""
+    m = flp()
+    g = torch.Generator().manual_seed(15)
+    x = torch.randn(16, D, generator=g)
+    x = (x * torch.logspace(-3, 1, 16)[:, None] + torch.logspace(1, 5, 16)[:, None]).cuda()
+    y, mean, rstd = m.layer_norm_forward(x)
+    ref = x.double().mean(1)
+    c = (x.double() - ref[:, None]).abs().mean(1)
+    k = (D / 256 + 32) * U
+    off = k * x.double().abs().mean(1)
+    check("mean", mean, ref, 1.01 * U * ref.abs() + (k + 5 * U) * (c + off))
 
 
 def test_empty_batch():
