@@ -523,7 +523,9 @@ flp_status flp_scale_inplace(int64_t n, flp_dtype x_dtype, void* x, const float*
  *   x, out    [N, D] x_dtype (FLP_BF16, FLP_F16 or FLP_F32).  Any D >= 1 (below 2^27):
  *             rows need no alignment beyond their element size.
  *   weight, bias  [D] of w_dtype (x_dtype or FLP_F32), each may be NULL (1 and 0).
- *   eps       >= 0, finite.  A constant row with eps = 0 has no norm (NaN).
+ *   eps       >= 0, finite.  A constant row with eps = 0 has no norm (NaN).  The sums are
+ *             fp32: a row whose squared deviations add up to more than fp32 holds (3.4e38)
+ *             has rstd 0, one whose squares all vanish (below 2^-150) counts as constant.
  *   out_mean, out_rstd  [N] float32, or NULL; the backward reads both.
  *
  * fp32 arithmetic, one rounding per output element; a row's results do not depend on

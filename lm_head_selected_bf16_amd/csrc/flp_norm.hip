@@ -289,7 +289,6 @@ __global__ __launch_bounds__(kTeamThreads) void k_norm_bwd_row(NormBwdArgs p) {
   __syncthreads();
   for (int64_t r0 = int64_t(blockIdx.x) * p.slab_rows; r0 < r1; r0 += kTeams) {
     const bool live = row < r1;
-    // sums over gw and gw (x - mean): the second takes its rstd afterwards
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
@@ -301,11 +300,11 @@ __global__ __launch_bounds__(kTeamThreads) void k_norm_bwd_row(NormBwdArgs p) {
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
         const float gr = to_f32(T(cg.c[k].v[e]));
-        const float xc = to_f32(T(cx.c[k].v[e])) - mean;
+        const float xh = (to_f32(T(cx.c[k].v[e])) - mean) * rstd;
         const float gw = gr * (e < 4 ? w0[e & 3] : w1[e & 3]);
         q1 += gw;
-        q2 = fmaf(gw, xc, q2);
-        aw[k][e] = fmaf(gr * rstd, xc, aw[k][e]);
+        q2 = fmaf(gw, xh, q2);
+        aw[k][e] = fmaf(gr, xh, aw[k][e]);
         ab[k][e] += gr;
       }
       s1 += q1;
@@ -313,9 +312,10 @@ __global__ __launch_bounds__(kTeamThreads) void k_norm_bwd_row(NormBwdArgs p) {
     }
     if (p.d_x != nullptr) {  // uniform over the launch
       const float m1 = team_sum<TEAM>(s1, red[turn][0]) * inv;
-      const float m2 = team_sum<TEAM>(s2, red[turn][1]) * inv * rstd;
-      // d_x = rstd gw - rstd m1 - (x - mean) rstd^2 m2
-      const float a0 = -(rstd * m1), a1 = -(rstd * rstd * m2);
+      const float m2 = team_sum<TEAM>(s2, red[turn][1]) * inv;
+      // d_x = rstd (gw - m1 - (x - mean) rstd m2): no factor rstd^2, which passes fp32 for
+      // rows that rstd itself, and d_x, can still take (a spread of 2^-65 with eps = 0)
+      const float a = -(rstd * m2);
       T* dx = static_cast<T*>(p.d_x) + row * D;
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kTeamThreads) void k_norm_bwd_row(NormBwdArgs p) {
         for (int e = 0; e < kChunk; ++e) {
           const float xc = to_f32(T(cx.c[k].v[e])) - mean;
           const float gw = to_f32(T(cg.c[k].v[e])) * (e < 4 ? w0[e & 3] : w1[e & 3]);
-          cx.c[k].v[e] = T(fmaf(gw, rstd, fmaf(xc, a1, a0)));
+          cx.c[k].v[e] = T(rstd * fmaf(xc, a, gw - m1));
         }
         cx.c[k].store(dx + int64_t(c) * kChunk, live ? D - int64_t(c) * kChunk : 0);
       }

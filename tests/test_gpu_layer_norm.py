@@ -213,6 +213,54 @@ def test_mean_of_rows_far_from_zero(D):
     check("mean", mean, ref, 1.01 * U * ref.abs() + (k + 5 * U) * (c + off))
 
 
+@pytest.mark.parametrize("D", [64, 777, 3000, 9000, 12289])
+@pytest.mark.parametrize("k", [-62, 55])
+def test_scale_of_the_rows(D, k):
+    """Without eps the norm does not depend on the rows' scale, and a power of two changes no
+    rounding: with x times 2^k and grad_out times 2^-30, out has the same bits, d_weight and
+    d_bias those times 2^-30 and d_x those times 2^(-30 - k)."""
+    m = flp()
+    g = torch.Generator().manual_seed(16)
+    x = (torch.randn(9, D, generator=g) + 0.25).cuda()
+    _, w, b, go = make(9, D, F32, F32, 17)
+    y, mean, rstd = m.layer_norm_forward(x, w, b, 0.0)
+    dx, dw, db = m.layer_norm_backward(go, x, mean, rstd, w)
+    x2, go2 = x * 2.0 ** k, go * 2.0 ** -30
+    y2, mean2, rstd2 = m.layer_norm_forward(x2, w, b, 0.0)
+    dx2, dw2, db2 = m.layer_norm_backward(go2, x2, mean2, rstd2, w)
+    assert torch.equal(y2, y) and torch.equal(rstd2 * 2.0 ** k, rstd)
+    assert torch.equal(dx2.double() * 2.0 ** (30 + k), dx.double())
+    assert torch.equal(dw2 * 2.0 ** 30, dw) and torch.equal(db2 * 2.0 ** 30, db)
+
+
+@pytest.mark.parametrize("D", [64, 777, 3000, 9000, 12289])
+def test_rows_whose_variance_is_subnormal(D):
+    """A spread of 2^-65 and eps = 0: the variance 2^-130 is held to steps of 2^-149, so each
+    square and their mean are off by half a step: 2^-19 of the variance, 2^-20 of rstd (times 2:
+    a row's variance is above half its expectation).  1 / rstd^2 passes fp32, rstd does not."""
+    m = flp()
+    g = torch.Generator().manual_seed(18)
+    x = torch.randn(9, D, generator=g).cuda()
+    _, w, b, go = make(9, D, F32, F32, 19)
+    y, mean, rstd = m.layer_norm_forward(x, w, b, 0.0)
+    dx, dw, db = m.layer_norm_backward(go, x, mean, rstd, w)
+    x2 = x * 2.0 ** -65
+    y2, mean2, rstd2 = m.layer_norm_forward(x2, w, b, 0.0)
+    dx2, dw2, db2 = m.layer_norm_backward(go, x2, mean2, rstd2, w)
+    rel = 2.0 ** -19 + 8 * U
+    r = reference(x, w, b, go, 0.0)
+    # out = fma(xhat, w, b): each of the two is rounded by itself, off by U |out| from the sum
+    check("out", y2, y.double(), rel * (r["xhat"] * w.double()).abs() + 2.1 * U * y.double().abs())
+    gw, xh = r["g"].abs(), r["xhat"].abs()
+    size = r["rstd"][:, None] * (gw + gw.mean(1, keepdim=True)
+                                 + 3 * xh * (gw * xh).mean(1, keepdim=True))
+    # each d_x is off by a rounding of each term and the sums' (k), with its own order of rows
+    check("d_x", dx2.double() * 2.0 ** -65, dx.double(), (rel + 2 * (D / 256 + 40) * U) * size)
+    # nine terms added in the same order
+    check("d_weight", dw2, dw.double(), (rel + 20 * U) * (go.double().abs() * xh).sum(0))
+    assert torch.equal(db2, db)
+
+
 def test_empty_batch():
     m = flp()
     x = torch.empty(0, 64, device="cuda", requires_grad=True)
