@@ -21,6 +21,7 @@ import math
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _abi
@@ -77,6 +78,13 @@ def _nodes():
 
 
 def _wants_grad(*tensors) -> bool:
+    """Whether a gradient is asked for.  Forward-mode differentiation is refused, as the autograd
+    nodes refuse it: a plain call would drop the inputs' tangents in silence."""
+    if forward_ad._current_level >= 0:  # inside a dual level (unpack_dual: 1 us per tensor)
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("forward-mode differentiation of this operator is not "
+                                          "implemented")
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:

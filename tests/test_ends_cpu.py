@@ -318,6 +318,27 @@ def test_a_status_inside_an_autograd_node_is_the_librarys_error():
     assert e.value.status != 0
 
 
+@pytest.mark.parametrize("grad", [False, True])
+def test_forward_mode_differentiation_is_refused(grad):
+    """An input with a tangent, whether or not anything requires a gradient: an error, not an
+    output without a tangent."""
+    from torch.autograd import forward_ad
+    x, w, b = torch.ones(4, 32), torch.ones(7, 32), torch.ones(7)
+    p, q = torch.ones(32), torch.ones(32)
+    ids = torch.zeros(4, dtype=torch.int64)
+    rng = torch.zeros(2, dtype=torch.int64)
+    calls = [(lambda w: flp.embedding(w, ids), [w]),
+             (lambda x: flp.dropout(x, 0.1, rng), [x]),
+             (lambda *a: flp.layer_norm(*a), [x, p, q]),
+             (lambda x, w, b: flp.linear_cross_entropy(x, w, ids, b), [x, w, b])]
+    with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+        for call, args in calls:
+            for k, t in enumerate(args):
+                dual = forward_ad.make_dual(t, torch.ones_like(t))
+                with pytest.raises(NotImplementedError, match="forward-mode"):
+                    call(*args[:k], dual, *args[k + 1:])
+
+
 def test_missing_nodes_are_an_error(monkeypatch):
     import sys
 

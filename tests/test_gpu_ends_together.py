@@ -186,3 +186,25 @@ def test_autograd_steps_on_two_streams():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_forward_mode_differentiation_is_refused():
+    """An input with a tangent: an error, where a plain call would give an output without one;
+    inside a dual level without tangents nothing changes."""
+    from torch.autograd import forward_ad
+    m = flp()
+    ids, targets, p, rng = step_inputs(torch.float32)
+    x = torch.randn(targets.numel(), p["head"].shape[1], device="cuda")
+    t = targets.reshape(-1)
+    calls = [(lambda w: m.embedding(w, ids), p["table"].detach()),
+             (lambda x: m.dropout(x, 0.1, rng), x),
+             (lambda x: m.layer_norm(x, p["w"].detach(), p["b"].detach()), x),
+             (lambda x: m.linear_cross_entropy(x, p["head"].detach(), t), x)]
+    want = [f(v) for f, v in calls]
+    with forward_ad.dual_level():
+        for (f, v), y in zip(calls, want):
+            assert torch.equal(f(v), y)
+            with pytest.raises(NotImplementedError):
+                f(forward_ad.make_dual(v, torch.ones_like(v)))
+            with pytest.raises(NotImplementedError):
+                f(forward_ad.make_dual(v.clone().requires_grad_(), torch.ones_like(v)))
