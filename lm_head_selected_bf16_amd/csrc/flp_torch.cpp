@@ -93,21 +93,28 @@ at::Tensor bytes(size_t n, const at::Tensor& like) {
 void same(bool ok) { TORCH_CHECK_VALUE(ok, "an input of the forward has changed since then"); }
 bool dense(const at::Tensor& t) { return t.is_cuda() && t.is_contiguous(); }
 
-// The gradients cannot be differentiated again: where the upstream gradient asks for it, the
-// use of what is derived from them raises.
+// The gradients cannot be differentiated again: where a graph of the backward is asked for, the
+// backward of what is derived from one that depends on something to be differentiated raises.
+// (Without the node such a gradient would pass for a constant.)
 struct FirstOrder : Function<FirstOrder> {
   static at::Tensor forward(AutogradContext*, const at::Tensor& t) { return at::alias(t); }
   static variable_list backward(AutogradContext*, variable_list) {
     throw std::runtime_error(
-        "trying to differentiate twice a function that is marked with once_differentiable");
+        "trying to differentiate twice a function that is marked with once_differentiable: what "
+        "its backward computes does not require grad");
   }
 };
 
-variable_list first_order(const at::Tensor& grad, variable_list out) {
-  if (!at::GradMode::is_enabled() || !grad.requires_grad()) return out;
-  for (at::Tensor& t : out)
-    if (t.defined()) t = FirstOrder::apply(t.detach().requires_grad_(true));
-  return out;
+at::Tensor first_order(const at::Tensor& t) {
+  return FirstOrder::apply(t.detach().requires_grad_(true));
+}
+
+// t, which depends on `from`.
+template <class... Ts>
+at::Tensor first_order(const at::Tensor& t, const Ts&... from) {
+  const bool graph = at::GradMode::is_enabled() && t.defined() &&
+                     ((from.defined() && from.requires_grad()) || ...);
+  return graph ? first_order(t) : t;
 }
 
 // Every backward runs on the stream of its forward, which autograd makes current for it;
@@ -144,7 +151,7 @@ struct EmbeddingNode : Function<EmbeddingNode> {
                                  ctx->saved_data["scale"].toDouble(), ptr(dw), code(g), ptr(ws),
                                  size_t(ws.numel()),
                                  reinterpret_cast<void*>(ctx->saved_data["stream"].toInt())));
-    return first_order(grads[0], {dw, at::Tensor(), at::Tensor(), at::Tensor()});
+    return {first_order(dw, grads[0]), at::Tensor(), at::Tensor(), at::Tensor()};
   }
 };
 
@@ -167,10 +174,9 @@ struct DropoutNode : Function<DropoutNode> {
     const at::Tensor rng = ctx->get_saved_variables()[0];
     same(dense(rng) && rng.scalar_type() == at::kLong && rng.numel() == 2 &&
          rng.device() == grads[0].device());
-    return first_order(grads[0],
-                       {run(grads[0].contiguous(), ctx->saved_data["p"].toDouble(), rng,
-                            ctx->saved_data["stream"].toInt()),
-                        at::Tensor(), at::Tensor(), at::Tensor()});
+    const at::Tensor dx = run(grads[0].contiguous(), ctx->saved_data["p"].toDouble(), rng,
+                              ctx->saved_data["stream"].toInt());
+    return {first_order(dx, grads[0]), at::Tensor(), at::Tensor(), at::Tensor()};
   }
 };
 
@@ -221,7 +227,8 @@ struct LayerNormNode : Function<LayerNormNode> {
           api.norm_backward(N, D, code(x), ptr(g), ptr(x), wd, ptr(w), fptr(stats),
                             fptr(stats) + N, ptr(dx), ptr(dw), ptr(db), ptr(ws), size,
                             reinterpret_cast<void*>(ctx->saved_data["stream"].toInt())));
-    return first_order(grads[0], {dx, dw, db, at::Tensor(), at::Tensor()});
+    return {first_order(dx, grads[0], x, w), first_order(dw, grads[0], x),
+            first_order(db, grads[0]), at::Tensor(), at::Tensor()};
   }
 };
 
@@ -286,10 +293,10 @@ struct CrossEntropyNode : Function<CrossEntropyNode> {
                             fptr(db), ptr(ws), size_t(ws.numel()),
                             reinterpret_cast<void*>(ctx->saved_data["stream"].toInt())));
     variable_list out(9);
-    out[0] = dh;
-    out[1] = dw;
-    out[3] = db;
-    return first_order(grads[0], out);
+    out[0] = first_order(dh, grads[0], hidden, weight, b);
+    out[1] = first_order(dw, grads[0], hidden, weight, b);
+    out[3] = first_order(db, grads[0], hidden, weight, b);
+    return out;
   }
 };
 
@@ -306,6 +313,7 @@ PYBIND11_MODULE(_flp_torch, m) {
     }
   });
   m.def("bind", &bind);
+  m.def("first_order", [](const at::Tensor& t) { return first_order(t); });
   m.def("embedding", [](const at::Tensor& weight, const at::Tensor& ids, double scale,
                         int64_t stream) { return EmbeddingNode::apply(weight, ids, scale, stream); });
   m.def("dropout", [](const at::Tensor& x, double p, const at::Tensor& rng, int64_t stream) {

@@ -22,7 +22,6 @@ from typing import Optional, Tuple
 
 import torch
 from torch.autograd import forward_ad
-from torch.autograd.function import once_differentiable
 
 from . import _abi
 from ._abi import FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpError
@@ -753,17 +752,19 @@ class LossAndGradients(torch.autograd.Function):
         return loss
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, g):
         grads, ctx.grads = ctx.grads, None
         if grads is not None:
-            dh, dw, db = (_scaled(x, g) for x in grads)
+            grads = [_scaled(x, g) for x in grads]
         else:
             hidden, weight, targets, bias, stats = ctx.saved_tensors
             need_h, need_w, _, need_b = ctx.needs_input_grad[:4]
-            dh, dw, db = cross_entropy_backward(g.contiguous(), stats, hidden, weight, targets,
-                                                bias, *ctx.terms, need_hidden=need_h,
-                                                need_weight=need_w, need_bias=need_b)
+            grads = cross_entropy_backward(g.contiguous(), stats, hidden, weight, targets, bias,
+                                           *ctx.terms, need_hidden=need_h, need_weight=need_w,
+                                           need_bias=need_b)
+        if torch.is_grad_enabled():  # a graph of the backward is asked for: it has none
+            grads = [None if x is None else _nodes().first_order(x) for x in grads]
+        dh, dw, db = grads
         return dh, dw, None, db, None, None, None
 
 

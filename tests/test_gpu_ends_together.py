@@ -208,3 +208,60 @@ def test_forward_mode_differentiation_is_refused():
                 f(forward_ad.make_dual(v, torch.ones_like(v)))
             with pytest.raises(NotImplementedError):
                 f(forward_ad.make_dual(v.clone().requires_grad_(), torch.ones_like(v)))
+
+
+@pytest.mark.parametrize("up", [None, "constant", "differentiable"])
+@pytest.mark.parametrize("op", ["layer_norm", "cross_entropy", "cross_entropy_at_once"])
+def test_a_penalty_on_a_first_gradient_is_refused(op, up):
+    """The first gradients of layer norm and of the loss depend on their inputs: a term made of
+    them cannot be differentiated, and says so beside other terms that can."""
+    from lm_head_selected_bf16_amd import torch_ops
+    m = flp()
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(12, 64, generator=g).cuda().requires_grad_()
+    w = torch.randn(90, 64, generator=g).cuda().requires_grad_()
+    b = torch.randn(90, generator=g).cuda().requires_grad_()
+    t = torch.arange(12, device="cuda")
+    if op == "layer_norm":
+        w, b = (v[0:1].expand(64).detach().clone().requires_grad_() for v in (w[0, :1], b))
+        out = m.layer_norm(x, w, b)
+    elif op == "cross_entropy":
+        out = m.linear_cross_entropy(x, w, t, b)
+    else:
+        out = torch_ops.LossAndGradients.apply(x, w, t, b, 0.0, 0.0, "mean")
+    seed = None if up is None and out.dim() == 0 else torch.ones_like(out)
+    if up == "differentiable":
+        seed = seed if seed is not None else torch.ones_like(out)
+        seed.requires_grad_()
+    first = torch.autograd.grad(out, [x, w, b], seed, create_graph=True)
+    # d_bias of the norm is a sum of the upstream gradient alone
+    depends = [True, True, op != "layer_norm" or up == "differentiable"]
+    for d, dep in zip(first, depends):
+        assert d.requires_grad == dep
+        if dep:
+            with pytest.raises(RuntimeError, match="differentiate twice"):
+                (out.sum() + d.pow(2).sum()).backward(retain_graph=True)
+    for v, d in zip((x, w, b), first):
+        v.grad = None
+    again = torch.autograd.grad(out, [x, w, b], None if seed is None else seed.detach())
+    for a, d in zip(again, first):
+        assert not a.requires_grad and torch.equal(a, d)
+
+
+def test_a_penalty_on_the_gradient_of_a_linear_operator():
+    """Dropout's and the embedding's gradients do not depend on their inputs: with a constant
+    upstream gradient they are constants."""
+    m = flp()
+    ids, _, p, rng = step_inputs(torch.float32)
+    x = torch.randn(3, 64, device="cuda", requires_grad=True)
+    for out, leaf in ((m.dropout(x, 0.1, rng), x), (m.embedding(p["table"], ids, 2.0), p["table"])):
+        (d,) = torch.autograd.grad(out, [leaf], torch.ones_like(out), create_graph=True)
+        assert not d.requires_grad
+        (out.sum() + d.pow(2).sum()).backward()
+        assert torch.equal(leaf.grad, d)
+        out = m.dropout(x, 0.1, rng)
+    up = torch.ones(*ids.shape, 96, device="cuda", requires_grad=True)
+    (d,) = torch.autograd.grad(m.embedding(p["table"], ids, 2.0), [p["table"]], up,
+                               create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        d.sum().backward()
