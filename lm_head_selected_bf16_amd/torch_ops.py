@@ -739,7 +739,9 @@ class LossAndGradients(torch.autograd.Function):
     """Autograd node of the linear cross entropy where its forward makes the gradients for an
     upstream gradient of 1 along with the loss: the first backward multiplies them by the
     upstream gradient in place (a second rounding unless that is a power of two) and hands them
-    over.  Any further backward through the same node recomputes."""
+    over.  Any further backward through the same node recomputes.  Once a graph capture has seen
+    the forward or a backward, the gradients stay as they are, since a replay fills or reads them
+    again, and every backward hands over copies."""
 
     @staticmethod
     def forward(ctx, hidden, weight, targets, bias, label_smoothing, z_loss, reduction):
@@ -748,14 +750,17 @@ class LossAndGradients(torch.autograd.Function):
         loss, stats, *ctx.grads = cross_entropy_gradients(
             hidden, weight, targets, bias, *ctx.terms, need_hidden=need_h, need_weight=need_w,
             need_bias=need_b)
+        ctx.replayed = torch.cuda.is_current_stream_capturing()
         ctx.save_for_backward(hidden, weight, targets, bias, stats)
         return loss
 
     @staticmethod
     def backward(ctx, g):
-        grads, ctx.grads = ctx.grads, None
-        if grads is not None:
-            grads = [_scaled(x, g) for x in grads]
+        ctx.replayed = ctx.replayed or torch.cuda.is_current_stream_capturing()
+        if ctx.grads is not None and ctx.replayed:
+            grads = [None if x is None else _scaled(x.clone(), g) for x in ctx.grads]
+        elif ctx.grads is not None:
+            grads, ctx.grads = [_scaled(x, g) for x in ctx.grads], None
         else:
             hidden, weight, targets, bias, stats = ctx.saved_tensors
             need_h, need_w, _, need_b = ctx.needs_input_grad[:4]

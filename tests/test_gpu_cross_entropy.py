@@ -399,6 +399,62 @@ def test_autograd_of_large_steps(dtype, N, D, V):
     assert torch.equal(dh, unit[2])
 
 
+def test_a_captured_backward_of_gradients_made_at_once():
+    """A backward that is captured by itself: every replay multiplies the forward's gradients by
+    the upstream gradient of the time, not what the replay before left, and an eager backward
+    beside it does too."""
+    from lm_head_selected_bf16_amd import torch_ops
+    m = flp()
+    h, w, b, t, up = make(70, 64, 900, BF16, 53)
+    _, _, *unit = at_once(h, w, b, t, 0.1, 1e-3, "mean")
+    leaves = [x.requires_grad_() for x in (h, w, b)]
+    loss = torch_ops.LossAndGradients.apply(h, w, t, b, 0.1, 1e-3, "mean")
+    g = torch.ones((), device="cuda")
+
+    def backward():  # the node's, without autograd around it
+        got = torch_ops.LossAndGradients.backward(loss.grad_fn, g)
+        return got[0], got[1], got[3]
+
+    def check_times(got, f):
+        for x, u in zip(got, unit):
+            assert torch.equal(x, (u.float() * f).to(x.dtype)), f
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = backward()
+    for f in (3.0, 3.0, 0.7, 1.0):
+        g.fill_(f)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_times(out, f)
+        check_times(torch.autograd.grad(loss, leaves, g, retain_graph=True), f)
+
+
+def test_an_eager_backward_of_a_captured_forward():
+    """What one replay's backward gave is not touched by the next replay."""
+    from lm_head_selected_bf16_amd import torch_ops
+    h, w, b, t, up = make(70, 64, 900, BF16, 54)
+    h.requires_grad_()
+    torch_ops.LossAndGradients.apply(h, w, t, b, 0.1, 1e-3, "mean")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = torch_ops.LossAndGradients.apply(h, w, t, b, 0.1, 1e-3, "mean")
+    g = torch.full((), 3.0, device="cuda")
+    seen = []
+    for rep in range(3):
+        with torch.no_grad():
+            h.data.copy_(make(70, 64, 900, BF16, 200 + rep)[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = torch_ops.LossAndGradients.backward(loss.grad_fn, g)[0]
+        unit = at_once(h.detach(), w, b, t, 0.1, 1e-3, "mean")[2]
+        seen.append((got, (unit.float() * 3).to(BF16)))
+        for x, y in seen:
+            assert torch.equal(x, y), rep
+
+
 def test_scale_inplace():
     m = flp()
     code = {BF16: m.FLP_BF16, F16: m.FLP_F16, F32: m.FLP_F32}
