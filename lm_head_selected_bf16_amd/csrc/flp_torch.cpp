@@ -93,6 +93,13 @@ at::Tensor bytes(size_t n, const at::Tensor& like) {
 void same(bool ok) { TORCH_CHECK_VALUE(ok, "an input of the forward has changed since then"); }
 bool dense(const at::Tensor& t) { return t.is_cuda() && t.is_contiguous(); }
 
+// The upstream gradient as the library takes it.  contiguous() returns a dense view at any
+// offset of its storage (what the backward of a concatenation hands on) as it is.
+at::Tensor aligned16(const at::Tensor& t) {
+  at::Tensor c = t.contiguous();
+  return reinterpret_cast<uintptr_t>(ptr(c)) % 16 == 0 ? c : c.clone();
+}
+
 // The gradients cannot be differentiated again: where a graph of the backward is asked for, the
 // backward of what is derived from one that depends on something to be differentiated raises.
 // (Without the node such a gradient would pass for a constant.)
@@ -141,7 +148,7 @@ struct EmbeddingNode : Function<EmbeddingNode> {
     const at::Tensor ids = ctx->get_saved_variables()[0];
     const int64_t N = ctx->saved_data["N"].toInt(), V = ctx->saved_data["V"].toInt();
     same(dense(ids) && ids.numel() == N && ids.device() == grads[0].device());
-    const at::Tensor g = grads[0].contiguous();
+    const at::Tensor g = aligned16(grads[0]);
     const int64_t D = g.size(-1);
     at::Tensor dw = at::empty({V, D}, g.options());
     const size_t size = api.embedding_backward_bytes(N, D, V);

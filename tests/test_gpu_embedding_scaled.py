@@ -114,6 +114,25 @@ def test_sorting_by_counting_keeps_the_order_of_the_radix_passes(ids, idt):
                            want), N
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("off", [1, 3, 8])
+def test_upstream_gradient_off_the_16_byte_grid(dtype, off):
+    """A dense view that begins `off` elements into its storage, given as it is and made by the
+    backward of a concatenation."""
+    m = flp()
+    w = torch.randn(50, 64, device="cuda").to(dtype).requires_grad_()
+    ids = torch.tensor([4, 9, -1, 4, 49, 0], device="cuda")
+    whole = torch.randn(off + 6 * 64, device="cuda").to(dtype)
+    up = whole[off:].view(6, 64)
+    want = m.embedding_backward(up.clone(), ids, 50, scale=3.0)
+    (got,) = torch.autograd.grad(m.embedding(w, ids, 3.0), [w], up)
+    assert torch.equal(got, want)
+    cat = torch.cat([torch.zeros(off, device="cuda", dtype=dtype),
+                     m.embedding(w, ids, 3.0).flatten()])
+    (got,) = torch.autograd.grad(cat, [w], whole)
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.5])
 def test_more_rows_than_one_launch_has_waves(scale):
     N = 2 ** 26 + 37
