@@ -6,6 +6,7 @@
 // here.  Autograd runs a backward on a thread of its own, which has to take over the Python
 // interpreter for a node written in Python and then runs it from cold caches: a layer norm of
 // 37 x 1003, forward and backward, took 118 us on the host that way and takes 74 here.
+#include <torch/csrc/Exceptions.h>
 #include <torch/extension.h>
 
 #include <cstdint>
@@ -25,7 +26,6 @@ using OptTensor = std::optional<at::Tensor>;
 
 // The entry points of the loaded library.
 struct Api {
-  decltype(&::flp_status_string) status_string;
   decltype(&::flp_embedding_scaled_forward) embedding_forward;
   decltype(&::flp_embedding_scaled_backward) embedding_backward;
   decltype(&::flp_embedding_backward_workspace_bytes) embedding_backward_bytes;
@@ -44,7 +44,6 @@ void bind(const std::map<std::string, uintptr_t>& at) {
   auto take = [&](auto& f, const char* name) {
     f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(at.at(name));
   };
-  take(api.status_string, "flp_status_string");
   take(api.embedding_forward, "flp_embedding_scaled_forward");
   take(api.embedding_backward, "flp_embedding_scaled_backward");
   take(api.embedding_backward_bytes, "flp_embedding_backward_workspace_bytes");
@@ -58,17 +57,17 @@ void bind(const std::map<std::string, uintptr_t>& at) {
   take(api.loss_backward_bytes, "flp_cross_entropy_backward_workspace_bytes");
 }
 
-// A non-OK status: FlpError in Python.
-struct StatusError : std::runtime_error {
-  StatusError(const char* f, int s)
-      : std::runtime_error(std::string(f) + " failed: " + api.status_string(flp_status(s))),
-        fn(f), status(s) {}
-  const char* fn;
-  int status;
-};
-
+// A non-OK status: FlpError in Python, as a Python exception from here on.  A backward runs in
+// autograd's engine, which hands those on as they are and any other but torch's own as
+// RuntimeError.
 void check(const char* fn, flp_status st) {
-  if (st != FLP_OK) throw StatusError(fn, int(st));
+  if (st == FLP_OK) return;
+  py::gil_scoped_acquire interpreter;
+  py::object cls = py::module_::import("lm_head_selected_bf16_amd._abi").attr("FlpError");
+  PyErr_SetObject(cls.ptr(), cls(fn, int(st)).ptr());
+  python_error e;
+  e.persist();
+  throw e;
 }
 
 flp_dtype code(const at::Tensor& t) {
@@ -311,12 +310,11 @@ struct CrossEntropyNode : Function<CrossEntropyNode> {
 
 PYBIND11_MODULE(_flp_torch, m) {
   m.doc() = "Autograd nodes over libflp.so.";
-  py::register_exception_translator([](std::exception_ptr p) {
+  py::register_exception_translator([](std::exception_ptr p) {  // out of a forward
     try {
       if (p) std::rethrow_exception(p);
-    } catch (const StatusError& e) {
-      py::object cls = py::module_::import("lm_head_selected_bf16_amd._abi").attr("FlpError");
-      PyErr_SetObject(cls.ptr(), cls(e.fn, e.status).ptr());
+    } catch (python_error& e) {
+      e.restore();
     }
   });
   m.def("bind", &bind);

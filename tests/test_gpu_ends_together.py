@@ -265,3 +265,26 @@ def test_a_penalty_on_the_gradient_of_a_linear_operator():
                                create_graph=True)
     with pytest.raises(RuntimeError, match="differentiate twice"):
         d.sum().backward()
+
+
+@pytest.mark.parametrize("how", ["grad", "backward"])
+def test_a_status_inside_a_backward_is_the_librarys_error(how):
+    """Data exchanged for a view off the 16-byte grid between forward and backward: the library
+    refuses it inside autograd's engine, and the error keeps its type and status.  The next step
+    is not touched by it."""
+    m = flp()
+    g = torch.Generator().manual_seed(6)
+    w = torch.randn(90, 64, generator=g).cuda()
+    t = torch.arange(12, device="cuda")
+    x = torch.randn(12, 64, generator=g).cuda().requires_grad_()
+    loss = m.linear_cross_entropy(x, w, t)
+    (want,) = torch.autograd.grad(loss, [x], retain_graph=True)
+    kept = x.data
+    x.data = torch.cat([kept.flatten()[:1], kept.flatten()])[1:].view(12, 64)
+    with pytest.raises(m.FlpError, match="flp_cross_entropy_backward failed: FLP_MISALIGNED") as e:
+        loss.backward() if how == "backward" else torch.autograd.grad(loss, [x])
+    assert e.value.status == 4
+    x.data = kept
+    assert torch.equal(torch.autograd.grad(m.linear_cross_entropy(x, w, t), [x])[0], want)
+    with pytest.raises(m.FlpError, match="flp_layer_norm_forward failed: FLP_INVALID_ARGUMENT"):
+        m.layer_norm(x, eps=-1.0)
