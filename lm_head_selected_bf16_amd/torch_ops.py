@@ -22,6 +22,7 @@ from typing import Optional, Tuple
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.function import once_differentiable
 
 from . import _abi
 from ._abi import FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpError
@@ -578,12 +579,26 @@ def embedding_backward(grad: torch.Tensor, ids: torch.Tensor, num_embeddings: in
     return d_weight
 
 
-class Embedding:
-    """The differentiable lookup, under the name of its autograd node."""
+class Embedding(torch.autograd.Function):
+    """Autograd node of the lookup in Python, over libflp.so alone; the ids are not
+    differentiable.  embedding() takes the node of csrc/flp_torch.cpp, with the same bits."""
 
     @staticmethod
-    def apply(weight, ids, scale=1.0):
-        return embedding(weight, ids, scale)
+    def forward(ctx, weight, ids, scale=1.0):
+        ctx.save_for_backward(ids)
+        ctx.num_embeddings, ctx.scale = int(weight.shape[0]), scale
+        return embedding_forward(weight, ids, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        (ids,) = ctx.saved_tensors
+        if not ctx.needs_input_grad[0]:
+            return None, None, None
+        grad = grad.contiguous()
+        if grad.data_ptr() % 16:  # a dense view at any offset of its storage
+            grad = grad.clone()
+        return embedding_backward(grad, ids, ctx.num_embeddings, scale=ctx.scale), None, None
 
 
 def embedding(weight, ids, scale=1.0):

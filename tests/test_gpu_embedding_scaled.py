@@ -133,6 +133,23 @@ def test_upstream_gradient_off_the_16_byte_grid(dtype, off):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("args", [(), (1.0,), (3.0,)])
+def test_the_function_of_the_lookup(args):
+    """Embedding is an autograd.Function with forward and backward of its own, and gives the bits
+    of embedding(); its backward needs no second library."""
+    m = flp()
+    assert issubclass(m.Embedding, torch.autograd.Function)
+    ids = torch.tensor([[4, 9, -1], [4, 49, 50]], device="cuda")
+    w = torch.randn(50, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    whole = torch.randn(3 + 6 * 64, device="cuda").bfloat16()
+    for up in (torch.randn(2, 3, 64, device="cuda").bfloat16(), whole[3:].view(2, 3, 64),
+               whole[:64].expand(2, 3, 64)):
+        out, want = m.Embedding.apply(w, ids, *args), m.embedding(w, ids, *args)
+        assert torch.equal(out, want) and type(out.grad_fn).__name__ == "EmbeddingBackward"
+        assert torch.equal(torch.autograd.grad(out, [w], up)[0],
+                           torch.autograd.grad(want, [w], up)[0])
+
+
 @pytest.mark.parametrize("scale", [1.0, 0.5])
 def test_more_rows_than_one_launch_has_waves(scale):
     N = 2 ** 26 + 37
