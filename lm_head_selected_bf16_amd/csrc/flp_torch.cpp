@@ -9,6 +9,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/extension.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <map>
 #include <optional>
@@ -86,6 +87,18 @@ float* fptr(const at::Tensor& t) { return static_cast<float*>(ptr(t)); }
 
 at::Tensor bytes(size_t n, const at::Tensor& like) {
   return at::empty({int64_t(n > 16 ? n : 16)}, like.options().dtype(at::kByte));
+}
+
+// The same, halved as often as needed and at least `least`, as the device has room for.
+at::Tensor bytes(size_t n, size_t least, const at::Tensor& like) {
+  while (n > least) {
+    try {
+      return bytes(n, like);
+    } catch (const c10::OutOfMemoryError&) {
+      n = n / 2 > least ? n / 2 : least;
+    }
+  }
+  return bytes(n, like);
 }
 
 // A leaf's data may have been exchanged between the forward and the backward.
@@ -283,13 +296,10 @@ struct CrossEntropyNode : Function<CrossEntropyNode> {
     if (ctx->needs_input_grad(1)) dw = at::empty_like(weight);
     if (b.defined() && ctx->needs_input_grad(3)) db = at::empty_like(b);
     // a smaller workspace runs more row chunks, with the same bits
-    size_t size = api.loss_backward_bytes(N, D, V, code(hidden), N > 1 ? N : 1);
-    const size_t most = size_t(ctx->saved_data["most"].toInt());
-    if (size > most) {
-      const size_t least = api.loss_backward_bytes(N, D, V, code(hidden), 0);
-      size = least > most ? least : most;
-    }
-    const at::Tensor ws = bytes(size, hidden);
+    const size_t whole = api.loss_backward_bytes(N, D, V, code(hidden), N > 1 ? N : 1);
+    const size_t least = api.loss_backward_bytes(N, D, V, code(hidden), 0);
+    const size_t most = std::max(least, size_t(ctx->saved_data["most"].toInt()));
+    const at::Tensor ws = bytes(std::min(whole, most), least, hidden);
     check("flp_cross_entropy_backward",
           api.loss_backward(N, D, V, code(hidden), fptr(g), fptr(stats), ptr(hidden), ptr(weight),
                             fptr(b), ptr(targets), code(targets),

@@ -623,6 +623,18 @@ _REDUCTIONS = {"none": _abi.FLP_REDUCE_NONE, "sum": _abi.FLP_REDUCE_SUM,
                "mean": _abi.FLP_REDUCE_MEAN}
 
 
+def _chunked_workspace(size: int, least: int, device) -> torch.Tensor:
+    """A workspace of `size` bytes, or of as many, halved as often as needed and at least `least`,
+    as the device has room for: a smaller one runs more row chunks, with the same bits."""
+    while True:
+        try:
+            return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+        except torch.OutOfMemoryError:
+            if size <= least:
+                raise
+            size = max(size // 2, least)
+
+
 def _prepare_loss(hidden, weight, targets, bias, reduction):
     if reduction not in _REDUCTIONS:
         raise ValueError("reduction must be 'none', 'sum' or 'mean'")
@@ -664,7 +676,8 @@ def cross_entropy_backward(grad_out: torch.Tensor, stats: torch.Tensor, hidden: 
                            workspace_bytes: Optional[int] = None):
     """(d_hidden, d_weight, d_bias) through flp_cross_entropy_backward; unrequested ones are
     None.  grad_out: float32, of the loss's shape.  The workspace is as large as the backward of
-    linear_logp takes by default; a smaller one runs more row chunks with the same bits."""
+    linear_logp takes by default, or as the device has room for; a smaller one runs more row
+    chunks with the same bits."""
     (h2, t1, _, lead, N, D, V), red = _prepare_loss(hidden, weight, targets, bias, reduction)
     dev = hidden.device
     want = lead if reduction == "none" else ()
@@ -676,16 +689,16 @@ def cross_entropy_backward(grad_out: torch.Tensor, stats: torch.Tensor, hidden: 
     if need_bias is None:
         need_bias = bias is not None
     xd = _X_DTYPES[hidden.dtype]
+    size = _abi.flp_cross_entropy_backward_workspace_bytes
+    most = least = workspace_bytes
     if workspace_bytes is None:
-        workspace_bytes = _abi.flp_cross_entropy_backward_workspace_bytes(N, D, V, xd, max(N, 1))
-        if workspace_bytes > DEFAULT_BWD_WORKSPACE:
-            least = _abi.flp_cross_entropy_backward_workspace_bytes(N, D, V, xd, 0)
-            workspace_bytes = max(least, DEFAULT_BWD_WORKSPACE)
+        most, least = size(N, D, V, xd, max(N, 1)), size(N, D, V, xd, 0)
+        most = min(most, max(least, DEFAULT_BWD_WORKSPACE))
     with _on(dev):
         d_hidden = torch.empty_like(hidden) if need_hidden else None
         d_weight = torch.empty_like(weight) if need_weight else None
         d_bias = torch.empty(V, dtype=torch.float32, device=dev) if need_bias else None
-        ws = torch.empty(max(int(workspace_bytes), 16), dtype=torch.uint8, device=dev)
+        ws = _chunked_workspace(int(most), int(least), dev)
         st = _abi.flp_cross_entropy_backward(N, D, V, xd, _ptr(grad_out), _ptr(stats), _ptr(h2),
                                              _ptr(weight), _ptr(bias), _ptr(t1),
                                              _T_DTYPES[targets.dtype], float(label_smoothing),
@@ -709,18 +722,18 @@ def cross_entropy_gradients(hidden: torch.Tensor, weight: torch.Tensor, targets:
     if need_bias is None:
         need_bias = bias is not None
     xd = _X_DTYPES[hidden.dtype]
+    size = _abi.flp_cross_entropy_gradients_workspace_bytes
+    most = least = workspace_bytes
     if workspace_bytes is None:
-        size = _abi.flp_cross_entropy_gradients_workspace_bytes
-        workspace_bytes = size(N, D, V, xd, max(N, 1))
-        if workspace_bytes > DEFAULT_GRADIENTS_WORKSPACE:
-            workspace_bytes = max(size(N, D, V, xd, 0), DEFAULT_GRADIENTS_WORKSPACE)
+        most, least = size(N, D, V, xd, max(N, 1)), size(N, D, V, xd, 0)
+        most = min(most, max(least, DEFAULT_GRADIENTS_WORKSPACE))
     with _on(dev):
         loss = torch.empty((), dtype=torch.float32, device=dev)
         stats = torch.empty((2,) + lead, dtype=torch.float32, device=dev)
         d_hidden = torch.empty_like(hidden) if need_hidden else None
         d_weight = torch.empty_like(weight) if need_weight else None
         d_bias = torch.empty(V, dtype=torch.float32, device=dev) if need_bias else None
-        ws = torch.empty(max(int(workspace_bytes), 16), dtype=torch.uint8, device=dev)
+        ws = _chunked_workspace(int(most), int(least), dev)
         st = _abi.flp_cross_entropy_gradients(N, D, V, xd, _ptr(h2), _ptr(weight), _ptr(bias),
                                               _ptr(t1), _T_DTYPES[targets.dtype],
                                               float(label_smoothing), float(z_loss), red,

@@ -455,6 +455,52 @@ def test_an_eager_backward_of_a_captured_forward():
             assert torch.equal(x, y), rep
 
 
+@pytest.mark.parametrize("call", ["at once", "functional", "autograd"])
+def test_little_memory_means_smaller_chunks(call):
+    """With room for the outputs, the least workspace and a little beside (the allocator takes
+    20 MB at least for a tensor of over 1 MB), where a whole chunk of 4096 x 20000 takes 330 (two
+    calls) to 650 MB: the same bits.  With room for nothing, torch's error."""
+    from lm_head_selected_bf16_amd import torch_ops
+    m = flp()
+    h, w, b, t, up = make(4096, 64, 20000, BF16, 55)
+    one = torch.ones((), device="cuda")
+    leaf = h.clone().requires_grad_()
+    loss, stats = m.cross_entropy_forward(h, w, t, b)
+    kept = m.linear_cross_entropy(leaf, w, t, b)
+    assert not torch_ops._gradients_at_once(leaf, w, "mean")
+
+    def step():
+        if call == "at once":
+            return m.cross_entropy_gradients(h, w, t, b)[2:]
+        if call == "functional":
+            return m.cross_entropy_backward(one, stats, h, w, t, b)
+        return torch.autograd.grad(kept, [leaf], retain_graph=True)
+
+    want = step()
+    code = m.FLP_BF16
+    size = {"at once": m.flp_cross_entropy_gradients_workspace_bytes}.get(
+        call, m.flp_cross_entropy_backward_workspace_bytes)
+    room = (size(4096, 64, 20000, code, 0) >> 20) + 48
+    assert size(4096, 64, 20000, code, 4096) > 2 * room << 20
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    try:
+        torch.cuda.set_per_process_memory_fraction(
+            (torch.cuda.memory_reserved() + (room << 20)) / total)
+        got = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        del got
+        torch.cuda.empty_cache()
+        torch.cuda.set_per_process_memory_fraction(torch.cuda.memory_reserved() / total)
+        with pytest.raises(torch.OutOfMemoryError):
+            step()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert all(torch.equal(x, y) for x, y in zip(step(), want))
+
+
 def test_scale_inplace():
     m = flp()
     code = {BF16: m.FLP_BF16, F16: m.FLP_F16, F32: m.FLP_F32}
