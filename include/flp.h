@@ -412,9 +412,10 @@ flp_status flp_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p, co
                        void* out, void* stream);
 
 /*
- * Softmax cross entropy of the projected rows, without keeping the logits
- * z_iv = hidden_i . W_v + b_v: the training loss whose per-token part is -logp of
- * flp_forward, with label smoothing s and a squared log-partition term c:
+ * Softmax cross entropy of the projected rows, z_iv = hidden_i . W_v + b_v: the training
+ * loss whose per-token part is -logp of flp_forward, with label smoothing s and a squared
+ * log-partition term c (the logits are not kept; flp_cross_entropy_gradients holds those
+ * of one row chunk in its workspace):
  *
  *   loss_i = (1 - s) (lse_i - z_i[t_i]) + s (lse_i - mean_v z_iv) + c lse_i^2
  *
@@ -466,6 +467,11 @@ flp_status flp_cross_entropy_forward(int64_t N, int64_t D, int64_t V, flp_dtype 
  * For FLP_F16, dz is held times a power of two that brings its largest row factor to
  * 2^10, taken back when the fp32 sums are rounded: small gradients (a mean over many
  * rows) do not underflow on the way.
+ *
+ * For 16-bit types dz is rounded to x_dtype between its fp32 epilogue and the two
+ * products, whose matrix instructions take operands of that type (as flp_backward does);
+ * d_bias adds the unrounded entries.  The error this adds to d_hidden and d_weight is that
+ * of one more rounding of their size.
  *
  * Batches of up to 8192 rows sum d_hidden over slabs of the vocabulary, larger ones in
  * one walk: a row's d_hidden is bitwise the same among batches of one kind, and differs

@@ -15,8 +15,11 @@
 //
 // A row's sums run in an order fixed by D alone, so out, mean, rstd and d_x of a
 // row are bitwise the same whatever the other rows are.  d_w and d_b add rows in
-// fixed slabs (cut by N alone), each slab in ascending order, then the slabs in
-// ascending order: no atomics, the same bits on every run.
+// slabs cut by N alone.  Within a slab, each of its k teams or waves (k by D and the type:
+// 8 or 2 teams, 4 waves for wide rows) adds every k-th row in ascending order, and the k
+// sums are joined in a fixed order; over the slabs, sixteen sums of every sixteenth slab are
+// joined by a fixed tree.  N, D and the type fix the order: no atomics, the same bits on
+// every run.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -616,8 +616,8 @@ def embedding(weight, ids, scale=1.0):
 # ---- linear cross entropy -----------------------------------------------------------------------
 #
 # The training loss of the head: -logp with label smoothing, a squared log-partition term and a
-# reduction, without the logits.  Targets outside [0, V) are padding: loss 0, not counted, zero
-# gradients.
+# reduction, without an [N, V] tensor of logits.  Targets outside [0, V) are padding: loss 0, not
+# counted, zero gradients.
 
 _REDUCTIONS = {"none": _abi.FLP_REDUCE_NONE, "sum": _abi.FLP_REDUCE_SUM,
                "mean": _abi.FLP_REDUCE_MEAN}
@@ -819,7 +819,18 @@ def linear_cross_entropy(hidden, weight, targets, bias=None, label_smoothing=0.0
         (1 - s) (lse - z[target]) + s (lse - mean(z)) + z_loss lse^2,   s = label_smoothing
 
     per row ("none"), summed ("sum") or averaged over the rows whose target lies in [0, V)
-    ("mean", 0 when there are none); the other rows are padding with loss 0 and no gradient."""
+    ("mean", 0 when there are none); the other rows are padding with loss 0 and no gradient.
+
+    Where that is faster (reduced bfloat16 losses from D = 1024 on and large float32 ones, see
+    _gradients_at_once) the call makes the gradients along with the loss when one is asked for:
+    - it takes the three products of a whole step at once, so a loss without a backward belongs
+      under torch.no_grad();
+    - its workspace, freed on return, holds a row chunk's fp32 logits beside dz and dz^T: 8 bytes
+      per logit in bfloat16, 12 in float32, up to torch_ops.DEFAULT_GRADIENTS_WORKSPACE (24 GiB)
+      or what the device has room for;
+    - the gradients stay on the node until its first backward, which multiplies them by the
+      upstream gradient: one more rounding to their type unless that is a power of two.
+    cross_entropy_forward and cross_entropy_backward make none of these choices."""
     if not _wants_grad(hidden, weight, bias):
         return cross_entropy_forward(hidden, weight, targets, bias, label_smoothing, z_loss,
                                      reduction, return_stats=False)[0]
