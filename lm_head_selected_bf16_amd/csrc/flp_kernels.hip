@@ -926,6 +926,8 @@ __global__ __launch_bounds__(256) void k_fill(float* dst, int64_t n, float value
 // them in chunk order; the 64 lane pairs are then combined by a xor butterfly
 // whose combine step is symmetric, so every lane ends with the same bits.  The
 // row is read once with streaming loads, four chunks per lane in flight.
+// Where a maximum is -inf the exponents are taken as they are: entries of -inf add 0
+// (a lane may hold nothing else) and NaN entries make the sum NaN.
 
 template <class E>
 __device__ __forceinline__ void unpack8(const u32x4& v, float (&x)[8]);
@@ -998,10 +1000,11 @@ __global__ __launch_bounds__(256) void k_logits_fwd(LogitsArgs p) {
 #pragma unroll
       for (int k = 1; k < EPC; ++k) cm = fmaxf(cm, x[k]);
       const float Mn = fmaxf(M, cm);
+      const float base = Mn == -INFINITY ? 0.f : Mn;
       float e = 0.f;
 #pragma unroll
-      for (int k = 0; k < EPC; ++k) e += fast_exp2((x[k] - Mn) * kLog2e);
-      S = S * fast_exp2((M - Mn) * kLog2e) + e;
+      for (int k = 0; k < EPC; ++k) e += fast_exp2((x[k] - base) * kLog2e);
+      S = S * fast_exp2((M - base) * kLog2e) + e;
       M = Mn;
     }
   }
@@ -1009,8 +1012,9 @@ __global__ __launch_bounds__(256) void k_logits_fwd(LogitsArgs p) {
   for (int off = 1; off < 64; off <<= 1) {
     const float Mo = __shfl_xor(M, off), So = __shfl_xor(S, off);
     const float Mn = fmaxf(M, Mo);
-    const float a = (M == -INFINITY) ? 0.f : S * fast_exp2((M - Mn) * kLog2e);
-    const float b = (Mo == -INFINITY) ? 0.f : So * fast_exp2((Mo - Mn) * kLog2e);
+    const float base = Mn == -INFINITY ? 0.f : Mn;
+    const float a = S * fast_exp2((M - base) * kLog2e);
+    const float b = So * fast_exp2((Mo - base) * kLog2e);
     S = a + b;
     M = Mn;
   }

@@ -96,3 +96,43 @@ def test_logits_op_large_sampled():
     # every row: the softmax of a row sums to one, i.e. sum_v exp(z - lse) = 1 (fp64 on the GPU)
     s = torch.exp(inp["logits"].double() - lse.double()[:, None]).sum(dim=1)
     assert float((s - 1).abs().max()) < 1e-4
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("V", [8, 512, 1000, 4136, 20000])
+def test_masked_logits(V, dtype):
+    """Entries masked with -infinity, from single ones to all that a lane of the row's wave holds:
+    probability 0, the other entries' log-probabilities as without them; and NaN entries reach the
+    row's results."""
+    m = flp()
+    g = torch.Generator().manual_seed(V)
+    N = 6
+    z = torch.randn(N, V, generator=g).to(dtype)
+    keep = torch.ones(N, V, dtype=torch.bool)
+    keep[1, :V // 2] = False                   # whole chunks, the first ones of many lanes
+    keep[2, V // 2:] = False
+    keep[3] = torch.rand(V, generator=g) < 0.3
+    keep[4, 1:] = False                        # one entry left
+    t = torch.tensor([int(k.nonzero()[len(k.nonzero()) // 2]) if k.any() else 0 for k in keep])
+    keep[torch.arange(N), t] = True
+    z = torch.where(keep, z, -float("inf")).cuda()
+    t = t.cuda()
+    logp, lse = m.logits_forward(z, t)
+    ref = torch.log_softmax(z.double(), 1)
+    want = ref.gather(1, t[:, None])[:, 0]
+    # chains of at most V / 512 + 16 sums, exponents off by (|z| + 4) 4 U
+    tol = (V / 512 + 64) * 2.0 ** -24 * (1 + want.abs()) + 40 * 2.0 ** -24
+    assert bool(((logp.double() - want).abs() <= tol).all())
+    assert bool(((lse.double() - torch.logsumexp(z.double(), 1)).abs() <= tol).all())
+    up = torch.randn(N, generator=g).cuda()
+    d = m.logits_backward(up, lse, z, t)
+    onehot = torch.nn.functional.one_hot(t, V)
+    dref = up.double()[:, None] * (onehot - ref.exp())
+    step = torch.finfo(dtype).eps / 2
+    assert bool(((d.double() - dref).abs() <= (2 * step + 4 * tol[:, None]) * up.double().abs()[:, None]).all())
+    assert not d.cpu()[~keep].any()
+    for lo, hi in ((0, min(8, V)), (V - 8, V)):
+        bad = z.clone()
+        bad[:, lo:hi] = float("nan")
+        logp, lse = m.logits_forward(bad, t)
+        assert bool(logp.isnan().all()) and bool(lse.isnan().all())
