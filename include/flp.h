@@ -92,7 +92,8 @@ size_t flp_forward_workspace_bytes(int64_t N, int64_t D, int64_t V);
  *                (the docs page's Tensor Contract lists bf16 / fp16 / fp32).
  *   hidden       [N, D] x_dtype, 16-byte aligned.
  *   weight       [V, D] x_dtype, 16-byte aligned.
- *   bias         [V] float32, or NULL for no bias.
+ *   bias         [V] float32, or NULL for no bias.  Entries of -infinity or of a large
+ *                negative value (-1e30, the lowest float32) mask their columns.
  *   targets      [N] ids of t_dtype (FLP_I64 or FLP_I32); any value is legal,
  *                an id outside [0, V) marks the row as ignored (logp = 0).
  *   temperature  [N] float32 (> 0, finite; not checked), or NULL for T = 1.

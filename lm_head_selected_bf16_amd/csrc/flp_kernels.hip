@@ -62,9 +62,10 @@ constexpr int kGroupM = 8;        // row tiles per scheduling group
 constexpr int kTileCols = 256;    // vocabulary tile of the logits kernels
 constexpr int kHalfCols = 128;    // columns per wave column in the logits kernels
 // The exponent z log2 e - M log2 e as one FMA is off by the rounding of M log2 e.  Beyond
-// this size the cross entropy takes the difference z - M first, which is exact for the
-// entries that matter (entries masked with -1e30 or the lowest fp32 value would otherwise
-// overflow the exponential), and with lse also what its own rounding left out.
+// this size the forward takes the difference z - M first, which is exact for the entries
+// that matter (tiles masked with -1e30 or the lowest fp32 value would otherwise overflow the
+// exponential), and the cross entropy's backward z - lse with what lse's own rounding left
+// out.
 constexpr float kHugeLogit = 1e4f;
 
 struct BF16 {
@@ -608,8 +609,7 @@ __device__ __forceinline__ float lane_sum(const float (&e)[WNB][4]) {
 
 // LOSS (the cross entropy's forward) adds, when p.zsum is given, the tile's sum of logits
 // per row (times p.zunit, a power of two at most 1 / V, so that columns masked with the
-// lowest fp32 value cannot overflow it), and is safe for tiles and rows masked with such
-// values (kHugeLogit).
+// lowest fp32 value cannot overflow it).
 // SAVE keeps the products h W^T of the tile in p.logits, in the order of the lanes'
 // accumulators (kept_tile), for the dlogits kernel of the same row chunk.  16384 x 2688 x
 // 131072 bf16 on MI355X: this kernel 8.7 -> 9.8 ms, k_dz 9.4 -> 3.1 ms (17.2 GB read and
@@ -745,13 +745,12 @@ __global__ __launch_bounds__(128 * WM) void k_fwd(FwdArgs p) {
     for (int nb = 0; nb < WNB; ++nb)
 #pragma unroll
       for (int r = 0; r < 4; ++r) e[nb][r] = fast_exp2(fmaf(acc[mb][nb][r], k, -Ml));
-    if constexpr (LOSS) {
-      if (fabsf(M) > kHugeLogit) {
+    if (fabsf(M) > kHugeLogit) {
 #pragma unroll
-        for (int nb = 0; nb < WNB; ++nb)
+      for (int nb = 0; nb < WNB; ++nb)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) e[nb][r] = fast_exp2((acc[mb][nb][r] - base) * kLog2e);
-      }
+        for (int r = 0; r < 4; ++r)
+          e[nb][r] = fast_exp2((acc[mb][nb][r] * invT[mb] - base) * kLog2e);
     }
     float s = lane_sum<WNB>(e);
     f32x2_t q = pair16(s);

@@ -301,3 +301,38 @@ def test_longseq_chunked_equals_one_chunk():
     torch.cuda.synchronize()
     assert torch.equal(five[0], one[0]), "d_hidden"
     assert torch.equal(five[1], one[1]), "d_weight"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("low", [-1e30, -3e29, torch.finfo(torch.float32).min, -float("inf"), -2e4])
+@pytest.mark.parametrize("N,V", [(1, 600), (40, 1500), (300, 70001)])
+def test_masked_vocabulary(N, V, low, dtype):
+    """Entries masked through the bias, whole vocabulary tiles among them: the log-probabilities
+    are those of the remaining vocabulary, with and without a temperature, and masked entries
+    get no gradient."""
+    m = flp()
+    g = torch.Generator().manual_seed(V + N)
+    h = torch.randn(N, 64, generator=g).to(dtype).cuda()
+    w = (torch.randn(V, 64, generator=g) * 0.05).to(dtype).cuda()
+    b = (torch.randn(V, generator=g) * 0.3).cuda()
+    keep = torch.zeros(V, dtype=torch.bool, device="cuda")
+    keep[:200] = True
+    keep[520:590] = True
+    masked = torch.where(keep, b, torch.full_like(b, low))
+    t = keep.nonzero()[:, 0][torch.randint(0, 270, (N,), generator=g).cuda()]
+    index = torch.cumsum(keep, 0) - 1
+    for temp in (None, torch.rand(N, generator=g).cuda() + 0.5):
+        logp, lse = m.forward(h, w, t, masked, temp)
+        z = h.double() @ w[keep].double().t() + b[keep].double()
+        if temp is not None:
+            z = z / temp.double()[:, None]
+        ref = torch.log_softmax(z, 1)
+        want = ref.gather(1, index[t][:, None])[:, 0]
+        # logits off by 64 U of their products' sizes and 4 U of their own, exponents and sums
+        # by 4 U (|z| + 4) and 64 U
+        size = float((h.double().abs() @ w.double().abs().t()).max()) / (0.5 if temp is not None else 1)
+        tol = 2 * (64 * size + 8 * (float(z.abs().max()) + 8) + 64) * 2.0 ** -24
+        assert bool(((logp.double() - want).abs() <= tol).all())
+        assert bool(((lse.double() - torch.logsumexp(z, 1)).abs() <= tol).all())
+        dh, dw, db = m.backward(torch.ones(N, device="cuda"), lse, h, w, t, masked, temp)
+        assert not dw[~keep].any() and not db[~keep].any() and bool(dh.isfinite().all())
