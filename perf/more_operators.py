@@ -172,7 +172,7 @@ def prepare(case, seed):
         m, v = draw_().mul_(0.3), draw_().square_().mul_(0.5)
         if case["bits"] == 8:
             s["m"], s["m_scale"] = _to8(m)
-            s["v"], s["v_scale"] = _to8(v.sqrt_())
+            s["v"], s["v_scale"] = _to8(v.sqrt_(), divisor=True)
         else:
             s["m"], s["v"] = m, v
         s["step"] = 1000 + int(seed) % 7
@@ -273,14 +273,15 @@ def _plain_norm(s):
     return outs + (dr.to(dt), dy.to(dt))
 
 
-def _to8(x):
-    """x in 8 bits with a scale per _GROUP elements; what is positive stays so, since the roots
-    of second moments are divided by."""
+def _to8(x, divisor=False):
+    """x in 8 bits with a scale per _GROUP elements.  Of what is divided by (the roots of second
+    moments), no positive value becomes 0."""
     b = x.view(-1, _GROUP)
     top = b.abs().amax(dim=1, keepdim=True).clamp_(min=_FLOOR)
     q = b * (_TOP / top)
-    q = torch.where(b > 0, q.clamp(min=_LEAST), q).to(torch.float8_e4m3fn)
-    return q.view(-1), (top * (1.0 / _TOP)).view(-1)
+    if divisor:
+        q = torch.where(b > 0, q.clamp(min=_LEAST), q)
+    return q.to(torch.float8_e4m3fn).view(-1), (top * (1.0 / _TOP)).view(-1)
 
 
 def _from8(q, scale):
@@ -307,7 +308,7 @@ def _plain_adamw(s):
     if eight:
         q, scale = _to8(m)
         s["m"].copy_(q), s["m_scale"].copy_(scale)
-        q, scale = _to8(root)
+        q, scale = _to8(root, divisor=True)
         s["v"].copy_(q), s["v_scale"].copy_(scale)
     else:
         s["m"].copy_(m), s["v"].copy_(v)
@@ -437,8 +438,7 @@ def _exact_adamw(case, s):
     def in8(x):
         top = x.view(-1, _GROUP).abs().amax(dim=1).clamp(min=_FLOOR)
         q = x / top.repeat_interleave(_GROUP) * _TOP
-        code = q.float().to(torch.float8_e4m3fn).double()
-        return torch.where((x > 0) & (code < _LEAST), _LEAST, code), top / _TOP
+        return q.float().to(torch.float8_e4m3fn).double(), top / _TOP
 
     g = s["grad"].double()
     m = held("m") * b1 + g * (1 - b1)
@@ -453,7 +453,8 @@ def _exact_adamw(case, s):
         out["master"] = p
     if case["bits"] == 32:
         return {**out, "m": m, "v": v}
-    (out["m"], out["m_scale"]), (out["v"], out["v_scale"]) = in8(m), in8(root)
+    (out["m"], out["m_scale"]), (code, out["v_scale"]) = in8(m), in8(root)
+    out["v"] = torch.where((root > 0) & (code < _LEAST), _LEAST, code)
     return out
 
 
