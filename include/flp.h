@@ -564,6 +564,57 @@ flp_status flp_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, cons
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * One AdamW step over many tensors at once, with decoupled weight decay:
+ *
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t)  m / (sqrt(v / (1 - beta2^t)) + eps)
+ *
+ * in fp32, element by element; param, the states and the master copy are updated in place.
+ *
+ *   tensors      n_tensors descriptors in HOST memory, read during the call.  Their types may
+ *                differ from tensor to tensor; a tensor with n = 0 is left alone.
+ *   p_dtype      FLP_BF16, FLP_F16 or FLP_F32.  g_dtype: the same, or FLP_F32.
+ *   master       [n] float32 copy of the parameters that the step updates, param then being
+ *                its rounding; or NULL: param is updated and rounded itself.
+ *   state_bits   32: exp_avg and exp_avg_sq are [n] float32, m and v.
+ *                8: they are [n] bytes, e4m3 codes of m and of the ROOT of v in units of a
+ *                scale per 256 consecutive elements, exp_avg_scale and exp_avg_sq_scale
+ *                [ceil(n / 256)] float32 (the block's largest magnitude, at least 2^-100,
+ *                over 448).  The step itself uses m and v before they are rounded.  A positive
+ *                root rounds to no less than the smallest positive code.  A gradient that is
+ *                not finite makes its block's states NaN (in 32 bits, its element's).
+ *   step         number t of this step, from 1; or step_on_device, one int64 that the kernel
+ *                reads (below 1 counts as 1), so that a captured call takes part in every
+ *                replay's own step.  The caller counts.
+ *   lr           or lr_on_device, one float32.   grad_scale: one float32 on the device, or
+ *                NULL for 1 (a clipping factor, or what takes a loss scale back).
+ *   beta1, beta2 in [0, 1).   eps >= 0.
+ *
+ * param, states, scales and master copies of all tensors must be distinct memory; gradients
+ * may repeat.  Alignment: each pointer to its element size.  An element's result does not
+ * depend on the other tensors of the call.
+ */
+typedef struct flp_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;      /* state_bits 8 */
+  float* exp_avg_sq_scale;   /* state_bits 8 */
+  float* master;             /* or NULL */
+  int64_t n;
+  double weight_decay;
+  flp_dtype p_dtype;
+  flp_dtype g_dtype;
+} flp_adamw_tensor;
+
+flp_status flp_adamw_step(int64_t n_tensors, const flp_adamw_tensor* tensors, int state_bits,
+                          int64_t step, const int64_t* step_on_device, double lr,
+                          const float* lr_on_device, double beta1, double beta2, double eps,
+                          const float* grad_scale, void* stream);
+
+/*
  * Measurement probes (not part of the operator): the achievable dense bf16
  * MFMA rate and the shader clock it runs at, and the achievable streaming-read
  * bandwidth, so that figures can be quoted against measured peaks as well as
@@ -613,7 +664,8 @@ typedef enum flp_kernel_kind {
   FLP_K_DROPOUT = 11,   /* flp_dropout */
   FLP_K_LAYER_NORM = 12, /* flp_layer_norm_forward / flp_layer_norm_backward */
   FLP_K_LOSS = 13,      /* flp_cross_entropy_*: row losses, their sum, gradient factors */
-  FLP_K_COUNT = 14
+  FLP_K_ADAMW = 14,     /* flp_adamw_step */
+  FLP_K_COUNT = 15
 } flp_kernel_kind;
 
 void flp_profile_enable(int on);

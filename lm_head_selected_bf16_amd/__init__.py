@@ -25,7 +25,7 @@ from ._abi import (FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpErro
                    flp_cross_entropy_forward_workspace_bytes, flp_cross_entropy_gradients,
                    flp_cross_entropy_gradients_workspace_bytes, flp_scale_inplace,
                    flp_dropout, flp_layer_norm_backward, flp_layer_norm_backward_workspace_bytes,
-                   flp_layer_norm_forward,
+                   flp_layer_norm_forward, flp_adamw_step, flp_adamw_tensor,
                    flp_forward_indexed, flp_forward_noalloc, FLP_FORWARD_NOALLOC_MAX_BYTES,
                    flp_forward_indexed_workspace_bytes, flp_forward_partial,
                    flp_forward_partial_bytes, flp_forward_workspace_bytes, flp_logits_backward,
@@ -42,7 +42,8 @@ from .torch_ops import (LinearLogp, backward, backward_workspace_bytes,  # noqa:
                         Embedding, embedding, embedding_backward, embedding_forward,
                         cross_entropy_backward, cross_entropy_forward, cross_entropy_gradients,
                         linear_cross_entropy, dropout, dropout_forward, layer_norm,
-                        layer_norm_backward, layer_norm_forward)
+                        layer_norm_backward, layer_norm_forward, AdamWState, adamw_state,
+                        adamw_step)
 
 __all__ = [
     "FLP_BF16", "FLP_F16", "FLP_F32", "FLP_I32", "FLP_I64", "FLP_OK", "FlpError",
@@ -76,4 +77,5 @@ __all__ = [
     "layer_norm", "layer_norm_forward", "layer_norm_backward",
     "flp_layer_norm_forward", "flp_layer_norm_backward",
     "flp_layer_norm_backward_workspace_bytes",
+    "AdamWState", "adamw_state", "adamw_step", "flp_adamw_step", "flp_adamw_tensor",
 ]

@@ -85,6 +85,8 @@ SIGNATURES = {
     "flp_layer_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
     "flp_layer_norm_backward": (_int, [_i64, _i64, _int, _vp, _vp, _int, _vp, _fp, _fp, _vp, _vp,
                                        _vp, _vp, _sz, _vp]),
+    "flp_adamw_step": (_int, [_i64, _vp, _int, _i64, _vp, _double, _fp, _double, _double, _double,
+                              _fp, _vp]),
     "flp_probe_scratch_bytes": (_sz, []),
     "flp_probe_mfma": (_int, [_int, _i64, _vp, _sz, ctypes.POINTER(ctypes.c_double),
                               ctypes.POINTER(ctypes.c_double), _vp]),
@@ -361,6 +363,21 @@ def flp_layer_norm_backward(N, D, x_dtype, grad_out, x, w_dtype, weight, mean, r
                                               workspace_bytes, stream))
 
 
+class flp_adamw_tensor(ctypes.Structure):
+    """One tensor of flp_adamw_step; the pointers are int addresses (0 or None for NULL)."""
+    _fields_ = [("param", _vp), ("grad", _vp), ("exp_avg", _vp), ("exp_avg_sq", _vp),
+                ("exp_avg_scale", _vp), ("exp_avg_sq_scale", _vp), ("master", _vp), ("n", _i64),
+                ("weight_decay", _double), ("p_dtype", _int), ("g_dtype", _int)]
+
+
+def flp_adamw_step(n_tensors, tensors, state_bits, step, step_on_device, lr, lr_on_device, beta1,
+                   beta2, eps, grad_scale, stream) -> int:
+    """Raw call: tensors is a ctypes array of flp_adamw_tensor (or None), every other pointer
+    argument an int address (0 for NULL)."""
+    return int(load().flp_adamw_step(n_tensors, tensors, state_bits, step, step_on_device, lr,
+                                     lr_on_device, beta1, beta2, eps, grad_scale, stream))
+
+
 def flp_probe_scratch_bytes() -> int:
     return int(load().flp_probe_scratch_bytes())
 
@@ -382,7 +399,7 @@ def flp_probe_read(buffer: int, nbytes: int, scratch: int, scratch_bytes: int, s
 
 KERNEL_KINDS = ("forward", "merge", "dlogits", "transpose", "d_hidden", "d_weight", "d_bias",
                 "logits_forward", "logits_backward", "rows", "embedding", "dropout", "layer_norm",
-                "loss")
+                "loss", "adamw")
 
 
 def flp_profile_enable(on: bool) -> None:

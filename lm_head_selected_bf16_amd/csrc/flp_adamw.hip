@@ -1,0 +1,284 @@
+// One AdamW step over many tensors.
+//
+//   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,   g = grad * grad_scale
+//   p = p (1 - lr wd) - lr / (1 - b1^t)  m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// All arithmetic is fp32; p is rounded once to its type, or kept whole in an fp32 master
+// copy beside it.  m and v are held in fp32, or in 8 bits: each block of 256 elements has
+// a scale (its largest magnitude over 448), and an element is the e4m3 code of its ratio to
+// the scale (relative rounding error 2^-4, range 2^-18 within a block).  What is held of v
+// is its root: its range halves that way, and the update divides by the root.  A positive
+// root never rounds to 0: a coordinate whose m survives would otherwise be divided by eps.
+//
+// Bound by memory: one pass over grad, p, m, v and the master copies.
+//
+// The tensors of one mix of types go in launches of up to kAdamTensors; a launch's table of
+// tensors is its argument, so a captured call needs no memory of its own.  The elements are
+// cut into tiles of 2048 that never span two tensors, which the workgroups take in turn.
+// Every element's result is a function of its own block alone: no atomics, the same bits
+// on every run and in every grouping of the tensors.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "flp_chunk.h"
+#include "flp_launch.h"
+
+namespace flp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = kThreads * kChunk;
+constexpr float kTop = 448.0f;            // the largest e4m3 value
+constexpr float kLeast = 0x1p-9f;         // the smallest positive one
+constexpr float kBlockFloor = 0x1p-100f;  // a block's largest magnitude counts as at least this
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 loose8 __attribute__((aligned(1)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Eight codes: n valid elements at p (zeros past them).
+__device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int64_t n) {
+  if (n >= kChunk) return *reinterpret_cast<const loose8*>(p);
+  u32x2 w = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k)
+    if (k < n) w[k >> 2] |= uint32_t(p[k]) << (8 * (k & 3));
+  return w;
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t n, u32x2 w) {
+  if (n >= kChunk) {
+    *reinterpret_cast<loose8*>(p) = w;
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k)
+    if (k < n) p[k] = uint8_t(w[k >> 2] >> (8 * (k & 3)));
+}
+
+__device__ __forceinline__ void decode(u32x2 w, float scale, float (&x)[kChunk]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[h]), false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[h]), true);
+    x[4 * h] = lo.x * scale;
+    x[4 * h + 1] = lo.y * scale;
+    x[4 * h + 2] = hi.x * scale;
+    x[4 * h + 3] = hi.y * scale;
+  }
+}
+
+// The largest over the 32 lanes that hold a block, the same in each: quad permutations, the
+// mirrors of 8 and 16 lanes, and the 16-lane swap.
+__device__ __forceinline__ float block_max(float x) {
+  auto dpp = [](float v, auto ctrl) {
+    return __int_as_float(
+        __builtin_amdgcn_mov_dpp(__float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  x = fmaxf(x, dpp(x, std::integral_constant<int, 0xB1>{}));
+  x = fmaxf(x, dpp(x, std::integral_constant<int, 0x4E>{}));
+  x = fmaxf(x, dpp(x, std::integral_constant<int, 0x141>{}));
+  x = fmaxf(x, dpp(x, std::integral_constant<int, 0x140>{}));
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+
+// Codes of x and the block's scale.  The ratio is at most 448 (1 + 2^-22), which rounds to 448.
+template <bool DIVISOR>
+__device__ __forceinline__ u32x2 encode(const float (&x)[kChunk], float& scale) {
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) top = fmaxf(top, fabsf(x[k]));
+  top = fmaxf(block_max(top), kBlockFloor);
+  scale = top * (1.0f / kTop);
+  const float inv = (1.0f / top) * kTop;
+  float q[kChunk];
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) {
+    q[k] = x[k] * inv;
+    if (DIVISOR) q[k] = x[k] > 0.f && q[k] < kLeast ? kLeast : q[k];  // NaN stays
+  }
+  u32x2 w;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
+    w[h] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], v, true));
+  }
+  return w;
+}
+
+// The roots of v.  Where all of a wave's lie in the middle of fp32's range, an approximation and
+// one step of Newton's iteration: correctly rounded but for a case in some ten million, at half of
+// what the library's root costs, which takes the others (zeros, infinities).
+__device__ __forceinline__ void roots_of(const float (&v)[kChunk], float (&root)[kChunk]) {
+  float lo = v[0], hi = v[0];
+#pragma unroll
+  for (int e = 1; e < kChunk; ++e) {
+    lo = fminf(lo, v[e]);
+    hi = fmaxf(hi, v[e]);
+  }
+  if (__builtin_amdgcn_ballot_w64(!(lo > 0x1p-100f && hi < 0x1p100f)) != 0) {
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) root[e] = sqrtf(v[e]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < kChunk; ++e) {
+    const float y = __builtin_amdgcn_rsqf(v[e]);
+    const float r = v[e] * y;
+    root[e] = fmaf(fmaf(-r, r, v[e]), 0.5f * y, r);
+  }
+}
+
+// P, G: element types of the parameters and gradients.
+//
+// m and v are rounded after every product and sum, as the formula in fp32 tensors does it: the
+// codes of both then agree with it bit for bit, where a fused product would move some of them
+// across a rounding border.
+template <class P, class G, bool EIGHT, bool MASTER>
+__global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
+  // 1 / (1 - b1^t) and 1 / sqrt(1 - b2^t) in 64 bits: fp32 loses the early steps of b2 near 1
+  double lr = a.lr, c1 = a.c1, c2 = a.c2;
+  if (a.lr_on_device != nullptr) lr = *a.lr_on_device;
+  if (a.step_on_device != nullptr) {
+    const double t = double(max(*a.step_on_device, int64_t(1)));
+    c1 = -1.0 / expm1(t * a.log_b1);
+    c2 = 1.0 / sqrt(-expm1(t * a.log_b2));
+  }
+  const float rate = float(lr * c1), root_scale = float(c2);
+  const float grad_scale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
+  const int lane8 = int(threadIdx.x) * kChunk;
+  AdamTensor t = a.t[0];
+  float keep = float(1.0 - lr * double(t.decay));
+  int k = 0;
+
+  // The tile's elements from `first` on; FULL: all of them exist.
+  auto work = [&](int64_t first, auto whole) {
+    constexpr bool kFull = decltype(whole)::value;
+    const int64_t at = first + lane8;
+    const int64_t n = kFull ? int64_t(kChunk) : t.n - at;
+    float p[kChunk], m[kChunk], v[kChunk], root[kChunk];
+    Chunk<G> g;
+    Chunk<float> w, x;
+    Chunk<P> c;
+    g.load(static_cast<const G*>(t.grad) + at, n);
+    if constexpr (MASTER)
+      w.load(t.master + at, n);
+    else
+      c.load(static_cast<const P*>(t.param) + at, n);
+    if constexpr (EIGHT) {
+      const int64_t block = at / kAdamBlock;
+      const u32x2 cm = load_codes(static_cast<const uint8_t*>(t.m) + at, n);
+      const u32x2 cv = load_codes(static_cast<const uint8_t*>(t.v) + at, n);
+      decode(cm, n > 0 ? t.m_scale[block] : 0.f, m);
+      decode(cv, n > 0 ? t.v_scale[block] : 0.f, v);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) v[e] *= v[e];
+    } else {
+      x.load(static_cast<const float*>(t.m) + at, n);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) m[e] = x.v[e];
+      x.load(static_cast<const float*>(t.v) + at, n);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) v[e] = x.v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) {
+      if constexpr (MASTER)
+        p[e] = w.v[e];
+      else
+        p[e] = float(P(c.v[e]));
+      const float ge = float(G(g.v[e])) * grad_scale;
+      m[e] = a.b1 * m[e] + a.one_b1 * ge;
+      v[e] = a.b2 * v[e] + a.one_b2 * (ge * ge);
+    }
+    roots_of(v, root);
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) {
+      const float by = __builtin_amdgcn_rcpf(fmaf(root[e], root_scale, a.eps));
+      p[e] = fmaf(-rate, m[e] * by, p[e] * keep);
+    }
+    if constexpr (MASTER) {
+      // What is rounded is the master copy as stored: the compiler would make one instruction of
+      // the last sum and its rounding to fp16, which rounds the unrounded sum.
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) asm volatile("" : "+v"(p[e]));
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) w.v[e] = p[e];
+      w.store(t.master + at, n);
+    }
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) c.v[e] = P(p[e]);
+    c.store(static_cast<P*>(t.param) + at, n);
+    if constexpr (EIGHT) {
+      // past the tensor's end everything is 0, which changes no block's scale
+      float sm, sv;
+      const u32x2 cm = encode<false>(m, sm), cv = encode<true>(root, sv);
+      store_codes(static_cast<uint8_t*>(t.m) + at, n, cm);
+      store_codes(static_cast<uint8_t*>(t.v) + at, n, cv);
+      if ((threadIdx.x & (kAdamBlock / kChunk - 1)) == 0 && n > 0) {
+        t.m_scale[at / kAdamBlock] = sm;
+        t.v_scale[at / kAdamBlock] = sv;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) x.v[e] = m[e];
+      x.store(static_cast<float*>(t.m) + at, n);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) x.v[e] = v[e];
+      x.store(static_cast<float*>(t.v) + at, n);
+    }
+  };
+  for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    if (k + 1 < a.count && tile >= a.t[k + 1].first) {
+      do ++k;
+      while (k + 1 < a.count && tile >= a.t[k + 1].first);
+      t = a.t[k];
+      keep = float(1.0 - lr * double(t.decay));
+    }
+    const int64_t first = (tile - t.first) * kTile;
+    if (t.n - first >= kTile)
+      work(first, std::true_type{});
+    else
+      work(first, std::false_type{});
+  }
+}
+
+// f(parameter type, gradient type): gradients have the parameters' type or fp32.
+template <class F>
+void by_types(flp_dtype p, flp_dtype g, F f) {
+  if (p == FLP_F32) return f(float{}, float{});
+  if (p == FLP_BF16) return g == FLP_F32 ? f(__bf16{}, float{}) : f(__bf16{}, __bf16{});
+  return g == FLP_F32 ? f(_Float16{}, float{}) : f(_Float16{}, _Float16{});
+}
+
+}  // namespace
+
+hipError_t launch_adamw(flp_dtype p, flp_dtype g, bool eight, bool master, AdamArgs& a,
+                        hipStream_t s) {
+  ProfScope ps(FLP_K_ADAMW, s);
+  int64_t tiles = 0;
+  for (int k = 0; k < a.count; ++k) {
+    a.t[k].first = tiles;
+    tiles += (a.t[k].n + kTile - 1) / kTile;
+  }
+  a.tiles = tiles;
+  const dim3 grid(unsigned(std::min<int64_t>(tiles, 2048)));
+  by_types(p, g, [&](auto x, auto y) {
+    using P = decltype(x);
+    using G = decltype(y);
+    if (eight && master)
+      hipLaunchKernelGGL((k_adamw<P, G, true, true>), grid, dim3(kThreads), 0, s, a);
+    else if (eight)
+      hipLaunchKernelGGL((k_adamw<P, G, true, false>), grid, dim3(kThreads), 0, s, a);
+    else if (master)
+      hipLaunchKernelGGL((k_adamw<P, G, false, true>), grid, dim3(kThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_adamw<P, G, false, false>), grid, dim3(kThreads), 0, s, a);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace flp

@@ -1002,6 +1002,67 @@ flp_status flp_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p, co
   return FLP_OK;
 }
 
+// ---- AdamW ----
+
+flp_status flp_adamw_step(int64_t n_tensors, const flp_adamw_tensor* tensors, int state_bits,
+                          int64_t step, const int64_t* step_on_device, double lr,
+                          const float* lr_on_device, double beta1, double beta2, double eps,
+                          const float* grad_scale, void* stream) {
+  flp_status st = validate_adamw_step(n_tensors, tensors, state_bits, step, step_on_device, lr,
+                                      lr_on_device, beta1, beta2, eps, grad_scale);
+  if (st != FLP_OK) return st;
+  if ((st = check_device()) != FLP_OK) return st;
+  AdamArgs a{};
+  a.lr = lr;
+  // log 0 is -infinity, and expm1 of it -1: b = 0 needs no correction
+  a.log_b1 = std::log(beta1);
+  a.log_b2 = std::log(beta2);
+  if (step_on_device == nullptr) {
+    a.c1 = -1.0 / std::expm1(double(step) * a.log_b1);
+    a.c2 = 1.0 / std::sqrt(-std::expm1(double(step) * a.log_b2));
+  }
+  a.lr_on_device = lr_on_device;
+  a.step_on_device = step_on_device;
+  a.grad_scale = grad_scale;
+  a.b1 = float(beta1);
+  a.one_b1 = float(1.0 - beta1);
+  a.b2 = float(beta2);
+  a.one_b2 = float(1.0 - beta2);
+  a.eps = float(eps);
+  // Each mix of types in launches of its own, its tensors in their order.
+  const flp_dtype types[] = {FLP_BF16, FLP_F16, FLP_F32};
+  for (int mix = 0; mix < 12; ++mix) {
+    const flp_dtype p = types[mix >> 2];
+    const bool wide = (mix & 2) != 0, master = (mix & 1) != 0;
+    if (p == FLP_F32 && !wide) continue;
+    const flp_dtype g = wide ? FLP_F32 : p;
+    a.count = 0;
+    for (int64_t k = 0; k < n_tensors; ++k) {
+      const flp_adamw_tensor& t = tensors[k];
+      if (t.n == 0 || t.p_dtype != p || t.g_dtype != g || (t.master != nullptr) != master) continue;
+      AdamTensor& u = a.t[a.count++];
+      u.param = t.param;
+      u.grad = t.grad;
+      u.m = t.exp_avg;
+      u.v = t.exp_avg_sq;
+      u.m_scale = t.exp_avg_scale;
+      u.v_scale = t.exp_avg_sq_scale;
+      u.master = t.master;
+      u.n = t.n;
+      u.decay = float(t.weight_decay);
+      if (a.count < kAdamTensors) continue;
+      if (launch_adamw(p, g, state_bits == 8, master, a, static_cast<hipStream_t>(stream)) !=
+          hipSuccess)
+        return FLP_HIP_ERROR;
+      a.count = 0;
+    }
+    if (a.count > 0 && launch_adamw(p, g, state_bits == 8, master, a,
+                                    static_cast<hipStream_t>(stream)) != hipSuccess)
+      return FLP_HIP_ERROR;
+  }
+  return FLP_OK;
+}
+
 // ---- measurement probes ----
 
 size_t flp_probe_scratch_bytes(void) { return probe_scratch_bytes(); }
@@ -1078,7 +1139,7 @@ const char* flp_status_string(flp_status status) {
 
 const char* flp_build_info(void) {
   static const std::string info = [] {
-    char buf[2048];
+    char buf[4096];
     std::snprintf(buf, sizeof(buf),
                   "flp 0.2 gfx950 fallback=none vocab_tile=%lld row_quantum=%lld git=%s | %s",
                   (long long)kVocabTile, (long long)kRowQuantum,

@@ -258,6 +258,36 @@ hipError_t launch_loss_count(int64_t N, int64_t V, const void* targets, bool t64
 // x *= *factor in place (n elements); nothing is touched when the factor is 1.
 hipError_t launch_scale(flp_dtype x_dtype, int64_t n, void* x, const float* factor, hipStream_t s);
 
+// AdamW (flp_adamw.hip).
+struct AdamTensor {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;            // null for fp32 states
+  float* v_scale;
+  float* master;             // or null
+  int64_t n;
+  int64_t first;             // the tensor's first tile (set by the launcher)
+  float decay;
+};
+constexpr int kAdamTensors = 48;  // of a launch: its argument stays below 4 KB
+struct AdamArgs {
+  double lr, c1, c2;         // c1 = 1 / (1 - b1^t), c2 = 1 / sqrt(1 - b2^t)
+  double log_b1, log_b2;     // for a step on the device
+  const float* lr_on_device;      // or null
+  const int64_t* step_on_device;  // or null
+  const float* grad_scale;        // or null
+  float b1, one_b1, b2, one_b2, eps;
+  int count;
+  int64_t tiles;             // set by the launcher
+  AdamTensor t[kAdamTensors];
+};
+static_assert(sizeof(AdamArgs) <= 4096, "a kernel's arguments");
+// Tensors of one mix of types, none of them empty.
+hipError_t launch_adamw(flp_dtype p, flp_dtype g, bool eight, bool master, AdamArgs& a,
+                        hipStream_t s);
+
 // Measurement probes (flp_probe.hip); they synchronise the stream.
 size_t probe_scratch_bytes();
 hipError_t probe_mfma(int zero, int64_t iters, void* scratch, hipStream_t s, double* tflops,

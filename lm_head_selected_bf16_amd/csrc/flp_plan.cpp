@@ -4,7 +4,10 @@
 #include "flp_plan.h"
 
 #include <algorithm>
+#include <cmath>
 #include <limits>
+#include <new>
+#include <vector>
 
 namespace flp {
 
@@ -863,6 +866,82 @@ flp_status validate_dropout(int64_t n, flp_dtype x_dtype, const void* x, double 
   const Span ins[] = {span(x, size_t(n) * xs), span(rng, 16)};
   const Span outs[] = {span(out, size_t(n) * xs)};
   return any_alias(outs, 1, ins, 2) ? FLP_INVALID_ARGUMENT : FLP_OK;
+}
+
+namespace {
+
+// Whether an output span overlaps an input or another output, by a sweep over all of them (a
+// step has thousands).
+struct Range {
+  uintptr_t lo, hi;
+  bool out;
+};
+bool any_alias(std::vector<Range>& all) {
+  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t any = 0, outs = 0;  // the furthest ends so far
+  for (const Range& r : all) {
+    if (r.lo < outs || (r.out && r.lo < any)) return true;
+    any = std::max(any, r.hi);
+    if (r.out) outs = std::max(outs, r.hi);
+  }
+  return false;
+}
+
+}  // namespace
+
+flp_status validate_adamw_step(int64_t n_tensors, const flp_adamw_tensor* tensors, int state_bits,
+                               int64_t step, const int64_t* step_on_device, double lr,
+                               const float* lr_on_device, double beta1, double beta2, double eps,
+                               const float* grad_scale) {
+  const double most = double(std::numeric_limits<float>::max());
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return FLP_INVALID_ARGUMENT;
+  if (state_bits != 8 && state_bits != 32) return FLP_UNSUPPORTED_DTYPE;
+  if (!step_on_device && step < 1) return FLP_INVALID_ARGUMENT;
+  if (!lr_on_device && !(std::fabs(lr) <= most)) return FLP_INVALID_ARGUMENT;
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return FLP_INVALID_ARGUMENT;
+  if (!(eps >= 0.0 && eps <= most)) return FLP_INVALID_ARGUMENT;
+  if (!aligned(step_on_device, 8) || !aligned(lr_on_device, 4) || !aligned(grad_scale, 4))
+    return FLP_MISALIGNED;
+  const bool eight = state_bits == 8;
+  try {
+    std::vector<Range> all;
+    all.reserve(size_t(n_tensors) * 7 + 3);
+    auto add = [&](const void* p, int64_t bytes, bool out) {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+      if (p != nullptr) all.push_back({lo, lo + size_t(bytes), out});
+    };
+    add(step_on_device, 8, false);
+    add(lr_on_device, 4, false);
+    add(grad_scale, 4, false);
+    for (int64_t k = 0; k < n_tensors; ++k) {
+      const flp_adamw_tensor& t = tensors[k];
+      const flp_dtype p = t.p_dtype, g = t.g_dtype;
+      if (t.n < 0 || !(std::fabs(t.weight_decay) <= most)) return FLP_INVALID_ARGUMENT;
+      if (p != FLP_BF16 && p != FLP_F16 && p != FLP_F32) return FLP_UNSUPPORTED_DTYPE;
+      if (g != p && g != FLP_F32) return FLP_UNSUPPORTED_DTYPE;
+      if (!mul_ok(t.n, 4)) return FLP_UNSUPPORTED_SHAPE;
+      if (t.n == 0) continue;
+      if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return FLP_INVALID_ARGUMENT;
+      if (eight && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return FLP_INVALID_ARGUMENT;
+      const size_t ps = dtype_size(p), gs = dtype_size(g), ss = eight ? 1 : 4;
+      if (!aligned(t.param, ps) || !aligned(t.grad, gs) || !aligned(t.exp_avg, ss) ||
+          !aligned(t.exp_avg_sq, ss) || !aligned(t.master, 4) ||
+          (eight && (!aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4))))
+        return FLP_MISALIGNED;
+      add(t.param, t.n * int64_t(ps), true);
+      add(t.grad, t.n * int64_t(gs), false);
+      add(t.exp_avg, t.n * int64_t(ss), true);
+      add(t.exp_avg_sq, t.n * int64_t(ss), true);
+      add(t.master, t.n * 4, true);
+      if (eight) {
+        add(t.exp_avg_scale, ceil_div(t.n, kAdamBlock) * 4, true);
+        add(t.exp_avg_sq_scale, ceil_div(t.n, kAdamBlock) * 4, true);
+      }
+    }
+    return any_alias(all) ? FLP_INVALID_ARGUMENT : FLP_OK;
+  } catch (const std::bad_alloc&) {
+    return FLP_HIP_ERROR;
+  }
 }
 
 }  // namespace flp

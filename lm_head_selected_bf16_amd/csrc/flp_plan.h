@@ -153,6 +153,9 @@ NormLayout norm_layout(int64_t N, int64_t D);
 // ---- dropout: elements whose 16 random bits are below this are dropped (65536: all) ----
 inline uint32_t dropout_threshold(double p) { return uint32_t(p * 65536.0 + 0.5); }
 
+// ---- AdamW: elements that share a scale of the 8-bit states ----
+constexpr int64_t kAdamBlock = 256;
+
 // ---- validation (pure host logic; never dereferences a pointer) ----
 flp_status validate_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,
                             const void* hidden, const void* weight, const float* bias,
@@ -267,5 +270,10 @@ flp_status validate_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype,
                                         const void* workspace, size_t workspace_bytes);
 flp_status validate_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p,
                             const int64_t* rng, const void* out);
+// Reads the host array `tensors`, none of the pointers in it.
+flp_status validate_adamw_step(int64_t n_tensors, const flp_adamw_tensor* tensors, int state_bits,
+                               int64_t step, const int64_t* step_on_device, double lr,
+                               const float* lr_on_device, double beta1, double beta2, double eps,
+                               const float* grad_scale);
 
 }  // namespace flp

@@ -15,6 +15,7 @@
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "flp.h"
 
@@ -38,6 +39,7 @@ struct Api {
   decltype(&::flp_cross_entropy_forward_workspace_bytes) loss_forward_bytes;
   decltype(&::flp_cross_entropy_backward) loss_backward;
   decltype(&::flp_cross_entropy_backward_workspace_bytes) loss_backward_bytes;
+  decltype(&::flp_adamw_step) adamw_step;
 };
 Api api;
 
@@ -56,6 +58,7 @@ void bind(const std::map<std::string, uintptr_t>& at) {
   take(api.loss_forward_bytes, "flp_cross_entropy_forward_workspace_bytes");
   take(api.loss_backward, "flp_cross_entropy_backward");
   take(api.loss_backward_bytes, "flp_cross_entropy_backward_workspace_bytes");
+  take(api.adamw_step, "flp_adamw_step");
 }
 
 // A non-OK status: FlpError in Python, as a Python exception from here on.  A backward runs in
@@ -316,6 +319,113 @@ struct CrossEntropyNode : Function<CrossEntropyNode> {
   }
 };
 
+// ---- AdamW ----
+//
+// No autograd node, but lists of tensors: with its arguments checked in Python, a step over 300
+// tensors would take several ms on the host.
+
+using Tensors = std::vector<at::Tensor>;
+using OptTensors = std::vector<OptTensor>;
+
+void adamw_step(const Tensors& params, const OptTensors& grads, const Tensors& exp_avg,
+                const Tensors& exp_avg_sq, const std::optional<Tensors>& exp_avg_scale,
+                const std::optional<Tensors>& exp_avg_sq_scale,
+                const std::optional<OptTensors>& master, const std::vector<double>& decay,
+                int64_t step, const OptTensor& step_on_device, double lr,
+                const OptTensor& lr_on_device, double beta1, double beta2, double eps,
+                const OptTensor& grad_scale, int64_t stream) {
+  const size_t count = params.size();
+  const bool eight = exp_avg_scale.has_value();
+  TORCH_CHECK_VALUE(grads.size() == count && exp_avg.size() == count &&
+                        exp_avg_sq.size() == count && decay.size() == count &&
+                        (!master || master->size() == count),
+                    "there must be as many gradients, states, master copies and weight decays as "
+                    "parameters");
+  TORCH_CHECK_VALUE(eight == exp_avg_sq_scale.has_value() &&
+                        (!eight || (exp_avg_scale->size() == count &&
+                                    exp_avg_sq_scale->size() == count)),
+                    "states in 8 bits need a scale tensor for each parameter's exp_avg and "
+                    "exp_avg_sq");
+  if (count == 0) return;
+  const at::Device device = params[0].device();
+  auto here = [&](const at::Tensor& t, const char* what) {
+    TORCH_CHECK_VALUE(t.layout() == at::kStrided && t.is_cuda() && t.is_contiguous() &&
+                          t.device() == device,
+                      what, " must be contiguous GPU tensors on one device");
+  };
+  auto scalar = [&](const OptTensor& t, at::ScalarType type, const char* what) -> void* {
+    if (!t) return nullptr;
+    here(*t, what);
+    TORCH_CHECK_VALUE(t->scalar_type() == type && t->numel() == 1, what, " must be one ", type,
+                      " element");
+    return t->data_ptr();
+  };
+  const at::ScalarType held = eight ? at::kFloat8_e4m3fn : at::kFloat;
+  std::vector<flp_adamw_tensor> list;
+  list.reserve(count);
+  Tensors written;
+  for (size_t k = 0; k < count; ++k) {
+    if (!grads[k]) continue;
+    const at::Tensor &p = params[k], &g = *grads[k];
+    const int64_t n = p.numel();
+    here(p, "parameters");
+    here(g, "gradients");
+    TORCH_CHECK_TYPE(p.scalar_type() == at::kBFloat16 || p.scalar_type() == at::kHalf ||
+                         p.scalar_type() == at::kFloat,
+                     "parameters must be bfloat16, float16 or float32");
+    TORCH_CHECK_TYPE(g.scalar_type() == p.scalar_type() || g.scalar_type() == at::kFloat,
+                     "a gradient must have its parameter's dtype or float32");
+    TORCH_CHECK_VALUE(g.sizes() == p.sizes(), "a gradient must have its parameter's shape");
+    flp_adamw_tensor t{};
+    t.param = ptr(p);
+    t.grad = ptr(g);
+    t.n = n;
+    t.weight_decay = decay[k];
+    t.p_dtype = code(p);
+    t.g_dtype = code(g);
+    written.push_back(p);
+    auto state = [&](const at::Tensor& s) {
+      here(s, "states");
+      TORCH_CHECK_TYPE(s.scalar_type() == held, "states must be ", held,
+                       eight ? " where they have scales" : " where they have no scales");
+      TORCH_CHECK_VALUE(s.numel() == n, "a state must have as many elements as its parameter");
+      written.push_back(s);
+      return ptr(s);
+    };
+    auto scale = [&](const at::Tensor& s) {
+      here(s, "scales");
+      TORCH_CHECK_VALUE(s.scalar_type() == at::kFloat && s.numel() == (n + 255) / 256,
+                        "scales must be float32, one for each 256 elements of the parameter");
+      written.push_back(s);
+      return fptr(s);
+    };
+    t.exp_avg = state(exp_avg[k]);
+    t.exp_avg_sq = state(exp_avg_sq[k]);
+    if (eight) {
+      t.exp_avg_scale = scale((*exp_avg_scale)[k]);
+      t.exp_avg_sq_scale = scale((*exp_avg_sq_scale)[k]);
+    }
+    if (master && (*master)[k]) {
+      const at::Tensor& w = *(*master)[k];
+      here(w, "master copies");
+      TORCH_CHECK_VALUE(w.scalar_type() == at::kFloat && w.numel() == n,
+                        "a master copy must be float32 with its parameter's elements");
+      written.push_back(w);
+      t.master = fptr(w);
+    }
+    list.push_back(t);
+  }
+  const auto* at_step = static_cast<const int64_t*>(scalar(step_on_device, at::kLong, "step"));
+  const auto* at_lr = static_cast<const float*>(scalar(lr_on_device, at::kFloat, "lr"));
+  const auto* at_scale = static_cast<const float*>(scalar(grad_scale, at::kFloat, "grad_scale"));
+  check("flp_adamw_step",
+        api.adamw_step(int64_t(list.size()), list.data(), eight ? 8 : 32, step, at_step, lr, at_lr,
+                       beta1, beta2, eps, at_scale, reinterpret_cast<void*>(stream)));
+  // what was saved for a backward has changed
+  for (const at::Tensor& t : written)
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_flp_torch, m) {
@@ -338,6 +448,7 @@ PYBIND11_MODULE(_flp_torch, m) {
                          double eps, int64_t stream) {
     return LayerNormNode::apply(x, weight, bias, eps, stream);
   });
+  m.def("adamw_step", &adamw_step);
   m.def("cross_entropy",
         [](const at::Tensor& hidden, const at::Tensor& weight, const at::Tensor& targets,
            const OptTensor& bias, double smoothing, double z_loss, int64_t reduction,

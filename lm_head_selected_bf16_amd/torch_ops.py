@@ -18,7 +18,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
-from typing import Optional, Tuple
+from typing import List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 from torch.autograd import forward_ad
@@ -979,3 +979,75 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
     dev = x.device
     with _on(dev):
         return _nodes().layer_norm(x, weight, bias, eps, _stream(dev))
+
+
+# ---- AdamW --------------------------------------------------------------------------------------
+
+class AdamWState(NamedTuple):
+    """What adamw_step keeps of each parameter between steps, in lists as long as theirs.
+
+    States in 32 bits are float32 tensors of the parameters' shapes: exp_avg holds the running
+    mean m of the gradients, exp_avg_sq that of their squares, v.  States in 8 bits are
+    float8_e4m3fn, exp_avg_sq holding the root of v, with float32 scales for 256 consecutive
+    elements each: element i of tensor k stands for
+    exp_avg[k].view(-1)[i] * exp_avg_scale[k][i // 256].  master: float32 copies of the
+    parameters (None for a parameter without one), or None."""
+    exp_avg: List[torch.Tensor]
+    exp_avg_sq: List[torch.Tensor]
+    exp_avg_scale: Optional[List[torch.Tensor]] = None
+    exp_avg_sq_scale: Optional[List[torch.Tensor]] = None
+    master: Optional[List[Optional[torch.Tensor]]] = None
+
+
+def adamw_state(params: Sequence[torch.Tensor], bits: int = 32, master: bool = False
+                ) -> AdamWState:
+    """The state before the first step: zeros, in 32 or 8 bits per element; with master, a float32
+    copy of every 16-bit parameter."""
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+    copies = None
+    if master:
+        copies = [None if p.dtype == torch.float32 else p.detach().float().contiguous()
+                  for p in params]
+
+    def zeros(p, n, dtype):
+        return torch.zeros(n, dtype=dtype, device=p.device)
+
+    if bits == 32:
+        m, v = ([zeros(p, p.shape, torch.float32) for p in params] for _ in range(2))
+        return AdamWState(m, v, None, None, copies)
+    m, v = ([zeros(p, p.shape, torch.uint8).view(torch.float8_e4m3fn) for p in params]
+            for _ in range(2))
+    ms, vs = ([zeros(p, -(-p.numel() // 256), torch.float32) for p in params] for _ in range(2))
+    return AdamWState(m, v, ms, vs, copies)
+
+
+def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Tensor]],
+               state: AdamWState, step: Union[int, torch.Tensor],
+               lr: Union[float, torch.Tensor], betas: Tuple[float, float] = (0.9, 0.999),
+               eps: float = 1e-8, weight_decay: Union[float, Sequence[float]] = 0.01,
+               grad_scale: Optional[torch.Tensor] = None) -> None:
+    """One AdamW step over all params at once, in place, through flp_adamw_step:
+
+        m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,   g = grad * grad_scale
+        p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+
+    params: bfloat16, float16 or float32, in any mix; grads: each of its parameter's dtype or
+    float32, None leaves its parameter alone.  step: the number t of this step, from 1.
+    weight_decay: one number, or one for each parameter.  step (int64), lr and grad_scale (float32)
+    may be one-element tensors on the device, which a captured call reads at every replay."""
+    params = list(params)
+    if isinstance(weight_decay, (int, float)):
+        weight_decay = [weight_decay] * len(params)
+    if not params:
+        return
+    at_step, at_lr = (x if isinstance(x, torch.Tensor) else None for x in (step, lr))
+    dev = params[0].device
+    if not params[0].is_cuda:
+        raise ValueError("parameters must be contiguous GPU tensors on one device")
+    with _on(dev):
+        _nodes().adamw_step(params, grads, state.exp_avg, state.exp_avg_sq, state.exp_avg_scale,
+                            state.exp_avg_sq_scale, state.master, weight_decay,
+                            1 if at_step is not None else int(step), at_step,
+                            0.0 if at_lr is not None else float(lr), at_lr, float(betas[0]),
+                            float(betas[1]), float(eps), grad_scale, _stream(dev))
