@@ -564,6 +564,86 @@ flp_status flp_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, cons
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * Root mean square norm of the rows x[i, :]:
+ *
+ *   rstd_i = 1 / sqrt(sum_d x_id^2 / D + eps),   out = x rstd weight
+ *
+ *   x, out    [N, D] x_dtype (FLP_BF16, FLP_F16 or FLP_F32), 1 <= D <= 16384, N < 2^31: rows
+ *             need no alignment beyond their element size.
+ *   weight    [D] of w_dtype (x_dtype or FLP_F32), or NULL for 1.
+ *   eps       >= 0, finite.  A row of zeros with eps = 0 has no norm (NaN).  Rows of any size
+ *             have their norm, as long as fp32 holds rstd.
+ *   out_rstd  [N] float32, or NULL; the backward reads it.
+ *
+ * fp32 arithmetic, one rounding per output element; a row's results do not depend on the
+ * other rows.
+ *
+ * Backward:  g = grad_out weight,  d_x = rstd (g - xhat mean_d(g xhat)),
+ *            d_weight = sum_i grad_out_i xhat_i,   xhat = x rstd
+ *
+ *   d_x, d_weight   may each be NULL.  workspace as for flp_residual_rms_norm_backward, with
+ *   gate_rows = 0.
+ */
+flp_status flp_rms_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                flp_dtype w_dtype, const void* weight, double eps, void* out,
+                                float* out_rstd, void* stream);
+flp_status flp_rms_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, const void* grad_out,
+                                 const void* x, flp_dtype w_dtype, const void* weight,
+                                 const float* rstd, void* d_x, void* d_weight, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * What stands between two blocks of a model: the residual stream x takes in the block's
+ * output y, and the next block's (or the head's) norm is made in the same pass:
+ *
+ *   p = y rstd(y) post_weight  (post_norm nonzero)   or  p = y
+ *   r = x + scale gate p,      n = r rstd(r) weight
+ *
+ * with the norm and the rounding of flp_rms_norm_forward (n is made from r before its
+ * rounding).
+ *
+ *   x, y, out_r, out_n   [N, D] x_dtype.  y = NULL (with post_norm = 0, no gate, out_r = NULL)
+ *                is flp_rms_norm_forward.
+ *   weight, post_weight  [D] of w_dtype, each may be NULL for 1 (post_weight only with
+ *                post_norm).
+ *   gate         [gate_rows, D] of w_dtype, N a multiple of gate_rows: row i takes gate row
+ *                i / (N / gate_rows).  One row is a gate per channel, one per sequence a
+ *                modulation, N rows a gate per element.  NULL with gate_rows = 0 for 1.
+ *   scale        finite.
+ *   out_rstd, out_post_rstd  [N] float32, or NULL; the backward reads them (the second with
+ *                post_norm only).
+ */
+flp_status flp_residual_rms_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                         const void* y, flp_dtype w_dtype, const void* weight,
+                                         int post_norm, const void* post_weight,
+                                         int64_t gate_rows, const void* gate, double scale,
+                                         double eps, void* out_r, void* out_n, float* out_rstd,
+                                         float* out_post_rstd, void* stream);
+/*
+ *   gw  = grad_n weight,   d_x = grad_r + rstd (gw - rhat mean_d(gw rhat)),   rhat = r rstd
+ *   d_weight = sum_i grad_n rhat,   d_gate = sum over a gate's rows of scale d_x p
+ *   g   = scale gate d_x post_weight,   d_post_weight = sum_i scale gate d_x yhat
+ *   d_y = rstd_y (g - yhat mean_d(g yhat)),   yhat = y rstd_y;   without post_norm d_y = g
+ *
+ *   grad_r, grad_n  [N, D] x_dtype; one of them may be NULL (zero).
+ *   rstd, post_rstd as written by the forward for the same inputs.
+ *   d_x, d_y [N, D] x_dtype, d_weight, d_post_weight [D], d_gate [gate_rows, D] w_dtype: each
+ *                may be NULL to skip it.
+ *   workspace >= flp_residual_rms_norm_backward_workspace_bytes(N, D, gate_rows), 16-byte
+ *                aligned: partial sums over rows (not needed, and not touched, when d_weight,
+ *                d_post_weight and a d_gate of fewer than N rows are all NULL).
+ *
+ * The sums over rows are fp32 in a fixed order and rounded once; N = 0 writes zeros to them.
+ */
+size_t flp_residual_rms_norm_backward_workspace_bytes(int64_t N, int64_t D, int64_t gate_rows);
+flp_status flp_residual_rms_norm_backward(
+    int64_t N, int64_t D, flp_dtype x_dtype, const void* grad_r, const void* grad_n, const void* x,
+    const void* y, flp_dtype w_dtype, const void* weight, int post_norm, const void* post_weight,
+    int64_t gate_rows, const void* gate, double scale, const float* rstd, const float* post_rstd,
+    void* d_x, void* d_y, void* d_weight, void* d_post_weight, void* d_gate, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/*
  * One AdamW step over many tensors at once, with decoupled weight decay:
  *
  *   g = grad * grad_scale
@@ -665,7 +745,8 @@ typedef enum flp_kernel_kind {
   FLP_K_LAYER_NORM = 12, /* flp_layer_norm_forward / flp_layer_norm_backward */
   FLP_K_LOSS = 13,      /* flp_cross_entropy_*: row losses, their sum, gradient factors */
   FLP_K_ADAMW = 14,     /* flp_adamw_step */
-  FLP_K_COUNT = 15
+  FLP_K_RMS_NORM = 15,  /* flp_rms_norm_*, flp_residual_rms_norm_* */
+  FLP_K_COUNT = 16
 } flp_kernel_kind;
 
 void flp_profile_enable(int on);

@@ -85,6 +85,15 @@ SIGNATURES = {
     "flp_layer_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
     "flp_layer_norm_backward": (_int, [_i64, _i64, _int, _vp, _vp, _int, _vp, _fp, _fp, _vp, _vp,
                                        _vp, _vp, _sz, _vp]),
+    "flp_rms_norm_forward": (_int, [_i64, _i64, _int, _vp, _int, _vp, _double, _vp, _fp, _vp]),
+    "flp_rms_norm_backward": (_int, [_i64, _i64, _int, _vp, _vp, _int, _vp, _fp, _vp, _vp, _vp, _sz,
+                                     _vp]),
+    "flp_residual_rms_norm_forward": (_int, [_i64, _i64, _int, _vp, _vp, _int, _vp, _int, _vp, _i64,
+                                             _vp, _double, _double, _vp, _vp, _fp, _fp, _vp]),
+    "flp_residual_rms_norm_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "flp_residual_rms_norm_backward": (_int, [_i64, _i64, _int, _vp, _vp, _vp, _vp, _int, _vp, _int,
+                                              _vp, _i64, _vp, _double, _fp, _fp, _vp, _vp, _vp, _vp,
+                                              _vp, _vp, _sz, _vp]),
     "flp_adamw_step": (_int, [_i64, _vp, _int, _i64, _vp, _double, _fp, _double, _double, _double,
                               _fp, _vp]),
     "flp_probe_scratch_bytes": (_sz, []),
@@ -363,6 +372,43 @@ def flp_layer_norm_backward(N, D, x_dtype, grad_out, x, w_dtype, weight, mean, r
                                               workspace_bytes, stream))
 
 
+def flp_rms_norm_forward(N, D, x_dtype, x, w_dtype, weight, eps, out, out_rstd, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_rms_norm_forward(N, D, x_dtype, x, w_dtype, weight, eps, out, out_rstd,
+                                           stream))
+
+
+def flp_rms_norm_backward(N, D, x_dtype, grad_out, x, w_dtype, weight, rstd, d_x, d_weight,
+                          workspace, workspace_bytes, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_rms_norm_backward(N, D, x_dtype, grad_out, x, w_dtype, weight, rstd, d_x,
+                                            d_weight, workspace, workspace_bytes, stream))
+
+
+def flp_residual_rms_norm_forward(N, D, x_dtype, x, y, w_dtype, weight, post_norm, post_weight,
+                                  gate_rows, gate, scale, eps, out_r, out_n, out_rstd,
+                                  out_post_rstd, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_residual_rms_norm_forward(
+        N, D, x_dtype, x, y, w_dtype, weight, post_norm, post_weight, gate_rows, gate, scale, eps,
+        out_r, out_n, out_rstd, out_post_rstd, stream))
+
+
+def flp_residual_rms_norm_backward_workspace_bytes(N: int, D: int, gate_rows: int) -> int:
+    return int(load().flp_residual_rms_norm_backward_workspace_bytes(N, D, gate_rows))
+
+
+def flp_residual_rms_norm_backward(N, D, x_dtype, grad_r, grad_n, x, y, w_dtype, weight, post_norm,
+                                   post_weight, gate_rows, gate, scale, rstd, post_rstd, d_x, d_y,
+                                   d_weight, d_post_weight, d_gate, workspace, workspace_bytes,
+                                   stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_residual_rms_norm_backward(
+        N, D, x_dtype, grad_r, grad_n, x, y, w_dtype, weight, post_norm, post_weight, gate_rows,
+        gate, scale, rstd, post_rstd, d_x, d_y, d_weight, d_post_weight, d_gate, workspace,
+        workspace_bytes, stream))
+
+
 class flp_adamw_tensor(ctypes.Structure):
     """One tensor of flp_adamw_step; the pointers are int addresses (0 or None for NULL)."""
     _fields_ = [("param", _vp), ("grad", _vp), ("exp_avg", _vp), ("exp_avg_sq", _vp),
@@ -399,7 +445,7 @@ def flp_probe_read(buffer: int, nbytes: int, scratch: int, scratch_bytes: int, s
 
 KERNEL_KINDS = ("forward", "merge", "dlogits", "transpose", "d_hidden", "d_weight", "d_bias",
                 "logits_forward", "logits_backward", "rows", "embedding", "dropout", "layer_norm",
-                "loss", "adamw")
+                "loss", "adamw", "rms_norm")
 
 
 def flp_profile_enable(on: bool) -> None:

@@ -1002,6 +1002,111 @@ flp_status flp_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p, co
   return FLP_OK;
 }
 
+// ---- root mean square norms ----
+
+flp_status flp_rms_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                flp_dtype w_dtype, const void* weight, double eps, void* out,
+                                float* out_rstd, void* stream) {
+  return flp_residual_rms_norm_forward(N, D, x_dtype, x, nullptr, w_dtype, weight, 0, nullptr, 0,
+                                       nullptr, 1.0, eps, nullptr, out, out_rstd, nullptr, stream);
+}
+
+flp_status flp_rms_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, const void* grad_out,
+                                 const void* x, flp_dtype w_dtype, const void* weight,
+                                 const float* rstd, void* d_x, void* d_weight, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  return flp_residual_rms_norm_backward(N, D, x_dtype, nullptr, grad_out, x, nullptr, w_dtype,
+                                        weight, 0, nullptr, 0, nullptr, 1.0, rstd, nullptr, d_x,
+                                        nullptr, d_weight, nullptr, nullptr, workspace,
+                                        workspace_bytes, stream);
+}
+
+flp_status flp_residual_rms_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                         const void* y, flp_dtype w_dtype, const void* weight,
+                                         int post_norm, const void* post_weight,
+                                         int64_t gate_rows, const void* gate, double scale,
+                                         double eps, void* out_r, void* out_n, float* out_rstd,
+                                         float* out_post_rstd, void* stream) {
+  const bool post = post_norm != 0;
+  flp_status st = validate_rms_forward(N, D, x_dtype, x, y, w_dtype, weight, post, post_weight,
+                                       gate_rows, gate, scale, eps, out_r, out_n, out_rstd,
+                                       out_post_rstd);
+  if (st != FLP_OK || N == 0) return st;
+  if ((st = check_device()) != FLP_OK) return st;
+  RmsFwdArgs a{};
+  a.N = N;
+  a.D = D;
+  a.x = x;
+  a.y = y;
+  a.weight = weight;
+  a.post = post;
+  a.post_weight = post_weight;
+  a.gate = gate;
+  a.gates = gate_rows > 1;
+  a.rows_per_gate = gate_rows > 0 ? N / gate_rows : N;
+  a.scale = float(scale);
+  a.eps = float(eps);
+  a.out_r = out_r;
+  a.out_n = out_n;
+  a.rstd = out_rstd;
+  a.post_rstd = out_post_rstd;
+  if (launch_rms_forward(x_dtype, w_dtype, a, static_cast<hipStream_t>(stream)) != hipSuccess)
+    return FLP_HIP_ERROR;
+  return FLP_OK;
+}
+
+size_t flp_residual_rms_norm_backward_workspace_bytes(int64_t N, int64_t D, int64_t gate_rows) {
+  if (N < 1 || D < 1 || gate_rows < 0) return 0;
+  return rms_layout(N, D, gate_rows).total;
+}
+
+flp_status flp_residual_rms_norm_backward(
+    int64_t N, int64_t D, flp_dtype x_dtype, const void* grad_r, const void* grad_n, const void* x,
+    const void* y, flp_dtype w_dtype, const void* weight, int post_norm, const void* post_weight,
+    int64_t gate_rows, const void* gate, double scale, const float* rstd, const float* post_rstd,
+    void* d_x, void* d_y, void* d_weight, void* d_post_weight, void* d_gate, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  const bool post = post_norm != 0;
+  flp_status st = validate_rms_backward(N, D, x_dtype, grad_r, grad_n, x, y, w_dtype, weight, post,
+                                        post_weight, gate_rows, gate, scale, rstd, post_rstd, d_x,
+                                        d_y, d_weight, d_post_weight, d_gate, workspace,
+                                        workspace_bytes);
+  if (st != FLP_OK) return st;
+  const RmsLayout L = rms_layout(N, D, gate_rows);
+  const bool sums = d_weight || d_post_weight || (d_gate && !L.gates);
+  if (!sums && (N == 0 || (!d_x && !d_y && !d_gate))) return FLP_OK;
+  if ((st = check_device()) != FLP_OK) return st;
+  RmsBwdArgs a{};
+  a.N = N;
+  a.D = D;
+  a.grad_r = grad_r;
+  a.grad_n = grad_n;
+  a.x = x;
+  a.y = y;
+  a.weight = weight;
+  a.post = post;
+  a.post_weight = post_weight;
+  a.gate = gate;
+  a.gates = L.gates;
+  a.gate_rows = gate_rows;
+  a.rows_per_gate = L.rows_per_gate;
+  a.scale = float(scale);
+  a.rstd = rstd;
+  a.post_rstd = post_rstd;
+  a.d_x = d_x;
+  a.d_y = d_y;
+  a.d_weight = d_weight;
+  a.d_post_weight = d_post_weight;
+  a.d_gate = d_gate;
+  a.slabs = N > 0 ? L.slabs : 0;  // no rows: the fold writes zeros
+  a.slabs_per_gate = N > 0 ? L.slabs_per_gate : 0;
+  a.slab_rows = L.slab_rows;
+  a.part = sums ? static_cast<float*>(workspace) : nullptr;
+  if (launch_rms_backward(x_dtype, w_dtype, a, static_cast<hipStream_t>(stream)) != hipSuccess)
+    return FLP_HIP_ERROR;
+  return FLP_OK;
+}
+
 // ---- AdamW ----
 
 flp_status flp_adamw_step(int64_t n_tensors, const flp_adamw_tensor* tensors, int state_bits,

@@ -258,6 +258,52 @@ hipError_t launch_loss_count(int64_t N, int64_t V, const void* targets, bool t64
 // x *= *factor in place (n elements); nothing is touched when the factor is 1.
 hipError_t launch_scale(flp_dtype x_dtype, int64_t n, void* x, const float* factor, hipStream_t s);
 
+// Root mean square norms around a block (flp_rms.hip).
+struct RmsFwdArgs {
+  int64_t N, D;
+  const void* x;             // [N][D]
+  const void* y;             // [N][D] or null
+  const void* weight;        // [D] or null
+  bool post;                 // y is normalised first
+  const void* post_weight;   // [D] or null
+  const void* gate;          // [N / rows_per_gate][D] or null
+  bool gates;                // more than one gate row
+  int64_t rows_per_gate;
+  bool wide;                 // the parameters are fp32 (set by the launcher)
+  float scale, eps;
+  void* out_r;               // [N][D], with y
+  void* out_n;               // [N][D]
+  float* rstd;               // [N] or null
+  float* post_rstd;          // [N] or null
+};
+struct RmsBwdArgs {
+  int64_t N, D;
+  const void* grad_r;        // [N][D] or null
+  const void* grad_n;        // [N][D] or null
+  const void* x;             // [N][D]
+  const void* y;             // [N][D] or null
+  const void* weight;        // [D] or null
+  bool post;
+  const void* post_weight;   // [D] or null
+  const void* gate;          // [gate_rows][D] or null
+  bool gates;                // a gate row for each row
+  int64_t gate_rows;         // 0 without a gate
+  int64_t rows_per_gate;     // N with one gate row, none, or one for each row
+  bool wide;                 // the parameters are fp32 (set by the launcher)
+  float scale;
+  const float* rstd;         // [N]
+  const float* post_rstd;    // [N], with post
+  void* d_x;                 // [N][D] or null
+  void* d_y;                 // [N][D] or null
+  void* d_weight;            // [D] or null
+  void* d_post_weight;       // [D] or null
+  void* d_gate;              // [gate_rows][D] or null
+  int64_t slabs, slabs_per_gate, slab_rows;
+  float* part;               // [slabs][2][D], or null for no sums over rows
+};
+hipError_t launch_rms_forward(flp_dtype x, flp_dtype w, const RmsFwdArgs& a, hipStream_t s);
+hipError_t launch_rms_backward(flp_dtype x, flp_dtype w, const RmsBwdArgs& a, hipStream_t s);
+
 // AdamW (flp_adamw.hip).
 struct AdamTensor {
   void* param;

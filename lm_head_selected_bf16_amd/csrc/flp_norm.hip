@@ -27,18 +27,11 @@
 #include <atomic>
 #include <type_traits>
 
-#include "flp_chunk.h"
 #include "flp_launch.h"
+#include "flp_row.h"
 
 namespace flp {
 namespace {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-template <class T>
-__device__ __forceinline__ float to_f32(T v) {
-  return float(v);
-}
 
 // Mean and rstd of a row from a first mean m and the means u of x - m and q of (x - m)^2:
 // x - m is exact where the offset is large, so m + u is the mean up to half a step, and a
@@ -57,40 +50,6 @@ struct Centre {
 // A team of TEAM threads (one wave, or four) owns a row; thread t holds the chunks of
 // eight elements t, t + TEAM, ... (at most NCH).  A row is read from memory once, with
 // 16-byte loads that all stay in flight, and both its sums run over the registers.
-// Eight parameters as fp32 (`wide`: they are stored as fp32, else in T).
-template <class T>
-__device__ __forceinline__ void load_params(const void* base, bool wide, int64_t d, int64_t n,
-                                            float (&x)[kChunk]) {
-  if (sizeof(T) == 4 || wide) {
-    Chunk<float> c;
-    c.load(static_cast<const float*>(base) + d, n);
-#pragma unroll
-    for (int k = 0; k < kChunk; ++k) x[k] = c.v[k];
-  } else {
-    Chunk<T> c;
-    c.load(static_cast<const T*>(base) + d, n);
-#pragma unroll
-    for (int k = 0; k < kChunk; ++k) x[k] = to_f32(T(c.v[k]));
-  }
-}
-
-// Sum over the wave, the same bits in every lane: quad permutations, the mirrors of 8
-// and 16 lanes (each then meets the other half's value), and the 16- and 32-lane swaps,
-// all of them VALU moves.
-__device__ __forceinline__ float wave_sum(float x) {
-  auto dpp = [](float v, auto ctrl) {
-    return __int_as_float(
-        __builtin_amdgcn_mov_dpp(__float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true));
-  };
-  x += dpp(x, std::integral_constant<int, 0xB1>{});
-  x += dpp(x, std::integral_constant<int, 0x4E>{});
-  x += dpp(x, std::integral_constant<int, 0x141>{});
-  x += dpp(x, std::integral_constant<int, 0x140>{});
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
 
 // Sum over the team, the same bits in every thread.  A team of four waves meets in LDS
 // (`red`: a float per wave of the workgroup, another slot on every call in turn).
@@ -121,19 +80,6 @@ __device__ __forceinline__ void team_sum2(float& x, float& y, float (&red)[3][8]
 constexpr int kTeamThreads = 512;
 // Workgroups of a forward launch: two per compute unit (256 and 1024 measured the same).
 constexpr int64_t kFwdGroups = 512;
-
-// A row's chunks of one thread.
-template <class T, int TEAM, int NCH>
-struct Row {
-  Chunk<T> c[NCH];
-  __device__ __forceinline__ void load(const T* row, int64_t D, int t, bool live) {
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int64_t d = int64_t(k * TEAM + t) * kChunk;
-      c[k].load(row + d, live ? D - d : 0);
-    }
-  }
-};
 
 // A [D] parameter in LDS as fp32, in two planes (the chunks' first and second four
 // elements) so that a wave's 16-byte reads are contiguous; `value` where it is absent.

@@ -868,6 +868,102 @@ flp_status validate_dropout(int64_t n, flp_dtype x_dtype, const void* x, double 
   return any_alias(outs, 1, ins, 2) ? FLP_INVALID_ARGUMENT : FLP_OK;
 }
 
+RmsLayout rms_layout(int64_t N, int64_t D, int64_t gate_rows) {
+  RmsLayout L;
+  L.gates = gate_rows > 1 && gate_rows == N;
+  const int64_t parts = gate_rows > 1 && !L.gates ? gate_rows : 1;
+  L.rows_per_gate = N / parts;
+  L.slab_rows = std::min(std::max(kNormMinRows, ceil_div(N, kNormSlabs)),
+                         std::max<int64_t>(L.rows_per_gate, 1));
+  L.slabs_per_gate = ceil_div(L.rows_per_gate, L.slab_rows);
+  L.slabs = L.slabs_per_gate * parts;
+  L.total = align_up(size_t(L.slabs) * 2 * size_t(D) * 4);
+  return L;
+}
+
+namespace {
+
+flp_status check_rms(int64_t N, int64_t D, flp_dtype x_dtype, flp_dtype w_dtype, const void* y,
+                     bool post, const void* post_weight, int64_t gate_rows, const void* gate,
+                     double scale) {
+  const flp_status st = check_norm_dims(N, D, x_dtype, w_dtype);
+  if (st != FLP_OK) return st;
+  if (gate_rows < 0 || !(std::fabs(scale) <= double(std::numeric_limits<float>::max())))
+    return FLP_INVALID_ARGUMENT;
+  if (D > kRmsMaxWidth) return FLP_UNSUPPORTED_SHAPE;
+  // a launch of a workgroup per slab, and of one per sixteen columns of a gate, stays in range
+  if (N >= (int64_t(1) << 31)) return FLP_UNSUPPORTED_SHAPE;
+  if (N > 0) {
+    if (gate_rows > 0 && N % gate_rows != 0) return FLP_INVALID_ARGUMENT;
+    if ((gate != nullptr) != (gate_rows > 0)) return FLP_INVALID_ARGUMENT;
+    if (!y && (post || gate)) return FLP_INVALID_ARGUMENT;
+  }
+  return post_weight && !post ? FLP_INVALID_ARGUMENT : FLP_OK;
+}
+
+}  // namespace
+
+flp_status validate_rms_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                const void* y, flp_dtype w_dtype, const void* weight, bool post,
+                                const void* post_weight, int64_t gate_rows, const void* gate,
+                                double scale, double eps, const void* out_r, const void* out_n,
+                                const float* rstd, const float* post_rstd) {
+  flp_status st = check_rms(N, D, x_dtype, w_dtype, y, post, post_weight, gate_rows, gate, scale);
+  if (st != FLP_OK) return st;
+  if (!(eps >= 0.0) || eps > double(std::numeric_limits<float>::max())) return FLP_INVALID_ARGUMENT;
+  if (N == 0) return FLP_OK;
+  if (!x || !out_n || (y != nullptr) != (out_r != nullptr)) return FLP_INVALID_ARGUMENT;
+  const size_t xs = dtype_size(x_dtype), ws = dtype_size(w_dtype);
+  if (!aligned(x, xs) || !aligned(y, xs) || !aligned(out_r, xs) || !aligned(out_n, xs) ||
+      !aligned(weight, ws) || !aligned(post_weight, ws) || !aligned(gate, ws) ||
+      !aligned(rstd, 4) || !aligned(post_rstd, 4))
+    return FLP_MISALIGNED;
+  const size_t rows = size_t(N) * D * xs;
+  const Span ins[] = {span(x, rows), span(y, rows), span(weight, size_t(D) * ws),
+                      span(post_weight, size_t(D) * ws), span(gate, size_t(gate_rows) * D * ws)};
+  const Span outs[] = {span(out_r, rows), span(out_n, rows), span(rstd, size_t(N) * 4),
+                       span(post_rstd, size_t(N) * 4)};
+  return any_alias(outs, 4, ins, 5) ? FLP_INVALID_ARGUMENT : FLP_OK;
+}
+
+flp_status validate_rms_backward(int64_t N, int64_t D, flp_dtype x_dtype, const void* grad_r,
+                                 const void* grad_n, const void* x, const void* y,
+                                 flp_dtype w_dtype, const void* weight, bool post,
+                                 const void* post_weight, int64_t gate_rows, const void* gate,
+                                 double scale, const float* rstd, const float* post_rstd,
+                                 const void* d_x, const void* d_y, const void* d_weight,
+                                 const void* d_post_weight, const void* d_gate,
+                                 const void* workspace, size_t workspace_bytes) {
+  flp_status st = check_rms(N, D, x_dtype, w_dtype, y, post, post_weight, gate_rows, gate, scale);
+  if (st != FLP_OK) return st;
+  const size_t xs = dtype_size(x_dtype), ws = dtype_size(w_dtype);
+  const RmsLayout L = rms_layout(N, D, gate_rows);
+  const bool sums = d_weight || d_post_weight || (d_gate && !L.gates);
+  if (!d_x && !d_y && !sums && !d_gate) return FLP_OK;
+  if (N > 0 && ((!grad_r && !grad_n) || !x || !rstd || (post && !post_rstd) || (sums && !workspace)))
+    return FLP_INVALID_ARGUMENT;
+  if (N > 0 && ((!y && (d_y || grad_r)) || (!gate && d_gate) || (!post && d_post_weight)))
+    return FLP_INVALID_ARGUMENT;
+  if (!aligned(grad_r, xs) || !aligned(grad_n, xs) || !aligned(x, xs) || !aligned(y, xs) ||
+      !aligned(d_x, xs) || !aligned(d_y, xs) || !aligned(weight, ws) || !aligned(post_weight, ws) ||
+      !aligned(gate, ws) || !aligned(d_weight, ws) || !aligned(d_post_weight, ws) ||
+      !aligned(d_gate, ws) || !aligned(rstd, 4) || !aligned(post_rstd, 4) || !aligned(workspace, 16))
+    return FLP_MISALIGNED;
+  const size_t rows = size_t(N) * D * xs, one = size_t(D) * ws, gates = size_t(gate_rows) * one;
+  const Span ins[] = {span(grad_r, rows),      span(grad_n, rows),
+                      span(x, rows),           span(y, rows),
+                      span(weight, one),       span(post_weight, one),
+                      span(gate, gates),       span(rstd, size_t(N) * 4),
+                      span(post_rstd, size_t(N) * 4)};
+  const Span outs[] = {span(d_x, rows),          span(d_y, rows),
+                       span(d_weight, one),      span(d_post_weight, one),
+                       span(d_gate, gates),      span(sums && N > 0 ? workspace : nullptr,
+                                                      workspace_bytes)};
+  if (any_alias(outs, 6, ins, 9)) return FLP_INVALID_ARGUMENT;
+  if (sums && N > 0 && workspace_bytes < L.total) return FLP_WORKSPACE_TOO_SMALL;
+  return FLP_OK;
+}
+
 namespace {
 
 // Whether an output span overlaps an input or another output, by a sweep over all of them (a

@@ -153,6 +153,15 @@ NormLayout norm_layout(int64_t N, int64_t D);
 // ---- dropout: elements whose 16 random bits are below this are dropped (65536: all) ----
 inline uint32_t dropout_threshold(double p) { return uint32_t(p * 65536.0 + 0.5); }
 
+// ---- root mean square norms backward: slabs of rows, within the rows of one gate ----
+constexpr int64_t kRmsMaxWidth = 16384;  // elements that the eight waves of a team hold
+struct RmsLayout {
+  bool gates = false;        // a gate row for each row: the slabs need not respect them
+  int64_t rows_per_gate = 0, slab_rows = 0, slabs_per_gate = 0, slabs = 0;
+  size_t total = 0;          // fp32 [slabs][2][D]
+};
+RmsLayout rms_layout(int64_t N, int64_t D, int64_t gate_rows);
+
 // ---- AdamW: elements that share a scale of the 8-bit states ----
 constexpr int64_t kAdamBlock = 256;
 
@@ -270,6 +279,20 @@ flp_status validate_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype,
                                         const void* workspace, size_t workspace_bytes);
 flp_status validate_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p,
                             const int64_t* rng, const void* out);
+// Root mean square norms; y, post_weight, gate and out_r belong to the residual form.
+flp_status validate_rms_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
+                                const void* y, flp_dtype w_dtype, const void* weight, bool post,
+                                const void* post_weight, int64_t gate_rows, const void* gate,
+                                double scale, double eps, const void* out_r, const void* out_n,
+                                const float* rstd, const float* post_rstd);
+flp_status validate_rms_backward(int64_t N, int64_t D, flp_dtype x_dtype, const void* grad_r,
+                                 const void* grad_n, const void* x, const void* y,
+                                 flp_dtype w_dtype, const void* weight, bool post,
+                                 const void* post_weight, int64_t gate_rows, const void* gate,
+                                 double scale, const float* rstd, const float* post_rstd,
+                                 const void* d_x, const void* d_y, const void* d_weight,
+                                 const void* d_post_weight, const void* d_gate,
+                                 const void* workspace, size_t workspace_bytes);
 // Reads the host array `tensors`, none of the pointers in it.
 flp_status validate_adamw_step(int64_t n_tensors, const flp_adamw_tensor* tensors, int state_bits,
                                int64_t step, const int64_t* step_on_device, double lr,

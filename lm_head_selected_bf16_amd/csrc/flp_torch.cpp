@@ -40,6 +40,9 @@ struct Api {
   decltype(&::flp_cross_entropy_backward) loss_backward;
   decltype(&::flp_cross_entropy_backward_workspace_bytes) loss_backward_bytes;
   decltype(&::flp_adamw_step) adamw_step;
+  decltype(&::flp_residual_rms_norm_forward) rms_forward;
+  decltype(&::flp_residual_rms_norm_backward) rms_backward;
+  decltype(&::flp_residual_rms_norm_backward_workspace_bytes) rms_backward_bytes;
 };
 Api api;
 
@@ -59,6 +62,9 @@ void bind(const std::map<std::string, uintptr_t>& at) {
   take(api.loss_backward, "flp_cross_entropy_backward");
   take(api.loss_backward_bytes, "flp_cross_entropy_backward_workspace_bytes");
   take(api.adamw_step, "flp_adamw_step");
+  take(api.rms_forward, "flp_residual_rms_norm_forward");
+  take(api.rms_backward, "flp_residual_rms_norm_backward");
+  take(api.rms_backward_bytes, "flp_residual_rms_norm_backward_workspace_bytes");
 }
 
 // A non-OK status: FlpError in Python, as a Python exception from here on.  A backward runs in
@@ -319,6 +325,94 @@ struct CrossEntropyNode : Function<CrossEntropyNode> {
   }
 };
 
+// The norms around a block: {r, n}, or {n} without y.
+struct RmsNormNode : Function<RmsNormNode> {
+  static variable_list forward(AutogradContext* ctx, const at::Tensor& x, const OptTensor& y,
+                               const OptTensor& weight, const OptTensor& post_weight,
+                               const OptTensor& gate, bool post, double scale, double eps,
+                               int64_t stream) {
+    const int64_t D = x.size(-1), N = x.numel() / D;
+    const at::Tensor b = y.value_or(at::Tensor()), w = weight.value_or(at::Tensor()),
+                     pw = post_weight.value_or(at::Tensor()), g = gate.value_or(at::Tensor());
+    const at::Tensor& typed = w.defined() ? w : pw.defined() ? pw : g.defined() ? g : x;
+    const int64_t gates = g.defined() ? g.numel() / D : 0;
+    at::Tensor r, n = at::empty_like(x);
+    if (b.defined()) r = at::empty_like(x);
+    const at::Tensor stats = at::empty({post ? 2 : 1, N}, x.options().dtype(at::kFloat));
+    check("flp_residual_rms_norm_forward",
+          api.rms_forward(N, D, code(x), ptr(x), ptr(b), code(typed), ptr(w), post, ptr(pw), gates,
+                          ptr(g), scale, eps, ptr(r), ptr(n), fptr(stats),
+                          post ? fptr(stats) + N : nullptr, reinterpret_cast<void*>(stream)));
+    ctx->save_for_backward({x, b, w, pw, g, stats});
+    ctx->saved_data["type"] = int64_t(typed.scalar_type());
+    ctx->saved_data["post"] = post;
+    ctx->saved_data["gates"] = gates;
+    ctx->saved_data["scale"] = scale;
+    ctx->saved_data["stream"] = stream;
+    ctx->set_materialize_grads(false);
+    if (b.defined()) return {r, n};
+    return {n};
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list saved = ctx->get_saved_variables();
+    const at::Tensor &x = saved[0], &y = saved[1], &w = saved[2], &pw = saved[3], &gate = saved[4],
+                     &stats = saved[5];
+    const auto type = at::ScalarType(ctx->saved_data["type"].toInt());
+    const bool post = ctx->saved_data["post"].toBool();
+    const int64_t gates = ctx->saved_data["gates"].toInt(), N = stats.size(1);
+    variable_list out(9);
+    const at::Tensor gr = y.defined() ? grads[0] : at::Tensor();
+    const at::Tensor gn = y.defined() ? grads[1] : grads[0];
+    if (!gr.defined() && !gn.defined()) return out;
+    const at::Tensor& up = gn.defined() ? gn : gr;
+    auto rows = [&](const at::Tensor& t) {
+      return !t.defined() || (dense(t) && t.sizes() == up.sizes() && t.device() == up.device() &&
+                              t.scalar_type() == up.scalar_type());
+    };
+    same(rows(x) && rows(y) && x.dim() >= 1 && x.numel() == N * x.size(-1));
+    const int64_t D = x.size(-1);
+    auto param = [&](const at::Tensor& t, int64_t n) {
+      return !t.defined() || (dense(t) && t.numel() == n * D && t.scalar_type() == type &&
+                              t.device() == x.device());
+    };
+    same(param(w, 1) && param(pw, 1) && param(gate, gates));
+    const at::Tensor cr = gr.defined() ? gr.contiguous() : gr;
+    const at::Tensor cn = gn.defined() ? gn.contiguous() : gn;
+    // the inputs that are tensors have edges, in order
+    size_t edge = 0;
+    auto needs = [&](const at::Tensor& t) {
+      return t.defined() && ctx->needs_input_grad(edge++);
+    };
+    at::Tensor dx, dy, dw, dpw, dg, ws;
+    if (needs(x)) dx = at::empty_like(x);
+    if (needs(y)) dy = at::empty_like(y);
+    if (needs(w)) dw = at::empty_like(w);
+    if (needs(pw)) dpw = at::empty_like(pw);
+    if (needs(gate)) dg = at::empty_like(gate);
+    size_t size = 0;
+    if (dw.defined() || dpw.defined() || dg.defined()) {
+      ws = bytes(api.rms_backward_bytes(N, D, gates), x);
+      size = size_t(ws.numel());
+    }
+    const flp_dtype wd = type == at::kBFloat16 ? FLP_BF16 : type == at::kHalf ? FLP_F16 : FLP_F32;
+    check("flp_residual_rms_norm_backward",
+          api.rms_backward(N, D, code(x), ptr(cr), ptr(cn), ptr(x), ptr(y), wd, ptr(w), post,
+                           ptr(pw), gates, ptr(gate), ctx->saved_data["scale"].toDouble(),
+                           fptr(stats), post ? fptr(stats) + N : nullptr, ptr(dx), ptr(dy),
+                           ptr(dw), ptr(dpw), ptr(dg), ptr(ws), size,
+                           reinterpret_cast<void*>(ctx->saved_data["stream"].toInt())));
+    auto once = [&](const at::Tensor& t) {
+      return first_order(t, gr, gn, x, y, w, pw, gate);
+    };
+    out[0] = once(dx);
+    out[1] = once(dy);
+    out[2] = once(dw);
+    out[3] = once(dpw);
+    out[4] = once(dg);
+    return out;
+  }
+};
+
 // ---- AdamW ----
 //
 // No autograd node, but lists of tensors: with its arguments checked in Python, a step over 300
@@ -447,6 +541,11 @@ PYBIND11_MODULE(_flp_torch, m) {
   m.def("layer_norm", [](const at::Tensor& x, const OptTensor& weight, const OptTensor& bias,
                          double eps, int64_t stream) {
     return LayerNormNode::apply(x, weight, bias, eps, stream);
+  });
+  m.def("rms_norm", [](const at::Tensor& x, const OptTensor& y, const OptTensor& weight,
+                       const OptTensor& post_weight, const OptTensor& gate, bool post,
+                       double scale, double eps, int64_t stream) {
+    return RmsNormNode::apply(x, y, weight, post_weight, gate, post, scale, eps, stream);
   });
   m.def("adamw_step", &adamw_step);
   m.def("cross_entropy",

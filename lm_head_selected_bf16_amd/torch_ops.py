@@ -981,6 +981,188 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
         return _nodes().layer_norm(x, weight, bias, eps, _stream(dev))
 
 
+# ---- root mean square norms around a block ------------------------------------------------------
+
+def _prepare_rms(x, y, weight, post_weight, gate, post_norm):
+    """(rows, width, parameters' dtype, gate rows)."""
+    if x.dtype not in _X_DTYPES:
+        raise TypeError("x must be bfloat16, float16 or float32")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have a last dimension of at least one element")
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous GPU tensor")
+    D = int(x.shape[-1])
+    if y is not None and (y.dtype != x.dtype or y.shape != x.shape or not y.is_contiguous()
+                          or y.device != x.device):
+        raise ValueError("y must be contiguous with the dtype, shape and device of x")
+    wd = None
+    for name, t in (("weight", weight), ("post_weight", post_weight), ("gate", gate)):
+        if t is None:
+            continue
+        if t.dtype not in (x.dtype, torch.float32):
+            raise TypeError(f"{name} must have the dtype of x or float32")
+        if wd is not None and t.dtype != wd:
+            raise TypeError("weight, post_weight and gate must have the same dtype")
+        if not t.is_contiguous() or t.device != x.device:
+            raise ValueError(f"{name} must be contiguous and on the device of x")
+        if name != "gate" and tuple(t.shape) != (D,):
+            raise ValueError(f"{name} must be [D]")
+        wd = t.dtype
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight goes with post_norm")
+    N = x.numel() // D
+    return N, D, x.dtype if wd is None else wd, _gate_rows(x, gate, N, D)
+
+
+def _gate_rows(x, gate, N, D) -> int:
+    """How many gate rows there are, each for as many consecutive rows of x."""
+    if gate is None:
+        return 0
+    lead = list(gate.shape[:-1])
+    if gate.dim() < 1 or gate.shape[-1] != D:
+        raise ValueError("gate must be [.., D]")
+    while lead and lead[-1] == 1:
+        lead.pop()
+    G = math.prod(lead)
+    # leading dimensions of x, or so many groups of the rows of a 2-D one
+    ok = tuple(lead) == tuple(x.shape[:len(lead)]) and len(lead) < x.dim()
+    if not ok and not (x.dim() == 2 and len(lead) == 1 and G > 0 and N % G == 0):
+        raise ValueError("gate must be [D], begin with the leading sizes of x ([B, D] or [B, 1, D] "
+                         "for x [B, S, D]), or be [G, D] for x [N, D] with N a multiple of G")
+    return G
+
+
+def rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     return_stats: bool = True):
+    """(out, rstd) of the root mean square norm over the last dimension through
+    flp_rms_norm_forward; rstd is float32 of the leading shape, or None."""
+    N, D, wd, _ = _prepare_rms(x, None, weight, None, None, False)
+    dev = x.device
+    with _on(dev):
+        out = torch.empty_like(x)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if return_stats else None
+        st = _abi.flp_rms_norm_forward(N, D, _X_DTYPES[x.dtype], x.data_ptr(), _X_DTYPES[wd],
+                                       _ptr(weight), float(eps), out.data_ptr(), _ptr(rstd),
+                                       _stream(dev))
+    _check("flp_rms_norm_forward", st)
+    return out, rstd
+
+
+def rms_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor,
+                      weight: Optional[torch.Tensor] = None, need_input: bool = True,
+                      need_weight: bool = True):
+    """(d_x, d_weight) through flp_rms_norm_backward; unrequested ones are None, d_weight has the
+    dtype of weight (of x without one)."""
+    dx, _, dw, _, _ = residual_rms_norm_backward(None, grad_out, x, None, rstd, None, weight,
+                                                 need_input=need_input, need_weight=need_weight)
+    return dx, dw
+
+
+def rms_norm(x, weight=None, eps=1e-6):
+    """x / sqrt(mean(x^2) + eps) * weight over the last dimension, differentiable in x and weight;
+    weight [D] in the dtype of x or float32."""
+    if not _wants_grad(x, weight):
+        return rms_norm_forward(x, weight, eps, return_stats=False)[0]
+    _prepare_rms(x, None, weight, None, None, False)
+    dev = x.device
+    with _on(dev):
+        return _nodes().rms_norm(x, None, weight, None, None, False, 1.0, eps, _stream(dev))[0]
+
+
+def residual_rms_norm_forward(x: torch.Tensor, y: torch.Tensor,
+                              weight: Optional[torch.Tensor] = None,
+                              post_weight: Optional[torch.Tensor] = None,
+                              gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                              eps: float = 1e-6, post_norm: Optional[bool] = None,
+                              return_stats: bool = True):
+    """(r, n, rstd, post_rstd) of residual_rms_norm through flp_residual_rms_norm_forward; the
+    statistics are float32 of the leading shape, or None (post_rstd without post_norm)."""
+    post = post_weight is not None if post_norm is None else bool(post_norm)
+    N, D, wd, G = _prepare_rms(x, y, weight, post_weight, gate, post)
+    dev = x.device
+    with _on(dev):
+        r, n = torch.empty_like(x), torch.empty_like(x)
+        rstd = post_rstd = None
+        if return_stats:
+            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            post_rstd = torch.empty_like(rstd) if post else None
+        st = _abi.flp_residual_rms_norm_forward(
+            N, D, _X_DTYPES[x.dtype], x.data_ptr(), y.data_ptr(), _X_DTYPES[wd], _ptr(weight),
+            int(post), _ptr(post_weight), G, _ptr(gate), float(scale), float(eps), r.data_ptr(),
+            n.data_ptr(), _ptr(rstd), _ptr(post_rstd), _stream(dev))
+    _check("flp_residual_rms_norm_forward", st)
+    return r, n, rstd, post_rstd
+
+
+def residual_rms_norm_backward(grad_r: Optional[torch.Tensor], grad_n: Optional[torch.Tensor],
+                               x: torch.Tensor, y: Optional[torch.Tensor], rstd: torch.Tensor,
+                               post_rstd: Optional[torch.Tensor] = None,
+                               weight: Optional[torch.Tensor] = None,
+                               post_weight: Optional[torch.Tensor] = None,
+                               gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                               post_norm: Optional[bool] = None, need_input: bool = True,
+                               need_block: bool = True, need_weight: bool = True,
+                               need_post_weight: Optional[bool] = None,
+                               need_gate: Optional[bool] = None):
+    """(d_x, d_y, d_weight, d_post_weight, d_gate) through flp_residual_rms_norm_backward;
+    unrequested ones are None.  grad_r or grad_n may be None (zero)."""
+    post = post_weight is not None if post_norm is None else bool(post_norm)
+    N, D, wd, G = _prepare_rms(x, y, weight, post_weight, gate, post)
+    need_post_weight = post if need_post_weight is None else need_post_weight and post
+    need_gate = gate is not None if need_gate is None else need_gate and gate is not None
+    for name, t in (("grad_r", grad_r), ("grad_n", grad_n)):
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape or not t.is_contiguous()
+                              or t.device != x.device):
+            raise ValueError(f"{name} must be contiguous with the dtype, shape and device of x")
+    for name, t in (("rstd", rstd), ("post_rstd", post_rstd)):
+        if t is None and (name == "rstd" or post):
+            raise ValueError(f"{name} is needed")
+        if t is not None and (t.dtype != torch.float32 or t.shape != x.shape[:-1]
+                              or not t.is_contiguous() or t.device != x.device):
+            raise ValueError(f"{name} must be contiguous float32 with the leading shape of x")
+    dev = x.device
+    with _on(dev):
+        dx = torch.empty_like(x) if need_input else None
+        dy = torch.empty_like(x) if need_block and y is not None else None
+        dw = torch.empty(D, dtype=wd, device=dev) if need_weight else None
+        dpw = torch.empty(D, dtype=wd, device=dev) if need_post_weight else None
+        dg = torch.empty_like(gate) if need_gate else None
+        ws, size = None, 0
+        if need_weight or need_post_weight or need_gate:
+            size = max(_abi.flp_residual_rms_norm_backward_workspace_bytes(N, D, G), 16)
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        st = _abi.flp_residual_rms_norm_backward(
+            N, D, _X_DTYPES[x.dtype], _ptr(grad_r), _ptr(grad_n), x.data_ptr(), _ptr(y),
+            _X_DTYPES[wd], _ptr(weight), int(post), _ptr(post_weight), G, _ptr(gate), float(scale),
+            rstd.data_ptr(), _ptr(post_rstd), _ptr(dx), _ptr(dy), _ptr(dw), _ptr(dpw), _ptr(dg),
+            _ptr(ws), size, _stream(dev))
+    _check("flp_residual_rms_norm_backward", st)
+    return dx, dy, dw, dpw, dg
+
+
+def residual_rms_norm(x, y, weight=None, post_weight=None, gate=None, scale=1.0, eps=1e-6,
+                      post_norm=None):
+    """(r, n): the residual stream x with the block's output y taken in, and its norm for the next
+    block or the head, in one pass:
+
+        p = rms_norm(y, post_weight) where post_norm (by default where post_weight is given), or y
+        r = x + scale * gate * p,    n = rms_norm(r, weight)
+
+    differentiable in x, y, weight, post_weight and gate.  weight and post_weight [D], gate [D],
+    or with a row for each leading index of x ([B, D] or [B, 1, D] for x [B, S, D]; x's own shape
+    for a gate per element), or [G, D] for x [N, D], each row for N / G rows in turn; all of them
+    in the dtype of x or all in float32."""
+    if not _wants_grad(x, y, weight, post_weight, gate):
+        return residual_rms_norm_forward(x, y, weight, post_weight, gate, scale, eps, post_norm,
+                                         return_stats=False)[:2]
+    post = post_weight is not None if post_norm is None else bool(post_norm)
+    _prepare_rms(x, y, weight, post_weight, gate, post)
+    dev = x.device
+    with _on(dev):
+        return tuple(_nodes().rms_norm(x, y, weight, post_weight, gate, post, float(scale), eps,
+                                       _stream(dev)))
+
+
 # ---- AdamW --------------------------------------------------------------------------------------
 
 class AdamWState(NamedTuple):

@@ -106,3 +106,117 @@ def test_adamw_python_checks():
     assert [t.numel() for t in s.exp_avg_scale] == [2, 1]
     assert s.master[0] is None and s.master[1].dtype == torch.float32
     assert s.exp_avg_sq[0].dtype == torch.float8_e4m3fn
+
+
+# ---- root mean square norms --------------------------------------------------------------------
+
+N, D = 40, 64
+
+
+def rms_fwd(**kw):
+    a = dict(N=N, D=D, x=BF16, xp=A[0], y=A[1], w=F32, wp=A[2], post=1, pw=A[3], gates=4, gate=A[4],
+             scale=0.5, eps=1e-6, r=A[5], n=A[6], rstd=A[7], prstd=A[8])
+    a.update(kw)
+    return name(abi.flp_residual_rms_norm_forward(
+        a["N"], a["D"], a["x"], a["xp"], a["y"], a["w"], a["wp"], a["post"], a["pw"], a["gates"],
+        a["gate"], a["scale"], a["eps"], a["r"], a["n"], a["rstd"], a["prstd"], 0))
+
+
+SHARED = [
+    (dict(N=-1), "FLP_INVALID_ARGUMENT"),
+    (dict(D=0), "FLP_INVALID_ARGUMENT"),
+    (dict(D=16385), "FLP_UNSUPPORTED_SHAPE"),
+    (dict(N=1 << 31, gates=1), "FLP_UNSUPPORTED_SHAPE"),
+    (dict(x=I64), "FLP_UNSUPPORTED_DTYPE"),
+    (dict(w=F16), "FLP_UNSUPPORTED_DTYPE"),
+    (dict(scale=NAN), "FLP_INVALID_ARGUMENT"),
+    (dict(scale=1e39), "FLP_INVALID_ARGUMENT"),
+    (dict(gates=3), "FLP_INVALID_ARGUMENT"),             # 40 rows
+    (dict(gates=-1), "FLP_INVALID_ARGUMENT"),
+    (dict(gates=0), "FLP_INVALID_ARGUMENT"),             # a gate without rows
+    (dict(gate=0), "FLP_INVALID_ARGUMENT"),              # rows without a gate
+    (dict(post=0), "FLP_INVALID_ARGUMENT"),              # post_weight without post_norm
+    (dict(xp=0), "FLP_INVALID_ARGUMENT"),
+    (dict(y=0), "FLP_INVALID_ARGUMENT"),
+    (dict(xp=A[0] + 1), "FLP_MISALIGNED"),
+    (dict(gate=A[4] + 2), "FLP_MISALIGNED"),
+]
+
+
+@pytest.mark.parametrize("kw,expect", SHARED + [
+    (dict(eps=-1e-6), "FLP_INVALID_ARGUMENT"),
+    (dict(eps=INF), "FLP_INVALID_ARGUMENT"),
+    (dict(n=0), "FLP_INVALID_ARGUMENT"),
+    (dict(r=0), "FLP_INVALID_ARGUMENT"),
+    (dict(y=0, post=0, pw=0, gates=0, gate=0), "FLP_INVALID_ARGUMENT"),  # r without y
+    (dict(n=A[6] + 1), "FLP_MISALIGNED"),
+    (dict(rstd=A[7] + 2), "FLP_MISALIGNED"),
+    (dict(r=A[0]), "FLP_INVALID_ARGUMENT"),              # in place
+    (dict(n=A[1] + 64), "FLP_INVALID_ARGUMENT"),
+    (dict(n=A[4] + 512), "FLP_INVALID_ARGUMENT"),        # inside the third gate row
+    (dict(prstd=A[7] + 156), "FLP_INVALID_ARGUMENT"),    # the last statistic
+    (dict(N=0, xp=0, y=0, r=0, n=0), "FLP_OK"),
+])
+def test_residual_rms_norm_forward_gates(kw, expect):
+    assert rms_fwd(**kw) == expect
+
+
+def rms_bwd(**kw):
+    a = dict(N=N, D=D, x=BF16, gr=A[0], gn=A[1], xp=A[2], y=A[3], w=F32, wp=A[4], post=1, pw=A[5],
+             gates=4, gate=A[6], scale=0.5, rstd=A[7], prstd=A[8], dx=A[9], dy=A[10], dw=A[11],
+             dpw=A[12], dg=A[13], ws=A[14],
+             wsb=abi.flp_residual_rms_norm_backward_workspace_bytes(N, D, 4))
+    a.update(kw)
+    return name(abi.flp_residual_rms_norm_backward(
+        a["N"], a["D"], a["x"], a["gr"], a["gn"], a["xp"], a["y"], a["w"], a["wp"], a["post"],
+        a["pw"], a["gates"], a["gate"], a["scale"], a["rstd"], a["prstd"], a["dx"], a["dy"],
+        a["dw"], a["dpw"], a["dg"], a["ws"], a["wsb"], 0))
+
+
+NONE = dict(dx=0, dy=0, dw=0, dpw=0, dg=0, ws=0, wsb=0)
+
+
+@pytest.mark.parametrize("kw,expect", SHARED + [
+    (dict(gr=0, gn=0), "FLP_INVALID_ARGUMENT"),
+    (dict(rstd=0), "FLP_INVALID_ARGUMENT"),
+    (dict(prstd=0), "FLP_INVALID_ARGUMENT"),
+    (dict(ws=0), "FLP_INVALID_ARGUMENT"),
+    (dict(gates=0, gate=0), "FLP_INVALID_ARGUMENT"),     # d_gate without a gate
+    (dict(post=0, pw=0), "FLP_INVALID_ARGUMENT"),        # d_post_weight without post_norm
+    (dict(ws=A[14] + 4), "FLP_MISALIGNED"),
+    (dict(dg=A[13] + 2), "FLP_MISALIGNED"),
+    (dict(wsb=4095), "FLP_WORKSPACE_TOO_SMALL"),
+    (dict(dx=A[0]), "FLP_INVALID_ARGUMENT"),             # d_x over grad_r
+    (dict(dy=A[9] + 128), "FLP_INVALID_ARGUMENT"),
+    (dict(dpw=A[11] + 64), "FLP_INVALID_ARGUMENT"),
+    (dict(ws=A[13] + 256), "FLP_INVALID_ARGUMENT"),      # workspace inside d_gate
+    (NONE, "FLP_OK"),
+    (dict(NONE, N=0, gr=0, gn=0, xp=0, y=0, rstd=0, prstd=0), "FLP_OK"),
+])
+def test_residual_rms_norm_backward_gates(kw, expect):
+    assert rms_bwd(**kw) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(xp=0), "FLP_INVALID_ARGUMENT"), (dict(out=0), "FLP_INVALID_ARGUMENT"),
+    (dict(out=A[0]), "FLP_INVALID_ARGUMENT"), (dict(D=0), "FLP_INVALID_ARGUMENT"),
+    (dict(wp=A[1] + 2), "FLP_MISALIGNED"), (dict(eps=NAN), "FLP_INVALID_ARGUMENT"),
+])
+def test_rms_norm_gates(kw, expect):
+    a = dict(D=D, xp=A[0], wp=A[1], eps=1e-6, out=A[2])
+    a.update(kw)
+    assert name(abi.flp_rms_norm_forward(N, a["D"], BF16, a["xp"], F32, a["wp"], a["eps"], a["out"],
+                                         A[3], 0)) == expect
+    if "out" not in kw and "eps" not in kw:
+        assert name(abi.flp_rms_norm_backward(N, a["D"], BF16, A[4], a["xp"], F32, a["wp"], A[3],
+                                              A[5], A[6], A[7], 1 << 20, 0)) == expect
+
+
+def test_rms_norm_workspace_bytes():
+    size = abi.flp_residual_rms_norm_backward_workspace_bytes
+    # two fp32 rows of D per slab: at most 256 slabs, more where gates cut the rows finer
+    assert size(16384, 2688, 0) == size(16384, 2688, 1) == size(16384, 2688, 16384) \
+        == 256 * 2 * 2688 * 4
+    assert size(4097, 64, 17) == 17 * 15 * 2 * 64 * 4      # 241 rows a gate, slabs of 17
+    assert size(20, 64, 10) == 10 * 2 * 64 * 4
+    assert size(0, 64, 0) == 0
