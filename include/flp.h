@@ -564,6 +564,63 @@ flp_status flp_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, cons
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * The first half of a gated feed-forward block: both projections, the activation and the
+ * product in one kernel:
+ *
+ *   z = x w_gate^T,   u = x w_up^T,   out = act(z) u
+ *
+ *   activation   FLP_ACT_SILU       z / (1 + exp(-z))
+ *                FLP_ACT_GELU       z Phi(z), Phi the normal distribution function
+ *                FLP_ACT_GELU_TANH  0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))
+ *   x            [N, D] x_dtype (FLP_BF16, FLP_F16 or FLP_F32), 16-byte aligned.
+ *   w_gate, w_up [F, D] x_dtype, each 16-byte aligned (they may be the halves of one [2 F, D]).
+ *   out          [N, F] x_dtype, aligned to its element size; made in fp32 from the fp32 sums
+ *                and rounded once.
+ *   saved        flp_gated_linear_saved_bytes(N, F, x_dtype) bytes, 16-byte aligned: act(z)
+ *                and u act'(z) for the backward, in 24 bits each (fp32: 32) and a layout of
+ *                their own; or NULL.
+ *
+ * Requirements: D % 32 == 0 (and the size limits of flp_forward), 1 <= F <= 64 * 65535,
+ * N <= 64 * 65535, N F below about 2^36.
+ */
+typedef enum flp_activation {
+  FLP_ACT_SILU = 0,
+  FLP_ACT_GELU = 1,
+  FLP_ACT_GELU_TANH = 2
+} flp_activation;
+
+size_t flp_gated_linear_saved_bytes(int64_t N, int64_t F, flp_dtype x_dtype);
+flp_status flp_gated_linear_forward(int64_t N, int64_t D, int64_t F, flp_dtype x_dtype,
+                                    const void* x, const void* w_gate, const void* w_up,
+                                    flp_activation activation, void* out, void* saved,
+                                    void* stream);
+/*
+ *   dz  = grad_out u act'(z),   du = grad_out act(z)
+ *   d_x = dz w_gate + du w_up,   d_w_gate = dz^T x,   d_w_up = du^T x
+ *
+ *   grad_out   [N, F] x_dtype, aligned to its element size.
+ *   saved      as written by the forward for the same inputs.
+ *   d_x [N, D], d_w_gate, d_w_up [F, D] x_dtype, 16-byte aligned: each may be NULL to skip it.
+ *   workspace  >= flp_gated_linear_backward_workspace_bytes(N, D, F, x_dtype, d_x wanted, a
+ *              weight gradient wanted), 16-byte aligned: dz and du in the layouts of the two
+ *              products (4 N F elements), and the weights and x transposed.
+ *
+ * For 16-bit types dz and du are rounded to x_dtype on the way, whose matrix instructions take
+ * operands of that type; the products' sums are fp32 and rounded once.  The sums run in an order fixed by the sizes; d_x of a row is bitwise
+ * the same among batches of up to 2048 rows, and among larger ones.  N = 0 writes zeros to
+ * d_w_gate and d_w_up.
+ */
+size_t flp_gated_linear_backward_workspace_bytes(int64_t N, int64_t D, int64_t F,
+                                                 flp_dtype x_dtype, int need_d_x,
+                                                 int need_d_weights);
+flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype x_dtype,
+                                     const void* grad_out, const void* saved, const void* x,
+                                     const void* w_gate, const void* w_up,
+                                     flp_activation activation, void* d_x, void* d_w_gate,
+                                     void* d_w_up, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
  * Root mean square norm of the rows x[i, :]:
  *
  *   rstd_i = 1 / sqrt(sum_d x_id^2 / D + eps),   out = x rstd weight
@@ -746,7 +803,8 @@ typedef enum flp_kernel_kind {
   FLP_K_LOSS = 13,      /* flp_cross_entropy_*: row losses, their sum, gradient factors */
   FLP_K_ADAMW = 14,     /* flp_adamw_step */
   FLP_K_RMS_NORM = 15,  /* flp_rms_norm_*, flp_residual_rms_norm_* */
-  FLP_K_COUNT = 16
+  FLP_K_GATED = 16,     /* flp_gated_linear_*, besides its products in the backward */
+  FLP_K_COUNT = 17
 } flp_kernel_kind;
 
 void flp_profile_enable(int on);

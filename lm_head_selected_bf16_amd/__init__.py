@@ -26,6 +26,9 @@ from ._abi import (FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpErro
                    flp_cross_entropy_gradients_workspace_bytes, flp_scale_inplace,
                    flp_dropout, flp_layer_norm_backward, flp_layer_norm_backward_workspace_bytes,
                    flp_layer_norm_forward, flp_adamw_step, flp_adamw_tensor,
+                   FLP_ACT_GELU, FLP_ACT_GELU_TANH, FLP_ACT_SILU, flp_gated_linear_backward,
+                   flp_gated_linear_backward_workspace_bytes, flp_gated_linear_forward,
+                   flp_gated_linear_saved_bytes,
                    flp_rms_norm_backward, flp_rms_norm_forward,
                    flp_residual_rms_norm_backward, flp_residual_rms_norm_forward,
                    flp_residual_rms_norm_backward_workspace_bytes,
@@ -46,7 +49,8 @@ from .torch_ops import (LinearLogp, backward, backward_workspace_bytes,  # noqa:
                         cross_entropy_backward, cross_entropy_forward, cross_entropy_gradients,
                         linear_cross_entropy, dropout, dropout_forward, layer_norm,
                         layer_norm_backward, layer_norm_forward, AdamWState, adamw_state,
-                        adamw_step, rms_norm, rms_norm_forward, rms_norm_backward,
+                        adamw_step, gated_linear, gated_linear_forward, gated_linear_backward,
+                        rms_norm, rms_norm_forward, rms_norm_backward,
                         residual_rms_norm, residual_rms_norm_forward, residual_rms_norm_backward)
 
 __all__ = [
@@ -82,6 +86,10 @@ __all__ = [
     "flp_layer_norm_forward", "flp_layer_norm_backward",
     "flp_layer_norm_backward_workspace_bytes",
     "AdamWState", "adamw_state", "adamw_step", "flp_adamw_step", "flp_adamw_tensor",
+    "gated_linear", "gated_linear_forward", "gated_linear_backward", "flp_gated_linear_forward",
+    "flp_gated_linear_backward", "flp_gated_linear_saved_bytes",
+    "flp_gated_linear_backward_workspace_bytes", "FLP_ACT_SILU", "FLP_ACT_GELU",
+    "FLP_ACT_GELU_TANH",
     "rms_norm", "rms_norm_forward", "rms_norm_backward", "flp_rms_norm_forward",
     "flp_rms_norm_backward", "residual_rms_norm", "residual_rms_norm_forward",
     "residual_rms_norm_backward", "flp_residual_rms_norm_forward",

@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libflp.so")
 FLP_BF16, FLP_F32, FLP_I64, FLP_I32, FLP_F16 = 0, 1, 2, 3, 4
 # flp_reduction
 FLP_REDUCE_NONE, FLP_REDUCE_SUM, FLP_REDUCE_MEAN = 0, 1, 2
+# flp_activation
+FLP_ACT_SILU, FLP_ACT_GELU, FLP_ACT_GELU_TANH = 0, 1, 2
 # flp_status
 STATUS_NAMES = {
     0: "FLP_OK",
@@ -85,6 +87,12 @@ SIGNATURES = {
     "flp_layer_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
     "flp_layer_norm_backward": (_int, [_i64, _i64, _int, _vp, _vp, _int, _vp, _fp, _fp, _vp, _vp,
                                        _vp, _vp, _sz, _vp]),
+    "flp_gated_linear_saved_bytes": (_sz, [_i64, _i64, _int]),
+    "flp_gated_linear_forward": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp,
+                                        _vp]),
+    "flp_gated_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _int, _int]),
+    "flp_gated_linear_backward": (_int, [_i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _int, _vp,
+                                         _vp, _vp, _vp, _sz, _vp]),
     "flp_rms_norm_forward": (_int, [_i64, _i64, _int, _vp, _int, _vp, _double, _vp, _fp, _vp]),
     "flp_rms_norm_backward": (_int, [_i64, _i64, _int, _vp, _vp, _int, _vp, _fp, _vp, _vp, _vp, _sz,
                                      _vp]),
@@ -372,6 +380,31 @@ def flp_layer_norm_backward(N, D, x_dtype, grad_out, x, w_dtype, weight, mean, r
                                               workspace_bytes, stream))
 
 
+def flp_gated_linear_saved_bytes(N: int, F: int, x_dtype: int) -> int:
+    return int(load().flp_gated_linear_saved_bytes(N, F, x_dtype))
+
+
+def flp_gated_linear_forward(N, D, F, x_dtype, x, w_gate, w_up, activation, out, saved,
+                             stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_gated_linear_forward(N, D, F, x_dtype, x, w_gate, w_up, activation, out,
+                                               saved, stream))
+
+
+def flp_gated_linear_backward_workspace_bytes(N: int, D: int, F: int, x_dtype: int, need_d_x: int,
+                                              need_d_weights: int) -> int:
+    return int(load().flp_gated_linear_backward_workspace_bytes(N, D, F, x_dtype, need_d_x,
+                                                                need_d_weights))
+
+
+def flp_gated_linear_backward(N, D, F, x_dtype, grad_out, saved, x, w_gate, w_up, activation, d_x,
+                              d_w_gate, d_w_up, workspace, workspace_bytes, stream) -> int:
+    """Raw call: every pointer argument is an int address (0 for NULL)."""
+    return int(load().flp_gated_linear_backward(N, D, F, x_dtype, grad_out, saved, x, w_gate, w_up,
+                                                activation, d_x, d_w_gate, d_w_up, workspace,
+                                                workspace_bytes, stream))
+
+
 def flp_rms_norm_forward(N, D, x_dtype, x, w_dtype, weight, eps, out, out_rstd, stream) -> int:
     """Raw call: every pointer argument is an int address (0 for NULL)."""
     return int(load().flp_rms_norm_forward(N, D, x_dtype, x, w_dtype, weight, eps, out, out_rstd,
@@ -445,7 +478,7 @@ def flp_probe_read(buffer: int, nbytes: int, scratch: int, scratch_bytes: int, s
 
 KERNEL_KINDS = ("forward", "merge", "dlogits", "transpose", "d_hidden", "d_weight", "d_bias",
                 "logits_forward", "logits_backward", "rows", "embedding", "dropout", "layer_norm",
-                "loss", "adamw", "rms_norm")
+                "loss", "adamw", "rms_norm", "gated")
 
 
 def flp_profile_enable(on: bool) -> None:

@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libflp.so")
 NODES = os.path.join(PKG, "_flp_torch.so")
 SOURCES = ["flp_kernels.hip", "flp_rows.hip", "flp_loss.hip", "flp_embed.hip", "flp_dropout.hip", "flp_norm.hip",
-           "flp_rms.hip", "flp_adamw.hip",
+           "flp_rms.hip", "flp_adamw.hip", "flp_gated.hip",
            "flp_probe.hip", "flp_noalloc.hip",
            "flp_api.cpp", "flp_plan.cpp"]
 

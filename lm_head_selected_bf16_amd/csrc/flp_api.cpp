@@ -1002,6 +1002,115 @@ flp_status flp_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p, co
   return FLP_OK;
 }
 
+// ---- gated projection ----
+
+size_t flp_gated_linear_saved_bytes(int64_t N, int64_t F, flp_dtype x_dtype) {
+  if (N < 1 || F < 1) return 0;
+  return gated_saved_bytes(N, F, x_dtype);
+}
+
+flp_status flp_gated_linear_forward(int64_t N, int64_t D, int64_t F, flp_dtype x_dtype,
+                                    const void* x, const void* w_gate, const void* w_up,
+                                    flp_activation activation, void* out, void* saved,
+                                    void* stream) {
+  flp_status st = validate_gated_forward(N, D, F, x_dtype, x, w_gate, w_up, activation, out, saved);
+  if (st != FLP_OK || N == 0) return st;
+  if ((st = check_device()) != FLP_OK) return st;
+  GatedFwdArgs a{};
+  a.N = N;
+  a.D = D;
+  a.F = F;
+  a.act = activation;
+  a.x = x;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.out = out;
+  a.saved = saved;
+  a.ld_saved = round_up(F, kGatedPad);
+  if (launch_gated_forward(x_dtype, a, static_cast<hipStream_t>(stream)) != hipSuccess)
+    return FLP_HIP_ERROR;
+  return FLP_OK;
+}
+
+size_t flp_gated_linear_backward_workspace_bytes(int64_t N, int64_t D, int64_t F,
+                                                 flp_dtype x_dtype, int need_d_x,
+                                                 int need_d_weights) {
+  if (N < 1 || D < 1 || F < 1) return 0;
+  return gated_layout(N, D, F, x_dtype, need_d_x != 0, need_d_weights != 0).total;
+}
+
+flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype x_dtype,
+                                     const void* grad_out, const void* saved, const void* x,
+                                     const void* w_gate, const void* w_up,
+                                     flp_activation activation, void* d_x, void* d_w_gate,
+                                     void* d_w_up, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  flp_status st = validate_gated_backward(N, D, F, x_dtype, grad_out, saved, x, w_gate, w_up,
+                                          activation, d_x, d_w_gate, d_w_up, workspace,
+                                          workspace_bytes);
+  if (st != FLP_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t xs = dtype_size(x_dtype);
+  const bool dw = d_w_gate != nullptr || d_w_up != nullptr;
+  if (!dw && (d_x == nullptr || N == 0)) return FLP_OK;
+  if ((st = check_device()) != FLP_OK) return st;
+  if (N == 0) {
+    for (void* d : {d_w_gate, d_w_up})
+      if (d != nullptr && launch_zero(d, size_t(F) * D * xs, s) != hipSuccess) return FLP_HIP_ERROR;
+    return FLP_OK;
+  }
+  const GatedLayout L = gated_layout(N, D, F, x_dtype, d_x != nullptr, dw);
+  GatedDzArgs z{};
+  z.N = N;
+  z.F = F;
+  z.grad = grad_out;
+  z.saved = saved;
+  z.ld_saved = L.fp;
+  z.dz = d_x ? at(workspace, L.dz_off) : nullptr;
+  z.dzT = dw ? at(workspace, L.dzt_off) : nullptr;
+  if (launch_gated_dz(x_dtype, z, s) != hipSuccess) return FLP_HIP_ERROR;
+  if (d_x != nullptr) {
+    void* wt = at(workspace, L.wt_off);
+    void* wt_up = at(wt, size_t(L.fp) * D * xs);
+    if (launch_transpose(x_dtype, w_gate, F, L.fp, D, D, wt, s) != hipSuccess ||
+        launch_transpose(x_dtype, w_up, F, L.fp, D, D, wt_up, s) != hipSuccess)
+      return FLP_HIP_ERROR;
+    GemmArgs g{};
+    g.a = z.dz;
+    g.b = wt;
+    g.lda_b = g.ldb_b = 128;
+    g.a_ks = N * 128;
+    g.b_ks = D * 128;
+    g.M = N;
+    g.N = D;
+    g.K = 2 * L.fp;
+    g.out = d_x;
+    g.ldo = D;
+    g.k_slab = L.k_slab;
+    if (L.k_slab > 0) g.acc = reinterpret_cast<float*>(at(workspace, L.slab_off));
+    if (launch_dx(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
+  }
+  if (dw) {
+    void* xt = at(workspace, L.xt_off);
+    if (launch_transpose(x_dtype, x, N, L.np, D, D, xt, s) != hipSuccess) return FLP_HIP_ERROR;
+    for (int up = 0; up < 2; ++up) {
+      GemmArgs g{};
+      g.a = at(z.dzT, size_t(up) * L.fp * 128);
+      g.b = xt;
+      g.lda_b = g.ldb_b = 128;
+      g.a_ks = 2 * L.fp * 128;
+      g.b_ks = D * 128;
+      g.M = F;
+      g.N = D;
+      g.K = L.np;
+      g.out = up ? d_w_up : d_w_gate;
+      g.ldo = D;
+      if (g.out != nullptr && launch_dw(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
+    }
+  }
+  return FLP_OK;
+}
+
 // ---- root mean square norms ----
 
 flp_status flp_rms_norm_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,

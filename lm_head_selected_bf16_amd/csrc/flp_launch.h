@@ -258,6 +258,28 @@ hipError_t launch_loss_count(int64_t N, int64_t V, const void* targets, bool t64
 // x *= *factor in place (n elements); nothing is touched when the factor is 1.
 hipError_t launch_scale(flp_dtype x_dtype, int64_t n, void* x, const float* factor, hipStream_t s);
 
+// Gated projection (flp_gated.hip).
+struct GatedFwdArgs {
+  int64_t N, D, F;
+  flp_activation act;
+  const void* x;             // [N][D]
+  const void* w_gate;        // [F][D]
+  const void* w_up;          // [F][D]
+  void* out;                 // [N][F]
+  void* saved;               // [N][ld_saved] act(z) and u act'(z), by four columns, or null
+  int64_t ld_saved;          // F rounded up to 64
+};
+struct GatedDzArgs {
+  int64_t N, F;
+  const void* grad;          // [N][F]
+  const void* saved;         // as above
+  int64_t ld_saved;
+  void* dz;                  // K-blocked: N rows, K = 2 ld_saved (dz, du), or null
+  void* dzT;                 // K-blocked: 2 ld_saved rows, K = N rounded up to 64, or null
+};
+hipError_t launch_gated_forward(flp_dtype x, const GatedFwdArgs& a, hipStream_t s);
+hipError_t launch_gated_dz(flp_dtype x, const GatedDzArgs& a, hipStream_t s);
+
 // Root mean square norms around a block (flp_rms.hip).
 struct RmsFwdArgs {
   int64_t N, D;

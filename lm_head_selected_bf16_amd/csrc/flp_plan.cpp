@@ -868,6 +868,96 @@ flp_status validate_dropout(int64_t n, flp_dtype x_dtype, const void* x, double 
   return any_alias(outs, 1, ins, 2) ? FLP_INVALID_ARGUMENT : FLP_OK;
 }
 
+GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need_dx,
+                         bool need_dw) {
+  GatedLayout L;
+  const size_t xs = dtype_size(x);
+  L.fp = round_up(F, kGatedPad);
+  L.np = round_up(N, kGatedPad);
+  const int64_t K = 2 * L.fp;
+  size_t at = 0;
+  auto take = [&](size_t& off, size_t bytes) {
+    off = at;
+    at += align_up(bytes);
+  };
+  if (need_dx) {
+    take(L.dz_off, size_t(K) * N * xs);
+    take(L.wt_off, size_t(K) * D * xs);
+    const int64_t slabs = std::min<int64_t>(8, K / 1024);
+    if (N <= kGatedSlabRows && slabs > 1) {
+      L.k_slab = round_up(ceil_div(K, slabs), 256);
+      take(L.slab_off, size_t(ceil_div(K, L.k_slab)) * N * D * 4);
+    }
+  }
+  if (need_dw) {
+    take(L.dzt_off, size_t(K) * L.np * xs);
+    take(L.xt_off, size_t(D) * L.np * xs);
+  }
+  L.total = at;
+  return L;
+}
+
+namespace {
+
+flp_status check_gated(int64_t N, int64_t D, int64_t F, flp_dtype x, flp_activation act) {
+  const flp_status st = check_dims(N, D, F, x, FLP_I64);  // F stands where the vocabulary does
+  if (st != FLP_OK) return st;
+  if (act != FLP_ACT_SILU && act != FLP_ACT_GELU && act != FLP_ACT_GELU_TANH)
+    return FLP_INVALID_ARGUMENT;
+  // a launch's second grid dimension counts 64 tokens or weight rows, and a launch holds fewer
+  // than 2^32 threads (256 for 64 x 64 elements of dz)
+  if (N > int64_t(65535) * 64 || F > int64_t(65535) * 64) return FLP_UNSUPPORTED_SHAPE;
+  if (ceil_div(N, 64) * ceil_div(F, 64) >= (int64_t(1) << 24)) return FLP_UNSUPPORTED_SHAPE;
+  return FLP_OK;
+}
+
+}  // namespace
+
+flp_status validate_gated_forward(int64_t N, int64_t D, int64_t F, flp_dtype x_dtype, const void* x,
+                                  const void* w_gate, const void* w_up, flp_activation act,
+                                  const void* out, const void* saved) {
+  const flp_status st = check_gated(N, D, F, x_dtype, act);
+  if (st != FLP_OK || N == 0) return st;
+  if (!x || !w_gate || !w_up || !out) return FLP_INVALID_ARGUMENT;
+  const size_t xs = dtype_size(x_dtype);
+  if (!aligned(x, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(out, xs) ||
+      !aligned(saved, 16))
+    return FLP_MISALIGNED;
+  const Span ins[] = {span(x, size_t(N) * D * xs), span(w_gate, size_t(F) * D * xs),
+                      span(w_up, size_t(F) * D * xs)};
+  const Span outs[] = {span(out, size_t(N) * F * xs),
+                       span(saved, gated_saved_bytes(N, F, x_dtype))};
+  return any_alias(outs, 2, ins, 3) ? FLP_INVALID_ARGUMENT : FLP_OK;
+}
+
+flp_status validate_gated_backward(int64_t N, int64_t D, int64_t F, flp_dtype x_dtype,
+                                   const void* grad, const void* saved, const void* x,
+                                   const void* w_gate, const void* w_up, flp_activation act,
+                                   const void* d_x, const void* d_w_gate, const void* d_w_up,
+                                   const void* workspace, size_t workspace_bytes) {
+  const flp_status st = check_gated(N, D, F, x_dtype, act);
+  if (st != FLP_OK) return st;
+  const bool dw = d_w_gate || d_w_up;
+  if (!d_x && !dw) return FLP_OK;
+  if (N > 0 && (!grad || !saved || !workspace)) return FLP_INVALID_ARGUMENT;
+  if (N > 0 && ((d_x && (!w_gate || !w_up)) || (dw && !x))) return FLP_INVALID_ARGUMENT;
+  const size_t xs = dtype_size(x_dtype);
+  if (!aligned(grad, xs) || !aligned(saved, 16) || !aligned(x, 16) || !aligned(w_gate, 16) ||
+      !aligned(w_up, 16) || !aligned(d_x, 16) || !aligned(d_w_gate, 16) || !aligned(d_w_up, 16) ||
+      !aligned(workspace, 16))
+    return FLP_MISALIGNED;
+  const size_t weight = size_t(F) * D * xs, rows = size_t(N) * D * xs;
+  const Span ins[] = {span(grad, size_t(N) * F * xs),
+                      span(saved, gated_saved_bytes(N, F, x_dtype)),
+                      span(x, rows), span(w_gate, weight), span(w_up, weight)};
+  const Span outs[] = {span(d_x, rows), span(d_w_gate, weight), span(d_w_up, weight),
+                       span(N > 0 ? workspace : nullptr, workspace_bytes)};
+  if (any_alias(outs, 4, ins, 5)) return FLP_INVALID_ARGUMENT;
+  if (N > 0 && workspace_bytes < gated_layout(N, D, F, x_dtype, d_x != nullptr, dw).total)
+    return FLP_WORKSPACE_TOO_SMALL;
+  return FLP_OK;
+}
+
 RmsLayout rms_layout(int64_t N, int64_t D, int64_t gate_rows) {
   RmsLayout L;
   L.gates = gate_rows > 1 && gate_rows == N;

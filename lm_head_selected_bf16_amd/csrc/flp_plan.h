@@ -153,6 +153,24 @@ NormLayout norm_layout(int64_t N, int64_t D);
 // ---- dropout: elements whose 16 random bits are below this are dropped (65536: all) ----
 inline uint32_t dropout_threshold(double p) { return uint32_t(p * 65536.0 + 0.5); }
 
+// ---- gated projection backward ----
+constexpr int64_t kGatedPad = 64;  // columns and tokens of dz are padded to this with zeros
+// A batch of up to kGatedSlabRows rows sums d_x over slabs of [dz | du]: its output tiles are too
+// few to fill the chip.
+constexpr int64_t kGatedSlabRows = 2048;
+struct GatedLayout {
+  int64_t fp = 0, np = 0;    // F and N rounded up to kGatedPad
+  int64_t k_slab = 0;        // columns of a slab of d_x (a multiple of 256), 0: one walk
+  size_t dz_off = 0, wt_off = 0, slab_off = 0;  // d_x: [dz | du], [Wg; Wu]^T, slab sums
+  size_t dzt_off = 0, xt_off = 0;               // weight gradients: their transposes
+  size_t total = 0;
+};
+// What the forward keeps for the backward: two numbers of 3 bytes (fp32: 4) per element.
+inline size_t gated_saved_bytes(int64_t N, int64_t F, flp_dtype x) {
+  return size_t(N) * size_t(round_up(F, kGatedPad)) * (x == FLP_F32 ? 8 : 6);
+}
+GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need_dx, bool need_dw);
+
 // ---- root mean square norms backward: slabs of rows, within the rows of one gate ----
 constexpr int64_t kRmsMaxWidth = 16384;  // elements that the eight waves of a team hold
 struct RmsLayout {
@@ -279,6 +297,15 @@ flp_status validate_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype,
                                         const void* workspace, size_t workspace_bytes);
 flp_status validate_dropout(int64_t n, flp_dtype x_dtype, const void* x, double p,
                             const int64_t* rng, const void* out);
+// Gated projection.
+flp_status validate_gated_forward(int64_t N, int64_t D, int64_t F, flp_dtype x_dtype, const void* x,
+                                  const void* w_gate, const void* w_up, flp_activation act,
+                                  const void* out, const void* saved);
+flp_status validate_gated_backward(int64_t N, int64_t D, int64_t F, flp_dtype x_dtype,
+                                   const void* grad, const void* saved, const void* x,
+                                   const void* w_gate, const void* w_up, flp_activation act,
+                                   const void* d_x, const void* d_w_gate, const void* d_w_up,
+                                   const void* workspace, size_t workspace_bytes);
 // Root mean square norms; y, post_weight, gate and out_r belong to the residual form.
 flp_status validate_rms_forward(int64_t N, int64_t D, flp_dtype x_dtype, const void* x,
                                 const void* y, flp_dtype w_dtype, const void* weight, bool post,

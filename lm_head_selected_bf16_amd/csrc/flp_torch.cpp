@@ -40,6 +40,10 @@ struct Api {
   decltype(&::flp_cross_entropy_backward) loss_backward;
   decltype(&::flp_cross_entropy_backward_workspace_bytes) loss_backward_bytes;
   decltype(&::flp_adamw_step) adamw_step;
+  decltype(&::flp_gated_linear_saved_bytes) gated_saved_bytes;
+  decltype(&::flp_gated_linear_forward) gated_forward;
+  decltype(&::flp_gated_linear_backward) gated_backward;
+  decltype(&::flp_gated_linear_backward_workspace_bytes) gated_backward_bytes;
   decltype(&::flp_residual_rms_norm_forward) rms_forward;
   decltype(&::flp_residual_rms_norm_backward) rms_backward;
   decltype(&::flp_residual_rms_norm_backward_workspace_bytes) rms_backward_bytes;
@@ -62,6 +66,10 @@ void bind(const std::map<std::string, uintptr_t>& at) {
   take(api.loss_backward, "flp_cross_entropy_backward");
   take(api.loss_backward_bytes, "flp_cross_entropy_backward_workspace_bytes");
   take(api.adamw_step, "flp_adamw_step");
+  take(api.gated_saved_bytes, "flp_gated_linear_saved_bytes");
+  take(api.gated_forward, "flp_gated_linear_forward");
+  take(api.gated_backward, "flp_gated_linear_backward");
+  take(api.gated_backward_bytes, "flp_gated_linear_backward_workspace_bytes");
   take(api.rms_forward, "flp_residual_rms_norm_forward");
   take(api.rms_backward, "flp_residual_rms_norm_backward");
   take(api.rms_backward_bytes, "flp_residual_rms_norm_backward_workspace_bytes");
@@ -325,6 +333,52 @@ struct CrossEntropyNode : Function<CrossEntropyNode> {
   }
 };
 
+struct GatedLinearNode : Function<GatedLinearNode> {
+  static at::Tensor forward(AutogradContext* ctx, const at::Tensor& x, const at::Tensor& w_gate,
+                            const at::Tensor& w_up, int64_t act, int64_t stream) {
+    const int64_t F = w_gate.size(0), D = w_gate.size(1), N = x.numel() / D;
+    auto shape = x.sizes().vec();
+    shape.back() = F;
+    at::Tensor out = at::empty(shape, x.options());
+    const at::Tensor saved = bytes(api.gated_saved_bytes(N, F, code(x)), x);
+    check("flp_gated_linear_forward",
+          api.gated_forward(N, D, F, code(x), ptr(x), ptr(w_gate), ptr(w_up), flp_activation(act),
+                            ptr(out), ptr(saved), reinterpret_cast<void*>(stream)));
+    ctx->save_for_backward({x, w_gate, w_up, saved});
+    ctx->saved_data["act"] = act;
+    ctx->saved_data["stream"] = stream;
+    ctx->saved_data["F"] = F;
+    return out;
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list saved = ctx->get_saved_variables();
+    const at::Tensor &x = saved[0], &wg = saved[1], &wu = saved[2];
+    const int64_t F = ctx->saved_data["F"].toInt();
+    const at::Tensor g = grads[0].contiguous();
+    const int64_t N = g.numel() / F;
+    same(dense(x) && dense(wg) && dense(wu) && wg.dim() == 2 && wg.size(0) == F &&
+         wu.sizes() == wg.sizes() && x.dim() >= 1 && x.size(-1) == wg.size(1) &&
+         x.numel() == N * wg.size(1) && x.scalar_type() == g.scalar_type() &&
+         wg.scalar_type() == g.scalar_type() && wu.scalar_type() == g.scalar_type() &&
+         x.device() == g.device() && wg.device() == g.device() && wu.device() == g.device());
+    const int64_t D = wg.size(1);
+    at::Tensor dx, dwg, dwu;
+    if (ctx->needs_input_grad(0)) dx = at::empty_like(x);
+    if (ctx->needs_input_grad(1)) dwg = at::empty_like(wg);
+    if (ctx->needs_input_grad(2)) dwu = at::empty_like(wu);
+    const at::Tensor ws = bytes(api.gated_backward_bytes(N, D, F, code(x), dx.defined(),
+                                                         dwg.defined() || dwu.defined()),
+                                x);
+    check("flp_gated_linear_backward",
+          api.gated_backward(N, D, F, code(x), ptr(g), ptr(saved[3]), ptr(x), ptr(wg), ptr(wu),
+                             flp_activation(ctx->saved_data["act"].toInt()), ptr(dx), ptr(dwg),
+                             ptr(dwu), ptr(ws), size_t(ws.numel()),
+                             reinterpret_cast<void*>(ctx->saved_data["stream"].toInt())));
+    return {first_order(dx, grads[0], x, wg, wu), first_order(dwg, grads[0], x, wg, wu),
+            first_order(dwu, grads[0], x, wg, wu), at::Tensor(), at::Tensor()};
+  }
+};
+
 // The norms around a block: {r, n}, or {n} without y.
 struct RmsNormNode : Function<RmsNormNode> {
   static variable_list forward(AutogradContext* ctx, const at::Tensor& x, const OptTensor& y,
@@ -541,6 +595,10 @@ PYBIND11_MODULE(_flp_torch, m) {
   m.def("layer_norm", [](const at::Tensor& x, const OptTensor& weight, const OptTensor& bias,
                          double eps, int64_t stream) {
     return LayerNormNode::apply(x, weight, bias, eps, stream);
+  });
+  m.def("gated_linear", [](const at::Tensor& x, const at::Tensor& w_gate, const at::Tensor& w_up,
+                           int64_t act, int64_t stream) {
+    return GatedLinearNode::apply(x, w_gate, w_up, act, stream);
   });
   m.def("rms_norm", [](const at::Tensor& x, const OptTensor& y, const OptTensor& weight,
                        const OptTensor& post_weight, const OptTensor& gate, bool post,

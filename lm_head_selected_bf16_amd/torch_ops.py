@@ -981,6 +981,89 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
         return _nodes().layer_norm(x, weight, bias, eps, _stream(dev))
 
 
+# ---- gated projection of a feed-forward block ----------------------------------------------------
+
+_ACTIVATIONS = {"silu": _abi.FLP_ACT_SILU, "gelu": _abi.FLP_ACT_GELU,
+                "gelu_tanh": _abi.FLP_ACT_GELU_TANH}
+
+
+def _prepare_gated(x, w_gate, w_up, activation):
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be 'silu', 'gelu' or 'gelu_tanh'")
+    if x.dtype not in _X_DTYPES or w_gate.dtype != x.dtype or w_up.dtype != x.dtype:
+        raise TypeError("x, w_gate and w_up must have the same dtype: bfloat16, float16 or float32")
+    if not (x.is_cuda and w_gate.device == x.device and w_up.device == x.device):
+        raise ValueError("x, w_gate and w_up must be on one GPU")
+    for name, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up)):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if (w_gate.dim() != 2 or w_up.shape != w_gate.shape or x.dim() < 1
+            or x.shape[-1] != w_gate.shape[1] or x.shape[-1] < 1):
+        raise ValueError("w_gate and w_up must be [F, D] with D = x.shape[-1]")
+    F, D = int(w_gate.shape[0]), int(w_gate.shape[1])
+    return x.numel() // D, D, F, _ACTIVATIONS[activation]
+
+
+def gated_linear_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                         activation: str = "silu", return_saved: bool = True
+                         ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(out, saved) through flp_gated_linear_forward; saved (bytes, for the backward) or None."""
+    N, D, F, act = _prepare_gated(x, w_gate, w_up, activation)
+    dev, xd = x.device, _X_DTYPES[x.dtype]
+    with _on(dev):
+        out = torch.empty(x.shape[:-1] + (F,), dtype=x.dtype, device=dev)
+        saved = None
+        if return_saved:
+            saved = torch.empty(max(_abi.flp_gated_linear_saved_bytes(N, F, xd), 16),
+                                dtype=torch.uint8, device=dev)
+        st = _abi.flp_gated_linear_forward(N, D, F, xd, x.data_ptr(), w_gate.data_ptr(),
+                                           w_up.data_ptr(), act, out.data_ptr(), _ptr(saved),
+                                           _stream(dev))
+    _check("flp_gated_linear_forward", st)
+    return out, saved
+
+
+def gated_linear_backward(grad_out: torch.Tensor, saved: torch.Tensor, x: torch.Tensor,
+                          w_gate: torch.Tensor, w_up: torch.Tensor, activation: str = "silu",
+                          need_input: bool = True, need_gate: bool = True, need_up: bool = True):
+    """(d_x, d_w_gate, d_w_up) through flp_gated_linear_backward; unrequested ones are None."""
+    N, D, F, act = _prepare_gated(x, w_gate, w_up, activation)
+    dev, xd = x.device, _X_DTYPES[x.dtype]
+    if (grad_out.dtype != x.dtype or grad_out.shape != x.shape[:-1] + (F,)
+            or not grad_out.is_contiguous() or grad_out.device != dev):
+        raise ValueError("grad_out must be contiguous with the dtype, shape and device of the output")
+    if (saved.dtype != torch.uint8 or not saved.is_contiguous() or saved.device != dev
+            or saved.numel() < _abi.flp_gated_linear_saved_bytes(N, F, xd)):
+        raise ValueError("saved must be what gated_linear_forward returned")
+    with _on(dev):
+        dx = torch.empty_like(x) if need_input else None
+        dwg = torch.empty_like(w_gate) if need_gate else None
+        dwu = torch.empty_like(w_up) if need_up else None
+        size = _abi.flp_gated_linear_backward_workspace_bytes(N, D, F, xd, int(need_input),
+                                                              int(need_gate or need_up))
+        ws = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+        st = _abi.flp_gated_linear_backward(N, D, F, xd, grad_out.data_ptr(), saved.data_ptr(),
+                                            x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), act,
+                                            _ptr(dx), _ptr(dwg), _ptr(dwu), ws.data_ptr(),
+                                            ws.numel(), _stream(dev))
+    _check("flp_gated_linear_backward", st)
+    return dx, dwg, dwu
+
+
+def gated_linear(x, w_gate, w_up, activation="silu"):
+    """act(x @ w_gate^T) * (x @ w_up^T), the first half of a gated feed-forward block,
+    differentiable in x, w_gate and w_up.  x [.., D] with D a multiple of 32, w_gate and w_up
+    [F, D] (they may be the halves of one [2 F, D] tensor); activation "silu", "gelu" (the exact
+    one) or "gelu_tanh".  For the backward two numbers per element of the output are kept, 6 bytes (float32:
+    8)."""
+    if not _wants_grad(x, w_gate, w_up):
+        return gated_linear_forward(x, w_gate, w_up, activation, return_saved=False)[0]
+    act = _prepare_gated(x, w_gate, w_up, activation)[3]
+    dev = x.device
+    with _on(dev):
+        return _nodes().gated_linear(x, w_gate, w_up, act, _stream(dev))
+
+
 # ---- root mean square norms around a block ------------------------------------------------------
 
 def _prepare_rms(x, y, weight, post_weight, gate, post_norm):

@@ -220,3 +220,90 @@ def test_rms_norm_workspace_bytes():
     assert size(4097, 64, 17) == 17 * 15 * 2 * 64 * 4      # 241 rows a gate, slabs of 17
     assert size(20, 64, 10) == 10 * 2 * 64 * 4
     assert size(0, 64, 0) == 0
+
+
+# ---- gated projection --------------------------------------------------------------------------
+
+F = 100
+
+
+def gated_fwd(**kw):
+    a = dict(N=N, D=D, F=F, x=BF16, xp=A[0], wg=A[1], wu=A[2], act=0, out=A[3], saved=A[4])
+    a.update(kw)
+    return name(abi.flp_gated_linear_forward(a["N"], a["D"], a["F"], a["x"], a["xp"], a["wg"],
+                                             a["wu"], a["act"], a["out"], a["saved"], 0))
+
+
+GATED = [
+    (dict(N=-1), "FLP_INVALID_ARGUMENT"),
+    (dict(F=0), "FLP_INVALID_ARGUMENT"),
+    (dict(D=48), "FLP_UNSUPPORTED_SHAPE"),               # no multiple of 32
+    (dict(D=1 << 23), "FLP_UNSUPPORTED_SHAPE"),          # 256 rows pass 2^31 bytes
+    (dict(F=64 * 65535 + 1), "FLP_UNSUPPORTED_SHAPE"),
+    (dict(N=64 * 65535 + 1), "FLP_UNSUPPORTED_SHAPE"),
+    (dict(N=64 * 65535, F=64 * 256 + 1), "FLP_UNSUPPORTED_SHAPE"),
+    (dict(x=I32), "FLP_UNSUPPORTED_DTYPE"),
+    (dict(act=3), "FLP_INVALID_ARGUMENT"),
+    (dict(act=-1), "FLP_INVALID_ARGUMENT"),
+    (dict(wg=0), "FLP_INVALID_ARGUMENT"),
+    (dict(wu=0), "FLP_INVALID_ARGUMENT"),
+    (dict(xp=A[0] + 8), "FLP_MISALIGNED"),
+    (dict(wu=A[2] + 2), "FLP_MISALIGNED"),
+    (dict(saved=A[4] + 8), "FLP_MISALIGNED"),
+]
+
+
+@pytest.mark.parametrize("kw,expect", GATED + [
+    (dict(xp=0), "FLP_INVALID_ARGUMENT"),
+    (dict(out=0), "FLP_INVALID_ARGUMENT"),
+    (dict(out=A[3] + 1), "FLP_MISALIGNED"),
+    (dict(out=A[0]), "FLP_INVALID_ARGUMENT"),
+    (dict(out=A[2] + F * D * 2 - 2), "FLP_INVALID_ARGUMENT"),      # the last weight
+    (dict(out=A[4] + N * 128 * 6 - 2), "FLP_INVALID_ARGUMENT"),    # saved: rows of 128
+    (dict(N=0, xp=0, wg=0, wu=0, out=0, saved=0), "FLP_OK"),
+])
+def test_gated_linear_forward_gates(kw, expect):
+    assert gated_fwd(**kw) == expect
+
+
+def gated_bwd(**kw):
+    a = dict(N=N, D=D, F=F, x=BF16, g=A[0], saved=A[1], xp=A[2], wg=A[3], wu=A[4], act=1, dx=A[5],
+             dwg=A[6], dwu=A[7], ws=A[8],
+             wsb=abi.flp_gated_linear_backward_workspace_bytes(N, D, F, BF16, 1, 1))
+    a.update(kw)
+    return name(abi.flp_gated_linear_backward(a["N"], a["D"], a["F"], a["x"], a["g"], a["saved"],
+                                              a["xp"], a["wg"], a["wu"], a["act"], a["dx"],
+                                              a["dwg"], a["dwu"], a["ws"], a["wsb"], 0))
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(kw, saved=A[1] + 8) if "saved" in kw else kw, e) for kw, e in GATED] + [
+    (dict(g=0), "FLP_INVALID_ARGUMENT"),
+    (dict(saved=0), "FLP_INVALID_ARGUMENT"),
+    (dict(ws=0), "FLP_INVALID_ARGUMENT"),
+    (dict(xp=0), "FLP_INVALID_ARGUMENT"),                # the weight gradients need x
+    (dict(g=A[0] + 1), "FLP_MISALIGNED"),
+    (dict(dx=A[5] + 2), "FLP_MISALIGNED"),
+    (dict(dwu=A[7] + 8), "FLP_MISALIGNED"),
+    (dict(ws=A[8] + 8), "FLP_MISALIGNED"),
+    (dict(wsb=abi.flp_gated_linear_backward_workspace_bytes(N, D, F, BF16, 1, 0)),
+     "FLP_WORKSPACE_TOO_SMALL"),
+    (dict(dx=A[0]), "FLP_INVALID_ARGUMENT"),
+    (dict(dwu=A[6] + 64), "FLP_INVALID_ARGUMENT"),
+    (dict(ws=A[7] + 64), "FLP_INVALID_ARGUMENT"),
+    (dict(dx=0, dwg=0, dwu=0, ws=0, g=0), "FLP_OK"),     # nothing requested
+    (dict(N=0, g=0, saved=0, xp=0, dwg=0, dwu=0, ws=0, wsb=0), "FLP_OK"),
+])
+def test_gated_linear_backward_gates(kw, expect):
+    assert gated_bwd(**kw) == expect
+
+
+def test_gated_linear_sizes():
+    assert abi.flp_gated_linear_saved_bytes(40, 100, BF16) == 40 * 128 * 6
+    assert abi.flp_gated_linear_saved_bytes(40, 100, F32) == 40 * 128 * 8
+    assert abi.flp_gated_linear_saved_bytes(0, 100, BF16) == 0
+    size = abi.flp_gated_linear_backward_workspace_bytes
+    # [dz | du] and its transpose over 64 tokens, [Wg; Wu]^T, x^T
+    assert size(64, 64, 128, BF16, 1, 0) == 2 * 128 * 64 * 2 + 2 * 128 * 64 * 2
+    assert size(40, 64, 128, BF16, 0, 1) == 2 * 128 * 64 * 2 + 64 * 64 * 2
+    assert size(0, 64, 128, BF16, 1, 1) == 0
