@@ -1088,25 +1088,26 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
     g.ldo = D;
     g.k_slab = L.k_slab;
     if (L.k_slab > 0) g.acc = reinterpret_cast<float*>(at(workspace, L.slab_off));
-    if (launch_dx(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
+    if (launch_gated_dx(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
   }
   if (dw) {
     void* xt = at(workspace, L.xt_off);
     if (launch_transpose(x_dtype, x, N, L.np, D, D, xt, s) != hipSuccess) return FLP_HIP_ERROR;
-    for (int up = 0; up < 2; ++up) {
-      GemmArgs g{};
-      g.a = at(z.dzT, size_t(up) * L.fp * 128);
-      g.b = xt;
-      g.lda_b = g.ldb_b = 128;
-      g.a_ks = 2 * L.fp * 128;
-      g.b_ks = D * 128;
-      g.M = F;
-      g.N = D;
-      g.K = L.np;
-      g.out = up ? d_w_up : d_w_gate;
-      g.ldo = D;
-      if (g.out != nullptr && launch_dw(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
-    }
+    GemmArgs g{};
+    g.a = z.dzT;
+    g.b = xt;
+    g.lda_b = g.ldb_b = 128;
+    g.a_ks = 2 * L.fp * 128;
+    g.b_ks = D * 128;
+    g.M = 2 * L.fp;
+    g.N = D;
+    g.K = L.np;
+    g.ldo = D;
+    g.out = d_w_gate;
+    g.out2 = d_w_up;
+    g.split = L.fp;
+    g.rows_each = F;
+    if (launch_gated_dw(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
   }
   return FLP_OK;
 }

@@ -25,6 +25,7 @@
 
 #include "flp_chunk.h"
 #include "flp_engine.h"
+#include "flp_gemm.h"
 #include "flp_launch.h"
 
 namespace flp {
@@ -389,7 +390,65 @@ hipError_t dz_all(const GatedDzArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---- products of the backward -----------------------------------------------------------------
+//
+// The largest tile that gives most compute units a workgroup.  A chain over K is the same in
+// every tile, so the tile does not change the bits.
+
+template <class E>
+hipError_t dw_all(const GemmArgs& a, hipStream_t s) {
+  constexpr bool k16 = E::kSize == 2;
+  auto fills = [&](int64_t bm, int64_t bn) {
+    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn) >= 160;
+  };
+  if constexpr (k16) {
+    if (fills(256, 224)) return gemm_cfg<E, 256, 224, 4, 2, false, 0, 2, kGemmNSA, false, true>(a, s);
+  }
+  if (fills(128, 128)) return gemm_cfg<E, 128, 128, 2, 2, false, 0, k16 ? 3 : 2, k16 ? 3 : 2, false, true>(a, s);
+  if (fills(64, 64)) return gemm_cfg<E, 64, 64, 2, 2, false, 0, 4, 4, false, true>(a, s);
+  return gemm_cfg<E, 64, 32, 4, 1, false, 0, 8, 8, false, true>(a, s);
+}
+
+template <class E>
+hipError_t dx_all(const GemmArgs& a, hipStream_t s) {
+  constexpr bool k16 = E::kSize == 2;
+  if (a.k_slab == 0) {
+    if constexpr (k16) return gemm_cfg<E, 256, 224, 4, 2, false, 0, 2, kGemmNSA>(a, s);
+    return gemm_cfg<E, 128, 128, 2, 2, false, 0>(a, s);
+  }
+  const int64_t slabs = (a.K + a.k_slab - 1) / a.k_slab;
+  auto fills = [&](int64_t bm, int64_t bn) {
+    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn) * slabs >= 160;
+  };
+  hipError_t e;
+  if (k16 && a.M > 128 && fills(256, 224))
+    e = gemm_cfg<E, 256, k16 ? 224 : 128, 4, 2, false, 2, 2, k16 ? kGemmNSA : 2>(a, s);
+  else if (a.M > 64 && fills(128, 128))
+    e = gemm_cfg<E, 128, 128, 2, 2, false, 2, k16 ? 3 : 2>(a, s);
+  else if (a.M > 32 && fills(64, 64))
+    e = gemm_cfg<E, 64, 64, 2, 2, false, 2, 4>(a, s);
+  else
+    e = gemm_cfg<E, 64, 32, 4, 1, false, 2, 8>(a, s);
+  if (e != hipSuccess) return e;
+  const int64_t n = a.M * a.N;
+  hipLaunchKernelGGL(k_slab_fold<E>, dim3(unsigned(std::min<int64_t>((n + 1023) / 1024, 4096))),
+                     dim3(256), 0, s, a, int(slabs));
+  return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_gated_dx(flp_dtype x, const GemmArgs& a, hipStream_t s) {
+  ProfScope ps(FLP_K_DHIDDEN, s);
+  if (x == FLP_BF16) return dx_all<BF16>(a, s);
+  return x == FLP_F16 ? dx_all<F16>(a, s) : dx_all<F32>(a, s);
+}
+
+hipError_t launch_gated_dw(flp_dtype x, const GemmArgs& a, hipStream_t s) {
+  ProfScope ps(FLP_K_DWEIGHT, s);
+  if (x == FLP_BF16) return dw_all<BF16>(a, s);
+  return x == FLP_F16 ? dw_all<F16>(a, s) : dw_all<F32>(a, s);
+}
 
 hipError_t launch_gated_forward(flp_dtype x, const GatedFwdArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_GATED, s);

@@ -128,6 +128,8 @@ struct GemmArgs {
   int store_acc;         // store fp32 to acc (else store to out in x dtype)
   const float* scale = nullptr;  // fp16: factor of the rounded result, or null for 1
   int64_t k_slab = 0;    // d_hidden: > 0 sums K in slabs of this length, held in acc [slabs][M][N]
+  void* out2 = nullptr;  // two results in one (gated projection): the rows from split on
+  int64_t split = 0, rows_each = 0;
 };
 
 hipError_t launch_forward(flp_dtype x, const FwdArgs& a, hipStream_t s);
@@ -279,6 +281,8 @@ struct GatedDzArgs {
 };
 hipError_t launch_gated_forward(flp_dtype x, const GatedFwdArgs& a, hipStream_t s);
 hipError_t launch_gated_dz(flp_dtype x, const GatedDzArgs& a, hipStream_t s);
+hipError_t launch_gated_dx(flp_dtype x, const GemmArgs& a, hipStream_t s);
+hipError_t launch_gated_dw(flp_dtype x, const GemmArgs& a, hipStream_t s);
 
 // Root mean square norms around a block (flp_rms.hip).
 struct RmsFwdArgs {

@@ -883,9 +883,9 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need
   if (need_dx) {
     take(L.dz_off, size_t(K) * N * xs);
     take(L.wt_off, size_t(K) * D * xs);
-    const int64_t slabs = std::min<int64_t>(8, K / 1024);
+    const int64_t slabs = std::min<int64_t>(kGatedSlabs, K / 256);
     if (N <= kGatedSlabRows && slabs > 1) {
-      L.k_slab = round_up(ceil_div(K, slabs), 256);
+      L.k_slab = round_up(ceil_div(K, slabs), 128);
       take(L.slab_off, size_t(ceil_div(K, L.k_slab)) * N * D * 4);
     }
   }

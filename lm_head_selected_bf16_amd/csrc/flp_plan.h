@@ -158,9 +158,10 @@ constexpr int64_t kGatedPad = 64;  // columns and tokens of dz are padded to thi
 // A batch of up to kGatedSlabRows rows sums d_x over slabs of [dz | du]: its output tiles are too
 // few to fill the chip.
 constexpr int64_t kGatedSlabRows = 2048;
+constexpr int64_t kGatedSlabs = 8;
 struct GatedLayout {
   int64_t fp = 0, np = 0;    // F and N rounded up to kGatedPad
-  int64_t k_slab = 0;        // columns of a slab of d_x (a multiple of 256), 0: one walk
+  int64_t k_slab = 0;        // columns of a slab of d_x (a multiple of 128), 0: one walk
   size_t dz_off = 0, wt_off = 0, slab_off = 0;  // d_x: [dz | du], [Wg; Wu]^T, slab sums
   size_t dzt_off = 0, xt_off = 0;               // weight gradients: their transposes
   size_t total = 0;
