@@ -580,7 +580,7 @@ flp_status flp_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, cons
  *                and u act'(z) for the backward, in 24 bits each (fp32: 32) and a layout of
  *                their own; or NULL.
  *
- * Requirements: D % 32 == 0 (and the size limits of flp_forward), 1 <= F <= 64 * 65535,
+ * Requirements: D % 32 == 0 (and the size limits of flp_forward), 1 <= F <= 64 * 32767,
  * N <= 64 * 65535, N F below about 2^36.
  */
 typedef enum flp_activation {
@@ -602,13 +602,13 @@ flp_status flp_gated_linear_forward(int64_t N, int64_t D, int64_t F, flp_dtype x
  *   saved      as written by the forward for the same inputs.
  *   d_x [N, D], d_w_gate, d_w_up [F, D] x_dtype, 16-byte aligned: each may be NULL to skip it.
  *   workspace  >= flp_gated_linear_backward_workspace_bytes(N, D, F, x_dtype, d_x wanted, a
- *              weight gradient wanted), 16-byte aligned: dz and du in the layouts of the two
- *              products (4 N F elements), and the weights and x transposed.
+ *              weight gradient wanted), 16-byte aligned: dz and du (2 N F elements; fp32: also
+ *              transposed, with the weights and x), and fp32 sums over slabs of small products.
  *
  * For 16-bit types dz and du are rounded to x_dtype on the way, whose matrix instructions take
- * operands of that type; the products' sums are fp32 and rounded once.  The sums run in an order fixed by the sizes; d_x of a row is bitwise
- * the same among batches of up to 2048 rows, and among larger ones.  N = 0 writes zeros to
- * d_w_gate and d_w_up.
+ * operands of that type; the products' sums are fp32 and rounded once.  They run in an order
+ * fixed by the sizes; d_x of a row is bitwise the same among batches of up to 2048 rows, among
+ * those of up to 8192 and among larger ones.  N = 0 writes zeros to d_w_gate and d_w_up.
  */
 size_t flp_gated_linear_backward_workspace_bytes(int64_t N, int64_t D, int64_t F,
                                                  flp_dtype x_dtype, int need_d_x,

@@ -1066,9 +1066,37 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
   z.grad = grad_out;
   z.saved = saved;
   z.ld_saved = L.fp;
-  z.dz = d_x ? at(workspace, L.dz_off) : nullptr;
-  z.dzT = dw ? at(workspace, L.dzt_off) : nullptr;
+  z.ldz = L.ldz;
+  const bool wide = x_dtype == FLP_F32;
+  float* acc = reinterpret_cast<float*>(at(workspace, L.acc_off));
+  z.dz = d_x || !wide ? at(workspace, L.dz_off) : nullptr;
+  z.dzT = dw && wide ? at(workspace, L.dzt_off) : nullptr;
   if (launch_gated_dz(x_dtype, z, s) != hipSuccess) return FLP_HIP_ERROR;
+  if (!wide) {
+    GatedGemmArgs g{};
+    g.dz = z.dz;
+    g.rows = N;
+    g.fp = L.fp;
+    g.ldz = L.ldz;
+    g.F = F;
+    g.D = D;
+    g.w_gate = w_gate;
+    g.w_up = w_up;
+    g.x = x;
+    g.acc = acc;
+    if (d_x != nullptr) {
+      g.out = d_x;
+      g.slab = L.dx_slab;
+      if (launch_gated_dx16(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
+    }
+    if (dw) {
+      g.out = d_w_gate;
+      g.out2 = d_w_up;
+      g.slab = L.dw_slab;
+      if (launch_gated_dw16(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
+    }
+    return FLP_OK;
+  }
   if (d_x != nullptr) {
     void* wt = at(workspace, L.wt_off);
     void* wt_up = at(wt, size_t(L.fp) * D * xs);
@@ -1086,9 +1114,9 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
     g.K = 2 * L.fp;
     g.out = d_x;
     g.ldo = D;
-    g.k_slab = L.k_slab;
-    if (L.k_slab > 0) g.acc = reinterpret_cast<float*>(at(workspace, L.slab_off));
-    if (launch_gated_dx(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
+    g.k_slab = L.dx_slab;
+    g.acc = acc;
+    if (launch_gated_dx(g, s) != hipSuccess) return FLP_HIP_ERROR;
   }
   if (dw) {
     void* xt = at(workspace, L.xt_off);
@@ -1107,7 +1135,7 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
     g.out2 = d_w_up;
     g.split = L.fp;
     g.rows_each = F;
-    if (launch_gated_dw(x_dtype, g, s) != hipSuccess) return FLP_HIP_ERROR;
+    if (launch_gated_dw(g, s) != hipSuccess) return FLP_HIP_ERROR;
   }
   return FLP_OK;
 }

@@ -11,9 +11,10 @@
 // last 8): kept in 16, their roundings make the gradients' error 3.1e-3 where the rounding of
 // dz, du and the result alone gives 2.4e-3.
 //
-// Backward: dz and du side by side, once K-blocked by columns (the A operand of d_x, against
-// [Wg; Wu]^T) and once by tokens (that of the weight gradients, against x^T), and two
-// products.  Their rounding to the element type is what the matrix instructions take.
+// Backward: dz and du side by side, rounded to the element type that the matrix instructions
+// take, and two products, d_x = [dz | du] [Wg; Wu] and [d_Wg; d_Wu] = [dz | du]^T x.  The
+// 16-bit ones read every operand as it lies and turn it on the way from LDS to the registers
+// (flp_tr.h); the fp32 ones take transposed copies, which cost little beside their products.
 //
 // Bound by the matrix instructions for many rows, by reading the weights for few.
 #include <hip/hip_runtime.h>
@@ -27,6 +28,7 @@
 #include "flp_engine.h"
 #include "flp_gemm.h"
 #include "flp_launch.h"
+#include "flp_tr.h"
 
 namespace flp {
 namespace {
@@ -64,19 +66,20 @@ __device__ __forceinline__ float act_slope(float z, float f) {
 template <class E>
 struct Kept {
   static constexpr int kBytes = E::kSize == 2 ? 24 : 32;
-  // to 24 bits, to nearest; an infinity or NaN only loses bits that do not make it
-  __device__ __forceinline__ static uint32_t round24(float v) {
-    const uint32_t b = __float_as_uint(v);
-    return (b & 0x7F800000u) == 0x7F800000u ? b : b + 0x80u;
-  }
   struct Packed {
     uint32_t h0, h1, lo;
   };
+  // Four values to 24 bits, to nearest: half a step is added and the rest cut off.  Infinities
+  // stay, and so do NaN, whose last bits are zeros (they come from 16-bit operands or are the
+  // instructions' own).
   __device__ __forceinline__ static Packed pack(const f32x4_t& v) {
-    const uint32_t b0 = round24(v.x), b1 = round24(v.y), b2 = round24(v.z), b3 = round24(v.w);
-    return {(b0 >> 16) | (b1 & 0xFFFF0000u), (b2 >> 16) | (b3 & 0xFFFF0000u),
-            ((b0 >> 8) & 0xFFu) | (b1 & 0xFF00u) | ((b2 << 8) & 0xFF0000u) |
-                ((b3 << 16) & 0xFF000000u)};
+    uint32_t b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(v[e]) + 0x80u;
+    return {__builtin_amdgcn_perm(b[1], b[0], 0x07060302u),
+            __builtin_amdgcn_perm(b[3], b[2], 0x07060302u),
+            __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0501u) |
+                __builtin_amdgcn_perm(b[3], b[2], 0x05010C0Cu)};
   }
   __device__ __forceinline__ static void store(char* p, const f32x4_t& a, const f32x4_t& b) {
     typedef u32x4 loose16 __attribute__((aligned(8)));
@@ -238,12 +241,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gated_fwd(GatedFwdArgs p) {
 }
 
 // ---- dz and du, for both products -------------------------------------------------------------
-//
-// A workgroup takes 64 tokens x 64 columns: whole rows in, and out of LDS the same tile by
-// columns (dz: the K of d_x) and by tokens (dzT), each a contiguous K-blocked piece.  The K
-// positions of 16-bit operands take the order of launch_transpose, whose results they meet:
-// position 32 b + 8 g + 4 h + r holds column (token) 32 b + 16 h + 4 g + r.
-// Columns past F and tokens past N are zeros.
+
 template <class E>
 struct Elem;
 template <>
@@ -259,85 +257,175 @@ struct Elem<F32> {
   using T = float;
 };
 
+// dz and du of eight columns of a row, zeros from the nth on.
+template <class E>
+__device__ __forceinline__ void dz_of(const GatedDzArgs& p, int64_t row, int64_t col, int64_t n,
+                                      float (&dz)[kChunk], float (&du)[kChunk]) {
+  using T = typename Elem<E>::T;
+  Chunk<T> gr;
+  gr.load(static_cast<const T*>(p.grad) + row * p.F + col, n);
+  float a[kChunk], b[kChunk];
+  if (n > 0)
+    Kept<E>::load8(static_cast<const char*>(p.saved) + (row * p.ld_saved + col) / 4 * Kept<E>::kBytes,
+                   a, b);
+#pragma unroll
+  for (int e = 0; e < kChunk; ++e) {
+    const float g = float(T(gr.v[e]));
+    dz[e] = e < n ? g * b[e] : 0.f;
+    du[e] = e < n ? g * a[e] : 0.f;
+  }
+}
+
+// 16-bit types: [dz | du] as rows, one wave per 512 columns of a row.  Columns past F are zeros.
 template <class E>
 __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
-  using T = typename Elem<E>::T;
-  constexpr bool k16 = E::kSize == 2;
-  constexpr int kPitch = k16 ? 33 : 65;  // words of a tile row
-  __shared__ uint32_t tile[2][64][kPitch];
+  const int64_t col = int64_t(blockIdx.x) * 512 + (threadIdx.x & 63) * kChunk;
+  if (col >= p.ld_saved) return;
+  const int64_t n = p.F - col;
+  for (int64_t row = int64_t(blockIdx.y) * 4 + (threadIdx.x >> 6); row < p.N;
+       row += int64_t(gridDim.y) * 4) {
+    float dz[kChunk], du[kChunk];
+    dz_of<E>(p, row, col, n, dz, du);
+    uint16_t* out = static_cast<uint16_t*>(p.dz) + row * p.ldz + col;
+    *reinterpret_cast<u32x4*>(out) = u32x4{pack2<E>(dz[0], dz[1]), pack2<E>(dz[2], dz[3]),
+                                           pack2<E>(dz[4], dz[5]), pack2<E>(dz[6], dz[7])};
+    *reinterpret_cast<u32x4*>(out + p.ld_saved) =
+        u32x4{pack2<E>(du[0], du[1]), pack2<E>(du[2], du[3]), pack2<E>(du[4], du[5]),
+              pack2<E>(du[6], du[7])};
+  }
+}
+
+// fp32, whose products take K-blocked operands: a workgroup takes 64 tokens x 64 columns, whole
+// rows in, and out of LDS the same tile by columns (dz: the K of d_x) and by tokens (dzT), each a
+// contiguous K-blocked piece.  Columns past F and tokens past N are zeros.
+__global__ __launch_bounds__(256) void k_gated_dz32(GatedDzArgs p) {
+  __shared__ float tile[2][64][65];
   const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
   const int t = threadIdx.x;
-  {
-    const int rl = t >> 2, seg = (t & 3) * 16;
-    const int64_t row = r0 + rl;
+  const int rl = t >> 2;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int cl = seg + half * 8;
-      const int64_t n = row < p.N ? p.F - (c0 + cl) : 0;
-      Chunk<T> gr;
-      gr.load(static_cast<const T*>(p.grad) + row * p.F + c0 + cl, n);
-      float a[kChunk], b[kChunk], dz[kChunk], du[kChunk];
-      if (n > 0)
-        Kept<E>::load8(static_cast<const char*>(p.saved) +
-                           (row * p.ld_saved + c0 + cl) / 4 * Kept<E>::kBytes,
-                       a, b);
+  for (int half = 0; half < 2; ++half) {
+    const int cl = (t & 3) * 16 + half * 8;
+    float dz[kChunk], du[kChunk];
+    dz_of<F32>(p, r0 + rl, c0 + cl, r0 + rl < p.N ? p.F - (c0 + cl) : 0, dz, du);
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) {
-        const float g = float(T(gr.v[e]));
-        dz[e] = e < n ? g * b[e] : 0.f;
-        du[e] = e < n ? g * a[e] : 0.f;
-      }
-      if constexpr (k16) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          tile[0][rl][cl / 2 + e] = pack2<E>(dz[2 * e], dz[2 * e + 1]);
-          tile[1][rl][cl / 2 + e] = pack2<E>(du[2 * e], du[2 * e + 1]);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-          tile[0][rl][cl + e] = __float_as_uint(dz[e]);
-          tile[1][rl][cl + e] = __float_as_uint(du[e]);
-        }
-      }
+    for (int e = 0; e < kChunk; ++e) {
+      tile[0][rl][cl + e] = dz[e];
+      tile[1][rl][cl + e] = du[e];
     }
   }
   __syncthreads();
   const int64_t rows_t = 2 * p.ld_saved;
+  float* const dz = static_cast<float*>(p.dz);
+  float* const dzT = static_cast<float*>(p.dzT);
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const int64_t k0 = c0 + m * p.ld_saved;  // column of [dz | du], row of its transpose
-    if constexpr (k16) {
-      uint16_t* const dz = static_cast<uint16_t*>(p.dz);
-      uint16_t* const dzT = static_cast<uint16_t*>(p.dzT);
 #pragma unroll
-      for (int pass = 0; pass < 2; ++pass) {
-        const int rl = (t >> 3) + 32 * pass, j = t & 7;
-        const int from = 32 * (j >> 2) + 4 * (j & 3);
-        if (dz != nullptr && r0 + rl < p.N) {
-          const uint32_t* w = tile[m][rl] + from / 2;
-          *reinterpret_cast<u32x4*>(dz + kblk<64>(r0 + rl, k0 + 8 * j, p.N)) =
-              u32x4{w[0], w[1], w[8], w[9]};
-        }
-        if (dzT != nullptr) {
-          uint32_t h[8];
+    for (int pass = 0; pass < 16; ++pass) {
+      const int a = (t >> 6) + 4 * pass, b = t & 63;
+      if (dz != nullptr && r0 + a < p.N) dz[kblk<32>(r0 + a, k0 + b, p.N)] = tile[m][a][b];
+      if (dzT != nullptr) dzT[kblk<32>(k0 + a, r0 + b, rows_t)] = tile[m][b][a];
+    }
+  }
+}
+
+// ---- 16-bit products of the backward -------------------------------------------------------------
+//
+// d_x = [dz | du] [Wg; Wu] (turned B), [d_Wg; d_Wu] = [dz | du]^T x (both turned: TURNED), over
+// all of K or, in the grid's second dimension, over slabs of it whose fp32 sums go to p.acc.
+template <class E, bool TURNED, int BM, int BN, int WM, int WN, bool SLABS>
+__global__ __launch_bounds__(64 * WM * WN) void k_gated_gemm(GatedGemmArgs p) {
+  constexpr int NW = WM * WN, RW = BM / WM, CW = BN / WN, NA = RW / 16, NB = CW / 16;
+  using OpA = std::conditional_t<TURNED, TurnedOp<BM, NW, NA, false>, PlainOp<BM, NW, NA>>;
+  using OpB = TurnedOp<BN, NW, NB, !TURNED>;
+  using Ring = TrRing<E, OpA, OpB, NA, NB, NW>;
+  extern __shared__ u32x4 smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % WM, wn = wave / WM, i = lane & 15, g = lane >> 4;
+  const int64_t M = TURNED ? 2 * p.fp : p.rows, K = TURNED ? p.rows : 2 * p.fp;
+  const int nbm = int((M + BM - 1) / BM), nbn = int((p.D + BN - 1) / BN);
+  int tm, tn;
+  tile_of<1>(blockIdx.x, nbm, nbn, tm, tn);
+  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
+  const int64_t k0 = SLABS ? int64_t(blockIdx.y) * p.slab : 0;
+  const int64_t kn = SLABS ? min(p.slab, K - k0) : K;
+  OpA a;
+  OpB b;
+  const char* const dz = static_cast<const char*>(p.dz);
+  const char* const x = static_cast<const char*>(p.x);
+  if constexpr (TURNED) {
+    a.init(dz, dz, 0, p.rows, 2 * p.ldz, m0, M, k0, lane, wave, wm * NA);
+    b.init(x, x, 0, p.rows, 2 * p.D, n0, p.D, k0, lane, wave, wn * NB);
+  } else {
+    a.init(dz + m0 * 2 * p.ldz + k0 * 2, 2 * p.ldz, M - m0, lane, wm * RW);
+    b.init(static_cast<const char*>(p.w_gate), static_cast<const char*>(p.w_up), p.fp, p.F, 2 * p.D,
+           n0, p.D, k0, lane, wave, wn * NB);
+  }
+  f32x4_t acc[NA][NB];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            h[k] = (tile[m][from + 16 * (k >> 2) + (k & 3)][rl >> 1] >> (16 * (rl & 1))) & 0xFFFFu;
-          *reinterpret_cast<u32x4*>(dzT + kblk<64>(k0 + rl, r0 + 8 * j, rows_t)) =
-              u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
-                    h[6] | (h[7] << 16)};
-        }
+  for (int mb = 0; mb < NA; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  Ring::run(acc, a, b, int((kn + kTrRows - 1) / kTrRows), smem, wave);
+  if constexpr (SLABS) {
+#pragma unroll
+    for (int mb = 0; mb < NA; ++mb) {
+      const int64_t m = m0 + wm * RW + mb * 16 + i;
+      if (m >= M) continue;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int64_t n = n0 + wn * CW + nb * 16 + 4 * g;
+        if (n < p.D)
+          *reinterpret_cast<f32x4_t*>(p.acc + (int64_t(blockIdx.y) * M + m) * p.D + n) = acc[mb][nb];
       }
+    }
+  } else {
+    // The tile is staged in the ring (rows of BN values plus 16 bytes) and written as 16-byte
+    // chunks of whole rows; D is a multiple of 32, so every chunk lies inside one row.
+    constexpr int kRowB = BN * 2 + 16, kCh = BN * 2 / 16;
+    static_assert(size_t(BM) * kRowB <= Ring::kLds, "the staged tile fits the ring");
+    char* lds = reinterpret_cast<char*>(smem);
+    __syncthreads();  // every wave is done reading the ring
+#pragma unroll
+    for (int mb = 0; mb < NA; ++mb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int rl = wm * RW + mb * 16 + i, cl = wn * CW + nb * 16 + 4 * g;
+        *reinterpret_cast<u32x2*>(lds + rl * kRowB + cl * 2) =
+            u32x2{pack2<E>(acc[mb][nb][0], acc[mb][nb][1]), pack2<E>(acc[mb][nb][2], acc[mb][nb][3])};
+      }
+    __syncthreads();
+    for (int idx = tid; idx < BM * kCh; idx += 64 * NW) {
+      const int rl = idx / kCh, ch = idx - rl * kCh;
+      const int64_t m = m0 + rl, n = n0 + ch * 8;
+      const bool up = TURNED && m >= p.fp;
+      const int64_t mo = up ? m - p.fp : m;
+      uint16_t* const out = static_cast<uint16_t*>(up ? p.out2 : p.out);
+      if (mo < (TURNED ? p.F : M) && n < p.D && out != nullptr)
+        *reinterpret_cast<u32x4*>(out + mo * p.D + n) =
+            *reinterpret_cast<const u32x4*>(lds + rl * kRowB + ch * 16);
+    }
+  }
+}
+
+// The slabs' fp32 sums added in ascending order and rounded once.
+template <class E, bool TURNED>
+__global__ __launch_bounds__(256) void k_gated_fold(GatedGemmArgs p, int slabs) {
+  const int64_t M = TURNED ? 2 * p.fp : p.rows, n = M * p.D;  // a multiple of 32
+  for (int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
+       i += int64_t(gridDim.x) * 1024) {
+    f32x4_t s = *reinterpret_cast<const f32x4_t*>(p.acc + i);
+    for (int k = 1; k < slabs; ++k) s += *reinterpret_cast<const f32x4_t*>(p.acc + k * n + i);
+    if constexpr (TURNED) {
+      const int64_t half = p.fp * p.D;
+      const bool up = i >= half;
+      const int64_t at = up ? i - half : i;
+      void* const out = up ? p.out2 : p.out;
+      if (at < p.F * p.D && out != nullptr) store4<E>(out, at, s);
     } else {
-      uint32_t* const dz = static_cast<uint32_t*>(p.dz);
-      uint32_t* const dzT = static_cast<uint32_t*>(p.dzT);
-#pragma unroll
-      for (int pass = 0; pass < 16; ++pass) {
-        const int a = (t >> 6) + 4 * pass, b = t & 63;
-        if (dz != nullptr && r0 + a < p.N) dz[kblk<32>(r0 + a, k0 + b, p.N)] = tile[m][a][b];
-        if (dzT != nullptr) dzT[kblk<32>(k0 + a, r0 + b, rows_t)] = tile[m][b][a];
-      }
+      store4<E>(p.out, i, s);
     }
   }
 }
@@ -383,71 +471,91 @@ hipError_t fwd_all(const GatedFwdArgs& a, hipStream_t s) {
   return odd ? fwd_rows<E, true>(a, s) : fwd_rows<E, false>(a, s);
 }
 
-template <class E>
-hipError_t dz_all(const GatedDzArgs& a, hipStream_t s) {
-  const dim3 grid(unsigned(a.ld_saved / 64), unsigned((a.N + 63) / 64));
-  hipLaunchKernelGGL(k_gated_dz<E>, grid, dim3(256), 0, s, a);
+template <class E, bool TURNED, int BM, int BN, int WM, int WN, bool SLABS>
+hipError_t gemm16_cfg(const GatedGemmArgs& a, int64_t slabs, hipStream_t s) {
+  constexpr int NW = WM * WN, NA = BM / WM / 16, NB = BN / WN / 16;
+  using OpA = std::conditional_t<TURNED, TurnedOp<BM, NW, NA, false>, PlainOp<BM, NW, NA>>;
+  constexpr size_t kLds = TrRing<E, OpA, TurnedOp<BN, NW, NB, !TURNED>, NA, NB, NW>::kLds;
+  static std::atomic<int> ready[kMaxDevices];
+  const hipError_t e = prepare(k_gated_gemm<E, TURNED, BM, BN, WM, WN, SLABS>, kLds, ready);
+  if (e != hipSuccess) return e;
+  const int64_t M = TURNED ? 2 * a.fp : a.rows;
+  const int64_t blocks = ((M + BM - 1) / BM) * ((a.D + BN - 1) / BN);
+  hipLaunchKernelGGL((k_gated_gemm<E, TURNED, BM, BN, WM, WN, SLABS>),
+                     dim3(unsigned(blocks), unsigned(slabs)), dim3(64 * NW), kLds, s, a);
   return hipGetLastError();
 }
 
-// ---- products of the backward -----------------------------------------------------------------
-//
-// The largest tile that gives most compute units a workgroup.  A chain over K is the same in
-// every tile, so the tile does not change the bits.
-
-template <class E>
-hipError_t dw_all(const GemmArgs& a, hipStream_t s) {
-  constexpr bool k16 = E::kSize == 2;
-  auto fills = [&](int64_t bm, int64_t bn) {
-    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn) >= 160;
-  };
-  if constexpr (k16) {
-    if (fills(256, 224)) return gemm_cfg<E, 256, 224, 4, 2, false, 0, 2, kGemmNSA, false, true>(a, s);
-  }
-  if (fills(128, 128)) return gemm_cfg<E, 128, 128, 2, 2, false, 0, k16 ? 3 : 2, k16 ? 3 : 2, false, true>(a, s);
-  if (fills(64, 64)) return gemm_cfg<E, 64, 64, 2, 2, false, 0, 4, 4, false, true>(a, s);
-  return gemm_cfg<E, 64, 32, 4, 1, false, 0, 8, 8, false, true>(a, s);
+// The larger tile where it gives most compute units a workgroup (a chain over K is the same in
+// both, so the tile does not change the bits).
+template <class E, bool TURNED>
+hipError_t gemm16(const GatedGemmArgs& a, hipStream_t s) {
+  const int64_t M = TURNED ? 2 * a.fp : a.rows, K = TURNED ? a.rows : 2 * a.fp;
+  const int64_t slabs = a.slab > 0 ? (K + a.slab - 1) / a.slab : 1;
+  const bool large = M > 128 && ((M + 255) / 256) * ((a.D + 223) / 224) * slabs >= kGatedTiles;
+  if (slabs == 1)
+    return large ? gemm16_cfg<E, TURNED, 256, 224, 4, 2, false>(a, 1, s)
+                 : gemm16_cfg<E, TURNED, 128, 128, 2, 2, false>(a, 1, s);
+  const hipError_t e = large ? gemm16_cfg<E, TURNED, 256, 224, 4, 2, true>(a, slabs, s)
+                             : gemm16_cfg<E, TURNED, 128, 128, 2, 2, true>(a, slabs, s);
+  if (e != hipSuccess) return e;
+  const int64_t n = M * a.D;
+  hipLaunchKernelGGL((k_gated_fold<E, TURNED>),
+                     dim3(unsigned(std::min<int64_t>((n + 1023) / 1024, 4096))), dim3(256), 0, s, a,
+                     int(slabs));
+  return hipGetLastError();
 }
 
 template <class E>
-hipError_t dx_all(const GemmArgs& a, hipStream_t s) {
-  constexpr bool k16 = E::kSize == 2;
-  if (a.k_slab == 0) {
-    if constexpr (k16) return gemm_cfg<E, 256, 224, 4, 2, false, 0, 2, kGemmNSA>(a, s);
-    return gemm_cfg<E, 128, 128, 2, 2, false, 0>(a, s);
-  }
-  const int64_t slabs = (a.K + a.k_slab - 1) / a.k_slab;
-  auto fills = [&](int64_t bm, int64_t bn) {
-    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn) * slabs >= 160;
-  };
-  hipError_t e;
-  if (k16 && a.M > 128 && fills(256, 224))
-    e = gemm_cfg<E, 256, k16 ? 224 : 128, 4, 2, false, 2, 2, k16 ? kGemmNSA : 2>(a, s);
-  else if (a.M > 64 && fills(128, 128))
-    e = gemm_cfg<E, 128, 128, 2, 2, false, 2, k16 ? 3 : 2>(a, s);
-  else if (a.M > 32 && fills(64, 64))
-    e = gemm_cfg<E, 64, 64, 2, 2, false, 2, 4>(a, s);
-  else
-    e = gemm_cfg<E, 64, 32, 4, 1, false, 2, 8>(a, s);
-  if (e != hipSuccess) return e;
-  const int64_t n = a.M * a.N;
-  hipLaunchKernelGGL(k_slab_fold<E>, dim3(unsigned(std::min<int64_t>((n + 1023) / 1024, 4096))),
-                     dim3(256), 0, s, a, int(slabs));
+hipError_t dz16(const GatedDzArgs& a, hipStream_t s) {
+  const dim3 grid(unsigned((a.ld_saved + 511) / 512),
+                  unsigned(std::min<int64_t>((a.N + 3) / 4, 65535)));
+  hipLaunchKernelGGL(k_gated_dz<E>, grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gated_dx(flp_dtype x, const GemmArgs& a, hipStream_t s) {
+hipError_t launch_gated_dx16(flp_dtype x, const GatedGemmArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_DHIDDEN, s);
-  if (x == FLP_BF16) return dx_all<BF16>(a, s);
-  return x == FLP_F16 ? dx_all<F16>(a, s) : dx_all<F32>(a, s);
+  return x == FLP_BF16 ? gemm16<BF16, false>(a, s) : gemm16<F16, false>(a, s);
 }
 
-hipError_t launch_gated_dw(flp_dtype x, const GemmArgs& a, hipStream_t s) {
+hipError_t launch_gated_dw16(flp_dtype x, const GatedGemmArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_DWEIGHT, s);
-  if (x == FLP_BF16) return dw_all<BF16>(a, s);
-  return x == FLP_F16 ? dw_all<F16>(a, s) : dw_all<F32>(a, s);
+  return x == FLP_BF16 ? gemm16<BF16, true>(a, s) : gemm16<F16, true>(a, s);
+}
+
+// fp32: the largest tile that gives most compute units a workgroup.
+hipError_t launch_gated_dw(const GemmArgs& a, hipStream_t s) {
+  ProfScope ps(FLP_K_DWEIGHT, s);
+  auto fills = [&](int64_t bm, int64_t bn) {
+    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn) >= kGatedTiles;
+  };
+  if (fills(128, 128)) return gemm_cfg<F32, 128, 128, 2, 2, false, 0, 2, 2, false, true>(a, s);
+  if (fills(64, 64)) return gemm_cfg<F32, 64, 64, 2, 2, false, 0, 4, 4, false, true>(a, s);
+  return gemm_cfg<F32, 64, 32, 4, 1, false, 0, 8, 8, false, true>(a, s);
+}
+
+hipError_t launch_gated_dx(const GemmArgs& a, hipStream_t s) {
+  ProfScope ps(FLP_K_DHIDDEN, s);
+  if (a.k_slab == 0) return gemm_cfg<F32, 128, 128, 2, 2, false, 0>(a, s);
+  const int64_t slabs = (a.K + a.k_slab - 1) / a.k_slab;
+  auto fills = [&](int64_t bm, int64_t bn) {
+    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn) * slabs >= kGatedTiles;
+  };
+  hipError_t e;
+  if (a.M > 64 && fills(128, 128))
+    e = gemm_cfg<F32, 128, 128, 2, 2, false, 2, 2>(a, s);
+  else if (a.M > 32 && fills(64, 64))
+    e = gemm_cfg<F32, 64, 64, 2, 2, false, 2, 4>(a, s);
+  else
+    e = gemm_cfg<F32, 64, 32, 4, 1, false, 2, 8>(a, s);
+  if (e != hipSuccess) return e;
+  const int64_t n = a.M * a.N;
+  hipLaunchKernelGGL(k_slab_fold<F32>, dim3(unsigned(std::min<int64_t>((n + 1023) / 1024, 4096))),
+                     dim3(256), 0, s, a, int(slabs));
+  return hipGetLastError();
 }
 
 hipError_t launch_gated_forward(flp_dtype x, const GatedFwdArgs& a, hipStream_t s) {
@@ -458,8 +566,11 @@ hipError_t launch_gated_forward(flp_dtype x, const GatedFwdArgs& a, hipStream_t 
 
 hipError_t launch_gated_dz(flp_dtype x, const GatedDzArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_GATED, s);
-  if (x == FLP_BF16) return dz_all<BF16>(a, s);
-  return x == FLP_F16 ? dz_all<F16>(a, s) : dz_all<F32>(a, s);
+  if (x == FLP_BF16) return dz16<BF16>(a, s);
+  if (x == FLP_F16) return dz16<F16>(a, s);
+  const dim3 grid(unsigned(a.ld_saved / 64), unsigned((a.N + 63) / 64));
+  hipLaunchKernelGGL(k_gated_dz32, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace flp

@@ -276,13 +276,29 @@ struct GatedDzArgs {
   const void* grad;          // [N][F]
   const void* saved;         // as above
   int64_t ld_saved;
-  void* dz;                  // K-blocked: N rows, K = 2 ld_saved (dz, du), or null
-  void* dzT;                 // K-blocked: 2 ld_saved rows, K = N rounded up to 64, or null
+  int64_t ldz;               // 16 bits: elements from row to row of dz
+  void* dz;                  // [N][ldz] dz, then du from ld_saved on; fp32: K-blocked (or null)
+  void* dzT;                 // fp32 only, K-blocked: 2 ld_saved rows, K = N rounded up to 64, or null
 };
 hipError_t launch_gated_forward(flp_dtype x, const GatedFwdArgs& a, hipStream_t s);
 hipError_t launch_gated_dz(flp_dtype x, const GatedDzArgs& a, hipStream_t s);
-hipError_t launch_gated_dx(flp_dtype x, const GemmArgs& a, hipStream_t s);
-hipError_t launch_gated_dw(flp_dtype x, const GemmArgs& a, hipStream_t s);
+// fp32: the products from K-blocked operands.
+hipError_t launch_gated_dx(const GemmArgs& a, hipStream_t s);
+hipError_t launch_gated_dw(const GemmArgs& a, hipStream_t s);
+// 16 bits: the same from operands as they lie.
+struct GatedGemmArgs {
+  const void* dz;            // [rows][ldz], 2 fp columns
+  int64_t rows, fp, ldz, F, D;
+  const void* w_gate;        // [F][D], for d_x
+  const void* w_up;
+  const void* x;             // [rows][D], for the weight gradients
+  void* out;                 // d_x [rows][D], or d_w_gate [F][D] or null
+  void* out2;                // d_w_up or null
+  int64_t slab;              // columns (rows) of dz per slab, 0: one walk
+  float* acc;                // [slabs][rows or 2 fp][D]
+};
+hipError_t launch_gated_dx16(flp_dtype x, const GatedGemmArgs& a, hipStream_t s);
+hipError_t launch_gated_dw16(flp_dtype x, const GatedGemmArgs& a, hipStream_t s);
 
 // Root mean square norms around a block (flp_rms.hip).
 struct RmsFwdArgs {

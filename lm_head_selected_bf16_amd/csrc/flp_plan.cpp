@@ -872,6 +872,7 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need
                          bool need_dw) {
   GatedLayout L;
   const size_t xs = dtype_size(x);
+  const bool wide = x == FLP_F32;
   L.fp = round_up(F, kGatedPad);
   L.np = round_up(N, kGatedPad);
   const int64_t K = 2 * L.fp;
@@ -880,19 +881,32 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need
     off = at;
     at += align_up(bytes);
   };
-  if (need_dx) {
-    take(L.dz_off, size_t(K) * N * xs);
-    take(L.wt_off, size_t(K) * D * xs);
-    const int64_t slabs = std::min<int64_t>(kGatedSlabs, K / 256);
-    if (N <= kGatedSlabRows && slabs > 1) {
-      L.k_slab = round_up(ceil_div(K, slabs), 128);
-      take(L.slab_off, size_t(ceil_div(K, L.k_slab)) * N * D * 4);
-    }
-  }
-  if (need_dw) {
+  auto slab_of = [&](int64_t k, int64_t slabs) {  // of at least 256
+    slabs = std::min({slabs, kGatedSlabs, k / 256});
+    return slabs > 1 ? round_up(ceil_div(k, slabs), 128) : 0;
+  };
+  // 128 bytes past a multiple of 256, or else the rows of a tile would meet in few of the L2's
+  // channels (F = 7168, whose rows are 7 * 4096 bytes apart: products a third slower)
+  L.ldz = K + (wide ? 0 : kGatedPad);
+  if (need_dx || !wide) take(L.dz_off, size_t(L.ldz) * N * xs);
+  if (wide && need_dx) take(L.wt_off, size_t(K) * D * xs);
+  if (wide && need_dw) {
     take(L.dzt_off, size_t(K) * L.np * xs);
     take(L.xt_off, size_t(D) * L.np * xs);
   }
+  size_t acc = 0;
+  if (need_dx) {
+    // as many slabs as the smallest batch of the size needs
+    const int64_t least = N <= kGatedRowsSmall ? 1 : N <= kGatedRowsMiddle ? kGatedRowsSmall
+                                                                            : kGatedRowsMiddle;
+    L.dx_slab = slab_of(K, ceil_div(kGatedTiles * 128 * 128, least * D));
+    if (L.dx_slab > 0) acc = size_t(ceil_div(K, L.dx_slab)) * N * D * 4;
+  }
+  if (need_dw && !wide) {
+    L.dw_slab = slab_of(L.np, kGatedTiles / std::max<int64_t>(ceil_div(K, 128) * ceil_div(D, 128), 1));
+    if (L.dw_slab > 0) acc = std::max(acc, size_t(ceil_div(L.np, L.dw_slab)) * K * D * 4);
+  }
+  take(L.acc_off, acc);
   L.total = at;
   return L;
 }
@@ -904,9 +918,10 @@ flp_status check_gated(int64_t N, int64_t D, int64_t F, flp_dtype x, flp_activat
   if (st != FLP_OK) return st;
   if (act != FLP_ACT_SILU && act != FLP_ACT_GELU && act != FLP_ACT_GELU_TANH)
     return FLP_INVALID_ARGUMENT;
-  // a launch's second grid dimension counts 64 tokens or weight rows, and a launch holds fewer
-  // than 2^32 threads (256 for 64 x 64 elements of dz)
-  if (N > int64_t(65535) * 64 || F > int64_t(65535) * 64) return FLP_UNSUPPORTED_SHAPE;
+  // a launch's second grid dimension counts 64 tokens or weight rows, 256 rows of dz (of 2 F
+  // elements) stay below 2^31 bytes, and a launch holds fewer than 2^32 threads (256 for 64 x 64
+  // elements of dz)
+  if (N > int64_t(65535) * 64 || F > int64_t(32767) * 64) return FLP_UNSUPPORTED_SHAPE;
   if (ceil_div(N, 64) * ceil_div(F, 64) >= (int64_t(1) << 24)) return FLP_UNSUPPORTED_SHAPE;
   return FLP_OK;
 }

@@ -154,16 +154,19 @@ NormLayout norm_layout(int64_t N, int64_t D);
 inline uint32_t dropout_threshold(double p) { return uint32_t(p * 65536.0 + 0.5); }
 
 // ---- gated projection backward ----
-constexpr int64_t kGatedPad = 64;  // columns and tokens of dz are padded to this with zeros
-// A batch of up to kGatedSlabRows rows sums d_x over slabs of [dz | du]: its output tiles are too
-// few to fill the chip.
-constexpr int64_t kGatedSlabRows = 2048;
-constexpr int64_t kGatedSlabs = 8;
+constexpr int64_t kGatedPad = 64;  // columns of dz, and tokens of fp32 transposes, are padded to this
+// Sums over slabs of K where a product has too few output tiles to fill the chip.  d_x: the number
+// of slabs depends on D, F, the type and which of three sizes the batch has, so that a row's d_x
+// does not depend on the others of such a batch; the weight gradients: on all sizes.
+constexpr int64_t kGatedRowsSmall = 2048, kGatedRowsMiddle = 8192;
+constexpr int64_t kGatedSlabs = 8, kGatedTiles = 160;
 struct GatedLayout {
   int64_t fp = 0, np = 0;    // F and N rounded up to kGatedPad
-  int64_t k_slab = 0;        // columns of a slab of d_x (a multiple of 128), 0: one walk
-  size_t dz_off = 0, wt_off = 0, slab_off = 0;  // d_x: [dz | du], [Wg; Wu]^T, slab sums
-  size_t dzt_off = 0, xt_off = 0;               // weight gradients: their transposes
+  int64_t ldz = 0;           // 16 bits: elements from row to row of [dz | du]
+  int64_t dx_slab = 0, dw_slab = 0;  // columns (tokens) of a slab, multiples of 128; 0: one walk
+  size_t dz_off = 0;                 // [dz | du]; fp32: K-blocked, for d_x
+  size_t wt_off = 0, dzt_off = 0, xt_off = 0;  // fp32: [Wg; Wu]^T, [dz | du]^T, x^T
+  size_t acc_off = 0;                // fp32 slab sums of d_x, then of the weight gradients
   size_t total = 0;
 };
 // What the forward keeps for the backward: two numbers of 3 bytes (fp32: 4) per element.

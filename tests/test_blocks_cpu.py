@@ -239,7 +239,7 @@ GATED = [
     (dict(F=0), "FLP_INVALID_ARGUMENT"),
     (dict(D=48), "FLP_UNSUPPORTED_SHAPE"),               # no multiple of 32
     (dict(D=1 << 23), "FLP_UNSUPPORTED_SHAPE"),          # 256 rows pass 2^31 bytes
-    (dict(F=64 * 65535 + 1), "FLP_UNSUPPORTED_SHAPE"),
+    (dict(F=64 * 32767 + 1), "FLP_UNSUPPORTED_SHAPE"),
     (dict(N=64 * 65535 + 1), "FLP_UNSUPPORTED_SHAPE"),
     (dict(N=64 * 65535, F=64 * 256 + 1), "FLP_UNSUPPORTED_SHAPE"),
     (dict(x=I32), "FLP_UNSUPPORTED_DTYPE"),
@@ -286,7 +286,7 @@ def gated_bwd(**kw):
     (dict(dx=A[5] + 2), "FLP_MISALIGNED"),
     (dict(dwu=A[7] + 8), "FLP_MISALIGNED"),
     (dict(ws=A[8] + 8), "FLP_MISALIGNED"),
-    (dict(wsb=abi.flp_gated_linear_backward_workspace_bytes(N, D, F, BF16, 1, 0)),
+    (dict(wsb=abi.flp_gated_linear_backward_workspace_bytes(N, D, F, BF16, 1, 1) - 1),
      "FLP_WORKSPACE_TOO_SMALL"),
     (dict(dx=A[0]), "FLP_INVALID_ARGUMENT"),
     (dict(dwu=A[6] + 64), "FLP_INVALID_ARGUMENT"),
@@ -303,7 +303,12 @@ def test_gated_linear_sizes():
     assert abi.flp_gated_linear_saved_bytes(40, 100, F32) == 40 * 128 * 8
     assert abi.flp_gated_linear_saved_bytes(0, 100, BF16) == 0
     size = abi.flp_gated_linear_backward_workspace_bytes
-    # [dz | du] and its transpose over 64 tokens, [Wg; Wu]^T, x^T
-    assert size(64, 64, 128, BF16, 1, 0) == 2 * 128 * 64 * 2 + 2 * 128 * 64 * 2
-    assert size(40, 64, 128, BF16, 0, 1) == 2 * 128 * 64 * 2 + 64 * 64 * 2
+    # 16 bits: [dz | du] with 64 columns between the rows, and fp32 sums over slabs of its 256
+    # columns or tokens (none of 64 tokens)
+    assert size(64, 64, 128, BF16, 1, 1) == size(64, 64, 128, BF16, 0, 1) == (256 + 64) * 64 * 2
+    assert size(64, 64, 256, BF16, 1, 0) == (512 + 64) * 64 * 2 + 2 * 64 * 64 * 4
+    assert size(1024, 64, 128, BF16, 0, 1) == (256 + 64) * 1024 * 2 + 4 * 256 * 64 * 4
+    # fp32: beside it [Wg; Wu]^T; its transpose over 64 tokens and x^T
+    assert size(64, 64, 128, F32, 1, 0) == 2 * 128 * 64 * 4 + 2 * 128 * 64 * 4
+    assert size(40, 64, 128, F32, 0, 1) == 2 * 128 * 64 * 4 + 64 * 64 * 4
     assert size(0, 64, 128, BF16, 1, 1) == 0
