@@ -1066,7 +1066,6 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
   z.grad = grad_out;
   z.saved = saved;
   z.ld_saved = L.fp;
-  z.ldz = L.ldz;
   const bool wide = x_dtype == FLP_F32;
   float* acc = reinterpret_cast<float*>(at(workspace, L.acc_off));
   z.dz = d_x || !wide ? at(workspace, L.dz_off) : nullptr;
@@ -1077,7 +1076,6 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
     g.dz = z.dz;
     g.rows = N;
     g.fp = L.fp;
-    g.ldz = L.ldz;
     g.F = F;
     g.D = D;
     g.w_gate = w_gate;

@@ -62,10 +62,20 @@ __device__ __forceinline__ float act_slope(float z, float f) {
 }
 
 // What the forward keeps of four consecutive columns of a row: a and b, 12 bytes each (the upper
-// halves of their fp32 values, then the next bytes) or, in fp32, 16.
+// halves of their fp32 values, then the next bytes) or, in fp32, 16.  A block of 16 x 16 elements
+// is one MFMA tile in the order of its lanes, so that every store is one contiguous piece: 16
+// bytes of each lane (row i % 16, columns 4 (lane / 16)), then the rest of each.  (In rows, a
+// lane's 24 bytes after the other's, the forward of 16384 x 2688 x 7168 took 1100 us, now 1042.)
 template <class E>
 struct Kept {
-  static constexpr int kBytes = E::kSize == 2 ? 24 : 32;
+  static constexpr int kRest = E::kSize == 2 ? 8 : 16;  // bytes of a lane's second piece
+  static constexpr int kBlock = 64 * (16 + kRest);
+  static __device__ __forceinline__ int64_t block(int64_t row, int64_t col, int64_t ld) {
+    return ((row >> 4) * (ld >> 4) + (col >> 4)) * kBlock;
+  }
+  static __device__ __forceinline__ int lane(int64_t row, int64_t col) {
+    return int((col >> 2) & 3) * 16 + int(row & 15);
+  }
   struct Packed {
     uint32_t h0, h1, lo;
   };
@@ -81,15 +91,16 @@ struct Kept {
             __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0501u) |
                 __builtin_amdgcn_perm(b[3], b[2], 0x05010C0Cu)};
   }
-  __device__ __forceinline__ static void store(char* p, const f32x4_t& a, const f32x4_t& b) {
-    typedef u32x4 loose16 __attribute__((aligned(8)));
+  __device__ __forceinline__ static void store(char* block, int lane, const f32x4_t& a,
+                                               const f32x4_t& b) {
+    u32x4* const first = reinterpret_cast<u32x4*>(block) + lane;
     if constexpr (E::kSize == 2) {
       const Packed u = pack(a), v = pack(b);
-      *reinterpret_cast<loose16*>(p) = u32x4{u.h0, u.h1, v.h0, v.h1};
-      *reinterpret_cast<u32x2*>(p + 16) = u32x2{u.lo, v.lo};
+      *first = u32x4{u.h0, u.h1, v.h0, v.h1};
+      reinterpret_cast<u32x2*>(block + 1024)[lane] = u32x2{u.lo, v.lo};
     } else {
-      reinterpret_cast<f32x4_t*>(p)[0] = a;
-      reinterpret_cast<f32x4_t*>(p)[1] = b;
+      *reinterpret_cast<f32x4_t*>(first) = a;
+      reinterpret_cast<f32x4_t*>(block + 1024)[lane] = b;
     }
   }
   __device__ __forceinline__ static void unpack(uint32_t h0, uint32_t h1, uint32_t lo, float* v) {
@@ -98,23 +109,20 @@ struct Kept {
     v[2] = __uint_as_float((h1 << 16) | ((lo >> 8) & 0xFF00u));
     v[3] = __uint_as_float((h1 & 0xFFFF0000u) | ((lo >> 16) & 0xFF00u));
   }
-  // Eight columns: a and b (p a multiple of eight columns: 16-byte aligned).
-  __device__ __forceinline__ static void load8(const char* p, float (&a)[8], float (&b)[8]) {
-    const u32x4* q = reinterpret_cast<const u32x4*>(p);
+  // Four columns: a and b.
+  __device__ __forceinline__ static void load4(const char* block, int lane, float* a, float* b) {
+    const u32x4 w = reinterpret_cast<const u32x4*>(block)[lane];
     if constexpr (E::kSize == 2) {
-      const u32x4 w0 = q[0], w1 = q[1], w2 = q[2];
-      unpack(w0.x, w0.y, w1.x, a);
-      unpack(w0.z, w0.w, w1.y, b);
-      unpack(w1.z, w1.w, w2.z, a + 4);
-      unpack(w2.x, w2.y, w2.w, b + 4);
+      const u32x2 l = reinterpret_cast<const u32x2*>(block + 1024)[lane];
+      unpack(w.x, w.y, l.x, a);
+      unpack(w.z, w.w, l.y, b);
     } else {
+      const u32x4 v = reinterpret_cast<const u32x4*>(block + 1024)[lane];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[4 * h + e] = __uint_as_float(q[2 * h][e]);
-          b[4 * h + e] = __uint_as_float(q[2 * h + 1][e]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        a[e] = __uint_as_float(w[e]);
+        b[e] = __uint_as_float(v[e]);
+      }
     }
   }
 };
@@ -231,10 +239,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gated_fwd(GatedFwdArgs p) {
         a[r] = z[r] * f;
         b[r] = u[r] * act_slope<ACT>(z[r], f);
       }
-      if (p.saved != nullptr)  // rows of a multiple of 64 columns
-        Kept<E>::store(static_cast<char*>(p.saved) +
-                           (row * p.ld_saved + col) / 4 * Kept<E>::kBytes,
-                       a, b);
+      if (p.saved != nullptr)
+        Kept<E>::store(static_cast<char*>(p.saved) + Kept<E>::block(row, col, p.ld_saved), lane, a,
+                       b);
       store_loose4<E>(p.out, row * p.F + col, a * u, p.F - col);
     }
   }
@@ -257,41 +264,75 @@ struct Elem<F32> {
   using T = float;
 };
 
-// dz and du of eight columns of a row, zeros from the nth on.
-template <class E>
-__device__ __forceinline__ void dz_of(const GatedDzArgs& p, int64_t row, int64_t col, int64_t n,
-                                      float (&dz)[kChunk], float (&du)[kChunk]) {
-  using T = typename Elem<E>::T;
-  Chunk<T> gr;
-  gr.load(static_cast<const T*>(p.grad) + row * p.F + col, n);
-  float a[kChunk], b[kChunk];
-  if (n > 0)
-    Kept<E>::load8(static_cast<const char*>(p.saved) + (row * p.ld_saved + col) / 4 * Kept<E>::kBytes,
-                   a, b);
-#pragma unroll
-  for (int e = 0; e < kChunk; ++e) {
-    const float g = float(T(gr.v[e]));
-    dz[e] = e < n ? g * b[e] : 0.f;
-    du[e] = e < n ? g * a[e] : 0.f;
-  }
-}
-
-// 16-bit types: [dz | du] as rows, one wave per 512 columns of a row.  Columns past F are zeros.
+// 16-bit types: [dz | du] as rows.  A wave takes 16 rows x 64 columns: the gradient as whole
+// lines, through LDS into the lanes of the kept blocks, and dz and du back through LDS into whole
+// lines (straight from the lanes, 32 bytes of a row at a time, 361 us for 16384 x 7168; 280 with
+// lines both ways).  Columns past F are zeros.
 template <class E>
 __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
-  const int64_t col = int64_t(blockIdx.x) * 512 + (threadIdx.x & 63) * kChunk;
-  if (col >= p.ld_saved) return;
-  const int64_t n = p.F - col;
-  for (int64_t row = int64_t(blockIdx.y) * 4 + (threadIdx.x >> 6); row < p.N;
-       row += int64_t(gridDim.y) * 4) {
-    float dz[kChunk], du[kChunk];
-    dz_of<E>(p, row, col, n, dz, du);
-    uint16_t* out = static_cast<uint16_t*>(p.dz) + row * p.ldz + col;
-    *reinterpret_cast<u32x4*>(out) = u32x4{pack2<E>(dz[0], dz[1]), pack2<E>(dz[2], dz[3]),
-                                           pack2<E>(dz[4], dz[5]), pack2<E>(dz[6], dz[7])};
-    *reinterpret_cast<u32x4*>(out + p.ld_saved) =
-        u32x4{pack2<E>(du[0], du[1]), pack2<E>(du[2], du[3]), pack2<E>(du[4], du[5]),
-              pack2<E>(du[6], du[7])};
+  using T = typename Elem<E>::T;
+  constexpr int kPitch = 72;  // elements of a row in LDS: 16 bytes more than its 64
+  __shared__ __attribute__((aligned(16))) uint16_t tiles[4][2][16 * kPitch];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col0 = int64_t(blockIdx.x) * 256 + wave * 64;
+  if (col0 >= p.ld_saved) return;
+  uint16_t* const one = tiles[wave][0];
+  uint16_t* const two = tiles[wave][1];
+  const int i = lane & 15, g = lane >> 4;  // of the kept blocks
+  const int lr = lane >> 3, lc = (lane & 7) * 8;  // of the lines: rows lr and lr + 8
+  for (int64_t row0 = int64_t(blockIdx.y) * 16; row0 < p.N; row0 += int64_t(gridDim.y) * 16) {
+    Chunk<T> gr[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t row = row0 + lr + 8 * q;
+      gr[q].load(static_cast<const T*>(p.grad) + row * p.F + col0 + lc,
+                 row < p.N ? p.F - (col0 + lc) : 0);
+    }
+    float a[4][4], b[4][4];
+    const char* const block = static_cast<const char*>(p.saved) + Kept<E>::block(row0, col0, p.ld_saved);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) Kept<E>::load4(block + k * Kept<E>::kBlock, lane, a[k], b[k]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      *reinterpret_cast<u32x4*>(one + (lr + 8 * q) * kPitch + lc) = gr[q].w[0];
+    u32x2 dz[4], du[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      typedef T vec __attribute__((ext_vector_type(4)));
+      const int at = i * kPitch + k * 16 + 4 * g;
+      const vec gv = *reinterpret_cast<const vec*>(one + at);
+      // what was kept past the rows' and columns' ends was not written: no product of it
+      const int64_t n = row0 + i < p.N ? p.F - (col0 + k * 16 + 4 * g) : 0;
+      float z[4], u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float gf = float(T(gv[e]));
+        z[e] = e < n ? gf * b[k][e] : 0.f;
+        u[e] = e < n ? gf * a[k][e] : 0.f;
+      }
+      dz[k] = u32x2{pack2<E>(z[0], z[1]), pack2<E>(z[2], z[3])};
+      du[k] = u32x2{pack2<E>(u[0], u[1]), pack2<E>(u[2], u[3])};
+    }
+    __builtin_amdgcn_wave_barrier();  // the gradient has been read by all lanes of the wave
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = i * kPitch + k * 16 + 4 * g;
+      *reinterpret_cast<u32x2*>(one + at) = dz[k];
+      *reinterpret_cast<u32x2*>(two + at) = du[k];
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t row = row0 + lr + 8 * q;
+      const u32x4 z = *reinterpret_cast<const u32x4*>(one + (lr + 8 * q) * kPitch + lc);
+      const u32x4 u = *reinterpret_cast<const u32x4*>(two + (lr + 8 * q) * kPitch + lc);
+      if (row < p.N) {
+        uint16_t* const out = static_cast<uint16_t*>(p.dz) + row * 2 * p.ld_saved + col0 + lc;
+        *reinterpret_cast<u32x4*>(out) = z;
+        *reinterpret_cast<u32x4*>(out + p.ld_saved) = u;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -302,16 +343,19 @@ __global__ __launch_bounds__(256) void k_gated_dz32(GatedDzArgs p) {
   __shared__ float tile[2][64][65];
   const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
   const int t = threadIdx.x;
-  const int rl = t >> 2;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int cl = (t & 3) * 16 + half * 8;
-    float dz[kChunk], du[kChunk];
-    dz_of<F32>(p, r0 + rl, c0 + cl, r0 + rl < p.N ? p.F - (c0 + cl) : 0, dz, du);
+  for (int q = 0; q < 4; ++q) {  // four rows of blocks, the lanes as in the kept blocks
+    const int rl = q * 16 + (t & 15), cl = (t >> 4) * 4;
+    const int64_t row = r0 + rl, col = c0 + cl, n = row < p.N ? p.F - col : 0;
+    float a[4], b[4];
+    if (n > 0)
+      Kept<F32>::load4(static_cast<const char*>(p.saved) + Kept<F32>::block(row, col, p.ld_saved),
+                       Kept<F32>::lane(row, col), a, b);
 #pragma unroll
-    for (int e = 0; e < kChunk; ++e) {
-      tile[0][rl][cl + e] = dz[e];
-      tile[1][rl][cl + e] = du[e];
+    for (int e = 0; e < 4; ++e) {
+      const float g = e < n ? static_cast<const float*>(p.grad)[row * p.F + col + e] : 0.f;
+      tile[0][rl][cl + e] = e < n ? g * b[e] : 0.f;
+      tile[1][rl][cl + e] = e < n ? g * a[e] : 0.f;
     }
   }
   __syncthreads();
@@ -356,10 +400,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gated_gemm(GatedGemmArgs p) {
   const char* const dz = static_cast<const char*>(p.dz);
   const char* const x = static_cast<const char*>(p.x);
   if constexpr (TURNED) {
-    a.init(dz, dz, 0, p.rows, 2 * p.ldz, m0, M, k0, lane, wave, wm * NA);
+    a.init(dz, dz, 0, p.rows, 4 * p.fp, m0, M, k0, lane, wave, wm * NA);
     b.init(x, x, 0, p.rows, 2 * p.D, n0, p.D, k0, lane, wave, wn * NB);
   } else {
-    a.init(dz + m0 * 2 * p.ldz + k0 * 2, 2 * p.ldz, M - m0, lane, wm * RW);
+    a.init(dz + m0 * 4 * p.fp + k0 * 2, 4 * p.fp, M - m0, lane, wm * RW);
     b.init(static_cast<const char*>(p.w_gate), static_cast<const char*>(p.w_up), p.fp, p.F, 2 * p.D,
            n0, p.D, k0, lane, wave, wn * NB);
   }
@@ -508,8 +552,8 @@ hipError_t gemm16(const GatedGemmArgs& a, hipStream_t s) {
 
 template <class E>
 hipError_t dz16(const GatedDzArgs& a, hipStream_t s) {
-  const dim3 grid(unsigned((a.ld_saved + 511) / 512),
-                  unsigned(std::min<int64_t>((a.N + 3) / 4, 65535)));
+  const dim3 grid(unsigned((a.ld_saved + 255) / 256),
+                  unsigned(std::min<int64_t>((a.N + 15) / 16, 65535)));
   hipLaunchKernelGGL(k_gated_dz<E>, grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }

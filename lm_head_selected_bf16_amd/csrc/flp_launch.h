@@ -268,7 +268,7 @@ struct GatedFwdArgs {
   const void* w_gate;        // [F][D]
   const void* w_up;          // [F][D]
   void* out;                 // [N][F]
-  void* saved;               // [N][ld_saved] act(z) and u act'(z), by four columns, or null
+  void* saved;               // act(z) and u act'(z) in blocks of 16 x 16, or null
   int64_t ld_saved;          // F rounded up to 64
 };
 struct GatedDzArgs {
@@ -276,8 +276,7 @@ struct GatedDzArgs {
   const void* grad;          // [N][F]
   const void* saved;         // as above
   int64_t ld_saved;
-  int64_t ldz;               // 16 bits: elements from row to row of dz
-  void* dz;                  // [N][ldz] dz, then du from ld_saved on; fp32: K-blocked (or null)
+  void* dz;                  // [N][2 ld_saved] dz, du; fp32: K-blocked (or null)
   void* dzT;                 // fp32 only, K-blocked: 2 ld_saved rows, K = N rounded up to 64, or null
 };
 hipError_t launch_gated_forward(flp_dtype x, const GatedFwdArgs& a, hipStream_t s);
@@ -287,8 +286,8 @@ hipError_t launch_gated_dx(const GemmArgs& a, hipStream_t s);
 hipError_t launch_gated_dw(const GemmArgs& a, hipStream_t s);
 // 16 bits: the same from operands as they lie.
 struct GatedGemmArgs {
-  const void* dz;            // [rows][ldz], 2 fp columns
-  int64_t rows, fp, ldz, F, D;
+  const void* dz;            // [rows][2 fp]
+  int64_t rows, fp, F, D;
   const void* w_gate;        // [F][D], for d_x
   const void* w_up;
   const void* x;             // [rows][D], for the weight gradients

@@ -885,10 +885,7 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need
     slabs = std::min({slabs, kGatedSlabs, k / 256});
     return slabs > 1 ? round_up(ceil_div(k, slabs), 128) : 0;
   };
-  // 128 bytes past a multiple of 256, or else the rows of a tile would meet in few of the L2's
-  // channels (F = 7168, whose rows are 7 * 4096 bytes apart: products a third slower)
-  L.ldz = K + (wide ? 0 : kGatedPad);
-  if (need_dx || !wide) take(L.dz_off, size_t(L.ldz) * N * xs);
+  if (need_dx || !wide) take(L.dz_off, size_t(K) * N * xs);
   if (wide && need_dx) take(L.wt_off, size_t(K) * D * xs);
   if (wide && need_dw) {
     take(L.dzt_off, size_t(K) * L.np * xs);

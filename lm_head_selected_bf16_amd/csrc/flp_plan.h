@@ -162,16 +162,16 @@ constexpr int64_t kGatedRowsSmall = 2048, kGatedRowsMiddle = 8192;
 constexpr int64_t kGatedSlabs = 8, kGatedTiles = 160;
 struct GatedLayout {
   int64_t fp = 0, np = 0;    // F and N rounded up to kGatedPad
-  int64_t ldz = 0;           // 16 bits: elements from row to row of [dz | du]
   int64_t dx_slab = 0, dw_slab = 0;  // columns (tokens) of a slab, multiples of 128; 0: one walk
   size_t dz_off = 0;                 // [dz | du]; fp32: K-blocked, for d_x
   size_t wt_off = 0, dzt_off = 0, xt_off = 0;  // fp32: [Wg; Wu]^T, [dz | du]^T, x^T
   size_t acc_off = 0;                // fp32 slab sums of d_x, then of the weight gradients
   size_t total = 0;
 };
-// What the forward keeps for the backward: two numbers of 3 bytes (fp32: 4) per element.
+// What the forward keeps for the backward: two numbers of 3 bytes (fp32: 4) per element, in
+// blocks of 16 rows by 16 columns.
 inline size_t gated_saved_bytes(int64_t N, int64_t F, flp_dtype x) {
-  return size_t(N) * size_t(round_up(F, kGatedPad)) * (x == FLP_F32 ? 8 : 6);
+  return size_t(round_up(N, 16)) * size_t(round_up(F, kGatedPad)) * (x == FLP_F32 ? 8 : 6);
 }
 GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need_dx, bool need_dw);
 

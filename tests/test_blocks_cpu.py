@@ -259,7 +259,7 @@ GATED = [
     (dict(out=A[3] + 1), "FLP_MISALIGNED"),
     (dict(out=A[0]), "FLP_INVALID_ARGUMENT"),
     (dict(out=A[2] + F * D * 2 - 2), "FLP_INVALID_ARGUMENT"),      # the last weight
-    (dict(out=A[4] + N * 128 * 6 - 2), "FLP_INVALID_ARGUMENT"),    # saved: rows of 128
+    (dict(out=A[4] + 48 * 128 * 6 - 2), "FLP_INVALID_ARGUMENT"),   # saved: 48 rows of 128
     (dict(N=0, xp=0, wg=0, wu=0, out=0, saved=0), "FLP_OK"),
 ])
 def test_gated_linear_forward_gates(kw, expect):
@@ -299,15 +299,14 @@ def test_gated_linear_backward_gates(kw, expect):
 
 
 def test_gated_linear_sizes():
-    assert abi.flp_gated_linear_saved_bytes(40, 100, BF16) == 40 * 128 * 6
-    assert abi.flp_gated_linear_saved_bytes(40, 100, F32) == 40 * 128 * 8
+    assert abi.flp_gated_linear_saved_bytes(40, 100, BF16) == 48 * 128 * 6
+    assert abi.flp_gated_linear_saved_bytes(40, 100, F32) == 48 * 128 * 8
     assert abi.flp_gated_linear_saved_bytes(0, 100, BF16) == 0
     size = abi.flp_gated_linear_backward_workspace_bytes
-    # 16 bits: [dz | du] with 64 columns between the rows, and fp32 sums over slabs of its 256
-    # columns or tokens (none of 64 tokens)
-    assert size(64, 64, 128, BF16, 1, 1) == size(64, 64, 128, BF16, 0, 1) == (256 + 64) * 64 * 2
-    assert size(64, 64, 256, BF16, 1, 0) == (512 + 64) * 64 * 2 + 2 * 64 * 64 * 4
-    assert size(1024, 64, 128, BF16, 0, 1) == (256 + 64) * 1024 * 2 + 4 * 256 * 64 * 4
+    # 16 bits: [dz | du], and fp32 sums over slabs of its 256 columns or tokens (none of 64 tokens)
+    assert size(64, 64, 128, BF16, 1, 1) == size(64, 64, 128, BF16, 0, 1) == 256 * 64 * 2
+    assert size(64, 64, 256, BF16, 1, 0) == 512 * 64 * 2 + 2 * 64 * 64 * 4
+    assert size(1024, 64, 128, BF16, 0, 1) == 256 * 1024 * 2 + 4 * 256 * 64 * 4
     # fp32: beside it [Wg; Wu]^T; its transpose over 64 tokens and x^T
     assert size(64, 64, 128, F32, 1, 0) == 2 * 128 * 64 * 4 + 2 * 128 * 64 * 4
     assert size(40, 64, 128, F32, 0, 1) == 2 * 128 * 64 * 4 + 64 * 64 * 4
