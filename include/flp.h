@@ -581,7 +581,7 @@ flp_status flp_layer_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, cons
  *                their own; or NULL.
  *
  * Requirements: D % 32 == 0 (and the size limits of flp_forward), 1 <= F <= 64 * 32767,
- * N <= 64 * 65535, N F below about 2^36.
+ * N <= 64 * 65535, N F + 2 D F + N D below about 2^36.
  */
 typedef enum flp_activation {
   FLP_ACT_SILU = 0,

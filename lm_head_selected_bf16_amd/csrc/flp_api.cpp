@@ -1070,6 +1070,12 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
   float* acc = reinterpret_cast<float*>(at(workspace, L.acc_off));
   z.dz = d_x || !wide ? at(workspace, L.dz_off) : nullptr;
   z.dzT = dw && wide ? at(workspace, L.dzt_off) : nullptr;
+  z.D = D;
+  z.w_gate = w_gate;
+  z.w_up = w_up;
+  z.x = x;
+  z.wt = d_x && wide ? at(workspace, L.wt_off) : nullptr;
+  z.xt = dw && wide ? at(workspace, L.xt_off) : nullptr;
   if (launch_gated_dz(x_dtype, z, s) != hipSuccess) return FLP_HIP_ERROR;
   if (!wide) {
     GatedGemmArgs g{};
@@ -1096,14 +1102,9 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
     return FLP_OK;
   }
   if (d_x != nullptr) {
-    void* wt = at(workspace, L.wt_off);
-    void* wt_up = at(wt, size_t(L.fp) * D * xs);
-    if (launch_transpose(x_dtype, w_gate, F, L.fp, D, D, wt, s) != hipSuccess ||
-        launch_transpose(x_dtype, w_up, F, L.fp, D, D, wt_up, s) != hipSuccess)
-      return FLP_HIP_ERROR;
     GemmArgs g{};
     g.a = z.dz;
-    g.b = wt;
+    g.b = z.wt;
     g.lda_b = g.ldb_b = 128;
     g.a_ks = N * 128;
     g.b_ks = D * 128;
@@ -1117,11 +1118,9 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
     if (launch_gated_dx(g, s) != hipSuccess) return FLP_HIP_ERROR;
   }
   if (dw) {
-    void* xt = at(workspace, L.xt_off);
-    if (launch_transpose(x_dtype, x, N, L.np, D, D, xt, s) != hipSuccess) return FLP_HIP_ERROR;
     GemmArgs g{};
     g.a = z.dzT;
-    g.b = xt;
+    g.b = z.xt;
     g.lda_b = g.ldb_b = 128;
     g.a_ks = 2 * L.fp * 128;
     g.b_ks = D * 128;

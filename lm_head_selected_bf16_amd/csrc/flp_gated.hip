@@ -348,13 +348,51 @@ __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
   }
 }
 
-// fp32, whose products take K-blocked operands: a workgroup takes 64 tokens x 64 columns, whole
-// rows in, and out of LDS the same tile by columns (dz: the K of d_x) and by tokens (dzT), each a
-// contiguous K-blocked piece.  Columns past F and tokens past N are zeros.
+// A 64 x 64 tile of src [rows][cols] to dst = src^T, K-blocked with cols rows; source rows past
+// the end are zeros.
+__device__ __forceinline__ void turn_tile(const float* src, int64_t rows, int64_t cols, int64_t r0,
+                                          int64_t c0, float* dst, float (&tile)[64][65]) {
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {  // sixteen loads in flight
+    const int k = ty + 4 * u;
+    tile[k][tx] = r0 + k < rows && c0 + tx < cols ? src[(r0 + k) * cols + c0 + tx] : 0.f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const int k = ty + 4 * u;
+    if (c0 + k < cols) dst[kblk<32>(c0 + k, r0 + tx, cols)] = tile[tx][k];
+  }
+}
+
+// fp32, whose products take K-blocked operands, all of them made in one launch: dz and du in
+// tiles of 64 tokens x 64 columns, whole rows in, and out of LDS the same tile by columns (dz: the
+// K of d_x) and by tokens (dzT), each a contiguous piece; then the weights' transposes and x's.
+// Columns past F and tokens past N are zeros.  (In four launches, 201 x 288 x 771 took 27 us
+// for these.)
 __global__ __launch_bounds__(256) void k_gated_dz32(GatedDzArgs p) {
   __shared__ float tile[2][64][65];
-  const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
   const int t = threadIdx.x;
+  const int64_t nc = p.ld_saved / 64, nd = (p.D + 63) / 64, nt = (p.N + 63) / 64;
+  int64_t b = blockIdx.x;
+  if (b >= nc * nt) {
+    b -= nc * nt;
+    if (p.wt != nullptr) {
+      if (b < 2 * nc * nd) {
+        const bool up = b >= nc * nd;
+        if (up) b -= nc * nd;
+        turn_tile(static_cast<const float*>(up ? p.w_up : p.w_gate), p.F, p.D, b / nd * 64,
+                  b % nd * 64, static_cast<float*>(p.wt) + (up ? p.ld_saved * p.D : 0), tile[0]);
+        return;
+      }
+      b -= 2 * nc * nd;
+    }
+    turn_tile(static_cast<const float*>(p.x), p.N, p.D, b / nd * 64, b % nd * 64,
+              static_cast<float*>(p.xt), tile[0]);
+    return;
+  }
+  const int64_t r0 = b / nc * 64, c0 = b % nc * 64;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {  // four rows of blocks, the lanes as in the kept blocks
     const int rl = q * 16 + (t & 15), cl = (t >> 4) * 4;
@@ -624,8 +662,9 @@ hipError_t launch_gated_dz(flp_dtype x, const GatedDzArgs& a, hipStream_t s) {
   ProfScope ps(FLP_K_GATED, s);
   if (x == FLP_BF16) return dz16<BF16>(a, s);
   if (x == FLP_F16) return dz16<F16>(a, s);
-  const dim3 grid(unsigned(a.ld_saved / 64), unsigned((a.N + 63) / 64));
-  hipLaunchKernelGGL(k_gated_dz32, grid, dim3(256), 0, s, a);
+  const int64_t nc = a.ld_saved / 64, nd = (a.D + 63) / 64, nt = (a.N + 63) / 64;
+  const int64_t blocks = nc * nt + (a.wt ? 2 * nc * nd : 0) + (a.xt ? nt * nd : 0);
+  hipLaunchKernelGGL(k_gated_dz32, dim3(unsigned(blocks)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

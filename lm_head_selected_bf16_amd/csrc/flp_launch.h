@@ -277,7 +277,14 @@ struct GatedDzArgs {
   const void* saved;         // as above
   int64_t ld_saved;
   void* dz;                  // [N][2 ld_saved] dz, du; fp32: K-blocked (or null)
-  void* dzT;                 // fp32 only, K-blocked: 2 ld_saved rows, K = N rounded up to 64, or null
+  // fp32 only: the other operands of the products, K-blocked, each or null
+  void* dzT;                 // 2 ld_saved rows, K = N rounded up to 64
+  int64_t D;
+  const void* w_gate;        // [F][D]
+  const void* w_up;
+  const void* x;             // [N][D]
+  void* wt;                  // D rows, K = 2 ld_saved: [Wg; Wu]^T
+  void* xt;                  // D rows, K = N rounded up to 64: x^T
 };
 hipError_t launch_gated_forward(flp_dtype x, const GatedFwdArgs& a, hipStream_t s);
 hipError_t launch_gated_dz(flp_dtype x, const GatedDzArgs& a, hipStream_t s);
@@ -358,7 +365,7 @@ struct AdamTensor {
   int64_t first;             // the tensor's first tile (set by the launcher)
   float decay;
 };
-constexpr int kAdamTensors = 48;  // of a launch: its argument stays below 4 KB
+constexpr int kAdamTensors = 48;  // of a launch: at most a wave's lanes, and an argument below 4 KB
 struct AdamArgs {
   double lr, c1, c2;         // c1 = 1 / (1 - b1^t), c2 = 1 / sqrt(1 - b2^t)
   double log_b1, log_b2;     // for a step on the device

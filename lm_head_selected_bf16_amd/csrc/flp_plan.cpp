@@ -919,7 +919,8 @@ flp_status check_gated(int64_t N, int64_t D, int64_t F, flp_dtype x, flp_activat
   // elements) stay below 2^31 bytes, and a launch holds fewer than 2^32 threads (256 for 64 x 64
   // elements of dz)
   if (N > int64_t(65535) * 64 || F > int64_t(32767) * 64) return FLP_UNSUPPORTED_SHAPE;
-  if (ceil_div(N, 64) * ceil_div(F, 64) >= (int64_t(1) << 24)) return FLP_UNSUPPORTED_SHAPE;
+  const int64_t nt = ceil_div(N, 64), nc = ceil_div(F, 64), nd = ceil_div(D, 64);
+  if (nc * nt + 2 * nc * nd + nt * nd >= (int64_t(1) << 24)) return FLP_UNSUPPORTED_SHAPE;
   return FLP_OK;
 }
 
