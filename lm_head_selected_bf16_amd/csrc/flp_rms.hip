@@ -53,6 +53,7 @@ __device__ __forceinline__ float team_sum(float x, float* red) {
   const int wave = threadIdx.x >> 6, first = wave & ~(kWaves - 1);
   if ((threadIdx.x & 63) == 0) red[wave] = x;
   __syncthreads();
+  if constexpr (kWaves == 2) return red[first] + red[first + 1];
   float s = (red[first] + red[first + 1]) + (red[first + 2] + red[first + 3]);
   if constexpr (kWaves == 8)
     s += (red[first + 4] + red[first + 5]) + (red[first + 6] + red[first + 7]);
@@ -449,25 +450,34 @@ __global__ __launch_bounds__(kThreads) void k_rms_bwd(RmsBwdArgs p) {
   }
 }
 
-// The sums over rows from the slab partials: what = 0 d_weight, 1 d_post_weight, 2 + k row k
-// of d_gate.  16 columns per workgroup, sixteen threads per column each adding every
-// sixteenth slab in ascending order (eight loads in flight), then the sixteen by a fixed tree.
+// The sums over rows from the slab partials: what = 0 d_weight, 1 d_post_weight (and with one
+// gate row, d_gate, which has the same sums), 2 + k row k of d_gate.  16 columns per workgroup,
+// sixteen threads per column each adding every sixteenth slab in ascending order (eight loads in
+// flight), then the sixteen by a fixed tree.
 template <class T>
 __global__ __launch_bounds__(256) void k_rms_fold(RmsBwdArgs p, int64_t blocks, int64_t per) {
   __shared__ float s[16][17];
   const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const bool one_gate = p.gate_rows == 1 && !p.gates;
   auto param = [&](const void* base, int64_t i) {
     return p.wide || sizeof(T) == 4 ? static_cast<const float*>(base)[i]
                                     : to_f32(static_cast<const T*>(base)[i]);
   };
+  auto put = [&](void* out, int64_t at, float v) {
+    if (out == nullptr) return;
+    if (p.wide || sizeof(T) == 4)
+      static_cast<float*>(out)[at] = v;
+    else
+      static_cast<T*>(out)[at] = T(v);
+  };
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int64_t what = b / per, d = (b % per) * 16 + c;
-    void* out = what == 0 ? p.d_weight : what == 1 ? p.d_post_weight : p.d_gate;
-    if (out == nullptr) continue;  // the same for the whole workgroup
+    void* const out = what == 0 ? p.d_weight : what == 1 ? p.d_post_weight : p.d_gate;
+    if (out == nullptr && !(what == 1 && one_gate && p.d_gate != nullptr)) continue;  // all of it
     const int64_t lo = what < 2 ? 0 : (what - 2) * p.slabs_per_gate;
     const int64_t hi = what < 2 ? p.slabs : lo + p.slabs_per_gate;
     // d_post_weight: each gate's sums times the gate (with a gate per row they hold it already)
-    const bool gated = what == 1 && p.gate != nullptr && !p.gates;
+    const bool gated = what == 1 && p.gate != nullptr && !p.gates && !one_gate;
     float a = 0.f;
     if (d < p.D) {
       const float* src = p.part + (what == 0 ? 0 : p.D) + d;
@@ -493,12 +503,16 @@ __global__ __launch_bounds__(256) void k_rms_fold(RmsBwdArgs p, int64_t blocks, 
     if (q == 0 && d < p.D) {
       float v = s[0][c];
       if (what > 0) v *= p.scale;
-      if (what > 1 && p.post_weight != nullptr) v *= param(p.post_weight, d);
-      const int64_t at = (what < 2 ? 0 : (what - 2) * p.D) + d;
-      if (p.wide || sizeof(T) == 4)
-        static_cast<float*>(out)[at] = v;
+      const float to_gate = p.post_weight != nullptr && p.d_gate != nullptr && what > 0
+                                ? v * param(p.post_weight, d) : v;
+      if (what == 1 && one_gate) {
+        put(p.d_gate, d, to_gate);
+        v *= param(p.gate, d);
+      }
+      if (what < 2)
+        put(out, d, v);
       else
-        static_cast<T*>(out)[at] = T(v);
+        put(out, (what - 2) * p.D + d, to_gate);
     }
   }
 }
@@ -526,18 +540,23 @@ void by_width_fwd(int64_t D, F f) {
   return f(w8, integral_constant<int, 4>{});
 }
 
-// Backward: four rows' chunks and two sums for each, so one wave holds two chunks per thread
-// (six spill), four waves two, eight waves up to four.
+// Backward: four rows' chunks and two sums for each, so one wave holds up to four chunks per
+// thread of a 16-bit row (six spill), three of an fp32 one, and two waves three.
 template <class T, class F>
 void by_width_bwd(int64_t D, F f) {
   using std::integral_constant;
   const int64_t chunks = (D + kChunk - 1) / kChunk;
   constexpr integral_constant<int, 64> w1{};
+  constexpr integral_constant<int, 128> w2{};
   constexpr integral_constant<int, 256> w4{};
   constexpr integral_constant<int, 512> w8{};
   if (chunks <= 64) return f(w1, integral_constant<int, 1>{});
   if (chunks <= 128) return f(w1, integral_constant<int, 2>{});
-  if (chunks <= 256) return f(w4, integral_constant<int, 1>{});
+  if (chunks <= 192) return f(w1, integral_constant<int, 3>{});
+  if (chunks <= 256)
+    return f(integral_constant<int, sizeof(T) == 2 ? 64 : 128>{},
+             integral_constant<int, sizeof(T) == 2 ? 4 : 2>{});
+  if (chunks <= 384) return f(w2, integral_constant<int, 3>{});
   if (chunks <= 512) return f(w4, integral_constant<int, 2>{});
   if (chunks <= 1024) return f(w8, integral_constant<int, 2>{});
   return f(w8, integral_constant<int, 4>{});
@@ -600,7 +619,7 @@ hipError_t rms_bwd(const RmsBwdArgs& a, hipStream_t s) {
   if (a.d_weight == nullptr && a.d_post_weight == nullptr && !gate_sums) return hipGetLastError();
   RmsBwdArgs b = a;
   if (!gate_sums) b.d_gate = nullptr;
-  const int64_t per = (a.D + 15) / 16, blocks = per * (2 + (gate_sums ? a.gate_rows : 0));
+  const int64_t per = (a.D + 15) / 16, blocks = per * (2 + (gate_sums && a.gate_rows > 1 ? a.gate_rows : 0));
   hipLaunchKernelGGL(k_rms_fold<T>, dim3(unsigned(std::min<int64_t>(blocks, 1 << 16))), dim3(256),
                      0, s, b, blocks, per);
   return hipGetLastError();
