@@ -150,9 +150,13 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
   const float rate = float(lr * c1), root_scale = float(c2);
   const float grad_scale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
   const int lane8 = int(threadIdx.x) * kChunk;
-  AdamTensor t = a.t[0];
-  float keep = float(1.0 - lr * double(t.decay));
-  int k = 0;
+  // Lane k knows tensor k's first tile: a ballot finds a tile's tensor (a walk through the table
+  // costs a load's latency for each tensor).
+  const int lane = threadIdx.x & 63;
+  const int64_t first_of = lane < a.count ? a.t[lane].first : INT64_MAX;
+  AdamTensor t;
+  float keep = 1.0f;
+  int k = -1;
 
   // The tile's elements from `first` on; FULL: all of them exist.
   auto work = [&](int64_t first, auto whole) {
@@ -232,9 +236,9 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
     }
   };
   for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-    if (k + 1 < a.count && tile >= a.t[k + 1].first) {
-      do ++k;
-      while (k + 1 < a.count && tile >= a.t[k + 1].first);
+    const int now = __popcll(__builtin_amdgcn_ballot_w64(tile >= first_of)) - 1;
+    if (now != k) {
+      k = now;
       t = a.t[k];
       keep = float(1.0 - lr * double(t.decay));
     }

@@ -7,6 +7,7 @@
 // interpreter for a node written in Python and then runs it from cold caches: a layer norm of
 // 37 x 1003, forward and backward, took 118 us on the host that way and takes 74 here.
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
 #include <torch/extension.h>
 
 #include <algorithm>
@@ -472,20 +473,53 @@ struct RmsNormNode : Function<RmsNormNode> {
 // No autograd node, but lists of tensors: with its arguments checked in Python, a step over 300
 // tensors would take several ms on the host.
 
-using Tensors = std::vector<at::Tensor>;
-using OptTensors = std::vector<OptTensor>;
+// A list or tuple of tensors or None, as Python holds it (a copy into a vector costs 60 ns for each).
+class List {
+ public:
+  explicit List(py::handle from, const char* what)
+      : held_(py::reinterpret_steal<py::object>(PySequence_Fast(from.ptr(), what))) {
+    if (!held_) throw py::error_already_set();
+  }
+  size_t size() const { return size_t(PySequence_Fast_GET_SIZE(held_.ptr())); }
+  const at::Tensor* at(size_t k) const {
+    PyObject* const o = PySequence_Fast_GET_ITEM(held_.ptr(), Py_ssize_t(k));
+    if (o == Py_None) return nullptr;
+    TORCH_CHECK_TYPE(THPVariable_Check(o), "expected a tensor, got ", Py_TYPE(o)->tp_name);
+    return &THPVariable_Unpack(o);
+  }
+  const at::Tensor& need(size_t k) const {
+    const at::Tensor* const t = at(k);
+    TORCH_CHECK_TYPE(t != nullptr, "expected a tensor, got None");
+    return *t;
+  }
 
-void adamw_step(const Tensors& params, const OptTensors& grads, const Tensors& exp_avg,
-                const Tensors& exp_avg_sq, const std::optional<Tensors>& exp_avg_scale,
-                const std::optional<Tensors>& exp_avg_sq_scale,
-                const std::optional<OptTensors>& master, const std::vector<double>& decay,
-                int64_t step, const OptTensor& step_on_device, double lr,
+ private:
+  py::object held_;
+};
+
+// decay: a number, or one for each parameter.
+void adamw_step(py::handle params_, py::handle grads_, py::handle exp_avg_, py::handle exp_avg_sq_,
+                py::handle exp_avg_scale_, py::handle exp_avg_sq_scale_, py::handle master_,
+                py::handle decay_, int64_t step, const OptTensor& step_on_device, double lr,
                 const OptTensor& lr_on_device, double beta1, double beta2, double eps,
                 const OptTensor& grad_scale, int64_t stream) {
+  auto list = [](py::handle h) {
+    return h.is_none() ? std::optional<List>() : std::optional<List>(List(h, "expected a list of tensors"));
+  };
+  const List params(params_, "expected a list of parameters"), grads(grads_, "expected a list of gradients"),
+      exp_avg(exp_avg_, "expected a list of states"), exp_avg_sq(exp_avg_sq_, "expected a list of states");
+  const auto exp_avg_scale = list(exp_avg_scale_), exp_avg_sq_scale = list(exp_avg_sq_scale_),
+             master = list(master_);
+  const bool one_decay = PyFloat_Check(decay_.ptr()) || PyLong_Check(decay_.ptr());
+  std::vector<double> decay;
+  if (one_decay)
+    decay.push_back(decay_.cast<double>());
+  else
+    decay = decay_.cast<std::vector<double>>();
   const size_t count = params.size();
   const bool eight = exp_avg_scale.has_value();
   TORCH_CHECK_VALUE(grads.size() == count && exp_avg.size() == count &&
-                        exp_avg_sq.size() == count && decay.size() == count &&
+                        exp_avg_sq.size() == count && (one_decay || decay.size() == count) &&
                         (!master || master->size() == count),
                     "there must be as many gradients, states, master copies and weight decays as "
                     "parameters");
@@ -495,7 +529,7 @@ void adamw_step(const Tensors& params, const OptTensors& grads, const Tensors& e
                     "states in 8 bits need a scale tensor for each parameter's exp_avg and "
                     "exp_avg_sq");
   if (count == 0) return;
-  const at::Device device = params[0].device();
+  const at::Device device = params.need(0).device();
   auto here = [&](const at::Tensor& t, const char* what) {
     TORCH_CHECK_VALUE(t.layout() == at::kStrided && t.is_cuda() && t.is_contiguous() &&
                           t.device() == device,
@@ -509,12 +543,14 @@ void adamw_step(const Tensors& params, const OptTensors& grads, const Tensors& e
     return t->data_ptr();
   };
   const at::ScalarType held = eight ? at::kFloat8_e4m3fn : at::kFloat;
-  std::vector<flp_adamw_tensor> list;
-  list.reserve(count);
-  Tensors written;
+  std::vector<flp_adamw_tensor> table;
+  table.reserve(count);
+  std::vector<const at::Tensor*> written;
+  written.reserve(count * 5);
   for (size_t k = 0; k < count; ++k) {
-    if (!grads[k]) continue;
-    const at::Tensor &p = params[k], &g = *grads[k];
+    const at::Tensor* const grad = grads.at(k);
+    if (grad == nullptr) continue;
+    const at::Tensor &p = params.need(k), &g = *grad;
     const int64_t n = p.numel();
     here(p, "parameters");
     here(g, "gradients");
@@ -528,50 +564,50 @@ void adamw_step(const Tensors& params, const OptTensors& grads, const Tensors& e
     t.param = ptr(p);
     t.grad = ptr(g);
     t.n = n;
-    t.weight_decay = decay[k];
+    t.weight_decay = decay[one_decay ? 0 : k];
     t.p_dtype = code(p);
     t.g_dtype = code(g);
-    written.push_back(p);
+    written.push_back(&p);
     auto state = [&](const at::Tensor& s) {
       here(s, "states");
       TORCH_CHECK_TYPE(s.scalar_type() == held, "states must be ", held,
                        eight ? " where they have scales" : " where they have no scales");
       TORCH_CHECK_VALUE(s.numel() == n, "a state must have as many elements as its parameter");
-      written.push_back(s);
+      written.push_back(&s);
       return ptr(s);
     };
     auto scale = [&](const at::Tensor& s) {
       here(s, "scales");
       TORCH_CHECK_VALUE(s.scalar_type() == at::kFloat && s.numel() == (n + 255) / 256,
                         "scales must be float32, one for each 256 elements of the parameter");
-      written.push_back(s);
+      written.push_back(&s);
       return fptr(s);
     };
-    t.exp_avg = state(exp_avg[k]);
-    t.exp_avg_sq = state(exp_avg_sq[k]);
+    t.exp_avg = state(exp_avg.need(k));
+    t.exp_avg_sq = state(exp_avg_sq.need(k));
     if (eight) {
-      t.exp_avg_scale = scale((*exp_avg_scale)[k]);
-      t.exp_avg_sq_scale = scale((*exp_avg_sq_scale)[k]);
+      t.exp_avg_scale = scale(exp_avg_scale->need(k));
+      t.exp_avg_sq_scale = scale(exp_avg_sq_scale->need(k));
     }
-    if (master && (*master)[k]) {
-      const at::Tensor& w = *(*master)[k];
+    if (master && master->at(k) != nullptr) {
+      const at::Tensor& w = master->need(k);
       here(w, "master copies");
       TORCH_CHECK_VALUE(w.scalar_type() == at::kFloat && w.numel() == n,
                         "a master copy must be float32 with its parameter's elements");
-      written.push_back(w);
+      written.push_back(&w);
       t.master = fptr(w);
     }
-    list.push_back(t);
+    table.push_back(t);
   }
   const auto* at_step = static_cast<const int64_t*>(scalar(step_on_device, at::kLong, "step"));
   const auto* at_lr = static_cast<const float*>(scalar(lr_on_device, at::kFloat, "lr"));
   const auto* at_scale = static_cast<const float*>(scalar(grad_scale, at::kFloat, "grad_scale"));
   check("flp_adamw_step",
-        api.adamw_step(int64_t(list.size()), list.data(), eight ? 8 : 32, step, at_step, lr, at_lr,
+        api.adamw_step(int64_t(table.size()), table.data(), eight ? 8 : 32, step, at_step, lr, at_lr,
                        beta1, beta2, eps, at_scale, reinterpret_cast<void*>(stream)));
   // what was saved for a backward has changed
-  for (const at::Tensor& t : written)
-    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  for (const at::Tensor* t : written)
+    if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 
 }  // namespace

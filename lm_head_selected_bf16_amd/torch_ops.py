@@ -1301,9 +1301,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Te
     float32, None leaves its parameter alone.  step: the number t of this step, from 1.
     weight_decay: one number, or one for each parameter.  step (int64), lr and grad_scale (float32)
     may be one-element tensors on the device, which a captured call reads at every replay."""
-    params = list(params)
-    if isinstance(weight_decay, (int, float)):
-        weight_decay = [weight_decay] * len(params)
+    if not isinstance(params, (list, tuple)):
+        params = list(params)
     if not params:
         return
     at_step, at_lr = (x if isinstance(x, torch.Tensor) else None for x in (step, lr))
