@@ -22,7 +22,7 @@
 // A row's sums run in an order fixed by D and the type alone, so r, n, d_x, d_y and the
 // statistics of a row are bitwise the same whatever the other rows are.  The sums over rows
 // run in slabs: within a slab each of its teams adds every k-th row in ascending order, the
-// teams are joined in order, and over the slabs sixteen sums of every sixteenth slab are
+// teams are joined in order, and over the slabs thirty-two sums of every 32nd slab are
 // joined by a fixed tree.  N, D, the number of gates and the type fix the order: no atomics.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -286,16 +286,20 @@ __global__ __launch_bounds__(kThreads) void k_rms_bwd(RmsBwdArgs p) {
   int64_t row = r0 + team;
   Row<T, TEAM, NCH> cx, cy, cr, cn;
   float rstd, rstd_y;
-  auto load = [&] {
-    const bool live = row < r1;
-    cx.load(static_cast<const T*>(p.x) + row * D, D, t, live);
-    if constexpr (Y) cy.load(static_cast<const T*>(p.y) + row * D, D, t, live);
-    cn.load(static_cast<const T*>(p.grad_n) + row * D, D, t, live && p.grad_n != nullptr);
-    cr.load(static_cast<const T*>(p.grad_r) + row * D, D, t, live && p.grad_r != nullptr);
-    rstd = live ? p.rstd[row] : 0.f;
-    rstd_y = !live ? 0.f : Y && p.post ? p.post_rstd[row] : 1.f;
+  auto load = [&](int64_t r) {  // all but y
+    const bool live = r < r1;
+    cx.load(static_cast<const T*>(p.x) + r * D, D, t, live);
+    cn.load(static_cast<const T*>(p.grad_n) + r * D, D, t, live && p.grad_n != nullptr);
+    cr.load(static_cast<const T*>(p.grad_r) + r * D, D, t, live && p.grad_r != nullptr);
+    rstd = live ? p.rstd[r] : 0.f;
   };
-  load();
+  auto load_y = [&](int64_t r) {
+    const bool live = r < r1;
+    if constexpr (Y) cy.load(static_cast<const T*>(p.y) + r * D, D, t, live);
+    rstd_y = !live ? 0.f : Y && p.post ? p.post_rstd[r] : 1.f;
+  };
+  load(row);
+  load_y(row);
   const int64_t gate_bytes = (p.wide ? 4 : int64_t(sizeof(T))) * D;
   const void* gate = p.gate == nullptr || GATES
                          ? nullptr
@@ -398,6 +402,7 @@ __global__ __launch_bounds__(kThreads) void k_rms_bwd(RmsBwdArgs p) {
         s3 += q;
       }
     }
+    load(row + kTeams);  // y's registers are the only ones still needed
     if (Y && p.d_y != nullptr) {
       float m3 = 0.f;
       if (p.post) m3 = team_sum<TEAM>(s3, red[turn][1]) * inv;
@@ -417,7 +422,7 @@ __global__ __launch_bounds__(kThreads) void k_rms_bwd(RmsBwdArgs p) {
     }
     row += kTeams;
     turn ^= 1;
-    load();
+    load_y(row);
   }
   if (p.part == nullptr) return;
   // The teams' sums side by side in LDS, added in their order.
@@ -451,13 +456,15 @@ __global__ __launch_bounds__(kThreads) void k_rms_bwd(RmsBwdArgs p) {
 }
 
 // The sums over rows from the slab partials: what = 0 d_weight, 1 d_post_weight (and with one
-// gate row, d_gate, which has the same sums), 2 + k row k of d_gate.  16 columns per workgroup,
-// sixteen threads per column each adding every sixteenth slab in ascending order (eight loads in
-// flight), then the sixteen by a fixed tree.
+// gate row, d_gate, which has the same sums), 2 + k row k of d_gate.  32 columns per workgroup,
+// thirty-two threads per column each adding every 32nd slab in ascending order (eight loads in
+// flight), then the thirty-two by a fixed tree.
+constexpr int kFoldCols = 32, kFoldWays = 32;
 template <class T>
-__global__ __launch_bounds__(256) void k_rms_fold(RmsBwdArgs p, int64_t blocks, int64_t per) {
-  __shared__ float s[16][17];
-  const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
+__global__ __launch_bounds__(kFoldCols * kFoldWays) void k_rms_fold(RmsBwdArgs p, int64_t blocks,
+                                                                    int64_t per) {
+  __shared__ float s[kFoldWays][kFoldCols + 1];
+  const int c = threadIdx.x % kFoldCols, q = threadIdx.x / kFoldCols;
   const bool one_gate = p.gate_rows == 1 && !p.gates;
   auto param = [&](const void* base, int64_t i) {
     return p.wide || sizeof(T) == 4 ? static_cast<const float*>(base)[i]
@@ -471,7 +478,7 @@ __global__ __launch_bounds__(256) void k_rms_fold(RmsBwdArgs p, int64_t blocks, 
       static_cast<T*>(out)[at] = T(v);
   };
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const int64_t what = b / per, d = (b % per) * 16 + c;
+    const int64_t what = b / per, d = (b % per) * kFoldCols + c;
     void* const out = what == 0 ? p.d_weight : what == 1 ? p.d_post_weight : p.d_gate;
     if (out == nullptr && !(what == 1 && one_gate && p.d_gate != nullptr)) continue;  // all of it
     const int64_t lo = what < 2 ? 0 : (what - 2) * p.slabs_per_gate;
@@ -481,13 +488,13 @@ __global__ __launch_bounds__(256) void k_rms_fold(RmsBwdArgs p, int64_t blocks, 
     float a = 0.f;
     if (d < p.D) {
       const float* src = p.part + (what == 0 ? 0 : p.D) + d;
-      for (int64_t k = lo + q; k < hi; k += 128) {
+      for (int64_t k = lo + q; k < hi; k += 8 * kFoldWays) {
         float v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const int64_t slab = k + 16 * u;
+          const int64_t slab = k + kFoldWays * u;
           v[u] = slab < hi ? src[slab * 2 * p.D] : 0.f;
-          if (gated && slab < hi) v[u] *= param(p.gate, slab / p.slabs_per_gate * p.D + d);
+          if (gated && slab < hi) v[u] *= param(p.gate, int64_t(uint32_t(slab) / uint32_t(p.slabs_per_gate)) * p.D + d);
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) a += v[u];
@@ -496,7 +503,7 @@ __global__ __launch_bounds__(256) void k_rms_fold(RmsBwdArgs p, int64_t blocks, 
     __syncthreads();  // the values of the turn before have been read
     s[q][c] = a;
 #pragma unroll
-    for (int h = 8; h >= 1; h >>= 1) {
+    for (int h = kFoldWays / 2; h >= 1; h >>= 1) {
       __syncthreads();
       if (q < h) s[q][c] += s[q + h][c];
     }
@@ -619,9 +626,9 @@ hipError_t rms_bwd(const RmsBwdArgs& a, hipStream_t s) {
   if (a.d_weight == nullptr && a.d_post_weight == nullptr && !gate_sums) return hipGetLastError();
   RmsBwdArgs b = a;
   if (!gate_sums) b.d_gate = nullptr;
-  const int64_t per = (a.D + 15) / 16, blocks = per * (2 + (gate_sums && a.gate_rows > 1 ? a.gate_rows : 0));
-  hipLaunchKernelGGL(k_rms_fold<T>, dim3(unsigned(std::min<int64_t>(blocks, 1 << 16))), dim3(256),
-                     0, s, b, blocks, per);
+  const int64_t per = (a.D + kFoldCols - 1) / kFoldCols, blocks = per * (2 + (gate_sums && a.gate_rows > 1 ? a.gate_rows : 0));
+  hipLaunchKernelGGL(k_rms_fold<T>, dim3(unsigned(std::min<int64_t>(blocks, 1 << 16))),
+                     dim3(kFoldCols * kFoldWays), 0, s, b, blocks, per);
   return hipGetLastError();
 }
 
