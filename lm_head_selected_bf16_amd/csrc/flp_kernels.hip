@@ -1451,7 +1451,11 @@ const char* kernel_ids() {
          "embedding: k_embed_fwd (scaled), radix sort (k_sort_hist, k_sort_scatter; 9-bit digits; <= 4096 tokens: k_sort_rank; "
          "zero riders), k_embed_runs<32-position groups>, k_embed_rows; k_dropout; layer norm: "
          "k_norm_fwd_row, k_norm_bwd_row<one or four waves per row>, k_norm_fold; wide rows: "
-         "k_norm_fwd, k_norm_dx, k_norm_params";
+         "k_norm_fwd, k_norm_dx, k_norm_params; "
+         "blocks: k_gated_fwd<256x256 8 waves, 128x128, 64x64, 32x64; both weights interleaved>, "
+         "k_gated_dz, k_gated_gemm<256x224, 128x128; ds_read_b64_tr_b16>, k_gated_fold; fp32: "
+         "k_gated_dz32, k_gemm, k_slab_fold; k_rms_fwd, k_rms_bwd<one to eight waves per row>, "
+         "k_rms_fold; k_adamw<8 or 32 bits; 2048-element tiles>";
 }
 
 }  // namespace flp

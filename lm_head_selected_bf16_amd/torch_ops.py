@@ -1305,6 +1305,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[Optional[torch.Te
         params = list(params)
     if not params:
         return
+    if not isinstance(weight_decay, (list, tuple)):
+        weight_decay = float(weight_decay)
     at_step, at_lr = (x if isinstance(x, torch.Tensor) else None for x in (step, lr))
     dev = params[0].device
     if not params[0].is_cuda:
