@@ -514,7 +514,7 @@ __global__ __launch_bounds__(kFoldCols * kFoldWays) void k_rms_fold(RmsBwdArgs p
                                 ? v * param(p.post_weight, d) : v;
       if (what == 1 && one_gate) {
         put(p.d_gate, d, to_gate);
-        v *= param(p.gate, d);
+        if (p.gate != nullptr) v *= param(p.gate, d);
       }
       if (what < 2)
         put(out, d, v);
@@ -626,6 +626,7 @@ hipError_t rms_bwd(const RmsBwdArgs& a, hipStream_t s) {
   if (a.d_weight == nullptr && a.d_post_weight == nullptr && !gate_sums) return hipGetLastError();
   RmsBwdArgs b = a;
   if (!gate_sums) b.d_gate = nullptr;
+  if (a.slabs == 0) b.gate = b.post_weight = nullptr;  // no rows: zeros, whatever they hold
   const int64_t per = (a.D + kFoldCols - 1) / kFoldCols, blocks = per * (2 + (gate_sums && a.gate_rows > 1 ? a.gate_rows : 0));
   hipLaunchKernelGGL(k_rms_fold<T>, dim3(unsigned(std::min<int64_t>(blocks, 1 << 16))),
                      dim3(kFoldCols * kFoldWays), 0, s, b, blocks, per);

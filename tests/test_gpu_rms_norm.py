@@ -261,6 +261,25 @@ def test_empty_batch():
     assert grads[0].shape == (0, 64) and all(not bool(v.any()) for v in grads[2:])
 
 
+@pytest.mark.parametrize("gates", [0, 1, 3])
+def test_no_rows_through_the_abi(gates):
+    """Without rows nothing is read, null pointers and infinite parameters neither: the sums over
+    rows are zeros."""
+    m = flp()
+    D = 37
+    w = torch.full((D,), math.inf, device="cuda", dtype=F16)
+    out = [torch.ones(n, D, device="cuda", dtype=F16) for n in (1, 1, max(gates, 1))]
+    for gate, post in ((0, 0), (0, w.data_ptr()), (out[0].data_ptr(), 0)):
+        for t in out[1:]:
+            t.fill_(1)
+        st = m._abi.flp_residual_rms_norm_backward(
+            0, D, m.FLP_F16, 0, 0, 0, 0, m.FLP_F16, 0, 1, post, gates, 0 if gates != 1 else gate, 0.5,
+            0, 0, 0, 0, 0, out[1].data_ptr(), out[2].data_ptr() if gates else 0, 0, 0,
+            torch.cuda.current_stream().cuda_stream)
+        assert st == m.FLP_OK
+        assert not bool(out[1].any()) and not (gates and bool(out[2].any()))
+
+
 @pytest.mark.parametrize("gates", [0, 1, 6, 24])
 @pytest.mark.parametrize("post", [False, True])
 def test_gradient_against_differences(gates, post):
