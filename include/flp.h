@@ -665,7 +665,8 @@ flp_status flp_rms_norm_backward(int64_t N, int64_t D, flp_dtype x_dtype, const 
  *                post_norm).
  *   gate         [gate_rows, D] of w_dtype, N a multiple of gate_rows: row i takes gate row
  *                i / (N / gate_rows).  One row is a gate per channel, one per sequence a
- *                modulation, N rows a gate per element.  NULL with gate_rows = 0 for 1.
+ *                modulation, N rows a gate per element; others than N at most 2^22.  NULL with
+ *                gate_rows = 0 for 1.
  *   scale        finite.
  *   out_rstd, out_post_rstd  [N] float32, or NULL; the backward reads them (the second with
  *                post_norm only).

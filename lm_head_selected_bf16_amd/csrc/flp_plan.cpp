@@ -994,8 +994,10 @@ flp_status check_rms(int64_t N, int64_t D, flp_dtype x_dtype, flp_dtype w_dtype,
   if (gate_rows < 0 || !(std::fabs(scale) <= double(std::numeric_limits<float>::max())))
     return FLP_INVALID_ARGUMENT;
   if (D > kRmsMaxWidth) return FLP_UNSUPPORTED_SHAPE;
-  // a launch of a workgroup per slab, and of one per sixteen columns of a gate, stays in range
   if (N >= (int64_t(1) << 31)) return FLP_UNSUPPORTED_SHAPE;
+  // the backward's workgroups of 512 threads, one for each of a gate row's rows at least, stay
+  // below 2^32 threads in a launch
+  if (N > gate_rows && gate_rows > kRmsMaxGates) return FLP_UNSUPPORTED_SHAPE;
   if (N > 0) {
     if (gate_rows > 0 && N % gate_rows != 0) return FLP_INVALID_ARGUMENT;
     if ((gate != nullptr) != (gate_rows > 0)) return FLP_INVALID_ARGUMENT;

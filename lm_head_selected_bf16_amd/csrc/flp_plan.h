@@ -177,6 +177,7 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need
 
 // ---- root mean square norms backward: slabs of rows, within the rows of one gate ----
 constexpr int64_t kRmsMaxWidth = 16384;  // elements that the eight waves of a team hold
+constexpr int64_t kRmsMaxGates = int64_t(1) << 22;  // gate rows that several rows share
 struct RmsLayout {
   bool gates = false;        // a gate row for each row: the slabs need not respect them
   int64_t rows_per_gate = 0, slab_rows = 0, slabs_per_gate = 0, slabs = 0;

@@ -133,6 +133,7 @@ SHARED = [
     (dict(scale=1e39), "FLP_INVALID_ARGUMENT"),
     (dict(gates=3), "FLP_INVALID_ARGUMENT"),             # 40 rows
     (dict(gates=-1), "FLP_INVALID_ARGUMENT"),
+    (dict(N=1 << 24, gates=1 << 23), "FLP_UNSUPPORTED_SHAPE"),
     (dict(gates=0), "FLP_INVALID_ARGUMENT"),             # a gate without rows
     (dict(gate=0), "FLP_INVALID_ARGUMENT"),              # rows without a gate
     (dict(post=0), "FLP_INVALID_ARGUMENT"),              # post_weight without post_norm
