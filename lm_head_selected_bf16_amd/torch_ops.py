@@ -1270,6 +1270,7 @@ def adamw_state(params: Sequence[torch.Tensor], bits: int = 32, master: bool = F
     copy of every 16-bit parameter."""
     if bits not in (8, 32):
         raise ValueError("bits must be 8 or 32")
+    params = list(params)
     copies = None
     if master:
         copies = [None if p.dtype == torch.float32 else p.detach().float().contiguous()

@@ -108,6 +108,15 @@ def test_adamw_python_checks():
     assert s.exp_avg_sq[0].dtype == torch.float8_e4m3fn
 
 
+def test_adamw_state_of_an_iterator():
+    """As of a module's parameters()."""
+    p = [torch.ones(3, dtype=torch.bfloat16), torch.ones(2, 2)]
+    for bits in (8, 32):
+        s = flp.adamw_state(iter(p), bits=bits, master=True)
+        assert [t.shape for t in s.exp_avg] == [t.shape for t in s.exp_avg_sq] == [(3,), (2, 2)]
+        assert len(s.master) == 2
+
+
 # ---- root mean square norms --------------------------------------------------------------------
 
 N, D = 40, 64
