@@ -1160,6 +1160,8 @@ def residual_rms_norm_forward(x: torch.Tensor, y: torch.Tensor,
                               return_stats: bool = True):
     """(r, n, rstd, post_rstd) of residual_rms_norm through flp_residual_rms_norm_forward; the
     statistics are float32 of the leading shape, or None (post_rstd without post_norm)."""
+    if not isinstance(y, torch.Tensor):
+        raise TypeError("y must be a tensor (rms_norm has none)")
     post = post_weight is not None if post_norm is None else bool(post_norm)
     N, D, wd, G = _prepare_rms(x, y, weight, post_weight, gate, post)
     dev = x.device
@@ -1235,6 +1237,8 @@ def residual_rms_norm(x, y, weight=None, post_weight=None, gate=None, scale=1.0,
     or with a row for each leading index of x ([B, D] or [B, 1, D] for x [B, S, D]; x's own shape
     for a gate per element), or [G, D] for x [N, D], each row for N / G rows in turn; all of them
     in the dtype of x or all in float32."""
+    if not isinstance(y, torch.Tensor):
+        raise TypeError("y must be a tensor (rms_norm has none)")
     if not _wants_grad(x, y, weight, post_weight, gate):
         return residual_rms_norm_forward(x, y, weight, post_weight, gate, scale, eps, post_norm,
                                          return_stats=False)[:2]

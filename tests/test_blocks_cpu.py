@@ -321,3 +321,11 @@ def test_gated_linear_sizes():
     assert size(64, 64, 128, F32, 1, 0) == 2 * 128 * 64 * 4 + 2 * 128 * 64 * 4
     assert size(40, 64, 128, F32, 0, 1) == 2 * 128 * 64 * 4 + 64 * 64 * 4
     assert size(0, 64, 128, BF16, 1, 1) == 0
+
+
+def test_residual_rms_norm_needs_the_block():
+    for x in (torch.ones(2, 4), torch.ones(2, 4, requires_grad=True)):
+        with pytest.raises(TypeError):
+            flp.residual_rms_norm(x, None)
+    with pytest.raises(TypeError):
+        flp.residual_rms_norm_forward(torch.ones(2, 4), None)
