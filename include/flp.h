@@ -721,7 +721,8 @@ flp_status flp_residual_rms_norm_backward(
  *                [ceil(n / 256)] float32 (the block's largest magnitude, at least 2^-100,
  *                over 448).  The step itself uses m and v before they are rounded.  A positive
  *                root rounds to no less than the smallest positive code.  A gradient that is
- *                not finite makes its block's states NaN (in 32 bits, its element's).
+ *                not finite reaches its own element's parameter and states, and in 8 bits an
+ *                infinite one makes all of its block's states NaN.
  *   step         number t of this step, from 1; or step_on_device, one int64 that the kernel
  *                reads (below 1 counts as 1), so that a captured call takes part in every
  *                replay's own step.  The caller counts.

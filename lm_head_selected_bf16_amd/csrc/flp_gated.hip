@@ -64,8 +64,9 @@ __device__ __forceinline__ void act_of(float z, float& f, float& slope) {
     f = z < 0.f ? tail : 1.0f - tail;
     slope = fmaf(z * 0.39894228040143268f, q, f);
   } else if constexpr (ACT == FLP_ACT_GELU_TANH) {
-    f = sigmoid(kTanhA * z * fmaf(kTanhB * z, z, 1.0f));
-    slope = fmaf(z * f * (1.0f - f), kTanhA * fmaf(3.0f * kTanhB * z, z, 1.0f), f);
+    const float zz = fminf(z * z, 0x1p120f);  // finite: f (1 - f) = 0 meets it in the slope
+    f = sigmoid(kTanhA * z * fmaf(kTanhB, zz, 1.0f));
+    slope = fmaf(z * f * (1.0f - f), kTanhA * fmaf(3.0f * kTanhB, zz, 1.0f), f);
   } else {
     f = sigmoid(z);
     slope = f * fmaf(z, 1.0f - f, 1.0f);

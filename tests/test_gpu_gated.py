@@ -147,6 +147,23 @@ def test_far_arguments(name, dtype):
         assert float((v.double() - ref[k]).norm() / ref[k].norm()) <= 4 * half_step(dtype) + 1e-5
 
 
+@pytest.mark.parametrize("big", [2.0 ** 65, 2.0 ** 70, 2.0 ** 120])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("name", ACTS)
+def test_arguments_whose_squares_pass_fp32(name, dtype, big):
+    """act(z) is z or 0 there and its slope 1 or 0, exactly."""
+    m = flp()
+    x = torch.zeros(2, 32, dtype=dtype, device="cuda")
+    x[0, 0], x[1, 0], x[:, 1] = big, -big, 1.0
+    wg, wu = (torch.zeros(1, 32, dtype=dtype, device="cuda") for _ in range(2))
+    wg[0, 0] = wu[0, 1] = 1.0
+    out, saved = m.gated_linear_forward(x, wg, wu, name)
+    assert out.view(-1).tolist() == [big, 0.0]
+    go = torch.ones_like(out)
+    dx = m.gated_linear_backward(go, saved, x, wg, wu, name, need_gate=False, need_up=False)[0]
+    assert dx[:, 0].tolist() == [1.0, 0.0] and dx[:, 1].tolist() == [big, 0.0]
+
+
 def test_infinite_and_nan_rows_stay_by_themselves():
     x, wg, wu, go = make(70, 96, 200, BF16, 4)
     clean = run(x, wg, wu, go, "silu")
