@@ -607,8 +607,8 @@ flp_status flp_gated_linear_forward(int64_t N, int64_t D, int64_t F, flp_dtype x
  *
  * For 16-bit types dz and du are rounded to x_dtype on the way, whose matrix instructions take
  * operands of that type; the products' sums are fp32 and rounded once.  They run in an order
- * fixed by the sizes; d_x of a row is bitwise the same among batches of up to 2048 rows, among
- * those of up to 8192 and among larger ones.  N = 0 writes zeros to d_w_gate and d_w_up.
+ * fixed by the sizes; d_x of a row is bitwise the same among batches of up to 512 rows, and
+ * among those of more, up to 1024, 2048, 8192 and beyond.  N = 0 writes zeros to d_w_gate and d_w_up.
  */
 size_t flp_gated_linear_backward_workspace_bytes(int64_t N, int64_t D, int64_t F,
                                                  flp_dtype x_dtype, int need_d_x,

@@ -893,10 +893,11 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need
   }
   size_t acc = 0;
   if (need_dx) {
-    // as many slabs as the smallest batch of the size needs
-    const int64_t least = N <= kGatedRowsSmall ? 1 : N <= kGatedRowsMiddle ? kGatedRowsSmall
-                                                                            : kGatedRowsMiddle;
-    L.dx_slab = slab_of(K, ceil_div(kGatedTiles * 128 * 128, least * D));
+    // what the smallest batch of the class needs to fill the chip, and no less than the class's own
+    int64_t least = 1, own = kGatedSlabs;
+    for (const GatedRows& c : kGatedRows)
+      if (N > c.above) least = c.above + 1, own = c.slabs;
+    L.dx_slab = slab_of(K, std::max(own, std::min(kGatedSlabs, ceil_div(kGatedTiles * 128 * 128, least * D))));
     if (L.dx_slab > 0) acc = size_t(ceil_div(K, L.dx_slab)) * N * D * 4;
   }
   if (need_dw && !wide) {

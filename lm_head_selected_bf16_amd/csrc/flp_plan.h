@@ -156,9 +156,20 @@ inline uint32_t dropout_threshold(double p) { return uint32_t(p * 65536.0 + 0.5)
 // ---- gated projection backward ----
 constexpr int64_t kGatedPad = 64;  // columns of dz, and tokens of fp32 transposes, are padded to this
 // Sums over slabs of K where a product has too few output tiles to fill the chip.  d_x: the number
-// of slabs depends on D, F, the type and which of three sizes the batch has, so that a row's d_x
-// does not depend on the others of such a batch; the weight gradients: on all sizes.
-constexpr int64_t kGatedRowsSmall = 2048, kGatedRowsMiddle = 8192;
+// of slabs depends on D, F, the type and which of five classes the batch's size is in, so that a
+// row's d_x does not depend on the others of such a batch; the weight gradients: on all sizes.
+//
+// d_x of bf16 (with dz), D x F = 2688 x 7168 | 1344 x 3587, in us by the number of slabs:
+//   512 rows    1: 124 | 66    5: 73 | 31    8: 61 | 37
+//   768 rows    1: 130 | 68    2: 91 | 47    5: 82 | 45    8: 109 | 43
+//   1000 rows   1: 137 | 69    2: 132 | 50   5: 97 | 48    8: 122 | 47
+//   1536 rows   1: 156 | 75    2: 148 | 69   3: 139 | 61   8: 193 | 71
+//   2048 rows   1: 230 | 83    2: 182 | 77   3: 257 | 86   8: 224 | 92
+//   3000 rows   1: 282 | 114   2: 335 | 114  3: 280 | 90   8: 357 | 121
+struct GatedRows {
+  int64_t above, slabs;  // batches of more rows; their slabs, at least
+};
+constexpr GatedRows kGatedRows[] = {{512, 5}, {1024, 2}, {2048, 1}, {8192, 1}};
 constexpr int64_t kGatedSlabs = 8, kGatedTiles = 160;
 struct GatedLayout {
   int64_t fp = 0, np = 0;    // F and N rounded up to kGatedPad

@@ -18,6 +18,9 @@
 //
 // Bound by memory: the forward reads x and y and writes r and n, the backward reads both
 // gradients, x and y and writes d_x and d_y; every row is read once and held in registers.
+// Measured, 16384 x 2688 bf16 with both norms and a gate: forward 70 us (5.0 TB/s), backward 119
+// (4.4 TB/s, two workgroups per compute unit by its registers) and the fold 6; 4097 x 1345 fp16
+// with fp32 parameters 20, 27 and 8.
 //
 // A row's sums run in an order fixed by D and the type alone, so r, n, d_x, d_y and the
 // statistics of a row are bitwise the same whatever the other rows are.  The sums over rows
@@ -39,7 +42,8 @@ namespace {
 
 // A row belongs to a team of one wave, of four or of eight (by_width_* below).
 constexpr int kThreads = 512;
-// Workgroups of a forward launch: two per compute unit.
+// Workgroups of a forward launch: two per compute unit (16384 x 2688 bf16 with y: 256 of them 74 us,
+// 512 and 768 74 to 76, 1024 78, 2048 82; 16384 x 512 fp32: 23.4, 22.5, 22.6, 23.9, 28.3).
 constexpr int64_t kFwdGroups = 512;
 
 // Sum over the team, the same bits in every thread.  A team of several waves meets in LDS
@@ -548,7 +552,8 @@ void by_width_fwd(int64_t D, F f) {
 }
 
 // Backward: four rows' chunks and two sums for each, so one wave holds up to four chunks per
-// thread of a 16-bit row (six spill), three of an fp32 one, and two waves three.
+// thread of a 16-bit row (six spill), three of an fp32 one, and two waves three.  (16384 x 2688
+// bf16: one wave with six 139 us, two with three 127; 4097 x 1345 fp16: four waves 36, one 28.)
 template <class T, class F>
 void by_width_bwd(int64_t D, F f) {
   using std::integral_constant;
