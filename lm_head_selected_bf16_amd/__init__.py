@@ -11,8 +11,11 @@ Also behind the same ABI: the vocabulary-shard partial forward and its merge
 (forward_partial, merge), the operator on materialised logits (logits_logp,
 logits_forward, logits_backward), the indexed row-subset variants of both
 operators (linear_logp_indexed, logits_logp_indexed, ...), the untied embedding
-lookup with its deterministic grad_weight (embedding), and measurement probes
-(flp_probe_mfma, flp_probe_read).
+lookup with its deterministic grad_weight (embedding), dropout, layer norm, the head's
+training loss (linear_cross_entropy), the gated projection of a feed-forward block
+(gated_linear), the norms around a block (rms_norm, residual_rms_norm), an AdamW step
+over many tensors (adamw_state, adamw_step), and measurement probes (flp_probe_mfma,
+flp_probe_read).
 """
 from ._abi import (FLP_BF16, FLP_F16, FLP_F32, FLP_I32, FLP_I64, FLP_OK, FlpError,  # noqa: F401
                    flp_backward, flp_backward_chunk_rows, flp_backward_indexed,
