@@ -193,6 +193,17 @@ def test_rows_do_not_depend_on_each_other(dtype):
     assert torch.equal(out[20:], m.gated_linear(x[:40].contiguous(), wg, wu))
 
 
+@pytest.mark.parametrize("few,many", [(1, 512), (513, 1024), (1025, 2048), (2049, 2100)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_d_x_within_a_class_of_batches(dtype, few, many):
+    """The batch sizes between which d_x has the same slabs, from their smallest to their largest."""
+    x, wg, wu, go = make(many, 672, 1500, dtype, 6)
+    whole = run(x, wg, wu, go, "silu")
+    part = run(x[-few:].contiguous(), wg, wu, go[-few:].contiguous(), "silu")
+    for k in ("out", "dx"):
+        assert torch.equal(whole[k][-few:], part[k]), k
+
+
 def test_halves_of_one_weight_and_odd_offsets():
     m = flp()
     x, wg, wu, go = make(50, 96, 129, BF16, 6)
