@@ -280,6 +280,14 @@ struct Elem<F32> {
   using T = float;
 };
 
+// What the lanes of a wave wrote to LDS is there for its other lanes behind this.  The hardware keeps
+// a wave's LDS accesses in order, so it costs no instruction; the fences keep the compiler to it.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // 16-bit types: [dz | du] as rows.  A wave takes 16 rows x 64 columns: the gradient as whole
 // lines, through LDS into the lanes of the kept blocks, and dz and du back through LDS into whole
 // lines (straight from the lanes, 32 bytes of a row at a time, 361 us for 16384 x 7168; 280 with
@@ -311,6 +319,7 @@ __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       *reinterpret_cast<u32x4*>(one + (lr + 8 * q) * kPitch + lc) = gr[q].w[0];
+    wave_exchange();  // the lines have been written by all lanes
     u32x2 dz[4], du[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -329,14 +338,14 @@ __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
       dz[k] = u32x2{pack2<E>(z[0], z[1]), pack2<E>(z[2], z[3])};
       du[k] = u32x2{pack2<E>(u[0], u[1]), pack2<E>(u[2], u[3])};
     }
-    __builtin_amdgcn_wave_barrier();  // the gradient has been read by all lanes of the wave
+    wave_exchange();  // the gradient has been read
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int at = i * kPitch + k * 16 + 4 * g;
       *reinterpret_cast<u32x2*>(one + at) = dz[k];
       *reinterpret_cast<u32x2*>(two + at) = du[k];
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_exchange();
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int64_t row = row0 + lr + 8 * q;
@@ -348,7 +357,7 @@ __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
         *reinterpret_cast<u32x4*>(out + p.ld_saved) = u;
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_exchange();
   }
 }
 
