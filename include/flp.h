@@ -719,8 +719,13 @@ flp_status flp_residual_rms_norm_backward(
  *                8: they are [n] bytes, e4m3 codes of m and of the ROOT of v in units of a
  *                scale per 256 consecutive elements, exp_avg_scale and exp_avg_sq_scale
  *                [ceil(n / 256)] float32 (the block's largest magnitude, at least 2^-100,
- *                over 448).  The step itself uses m and v before they are rounded.  A positive
- *                root rounds to no less than the smallest positive code.  A gradient that is
+ *                over 448).  The step itself uses m and v before they are rounded.  Codes are
+ *                rounded to nearest where beta1 <= 0.9 and beta2 <= 0.95.  With longer windows
+ *                a step moves a state by far less than half a code, and nearest rounding would
+ *                hold it still: they are rounded up or down by a threshold that depends on the
+ *                step's number and the element's index alone, to within one code and right on
+ *                average over the steps (so the number has to count on from step to step).  A
+ *                positive root rounds to no less than the smallest positive code.  A gradient that is
  *                not finite reaches its own element's parameter and states, and in 8 bits an
  *                infinite one makes all of its block's states NaN.
  *   step         number t of this step, from 1; or step_on_device, one int64 that the kernel

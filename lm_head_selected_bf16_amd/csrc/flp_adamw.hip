@@ -10,6 +10,20 @@
 // is its root: its range halves that way, and the update divides by the root.  A positive
 // root never rounds to 0: a coordinate whose m survives would otherwise be divided by eps.
 //
+// Half a step of e4m3 is 3 to 6 % of the value, while one step of the optimizer moves the root by
+// (1 - b2) / 2 of itself, 0.05 % at b2 = 0.999: rounded to nearest it would stand still.  So codes
+// are rounded up or down by a threshold that runs over time evenly through all of the step between
+// two codes (multiples of an irrational number, plus an offset of the element's own, a function of
+// step and index alone): what a code holds is right on average, and a drift far below half a step
+// arrives.  The roots' distribution around fp32's, gradients of fixed spread, and of a spread that
+// fell to a tenth (5 %, median, 95 % of the elements after six windows of b2 and more):
+//   b2 = 0.95    nearest 0.91 1.06 1.22, 0.90 1.03 1.25    dithered 0.85 1.00 1.16, 0.87 0.99 1.17
+//   b2 = 0.98    nearest 1.14 1.57 1.96, 5.8  11.6 16.7    dithered 0.81 1.00 1.21, 0.84 0.98 1.22
+//   b2 = 0.999   nearest 0.81 1.15 1.52, 6.4  9.0  13.2    dithered 0.77 1.00 1.25, 0.79 0.95 1.23
+// To nearest where b1 <= 0.9 and b2 <= 0.95: there the gradients' own spread moves a root by more
+// than half a step between two codes, an m without gradients decays by more than one, and each code is
+// within half a step of its value.
+//
 // Bound by memory: one pass over grad, p, m, v and the master copies.  Measured: 347 M bf16
 // elements with master copies and 32-bit states 1812 us, 5.36 TB/s; 584 M with 8-bit states and
 // none 1071 us, 5.45 TB/s (a large copy reaches 5.1).
@@ -87,9 +101,33 @@ __device__ __forceinline__ float block_max(float x) {
   return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 
+// How the states are held: fp32, or codes rounded to nearest or by the threshold of the step.
+enum Held { kWide, kNearest, kDithered };
+
+// The odd integers nearest to 2^32 times (sqrt(5) - 1) / 2, sqrt(1 / 2) and sqrt(3) / 2: multiples of
+// these, modulo 2^32, fill the range evenly.
+constexpr uint32_t kGolden = 0x9E3779B9u, kRoot2 = 0xB504F333u, kRoot3 = 0xDDB3D743u;
+
+// Thresholds of a chunk (its element e has kRoot3 e more).
+__device__ __forceinline__ uint32_t chunk_offset(int64_t chunk) {
+  uint32_t h = (uint32_t(chunk) * kGolden) ^ (uint32_t(uint64_t(chunk) >> 32) * kRoot3);
+  h ^= h >> 16;
+  h *= kRoot2;
+  return h ^ (h >> 15);
+}
+
+// q on the grid of e4m3, away from 0 where what it is past a grid point, as a part of the step to
+// the next, is at least 1 - u / 2^32 (in 20 bits: fp32's mantissa has 20 more than e4m3's).
+__device__ __forceinline__ float to_grid(float q, uint32_t u) {
+  const float a = fminf(fabsf(q), kTop);
+  const float base = a < 0x1p-6f ? 0x1p-6f : 0.f;  // below 2^-6 the grid's step is that of 2^-6
+  const uint32_t b = (__float_as_uint(a + base) + (u >> 12)) & 0xFFF00000u;
+  return q == q ? copysignf(__uint_as_float(b) - base, q) : q;
+}
+
 // Codes of x and the block's scale.  The ratio is at most 448 (1 + 2^-22), which rounds to 448.
-template <bool DIVISOR>
-__device__ __forceinline__ u32x2 encode(const float (&x)[kChunk], float& scale) {
+template <bool DIVISOR, bool DITHER>
+__device__ __forceinline__ u32x2 encode(const float (&x)[kChunk], float& scale, uint32_t u) {
   float top = 0.f;
 #pragma unroll
   for (int k = 0; k < kChunk; ++k) top = fmaxf(top, fabsf(x[k]));
@@ -100,6 +138,7 @@ __device__ __forceinline__ u32x2 encode(const float (&x)[kChunk], float& scale) 
 #pragma unroll
   for (int k = 0; k < kChunk; ++k) {
     q[k] = x[k] * inv;
+    if (DITHER) q[k] = to_grid(q[k], u + uint32_t(k) * kRoot3);
     if (DIVISOR) q[k] = x[k] > 0.f && q[k] < kLeast ? kLeast : q[k];  // NaN stays
   }
   u32x2 w;
@@ -136,16 +175,20 @@ __device__ __forceinline__ void roots_of(const float (&v)[kChunk], float (&root)
 
 // P, G: element types of the parameters and gradients.
 //
-// m and v are rounded after every product and sum, as the formula in fp32 tensors does it: the
-// codes of both then agree with it bit for bit, where a fused product would move some of them
+// m and v are rounded after every product and sum, as the formula in fp32 tensors does it: codes
+// rounded to nearest then agree with it bit for bit, where a fused product would move some of them
 // across a rounding border.
-template <class P, class G, bool EIGHT, bool MASTER>
+template <class P, class G, Held HELD, bool MASTER>
 __global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
+  constexpr bool kEight = HELD != kWide;
   // 1 / (1 - b1^t) and 1 / sqrt(1 - b2^t) in 64 bits: fp32 loses the early steps of b2 near 1
   double lr = a.lr, c1 = a.c1, c2 = a.c2;
+  uint32_t step_now = a.step;
   if (a.lr_on_device != nullptr) lr = *a.lr_on_device;
   if (a.step_on_device != nullptr) {
-    const double t = double(max(*a.step_on_device, int64_t(1)));
+    const int64_t step = max(*a.step_on_device, int64_t(1));
+    const double t = double(step);
+    step_now = uint32_t(step);
     c1 = -1.0 / expm1(t * a.log_b1);
     c2 = 1.0 / sqrt(-expm1(t * a.log_b2));
   }
@@ -174,7 +217,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
       w.load(t.master + at, n);
     else
       c.load(static_cast<const P*>(t.param) + at, n);
-    if constexpr (EIGHT) {
+    if constexpr (kEight) {
       const int64_t block = at / kAdamBlock;
       const u32x2 cm = load_codes(static_cast<const uint8_t*>(t.m) + at, n);
       const u32x2 cv = load_codes(static_cast<const uint8_t*>(t.v) + at, n);
@@ -218,10 +261,13 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) c.v[e] = P(p[e]);
     c.store(static_cast<P*>(t.param) + at, n);
-    if constexpr (EIGHT) {
+    if constexpr (kEight) {
       // past the tensor's end everything is 0, which changes no block's scale
       float sm, sv;
-      const u32x2 cm = encode<false>(m, sm), cv = encode<true>(root, sv);
+      constexpr bool kDither = HELD == kDithered;
+      const uint32_t u = kDither ? chunk_offset(at / kChunk) : 0u;
+      const u32x2 cm = encode<false, kDither>(m, sm, u + step_now * kGolden);
+      const u32x2 cv = encode<true, kDither>(root, sv, ((u << 16) | (u >> 16)) + step_now * kRoot2);
       store_codes(static_cast<uint8_t*>(t.m) + at, n, cm);
       store_codes(static_cast<uint8_t*>(t.v) + at, n, cv);
       if ((threadIdx.x & (kAdamBlock / kChunk - 1)) == 0 && n > 0) {
@@ -279,14 +325,19 @@ hipError_t launch_adamw(flp_dtype p, flp_dtype g, bool eight, bool master, AdamA
   by_types(p, g, [&](auto x, auto y) {
     using P = decltype(x);
     using G = decltype(y);
-    if (eight && master)
-      hipLaunchKernelGGL((k_adamw<P, G, true, true>), grid, dim3(kThreads), 0, s, a);
-    else if (eight)
-      hipLaunchKernelGGL((k_adamw<P, G, true, false>), grid, dim3(kThreads), 0, s, a);
-    else if (master)
-      hipLaunchKernelGGL((k_adamw<P, G, false, true>), grid, dim3(kThreads), 0, s, a);
+    auto run = [&](auto held) {
+      constexpr Held kHeld = decltype(held)::value;
+      if (master)
+        hipLaunchKernelGGL((k_adamw<P, G, kHeld, true>), grid, dim3(kThreads), 0, s, a);
+      else
+        hipLaunchKernelGGL((k_adamw<P, G, kHeld, false>), grid, dim3(kThreads), 0, s, a);
+    };
+    if (!eight)
+      run(std::integral_constant<Held, kWide>{});
+    else if (a.dither)
+      run(std::integral_constant<Held, kDithered>{});
     else
-      hipLaunchKernelGGL((k_adamw<P, G, false, false>), grid, dim3(kThreads), 0, s, a);
+      run(std::integral_constant<Held, kNearest>{});
   });
   return hipGetLastError();
 }

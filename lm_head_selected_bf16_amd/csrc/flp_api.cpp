@@ -1269,6 +1269,8 @@ flp_status flp_adamw_step(int64_t n_tensors, const flp_adamw_tensor* tensors, in
   a.b2 = float(beta2);
   a.one_b2 = float(1.0 - beta2);
   a.eps = float(eps);
+  a.step = uint32_t(step);
+  a.dither = adamw_dithers(beta1, beta2);
   // Each mix of types in launches of its own, its tensors in their order.
   const flp_dtype types[] = {FLP_BF16, FLP_F16, FLP_F32};
   for (int mix = 0; mix < 12; ++mix) {

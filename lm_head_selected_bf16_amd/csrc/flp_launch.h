@@ -373,6 +373,8 @@ struct AdamArgs {
   const int64_t* step_on_device;  // or null
   const float* grad_scale;        // or null
   float b1, one_b1, b2, one_b2, eps;
+  uint32_t step;             // without one on the device: its lower bits
+  bool dither;               // 8-bit states: rounded by the step's thresholds, not to nearest
   int count;
   int64_t tiles;             // set by the launcher
   AdamTensor t[kAdamTensors];

@@ -198,6 +198,8 @@ RmsLayout rms_layout(int64_t N, int64_t D, int64_t gate_rows);
 
 // ---- AdamW: elements that share a scale of the 8-bit states ----
 constexpr int64_t kAdamBlock = 256;
+// ---- whether their codes are rounded by thresholds (flp_adamw.hip), which longer windows need ----
+inline bool adamw_dithers(double beta1, double beta2) { return beta1 > 0.9 || beta2 > 0.95; }
 
 // ---- validation (pure host logic; never dereferences a pointer) ----
 flp_status validate_forward(int64_t N, int64_t D, int64_t V, flp_dtype x_dtype,

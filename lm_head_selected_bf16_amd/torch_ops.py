@@ -1259,7 +1259,9 @@ class AdamWState(NamedTuple):
     mean m of the gradients, exp_avg_sq that of their squares, v.  States in 8 bits are
     float8_e4m3fn, exp_avg_sq holding the root of v, with float32 scales for 256 consecutive
     elements each: element i of tensor k stands for
-    exp_avg[k].view(-1)[i] * exp_avg_scale[k][i // 256].  master: float32 copies of the
+    exp_avg[k].view(-1)[i] * exp_avg_scale[k][i // 256].  Steps with beta1 > 0.9 or beta2 > 0.95
+    round them up or down by a threshold of the step's number and the element's index, so that they
+    are right on average over the steps.  master: float32 copies of the
     parameters (None for a parameter without one), or None."""
     exp_avg: List[torch.Tensor]
     exp_avg_sq: List[torch.Tensor]
