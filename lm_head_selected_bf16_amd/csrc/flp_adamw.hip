@@ -186,11 +186,17 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
   uint32_t step_now = a.step;
   if (a.lr_on_device != nullptr) lr = *a.lr_on_device;
   if (a.step_on_device != nullptr) {
+    __shared__ double corrections[2];
     const int64_t step = max(*a.step_on_device, int64_t(1));
     const double t = double(step);
     step_now = uint32_t(step);
-    c1 = -1.0 / expm1(t * a.log_b1);
-    c2 = 1.0 / sqrt(-expm1(t * a.log_b2));
+    if (threadIdx.x < 64) {  // one wave: these take some hundred instructions
+      corrections[0] = -1.0 / expm1(t * a.log_b1);
+      corrections[1] = 1.0 / sqrt(-expm1(t * a.log_b2));
+    }
+    __syncthreads();
+    c1 = corrections[0];
+    c2 = corrections[1];
   }
   const float rate = float(lr * c1), root_scale = float(c2);
   const float grad_scale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
