@@ -727,7 +727,8 @@ flp_status flp_residual_rms_norm_backward(
  *                average over the steps (so the number has to count on from step to step).  A
  *                positive root rounds to no less than the smallest positive code.  A gradient that is
  *                not finite reaches its own element's parameter and states, and in 8 bits an
- *                infinite one makes all of its block's states NaN.
+ *                infinite one makes all of its block's states NaN (one whose square alone passes
+ *                fp32, those in exp_avg_sq).
  *   step         number t of this step, from 1; or step_on_device, one int64 that the kernel
  *                reads (below 1 counts as 1), so that a captured call takes part in every
  *                replay's own step.  The caller counts.

@@ -125,14 +125,15 @@ __device__ __forceinline__ float to_grid(float q, uint32_t u) {
   return q == q ? copysignf(__uint_as_float(b) - base, q) : q;
 }
 
-// Codes of x and the block's scale.  The ratio is at most 448 (1 + 2^-22), which rounds to 448.
+// Codes of x and the block's scale.  The ratio is at most 448 (1 + 2^-22), which rounds to 448.  The
+// scale of a block with an infinite element is NaN, and so is then all that it holds.
 template <bool DIVISOR, bool DITHER>
 __device__ __forceinline__ u32x2 encode(const float (&x)[kChunk], float& scale, uint32_t u) {
   float top = 0.f;
 #pragma unroll
   for (int k = 0; k < kChunk; ++k) top = fmaxf(top, fabsf(x[k]));
   top = fmaxf(block_max(top), kBlockFloor);
-  scale = top * (1.0f / kTop);
+  scale = top < __builtin_inff() ? top * (1.0f / kTop) : __builtin_nanf("");
   const float inv = (1.0f / top) * kTop;
   float q[kChunk];
 #pragma unroll

@@ -154,3 +154,27 @@ def test_the_same_bits_from_the_hosts_and_the_devices_number():
     for other in runs[1:]:
         for x, y in zip(runs[0], other):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("betas", [(0.9, 0.95), (0.9, 0.999)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_an_infinite_gradient_takes_its_blocks_states(bad, betas):
+    """All states of the block become NaN with an infinite gradient, whatever its other roots are; with a
+    NaN its element's own."""
+    m = flp()
+    g = torch.Generator().manual_seed(5)
+    p = torch.randn(1024, generator=g).cuda()
+    grad = torch.randn(1024, generator=g).cuda()
+    grad[400:420] = 0.0
+    state = m.adamw_state([p], bits=8)
+    grad[300] = bad
+    before = p.clone()
+    m.adamw_step([p], [grad], state, 1, 1e-3, betas=betas)
+    rest = torch.ones(1024, dtype=torch.bool, device="cuda")
+    rest[300] = False
+    assert bool(p[rest].isfinite().all()) and not bool(p[300].isfinite())
+    assert bool((p != before)[rest & (grad != 0)].all())
+    gone = ~rest if math.isnan(bad) else (torch.arange(1024, device="cuda") // 256) == 1
+    for codes, scale in ((state.exp_avg, state.exp_avg_scale),
+                         (state.exp_avg_sq, state.exp_avg_sq_scale)):
+        assert torch.equal(held(codes[0], scale[0]).isnan(), gone)
