@@ -734,7 +734,7 @@ flp_status flp_residual_rms_norm_backward(
  *                replay's own step.  The caller counts.
  *   lr           or lr_on_device, one float32.   grad_scale: one float32 on the device, or
  *                NULL for 1 (a clipping factor, or what takes a loss scale back).
- *   beta1, beta2 in [0, 1).   eps >= 0.
+ *   beta1, beta2 in [0, 1).   eps: 0, or at least 2^-126 (fp32's least normal value).
  *
  * param, states, scales and master copies of all tensors must be distinct memory; gradients
  * may repeat.  Alignment: each pointer to its element size.  An element's result does not

@@ -1102,6 +1102,8 @@ flp_status validate_adamw_step(int64_t n_tensors, const flp_adamw_tensor* tensor
   if (!lr_on_device && !(std::fabs(lr) <= most)) return FLP_INVALID_ARGUMENT;
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return FLP_INVALID_ARGUMENT;
   if (!(eps >= 0.0 && eps <= most)) return FLP_INVALID_ARGUMENT;
+  // the kernel multiplies by a reciprocal, infinite below: an element without moments would be 0 inf
+  if (eps > 0.0 && eps < double(std::numeric_limits<float>::min())) return FLP_INVALID_ARGUMENT;
   if (!aligned(step_on_device, 8) || !aligned(lr_on_device, 4) || !aligned(grad_scale, 4))
     return FLP_MISALIGNED;
   const bool eight = state_bits == 8;

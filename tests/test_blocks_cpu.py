@@ -329,3 +329,17 @@ def test_residual_rms_norm_needs_the_block():
             flp.residual_rms_norm(x, None)
     with pytest.raises(TypeError):
         flp.residual_rms_norm_forward(torch.ones(2, 4), None)
+
+
+@pytest.mark.parametrize("eps,expect", [
+    (1e-40, "FLP_INVALID_ARGUMENT"), (1e-300, "FLP_INVALID_ARGUMENT"),
+    (2.0 ** -126 * (1 - 2.0 ** -20), "FLP_INVALID_ARGUMENT")])
+def test_adamw_eps_below_the_normal_range(eps, expect):
+    """Its reciprocal is no fp32 number: an element without gradients would become NaN."""
+    assert adamw([tensor()], eps=eps) == expect
+
+
+def test_adamw_eps_at_the_edges():
+    """0 and the least normal value pass this gate (another argument is refused)."""
+    for eps in (0.0, 2.0 ** -126):
+        assert adamw([tensor(n=1 << 62)], eps=eps) == "FLP_UNSUPPORTED_SHAPE"
