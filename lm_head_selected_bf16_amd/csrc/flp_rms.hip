@@ -96,9 +96,11 @@ __device__ __forceinline__ float rstd_of(float part, float inv, float eps, float
 #pragma unroll
     for (int k = 0; k < TEAM / 64; ++k) top = fmaxf(top, red[1][first + k]);
   }
-  // the inverse of its power of two; 1 for a row of zeros, infinities or NaN
+  // the inverse of its power of two, or the normal value nearest to that; 1 for a row of zeros,
+  // infinities or NaN
   const int e = int(__float_as_uint(top) >> 23);
-  const float c = top == 0.f || e == 255 ? 1.0f : __uint_as_float(uint32_t(min(254 - e, 253)) << 23);
+  const float c = top == 0.f || e == 255
+                      ? 1.0f : __uint_as_float(uint32_t(max(min(254 - e, 253), 1)) << 23);
   float q = 0.f;
   each([&](float v) { q = fmaf(v * c, v * c, q); });
   q = team_sum<TEAM>(q, red[2]);
