@@ -606,9 +606,12 @@ flp_status flp_gated_linear_forward(int64_t N, int64_t D, int64_t F, flp_dtype x
  *              transposed, with the weights and x), and fp32 sums over slabs of small products.
  *
  * For 16-bit types dz and du are rounded to x_dtype on the way, whose matrix instructions take
- * operands of that type; the products' sums are fp32 and rounded once.  They run in an order
- * fixed by the sizes; d_x of a row is bitwise the same among batches of up to 512 rows, and
- * among those of more, up to 1024, 2048, 8192 and beyond.  N = 0 writes zeros to d_w_gate and d_w_up.
+ * operands of that type; the products' sums are fp32 and rounded once.  FLP_F16: where the
+ * largest finite magnitude in dz and du is below 1, or 2^15 or more, they are held times the power
+ * of two that takes it to about 2^10, and the sums times its inverse, so that they keep their
+ * bits.  The sums run in an order fixed by the sizes; d_x of a row is bitwise the same among batches
+ * of up to 512 rows, and among those of more, up to 1024, 2048, 8192 and beyond (FLP_F16: of those
+ * with the same power of two).  N = 0 writes zeros to d_w_gate and d_w_up.
  */
 size_t flp_gated_linear_backward_workspace_bytes(int64_t N, int64_t D, int64_t F,
                                                  flp_dtype x_dtype, int need_d_x,

@@ -1070,6 +1070,8 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
   float* acc = reinterpret_cast<float*>(at(workspace, L.acc_off));
   z.dz = d_x || !wide ? at(workspace, L.dz_off) : nullptr;
   z.dzT = dw && wide ? at(workspace, L.dzt_off) : nullptr;
+  z.top = reinterpret_cast<float*>(at(workspace, L.top_off));
+  z.parts = L.parts;
   z.D = D;
   z.w_gate = w_gate;
   z.w_up = w_up;
@@ -1088,6 +1090,7 @@ flp_status flp_gated_linear_backward(int64_t N, int64_t D, int64_t F, flp_dtype 
     g.w_up = w_up;
     g.x = x;
     g.acc = acc;
+    g.back = z.top + z.parts;
     if (d_x != nullptr) {
       g.out = d_x;
       g.slab = L.dx_slab;

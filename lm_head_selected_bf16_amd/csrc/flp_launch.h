@@ -277,6 +277,10 @@ struct GatedDzArgs {
   const void* saved;         // as above
   int64_t ld_saved;
   void* dz;                  // [N][2 ld_saved] dz, du; fp32: K-blocked (or null)
+  // fp16 only: the largest finite magnitudes of dz and du by workgroup, `parts` of them, then the
+  // inverse of the factor that dz and du are held with
+  float* top;
+  int parts;
   // fp32 only: the other operands of the products, K-blocked, each or null
   void* dzT;                 // 2 ld_saved rows, K = N rounded up to 64
   int64_t D;
@@ -302,6 +306,7 @@ struct GatedGemmArgs {
   void* out2;                // d_w_up or null
   int64_t slab;              // columns (rows) of dz per slab, 0: one walk
   float* acc;                // [slabs][rows or 2 fp][D]
+  const float* back;         // fp16 only: the inverse of dz's factor
 };
 hipError_t launch_gated_dx16(flp_dtype x, const GatedGemmArgs& a, hipStream_t s);
 hipError_t launch_gated_dw16(flp_dtype x, const GatedGemmArgs& a, hipStream_t s);

@@ -886,6 +886,10 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need
     return slabs > 1 ? round_up(ceil_div(k, slabs), 128) : 0;
   };
   if (need_dx || !wide) take(L.dz_off, size_t(K) * N * xs);
+  if (x == FLP_F16) {
+    L.parts = int(std::min(kGatedParts, ceil_div(L.fp, 256) * ceil_div(N, 16)));
+    take(L.top_off, size_t(L.parts + 1) * 4);
+  }
   if (wide && need_dx) take(L.wt_off, size_t(K) * D * xs);
   if (wide && need_dw) {
     take(L.dzt_off, size_t(K) * L.np * xs);

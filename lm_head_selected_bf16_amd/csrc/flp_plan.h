@@ -171,11 +171,14 @@ struct GatedRows {
 };
 constexpr GatedRows kGatedRows[] = {{512, 5}, {1024, 2}, {2048, 1}, {8192, 1}};
 constexpr int64_t kGatedSlabs = 8, kGatedTiles = 160;
+constexpr int64_t kGatedParts = 512;  // two workgroups per compute unit look for the largest dz
 struct GatedLayout {
   int64_t fp = 0, np = 0;    // F and N rounded up to kGatedPad
   int64_t dx_slab = 0, dw_slab = 0;  // columns (tokens) of a slab, multiples of 128; 0: one walk
   size_t dz_off = 0;                 // [dz | du]; fp32: K-blocked, for d_x
   size_t wt_off = 0, dzt_off = 0, xt_off = 0;  // fp32: [Wg; Wu]^T, [dz | du]^T, x^T
+  size_t top_off = 0;                // fp16: the largest magnitudes of dz, by workgroup, and 1 / its factor
+  int parts = 0;                     // these workgroups
   size_t acc_off = 0;                // fp32 slab sums of d_x, then of the weight gradients
   size_t total = 0;
 };
