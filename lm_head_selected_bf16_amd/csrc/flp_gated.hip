@@ -637,8 +637,9 @@ hipError_t fwd_rows(const GatedFwdArgs& a, hipStream_t s) {
 
 template <class E>
 hipError_t fwd_all(const GatedFwdArgs& a, hipStream_t s) {
-  const bool odd = (a.D * E::kSize / kStageBytes) % 2 == 1;
-  return odd ? fwd_rows<E, true>(a, s) : fwd_rows<E, false>(a, s);
+  if constexpr (E::kSize == 2)  // 32 fp32 values are two stages
+    if ((a.D * E::kSize / kStageBytes) % 2 == 1) return fwd_rows<E, true>(a, s);
+  return fwd_rows<E, false>(a, s);
 }
 
 template <class E, bool TURNED, int BM, int BN, int WM, int WN, bool SLABS>
@@ -668,8 +669,14 @@ hipError_t gemm16(const GatedGemmArgs& a, hipStream_t s) {
   if (slabs == 1)
     return large ? gemm16_cfg<E, TURNED, 256, 224, 4, 2, false>(a, 1, s)
                  : gemm16_cfg<E, TURNED, 128, 128, 2, 2, false>(a, 1, s);
-  const hipError_t e = large ? gemm16_cfg<E, TURNED, 256, 224, 4, 2, true>(a, slabs, s)
-                             : gemm16_cfg<E, TURNED, 128, 128, 2, 2, true>(a, slabs, s);
+  hipError_t e = hipSuccess;
+  if constexpr (TURNED) {
+    // at most kGatedTiles of the smaller tiles: fewer of the larger ones
+    e = gemm16_cfg<E, TURNED, 128, 128, 2, 2, true>(a, slabs, s);
+  } else {
+    e = large ? gemm16_cfg<E, TURNED, 256, 224, 4, 2, true>(a, slabs, s)
+              : gemm16_cfg<E, TURNED, 128, 128, 2, 2, true>(a, slabs, s);
+  }
   if (e != hipSuccess) return e;
   const int64_t n = M * a.D;
   hipLaunchKernelGGL((k_gated_fold<E, TURNED>),
