@@ -599,7 +599,8 @@ flp_status flp_gated_linear_forward(int64_t N, int64_t D, int64_t F, flp_dtype x
  *   d_x = dz w_gate + du w_up,   d_w_gate = dz^T x,   d_w_up = du^T x
  *
  *   grad_out   [N, F] x_dtype, aligned to its element size.
- *   saved      as written by the forward for the same inputs.
+ *   saved      as written by the forward for the same inputs, activation among them: it holds
+ *              act(z) and u act'(z), so that activation is checked here, but not used again.
  *   d_x [N, D], d_w_gate, d_w_up [F, D] x_dtype, 16-byte aligned: each may be NULL to skip it.
  *   workspace  >= flp_gated_linear_backward_workspace_bytes(N, D, F, x_dtype, d_x wanted, a
  *              weight gradient wanted), 16-byte aligned: dz and du (2 N F elements; fp32: also

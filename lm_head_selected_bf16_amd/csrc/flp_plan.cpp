@@ -920,9 +920,9 @@ flp_status check_gated(int64_t N, int64_t D, int64_t F, flp_dtype x, flp_activat
   if (st != FLP_OK) return st;
   if (act != FLP_ACT_SILU && act != FLP_ACT_GELU && act != FLP_ACT_GELU_TANH)
     return FLP_INVALID_ARGUMENT;
-  // a launch's second grid dimension counts 64 tokens or weight rows, 256 rows of dz (of 2 F
-  // elements) stay below 2^31 bytes, and a launch holds fewer than 2^32 threads (256 for 64 x 64
-  // elements of dz)
+  // 256 rows of dz (of 2 F elements) stay below 2^31 bytes, and a launch holds fewer than 2^32
+  // threads (256 for 64 x 64 elements of dz, the weights and x).  N: the interface's own limit; the
+  // launches would hold more.
   if (N > int64_t(65535) * 64 || F > int64_t(32767) * 64) return FLP_UNSUPPORTED_SHAPE;
   const int64_t nt = ceil_div(N, 64), nc = ceil_div(F, 64), nd = ceil_div(D, 64);
   if (nc * nt + 2 * nc * nd + nt * nd >= (int64_t(1) << 24)) return FLP_UNSUPPORTED_SHAPE;

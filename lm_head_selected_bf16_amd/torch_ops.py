@@ -1026,7 +1026,8 @@ def gated_linear_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tens
 def gated_linear_backward(grad_out: torch.Tensor, saved: torch.Tensor, x: torch.Tensor,
                           w_gate: torch.Tensor, w_up: torch.Tensor, activation: str = "silu",
                           need_input: bool = True, need_gate: bool = True, need_up: bool = True):
-    """(d_x, d_w_gate, d_w_up) through flp_gated_linear_backward; unrequested ones are None."""
+    """(d_x, d_w_gate, d_w_up) through flp_gated_linear_backward; unrequested ones are None.  The
+    activation is the one that saved was made with (which holds its values already)."""
     N, D, F, act = _prepare_gated(x, w_gate, w_up, activation)
     dev, xd = x.device, _X_DTYPES[x.dtype]
     if (grad_out.dtype != x.dtype or grad_out.shape != x.shape[:-1] + (F,)
