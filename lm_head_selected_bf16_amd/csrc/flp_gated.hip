@@ -291,15 +291,21 @@ __device__ __forceinline__ void wave_exchange() {
 // fp16 holds normal values from 2^-14 to 2^16 only.  Where the largest finite dz or du of a call leaves
 // [1, 2^15), all of them are multiplied by the power of two that takes it to about 2^10, and the
 // products' fp32 sums by its inverse: gradients of 1e-6, whose dz would keep 5 of their 11 bits,
-// then lose none, and ones above 65504 stay finite.  Within those limits nothing is changed.  The pass
-// that looks for the largest takes 10 us at 1000 x 3587 (dz itself 10, both products 64).
+// then lose none, and ones above 65504 stay finite.  Within those limits nothing is changed.  The
+// largest is known when dz has been made: a second launch makes it again with its factor, or ends at
+// once, as ordinary gradients let it (5 us at 1000 x 3587, where looking for the largest first took
+// 10; 12 at 16384 x 7168).
 //
-// Returns the factor's exponent, from the largest values of `parts` workgroups.
+// The factor's exponent, from the largest values of `parts` workgroups; all threads call it.
 __device__ __forceinline__ int fp16_exponent(const float* top, int parts) {
+  __shared__ float tops[4];
   float m = 0.f;
-  for (int k = threadIdx.x & 63; k < parts; k += 64) m = fmaxf(m, top[k]);
+  for (int k = threadIdx.x; k < parts; k += 256) m = fmaxf(m, top[k]);
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
   if (m == 0.f || (m >= 1.0f && m < 0x1p15f)) return 0;
   return min(10 + 127 - int(__float_as_uint(m) >> 23), 120);
 }
@@ -309,11 +315,14 @@ __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(ui
 // lines, through LDS into the lanes of the kept blocks, and dz and du back through LDS into whole
 // lines (straight from the lanes, 32 bytes of a row at a time, 361 us for 16384 x 7168; 280 with
 // lines both ways).  Columns past F are zeros.
-// TOP: their largest finite magnitudes instead, one for each workgroup.
-template <class E, bool TOP>
+enum DzPass {
+  kOnly,   // bf16
+  kFirst,  // fp16: without a factor, and their largest finite magnitudes, one for each workgroup
+  kAgain,  // fp16: with the factor, if there is one; behind the magnitudes, its inverse
+};
+template <class E, DzPass PASS>
 __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
   using T = typename Elem<E>::T;
-  constexpr bool kScaled = !TOP && std::is_same_v<E, F16>;
   constexpr int kPitch = 72;  // elements of a row in LDS: 16 bytes more than its 64
   __shared__ __attribute__((aligned(16))) uint16_t tiles[4][2][16 * kPitch];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -322,11 +331,11 @@ __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
   const int i = lane & 15, g = lane >> 4;  // of the kept blocks
   const int lr = lane >> 3, lc = (lane & 7) * 8;  // of the lines: rows lr and lr + 8
   float factor = 1.0f, top = 0.f;
-  if constexpr (kScaled) {
+  if constexpr (PASS == kAgain) {
     const int e = fp16_exponent(p.top, p.parts);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.top[p.parts] = power_of_two(-e);
+    if (e == 0) return;
     factor = power_of_two(e);
-    // the products read its inverse behind the largest values
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.top[p.parts] = power_of_two(-e);
   }
   auto tile = [&](int64_t row0, int64_t col0) {
     Chunk<T> gr[2];
@@ -358,8 +367,8 @@ __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
         const float gf = float(T(gv[e]));
         z[e] = e < n ? gf * b[k][e] : 0.f;
         u[e] = e < n ? gf * a[k][e] : 0.f;
-        if constexpr (kScaled) z[e] *= factor, u[e] *= factor;
-        if constexpr (TOP) {
+        if constexpr (PASS == kAgain) z[e] *= factor, u[e] *= factor;
+        if constexpr (PASS == kFirst) {
           const float x = fabsf(z[e]), y = fabsf(u[e]);
           top = fmaxf(top, fmaxf(x < __builtin_inff() ? x : 0.f, y < __builtin_inff() ? y : 0.f));
         }
@@ -368,7 +377,6 @@ __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
       du[k] = u32x2{pack2<E>(u[0], u[1]), pack2<E>(u[2], u[3])};
     }
     wave_exchange();  // the gradient has been read
-    if constexpr (TOP) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int at = i * kPitch + k * 16 + 4 * g;
@@ -389,24 +397,26 @@ __global__ __launch_bounds__(256) void k_gated_dz(GatedDzArgs p) {
     }
     wave_exchange();
   };
-  if constexpr (TOP) {
-    const int64_t across = (p.ld_saved + 255) / 256, all = across * ((p.N + 15) / 16);
-    for (int64_t t = blockIdx.x; t < all; t += gridDim.x) {
+  const int64_t across = (p.ld_saved + 255) / 256, down = (p.N + 15) / 16;
+  if constexpr (PASS == kAgain) {
+    for (int64_t t = blockIdx.x; t < across * down; t += gridDim.x) {
       const int64_t col0 = t % across * 256 + wave * 64;
       if (col0 < p.ld_saved) tile(t / across * 16, col0);
     }
+  } else {
+    const int64_t col0 = int64_t(blockIdx.x) * 256 + wave * 64;
+    if (col0 < p.ld_saved)
+      for (int64_t r = blockIdx.y; r < down; r += gridDim.y) tile(r * 16, col0);
+  }
+  if constexpr (PASS == kFirst) {
+    __shared__ float tops[4];
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
-    __shared__ float tops[4];
     if (lane == 0) tops[wave] = top;
     __syncthreads();
     if (threadIdx.x == 0)
-      p.top[blockIdx.x] = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  } else {
-    const int64_t col0 = int64_t(blockIdx.x) * 256 + wave * 64;
-    if (col0 >= p.ld_saved) return;
-    for (int64_t row0 = int64_t(blockIdx.y) * 16; row0 < p.N; row0 += int64_t(gridDim.y) * 16)
-      tile(row0, col0);
+      p.top[int64_t(blockIdx.y) * gridDim.x + blockIdx.x] =
+          fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
   }
 }
 
@@ -687,14 +697,20 @@ hipError_t gemm16(const GatedGemmArgs& a, hipStream_t s) {
 
 template <class E>
 hipError_t dz16(const GatedDzArgs& a, hipStream_t s) {
-  const dim3 grid(unsigned((a.ld_saved + 255) / 256),
-                  unsigned(std::min<int64_t>((a.N + 15) / 16, 65535)));
+  const int64_t across = (a.ld_saved + 255) / 256, down = (a.N + 15) / 16;
   if constexpr (std::is_same_v<E, F16>) {
-    hipLaunchKernelGGL((k_gated_dz<E, true>), dim3(unsigned(a.parts)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_gated_dz<E, kFirst>), dim3(unsigned(across), unsigned(a.parts / across)),
+                       dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    // two workgroups per compute unit, which mostly have nothing to do
+    hipLaunchKernelGGL((k_gated_dz<E, kAgain>), dim3(unsigned(std::min<int64_t>(across * down, 512))),
+                       dim3(256), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_gated_dz<E, kOnly>),
+                       dim3(unsigned(across), unsigned(std::min<int64_t>(down, 65535))), dim3(256), 0,
+                       s, a);
   }
-  hipLaunchKernelGGL((k_gated_dz<E, false>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

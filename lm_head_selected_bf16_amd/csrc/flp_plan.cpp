@@ -887,7 +887,8 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, flp_dtype x, bool need
   };
   if (need_dx || !wide) take(L.dz_off, size_t(K) * N * xs);
   if (x == FLP_F16) {
-    L.parts = int(std::min(kGatedParts, ceil_div(L.fp, 256) * ceil_div(N, 16)));
+    const int64_t across = ceil_div(L.fp, 256);
+    L.parts = int(across * std::min(std::max<int64_t>(kGatedParts / across, 1), ceil_div(N, 16)));
     take(L.top_off, size_t(L.parts + 1) * 4);
   }
   if (wide && need_dx) take(L.wt_off, size_t(K) * D * xs);

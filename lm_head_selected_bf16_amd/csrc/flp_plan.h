@@ -171,7 +171,7 @@ struct GatedRows {
 };
 constexpr GatedRows kGatedRows[] = {{512, 5}, {1024, 2}, {2048, 1}, {8192, 1}};
 constexpr int64_t kGatedSlabs = 8, kGatedTiles = 160;
-constexpr int64_t kGatedParts = 512;  // two workgroups per compute unit look for the largest dz
+constexpr int64_t kGatedParts = 8192;  // workgroups of fp16's dz, whose largest magnitudes are kept
 struct GatedLayout {
   int64_t fp = 0, np = 0;    // F and N rounded up to kGatedPad
   int64_t dx_slab = 0, dw_slab = 0;  // columns (tokens) of a slab, multiples of 128; 0: one walk
