@@ -17,9 +17,11 @@
 // (flp_tr.h); the fp32 ones take transposed copies, which cost little beside their products.
 //
 // Bound by the matrix instructions for many rows, by reading the weights for few.  Measured: 16384 x
-// 2688 x 7168 bf16 silu forward 1042 to 1060 us (1200 TFLOP/s with act and 1.1 GB of stores; a
-// library product of the size alone 920), dz 269 (6.1 TB/s), d_x 942 (1340 TFLOP/s), both weights'
-// 1045 (1210); one row of 2688 x 7168 12.4 us (6.2 TB/s, part of it from the Infinity Cache).
+// 2688 x 7168 bf16 silu forward 1042 to 1110 us by the box (1210 to 1140 TFLOP/s with act and 0.94 GB of
+// stores; a library product of the size alone 920), dz 269 (1.41 GB, 5.2 TB/s), d_x 933 to 970
+// (1350 to 1300 TFLOP/s), both weights' 1036 to 1095 (1220 to 1150); one row of 2688 x 7168 12.4 us
+// (6.2 TB/s, part of it from the Infinity Cache).  fp32, 4096 x 1344 x 3584: forward 645 us
+// (122 TFLOP/s; a library product 154), operands 133, d_x 835 (94), weights' 719 (110).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -50,7 +52,9 @@ __device__ __forceinline__ float sigmoid(float v) {
 // gelu: with x = |z| / sqrt(2) and t = 1 / (1 + 0.4 x), 0.5 erfc(x) exp(x^2) is t times a polynomial
 // of t to 1.3e-7 of its value for every x (a weighted least-squares fit of degree 8), and the
 // exponential is the one that the slope needs: 20 instructions, where the library's erfc alone
-// takes some 60.
+// takes some 60.  The exponentials' arguments are rounded fp32 products, so that a factor's relative
+// error grows with its exponent: z^2 roundings on gelu's far side (1e-5 of a factor of 1e-38 at
+// z = -13), |v| of them in the logistic function of v < 0; on the scale of z both stay at a few 1e-7.
 constexpr float kTanhA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
 constexpr float kTail[9] = {0.112837933f, 0.112834759f, 0.103921957f, 0.084266752f, 0.0707311779f, -0.00283535989f, 0.084579125f, -0.0914728194f, 0.0251365416f};

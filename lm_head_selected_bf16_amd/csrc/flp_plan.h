@@ -166,6 +166,8 @@ constexpr int64_t kGatedPad = 64;  // columns of dz, and tokens of fp32 transpos
 //   1536 rows   1: 156 | 75    2: 148 | 69   3: 139 | 61   8: 193 | 71
 //   2048 rows   1: 230 | 83    2: 182 | 77   3: 257 | 86   8: 224 | 92
 //   3000 rows   1: 282 | 114   2: 335 | 114  3: 280 | 90   8: 357 | 121
+// A class has one number for all its batches, so some would be faster with another: 3000 x 1344 with
+// three, 256 x 2688 with five (by 13 %).  fp32 has the same classes, not measured by themselves.
 struct GatedRows {
   int64_t above, slabs;  // batches of more rows; their slabs, at least
 };

@@ -19,8 +19,12 @@
 // Bound by memory: the forward reads x and y and writes r and n, the backward reads both
 // gradients, x and y and writes d_x and d_y; every row is read once and held in registers.
 // Measured, 16384 x 2688 bf16 with both norms and a gate: forward 70 us (5.0 TB/s), backward 119
-// (4.4 TB/s, two workgroups per compute unit by its registers) and the fold 6; 4097 x 1345 fp16
-// with fp32 parameters 20, 27 and 8.
+// (4.4 TB/s: its 194 registers leave room for one workgroup per compute unit, and the 256 slabs
+// give it no more) and the fold 6, a gate for each row 103, 176 and 5; 4097 x 1345 fp16 with fp32
+// parameters and 17 gates 20, 27 and 8.  Wider rows of the same 134 MB a tensor, forward and backward:
+// 4096 bf16 93 and 183 us, fp32 103 and 165; 8192 bf16 104 and 175, fp32 112 and 172; 16384 bf16 106
+// and 193 (28 bytes of a thread spilled); 4096 rows of 16384 fp32 (268 MB) 203 and 488, 3.3 TB/s (212
+// bytes spilled).
 //
 // A row's sums run in an order fixed by D and the type alone, so r, n, d_x, d_y and the
 // statistics of a row are bitwise the same whatever the other rows are.  The sums over rows
@@ -40,9 +44,10 @@
 namespace flp {
 namespace {
 
-// A row belongs to a team of one wave, of four or of eight (by_width_* below).
+// A row belongs to a team of one wave, of four or of eight, in the backward of two too (by_width_*
+// below).
 constexpr int kThreads = 512;
-// Workgroups of a forward launch: two per compute unit (16384 x 2688 bf16 with y: 256 of them 74 us,
+// Workgroups of a forward launch: two for each compute unit, in turn (16384 x 2688 bf16 with y: 256 of them 74 us,
 // 512 and 768 74 to 76, 1024 78, 2048 82; 16384 x 512 fp32: 23.4, 22.5, 22.6, 23.9, 28.3).
 constexpr int64_t kFwdGroups = 512;
 
