@@ -13,6 +13,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -41,16 +43,7 @@ def _git_hash() -> str:
         return "unknown"
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source into libflp.so (always recompiles). Returns the path."""
-    tmp = LIB + ".tmp"
-    cmd = [_hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
-           "-ffp-contract=off", "-fno-fast-math",
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           "-Wall", "-Wno-unused-function",
-           f"-DFLP_GIT_HASH=\"{_git_hash()}\"",
-           "-I", os.path.join(ROOT, "include"),
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -60,6 +53,23 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{errs}")
     if verbose and errs.strip():
         print(errs, file=sys.stderr)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source (always recompiles, side by side) and link libflp.so. Returns the path."""
+    flags = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
+             "-ffp-contract=off", "-fno-fast-math",
+             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+             "-Wall", "-Wno-unused-function",
+             f"-DFLP_GIT_HASH=\"{_git_hash()}\"",
+             "-I", os.path.join(ROOT, "include")]
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as objects:
+        outs = [os.path.join(objects, s + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 1, 8)) as pool:
+            list(pool.map(lambda so: _run([_hipcc(), *flags, "-c", os.path.join(CSRC, so[0]), "-o", so[1]],
+                                          verbose), zip(SOURCES, outs)))
+        _run([_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *outs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     build_nodes(verbose)
     return LIB
