@@ -724,7 +724,8 @@ flp_status flp_residual_rms_norm_backward(
  *                scale per 256 consecutive elements, exp_avg_scale and exp_avg_sq_scale
  *                [ceil(n / 256)] float32 (the block's largest magnitude, at least 2^-100,
  *                over 448).  The step itself uses m and v before they are rounded.  Codes are
- *                rounded to nearest where beta1 <= 0.9 and beta2 <= 0.95.  With longer windows
+ *                rounded to nearest where beta1 <= 0.9 and beta2 <= 0.95 (but for an m that fades
+ *                to 0 through the last five codes).  With longer windows
  *                a step moves a state by far less than half a code, and nearest rounding would
  *                hold it still: they are rounded up or down by a threshold that depends on the
  *                step's number and the element's index alone, to within one code and right on

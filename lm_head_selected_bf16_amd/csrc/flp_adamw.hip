@@ -21,8 +21,11 @@
 //   b2 = 0.98    nearest 1.14 1.57 1.96, 5.8  11.6 16.7    dithered 0.81 1.00 1.21, 0.84 0.98 1.22
 //   b2 = 0.999   nearest 0.81 1.15 1.52, 6.4  9.0  13.2    dithered 0.77 1.00 1.25, 0.79 0.95 1.23
 // To nearest where b1 <= 0.9 and b2 <= 0.95: there the gradients' own spread moves a root by more
-// than half a step between two codes, an m without gradients decays by more than one, and each code is
-// within half a step of its value.
+// than half a step between two codes, an m without gradients decays by more than one down to five
+// times the least code, and each code is within half a step of its value.  From there on 0.9 of a code
+// rounds to the same code, and the element would move at a constant rate for good (0.2 lr a step beside
+// others of unit gradients): an m below five least codes whose gradient adds less than half of one is
+// rounded by its threshold here too, until it is 0.
 //
 // Bound by memory: one pass over grad, p, m, v and the master copies.  Measured: 347 M bf16
 // elements with master copies and 32-bit states 1812 us, 5.36 TB/s; 584 M with 8-bit states and
@@ -51,6 +54,7 @@ constexpr int kThreads = 256;
 constexpr int kTile = kThreads * kChunk;
 constexpr float kTop = 448.0f;            // the largest e4m3 value
 constexpr float kLeast = 0x1p-9f;         // the smallest positive one
+constexpr float kFaint = 5.0f * kLeast;   // 0.9 of up to five least codes is rounded to the same again
 constexpr float kBlockFloor = 0x1p-100f;  // a block's largest magnitude counts as at least this
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -129,8 +133,11 @@ __device__ __forceinline__ float to_grid(float q, uint32_t u) {
 
 // Codes of x and the block's scale.  The ratio is at most 448 (1 + 2^-22), which rounds to 448.  The
 // scale of a block with an infinite element is NaN, and so is then all that it holds.
-template <bool DIVISOR, bool DITHER>
-__device__ __forceinline__ u32x2 encode(const float (&x)[kChunk], float& scale, uint32_t u) {
+// FADE: to nearest, but for small x that `added` (what its gradient added, or more where it was 0
+// before) does not keep from 0.
+template <bool DIVISOR, bool DITHER, bool FADE>
+__device__ __forceinline__ u32x2 encode(const float (&x)[kChunk], float& scale, uint32_t u,
+                                        const float (&added)[kChunk]) {
   float top = 0.f;
 #pragma unroll
   for (int k = 0; k < kChunk; ++k) top = fmaxf(top, fabsf(x[k]));
@@ -138,11 +145,19 @@ __device__ __forceinline__ u32x2 encode(const float (&x)[kChunk], float& scale, 
   scale = top < __builtin_inff() ? top * (1.0f / kTop) : __builtin_nanf("");
   const float inv = (1.0f / top) * kTop;
   float q[kChunk];
+  bool fades = false;
 #pragma unroll
   for (int k = 0; k < kChunk; ++k) {
     q[k] = x[k] * inv;
+    if (FADE) fades |= fabsf(q[k]) < kFaint && fabsf(added[k]) * inv < 0.5f * kLeast;
     if (DITHER) q[k] = to_grid(q[k], u + uint32_t(k) * kRoot3);
     if (DIVISOR) q[k] = x[k] > 0.f && q[k] < kLeast ? kLeast : q[k];  // NaN stays
+  }
+  if (FADE && __builtin_amdgcn_ballot_w64(fades) != 0) {  // of few waves
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k)
+      if (fabsf(q[k]) < kFaint && fabsf(added[k]) * inv < 0.5f * kLeast)
+        q[k] = to_grid(q[k], u + uint32_t(k) * kRoot3);
   }
   u32x2 w;
 #pragma unroll
@@ -217,7 +232,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
     constexpr bool kFull = decltype(whole)::value;
     const int64_t at = first + lane8;
     const int64_t n = kFull ? int64_t(kChunk) : t.n - at;
-    float p[kChunk], m[kChunk], v[kChunk], root[kChunk];
+    float p[kChunk], m[kChunk], v[kChunk], root[kChunk], added[kChunk];
     Chunk<G> g;
     Chunk<float> w, x;
     Chunk<P> c;
@@ -249,6 +264,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
       else
         p[e] = float(P(c.v[e]));
       const float ge = float(G(g.v[e])) * grad_scale;
+      added[e] = m[e] != 0.f ? a.one_b1 * ge : __builtin_inff();
       m[e] = a.b1 * m[e] + a.one_b1 * ge;
       v[e] = a.b2 * v[e] + a.one_b2 * (ge * ge);
     }
@@ -274,9 +290,10 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamArgs a) {
       // past the tensor's end everything is 0, which changes no block's scale
       float sm, sv;
       constexpr bool kDither = HELD == kDithered;
-      const uint32_t u = kDither ? chunk_offset(at / kChunk) : 0u;
-      const u32x2 cm = encode<false, kDither>(m, sm, u + step_now * kGolden);
-      const u32x2 cv = encode<true, kDither>(root, sv, ((u << 16) | (u >> 16)) + step_now * kRoot2);
+      const uint32_t u = chunk_offset(at / kChunk);
+      const u32x2 cm = encode<false, kDither, !kDither>(m, sm, u + step_now * kGolden, added);
+      const u32x2 cv = encode<true, kDither, false>(
+          root, sv, ((u << 16) | (u >> 16)) + step_now * kRoot2, added);
       store_codes(static_cast<uint8_t*>(t.m) + at, n, cm);
       store_codes(static_cast<uint8_t*>(t.v) + at, n, cv);
       if ((threadIdx.x & (kAdamBlock / kChunk - 1)) == 0 && n > 0) {

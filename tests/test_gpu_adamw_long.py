@@ -70,27 +70,31 @@ def test_second_moments_follow_their_gradients(betas, before, after):
         assert abs(float(x / y) - 1) <= SPREAD ** 2 + 3 * SPREAD / 32, (name, float(x), float(y))
 
 
-@pytest.mark.parametrize("betas", [(0.9, 0.999), (0.95, 0.99)])
-def test_elements_without_gradients_come_to_rest(betas):
+@pytest.mark.parametrize("spread", [0.0, 1.0])
+@pytest.mark.parametrize("betas", [(0.9, 0.999), (0.95, 0.99), (0.9, 0.95), (0.5, 0.9)])
+def test_elements_without_gradients_come_to_rest(betas, spread):
     """Beside elements that have some, with constant size too (the block's scale stands still)."""
     m = flp()
     n = 256 * BLOCKS
     p = torch.zeros(n, device="cuda")
     state = m.adamw_state([p], bits=8)
-    on = torch.ones(n, device="cuda")
-    off = (pattern() != 0).float()
+    g = torch.Generator(device="cuda").manual_seed(7)
+    has = (pattern() != 0).float()
+
+    def draw():
+        return 1 + spread * torch.randn(n, generator=g, device="cuda")
     for t in range(1, 100):
-        m.adamw_step([p], [on], state, t, 1e-3, betas=betas, weight_decay=0.0)
+        m.adamw_step([p], [draw()], state, t, 1e-3, betas=betas, weight_decay=0.0)
     # from 448 to below the least code's half in log(448 * 1024) / (1 - b1) steps; from code 1 to 0 in
     # a visit of the thresholds to 1 - b1 of their range, some 3 / (1 - b1) steps at most
     last = 100 + int((math.log(448 * 1024) + 30) / (1 - betas[0]))
     for t in range(100, last):
-        m.adamw_step([p], [off], state, t, 1e-3, betas=betas, weight_decay=0.0)
+        m.adamw_step([p], [draw() * has], state, t, 1e-3, betas=betas, weight_decay=0.0)
     assert not bool(part(state.exp_avg[0].float(), "none").any())
     assert bool((part(state.exp_avg_sq[0].float(), "none") > 0).all())
     was = p.clone()
     for t in range(last, last + 50):
-        m.adamw_step([p], [off], state, t, 1e-3, betas=betas, weight_decay=0.0)
+        m.adamw_step([p], [draw() * has], state, t, 1e-3, betas=betas, weight_decay=0.0)
     assert torch.equal(part(p, "none"), part(was, "none"))
     assert bool((part(p, "same") != part(was, "same")).all())
 
